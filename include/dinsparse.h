@@ -53,8 +53,9 @@ extern "C" {
 
 #define DSF_MAX_TABLES 32
 
-/* Table element types. */
-enum { DSF_F32 = 0, DSF_BF16 = 1 };
+/* Element types. Tables are fp32 or bf16; the dense operators at the end of
+ * this header also take e4m3 (8 bits, finite values to +-448, with scales). */
+enum { DSF_F32 = 0, DSF_BF16 = 1, DSF_E4M3 = 2 };
 
 /* Attention-MLP arithmetic. BF16_TC: bf16 operands on tcgen05 tensor cores,
  * fp32 accumulation (the pages' half-precision MLP, "integrating DynamicEmb",
@@ -394,6 +395,113 @@ int din_sparse_bwd(const dsf_tables* tables, const dsf_kjt* kjt, const dsf_seq* 
  * accumulators (the pool's for hash-table tables, as for the gradients). */
 int emb_adagrad_update(const dsf_tables* tables, float* const* accum, const dsf_row_grads* row_grads, float lr,
                        float eps, int32_t* status_dev, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dense-tower operators of any width: a dense layer, a gated feed-forward
+ * layer and a root-mean-square norm, with their gradients. They stand beside
+ * ctr_towers_fwd (one fixed network, forward only) for towers of other
+ * widths and activations, for residual and gated tower blocks (the norm, the
+ * gated layer, the dense layer back with the residual), for serving in 8 bits
+ * and for training: the gradients they leave at the tower's inputs are the
+ * dpooled_dev and ddin_dev of din_sparse_bwd. The pages name the towers'
+ * widths only (current state analysis, section 4.4); these operators have no
+ * counterpart there.
+ *
+ *   dense   y = residual + act(x W^T + bias)                       W [R, K]
+ *   glu     h = act(x Wg^T + bg) * (x Wu^T + bu)    W [2F, K] = [Wg; Wu]
+ *   norm    s = x + residual (rounded to x's type),
+ *           y = s * weight / sqrt(mean(s^2) + eps)
+ *
+ * Matrices are row-major with a row stride in elements (ld*; at least the
+ * row's length); M is the number of rows (samples). Types of a layer:
+ *   DSF_BF16  x, W, residual, y, dy, dx, dW are bf16; fp32 accumulation on
+ *             the tensor cores, one rounding at the output. The backward
+ *             rounds dz to bf16 where it enters the products for dx and dW.
+ *   DSF_F32   all fp32, to fp32's accuracy: every operand is taken as the
+ *             exact sum of three bf16 terms, and the six products of terms
+ *             that reach fp32's last bits are accumulated in fp32 (an
+ *             infinite operand gives infinities or NaN in what it enters).
+ *   DSF_E4M3  x [M, K] e4m3 with x_scale_dev fp32 [M], W e4m3 with
+ *             layer->scale fp32 [R]: x and W stand for value * scale.
+ *             residual and y are bf16. Forward only.
+ * Biases and their gradients are fp32.
+ *
+ * Alignment: every pointer is aligned to its element. When a row of x, W
+ * (K elements) or, in a backward call, dy (R, or F elements) is a multiple of
+ * 16 bytes, those rows start at 16-byte boundaries (pointer and stride);
+ * other widths are laid out in the workspace by each call. Any alignment of
+ * the other matrices is taken; rows at 16-byte boundaries are faster.
+ * y may be the residual itself (same pointer and stride); apart from that the
+ * outputs overlap no input.
+ * The workspace (256-byte aligned) needs no initialisation and holds nothing
+ * from one call to the next. M = 0 is valid (a backward call zeroes dW, db).
+ * Non-finite values reach only the results that are computed from them. */
+enum { DSF_ACT_NONE = 0, DSF_ACT_RELU = 1, DSF_ACT_SILU = 2, DSF_ACT_GELU = 3 };
+
+typedef struct {
+  const void* W;      /* device [R, K] of dtype; ctr_glu_*: R = 2F, the F gate rows first */
+  const float* bias;  /* device [R], nullable */
+  const float* scale; /* device [R]: DSF_E4M3 only (NULL otherwise) */
+  int64_t ldw;        /* W's row stride, elements */
+  int32_t R, K;       /* 1 .. 2^20 */
+  int32_t dtype;      /* DSF_F32, DSF_BF16 or DSF_E4M3 */
+  int32_t act;        /* DSF_ACT_*; GELU is the exact one, z Phi(z) */
+} dsf_dense;
+
+/* Workspace bytes of the forward call (backward = 0), or of both calls
+ * (backward = 1), for up to M rows; gated: 1 for ctr_glu_*, 0 for
+ * ctr_dense_*. 0 for invalid arguments. */
+size_t dsf_dense_workspace_bytes(const dsf_dense* layer, int64_t M, int32_t gated, int32_t backward);
+
+/* y_dev [M, R] = residual + act(x W^T + bias). residual_dev nullable.
+ * DSF_FLAG_TIMEOUT in *status_dev (nullable) if a device wait ran out. */
+int ctr_dense_fwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const float* x_scale_dev,
+                  const void* residual_dev, int64_t ldr, int64_t M, void* y_dev, int64_t ldy, void* workspace_dev,
+                  size_t ws_bytes, int32_t* status_dev, void* stream);
+
+/* The gradients of ctr_dense_fwd for dy_dev [M, R]: dx_dev [M, K], dW_dev
+ * [R, K] (contiguous), both of the layer's type, and db_dev fp32 [R]; each
+ * nullable, and overwritten. The residual's gradient is dy itself. z = x W^T
+ * + bias is computed again (the forward keeps nothing); ReLU's gradient at 0
+ * is 0. Sums run in a fixed order: equal inputs give equal bits. */
+int ctr_dense_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const void* dy_dev, int64_t lddy, int64_t M,
+                  void* dx_dev, int64_t lddx, void* dW_dev, float* db_dev, void* workspace_dev, size_t ws_bytes,
+                  int32_t* status_dev, void* stream);
+
+/* h_dev [M, F] = act(x Wg^T + bg) * (x Wu^T + bu), F = R / 2, in one pass over
+ * x and W. */
+int ctr_glu_fwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const float* x_scale_dev, int64_t M,
+                void* h_dev, int64_t ldh, void* workspace_dev, size_t ws_bytes, int32_t* status_dev, void* stream);
+
+/* The gradients of ctr_glu_fwd for dh_dev [M, F]: dx_dev [M, K], dW_dev
+ * [2F, K], db_dev [2F], as ctr_dense_bwd's. */
+int ctr_glu_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const void* dh_dev, int64_t lddh, int64_t M,
+                void* dx_dev, int64_t lddx, void* dW_dev, float* db_dev, void* workspace_dev, size_t ws_bytes,
+                int32_t* status_dev, void* stream);
+
+/* The norm of M rows of N (1 .. 32768) elements. x_dev, residual_dev
+ * (nullable) and sum_dev (nullable: s, which may be written over x or
+ * residual) are of x_dtype (DSF_F32 or DSF_BF16). weight_dev fp32 [N],
+ * nullable (ones). y_dev is of y_dtype: DSF_F32, DSF_BF16, or DSF_E4M3 with
+ * y_scale_dev fp32 [M] written: scale = max(max|y| of the row / 448, 2^-126),
+ * values y / scale rounded to nearest even. eps > 0. */
+int ctr_rms_norm_fwd(const void* x_dev, int64_t ldx, const void* residual_dev, int64_t ldr, int32_t x_dtype,
+                     const float* weight_dev, int64_t M, int32_t N, float eps, void* sum_dev, int64_t lds,
+                     void* y_dev, int64_t ldy, int32_t y_dtype, float* y_scale_dev, void* stream);
+
+/* Workspace bytes of ctr_rms_norm_bwd (0 for invalid arguments). */
+size_t dsf_rms_norm_workspace_bytes(int64_t M, int32_t N);
+
+/* The norm's gradients at s_dev [M, N] (x_dtype: the forward's sum, or its x
+ * without a residual) for dy_dev (dy_dtype DSF_F32 or DSF_BF16): dx_dev of
+ * x_dtype, the gradient of s, plus dsum_dev where given (nullable, of x_dtype:
+ * what reaches s past the norm; dx may be written over it). It is the
+ * gradient of x and of residual alike. dweight_dev fp32 [N], nullable (the
+ * workspace is needed only with it). Equal inputs give equal bits. */
+int ctr_rms_norm_bwd(const void* dy_dev, int64_t lddy, int32_t dy_dtype, const void* s_dev, int64_t lds,
+                     int32_t x_dtype, const float* weight_dev, int64_t M, int32_t N, float eps, const void* dsum_dev,
+                     int64_t ldds, void* dx_dev, int64_t lddx, float* dweight_dev, void* workspace_dev,
+                     size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -15,7 +15,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdinsparse.so")
 
-DSF_F32, DSF_BF16 = 0, 1
+DSF_F32, DSF_BF16, DSF_E4M3 = 0, 1, 2
+DSF_ACT_NONE, DSF_ACT_RELU, DSF_ACT_SILU, DSF_ACT_GELU = 0, 1, 2, 3
 DSF_MODE_BF16_TC, DSF_MODE_FP32 = 0, 1
 DSF_OK, DSF_EINVAL, DSF_EUNSUPPORTED, DSF_ECUDA, DSF_EWORKSPACE = 0, 1, 2, 3, 4
 FLAG_ID_RANGE = 0x01
@@ -33,7 +34,9 @@ EXPORTS = ["dsf_workspace_bytes", "dsf_workspace_init", "dsf_prepare_mlp", "emb_
            "emb_bag_pool_noalloc", "dsf_towers_workspace_bytes", "dsf_prepare_towers", "ctr_towers_fwd",
            "dsf_hash_workspace_bytes", "dsf_hash_init", "dsf_hash_insert", "dsf_hash_find",
            "dsf_bwd_workspace_bytes", "din_sparse_bwd", "emb_adagrad_update", "dsf_read_status",
-           "dsf_bwd_workspace_offsets"]
+           "dsf_bwd_workspace_offsets",
+           "dsf_dense_workspace_bytes", "ctr_dense_fwd", "ctr_dense_bwd", "ctr_glu_fwd", "ctr_glu_bwd",
+           "dsf_rms_norm_workspace_bytes", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd"]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -67,6 +70,11 @@ class CSeq(ctypes.Structure):
 class CMlp(ctypes.Structure):
     _fields_ = [("W1", _vp), ("b1", _vp), ("W2", _vp), ("b2", _vp), ("w3", _vp), ("b3", _vp),
                 ("K1", _i32), ("N1", _i32), ("N2", _i32), ("mode", _i32)]
+
+
+class CDense(ctypes.Structure):
+    _fields_ = [("W", _vp), ("bias", _vp), ("scale", _vp), ("ldw", _i64), ("R", _i32), ("K", _i32), ("dtype", _i32),
+                ("act", _i32)]
 
 
 class DsfError(RuntimeError):
@@ -132,6 +140,21 @@ def lib() -> ctypes.CDLL:
         L.dsf_read_status.restype = ctypes.c_int
         L.dsf_bwd_workspace_offsets.argtypes = [_i32, _i64, _i64, _i32, _vp]
         L.dsf_bwd_workspace_offsets.restype = ctypes.c_int
+        L.dsf_dense_workspace_bytes.argtypes = [P(CDense), _i64, _i32, _i32]
+        L.dsf_dense_workspace_bytes.restype = _sz
+        L.ctr_dense_fwd.argtypes = [P(CDense), _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _sz, _vp, _vp]
+        L.ctr_glu_fwd.argtypes = [P(CDense), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp, _vp]
+        for f in (L.ctr_dense_bwd, L.ctr_glu_bwd):
+            f.argtypes = [P(CDense), _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
+        L.dsf_rms_norm_workspace_bytes.argtypes = [_i64, _i32]
+        L.dsf_rms_norm_workspace_bytes.restype = _sz
+        L.ctr_rms_norm_fwd.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, ctypes.c_float, _vp, _i64, _vp, _i64,
+                                       _i32, _vp, _vp]
+        L.ctr_rms_norm_bwd.argtypes = [_vp, _i64, _i32, _vp, _i64, _i32, _vp, _i64, _i32, ctypes.c_float, _vp, _i64, _vp,
+                                       _i64, _vp, _vp, _sz, _vp]
+        for f in (L.ctr_dense_fwd, L.ctr_glu_fwd, L.ctr_dense_bwd, L.ctr_glu_bwd, L.ctr_rms_norm_fwd,
+                  L.ctr_rms_norm_bwd):
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -475,3 +498,200 @@ def emb_adagrad_update(tables: EmbeddingTables, state: SparseState, lr: float = 
     _check(lib().emb_adagrad_update(ctypes.byref(tables.c), state.accum_ptrs, ctypes.byref(state.c),
                                     float(lr), float(eps), _dptr(status), _stream_ptr(stream)),
            "emb_adagrad_update")
+
+
+# ------------------------------------------------------------- dense-tower operators
+_DTYPES = {torch.float32: DSF_F32, torch.bfloat16: DSF_BF16, torch.float8_e4m3fn: DSF_E4M3}
+
+
+def _mat(name: str, t: torch.Tensor, dtype, shape, device):
+    """Pointer and row stride of a [rows, cols] matrix whose columns are
+    contiguous; raises ValueError for anything else."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError("%s: %s %s on %s expected, got %s %s on %s" % (
+            name, dtype, list(shape), device, t.dtype, list(t.shape), t.device))
+    if shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError("%s: columns must be contiguous" % name)
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError("%s: rows overlap" % name)
+    return t.data_ptr(), ld
+
+
+def _vec(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[int]:
+    """Pointer of a contiguous fp32 [n] vector (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s: contiguous float32 [%d] on %s expected" % (name, n, device))
+    return t.data_ptr()
+
+
+def _on_current(device) -> None:
+    """The calls launch on the current device: its tensors have to be there."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
+
+
+class DenseLayer:
+    """Device weights of a dense layer (W [N, K]) or a gated layer (W [2F, K]:
+    the gate rows, then the up rows): float32, bfloat16, or float8_e4m3fn with
+    scale float32 [rows]. bias: float32 [rows] or None. act: DSF_ACT_*."""
+
+    def __init__(self, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: int = DSF_ACT_NONE,
+                 scale: Optional[torch.Tensor] = None):
+        if W.dim() != 2 or W.dtype not in _DTYPES:
+            raise ValueError("W: a float32, bfloat16 or float8_e4m3fn matrix expected")
+        R, K = int(W.shape[0]), int(W.shape[1])
+        self.dtype = _DTYPES[W.dtype]
+        ptr, ldw = _mat("W", W, W.dtype, (R, K), W.device)
+        if (scale is not None) != (self.dtype == DSF_E4M3):
+            raise ValueError("scale: given for float8_e4m3fn weights, and only for them")
+        self.W, self.bias, self.scale, self.R, self.K, self.act = W, bias, scale, R, K, int(act)
+        self.out_dtype = torch.bfloat16 if self.dtype == DSF_E4M3 else W.dtype
+        self.c = CDense(ptr, _vec("bias", bias, R, W.device), _vec("scale", scale, R, W.device), ldw, R, K, self.dtype,
+                        self.act)
+        self._ref = ctypes.byref(self.c)
+
+    @property
+    def device(self):
+        return self.W.device
+
+
+class DenseWorkspace:
+    """Scratch of a layer's calls for up to M rows; gated: for ctr_glu_*;
+    backward: for the gradients too."""
+
+    def __init__(self, layer: DenseLayer, M: int, gated: bool = False, backward: bool = False):
+        self.nbytes = int(lib().dsf_dense_workspace_bytes(layer._ref, int(M), int(bool(gated)), int(bool(backward))))
+        if self.nbytes == 0:
+            raise DsfError(DSF_EINVAL, "dsf_dense_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=layer.device)
+        self.ptr = self.buf.data_ptr()
+
+
+def _x_of(layer: DenseLayer, x: torch.Tensor):
+    _on_current(layer.device)
+    if x.dim() != 2:
+        raise ValueError("x: a matrix expected")
+    M = int(x.shape[0])
+    return (M,) + _mat("x", x, layer.W.dtype, (M, layer.K), layer.device)
+
+
+def _scale_of(layer: DenseLayer, x_scale, M: int):
+    if (x_scale is not None) != (layer.dtype == DSF_E4M3):
+        raise ValueError("x_scale: given for float8_e4m3fn layers, and only for them")
+    return _vec("x_scale", x_scale, M, layer.device)
+
+
+def _ws_of(layer: DenseLayer, workspace: DenseWorkspace):
+    if workspace.buf.device != layer.device:
+        raise ValueError("the workspace is on %s" % workspace.buf.device)
+    return workspace.ptr, workspace.nbytes
+
+
+def ctr_dense_fwd(layer: DenseLayer, x: torch.Tensor, y: torch.Tensor, workspace: DenseWorkspace,
+                  residual: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = residual + act(x W^T + bias); y may be the residual."""
+    M, xp, ldx = _x_of(layer, x)
+    yp, ldy = _mat("y", y, layer.out_dtype, (M, layer.R), layer.device)
+    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, layer.out_dtype, (M, layer.R), layer.device)
+    wp, nb = _ws_of(layer, workspace)
+    _check(lib().ctr_dense_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), rp, ldr, M, yp, ldy, wp, nb,
+                               _dptr(status), _stream_ptr(stream)), "ctr_dense_fwd")
+    return y
+
+
+def ctr_glu_fwd(layer: DenseLayer, x: torch.Tensor, h: torch.Tensor, workspace: DenseWorkspace,
+                x_scale: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """h [M, F] = act(x Wg^T + bg) * (x Wu^T + bu), W = [Wg; Wu]."""
+    M, xp, ldx = _x_of(layer, x)
+    hp, ldh = _mat("h", h, layer.out_dtype, (M, layer.R // 2), layer.device)
+    wp, nb = _ws_of(layer, workspace)
+    _check(lib().ctr_glu_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), M, hp, ldh, wp, nb, _dptr(status),
+                             _stream_ptr(stream)), "ctr_glu_fwd")
+    return h
+
+
+def _layer_bwd(name, layer, x, dy, cols, workspace, dx, dW, db, status, stream):
+    M, xp, ldx = _x_of(layer, x)
+    T, dev = layer.W.dtype, layer.device
+    gp, ldg = _mat("the upstream gradient", dy, T, (M, cols), dev)
+    dxp, lddx = (None, 0) if dx is None else _mat("dx", dx, T, (M, layer.K), dev)
+    dWp = None
+    if dW is not None:
+        dWp, ld = _mat("dW", dW, T, (layer.R, layer.K), dev)
+        if not dW.is_contiguous():
+            raise ValueError("dW: contiguous expected")
+    wp, nb = _ws_of(layer, workspace)
+    _check(getattr(lib(), name)(layer._ref, xp, ldx, gp, ldg, M, dxp, lddx, dWp, _vec("db", db, layer.R, dev), wp, nb,
+                                _dptr(status), _stream_ptr(stream)), name)
+
+
+def ctr_dense_bwd(layer: DenseLayer, x: torch.Tensor, dy: torch.Tensor, workspace: DenseWorkspace,
+                  dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                  db: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of ctr_dense_fwd for dy [M, N], each overwritten where given
+    (the residual's gradient is dy itself)."""
+    _layer_bwd("ctr_dense_bwd", layer, x, dy, layer.R, workspace, dx, dW, db, status, stream)
+
+
+def ctr_glu_bwd(layer: DenseLayer, x: torch.Tensor, dh: torch.Tensor, workspace: DenseWorkspace,
+                dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                db: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of ctr_glu_fwd for dh [M, F]."""
+    _layer_bwd("ctr_glu_bwd", layer, x, dh, layer.R // 2, workspace, dx, dW, db, status, stream)
+
+
+class RmsNormWorkspace:
+    """Scratch of ctr_rms_norm_bwd's weight gradient for up to M rows of N."""
+
+    def __init__(self, M: int, N: int, device="cuda"):
+        self.nbytes = int(lib().dsf_rms_norm_workspace_bytes(int(M), int(N)))
+        if self.nbytes == 0:
+            raise DsfError(DSF_EINVAL, "dsf_rms_norm_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+
+def ctr_rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, y_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """s = x + residual (into sum_out where given), y = s * weight /
+    sqrt(mean(s^2) + eps); y float32, bfloat16, or float8_e4m3fn with y_scale."""
+    dev = x.device
+    _on_current(dev)
+    if x.dim() != 2 or x.dtype not in _DTYPES or y.dtype not in _DTYPES:
+        raise ValueError("x and y: matrices of a supported type expected")
+    M, N = int(x.shape[0]), int(x.shape[1])
+    xp, ldx = _mat("x", x, x.dtype, (M, N), dev)
+    yp, ldy = _mat("y", y, y.dtype, (M, N), dev)
+    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, x.dtype, (M, N), dev)
+    sp, lds = (None, 0) if sum_out is None else _mat("sum_out", sum_out, x.dtype, (M, N), dev)
+    _check(lib().ctr_rms_norm_fwd(xp, ldx, rp, ldr, _DTYPES[x.dtype], _vec("weight", weight, N, dev), M, N, float(eps),
+                                  sp, lds, yp, ldy, _DTYPES[y.dtype], _vec("y_scale", y_scale, M, dev),
+                                  _stream_ptr(stream)), "ctr_rms_norm_fwd")
+    return y
+
+
+def ctr_rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, dx: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, dsum: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                     workspace: Optional[RmsNormWorkspace] = None, stream=None) -> None:
+    """dx = the norm's gradient at s for dy, plus dsum where given; dweight
+    (which needs the workspace) overwritten."""
+    dev = s.device
+    _on_current(dev)
+    if s.dim() != 2 or s.dtype not in _DTYPES or dy.dtype not in _DTYPES:
+        raise ValueError("s and dy: matrices of a supported type expected")
+    M, N = int(s.shape[0]), int(s.shape[1])
+    gp, ldg = _mat("dy", dy, dy.dtype, (M, N), dev)
+    sp, lds = _mat("s", s, s.dtype, (M, N), dev)
+    dp, ldd = (None, 0) if dsum is None else _mat("dsum", dsum, s.dtype, (M, N), dev)
+    xp, ldx = _mat("dx", dx, s.dtype, (M, N), dev)
+    if workspace is not None and workspace.buf.device != dev:
+        raise ValueError("the workspace is on %s" % workspace.buf.device)
+    _check(lib().ctr_rms_norm_bwd(gp, ldg, _DTYPES[dy.dtype], sp, lds, _DTYPES[s.dtype], _vec("weight", weight, N, dev),
+                                  M, N, float(eps), dp, ldd, xp, ldx, _vec("dweight", dweight, N, dev),
+                                  None if workspace is None else workspace.buf.data_ptr(),
+                                  0 if workspace is None else workspace.nbytes, _stream_ptr(stream)), "ctr_rms_norm_bwd")

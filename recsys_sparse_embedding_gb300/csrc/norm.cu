@@ -1,0 +1,451 @@
+// The root-mean-square norm of the dense towers: s = x + residual (rounded to
+// x's type, as later layers read it), y = s w / sqrt(mean(s^2) + eps), with an
+// optional 8-bit output (e4m3 values and one scale per row), and its gradient.
+//
+// Both directions are bound by HBM: a row is read once, held in registers
+// between the row sum and the outputs, and written once. A row belongs to a
+// group of G threads -- one warp up to N = 1024, so that the row sums are warp
+// shuffles and several rows are in flight per block, then 128 .. 1024 threads
+// -- and each thread holds 8 V elements of it (V <= 4, so a row's registers
+// stay near 32 per operand). Aligned rows move in 16-byte vectors, eight
+// elements a thread; others (odd N, odd strides) element by element, the
+// group's threads side by side.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "colsum.cuh"
+#include "dinsparse.h"
+
+namespace dsf {
+namespace norm {
+namespace {
+
+constexpr int kMaxN = 32768;
+constexpr int kBlock = 256;          // threads per block (a wider group is its own block)
+constexpr int kMaxPartials = 152 * 4;  // blocks of the backward, each with one row of weight-gradient sums
+constexpr float kE4m3Max = 448.f;
+
+struct FwdArgs {
+  const void *x, *res;
+  long long ldx, ldr;
+  const float* w;
+  long long M;
+  int N;
+  float eps;
+  void* sum;
+  long long lds;
+  void* y;
+  long long ldy;
+  float* scale;
+};
+
+struct BwdArgs {
+  const void *dy, *s, *dsum;
+  long long lddy, lds, ldds;
+  const float* w;
+  long long M;
+  int N;
+  float eps;
+  void* dx;
+  long long lddx;
+  float* part;  // [blocks][N], nullable
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __nv_fp8_e4m3 from_f<__nv_fp8_e4m3>(float v) { return __nv_fp8_e4m3(v); }
+
+// eight consecutive elements, 16-byte aligned (e4m3: 8 bytes)
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(u[k] << 16);
+    v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    u[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float* v) {
+  uint32_t u[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k], v[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2], v[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
+    u[k] = lo | hi << 16;
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+}
+
+// A group's share of a row: V sets of 8 elements per thread. ALIGNED: set i of
+// thread t is the 8 consecutive elements from 8 (t + i G); else its elements
+// are t, t + G, ... so that the group reads neighbouring elements.
+template <bool ALIGNED, int G, class T>
+__device__ __forceinline__ void load_set(const T* row, int i, int t, int N, float* v) {
+  if (ALIGNED) {
+    const int e = 8 * (t + i * G);
+    if (e < N) {
+      load8(row + e, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = (8 * i + j) * G + t;
+      v[j] = e < N ? to_f(row[e]) : 0.f;
+    }
+  }
+}
+template <bool ALIGNED, int G, class T>
+__device__ __forceinline__ void store_set(T* row, int i, int t, int N, const float* v) {
+  if (ALIGNED) {
+    const int e = 8 * (t + i * G);
+    if (e < N) store8(row + e, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = (8 * i + j) * G + t;
+      if (e < N) row[e] = from_f<T>(v[j]);
+    }
+  }
+}
+
+// Sum (or maximum) over the group's threads, the same bits in each. G > 32:
+// the group is the whole block; buf: G / 32 words of shared memory that no
+// other reduction in flight uses.
+template <int G, bool MAX>
+__device__ __forceinline__ float group_reduce(float v, float* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if (G == 32) return v;
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = buf[0];
+#pragma unroll
+  for (int k = 1; k < G / 32; ++k) v = MAX ? fmaxf(v, buf[k]) : v + buf[k];
+  return v;
+}
+
+template <class TX, class TY, int G, int V, bool ALIGNED>
+__global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdArgs a) {
+  constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
+  __shared__ float buf[2][32];
+  const int t = threadIdx.x % G;
+  const long long row = (long long)blockIdx.x * RPB + threadIdx.x / G;
+  if (row >= a.M) return;  // (a whole warp or the whole block)
+  const TX* x = static_cast<const TX*>(a.x) + row * a.ldx;
+  float s[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(x, i, t, a.N, s[i]);
+  if (a.res) {
+    const TX* r = static_cast<const TX*>(a.res) + row * a.ldr;
+    float v[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(r, i, t, a.N, v[i]);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = to_f(from_f<TX>(s[i][j] + v[i][j]));
+  }
+  if (a.sum) {
+    TX* o = static_cast<TX*>(a.sum) + row * a.lds;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(o, i, t, a.N, s[i]);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(s[i][j], s[i][j], ss);
+  ss = group_reduce<G, false>(ss, buf[0]);
+  const float r = 1.f / sqrtf(ss / float(a.N) + a.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float w[8];
+    if (a.w) {
+      load_set<ALIGNED, G>(a.w, i, t, a.N, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * w[j];
+  }
+  if (sizeof(TY) == 1) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[i][j]));
+    m = group_reduce<G, true>(m, buf[1]);
+    const float scale = fmaxf(m / kE4m3Max, 1.17549435e-38f), inv = 1.f / scale;
+    if (t == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] *= inv;
+  }
+  TY* y = static_cast<TY*>(a.y) + row * a.ldy;
+#pragma unroll
+  for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(y, i, t, a.N, s[i]);
+}
+
+// dx = r (g - s r^2 mean(g s)) + dsum with g = dy w and r = 1 / sqrt(mean(s^2)
+// + eps): both row sums come from one reading of s and dy. Blocks walk the
+// rows, so that a thread's weight-gradient sums (dy s r of its columns) stay
+// in registers over all of them; a block then writes one row of partial sums.
+template <class TY, class TX, int G, int V, bool ALIGNED>
+__global__ void __launch_bounds__(G > kBlock ? G : kBlock) bwd_kernel(const BwdArgs a) {
+  constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
+  __shared__ float buf[2][2][32];
+  __shared__ float wsum[G == 32 ? RPB : 1][G == 32 ? 8 * V * 32 : 1];
+  const int t = threadIdx.x % G, grp = threadIdx.x / G;
+  float dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  int par = 0;  // two sets of reduction buffers: a row's writes never meet the last row's reads
+  for (long long row = (long long)blockIdx.x * RPB + grp; row < a.M; row += (long long)gridDim.x * RPB, par ^= 1) {
+    float s[V][8], d[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(static_cast<const TX*>(a.s) + row * a.lds, i, t, a.N, s[i]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(static_cast<const TY*>(a.dy) + row * a.lddy, i, t, a.N, d[i]);
+    float ss = 0.f, gs = 0.f;
+    float w[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (a.w) {
+        load_set<ALIGNED, G>(a.w, i, t, a.N, w[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = fmaf(s[i][j], s[i][j], ss);
+        gs = fmaf(d[i][j] * w[i][j], s[i][j], gs);
+      }
+    }
+    ss = group_reduce<G, false>(ss, buf[par][0]);
+    gs = group_reduce<G, false>(gs, buf[par][1]);
+    const float r = 1.f / sqrtf(ss / float(a.N) + a.eps);
+    const float c = r * r * (gs / float(a.N));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] = fmaf(d[i][j] * r, s[i][j], dw[i][j]);
+        d[i][j] = r * (d[i][j] * w[i][j] - s[i][j] * c);
+      }
+    if (a.dsum) {
+      const TX* u = static_cast<const TX*>(a.dsum) + row * a.ldds;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v[8];
+        load_set<ALIGNED, G>(u, i, t, a.N, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i][j] += v[j];
+      }
+    }
+    TX* o = static_cast<TX*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(o, i, t, a.N, d[i]);
+  }
+  if (!a.part) return;
+  float* out = a.part + (long long)blockIdx.x * a.N;
+  if (G == 32) {  // the block's warps add up in shared memory, in warp order
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wsum[grp][(ALIGNED ? 8 * (t + i * G) + j : (8 * i + j) * G + t)] = dw[i][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.N; e += T) {
+      float v = wsum[0][e];
+#pragma unroll
+      for (int k = 1; k < RPB; ++k) v += wsum[k][e];
+      out[e] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = ALIGNED ? 8 * (t + i * G) + j : (8 * i + j) * G + t;
+        if (e < a.N) out[e] = dw[i][j];
+      }
+  }
+}
+
+// One variant per row length: (G, V) with 8 G V >= N, the smallest group first
+// (a longer row takes more sets per thread, then more threads).
+template <class F>
+bool by_length(int N, F&& f) {
+  if (N <= 256) return f.template operator()<32, 1>();
+  if (N <= 512) return f.template operator()<32, 2>();
+  if (N <= 1024) return f.template operator()<32, 4>();
+  if (N <= 2048) return f.template operator()<128, 2>();
+  if (N <= 4096) return f.template operator()<128, 4>();
+  if (N <= 8192) return f.template operator()<256, 4>();
+  if (N <= 16384) return f.template operator()<512, 4>();
+  return f.template operator()<1024, 4>();
+}
+
+bool aligned_rows(const void* p, long long ld, int es) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * es) % 16 == 0);
+}
+
+int esize(int dtype) { return dtype == DSF_F32 ? 4 : (dtype == DSF_BF16 ? 2 : 1); }
+
+long long bwd_blocks(long long M, int N) {
+  const long long rpb = N <= 1024 ? kBlock / 32 : 1;
+  const long long b = (M + rpb - 1) / rpb;
+  return b < kMaxPartials ? b : kMaxPartials;
+}
+
+template <class TX, class TY>
+struct Fwd {
+  const FwdArgs& a;
+  bool al;
+  cudaStream_t st;
+  template <int G, int V>
+  bool operator()() const {
+    constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
+    const unsigned grid = unsigned((a.M + RPB - 1) / RPB);
+    if (al) fwd_kernel<TX, TY, G, V, true><<<grid, T, 0, st>>>(a);
+    else fwd_kernel<TX, TY, G, V, false><<<grid, T, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+  }
+};
+template <class TY, class TX>
+struct Bwd {
+  const BwdArgs& a;
+  bool al;
+  cudaStream_t st;
+  template <int G, int V>
+  bool operator()() const {
+    constexpr int T = G == 32 ? kBlock : G;
+    const unsigned grid = unsigned(bwd_blocks(a.M, a.N));
+    if (al) bwd_kernel<TY, TX, G, V, true><<<grid, T, 0, st>>>(a);
+    else bwd_kernel<TY, TX, G, V, false><<<grid, T, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+  }
+};
+
+bool elem_aligned(const void* p, int es) { return (reinterpret_cast<uintptr_t>(p) % es) == 0; }
+
+}  // namespace
+}  // namespace norm
+}  // namespace dsf
+
+using namespace dsf;
+using namespace dsf::norm;
+
+extern "C" {
+
+int ctr_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldr, int32_t x_dtype, const float* w,
+                     int64_t M, int32_t N, float eps, void* sum, int64_t lds, void* y, int64_t ldy, int32_t y_dtype,
+                     float* y_scale, void* stream) {
+  if (M < 0 || M > INT32_MAX || N < 1 || !(eps > 0.f)) return DSF_EINVAL;
+  if (N > kMaxN) return DSF_EUNSUPPORTED;
+  if (x_dtype != DSF_F32 && x_dtype != DSF_BF16) return DSF_EUNSUPPORTED;
+  if (y_dtype != DSF_F32 && y_dtype != DSF_BF16 && y_dtype != DSF_E4M3) return DSF_EUNSUPPORTED;
+  if (M == 0) return DSF_OK;
+  const int ex = esize(x_dtype), ey = esize(y_dtype);
+  if (!x || !y || ldx < N || ldy < N || (res && ldr < N) || (sum && lds < N)) return DSF_EINVAL;
+  if (!elem_aligned(x, ex) || !elem_aligned(res, ex) || !elem_aligned(sum, ex) || !elem_aligned(y, ey) ||
+      !elem_aligned(w, 4) || !elem_aligned(y_scale, 4))
+    return DSF_EINVAL;
+  if ((y_dtype == DSF_E4M3) != (y_scale != nullptr)) return DSF_EINVAL;
+  const FwdArgs a{x, res, ldx, ldr, w, M, N, eps, sum, lds, y, ldy, y_scale};
+  const bool al = N % 8 == 0 && aligned_rows(x, ldx, ex) && aligned_rows(res, ldr, ex) &&
+                  aligned_rows(sum, lds, ex) && aligned_rows(w, 0, 4) &&
+                  (y_dtype == DSF_E4M3 ? (reinterpret_cast<uintptr_t>(y) % 8 == 0 && ldy % 8 == 0)
+                                       : aligned_rows(y, ldy, ey));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  bool ok;
+  if (x_dtype == DSF_F32) {
+    if (y_dtype == DSF_F32) ok = by_length(N, Fwd<float, float>{a, al, st});
+    else if (y_dtype == DSF_BF16) ok = by_length(N, Fwd<float, __nv_bfloat16>{a, al, st});
+    else ok = by_length(N, Fwd<float, __nv_fp8_e4m3>{a, al, st});
+  } else {
+    if (y_dtype == DSF_F32) ok = by_length(N, Fwd<__nv_bfloat16, float>{a, al, st});
+    else if (y_dtype == DSF_BF16) ok = by_length(N, Fwd<__nv_bfloat16, __nv_bfloat16>{a, al, st});
+    else ok = by_length(N, Fwd<__nv_bfloat16, __nv_fp8_e4m3>{a, al, st});
+  }
+  return ok ? DSF_OK : DSF_ECUDA;
+}
+
+size_t dsf_rms_norm_workspace_bytes(int64_t M, int32_t N) {
+  if (M < 0 || M > INT32_MAX || N < 1 || N > kMaxN) return 0;
+  const long long b = bwd_blocks(M, N);
+  return (size_t(b > 0 ? b : 1) * N * 4 + 255) / 256 * 256;
+}
+
+int ctr_rms_norm_bwd(const void* dy, int64_t lddy, int32_t dy_dtype, const void* s, int64_t lds, int32_t x_dtype,
+                     const float* w, int64_t M, int32_t N, float eps, const void* dsum, int64_t ldds, void* dx,
+                     int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream) {
+  if (M < 0 || M > INT32_MAX || N < 1 || !(eps > 0.f)) return DSF_EINVAL;
+  if (N > kMaxN) return DSF_EUNSUPPORTED;
+  if (x_dtype != DSF_F32 && x_dtype != DSF_BF16) return DSF_EUNSUPPORTED;
+  if (dy_dtype != DSF_F32 && dy_dtype != DSF_BF16) return DSF_EUNSUPPORTED;
+  const int ex = esize(x_dtype), ey = esize(dy_dtype);
+  if (!elem_aligned(dw, 4)) return DSF_EINVAL;
+  if (dw && (!ws || (reinterpret_cast<uintptr_t>(ws) % 256) || ws_bytes < dsf_rms_norm_workspace_bytes(M, N)))
+    return DSF_EWORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (dw && cudaMemsetAsync(dw, 0, size_t(N) * 4, st) != cudaSuccess) return DSF_ECUDA;
+    return DSF_OK;
+  }
+  if (!dy || !s || !dx || lddy < N || lds < N || lddx < N || (dsum && ldds < N)) return DSF_EINVAL;
+  if (!elem_aligned(dy, ey) || !elem_aligned(s, ex) || !elem_aligned(dsum, ex) || !elem_aligned(dx, ex) ||
+      !elem_aligned(w, 4))
+    return DSF_EINVAL;
+  const BwdArgs a{dy, s, dsum, lddy, lds, ldds, w, M, N, eps, dx, lddx, dw ? static_cast<float*>(ws) : nullptr};
+  const bool al = N % 8 == 0 && aligned_rows(dy, lddy, ey) && aligned_rows(s, lds, ex) &&
+                  aligned_rows(dsum, ldds, ex) && aligned_rows(dx, lddx, ex) && aligned_rows(w, 0, 4);
+  bool ok;
+  if (dy_dtype == DSF_F32)
+    ok = x_dtype == DSF_F32 ? by_length(N, Bwd<float, float>{a, al, st}) : by_length(N, Bwd<float, __nv_bfloat16>{a, al, st});
+  else
+    ok = x_dtype == DSF_F32 ? by_length(N, Bwd<__nv_bfloat16, float>{a, al, st})
+                            : by_length(N, Bwd<__nv_bfloat16, __nv_bfloat16>{a, al, st});
+  if (!ok) return DSF_ECUDA;
+  if (dw && !colsum(a.part, bwd_blocks(M, N), N, dw, st)) return DSF_ECUDA;
+  return DSF_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,437 @@
+"""The dense layer, the gated layer and the RMS norm against 64-bit
+evaluations (tests/dense_ref.py has the bounds), through the C ABI."""
+import pytest
+import torch
+
+import dense_ref as R
+from recsys_sparse_embedding_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+# 2-norm errors: one rounding to bf16 is off by at most 2^-8, 2^-8 / sqrt 3 = 2.3e-3 in the mean
+# over a binade; a gradient has two of them. fp32: sums of random sign, far below (K + 8) 2^-23.
+NORM_FWD = {BF16: 2.4e-3, F32: 3e-6}
+NORM_BWD = {BF16: 3.4e-3, F32: 3e-6}
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rnd(g, *shape, std=1.0):
+    return torch.randn(*shape, generator=g, device="cuda") * std
+
+
+def strided(t, extra, offset=0):
+    """t's values in rows `extra` elements longer, `offset` elements into the
+    buffer; NaN around them (e4m3: 0x7f bytes, its NaN)."""
+    rows, cols = t.shape
+    buf = torch.full((rows * (cols + extra) + offset + 64,), float("nan"), device=t.device).to(t.dtype)
+    v = buf[offset:offset + rows * (cols + extra)].view(rows, cols + extra)[:, :cols]
+    v.copy_(t)
+    return v, buf
+
+
+def is_nan(t):
+    return torch.isnan(t.float())
+
+
+def quantise(t):
+    s = (t.abs().amax(1) / 448).clamp_min(2.0 ** -126)
+    return (t / s[:, None]).to(E4M3), s
+
+
+def layer_of(g, dtype, rows, K, act, bias=True):
+    W = rnd(g, rows, K, std=(2.0 / (K + rows)) ** 0.5 * 2)
+    b = rnd(g, rows, std=0.3) if bias else None
+    ws = None
+    if dtype == E4M3:
+        W, ws = quantise(W)
+    return B.DenseLayer(W.to(dtype), b, act=R.ACTS[act], scale=ws)
+
+
+def x_of(g, dtype, M, K):
+    x = rnd(g, M, K)
+    return quantise(x) if dtype == E4M3 else (x.to(dtype), None)
+
+
+SIZES = [(1, 1, 1), (1, 256, 512), (2, 16, 8), (3, 37, 5), (8, 1024, 96), (9, 64, 300), (17, 176, 64), (64, 640, 33),
+         (127, 64, 129), (128, 128, 128), (129, 200, 257), (256, 512, 256), (300, 1000, 96), (513, 48, 1040),
+         (1000, 513, 300), (2049, 256, 512), (385, 2100, 700)]
+ACT_OF = ["none", "relu", "silu", "gelu"]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+@pytest.mark.parametrize("i", range(len(SIZES)))
+def test_dense_fwd(dtype, i):
+    M, K, N = SIZES[i]
+    g = gen(i)
+    for act in ACT_OF if M <= 130 else [ACT_OF[i % 4]]:
+        for with_res, bias in ((False, True), (True, False)):
+            layer = layer_of(g, dtype, N, K, act, bias)
+            x, xs = x_of(g, dtype, M, K)
+            res = rnd(g, M, N).to(layer.out_dtype) if with_res else None
+            ws = B.DenseWorkspace(layer, M)
+            y, buf = strided(torch.zeros(M, N, device="cuda").to(layer.out_dtype), 0)
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            B.ctr_dense_fwd(layer, x, y, ws, residual=res, x_scale=xs, status=st)
+            ref, tol = R.dense(x, layer.W, layer.bias, act, res, layer.out_dtype, xs, layer.scale)
+            assert int(st.item()) == 0
+            R.assert_within(y, ref, tol, "y %s" % act)
+            R.assert_norm(y, ref, NORM_FWD[layer.out_dtype], "y %s" % act, M, K, N)
+            assert is_nan(buf[M * N:]).all(), "written past the end"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+@pytest.mark.parametrize("i", range(len(SIZES)))
+def test_glu_fwd(dtype, i):
+    M, K, F = SIZES[i]
+    g = gen(100 + i)
+    for act in ACT_OF if M <= 130 else [ACT_OF[i % 4]]:
+        layer = layer_of(g, dtype, 2 * F, K, act, act != "relu")
+        x, xs = x_of(g, dtype, M, K)
+        ws = B.DenseWorkspace(layer, M, gated=True)
+        h, buf = strided(torch.zeros(M, F, device="cuda").to(layer.out_dtype), 0)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        B.ctr_glu_fwd(layer, x, h, ws, x_scale=xs, status=st)
+        ref, tol = R.glu(x, layer.W, layer.bias, act, layer.out_dtype, xs, layer.scale)
+        assert int(st.item()) == 0
+        R.assert_within(h, ref, tol, "h %s" % act)
+        R.assert_norm(h, ref, NORM_FWD[layer.out_dtype], "h %s" % act, M, K, F)
+        assert is_nan(buf[M * F:]).all(), "written past the end"
+
+
+def run_bwd(layer, x, dy, gated, **out):
+    ws = B.DenseWorkspace(layer, x.shape[0], gated=gated, backward=True)
+    ws.buf.fill_(0xff)  # (NaN in every type: nothing may be read before it is written)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    (B.ctr_glu_bwd if gated else B.ctr_dense_bwd)(layer, x, dy, ws, status=st, **out)
+    assert int(st.item()) == 0
+    return out
+
+
+def check_bwd(layer, x, dy, act, gated, out):
+    ref = R.grads(x, layer.W, layer.bias, act, dy, gated)
+    for name, t in out.items():
+        v, tol = ref[name]
+        R.assert_within(t, v, tol, "%s %s" % (name, act))
+        if act != "relu":  # (a ReLU's slope may go either way at z near 0)
+            R.assert_norm(t, v, 3e-6 if name == "db" else NORM_BWD[x.dtype], "%s %s" % (name, act),
+                          *x.shape, dy.shape[1])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("i", range(len(SIZES)))
+def test_layer_bwd(dtype, gated, i):
+    M, K, N = SIZES[i]
+    g = gen(200 + i)
+    for act in ACT_OF if M <= 130 else [ACT_OF[i % 4], ACT_OF[(i + 2) % 4]]:
+        layer = layer_of(g, dtype, 2 * N if gated else N, K, act, act != "gelu")
+        x, _ = x_of(g, dtype, M, K)
+        dy = rnd(g, M, N).to(dtype)
+        out = run_bwd(layer, x, dy, gated, dx=torch.empty_like(x), dW=torch.empty(layer.R, K, dtype=dtype, device="cuda"),
+                      db=torch.empty(layer.R, device="cuda"))
+        check_bwd(layer, x, dy, act, gated, out)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_layer_bwd_takes_any_of_its_outputs(dtype, gated):
+    g = gen(7)
+    M, K, N = 200, 96, 136
+    layer = layer_of(g, dtype, 2 * N if gated else N, K, "silu")
+    x, _ = x_of(g, dtype, M, K)
+    dy = rnd(g, M, N).to(dtype)
+    new = {"dx": lambda: torch.empty_like(x), "dW": lambda: torch.empty_like(layer.W),
+           "db": lambda: torch.empty(layer.R, device="cuda")}
+    for names in (("dx",), ("dW",), ("db",), ("dx", "db"), ()):
+        out = run_bwd(layer, x, dy, gated, **{n: new[n]() for n in names})
+        check_bwd(layer, x, dy, "silu", gated, out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+@pytest.mark.parametrize("extra,offset", [(16, 0), (16, 16), (3, 1), (1, 0)])
+def test_strided_rows(dtype, extra, offset):
+    """Rows longer than their matrix, buffers that start off a boundary (where
+    the row's own length allows it: K = 45 here), an in-place residual."""
+    g = gen(extra * 7 + offset)
+    whole = extra % 16 == 0
+    M, K, N = 150, 48 if whole else 45, 80 if whole else 77
+    layer = layer_of(g, dtype, N, K, "silu")
+    x, xs = x_of(g, dtype, M, K)
+    x, _ = strided(x, extra, offset)
+    res = rnd(g, M, N).to(layer.out_dtype)
+    y, buf = strided(res, extra, offset)
+    ws = B.DenseWorkspace(layer, M)
+    keep = is_nan(buf)
+    B.ctr_dense_fwd(layer, x, y, ws, residual=y, x_scale=xs)
+    ref, tol = R.dense(x, layer.W, layer.bias, "silu", res, layer.out_dtype, xs, layer.scale)
+    R.assert_within(y, ref, tol, "y")
+    assert is_nan(buf)[keep].all(), "written between the rows"
+    if dtype != E4M3:
+        dy, _ = strided(rnd(g, M, N).to(dtype), extra, offset)
+        dx, buf = strided(torch.zeros(M, K, device="cuda").to(dtype), extra, offset)
+        keep = is_nan(buf)
+        out = run_bwd(layer, x, dy, False, dx=dx, dW=torch.empty(N, K, dtype=dtype, device="cuda"),
+                      db=torch.empty(N, device="cuda"))
+        check_bwd(layer, x, dy, "silu", False, out)
+        assert is_nan(buf)[keep].all(), "written between the rows"
+
+
+def test_weights_with_a_row_stride():
+    g = gen(5)
+    for dtype in (BF16, F32):
+        W, _ = strided(rnd(g, 96, 64, std=0.1).to(dtype), 32)
+        layer = B.DenseLayer(W, None, act=B.DSF_ACT_GELU)
+        x, _ = x_of(g, dtype, 140, 64)
+        dy = rnd(g, 140, 96).to(dtype)
+        y = torch.empty(140, 96, dtype=dtype, device="cuda")
+        B.ctr_dense_fwd(layer, x, y, B.DenseWorkspace(layer, 140))
+        ref, tol = R.dense(x, W, None, "gelu", None, dtype)
+        R.assert_within(y, ref, tol, "y")
+        out = run_bwd(layer, x, dy, False, dx=torch.empty_like(x), dW=torch.empty(96, 64, dtype=dtype, device="cuda"),
+                      db=torch.empty(96, device="cuda"))
+        check_bwd(layer, x, dy, "gelu", False, out)
+
+
+@pytest.mark.parametrize("M", [1, 5, 200])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_non_finite_rows_stay_apart(dtype, bad, M):
+    """A row of x with a non-finite value gives non-finite results in its own
+    row only; other rows keep their bits."""
+    g = gen(M)
+    K, N = 192, 130
+    layer = layer_of(g, dtype, N, K, "silu")
+    x, _ = x_of(g, dtype, M, K)
+    ws = B.DenseWorkspace(layer, M)
+    clean, dirty = (torch.empty(M, N, dtype=dtype, device="cuda") for _ in range(2))
+    B.ctr_dense_fwd(layer, x, clean, ws)
+    row = M // 2
+    x[row, 100] = bad
+    B.ctr_dense_fwd(layer, x, dirty, ws)
+    others = torch.arange(M, device="cuda") != row
+    assert torch.equal(clean[others], dirty[others])
+    d = dirty[row].float()
+    if bad != bad:
+        assert torch.isnan(d).all()
+    elif dtype == F32:  # (an infinite operand's terms may cancel to NaN)
+        assert not torch.isfinite(d).any()
+    else:  # +-inf by the weight's sign, through SiLU: inf, or -inf / inf
+        w = layer.W[:, 100].float() * bad
+        assert torch.isposinf(d[w > 0]).all() and torch.isnan(d[w < 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_zero_rows(dtype):
+    g = gen(1)
+    layer = layer_of(g, dtype, 24, 40, "silu")
+    x = torch.empty(0, 40, dtype=dtype, device="cuda")
+    y = torch.empty(0, 24, dtype=dtype, device="cuda")
+    ws = B.DenseWorkspace(layer, 0, backward=True)
+    B.ctr_dense_fwd(layer, x, y, ws)
+    dW, db = torch.ones(24, 40, dtype=dtype, device="cuda"), torch.ones(24, device="cuda")
+    B.ctr_dense_bwd(layer, x, y, ws, dx=torch.empty_like(x), dW=dW, db=db)
+    assert not dW.any() and not db.any()
+
+
+def test_extreme_fp32_values():
+    """Operands at fp32's ends: the largest finite value, its products with
+    small weights, and denormals."""
+    K = 48
+    x = torch.zeros(130, K, device="cuda")
+    top = torch.finfo(F32).max
+    x[0, 0], x[1, 1], x[2, 2], x[3, 3] = top, -top, 1e-40, 3.39e38
+    W = torch.full((40, K), 0.25, device="cuda")
+    layer = B.DenseLayer(W)
+    y = torch.empty(130, 40, device="cuda")
+    B.ctr_dense_fwd(layer, x, y, B.DenseWorkspace(layer, 130))
+    ref = x.double() @ W.double().t()
+    assert torch.isfinite(y).all()
+    R.assert_within(y, ref, 56 * R.U * ref.abs() + 1e-38, "y")
+    assert not y[4:].any()
+
+
+def test_offsets_past_32_bits():
+    """An output of more than 2^31 elements; the rows around that offset and
+    the last ones are checked."""
+    N, K, g = 1032, 16, gen(3)
+    M = 2 ** 31 // N + 300
+    layer = layer_of(g, BF16, N, K, "relu")
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=BF16)
+    y = torch.empty(M, N, dtype=BF16, device="cuda")
+    B.ctr_dense_fwd(layer, x, y, B.DenseWorkspace(layer, M))
+    for a in (0, 2 ** 31 // N - 130, M - 257):
+        s = slice(a, min(M, a + 257))
+        ref, tol = R.dense(x[s], layer.W, layer.bias, "relu", None, BF16)
+        R.assert_within(y[s], ref, tol, "rows from %d" % a)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_equal_inputs_give_equal_bits(dtype):
+    g = gen(9)
+    M, K, N = 3000, 264, 392
+    layer = layer_of(g, dtype, 2 * N, K, "silu")
+    x, _ = x_of(g, dtype, M, K)
+    dy = rnd(g, M, N).to(dtype)
+    runs = []
+    for _ in range(3):
+        o = run_bwd(layer, x, dy, True, dx=torch.empty_like(x), dW=torch.empty_like(layer.W),
+                    db=torch.empty(layer.R, device="cuda"))
+        runs.append([t.clone() for t in o.values()])
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], r))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 700])
+def test_captured_and_replayed(dtype, M):
+    """Forward and backward captured into one graph: replays on new inputs in
+    the same buffers give what eager calls give, while an eager call runs on
+    another stream in its own workspace."""
+    g = gen(11)
+    K, N = 200, 168
+    layer = layer_of(g, dtype, 2 * N, K, "gelu")
+    x, _ = x_of(g, dtype, M, K)
+    dy = rnd(g, M, N).to(dtype)
+
+    def buffers():
+        return (torch.empty(M, N, dtype=dtype, device="cuda"), torch.empty_like(x), torch.empty_like(layer.W),
+                torch.empty(layer.R, device="cuda"), B.DenseWorkspace(layer, M, gated=True, backward=True))
+
+    def call(b, x, dy, stream=None):
+        B.ctr_glu_fwd(layer, x, b[0], b[4], stream=stream)
+        B.ctr_glu_bwd(layer, x, dy, b[4], dx=b[1], dW=b[2], db=b[3], stream=stream)
+
+    eager, graphed = buffers(), buffers()
+    call(eager, x, dy)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(graphed, x, dy)
+    other = torch.cuda.Stream()
+    for k in range(3):
+        x.copy_(rnd(g, M, K).to(dtype))
+        dy.copy_(rnd(g, M, N).to(dtype))
+        torch.cuda.synchronize()
+        graph.replay()
+        call(eager, x, dy, stream=other)
+        torch.cuda.synchronize()
+        for a, b in zip(eager[:4], graphed[:4]):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ RMS norm
+NORM_SIZES = [(1, 1), (1, 256), (3, 7), (5, 33), (64, 256), (9, 1000), (130, 1024), (33, 1032), (257, 48), (7, 2048),
+              (12, 3001), (3, 4096), (2, 8192), (3, 9999), (2, 16392), (2, 32768), (5000, 264)]
+
+
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("yt", [F32, BF16, E4M3])
+@pytest.mark.parametrize("i", range(len(NORM_SIZES)))
+def test_norm_fwd(xt, yt, i):
+    M, N = NORM_SIZES[i]
+    g = gen(i)
+    for with_res, with_w, extra in ((True, True, 0), (False, False, 0), (True, True, 3)):
+        x, _ = strided((rnd(g, M, N) * torch.exp(rnd(g, M, 1))).to(xt), extra)
+        res = rnd(g, M, N).to(xt) if with_res else None
+        w = 1 + 0.3 * rnd(g, N) if with_w else None
+        y, buf = strided(torch.zeros(M, N, device="cuda").to(yt), extra)
+        keep = is_nan(buf)
+        s = torch.empty(M, N, dtype=xt, device="cuda") if with_res else None
+        ys = torch.empty(M, device="cuda") if yt == E4M3 else None
+        B.ctr_rms_norm_fwd(x, y, weight=w, residual=res, sum_out=s, eps=1e-6, y_scale=ys)
+        assert is_nan(buf)[keep].all(), "written between the rows"
+        if with_res:
+            assert torch.equal(s, (x.float() + res.float()).to(xt))
+        ref, _ = R.norm(s if with_res else x, w, 1e-6)
+        tol = (N + 8) * R.U * ref.abs() + 1e-38  # (the row sum's bound halves in the root)
+        if yt == E4M3:
+            want = (ref.abs().amax(1) / 448).clamp_min(2.0 ** -126)
+            assert ((ys.double() - want).abs() <= (N + 10) * R.U * want).all()
+            # half a step of e4m3 (2^-4 of the value; 2^-10 below its smallest normal), as values
+            q = y.double() * ys.double()[:, None]
+            R.assert_within(q, ref, 2.0 ** -4 * ref.abs() + 2.0 ** -10 * want[:, None] + 3 * tol, "y e4m3")
+            assert (y.float().abs().amax(1)[want > 2.0 ** -126] == 448).all()
+        else:
+            R.assert_within(y, ref, tol + R.HALF[yt] * (ref.abs() + tol), "y")
+
+
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("i", range(len(NORM_SIZES)))
+def test_norm_bwd(xt, dt, i):
+    M, N = NORM_SIZES[i]
+    g = gen(300 + i)
+    for with_sum, with_w, extra in ((True, True, 0), (False, False, 0), (True, True, 5)):
+        s, _ = strided((rnd(g, M, N) * torch.exp(rnd(g, M, 1))).to(xt), extra)
+        dy = rnd(g, M, N).to(dt)
+        w = 1 + 0.3 * rnd(g, N) if with_w else None
+        up = rnd(g, M, N).to(xt) if with_sum else None
+        dx, buf = strided(torch.zeros(M, N, device="cuda").to(xt), extra)
+        keep = is_nan(buf)
+        dw = torch.empty(N, device="cuda") if with_w else None
+        B.ctr_rms_norm_bwd(dy, s, dx, weight=w, eps=1e-5, dsum=up, dweight=dw,
+                           workspace=B.RmsNormWorkspace(M, N) if with_w else None)
+        rx, tx, rw, tw = R.norm_grads(dy, s, w, 1e-5, up)
+        R.assert_within(dx, rx, tx + R.HALF[xt] * (rx.abs() + tx) + 1e-38, "dx")
+        assert is_nan(buf)[keep].all(), "written between the rows"
+        if with_w:
+            R.assert_within(dw, rw, tw, "dweight")
+
+
+def test_norm_in_place_and_odd_rows():
+    """The sum written over the residual, dx over the upstream gradient; rows
+    of zeros (scale 2^-126, values 0), of NaN, and of infinities."""
+    g = gen(2)
+    x, res = rnd(g, 40, 512).to(BF16), rnd(g, 40, 512).to(BF16)
+    x[3], res[3] = 0, 0
+    x[5, 9] = float("nan")
+    x[7, 11] = float("inf")
+    want = (x.float() + res.float()).to(BF16)
+    y, ys = torch.empty(40, 512, device="cuda").to(E4M3), torch.empty(40, device="cuda")
+    B.ctr_rms_norm_fwd(x, y, residual=res, sum_out=res, y_scale=ys)
+    assert torch.equal(res.nan_to_num(7), want.nan_to_num(7))
+    assert float(ys[3]) == 2.0 ** -126 and not y[3].float().any()
+    assert is_nan(y[5]).all() and is_nan(y[7, 11])
+    rest = [i for i in range(40) if i not in (5, 7)]
+    assert not is_nan(y[rest]).any()
+    s, dy, up = rnd(g, 40, 512).to(BF16), rnd(g, 40, 512).to(BF16), rnd(g, 40, 512).to(BF16)
+    rx, tx, _, _ = R.norm_grads(dy, s, None, 1e-6, up)
+    B.ctr_rms_norm_bwd(dy, s, up, dsum=up)
+    R.assert_within(up, rx, tx + R.HALF[BF16] * (rx.abs() + tx), "dx")
+
+
+def test_norm_zero_rows():
+    dw = torch.ones(16, device="cuda")
+    z = torch.empty(0, 16, device="cuda")
+    B.ctr_rms_norm_fwd(z, torch.empty_like(z))
+    B.ctr_rms_norm_bwd(z, z, torch.empty_like(z), dweight=dw, workspace=B.RmsNormWorkspace(0, 16))
+    assert not dw.any()
+
+
+# ------------------------------------------------------------------ the binding's refusals
+def test_binding_refuses_wrong_tensors():
+    g = gen(0)
+    layer = layer_of(g, BF16, 32, 64, "none")
+    x, y = rnd(g, 4, 64).to(BF16), torch.empty(4, 32, dtype=BF16, device="cuda")
+    ws = B.DenseWorkspace(layer, 4)
+    for args in ((x.float(), y), (x, y.float()), (x[:, :32], y), (x.cpu(), y), (x, y[:, :16]), (x, y.t()),
+                 (x.t().contiguous().t(), y)):
+        with pytest.raises(ValueError):
+            B.ctr_dense_fwd(layer, *args, ws)
+    with pytest.raises(ValueError):
+        B.ctr_dense_fwd(layer, x, y, ws, x_scale=torch.ones(4, device="cuda"))
+    with pytest.raises(ValueError):
+        B.DenseLayer(rnd(g, 8, 8).to(E4M3))
+    with pytest.raises(ValueError):
+        B.DenseLayer(rnd(g, 8, 8).half())
+    with pytest.raises(B.DsfError):  # a workspace without room for the backward
+        B.ctr_dense_bwd(layer, x, y, B.DenseWorkspace(layer, 0), dx=torch.empty_like(x))
+    with pytest.raises(B.DsfError):  # 16-byte rows at an odd address
+        B.ctr_dense_fwd(layer, strided(x, 8, 1)[0], y, ws)
+    with pytest.raises(B.DsfError):
+        B.ctr_rms_norm_fwd(x, torch.empty_like(x), eps=0.0)
