@@ -5,9 +5,11 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "colsum.cuh"
-#include "dense_math.cuh"
+#include "dense_small.cuh"
+#include "dense_tc.cuh"
 #include "dinsparse.h"
 
 namespace dsf {
@@ -39,156 +41,511 @@ int check_layer(const dsf_dense* l, bool gated) {
   return DSF_OK;
 }
 
-// Workspace: dz of the backward in fp32, [M, R].
+// ---------------------------------------------------------------- the products' shapes
+constexpr int kSms = 152;
+constexpr int kMaxSplits = 32;
+// partial sums of a split product: units fill the chip at most once, and a
+// unit holds at most 256 x 256 fp32 per pair of SMs
+constexpr size_t kPartBytes = size_t(kSms / 2) * 256 * 256 * 4;
+
+struct Plan {
+  int cfg, mt, nt, kbps, splits;
+};
+
+// Tile configuration and K-splits by an estimate in SM cycles: a K-block of
+// a 256 x 256 tile (on two SMs; fp32: 256 x 128), 128 x 128 or 128 x 64 tile takes kStep
+// cycles, the chip takes its units in whole waves, and a split product pays
+// for a second launch and its partial sums' way to L2 and back.
+Plan plan(long long M, long long N, int nb, bool gated, bool f32, long long nkb, int nseg, bool may_split) {
+  const double kStep[3] = {f32 ? 300. : 540., 300, 230};
+  constexpr double kUnit = 1500, kSecond = 5000, kBytesPerCycle = 2000;
+  Plan best{};
+  double cost = 1e300;
+  for (int cfg = 0; cfg < 3; ++cfg) {
+    if (cfg == 2 && gated) continue;
+    const long long on = cfg_bn(cfg, f32) / (gated ? 2 : 1), mt = (M + cfg_rows(cfg) - 1) / cfg_rows(cfg),
+                    nt = (N + on - 1) / on, tiles = mt * nt * nb, slots = cfg == 0 ? kSms / 2 : kSms;
+    if (tiles > INT32_MAX / 64) continue;
+    for (int want = 1; want <= kMaxSplits && want <= nkb; ++want) {
+      if (want > 1 && (!may_split || tiles * want > slots)) break;
+      const long long kbps = (nkb + want - 1) / want, splits = (nkb + kbps - 1) / kbps;
+      if (splits != want) continue;
+      const long long waves = (tiles * splits + slots - 1) / slots;
+      double c = kUnit + double(waves) * (kStep[cfg] * double(kbps) * nseg + 300);
+      if (splits > 1) c += kSecond + double(splits) * double(M) * double(N) * nb * (gated ? 2 : 1) * 8 / kBytesPerCycle;
+      if (c < cost) {
+        cost = c;
+        best = Plan{cfg, int(mt), int(nt), int(kbps), int(splits)};
+      }
+    }
+  }
+  return best;
+}
+
+long long up(long long v, long long to) { return (v + to - 1) / to * to; }
+
+// Workspace layout of a call: each part's offset; `total` grows with M.
+struct Layout {
+  size_t xp, wp, gp, dz, dzp, sums, part, total;
+  long long kp, np;  // padded row lengths of the laid-out operands and of dz
+};
+
+// Whether an operand with rows of `cols` elements is laid out in the workspace.
+bool laid_out(int dtype, long long cols) { return dtype == DSF_F32 || (cols * esize(dtype)) % 16 != 0; }
+
+Layout layout(const dsf_dense* l, long long M, bool gated, bool backward) {
+  Layout w{};
+  const int es = esize(l->dtype), terms = l->dtype == DSF_F32 ? 3 : 1, pes = l->dtype == DSF_F32 ? 2 : es;
+  const long long N = gated ? l->R / 2 : l->R, halves = gated ? 2 : 1;
+  w.kp = up(l->K, 16 / pes);
+  w.np = up(N, 8);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  auto part_of = [](size_t outputs) {
+    const size_t b = outputs * 4 * kMaxSplits;
+    return b < kPartBytes ? b : kPartBytes;
+  };
+  const bool lo = laid_out(l->dtype, l->K);
+  w.xp = take(lo ? size_t(terms) * M * w.kp * pes : 0);
+  w.wp = take(lo ? size_t(terms) * l->R * w.kp * pes : 0);
+  size_t part = part_of(size_t(M) * up(N, 4) * halves);
+  if (backward) {
+    const bool own_dz = gated || l->act != DSF_ACT_NONE;  // else dz is dy
+    w.gp = take(!own_dz && laid_out(l->dtype, N) ? size_t(terms) * M * w.np * pes : 0);
+    w.dz = take(own_dz ? size_t(halves) * M * w.np * es : 0);
+    w.dzp = take(own_dz && terms == 3 ? size_t(3) * halves * M * w.np * 2 : 0);
+    w.sums = take(size_t((M + 31) / 32) * l->R * 4);
+    const size_t px = part_of(size_t(M) * up(l->K, 4)), pw = part_of(size_t(l->R) * up(l->K, 4));
+    part = part > px ? part : px;
+    part = part > pw ? part : pw;
+  }
+  w.part = take(part);
+  w.total = o + 256;
+  return w;
+}
+
 size_t ws_bytes_of(const dsf_dense* l, long long M, bool gated, bool backward) {
-  return align256(256 + (backward ? size_t(M) * l->R * 4 : 0));
+  return layout(l, M, gated, backward).total;
 }
 
-__device__ __forceinline__ float ld_f(const float* p) { return *p; }
-__device__ __forceinline__ float ld_f(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float ld_f(const __nv_fp8_e4m3* p) { return float(*p); }
-__device__ __forceinline__ void st_f(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// acc[m][n] = sum over k of A(m, k) B(n, k), tiles of 64 x 64 by 256 threads,
-// K-steps of 16 through shared memory; epi(m, n, acc, acc of row n + gap).
-template <class TA, class TB, bool GATED, class Epi>
-__global__ void __launch_bounds__(256) product_kernel(const TA* A, long long am, long long ak, const TB* B,
-                                                      long long bn, long long bk, long long M, int N, long long K,
-                                                      int gap, const Epi epi) {
-  constexpr int T = 64, BK = 16, NB = GATED ? 2 : 1;
-  __shared__ float As[BK][T + 1], Bs[NB][BK][T + 1];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const long long m0 = (long long)blockIdx.x * T;
-  const int n0 = blockIdx.y * T;
-  float acc[NB][4][4] = {};
-  for (long long k0 = 0; k0 < K; k0 += BK) {
-    for (int e = tid; e < T * BK; e += 256) {
-      const int r = e / BK, c = e % BK;
-      const long long k = k0 + c, m = m0 + r;
-      const int n = n0 + r;
-      As[c][r] = m < M && k < K ? ld_f(A + m * am + k * ak) : 0.f;
-#pragma unroll
-      for (int h = 0; h < NB; ++h)
-        Bs[h][c][r] = n < N && k < K ? ld_f(B + (long long)(n + h * gap) * bn + k * bk) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < BK; ++c)
-#pragma unroll
-      for (int h = 0; h < NB; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[h][i][j] = fmaf(As[c][ty * 4 + i], Bs[h][c][tx * 4 + j], acc[h][i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const long long m = m0 + ty * 4 + i;
-      const int n = n0 + tx * 4 + j;
-      if (m < M && n < N) epi(m, n, acc[0][i][j], GATED ? acc[NB - 1][i][j] : 0.f);
-    }
-}
-
-__device__ __forceinline__ float act_any(int act, float z) {
-  return act == DSF_ACT_RELU ? act_value<DSF_ACT_RELU>(z)
-                             : (act == DSF_ACT_SILU ? act_value<DSF_ACT_SILU>(z)
-                                                    : (act == DSF_ACT_GELU ? act_value<DSF_ACT_GELU>(z) : z));
-}
-__device__ __forceinline__ float2 both_any(int act, float z) {
-  return act == DSF_ACT_RELU
-             ? act_both<DSF_ACT_RELU>(z)
-             : (act == DSF_ACT_SILU ? act_both<DSF_ACT_SILU>(z)
-                                    : (act == DSF_ACT_GELU ? act_both<DSF_ACT_GELU>(z) : make_float2(z, 1.f)));
-}
-
-template <class TO>
-struct FwdEpi {
-  TO* y;
-  const TO* res;
-  const float *bias, *xs, *ws;
-  long long ldy, ldr;
-  int act, gap;  // gap > 0: the gated layer, F
-  __device__ float z(long long m, int n, float acc) const {
-    if (xs) acc *= xs[m] * ws[n];
-    return bias ? acc + bias[n] : acc;
-  }
-  __device__ void operator()(long long m, int n, float a, float b) const {
-    float v = act_any(act, z(m, n, a));
-    if (gap) v *= z(m, n + gap, b);
-    if (res) v += ld_f(res + m * ldr + n);
-    st_f(y + m * ldy + n, v);
-  }
+// ---------------------------------------------------------------- small kernels
+// Lays a matrix out for the products: rows of `cols` elements from src (row
+// stride ld) into rows of ldd. fp32: the three bf16 terms, plane t at t *
+// rows * ldd; otherwise a copy. One thread per 8 (16-bit) or 16 (8-bit)
+// elements of a destination row.
+struct LayJob {
+  const void* src;
+  void* dst;
+  long long ld, rows, ldd, cols;
 };
 
-template <class T>
-struct DzEpi {
-  const T* dy;
-  const float* bias;
-  long long lddy;
-  float* dz;  // [M][R]
-  int act, gap, R;
-  __device__ void operator()(long long m, int n, float a, float b) const {
-    const float g = ld_f(dy + m * lddy + n);
-    const float2 f = both_any(act, bias ? a + bias[n] : a);
-    if (gap) {
-      const float u = bias ? b + bias[n + gap] : b;
-      dz[m * R + n] = g * u * f.y;
-      dz[m * R + n + gap] = g * f.x;
+// x's leading 8 significant bits, and what is left, three times: exact for
+// every finite x (the last term may fall below bf16's smallest denormal).
+// A non-finite x keeps its first term and has zeros after it.
+__device__ __forceinline__ void three_terms(float x, uint32_t* t) {
+  const uint32_t u = __float_as_uint(x), h1 = u & 0xffff0000u;
+  const bool fin = (u & 0x7f800000u) != 0x7f800000u;
+  const float r1 = fin ? x - __uint_as_float(h1) : 0.f;
+  const uint32_t h2 = __float_as_uint(r1) & 0xffff0000u;
+  const float r2 = r1 - __uint_as_float(h2);
+  // (a NaN whose payload lies in the low half stays a NaN)
+  t[0] = !fin && (u & 0x007fffffu) ? 0x7fc0u : h1 >> 16;
+  t[1] = h2 >> 16;
+  t[2] = __float_as_uint(r2) >> 16;
+}
+
+template <int ES>  // source element: 4 (fp32 -> three bf16 terms), 2 or 1 (copied)
+__global__ void __launch_bounds__(256) lay_kernel(const LayJob j0, const LayJob j1, const LayJob j2, int b0, int b1) {
+  const int blk = int(blockIdx.x), which = blk < b0 ? 0 : (blk < b1 ? 1 : 2);
+  const LayJob& j = which == 0 ? j0 : (which == 1 ? j1 : j2);
+  const int nblk = which == 0 ? b0 : (which == 1 ? b1 - b0 : int(gridDim.x) - b1);
+  const int local = blk - (which == 0 ? 0 : (which == 1 ? b0 : b1));
+  constexpr int V = ES == 1 ? 16 : 8;
+  const long long per_row = j.ldd / V, total = j.rows * per_row;
+  for (long long i = (long long)local * 256 + threadIdx.x; i < total; i += (long long)nblk * 256) {
+    const long long r = i / per_row;
+    const int c = int(i - r * per_row) * V;
+    if constexpr (ES == 4) {
+      const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
+      float x[8];
+      if (c + 8 <= j.cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
+        const float4 p = reinterpret_cast<const float4*>(s)[0], q = reinterpret_cast<const float4*>(s)[1];
+        x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = c + k < j.cols ? s[k] : 0.f;
+      }
+      uint32_t w[3][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t lo[3], hi[3];
+        three_terms(x[2 * k], lo);
+        three_terms(x[2 * k + 1], hi);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) w[t][k] = lo[t] | hi[t] << 16;
+      }
+      uint16_t* d = static_cast<uint16_t*>(j.dst) + r * j.ldd + c;
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint4*>(d + t * j.rows * j.ldd) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
     } else {
-      dz[m * R + n] = g * f.y;
+      using E = typename std::conditional<ES == 2, uint16_t, uint8_t>::type;
+      const E* s = static_cast<const E*>(j.src) + r * j.ld + c;
+      uint32_t w[4] = {};
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c + k < j.cols) w[k * ES / 4] |= uint32_t(s[k]) << (8 * ES * (k % (4 / ES)));
+      *reinterpret_cast<uint4*>(static_cast<E*>(j.dst) + r * j.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-};
+}
 
-template <class T>
-struct OutEpi {
-  T* o;
-  long long ld;
-  __device__ void operator()(long long m, int n, float a, float) const { st_f(o + m * ld + n, a); }
-};
-
-template <class TA, class TB, bool GATED, class Epi>
-bool product(const TA* A, long long am, long long ak, const TB* B, long long bn, long long bk, long long M, int N,
-             long long K, int gap, const Epi& epi, cudaStream_t s) {
-  product_kernel<TA, TB, GATED><<<dim3(unsigned((M + 63) / 64), unsigned((N + 63) / 64)), 256, 0, s>>>(
-      A, am, ak, B, bn, bk, M, N, K, gap, epi);
+bool lay(int dtype, const LayJob* jobs, int n, cudaStream_t s) {
+  LayJob j[3] = {};
+  int b[3] = {}, tot = 0;
+  const int V = dtype == DSF_E4M3 ? 16 : 8;
+  for (int i = 0; i < n; ++i) {
+    j[i] = jobs[i];
+    const long long blocks = (jobs[i].rows * (jobs[i].ldd / V) + 255) / 256;
+    b[i] = int(blocks < kSms * 16 ? blocks : kSms * 16);
+    tot += b[i];
+  }
+  if (tot == 0) return true;
+  if (dtype == DSF_F32) lay_kernel<4><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
+  else if (dtype == DSF_BF16) lay_kernel<2><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
+  else lay_kernel<1><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
   return cudaGetLastError() == cudaSuccess;
 }
 
-template <class T, class TO>
+// Sums over blocks of 256 rows of a matrix (db where dz is dy): part[block][n].
+constexpr int kSumRows = 256;
+template <class T>
+__global__ void __launch_bounds__(256) row_block_sums_kernel(const T* g, long long ld, long long M, int N, float* part) {
+  __shared__ float p[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.y * 32 + lane;
+  const long long r0 = (long long)blockIdx.x * kSumRows;
+  float s = 0.f;
+  if (n < N) {
+#pragma unroll 8
+    for (int i = 0; i < kSumRows / 8; ++i) {
+      const long long r = r0 + w + 8 * i;
+      if (r < M) s += elem(g[r * ld + n]);
+    }
+  }
+  p[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && n < N) {
+    float v = p[0][lane];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += p[k][lane];
+    part[(long long)blockIdx.x * N + n] = v;
+  }
+}
+
+// The end of a split product: the splits' partial sums, added in order, then
+// the forward's epilogue (fwd) or the plain sum. Four columns per thread.
+struct FinishArgs {
+  const float* part;  // [splits][planes][M][ldp]
+  long long M, ldp;
+  int N, splits, planes;
+  bool fwd, gated;
+  const float *bias, *xs, *ws;
+  const void* res;
+  long long ldr;
+  void* out;
+  long long ldo, out_plane;
+  int act;
+};
+template <class TO>
+__global__ void __launch_bounds__(256) finish_kernel(const FinishArgs a) {
+  const long long n4 = a.ldp / 4, per = a.M * n4, plane = a.M * a.ldp;
+  const long long total = per * (a.gated ? 1 : a.planes);
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long b = i / per, r = i - b * per, m = r / n4;
+    const int n = int(r - m * n4) * 4;
+    float v[2][4] = {};
+    const float* p = a.part + b * plane + m * a.ldp + n;
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) {
+      const float* q = p + (long long)z * a.planes * plane;
+      const float4 f = *reinterpret_cast<const float4*>(q);
+      v[0][0] += f.x, v[0][1] += f.y, v[0][2] += f.z, v[0][3] += f.w;
+      if (a.gated) {
+        const float4 h = *reinterpret_cast<const float4*>(q + plane);
+        v[1][0] += h.x, v[1][1] += h.y, v[1][2] += h.z, v[1][3] += h.w;
+      }
+    }
+    TO* o = static_cast<TO*>(a.out) + b * a.out_plane + m * a.ldo + n;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (n + k >= a.N) break;
+      float z = v[0][k];
+      if (a.fwd) {
+        if (a.xs) z *= a.xs[m] * a.ws[n + k];
+        if (a.bias) z += a.bias[n + k];
+        z = act_any(a.act, z);
+        if (a.gated) {
+          float u = v[1][k];
+          if (a.xs) u *= a.xs[m] * a.ws[a.N + n + k];
+          if (a.bias) u += a.bias[a.N + n + k];
+          z *= u;
+        }
+        if (a.res) z += elem(static_cast<const TO*>(a.res)[m * a.ldr + n + k]);
+      }
+      o[k] = TO(z);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+// The six pairs of terms, smallest products first.
+constexpr int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+
+bool tma_ok(const void* p, long long ld, int es) { return at(p, 16) && (ld * es) % 16 == 0; }
+
+struct Ctx {
+  const dsf_dense* l;
+  bool gated;
+  long long M;
+  int N, halves, es, eo, terms, kbe;  // kbe: K elements per K-block
+  uint8_t* ws;
+  Layout w;
+  int* status;
+  cudaStream_t s;
+  Mat X, W;  // operands [terms][M][K], [terms * halves][N][K]
+};
+
+Ctx context(const dsf_dense* l, bool gated, const void* x, long long ldx, long long M, void* ws, bool backward,
+            int* status, cudaStream_t s) {
+  Ctx c{};
+  c.l = l;
+  c.gated = gated;
+  c.M = M;
+  c.halves = gated ? 2 : 1;
+  c.N = l->R / c.halves;
+  c.es = esize(l->dtype);
+  c.eo = osize(l->dtype);
+  c.terms = l->dtype == DSF_F32 ? 3 : 1;
+  c.kbe = l->dtype == DSF_E4M3 ? 128 : 64;
+  c.ws = static_cast<uint8_t*>(ws);
+  c.w = layout(l, M, gated, backward);
+  c.status = status;
+  c.s = s;
+  if (laid_out(l->dtype, l->K)) {
+    c.X = Mat{c.ws + c.w.xp, M, l->K, c.w.kp, c.terms, M * c.w.kp};
+    c.W = Mat{c.ws + c.w.wp, c.N, l->K, c.w.kp, (long long)c.terms * c.halves, c.N * c.w.kp};
+  } else {
+    c.X = Mat{x, M, l->K, ldx, 1, 0};
+    c.W = Mat{l->W, c.N, l->K, l->ldw, c.halves, c.N * l->ldw};
+  }
+  return c;
+}
+
+bool lay_operands(const Ctx& c, const void* x, long long ldx, const void* dy, long long lddy) {
+  LayJob jobs[3];
+  int n = 0;
+  if (laid_out(c.l->dtype, c.l->K)) {
+    jobs[n++] = LayJob{x, c.ws + c.w.xp, ldx, c.M, c.w.kp, c.l->K};
+    jobs[n++] = LayJob{c.l->W, c.ws + c.w.wp, c.l->ldw, c.l->R, c.w.kp, c.l->K};
+  }
+  if (dy && laid_out(c.l->dtype, c.N)) jobs[n++] = LayJob{dy, c.ws + c.w.gp, lddy, c.M, c.w.np, c.N};
+  return lay(c.l->dtype, jobs, n, c.s);
+}
+
+void set_plan(Product& p, const Plan& q, long long M, long long N, int nb, long long nkb) {
+  p.cfg = q.cfg;
+  p.a.M = int(M);
+  p.a.N = int(N);
+  p.a.mt = q.mt;
+  p.a.nt = q.nt;
+  p.a.nb = nb;
+  p.a.nkb = int(nkb);
+  p.a.kbps = q.kbps;
+  p.a.splits = q.splits;
+}
+
+void set_part(Product& p, const Ctx& c, long long planes) {
+  const long long ldp = up(p.a.N, 4), n = planes * p.a.splits;
+  p.epi = kEpiPart;
+  p.a.has_in = 0;
+  p.a.out_tma = 1;
+  p.out = Mat{c.ws + c.w.part, p.a.M, p.a.N, ldp, n, p.a.M * ldp};
+}
+
+bool finish(const Ctx& c, const Product& p, FinishArgs f, bool f32) {
+  f.part = reinterpret_cast<const float*>(c.ws + c.w.part);
+  f.M = p.a.M;
+  f.N = p.a.N;
+  f.ldp = up(p.a.N, 4);
+  f.splits = p.a.splits;
+  const long long total = f.M * (f.ldp / 4) * (f.gated ? 1 : f.planes), blocks = (total + 255) / 256;
+  const unsigned grid = unsigned(blocks < kSms * 16 ? blocks : kSms * 16);
+  if (f32) finish_kernel<float><<<grid, 256, 0, c.s>>>(f);
+  else finish_kernel<__nv_bfloat16><<<grid, 256, 0, c.s>>>(f);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+// x W^T with the forward's epilogue (dz null) or the backward's into dz.
+bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi, void* y, long long ldy, bool dz,
+                   float* sums) {
+  const dsf_dense* l = c.l;
+  const bool f32 = l->dtype == DSF_F32;
+  Product p{};
+  p.A = c.X;
+  p.B = c.W;
+  p.major = kKK;
+  p.gated = c.gated;
+  p.f32 = f32;
+  p.epi = dz ? kEpiDz : kEpiFwd;
+  const long long nkb = (l->K + c.kbe - 1) / c.kbe;
+  p.a.nseg = f32 ? 6 : 1;
+  p.a.nbig = 1;
+  for (int i = 0; i < p.a.nseg; ++i) {
+    p.a.pa[i] = uint8_t(f32 ? kPairs[i][0] : 0);
+    p.a.pb[i] = uint8_t(f32 ? kPairs[i][1] : 0);
+  }
+  set_plan(p, plan(c.M, c.N, 1, c.gated, f32, nkb, p.a.nseg, !dz), c.M, c.N, 1, nkb);
+  p.a.act = l->act;
+  p.a.bias = l->bias;
+  p.a.xs = xs;
+  p.a.ws = l->scale;
+  p.a.status = c.status;
+  p.a.part = sums;
+  if (p.a.splits > 1) {
+    set_part(p, c, c.halves);
+  } else {
+    p.a.in = in;
+    p.a.ldi = ldi;
+    p.a.has_in = in != nullptr;
+    p.a.in_tma = in && tma_ok(in, ldi, c.eo);
+    p.in = Mat{in, c.M, c.N, ldi, 1, 0};
+    p.a.out = y;
+    p.a.ldo = ldy;
+    p.a.out_plane = c.M * ldy;
+    p.a.out_tma = tma_ok(y, ldy, c.eo);
+    p.out = Mat{y, c.M, c.N, ldy, dz ? c.halves : 1, c.M * ldy};
+  }
+  const bool ok = dz ? run_dz_product(p, c.s) : (l->dtype == DSF_E4M3 ? run_e4m3_product(p, c.s) : run_fwd_product(p, c.s));
+  if (!ok || p.a.splits == 1) return ok;
+  FinishArgs f{};
+  f.fwd = true;
+  f.gated = c.gated;
+  f.planes = c.halves;
+  f.bias = l->bias;
+  f.xs = xs;
+  f.ws = l->scale;
+  f.res = in;
+  f.ldr = ldi;
+  f.out = y;
+  f.ldo = ldy;
+  f.act = l->act;
+  return finish(c, p, f, f32);
+}
+
+// A gradient product over the pairs of terms: dx (dz [.][M][N] times W) or dW
+// (dz^T times x, one batch per half).
+bool grad_product(const Ctx& c, const Mat& dz, bool dW, void* out, long long ldo) {
+  const bool f32 = c.l->dtype == DSF_F32;
+  Product p{};
+  p.A = dz;
+  p.B = dW ? c.X : c.W;
+  p.major = dW ? kNN : kKN;
+  p.gated = false;
+  p.f32 = f32;
+  p.epi = kEpiOut;
+  const int pairs = f32 ? 6 : 1, nb = dW ? c.halves : 1;
+  for (int i = 0; i < pairs; ++i) {
+    const int ta = f32 ? kPairs[i][0] : 0, tb = f32 ? kPairs[i][1] : 0;
+    if (dW) {
+      p.a.pa[p.a.nseg] = uint8_t(ta * c.halves);
+      p.a.pb[p.a.nseg++] = uint8_t(tb);
+    } else {
+      for (int h = 0; h < c.halves; ++h) {
+        p.a.pa[p.a.nseg] = uint8_t(ta * c.halves + h);
+        p.a.pb[p.a.nseg++] = uint8_t(tb * c.halves + h);
+      }
+    }
+  }
+  p.a.nbig = dW ? 1 : c.halves;
+  const long long rows = dW ? c.N : c.M, depth = dW ? c.M : c.N, nkb = (depth + 63) / 64;
+  set_plan(p, plan(rows, c.l->K, nb, false, f32, nkb, p.a.nseg, true), rows, c.l->K, nb, nkb);
+  p.a.status = c.status;
+  if (p.a.splits > 1) {
+    set_part(p, c, nb);
+  } else {
+    p.a.out = out;
+    p.a.ldo = ldo;
+    p.a.out_plane = rows * ldo;
+    p.a.out_tma = tma_ok(out, ldo, c.es);
+    p.out = Mat{out, rows, c.l->K, ldo, nb, rows * ldo};
+  }
+  if (!run_grad_product(p, c.s)) return false;
+  if (p.a.splits == 1) return true;
+  FinishArgs f{};
+  f.planes = nb;
+  f.out = out;
+  f.ldo = ldo;
+  f.out_plane = rows * ldo;
+  return finish(c, p, f, f32);
+}
+
 int fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const float* xs, const void* res, long long ldr,
-        long long M, void* y, long long ldy, cudaStream_t s) {
-  const int N = gated ? l->R / 2 : l->R;
-  const FwdEpi<TO> e{static_cast<TO*>(y), static_cast<const TO*>(res), l->bias, xs, l->scale, ldy, ldr, l->act,
-                     gated ? N : 0};
-  const T *X = static_cast<const T*>(x), *W = static_cast<const T*>(l->W);
-  const bool ok = gated ? product<T, T, true>(X, ldx, 1, W, l->ldw, 1, M, N, l->K, N, e, s)
-                        : product<T, T, false>(X, ldx, 1, W, l->ldw, 1, M, N, l->K, 0, e, s);
+        long long M, void* y, long long ldy, void* ws, int* status, cudaStream_t s) {
+  bool ok;
+  if (M <= kSmallM) {
+    const int N = gated ? l->R / 2 : l->R;
+    const SmallArgs a{x, l->W, ldx, l->ldw, l->bias, xs, l->scale, res, ldr, y, ldy, int(M), N, l->K, l->act};
+    const bool vec = (l->K * esize(l->dtype)) % 16 == 0;
+    ok = l->dtype == DSF_F32    ? launch_small<float, float>(a, gated, vec, s)
+         : l->dtype == DSF_BF16 ? launch_small<__nv_bfloat16, __nv_bfloat16>(a, gated, vec, s)
+                                : launch_small<__nv_fp8_e4m3, __nv_bfloat16>(a, gated, vec, s);
+  } else {
+    const Ctx c = context(l, gated, x, ldx, M, ws, false, status, s);
+    ok = lay_operands(c, x, ldx, nullptr, 0) && layer_product(c, xs, res, ldr, y, ldy, false, nullptr);
+  }
   return ok ? DSF_OK : DSF_ECUDA;
 }
 
-template <class T>
 int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void* dy, long long lddy, long long M,
-        void* dx, long long lddx, void* dW, float* db, void* ws, cudaStream_t s) {
-  const int R = l->R, N = gated ? R / 2 : R, K = l->K;
-  float* dz = static_cast<float*>(ws);
-  const T *X = static_cast<const T*>(x), *W = static_cast<const T*>(l->W);
-  const DzEpi<T> e{static_cast<const T*>(dy), l->bias, lddy, dz, l->act, gated ? N : 0, R};
-  bool ok = gated ? product<T, T, true>(X, ldx, 1, W, l->ldw, 1, M, N, K, N, e, s)
-                  : product<T, T, false>(X, ldx, 1, W, l->ldw, 1, M, N, K, 0, e, s);
-  if (ok && dx)
-    ok = product<float, T, false>(dz, R, 1, W, 1, l->ldw, M, K, R, 0, OutEpi<T>{static_cast<T*>(dx), lddx}, s);
-  if (ok && dW)
-    ok = product<float, T, false>(dz, 1, R, X, 1, ldx, R, K, M, 0, OutEpi<T>{static_cast<T*>(dW), K}, s);
-  if (ok && db) ok = colsum(dz, M, R, db, s);
-  return ok ? DSF_OK : DSF_ECUDA;
+        void* dx, long long lddx, void* dW, float* db, void* ws, int* status, cudaStream_t s) {
+  const Ctx c = context(l, gated, x, ldx, M, ws, true, status, s);
+  const bool f32 = l->dtype == DSF_F32, own_dz = gated || l->act != DSF_ACT_NONE;
+  float* sums = reinterpret_cast<float*>(c.ws + c.w.sums);
+  if (!dx && !dW && !db) return DSF_OK;
+  if (!lay_operands(c, x, ldx, own_dz || (!dx && !dW) ? nullptr : dy, lddy)) return DSF_ECUDA;
+  Mat dz;
+  if (own_dz) {
+    void* d = c.ws + c.w.dz;
+    if (!layer_product(c, nullptr, dy, lddy, d, c.w.np, true, db ? sums : nullptr)) return DSF_ECUDA;
+    if (db && !colsum(sums, (M + 31) / 32, l->R, db, s)) return DSF_ECUDA;
+    if (f32) {
+      const LayJob j{d, c.ws + c.w.dzp, c.w.np, c.halves * M, c.w.np, c.N};
+      if ((dx || dW) && !lay(DSF_F32, &j, 1, s)) return DSF_ECUDA;
+      d = c.ws + c.w.dzp;
+    }
+    dz = Mat{d, M, c.N, c.w.np, (long long)c.terms * c.halves, M * c.w.np};
+  } else {
+    if (db) {
+      const long long blocks = (M + kSumRows - 1) / kSumRows;
+      const dim3 grid{unsigned(blocks), unsigned((c.N + 31) / 32)};
+      if (f32) row_block_sums_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(dy), lddy, M, c.N, sums);
+      else row_block_sums_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(dy), lddy, M, c.N, sums);
+      if (cudaGetLastError() != cudaSuccess || !colsum(sums, blocks, c.N, db, s)) return DSF_ECUDA;
+    }
+    dz = laid_out(l->dtype, c.N) ? Mat{c.ws + c.w.gp, M, c.N, c.w.np, c.terms, M * c.w.np} : Mat{dy, M, c.N, lddy, 1, 0};
+  }
+  if (dx && !grad_product(c, dz, false, dx, lddx)) return DSF_ECUDA;
+  if (dW && !grad_product(c, dz, true, dW, l->K)) return DSF_ECUDA;
+  return DSF_OK;
 }
 
 int run_fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const float* xs, const void* res,
-            long long ldr, long long M, void* y, long long ldy, void* ws, size_t ws_bytes, void* stream) {
+            long long ldr, long long M, void* y, long long ldy, void* ws, size_t ws_bytes, int* status,
+            void* stream) {
   if (int rc = check_layer(l, gated)) return rc;
   if (M < 0 || M > kMaxM) return DSF_EINVAL;
   if (M == 0) return DSF_OK;
@@ -197,14 +554,11 @@ int run_fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const 
   if ((l->dtype == DSF_E4M3) != (xs != nullptr) || !at(xs, 4)) return DSF_EINVAL;
   if (!y || ldy < N || !at(y, eo) || (res && (ldr < N || !at(res, eo)))) return DSF_EINVAL;
   if (!ws || !at(ws, 256) || ws_bytes < ws_bytes_of(l, M, gated, false)) return DSF_EWORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (l->dtype == DSF_F32) return fwd<float, float>(l, gated, x, ldx, xs, res, ldr, M, y, ldy, s);
-  if (l->dtype == DSF_BF16) return fwd<__nv_bfloat16, __nv_bfloat16>(l, gated, x, ldx, xs, res, ldr, M, y, ldy, s);
-  return fwd<__nv_fp8_e4m3, __nv_bfloat16>(l, gated, x, ldx, xs, res, ldr, M, y, ldy, s);
+  return fwd(l, gated, x, ldx, xs, res, ldr, M, y, ldy, ws, status, static_cast<cudaStream_t>(stream));
 }
 
 int run_bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void* dy, long long lddy, long long M,
-            void* dx, long long lddx, void* dW, float* db, void* ws, size_t ws_bytes, void* stream) {
+            void* dx, long long lddx, void* dW, float* db, void* ws, size_t ws_bytes, int* status, void* stream) {
   if (int rc = check_layer(l, gated)) return rc;
   if (l->dtype == DSF_E4M3) return DSF_EUNSUPPORTED;
   if (M < 0 || M > kMaxM) return DSF_EINVAL;
@@ -219,8 +573,7 @@ int run_bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const 
     if (db && cudaMemsetAsync(db, 0, size_t(l->R) * 4, s) != cudaSuccess) return DSF_ECUDA;
     return DSF_OK;
   }
-  if (l->dtype == DSF_F32) return bwd<float>(l, gated, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, s);
-  return bwd<__nv_bfloat16>(l, gated, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, s);
+  return bwd(l, gated, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, status, s);
 }
 
 }  // namespace
@@ -241,22 +594,22 @@ size_t dsf_dense_workspace_bytes(const dsf_dense* l, int64_t M, int32_t gated, i
 
 int ctr_dense_fwd(const dsf_dense* l, const void* x, int64_t ldx, const float* xs, const void* res, int64_t ldr,
                   int64_t M, void* y, int64_t ldy, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
-  return run_fwd(l, false, x, ldx, xs, res, ldr, M, y, ldy, ws, ws_bytes, stream);
+  return run_fwd(l, false, x, ldx, xs, res, ldr, M, y, ldy, ws, ws_bytes, status, stream);
 }
 
 int ctr_glu_fwd(const dsf_dense* l, const void* x, int64_t ldx, const float* xs, int64_t M, void* h, int64_t ldh,
                 void* ws, size_t ws_bytes, int32_t* status, void* stream) {
-  return run_fwd(l, true, x, ldx, xs, nullptr, 0, M, h, ldh, ws, ws_bytes, stream);
+  return run_fwd(l, true, x, ldx, xs, nullptr, 0, M, h, ldh, ws, ws_bytes, status, stream);
 }
 
 int ctr_dense_bwd(const dsf_dense* l, const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, void* dx,
                   int64_t lddx, void* dW, float* db, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
-  return run_bwd(l, false, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, ws_bytes, stream);
+  return run_bwd(l, false, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, ws_bytes, status, stream);
 }
 
 int ctr_glu_bwd(const dsf_dense* l, const void* x, int64_t ldx, const void* dh, int64_t lddh, int64_t M, void* dx,
                 int64_t lddx, void* dW, float* db, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
-  return run_bwd(l, true, x, ldx, dh, lddh, M, dx, lddx, dW, db, ws, ws_bytes, stream);
+  return run_bwd(l, true, x, ldx, dh, lddh, M, dx, lddx, dW, db, ws, ws_bytes, status, stream);
 }
 
 }  // extern "C"
