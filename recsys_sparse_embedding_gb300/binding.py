@@ -177,8 +177,8 @@ def _check(rc: int, where: str) -> None:
 
 
 def _stream_ptr(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (the current stream's handle without a Stream object: a third of a small call's time)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

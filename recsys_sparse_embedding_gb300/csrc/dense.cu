@@ -57,7 +57,7 @@ struct Plan {
 // cycles, the chip takes its units in whole waves, and a split product pays
 // for a second launch and its partial sums' way to L2 and back.
 Plan plan(long long M, long long N, int nb, bool gated, bool f32, long long nkb, int nseg, bool may_split) {
-  const double kStep[3] = {f32 ? 300. : 540., 300, 230};
+  const double kStep[3] = {f32 ? 430. : 560., 560, 400};
   constexpr double kUnit = 1500, kSecond = 5000, kBytesPerCycle = 2000;
   Plan best{};
   double cost = 1e300;

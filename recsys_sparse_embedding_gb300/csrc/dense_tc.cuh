@@ -492,15 +492,26 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) return;
           } else {  // rows side by side across the lanes
-            for (int r = 0; r < 32; ++r)
+            constexpr int RB = 16;  // rows in flight
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += RB) {
+              TO v[RB][CW / 32];
 #pragma unroll
-              for (int j = 0; j < CW / 32; ++j) {
-                const int e = lane + 32 * j;
-                TO v = TO(0.f);
-                if (row0 + r < a.M && col0 + e < a.N) v = in[(long long)(row0 + r) * a.ldi + col0 + e];
-                const int byte = e * int(sizeof(TO));
-                *reinterpret_cast<TO*>(buf + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15)) = v;
-              }
+              for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int j = 0; j < CW / 32; ++j) {
+                  const int e = lane + 32 * j;
+                  v[r][j] = TO(0.f);
+                  if (row0 + r0 + r < a.M && col0 + e < a.N) v[r][j] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + e];
+                }
+#pragma unroll
+              for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int j = 0; j < CW / 32; ++j) {
+                  const int byte = (lane + 32 * j) * int(sizeof(TO));
+                  *reinterpret_cast<TO*>(buf + (r0 + r) * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15)) = v[r][j];
+                }
+            }
             __syncwarp();
           }
         }
@@ -633,6 +644,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
           }
         } else {
           TO* o = out + plane * a.out_plane;
+#pragma unroll 8
           for (int r = 0; r < 32; ++r)
 #pragma unroll
             for (int j = 0; j < CW / 32; ++j) {
