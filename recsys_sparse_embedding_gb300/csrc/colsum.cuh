@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "pdl.cuh"
+
 namespace dsf {
 
 // out[n] = sum over r of P[r][n]. A block of 32 warps takes 32 columns: warp g
@@ -17,6 +19,8 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ 
   __shared__ float part[W][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int n = blockIdx.x * 32 + lane;
+  pdl_go();
+  pdl_wait();
   float s = 0.f;
   if (n < N) {
     for (long long r0 = g; r0 < rows; r0 += W * U) {
@@ -38,8 +42,7 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ 
 }
 
 inline bool colsum(const float* P, long long rows, int N, float* out, cudaStream_t s) {
-  colsum_kernel<><<<unsigned((N + 31) / 32), 1024, 0, s>>>(P, rows, N, out);
-  return cudaGetLastError() == cudaSuccess;
+  return pdl_launch(colsum_kernel<>, dim3(unsigned((N + 31) / 32)), 1024, s, P, rows, N, out);
 }
 
 }  // namespace dsf

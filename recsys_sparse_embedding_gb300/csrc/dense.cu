@@ -160,6 +160,8 @@ __device__ __forceinline__ void three_terms(float x, uint32_t* t) {
 
 template <int ES>  // source element: 4 (fp32 -> three bf16 terms), 2 or 1 (copied)
 __global__ void __launch_bounds__(256) lay_kernel(const LayJob j0, const LayJob j1, const LayJob j2, int b0, int b1) {
+  pdl_go();
+  pdl_wait();
   const int blk = int(blockIdx.x), which = blk < b0 ? 0 : (blk < b1 ? 1 : 2);
   const LayJob& j = which == 0 ? j0 : (which == 1 ? j1 : j2);
   const int nblk = which == 0 ? b0 : (which == 1 ? b1 - b0 : int(gridDim.x) - b1);
@@ -215,10 +217,8 @@ bool lay(int dtype, const LayJob* jobs, int n, cudaStream_t s) {
     tot += b[i];
   }
   if (tot == 0) return true;
-  if (dtype == DSF_F32) lay_kernel<4><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
-  else if (dtype == DSF_BF16) lay_kernel<2><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
-  else lay_kernel<1><<<tot, 256, 0, s>>>(j[0], j[1], j[2], b[0], b[0] + b[1]);
-  return cudaGetLastError() == cudaSuccess;
+  auto* kernel = dtype == DSF_F32 ? lay_kernel<4> : (dtype == DSF_BF16 ? lay_kernel<2> : lay_kernel<1>);
+  return pdl_launch(kernel, dim3(unsigned(tot)), 256, s, j[0], j[1], j[2], b[0], b[0] + b[1]);
 }
 
 // Sums over blocks of 256 rows of a matrix (db where dz is dy): part[block][n].
@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(256) row_block_sums_kernel(const T* g, long lo
   __shared__ float p[8][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.y * 32 + lane;
   const long long r0 = (long long)blockIdx.x * kSumRows;
+  pdl_go();
+  pdl_wait();
   float s = 0.f;
   if (n < N) {
 #pragma unroll 8
@@ -262,6 +264,8 @@ struct FinishArgs {
 };
 template <class TO>
 __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs a) {
+  pdl_go();
+  pdl_wait();
   const long long n4 = a.ldp / 4, per = a.M * n4, plane = a.M * a.ldp;
   const long long total = per * (a.gated ? 1 : a.planes);
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs a) {
 // The six pairs of terms, smallest products first.
 constexpr int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
 
-bool tma_ok(const void* p, long long ld, int es) { return at(p, 16) && (ld * es) % 16 == 0; }
+bool vec_rows(const void* p, long long ld, int es) { return at(p, 16) && (ld * es) % 16 == 0; }
 
 struct Ctx {
   const dsf_dense* l;
@@ -368,12 +372,14 @@ void set_plan(Product& p, const Plan& q, long long M, long long N, int nb, long 
   p.a.splits = q.splits;
 }
 
-void set_part(Product& p, const Ctx& c, long long planes) {
-  const long long ldp = up(p.a.N, 4), n = planes * p.a.splits;
+void set_part(Product& p, const Ctx& c) {
+  const long long ldp = up(p.a.N, 4);
   p.epi = kEpiPart;
-  p.a.has_in = 0;
-  p.a.out_tma = 1;
-  p.out = Mat{c.ws + c.w.part, p.a.M, p.a.N, ldp, n, p.a.M * ldp};
+  p.a.in = nullptr;
+  p.a.out = c.ws + c.w.part;
+  p.a.ldo = ldp;
+  p.a.out_plane = p.a.M * ldp;
+  p.a.out_vec = 1;
 }
 
 bool finish(const Ctx& c, const Product& p, FinishArgs f, bool f32) {
@@ -384,9 +390,7 @@ bool finish(const Ctx& c, const Product& p, FinishArgs f, bool f32) {
   f.splits = p.a.splits;
   const long long total = f.M * (f.ldp / 4) * (f.gated ? 1 : f.planes), blocks = (total + 255) / 256;
   const unsigned grid = unsigned(blocks < kSms * 16 ? blocks : kSms * 16);
-  if (f32) finish_kernel<float><<<grid, 256, 0, c.s>>>(f);
-  else finish_kernel<__nv_bfloat16><<<grid, 256, 0, c.s>>>(f);
-  return cudaGetLastError() == cudaSuccess;
+  return pdl_launch(f32 ? finish_kernel<float> : finish_kernel<__nv_bfloat16>, dim3(grid), 256, c.s, f);
 }
 
 // x W^T with the forward's epilogue (dz null) or the backward's into dz.
@@ -416,18 +420,15 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.a.status = c.status;
   p.a.part = sums;
   if (p.a.splits > 1) {
-    set_part(p, c, c.halves);
+    set_part(p, c);
   } else {
     p.a.in = in;
     p.a.ldi = ldi;
-    p.a.has_in = in != nullptr;
-    p.a.in_tma = in && tma_ok(in, ldi, c.eo);
-    p.in = Mat{in, c.M, c.N, ldi, 1, 0};
+    p.a.in_vec = in && vec_rows(in, ldi, c.eo);
     p.a.out = y;
     p.a.ldo = ldy;
     p.a.out_plane = c.M * ldy;
-    p.a.out_tma = tma_ok(y, ldy, c.eo);
-    p.out = Mat{y, c.M, c.N, ldy, dz ? c.halves : 1, c.M * ldy};
+    p.a.out_vec = vec_rows(y, ldy, c.eo);
   }
   const bool ok = dz ? run_dz_product(p, c.s) : (l->dtype == DSF_E4M3 ? run_e4m3_product(p, c.s) : run_fwd_product(p, c.s));
   if (!ok || p.a.splits == 1) return ok;
@@ -475,13 +476,12 @@ bool grad_product(const Ctx& c, const Mat& dz, bool dW, void* out, long long ldo
   set_plan(p, plan(rows, c.l->K, nb, false, f32, nkb, p.a.nseg, true), rows, c.l->K, nb, nkb);
   p.a.status = c.status;
   if (p.a.splits > 1) {
-    set_part(p, c, nb);
+    set_part(p, c);
   } else {
     p.a.out = out;
     p.a.ldo = ldo;
     p.a.out_plane = rows * ldo;
-    p.a.out_tma = tma_ok(out, ldo, c.es);
-    p.out = Mat{out, rows, c.l->K, ldo, nb, rows * ldo};
+    p.a.out_vec = vec_rows(out, ldo, c.es) && (nb == 1 || (rows * ldo * c.es) % 16 == 0);
   }
   if (!run_grad_product(p, c.s)) return false;
   if (p.a.splits == 1) return true;
@@ -532,9 +532,11 @@ int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void
     if (db) {
       const long long blocks = (M + kSumRows - 1) / kSumRows;
       const dim3 grid{unsigned(blocks), unsigned((c.N + 31) / 32)};
-      if (f32) row_block_sums_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(dy), lddy, M, c.N, sums);
-      else row_block_sums_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(dy), lddy, M, c.N, sums);
-      if (cudaGetLastError() != cudaSuccess || !colsum(sums, blocks, c.N, db, s)) return DSF_ECUDA;
+      const bool ok = f32 ? pdl_launch(row_block_sums_kernel<float>, grid, 256, s, static_cast<const float*>(dy), lddy, M,
+                                       c.N, sums)
+                          : pdl_launch(row_block_sums_kernel<__nv_bfloat16>, grid, 256, s,
+                                       static_cast<const __nv_bfloat16*>(dy), lddy, M, c.N, sums);
+      if (!ok || !colsum(sums, blocks, c.N, db, s)) return DSF_ECUDA;
     }
     dz = laid_out(l->dtype, c.N) ? Mat{c.ws + c.w.gp, M, c.N, c.w.np, c.terms, M * c.w.np} : Mat{dy, M, c.N, lddy, 1, 0};
   }

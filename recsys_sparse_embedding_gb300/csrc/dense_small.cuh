@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "dense_math.cuh"
+#include "pdl.cuh"
 
 namespace dsf {
 namespace dense {
@@ -72,6 +73,8 @@ template <class T, class TO, int MT, bool GATED, bool VEC>
 __global__ void __launch_bounds__(256) small_kernel(const SmallArgs a) {
   constexpr int NB = GATED ? 2 : 1, E = VEC ? 16 / int(sizeof(T)) : 1, U = VEC ? 4 : 8;
   const int lane = threadIdx.x & 31, n = blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_go();
+  pdl_wait();
   if (n >= a.N) return;
   const T* x = static_cast<const T*>(a.x);
   const T* w[NB];
@@ -150,10 +153,9 @@ __global__ void __launch_bounds__(256) small_kernel(const SmallArgs a) {
 
 template <class T, class TO, int MT, bool GATED>
 bool launch_small_v(const SmallArgs& a, bool vec, cudaStream_t s) {
-  const unsigned grid = unsigned((a.N + 7) / 8);
-  if (vec) small_kernel<T, TO, MT, GATED, true><<<grid, 256, 0, s>>>(a);
-  else small_kernel<T, TO, MT, GATED, false><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess;
+  const dim3 grid(unsigned((a.N + 7) / 8));
+  return vec ? pdl_launch(small_kernel<T, TO, MT, GATED, true>, grid, 256, s, a)
+             : pdl_launch(small_kernel<T, TO, MT, GATED, false>, grid, 256, s, a);
 }
 template <class T, class TO>
 bool launch_small(const SmallArgs& a, bool gated, bool vec, cudaStream_t s) {

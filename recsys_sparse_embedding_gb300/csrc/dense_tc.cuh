@@ -4,16 +4,17 @@
 // One persistent, warp-specialised kernel. A work unit is a tile of 128 CG x
 // BN accumulators (CG CTAs of a cluster work on one tile together: CG = 2
 // halves what each SM has to read of B), over all of K or one K-split.
-//   warp 8   brings A and B by TMA: K-blocks of 128 bytes per row in the
+//   warp 16  brings A and B by TMA: K-blocks of 128 bytes per row in the
 //            128-byte swizzle, through a ring of stages;
-//   warp 9   issues the MMAs (tcgen05.mma, in the cluster's first CTA) into
+//   warp 17  issues the MMAs (tcgen05.mma, in the cluster's first CTA) into
 //            one of two accumulators in tensor memory;
-//   warps 0-7 run the epilogue of the other accumulator: 32 rows (a warp's
-//            lane quarter) by 128 bytes of output at a time, one row per lane.
-//            Inputs (the residual, or the upstream gradient) and outputs pass
-//            through a 4 KB buffer per item by TMA, two items ahead, so that
-//            global memory sees whole rows of 128 bytes; a matrix whose rows
-//            are not at 16-byte boundaries is copied by the warp instead.
+//   warps 0-15 run the epilogue of the other accumulator, in items of 32 rows
+//            (a warp's lane quarter, one row per lane) by 32 columns. Inputs
+//            (the residual, or the upstream gradient; loaded an item ahead)
+//            and outputs change between a row per lane and 16 bytes of
+//            neighbouring lanes in a 2 or 4 KB buffer per warp, so that
+//            global memory sees whole row segments. (Not by TMA: its stores
+//            and loads queue behind the operands' loads, 2 us an item.)
 // So a tile's loads, MMAs and epilogue overlap the next tile's. Operands come
 // as three-dimensional tensors [plane][row][column]:
 //   - K-major (columns are K) or MN-major (rows are K: W in dx = dz W, both
@@ -38,9 +39,11 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "dense_math.cuh"
 #include "dinsparse.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace dsf {
@@ -58,21 +61,33 @@ enum Major { kKK = 0, kKN = 1, kNN = 2 };  // A and B K-major; B MN-major; both
 
 constexpr int kMaxSeg = 12;
 
+// Division of unsigned 32-bit numbers by a fixed divisor: q = (mulhi(n, m) + n) >> l
+// with l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, exact for every n below 2^31.
+struct Div {
+  uint32_t d, m, l;
+};
+inline Div make_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return Div{d, uint32_t(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const Div& v) { return (__umulhi(n, v.m) + n) >> v.l; }
+
 struct TcArgs {
   int M, N;          // rows; output columns (a gated layer's: F)
   int mt, nt, nb;    // tiles along M and N, batches (halves of dW)
+  Div by_splits, by_batch, by_group, by_last;  // splits; mt nt; 8 nt; M tiles of the last group of 8
   int nkb, kbps;     // K-blocks per segment, per split
   int nbig;          // PROMOTE: the last nbig segments are the products of leading terms
   int splits, nseg;
   uint8_t pa[kMaxSeg], pb[kMaxSeg];  // the segments' planes (A: + batch; B of a gated layer: 2 pb, 2 pb + 1)
   int act;
   const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
-  const void* in;
+  const void* in;            // nullable unless kEpiDz
   long long ldi;
-  int has_in, in_tma;
   void* out;
   long long ldo, out_plane;  // strides in elements
-  int out_tma;
+  int in_vec, out_vec;       // rows at 16-byte boundaries
   float* part;  // kEpiDz: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
   int* status;
 };
@@ -93,18 +108,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_store_3d(const void* map, int x, int y, int z, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
-               : "memory");
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>  // all but the last N groups have read their shared memory
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -118,8 +124,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// An arrival that orders nothing but itself: what it announces (accumulators
+// read, tcgen05.wait::ld done) is complete in registers. A release would wait
+// for the thread's global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t* slot, uint32_t cols) {
@@ -176,17 +185,20 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- shapes
-template <int CG, int BN, bool GATED, int EPI>
+template <int CG, int BN, bool GATED, int EPI, class TO>
 struct Shape {
-  static constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
+#ifndef DZW
+#define DZW 8
+#endif
+  static constexpr int kEpiWarps = GATED && sizeof(TO) == 4 && EPI != kEpiPart ? 8 : (GATED && EPI == kEpiDz ? DZW : 16), kThreads = 32 * (kEpiWarps + 2);
+  static constexpr int kGroups = kEpiWarps / 4;  // warps on one lane quarter
+  static constexpr int ITEM = 32 * 32 * int(sizeof(TO));
   static constexpr int BNC = BN / CG;            // B rows (or MN-major columns) in this CTA
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BNC * 128, STAGE = A_BYTES + B_BYTES;
-  // item buffers per epilogue warp, 4 KB each
-  static constexpr int NBUF = (EPI == kEpiFwd && !GATED) || EPI == kEpiDz ? 3 : 2;
-  static constexpr int EBYTES = kEpiWarps * NBUF * 4096;
-  static constexpr int kRoom = 227 * 1024 - 1024 - 512 - EBYTES;
+  static constexpr int EBYTES = kEpiWarps * ITEM;
+  static constexpr int kRoom = 227 * 1024 - 1024 - 256 - EBYTES;
   static constexpr int STAGES = kRoom / STAGE < 8 ? kRoom / STAGE : 8;
-  static constexpr int SMEM = STAGES * STAGE + EBYTES + 512 + 1024;
+  static constexpr int SMEM = STAGES * STAGE + EBYTES + 256 + 1024;
   static constexpr uint32_t TCOLS = 2 * BN;      // two accumulators
   static_assert(TCOLS <= 512 && (TCOLS & (TCOLS - 1)) == 0, "tensor memory columns");
   static_assert(STAGES >= 3, "ring");
@@ -194,11 +206,11 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tfull[2], tempty[2], in[8][3];
+  uint64_t full[8], empty[8], tfull[2], tempty[2];
   uint32_t tmem;
   int abort_;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= 256, "barrier block");
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -223,40 +235,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
   tmem_ld16(t + 16, v + 16);
 }
 
-// n uniform fp32 values per lane (bias, scales): columns c .. c + 31 below N
-__device__ __forceinline__ void load_cols(const float* p, int c, int N, bool vec, float* v) {
-  if (vec && c + 32 <= N) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p + c) + k);
-      v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = c + k < N ? __ldg(p + c + k) : 0.f;
-  }
-}
-
-template <int ACT, bool GATED>
-__device__ __forceinline__ void act_fwd(float* g, const float* u) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) g[k] = GATED ? act_value<ACT>(g[k]) * u[k] : act_value<ACT>(g[k]);
-}
-// in d (the upstream gradient): g <- its dz; gated: g <- dg, u <- du
-template <int ACT, bool GATED>
-__device__ __forceinline__ void act_bwd(const float* d, float* g, float* u) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const float2 f = act_both<ACT>(g[k]);
-    if (GATED) {
-      g[k] = d[k] * u[k] * f.y;
-      u[k] = d[k] * f.x;
-    } else {
-      g[k] = d[k] * f.y;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- the kernel
 constexpr int kRun = 4;  // PROMOTE: K-blocks of leading terms per run
 
@@ -267,16 +245,16 @@ __device__ __forceinline__ int runs_of(const TcArgs& a, int kbn) {
 }
 
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, class TO, bool PROMOTE>
-__global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
     tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mapA,
-              const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapI,
-              const __grid_constant__ CUtensorMap mapO) {
-  using S = Shape<CG, BN, GATED, EPI>;
+              const __grid_constant__ CUtensorMap mapB) {
+  using S = Shape<CG, BN, GATED, EPI, TO>;
   constexpr bool AMN = MAJOR == kNN, BMN = MAJOR != kKK;
   constexpr int kBK = KIND == kBf16 ? 64 : 128;            // K elements per block (128 bytes)
   constexpr int ON = GATED ? BN / 2 : BN;                  // output columns per tile
-  constexpr int CW = 128 / int(sizeof(TO));                // output columns per item
-  constexpr int NBUF = S::NBUF, STAGES = S::STAGES;
+  constexpr int CW = 32;                                   // output columns per item
+  constexpr int ROWB = CW * int(sizeof(TO));               // an item row's bytes
+  constexpr int STAGES = S::STAGES;
   static_assert(!(GATED && BMN), "a gated layer's product is K-major");
   extern __shared__ uint8_t dyn[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
@@ -287,6 +265,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
   const int unit0 = blockIdx.x / CG, units_step = gridDim.x / CG;
   const int tiles = a.mt * a.nt * a.nb, units = tiles * a.splits;
 
+  if (warp == S::kEpiWarps && lane == 0) {
+    prefetch_map(&mapA);
+    prefetch_map(&mapB);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&bars->full[i], 1);
@@ -296,21 +278,24 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
       mbar_init(&bars->tfull[i], 1);
       mbar_init(&bars->tempty[i], S::kEpiWarps * CG);
     }
-    for (int w = 0; w < S::kEpiWarps; ++w)
-      for (int i = 0; i < 3; ++i) mbar_init(&bars->in[w][i], 1);
     bars->abort_ = 0;
     fence_mbarrier_init();
   }
-  if (warp == 0) {
-    __syncwarp();
-    tmem_alloc_cg<CG>(&bars->tmem, S::TCOLS);
-    tmem_relinquish_cg<CG>();
-  }
-  tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
-  tc_fence_after();
-  const uint32_t tbase = bars->tmem;
+  pdl_go();
+  // (the loads start while tensor memory is being allocated)
+  uint32_t tbase = 0;
+  if (warp != S::kEpiWarps) {
+    if (warp == S::kEpiWarps + 1) {
+      tmem_alloc_cg<CG>(&bars->tmem, S::TCOLS);
+      tmem_relinquish_cg<CG>();
+      tc_fence_before();
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(S::kThreads - 32) : "memory");
+    tc_fence_after();
+    tbase = bars->tmem;
+  }
   volatile int* aborted = &bars->abort_;
 
   // a unit: split-minor, then N tiles within groups of M tiles, so that the
@@ -320,16 +305,16 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
   };
   auto unit_of = [&](int u) {
     Unit t;
-    t.split = u % a.splits;
-    int r = u / a.splits;
-    const int per_b = a.mt * a.nt;
-    t.batch = r / per_b;
-    r -= t.batch * per_b;
-    constexpr int G = 8;
-    const int grp = r / (G * a.nt), first = grp * G, gm = min(G, a.mt - first);
-    r -= grp * G * a.nt;
-    t.m0 = (first + r % gm) * 128 * CG + int(rank) * 128;
-    t.n0 = (r / gm) * ON;
+    uint32_t r = div_by(u, a.by_splits);
+    t.split = u - int(r) * a.splits;
+    t.batch = int(div_by(r, a.by_batch));
+    r -= uint32_t(t.batch) * a.by_batch.d;
+    const uint32_t grp = div_by(r, a.by_group);
+    r -= grp * a.by_group.d;
+    const bool whole = int(grp * 8 + 8) <= a.mt;
+    const uint32_t n = whole ? r >> 3 : div_by(r, a.by_last), gm = whole ? 8 : a.by_last.d;
+    t.m0 = int(grp * 8 + r - n * gm) * 128 * CG + int(rank) * 128;
+    t.n0 = int(n) * ON;
     t.kb0 = t.split * a.kbps;
     t.kbn = min(a.kbps, a.nkb - t.kb0);
     return t;
@@ -338,6 +323,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
   if (warp == S::kEpiWarps) {
     // ------------------------------------------------ loads (one thread)
     if (lane == 0) {
+      pdl_wait();
       uint32_t it = 0;  // K-blocks so far
       bool ok = true;
       const uint32_t full0 = CG == 2 ? mapa(smem_u32(&bars->full[0]), 0) : smem_u32(&bars->full[0]);
@@ -418,13 +404,18 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ epilogue
+    pdl_wait();
     const int q = warp & 3, grp = warp >> 2;
-    uint8_t* buf0 = sE + warp * (NBUF * 4096);
+    uint8_t* buf = sE + warp * S::ITEM;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
     constexpr bool IN = (EPI == kEpiFwd && !GATED) || EPI == kEpiDz;
-    constexpr int RING = IN && EPI == kEpiDz && GATED ? 2 : NBUF;  // (a gated dz: the third buffer holds du)
-    constexpr int AHEAD = RING - 1;                                // input items in flight
-    const bool has_in = IN && (EPI == kEpiDz || a.has_in);
+    constexpr int GR = S::kGroups;
+    // byte `at` of an item's row r; 16-byte slots XOR-swizzled by the row, so that neither a
+    // slot of 8 rows nor whole rows meet in a bank
+    auto slot = [](int r, int at) {
+      return r * ROWB + (((at >> 4) ^ (ROWB == 64 ? (r >> 1) & 3 : r & 7)) << 4) + (at & 15);
+    };
+    const bool has_in = IN && (EPI == kEpiDz || a.in);
     const TO* in = static_cast<const TO*>(a.in);
     TO* out = static_cast<TO*>(a.out);
     constexpr int halves = GATED ? 2 : 1;
@@ -432,38 +423,132 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
     constexpr int WALK = GATED && EPI == kEpiPart ? BN : ON;
     constexpr int NCH = WALK / CW;
     const uint32_t tempty0 = CG == 2 ? mapa(smem_u32(&bars->tempty[0]), 0) : smem_u32(&bars->tempty[0]);
-    const bool vec_b = a.bias && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
-    const bool vec_bu = vec_b && a.N % 4 == 0;
-    const bool vec_s = a.ws && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
-    const bool vec_su = vec_s && a.N % 4 == 0;
-
-    // the input of the warp's items, in order: (unit, chunk) pairs with a row and a column inside
-    int pu = unit0, pc = grp;
-    uint32_t pi = 0;  // items whose input was asked for
-    auto prefetch = [&]() {  // lane 0, TMA inputs
-      while (pu < units) {
-        const Unit t = unit_of(pu);
-        const int row = t.m0 + 32 * q, col = t.n0 + pc * CW;
-        const bool good = row < a.M && col < a.N;
-        const int c = pc;
-        pc += 2;
-        if (pc >= NCH) pc = grp, pu += units_step;
-        if (good && c < NCH) {
-          uint64_t* bar = &bars->in[warp][pi % RING];
-          mbar_arrive_expect_tx(bar, 4096);
-          tma_load_3d<1>(smem_u32(buf0 + (pi % RING) * 4096), &mapI, col, row, 0, smem_u32(bar));
-          ++pi;
-          return;
+    constexpr bool COLS = EPI == kEpiFwd || EPI == kEpiDz, SCALED = KIND == kE4m3 && EPI == kEpiFwd;
+    // columns j .. j + 7 of this lane's row, from and to an item's buffer
+    auto get8 = [&](const uint8_t* b, int j, float* v) {
+#pragma unroll
+      for (int k = 0; k < int(sizeof(TO)) / 2; ++k) {
+        const uint4 u = *reinterpret_cast<const uint4*>(b + slot(lane, j * int(sizeof(TO)) + 16 * k));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (sizeof(TO) == 4) {
+            v[4 * k + e] = __uint_as_float(w[e]);
+          } else {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          }
         }
       }
     };
-    if (has_in && a.in_tma && lane == 0)
-      for (int i = 0; i < AHEAD; ++i) prefetch();
+    auto put8 = [&](uint8_t* b, int j, const float* v) {
+#pragma unroll
+      for (int k = 0; k < int(sizeof(TO)) / 2; ++k) {
+        uint4 w;
+        if (sizeof(TO) == 4)
+          w = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                         __float_as_uint(v[4 * k + 3]));
+        else
+          w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        *reinterpret_cast<uint4*>(b + slot(lane, j * int(sizeof(TO)) + 16 * k)) = w;
+      }
+    };
 
-    uint32_t item = 0, run = 0;
+    // A 16-byte piece of an item for each lane: 4 (bf16) or 8 (fp32) lanes side
+    // by side on a row. Pieces past the matrix's edge element by element.
+    constexpr int EL = 16 / int(sizeof(TO)), LPR = CW / EL, RPI = 32 / LPR, NV = 32 / RPI;
+    const int piece_row = lane / LPR, piece_col = lane % LPR * EL;
+    auto load_item = [&](uint4* v, int r0, int c0) {
+      const int cc = c0 + piece_col;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = r0 + i * RPI + piece_row;
+        const TO* p = in + (long long)r * a.ldi + cc;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r >= a.M || cc >= a.N) continue;
+        if (cc + EL <= a.N) {
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p));
+        } else {
+          uint32_t w[4] = {};
+#pragma unroll
+          for (int e = 0; e < EL - 1; ++e)
+            if (cc + e < a.N) {
+              if (sizeof(TO) == 4) w[e] = __float_as_uint(to_float(p[e]));
+              else w[e / 2] |= (__float_as_uint(to_float(p[e])) >> 16) << (16 * (e & 1));
+            }
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    };
+    auto store_item = [&](TO* base, int r0, int c0) {  // from the buffer
+      __syncwarp();
+      if (a.out_vec) {
+        const int cc = c0 + piece_col;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int rr = i * RPI + piece_row, r = r0 + rr;
+          const uint8_t* b = buf + slot(rr, piece_col * int(sizeof(TO)));
+          TO* p = base + (long long)r * a.ldo + cc;
+          if (r >= a.M || cc >= a.N) continue;
+          if (cc + EL <= a.N) {
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
+          } else {
+            for (int e = 0; cc + e < a.N; ++e) p[e] = reinterpret_cast<const TO*>(b)[e];
+          }
+        }
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+          if (r0 + r < a.M && c0 + lane < a.N)
+            base[(long long)(r0 + r) * a.ldo + c0 + lane] =
+                *reinterpret_cast<const TO*>(buf + slot(r, lane * int(sizeof(TO))));
+      }
+      __syncwarp();
+    };
+    // The input of the warp's next item ((unit, item) pairs in order), where it
+    // can be loaded in pieces: bf16 into registers; fp32, whose sums take the
+    // registers, as far as L2.
+    constexpr bool PRE = IN && sizeof(TO) == 2;
+    uint4 pin[PRE ? NV : 1];
+    auto prefetch = [&](int u, int c) {
+      if (!IN) return;
+      if (c >= NCH) c = grp, u += units_step;
+      const bool any = has_in && a.in_vec && u < units && c < NCH;
+      const Unit t = unit_of(any ? u : unit0);
+      if (PRE) {
+        load_item(pin, any ? t.m0 + 32 * q : a.M, t.n0 + c * CW);
+      } else if (any) {
+        const int r = t.m0 + 32 * q + lane, cc = t.n0 + c * CW;
+        if (r < a.M && cc < a.N) prefetch_l2(in + (long long)r * a.ldi + cc);
+      }
+    };
+    prefetch(unit0, grp);
+    // bias and scales of an item's columns, one column per lane: handed round by
+    // shuffles (the L1 that 220 KB of shared memory leave does not keep them)
+    struct Cols {
+      float b, bu, s, su;
+    };
+    auto load_cols = [&](int c0) {
+      Cols v = {0.f, 0.f, 1.f, 1.f};
+      if (COLS && c0 + lane < a.N) {
+        const int n = c0 + lane;
+        if (a.bias) {
+          v.b = __ldg(a.bias + n);
+          if (GATED) v.bu = __ldg(a.bias + a.N + n);
+        }
+        if (SCALED) {
+          v.s = __ldg(a.ws + n);
+          if (GATED) v.su = __ldg(a.ws + a.N + n);
+        }
+      }
+      return v;
+    };
+
+    uint32_t run = 0;
     bool ok = true;
     constexpr bool PAIR = GATED && EPI != kEpiPart;  // an item takes gate and up accumulators
-    constexpr int NI = (NCH + 1) / 2;                // items per warp and tile
+    constexpr int NI = (NCH + GR - 1) / GR;          // items per warp and tile
     auto wait_run = [&]() {                          // the run's accumulator is complete
       if (*aborted) ok = false;
       if (ok && lane == 0) ok = mbar_wait(&bars->tfull[run & 1u], (run >> 1) & 1u);
@@ -484,187 +569,122 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
       // one item: 32 rows by CW columns. PROMOTE: pg, pu_ hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu_) {
         const int col0 = WALK == BN && GATED ? t.n0 + (c * CW) % ON : t.n0 + c * CW;
-        if (row0 >= a.M || col0 >= a.N) return;
-        uint8_t* buf = buf0 + (item % RING) * 4096;
-        if (has_in) {
-          if (a.in_tma) {
-            if (lane == 0) ok = mbar_wait(&bars->in[warp][item % RING], (item / RING) & 1u);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) return;
-          } else {  // rows side by side across the lanes
-            constexpr int RB = 16;  // rows in flight
-#pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += RB) {
-              TO v[RB][CW / 32];
-#pragma unroll
-              for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int j = 0; j < CW / 32; ++j) {
-                  const int e = lane + 32 * j;
-                  v[r][j] = TO(0.f);
-                  if (row0 + r0 + r < a.M && col0 + e < a.N) v[r][j] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + e];
-                }
-#pragma unroll
-              for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int j = 0; j < CW / 32; ++j) {
-                  const int byte = (lane + 32 * j) * int(sizeof(TO));
-                  *reinterpret_cast<TO*>(buf + (r0 + r) * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15)) = v[r][j];
-                }
-            }
-            __syncwarp();
-          }
+        if (row0 >= a.M || col0 >= a.N) {
+          prefetch(u, c + GR);
+          return;
         }
-        if (EPI == kEpiDz && GATED) {  // du's buffer is free once the last item's stores have read it
-          if (lane == 0) {
-            bulk_wait_read<0>();
-            if (a.in_tma) {
-              fence_proxy_async_smem();
-              prefetch();
+        if (has_in) {
+          if (a.in_vec) {
+            if (!PRE) {
+              uint4 v[NV];
+              load_item(v, row0, col0);
+#pragma unroll
+              for (int i = 0; i < NV; ++i)
+                *reinterpret_cast<uint4*>(buf + slot(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = v[i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < NV; ++i)
+                *reinterpret_cast<uint4*>(buf + slot(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = pin[PRE ? i : 0];
+            }
+          } else {  // one column per lane, 16 rows in flight
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+              TO v[16];
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                v[r] = TO(0.f);
+                if (row0 + r0 + r < a.M && col0 + lane < a.N) v[r] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + lane];
+              }
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                *reinterpret_cast<TO*>(buf + slot(r0 + r, lane * int(sizeof(TO)))) = v[r];
             }
           }
           __syncwarp();
         }
+        const Cols cols = load_cols(col0);
+        const float xs = SCALED && live ? __ldg(a.xs + row) : 0.f;
+        // g (and up): the accumulators of this lane's row, then the outputs
+        float g_[32], up_[PAIR ? 32 : 1];
+        float* g = g_;
+        float* up = up_;
+        if (PROMOTE) {
+          g = pg;
+          up = pu_;
+        } else {
+          tmem_ld32(tacc + uint32_t(c * CW), g);
+          if (PAIR) tmem_ld32(tacc + uint32_t(c * CW) + ON, up);
+          tmem_ld_wait();
+        }
+        // eight columns at a time, from the accumulators to the item's buffers
+        auto math = [&](auto act_tag) {
+          constexpr int ACT = decltype(act_tag)::value;
 #pragma unroll
-        for (int h = 0; h < CW / 32; ++h) {  // 32 columns at a time
-          const int col = col0 + 32 * h;
-          float g_[32], up_[PAIR ? 32 : 1];
-          float* g = g_;
-          float* up = up_;
-          if (PROMOTE) {  // (CW = 32: one pass)
-            g = pg;
-            up = pu_;
-          } else {
-            const uint32_t tc = tacc + uint32_t(c * CW + 32 * h);
-            tmem_ld32(tc, g);
-            if (PAIR) tmem_ld32(tc + ON, up);
-            tmem_ld_wait();
-          }
-          if (EPI == kEpiFwd || EPI == kEpiDz) {
-            if (KIND == kE4m3) {
-              const float xs = live ? __ldg(a.xs + row) : 0.f;
-              float w[32];
-              load_cols(a.ws, col, a.N, vec_s, w);
+          for (int j = 0; j < 32; j += 8) {
+            float* v = g + j;
+            float* w = up + (PAIR ? j : 0);
+            if (COLS) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) g[k] *= xs * w[k];
-              if (GATED) {
-                load_cols(a.ws + a.N, col, a.N, vec_su, w);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) up[GATED ? k : 0] *= xs * w[k];
-              }
-            }
-            if (a.bias) {
-              float b[32];
-              load_cols(a.bias, col, a.N, vec_b, b);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) g[k] += b[k];
-              if (GATED) {
-                load_cols(a.bias + a.N, col, a.N, vec_bu, b);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) up[GATED ? k : 0] += b[k];
-              }
-            }
-          }
-          float x[IN ? 32 : 1];  // the input's 32 columns of this row
-          if (has_in) {
-#pragma unroll
-            for (int k = 0; k < int(sizeof(TO)) * 2; ++k) {
-              const int slot = h * 4 + k;
-              const uint4 v = *reinterpret_cast<const uint4*>(buf + lane * 128 + ((slot ^ (lane & 7)) << 4));
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (sizeof(TO) == 4) {
-                  x[IN ? 4 * k + e : 0] = __uint_as_float(w[e]);
-                } else {
-                  x[IN ? (8 * k + 2 * e) & 31 : 0] = __uint_as_float(w[e] << 16);
-                  x[IN ? (8 * k + 2 * e + 1) & 31 : 0] = __uint_as_float(w[e] & 0xffff0000u);
+              for (int k = 0; k < 8; ++k) {
+                const float b = __shfl_sync(0xffffffffu, cols.b, j + k);
+                v[k] = SCALED ? fmaf(v[k], xs * __shfl_sync(0xffffffffu, cols.s, j + k), b) : v[k] + b;
+                if (PAIR) {
+                  const float bu = __shfl_sync(0xffffffffu, cols.bu, j + k);
+                  w[PAIR ? k : 0] = SCALED ? fmaf(w[PAIR ? k : 0], xs * __shfl_sync(0xffffffffu, cols.su, j + k), bu)
+                                           : w[PAIR ? k : 0] + bu;
                 }
               }
             }
-          }
-          if (EPI == kEpiFwd) {
-            switch (a.act) {
-              case DSF_ACT_RELU: act_fwd<DSF_ACT_RELU, GATED>(g, up); break;
-              case DSF_ACT_SILU: act_fwd<DSF_ACT_SILU, GATED>(g, up); break;
-              case DSF_ACT_GELU: act_fwd<DSF_ACT_GELU, GATED>(g, up); break;
-              default: act_fwd<DSF_ACT_NONE, GATED>(g, up);
-            }
-            if (has_in) {
+            float x[8];
+            if (has_in) get8(buf, j, x);
+            if (EPI == kEpiFwd) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) g[k] += x[IN ? k : 0];
+              for (int k = 0; k < 8; ++k) {
+                v[k] = act_value<ACT>(v[k]);
+                if (PAIR) v[k] *= w[PAIR ? k : 0];
+                if (has_in) v[k] += x[k];
+              }
             }
-          }
-          if (EPI == kEpiDz) {
-            switch (a.act) {
-              case DSF_ACT_RELU: act_bwd<DSF_ACT_RELU, GATED>(x, g, up); break;
-              case DSF_ACT_SILU: act_bwd<DSF_ACT_SILU, GATED>(x, g, up); break;
-              case DSF_ACT_GELU: act_bwd<DSF_ACT_GELU, GATED>(x, g, up); break;
-              default: act_bwd<DSF_ACT_NONE, GATED>(x, g, up);
-            }
-          }
-          auto put = [&](uint8_t* b, const float* v) {
+            if (EPI == kEpiDz) {
 #pragma unroll
-            for (int k = 0; k < int(sizeof(TO)) * 2; ++k) {
-              const int slot = h * 4 + k;
-              uint4 w;
-              if (sizeof(TO) == 4)
-                w = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
-                               __float_as_uint(v[4 * k + 3]));
-              else
-                w = make_uint4(pack_bf16x2(v[(8 * k) & 31], v[(8 * k + 1) & 31]),
-                               pack_bf16x2(v[(8 * k + 2) & 31], v[(8 * k + 3) & 31]),
-                               pack_bf16x2(v[(8 * k + 4) & 31], v[(8 * k + 5) & 31]),
-                               pack_bf16x2(v[(8 * k + 6) & 31], v[(8 * k + 7) & 31]));
-              *reinterpret_cast<uint4*>(b + lane * 128 + ((slot ^ (lane & 7)) << 4)) = w;
+              for (int k = 0; k < 8; ++k) {
+                const float2 f = act_both<ACT>(v[k]);
+                v[k] = (PAIR ? x[k] * w[PAIR ? k : 0] : x[k]) * f.y;
+                if (PAIR) w[PAIR ? k : 0] = x[k] * f.x;
+              }
             }
-          };
-          put(buf, g);
-          if (EPI == kEpiDz && GATED) put(buf0 + 2 * 4096, up);
-          if (EPI == kEpiDz && a.part) {
-            const float s = column_sum(g, lane);
-            float* p = a.part + (long long)(row0 >> 5) * (halves * a.N);
-            if (col + lane < a.N) p[col + lane] = s;
-            if (GATED) {
-              const float s2 = column_sum(up, lane);
-              if (col + lane < a.N) p[a.N + col + lane] = s2;
-            }
+            put8(buf, j, v);
           }
-        }
-        // the item's output
-        int plane = t.batch;
-        if (EPI == kEpiPart) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * a.nb + t.batch;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (a.out_tma) {
-          if (lane == 0) {
-            tma_store_3d(&mapO, col0, row0, plane, smem_u32(buf));
-            if (EPI == kEpiDz && GATED) tma_store_3d(&mapO, col0, row0, 1, smem_u32(buf0 + 2 * 4096));
-            bulk_commit();
+        };
+        if (EPI == kEpiFwd || EPI == kEpiDz) {
+          switch (a.act) {
+            case DSF_ACT_RELU: math(std::integral_constant<int, DSF_ACT_RELU>{}); break;
+            case DSF_ACT_SILU: math(std::integral_constant<int, DSF_ACT_SILU>{}); break;
+            case DSF_ACT_GELU: math(std::integral_constant<int, DSF_ACT_GELU>{}); break;
+            default: math(std::integral_constant<int, DSF_ACT_NONE>{});
           }
         } else {
-          TO* o = out + plane * a.out_plane;
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r)
+          math(std::integral_constant<int, DSF_ACT_NONE>{});
+        }
+        // (a gated dz: du takes the buffer after dg has left it)
+        int plane = t.batch;
+        if (EPI == kEpiPart) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * a.nb + t.batch;
+        store_item(out + plane * a.out_plane, row0, col0);
+        if (EPI == kEpiDz && PAIR) {
 #pragma unroll
-            for (int j = 0; j < CW / 32; ++j) {
-              const int e = lane + 32 * j, byte = e * int(sizeof(TO));
-              const int at = r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-              if (row0 + r < a.M && col0 + e < a.N)
-                o[(long long)(row0 + r) * a.ldo + col0 + e] = *reinterpret_cast<const TO*>(buf + at);
-            }
-          fence_proxy_async_smem();
-          __syncwarp();
+          for (int j = 0; j < 32; j += 8) put8(buf, j, up + (PAIR ? j : 0));
+          store_item(out + a.out_plane, row0, col0);
         }
-        if (!(EPI == kEpiDz && GATED)) {
-          // the buffer that the next item (or its input's load) takes is free
-          if (lane == 0) {
-            bulk_wait_read<1>();
-            if (has_in && a.in_tma) prefetch();
+        if (EPI == kEpiDz && a.part) {
+          float* p = a.part + (long long)(row0 >> 5) * (halves * a.N) + col0 + lane;
+          const float s = column_sum(g, lane);
+          if (col0 + lane < a.N) p[0] = s;
+          if (PAIR) {
+            const float s2 = column_sum(up, lane);
+            if (col0 + lane < a.N) p[a.N] = s2;
           }
-          __syncwarp();
         }
-        ++item;
+        prefetch(u, c + GR);
       };
       if (PROMOTE) {
         float sum[NI][PAIR ? 2 : 1][32];
@@ -676,40 +696,38 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI>::kThreads, 1)
           for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
-              float v[32];
-              tmem_ld32(tacc + uint32_t((grp + 2 * i) * CW + h * ON) % BN, v);
-              tmem_ld_wait();
+              if (grp + GR * i >= NCH) continue;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sum[i][h][k] = r ? sum[i][h][k] + v[k] : v[k];
+              for (int j = 0; j < 32; j += 16) {
+                float v[16];
+                tmem_ld16(tacc + uint32_t((grp + GR * i) * CW + h * ON + j), v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum[i][h][j + k] = r ? sum[i][h][j + k] + v[k] : v[k];
+              }
             }
           done_run();
         }
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (ok && grp + 2 * i < NCH) do_item(grp + 2 * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
+          if (ok && grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
       } else {
         if (!wait_run()) break;
         const uint32_t tacc = tbase + (run & 1u) * BN + lane_base;
 #pragma unroll 1
-        for (int c = grp; c < NCH && ok; c += 2) do_item(c, tacc, nullptr, nullptr);
+        for (int c = grp; c < NCH && ok; c += GR) do_item(c, tacc, nullptr, nullptr);
         if (!ok) break;
         done_run();
       }
     }
     if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
-    if (lane == 0) {
-      // (an aborted run: inputs asked for and not taken)
-      for (uint32_t i = item; has_in && a.in_tma && i < pi; ++i) mbar_wait(&bars->in[warp][i % RING], (i / RING) & 1u);
-      bulk_wait_all();
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
-  if (warp == 0) {
+  if (warp == S::kEpiWarps + 1) {
     __syncwarp();
     tmem_dealloc_cg<CG>(tbase, S::TCOLS);
   }
@@ -727,13 +745,13 @@ struct Mat {
 // a launch or a tensor map failed.
 struct Product {
   TcArgs a;
-  Mat A, B, in, out;
+  Mat A, B;
   int major;
   bool gated, f32;  // f32: fp32 operands (in terms) and outputs
   int epi, cfg;  // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
 };
 
-bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, bool f32, int box_cols, int box_rows);
+bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows);
 bool run_fwd_product(const Product& p, cudaStream_t s);   // K-major, bf16 operands
 bool run_e4m3_product(const Product& p, cudaStream_t s);  // K-major, e4m3 operands
 bool run_dz_product(const Product& p, cudaStream_t s);
@@ -741,7 +759,7 @@ bool run_grad_product(const Product& p, cudaStream_t s);  // MN-major operands
 
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, class TO, bool PROMOTE>
 bool launch_tc(const Product& p, cudaStream_t s) {
-  using S = Shape<CG, BN, GATED, EPI>;
+  using S = Shape<CG, BN, GATED, EPI, TO>;
   auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, TO, PROMOTE>;
   static int grid_max[64] = {};  // (host threads may race on it: each computes the same value)
   int dev = 0;
@@ -750,13 +768,15 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
   if (grid_max[dev] == 0) {
     int sms = 0, n = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess ||
@@ -772,20 +792,20 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   }
   const long long units = (long long)p.a.mt * p.a.nt * p.a.nb * p.a.splits;
   if (units <= 0 || units * CG > INT32_MAX) return false;
+  TcArgs a = p.a;
+  a.by_splits = make_div(uint32_t(a.splits));
+  a.by_batch = make_div(uint32_t(a.mt) * uint32_t(a.nt));
+  a.by_group = make_div(8u * uint32_t(a.nt));
+  a.by_last = make_div(a.mt % 8 ? uint32_t(a.mt % 8) : 8u);
   const long long g = units * CG < grid_max[dev] ? units * CG : grid_max[dev];
   cfg.gridDim = dim3(unsigned(g));
   constexpr int es = KIND == kBf16 ? 2 : 1;
-  CUtensorMap mA, mB, mI, mO;
-  if (!tensor_map_3d(&mA, p.A, es, false, MAJOR == kNN ? 64 : 128 / es, MAJOR == kNN ? 64 : 128)) return false;
-  if (!tensor_map_3d(&mB, p.B, es, false, MAJOR != kKK ? 64 : 128 / es,
+  CUtensorMap mA, mB;
+  if (!tensor_map_3d(&mA, p.A, es, MAJOR == kNN ? 64 : 128 / es, MAJOR == kNN ? 64 : 128)) return false;
+  if (!tensor_map_3d(&mB, p.B, es, MAJOR != kKK ? 64 : 128 / es,
                      MAJOR != kKK ? 64 : (GATED && CG == 1 ? BN / 2 : BN / CG)))
     return false;
-  constexpr int cw = 128 / int(sizeof(TO));
-  mI = mA;
-  mO = mA;
-  if (p.a.has_in && p.a.in_tma && !tensor_map_3d(&mI, p.in, sizeof(TO), sizeof(TO) == 4, cw, 32)) return false;
-  if (p.a.out_tma && !tensor_map_3d(&mO, p.out, sizeof(TO), sizeof(TO) == 4, cw, 32)) return false;
-  return cudaLaunchKernelEx(&cfg, kernel, p.a, mA, mB, mI, mO) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kernel, a, mA, mB) == cudaSuccess;
 }
 
 // Tile configurations: accumulator columns (an fp32 product's wide tiles are

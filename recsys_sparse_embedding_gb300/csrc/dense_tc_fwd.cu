@@ -26,17 +26,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
 }  // namespace
 
 // x as a 3-D tensor of esize-byte elements whose boxes are box_cols (128
-// bytes, the swizzle span) by box_rows; reads past its edges give zeros,
-// writes past them are dropped.
-bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, bool f32, int box_cols, int box_rows) {
+// bytes, the swizzle span) by box_rows; reads past its edges give zeros.
+bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[3] = {cuuint64_t(x.cols), cuuint64_t(x.rows), cuuint64_t(x.planes)};
   const cuuint64_t strides[2] = {cuuint64_t(x.ld) * esize,
                                  cuuint64_t(x.planes > 1 ? x.plane : x.ld) * esize};
   const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1}, es[3] = {1, 1, 1};
-  const CUtensorMapDataType t = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                    : (esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8);
+  const CUtensorMapDataType t = esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return fn(m, t, 3, const_cast<void*>(x.p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -18,6 +18,7 @@
 
 #include "colsum.cuh"
 #include "dinsparse.h"
+#include "pdl.cuh"
 
 namespace dsf {
 namespace norm {
@@ -161,6 +162,8 @@ template <class TX, class TY, int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdArgs a) {
   constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
   __shared__ float buf[2][32];
+  pdl_go();
+  pdl_wait();
   const int t = threadIdx.x % G;
   const long long row = (long long)blockIdx.x * RPB + threadIdx.x / G;
   if (row >= a.M) return;  // (a whole warp or the whole block)
@@ -236,6 +239,8 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) bwd_kernel(const BwdA
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  pdl_go();
+  pdl_wait();
   int par = 0;  // two sets of reduction buffers: a row's writes never meet the last row's reads
   for (long long row = (long long)blockIdx.x * RPB + grp; row < a.M; row += (long long)gridDim.x * RPB, par ^= 1) {
     float s[V][8], d[V][8];
@@ -344,9 +349,7 @@ struct Fwd {
   bool operator()() const {
     constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
     const unsigned grid = unsigned((a.M + RPB - 1) / RPB);
-    if (al) fwd_kernel<TX, TY, G, V, true><<<grid, T, 0, st>>>(a);
-    else fwd_kernel<TX, TY, G, V, false><<<grid, T, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess;
+    return pdl_launch(al ? fwd_kernel<TX, TY, G, V, true> : fwd_kernel<TX, TY, G, V, false>, dim3(grid), T, st, a);
   }
 };
 template <class TY, class TX>
@@ -358,9 +361,7 @@ struct Bwd {
   bool operator()() const {
     constexpr int T = G == 32 ? kBlock : G;
     const unsigned grid = unsigned(bwd_blocks(a.M, a.N));
-    if (al) bwd_kernel<TY, TX, G, V, true><<<grid, T, 0, st>>>(a);
-    else bwd_kernel<TY, TX, G, V, false><<<grid, T, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess;
+    return pdl_launch(al ? bwd_kernel<TY, TX, G, V, true> : bwd_kernel<TY, TX, G, V, false>, dim3(grid), T, st, a);
   }
 };
 
