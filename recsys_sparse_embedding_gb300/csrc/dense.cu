@@ -53,11 +53,11 @@ struct Plan {
 };
 
 // Tile configuration and K-splits by an estimate in SM cycles: a K-block of
-// a 256 x 256 tile (on two SMs; fp32: 256 x 128), 128 x 128 or 128 x 64 tile takes kStep
+// a 256 x 256 tile (on two SMs; fp32: 256 x 128, six products), 128 x 128 or 128 x 64 tile takes kStep
 // cycles, the chip takes its units in whole waves, and a split product pays
 // for a second launch and its partial sums' way to L2 and back.
 Plan plan(long long M, long long N, int nb, bool gated, bool f32, long long nkb, int nseg, bool may_split) {
-  const double kStep[3] = {f32 ? 430. : 560., 560, 400};
+  const double kStep[3] = {f32 ? 1700. : 560., f32 ? 1800. : 560., f32 ? 1300. : 400.};
   constexpr double kUnit = 1500, kSecond = 5000, kBytesPerCycle = 2000;
   Plan best{};
   double cost = 1e300;
@@ -86,7 +86,7 @@ long long up(long long v, long long to) { return (v + to - 1) / to * to; }
 
 // Workspace layout of a call: each part's offset; `total` grows with M.
 struct Layout {
-  size_t xp, wp, gp, dz, dzp, sums, part, total;
+  size_t xp, wp, gp, dz, sums, part, total;
   long long kp, np;  // padded row lengths of the laid-out operands and of dz
 };
 
@@ -116,8 +116,7 @@ Layout layout(const dsf_dense* l, long long M, bool gated, bool backward) {
   if (backward) {
     const bool own_dz = gated || l->act != DSF_ACT_NONE;  // else dz is dy
     w.gp = take(!own_dz && laid_out(l->dtype, N) ? size_t(terms) * M * w.np * pes : 0);
-    w.dz = take(own_dz ? size_t(halves) * M * w.np * es : 0);
-    w.dzp = take(own_dz && terms == 3 ? size_t(3) * halves * M * w.np * 2 : 0);
+    w.dz = take(own_dz ? size_t(terms) * halves * M * w.np * 2 : 0);
     w.sums = take(size_t((M + 31) / 32) * l->R * 4);
     const size_t px = part_of(size_t(M) * up(l->K, 4)), pw = part_of(size_t(l->R) * up(l->K, 4));
     part = part > px ? part : px;
@@ -143,21 +142,6 @@ struct LayJob {
   long long ld, rows, ldd, cols;
 };
 
-// x's leading 8 significant bits, and what is left, three times: exact for
-// every finite x (the last term may fall below bf16's smallest denormal).
-// A non-finite x keeps its first term and has zeros after it.
-__device__ __forceinline__ void three_terms(float x, uint32_t* t) {
-  const uint32_t u = __float_as_uint(x), h1 = u & 0xffff0000u;
-  const bool fin = (u & 0x7f800000u) != 0x7f800000u;
-  const float r1 = fin ? x - __uint_as_float(h1) : 0.f;
-  const uint32_t h2 = __float_as_uint(r1) & 0xffff0000u;
-  const float r2 = r1 - __uint_as_float(h2);
-  // (a NaN whose payload lies in the low half stays a NaN)
-  t[0] = !fin && (u & 0x007fffffu) ? 0x7fc0u : h1 >> 16;
-  t[1] = h2 >> 16;
-  t[2] = __float_as_uint(r2) >> 16;
-}
-
 template <int ES>  // source element: 4 (fp32 -> three bf16 terms), 2 or 1 (copied)
 __global__ void __launch_bounds__(256) lay_kernel(const LayJob j0, const LayJob j1, const LayJob j2, int b0, int b1) {
   pdl_go();
@@ -181,19 +165,17 @@ __global__ void __launch_bounds__(256) lay_kernel(const LayJob j0, const LayJob 
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = c + k < j.cols ? s[k] : 0.f;
       }
-      uint32_t w[3][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t lo[3], hi[3];
-        three_terms(x[2 * k], lo);
-        three_terms(x[2 * k + 1], hi);
-#pragma unroll
-        for (int t = 0; t < 3; ++t) w[t][k] = lo[t] | hi[t] << 16;
-      }
       uint16_t* d = static_cast<uint16_t*>(j.dst) + r * j.ldd + c;
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<uint4*>(d + t * j.rows * j.ldd) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+      for (int t = 0; t < 3; ++t) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = take_term(x[2 * k]), hi = take_term(x[2 * k + 1]);
+          w[k] = __byte_perm(lo, hi, 0x7632);
+        }
+        *reinterpret_cast<uint4*>(d + t * j.rows * j.ldd) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     } else {
       using E = typename std::conditional<ES == 2, uint16_t, uint8_t>::type;
       const E* s = static_cast<const E*>(j.src) + r * j.ld + c;
@@ -306,9 +288,6 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs a) {
 }
 
 // ---------------------------------------------------------------- products
-// The six pairs of terms, smallest products first.
-constexpr int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-
 bool vec_rows(const void* p, long long ld, int es) { return at(p, 16) && (ld * es) % 16 == 0; }
 
 struct Ctx {
@@ -406,12 +385,9 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.f32 = f32;
   p.epi = dz ? kEpiDz : kEpiFwd;
   const long long nkb = (l->K + c.kbe - 1) / c.kbe;
-  p.a.nseg = f32 ? 6 : 1;
-  p.a.nbig = 1;
-  for (int i = 0; i < p.a.nseg; ++i) {
-    p.a.pa[i] = uint8_t(f32 ? kPairs[i][0] : 0);
-    p.a.pb[i] = uint8_t(f32 ? kPairs[i][1] : 0);
-  }
+  p.a.nseg = 1;
+  p.a.a_term = 1;
+  p.a.b_term = 1;
   set_plan(p, plan(c.M, c.N, 1, c.gated, f32, nkb, p.a.nseg, !dz), c.M, c.N, 1, nkb);
   p.a.act = l->act;
   p.a.bias = l->bias;
@@ -428,7 +404,7 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
     p.a.out = y;
     p.a.ldo = ldy;
     p.a.out_plane = c.M * ldy;
-    p.a.out_vec = vec_rows(y, ldy, c.eo);
+    p.a.out_vec = vec_rows(y, ldy, dz ? 2 : c.eo);
   }
   const bool ok = dz ? run_dz_product(p, c.s) : (l->dtype == DSF_E4M3 ? run_e4m3_product(p, c.s) : run_fwd_product(p, c.s));
   if (!ok || p.a.splits == 1) return ok;
@@ -447,7 +423,7 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   return finish(c, p, f, f32);
 }
 
-// A gradient product over the pairs of terms: dx (dz [.][M][N] times W) or dW
+// A gradient product: dx (dz [.][M][N] times W) or dW
 // (dz^T times x, one batch per half).
 bool grad_product(const Ctx& c, const Mat& dz, bool dW, void* out, long long ldo) {
   const bool f32 = c.l->dtype == DSF_F32;
@@ -458,20 +434,11 @@ bool grad_product(const Ctx& c, const Mat& dz, bool dW, void* out, long long ldo
   p.gated = false;
   p.f32 = f32;
   p.epi = kEpiOut;
-  const int pairs = f32 ? 6 : 1, nb = dW ? c.halves : 1;
-  for (int i = 0; i < pairs; ++i) {
-    const int ta = f32 ? kPairs[i][0] : 0, tb = f32 ? kPairs[i][1] : 0;
-    if (dW) {
-      p.a.pa[p.a.nseg] = uint8_t(ta * c.halves);
-      p.a.pb[p.a.nseg++] = uint8_t(tb);
-    } else {
-      for (int h = 0; h < c.halves; ++h) {
-        p.a.pa[p.a.nseg] = uint8_t(ta * c.halves + h);
-        p.a.pb[p.a.nseg++] = uint8_t(tb * c.halves + h);
-      }
-    }
-  }
-  p.a.nbig = dW ? 1 : c.halves;
+  const int nb = dW ? c.halves : 1;
+  p.a.nseg = dW ? 1 : c.halves;
+  p.a.a_term = c.halves;
+  p.a.a_seg = dW ? 0 : 1;
+  p.a.b_term = dW ? 1 : c.halves;
   const long long rows = dW ? c.N : c.M, depth = dW ? c.M : c.N, nkb = (depth + 63) / 64;
   set_plan(p, plan(rows, c.l->K, nb, false, f32, nkb, p.a.nseg, true), rows, c.l->K, nb, nkb);
   p.a.status = c.status;
@@ -522,11 +489,6 @@ int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void
     void* d = c.ws + c.w.dz;
     if (!layer_product(c, nullptr, dy, lddy, d, c.w.np, true, db ? sums : nullptr)) return DSF_ECUDA;
     if (db && !colsum(sums, (M + 31) / 32, l->R, db, s)) return DSF_ECUDA;
-    if (f32) {
-      const LayJob j{d, c.ws + c.w.dzp, c.w.np, c.halves * M, c.w.np, c.N};
-      if ((dx || dW) && !lay(DSF_F32, &j, 1, s)) return DSF_ECUDA;
-      d = c.ws + c.w.dzp;
-    }
     dz = Mat{d, M, c.N, c.w.np, (long long)c.terms * c.halves, M * c.w.np};
   } else {
     if (db) {

@@ -4,33 +4,35 @@
 // One persistent, warp-specialised kernel. A work unit is a tile of 128 CG x
 // BN accumulators (CG CTAs of a cluster work on one tile together: CG = 2
 // halves what each SM has to read of B), over all of K or one K-split.
-//   warp 16  brings A and B by TMA: K-blocks of 128 bytes per row in the
+//   the load warp  brings A and B by TMA: K-blocks of 128 bytes per row in the
 //            128-byte swizzle, through a ring of stages;
-//   warp 17  issues the MMAs (tcgen05.mma, in the cluster's first CTA) into
-//            one of two accumulators in tensor memory;
-//   warps 0-15 run the epilogue of the other accumulator, in items of 32 rows
-//            (a warp's lane quarter, one row per lane) by 32 columns. Inputs
-//            (the residual, or the upstream gradient; loaded an item ahead)
-//            and outputs change between a row per lane and 16 bytes of
-//            neighbouring lanes in a 2 or 4 KB buffer per warp, so that
-//            global memory sees whole row segments. (Not by TMA: its stores
-//            and loads queue behind the operands' loads, 2 us an item.)
+//   the MMA warp  issues the MMAs (tcgen05.mma, in the cluster's first CTA)
+//            into one of two accumulators in tensor memory;
+//   the bias warp  keeps the bias of this tile's and the next one's columns
+//            in shared memory;
+//   16 (or 8) epilogue warps  turn the other accumulator into outputs, in
+//            items of 32 rows (a warp's lane quarter, one row per lane) by 32
+//            columns. Inputs (the residual, or the upstream gradient; loaded
+//            an item ahead) and outputs change between a row per lane and 16
+//            bytes of neighbouring lanes in a 2 or 4 KB buffer per warp, so
+//            that global memory sees whole row segments. (Not by TMA: its
+//            stores and loads queue behind the operands' loads, 2 us an item.)
 // So a tile's loads, MMAs and epilogue overlap the next tile's. Operands come
 // as three-dimensional tensors [plane][row][column]:
 //   - K-major (columns are K) or MN-major (rows are K: W in dx = dz W, both
 //     operands in dW = dz^T x, which needs no transposed copies);
-//   - planes: the three bf16 terms of an fp32 operand (Terms below), and the
-//     gate and up halves of a gated layer. A product runs over a list of
-//     plane pairs (segments) into one accumulator.
+//   - planes: the three bf16 terms of an fp32 operand, and the gate and up
+//     halves of a gated layer (both in one tile of the forward; two segments
+//     of K in dx; two batches in dW).
 //
-// Terms: x = x1 + x2 + x3 exactly, each the leading 8 significant bits of what
-// is left. x y = sum of the terms' products; those below 2^-21 of it (x2 y3,
-// x3 y2, x3 y3) are dropped. The tensor cores truncate each addition to the
-// accumulator (measured: a run of n additions is low by about n 2^-25 of the
-// sum), so an fp32 product (PROMOTE) keeps its runs short: the five smaller
-// pairs, at most 2^-7 of the sum, share one run, x1 y1 takes a run of its own
-// per 4 K-blocks (16 additions), and the epilogue warps add the runs up in
-// registers, rounding to nearest. Tiles are half as wide for it.
+// fp32 operands (F32): x = x1 + x2 + x3 exactly, each term the leading 8
+// significant bits of what is left. x y is the sum of the terms' products;
+// those below 2^-21 of it (x2 y3, x3 y2, x3 y3) are dropped. A K-block's three
+// terms of A and of B are loaded once and multiplied six ways: x1 y1 into one
+// accumulator, the five smaller products into another. The tensor cores
+// truncate each addition to an accumulator (measured: a run of n additions is
+// low by about n 2^-25 of the sum), so a run is 4 K-blocks, and the epilogue
+// warps add the runs up in registers, rounding to nearest.
 //
 // Every wait is bounded; one that runs out sets DSF_FLAG_TIMEOUT.
 #pragma once
@@ -52,14 +54,13 @@ namespace dense {
 // What the epilogue does with an accumulator.
 enum Epi {
   kEpiFwd = 0,   // out = residual + act(z), or act(z) * z' for a gated layer
-  kEpiDz = 1,    // out = dz (planes dg, du for a gated layer) from in = dy; column sums
+  kEpiDz = 1,    // out = dz (planes dg, du for a gated layer; fp32: its three
+                 // terms) from in = dy; column sums
   kEpiOut = 2,   // out = the accumulator
   kEpiPart = 3,  // fp32 partial sums of a K-split: plane split * planes + (half or batch)
 };
 enum Kind { kBf16 = 0, kE4m3 = 1 };
 enum Major { kKK = 0, kKN = 1, kNN = 2 };  // A and B K-major; B MN-major; both
-
-constexpr int kMaxSeg = 12;
 
 // Division of unsigned 32-bit numbers by a fixed divisor: q = (mulhi(n, m) + n) >> l
 // with l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, exact for every n below 2^31.
@@ -78,9 +79,10 @@ struct TcArgs {
   int mt, nt, nb;    // tiles along M and N, batches (halves of dW)
   Div by_splits, by_batch, by_group, by_last;  // splits; mt nt; 8 nt; M tiles of the last group of 8
   int nkb, kbps;     // K-blocks per segment, per split
-  int nbig;          // PROMOTE: the last nbig segments are the products of leading terms
-  int splits, nseg;
-  uint8_t pa[kMaxSeg], pb[kMaxSeg];  // the segments' planes (A: + batch; B of a gated layer: 2 pb, 2 pb + 1)
+  int splits, nseg;  // K-splits; segments of K (the halves in dx)
+  // planes: A: term * a_term + segment * a_seg + batch; B: term * b_term +
+  // segment (a gated layer's: twice that, + half)
+  int a_term, a_seg, b_term;
   int act;
   const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
   const void* in;            // nullable unless kEpiDz
@@ -125,9 +127,9 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // An arrival that orders nothing but itself: what it announces (accumulators
-// read, tcgen05.wait::ld done) is complete in registers. A release would wait
-// for the thread's global stores.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+// and bias read) is complete in registers. A release would wait for the
+// thread's global stores.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <int CG>
@@ -185,28 +187,36 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- shapes
-template <int CG, int BN, bool GATED, int EPI, class TO>
+template <int CG, int BN, bool GATED, int EPI, bool F32>
 struct Shape {
-#ifndef DZW
-#define DZW 8
-#endif
-  static constexpr int kEpiWarps = GATED && sizeof(TO) == 4 && EPI != kEpiPart ? 8 : (GATED && EPI == kEpiDz ? DZW : 16), kThreads = 32 * (kEpiWarps + 2);
-  static constexpr int kGroups = kEpiWarps / 4;  // warps on one lane quarter
+  using TO = typename std::conditional<F32 || EPI == kEpiPart, float, __nv_bfloat16>::type;  // input and output
+  static constexpr int ON = GATED ? BN / 2 : BN;  // output columns per tile
+  // Epilogue warps: four per lane quarter (scheduler). Two where the kernel
+  // needs the registers (168 instead of 96 a thread: a gated dz, whose items
+  // hold 64 sums or outputs each), which in fp32 is also all that 64 columns
+  // have work for.
+  static constexpr int kEpiWarps = GATED && ((F32 && EPI != kEpiPart) || EPI == kEpiDz) ? 8 : 16;
+  static constexpr int kGroups = kEpiWarps / 4;
+  static constexpr int kLoad = kEpiWarps, kMma = kEpiWarps + 1, kBias = kEpiWarps + 2;
+  static constexpr int kThreads = 32 * (kEpiWarps + 3);
   static constexpr int ITEM = 32 * 32 * int(sizeof(TO));
-  static constexpr int BNC = BN / CG;            // B rows (or MN-major columns) in this CTA
+  static constexpr int BNC = BN / CG;  // B rows (or MN-major columns) in this CTA
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BNC * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int EBYTES = kEpiWarps * ITEM;
-  static constexpr int kRoom = 227 * 1024 - 1024 - 256 - EBYTES;
+  static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiDz;
+  static constexpr int BIAS_BYTES = BIAS ? 2 * BN * 4 : 0, BAR_BYTES = 256;
+  static constexpr int kRoom = 227 * 1024 - EBYTES - BIAS_BYTES - BAR_BYTES;
   static constexpr int STAGES = kRoom / STAGE < 8 ? kRoom / STAGE : 8;
-  static constexpr int SMEM = STAGES * STAGE + EBYTES + 256 + 1024;
-  static constexpr uint32_t TCOLS = 2 * BN;      // two accumulators
+  static constexpr int SMEM = STAGES * STAGE + EBYTES + BIAS_BYTES + BAR_BYTES;
+  static constexpr int ACC = F32 ? 2 * BN : BN;  // tensor-memory columns of an accumulator
+  static constexpr uint32_t TCOLS = 2 * ACC;
   static_assert(TCOLS <= 512 && (TCOLS & (TCOLS - 1)) == 0, "tensor memory columns");
-  static_assert(STAGES >= 3, "ring");
+  static_assert(STAGES >= 4, "ring");
   static_assert(B_BYTES % (GATED && CG == 1 ? 2048 : 1024) == 0, "swizzle atoms");
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tfull[2], tempty[2];
+  uint64_t full[8], empty[8], tfull[2], tempty[2], bfull[2], bempty[2];
   uint32_t tmem;
   int abort_;
 };
@@ -214,6 +224,19 @@ static_assert(sizeof(Bars) <= 256, "barrier block");
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The leading 8 significant bits of x, as bf16 bits in the upper half of the
+// word; x becomes what is left. A non-finite x leaves 0 (a NaN stays one).
+__device__ __forceinline__ uint32_t take_term(float& x) {
+  const uint32_t u = __float_as_uint(x);
+  if ((u & 0x7f800000u) == 0x7f800000u) {
+    x = 0.f;
+    return u & 0x007fffffu ? 0x7fc00000u : u;
+  }
+  const uint32_t h = u & 0xffff0000u;
+  x -= __uint_as_float(h);
+  return h;
+}
 
 // sums of 32 columns over a warp's 32 rows (one row per lane): lane l returns
 // column l's. Each step halves the columns a lane holds.
@@ -235,37 +258,41 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
   tmem_ld16(t + 16, v + 16);
 }
 
-// ---------------------------------------------------------------- the kernel
-constexpr int kRun = 4;  // PROMOTE: K-blocks of leading terms per run
-
-// Accumulator runs of a unit with kbn K-blocks per segment.
-template <bool PROMOTE>
-__device__ __forceinline__ int runs_of(const TcArgs& a, int kbn) {
-  return PROMOTE ? (a.nseg > a.nbig ? 1 : 0) + (a.nbig * kbn + kRun - 1) / kRun : 1;
+// Byte `at` of row r of a 32-row buffer with ROWB bytes per row: 16-byte slots
+// XOR-swizzled by the row, so that neither a slot of 8 rows nor whole rows
+// meet in a bank.
+template <int ROWB>
+__device__ __forceinline__ int slot(int r, int at) {
+  return r * ROWB + (((at >> 4) ^ (ROWB == 64 ? (r >> 1) & 3 : r & 7)) << 4) + (at & 15);
 }
 
-template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, class TO, bool PROMOTE>
-__global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
+constexpr int kRun = 4;  // F32: K-blocks per accumulator run
+
+// ---------------------------------------------------------------- the kernel
+template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
+__global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
     tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mapA,
               const __grid_constant__ CUtensorMap mapB) {
-  using S = Shape<CG, BN, GATED, EPI, TO>;
+  using S = Shape<CG, BN, GATED, EPI, F32>;
+  using TO = typename S::TO;
   constexpr bool AMN = MAJOR == kNN, BMN = MAJOR != kKK;
-  constexpr int kBK = KIND == kBf16 ? 64 : 128;            // K elements per block (128 bytes)
-  constexpr int ON = GATED ? BN / 2 : BN;                  // output columns per tile
-  constexpr int CW = 32;                                   // output columns per item
-  constexpr int ROWB = CW * int(sizeof(TO));               // an item row's bytes
-  constexpr int STAGES = S::STAGES;
+  constexpr int kBK = KIND == kBf16 ? 64 : 128;  // K elements per block (128 bytes)
+  constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : 1;
   static_assert(!(GATED && BMN), "a gated layer's product is K-major");
-  extern __shared__ uint8_t dyn[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sE = sm + STAGES * S::STAGE;
-  Bars* bars = reinterpret_cast<Bars*>(sE + S::EBYTES);
+  float* sBias = reinterpret_cast<float*>(sE + S::EBYTES);
+  Bars* bars = reinterpret_cast<Bars*>(sE + S::EBYTES + S::BIAS_BYTES);
+  if (smem_u32(sm) & 1023u) {  // (the swizzle atoms' alignment; every thread of the grid takes the same way)
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int unit0 = blockIdx.x / CG, units_step = gridDim.x / CG;
   const int tiles = a.mt * a.nt * a.nb, units = tiles * a.splits;
 
-  if (warp == S::kEpiWarps && lane == 0) {
+  if (warp == S::kLoad && lane == 0) {
     prefetch_map(&mapA);
     prefetch_map(&mapB);
   }
@@ -277,6 +304,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
       mbar_init(&bars->tempty[i], S::kEpiWarps * CG);
+      mbar_init(&bars->bfull[i], 1);
+      mbar_init(&bars->bempty[i], S::kEpiWarps);
     }
     bars->abort_ = 0;
     fence_mbarrier_init();
@@ -286,8 +315,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
   pdl_go();
   // (the loads start while tensor memory is being allocated)
   uint32_t tbase = 0;
-  if (warp != S::kEpiWarps) {
-    if (warp == S::kEpiWarps + 1) {
+  if (warp != S::kLoad) {
+    if (warp == S::kMma) {
       tmem_alloc_cg<CG>(&bars->tmem, S::TCOLS);
       tmem_relinquish_cg<CG>();
       tc_fence_before();
@@ -320,46 +349,47 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
     return t;
   };
 
-  if (warp == S::kEpiWarps) {
+  if (warp == S::kLoad) {
     // ------------------------------------------------ loads (one thread)
     if (lane == 0) {
       pdl_wait();
-      uint32_t it = 0;  // K-blocks so far
+      uint32_t it = 0;  // stages filled so far
       bool ok = true;
       const uint32_t full0 = CG == 2 ? mapa(smem_u32(&bars->full[0]), 0) : smem_u32(&bars->full[0]);
       for (int u = unit0; u < units && ok; u += units_step) {
         const Unit t = unit_of(u);
-        for (int sg = 0; sg < a.nseg && ok; ++sg) {
-          const int za = a.pa[sg] + t.batch, zb = a.pb[sg];
-          for (int k = 0; k < t.kbn; ++k, ++it) {
-            const int st = int(it % STAGES);
-            if (it >= STAGES && !(ok = mbar_wait(&bars->empty[st], ((it / STAGES) - 1) & 1u))) break;
-            const uint32_t bar = full0 + uint32_t(st) * 8u;
-            if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], uint32_t(CG * S::STAGE));
-            const uint32_t sa = smem_u32(sm + st * S::STAGE), sb = sa + S::A_BYTES;
-            const int kx = (t.kb0 + k) * kBK;
-            if (AMN) {
-              tma_load_3d<CG>(sa, &mapA, t.m0, kx, za, bar);
-              tma_load_3d<CG>(sa + 8192, &mapA, t.m0 + 64, kx, za, bar);
-            } else {
-              tma_load_3d<CG>(sa, &mapA, kx, t.m0, za, bar);
-            }
-            if (GATED) {
-              if (CG == 2) {  // the gate half in one CTA, the up half in the other
-                tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb + int(rank), bar);
+        for (int sg = 0; sg < a.nseg && ok; ++sg)
+          for (int k = 0; k < t.kbn && ok; ++k)
+#pragma unroll 1
+            for (int term = 0; term < TERMS; ++term, ++it) {
+              const int st = int(it % STAGES);
+              if (it >= STAGES && !(ok = mbar_wait(&bars->empty[st], ((it / STAGES) - 1) & 1u))) break;
+              const int za = term * a.a_term + sg * a.a_seg + t.batch, zb = term * a.b_term + sg;
+              const uint32_t bar = full0 + uint32_t(st) * 8u;
+              if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], uint32_t(CG * S::STAGE));
+              const uint32_t sa = smem_u32(sm + st * S::STAGE), sb = sa + S::A_BYTES;
+              const int kx = (t.kb0 + k) * kBK;
+              if (AMN) {
+                tma_load_3d<CG>(sa, &mapA, t.m0, kx, za, bar);
+                tma_load_3d<CG>(sa + 8192, &mapA, t.m0 + 64, kx, za, bar);
               } else {
-                tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb, bar);
-                tma_load_3d<CG>(sb + S::B_BYTES / 2, &mapB, kx, t.n0, 2 * zb + 1, bar);
+                tma_load_3d<CG>(sa, &mapA, kx, t.m0, za, bar);
               }
-            } else if (BMN) {
+              if (GATED) {
+                if (CG == 2) {  // the gate half in one CTA, the up half in the other
+                  tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb + int(rank), bar);
+                } else {
+                  tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb, bar);
+                  tma_load_3d<CG>(sb + S::B_BYTES / 2, &mapB, kx, t.n0, 2 * zb + 1, bar);
+                }
+              } else if (BMN) {
 #pragma unroll
-              for (int j = 0; j < S::BNC / 64; ++j)
-                tma_load_3d<CG>(sb + j * 8192, &mapB, t.n0 + int(rank) * S::BNC + 64 * j, kx, zb, bar);
-            } else {
-              tma_load_3d<CG>(sb, &mapB, kx, t.n0 + int(rank) * S::BNC, zb, bar);
+                for (int j = 0; j < S::BNC / 64; ++j)
+                  tma_load_3d<CG>(sb + j * 8192, &mapB, t.n0 + int(rank) * S::BNC + 64 * j, kx, zb, bar);
+              } else {
+                tma_load_3d<CG>(sb, &mapB, kx, t.n0 + int(rank) * S::BNC, zb, bar);
+              }
             }
-          }
-        }
       }
       // the last loads have landed before the CTA may end (bounded)
       if (!ok) atomicExch(&bars->abort_, 1);
@@ -367,39 +397,87 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
         if (!mbar_wait(&bars->full[j % STAGES], (j / STAGES) & 1u)) atomicExch(&bars->abort_, 1);
     }
     __syncwarp();
-  } else if (warp == S::kEpiWarps + 1) {
+  } else if (warp == S::kMma) {
     // ------------------------------------------------ MMAs (one thread of the cluster)
     if (lane == 0 && rank == 0) {
       constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (AMN ? 1u << 15 : 0u) |
                               (BMN ? 1u << 16 : 0u) | (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
       uint32_t it = 0, run = 0;
       bool ok = true;
+      // a K-block of A in stage sa times one of B in stage sb
+      auto block = [&](uint32_t d, uint32_t sta, uint32_t stb, bool accumulate) {
+        const uint32_t sa = smem_u32(sm + sta * S::STAGE), sb = smem_u32(sm + stb * S::STAGE) + S::A_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma<CG, KIND>(d, AMN ? mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
+                        BMN ? mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32), ID,
+                        (accumulate || kk > 0) ? 1u : 0u);
+      };
+      auto wait_full = [&](uint32_t i) {
+        if (ok) ok = mbar_wait(&bars->full[i % STAGES], (i / STAGES) & 1u);
+        tc_fence_after();
+        return ok;
+      };
       for (int u = unit0; u < units && ok; u += units_step) {
         const Unit t = unit_of(u);
-        int left = a.nseg * t.kbn, len = left;
-        if (PROMOTE) len = a.nseg > a.nbig ? (a.nseg - a.nbig) * t.kbn : min(left, kRun);
-        for (; left > 0 && ok; ++run) {
-          const uint32_t acc = run & 1u;
+        for (int left = a.nseg * t.kbn; left > 0 && ok; ++run) {
+          const int len = F32 ? min(left, kRun) : left;
+          const uint32_t acc = run & 1u, d = tbase + acc * S::ACC;
           if (run >= 2 && !(ok = mbar_wait(&bars->tempty[acc], ((run >> 1) - 1) & 1u))) break;
           tc_fence_after();
-          const uint32_t d = tbase + acc * BN;
-          for (int k = 0; k < len; ++k, ++it) {
-            const uint32_t st = it % STAGES;
-            if (!(ok = mbar_wait(&bars->full[st], (it / STAGES) & 1u))) break;
-            tc_fence_after();
-            const uint32_t sa = smem_u32(sm + st * S::STAGE), sb = sa + S::A_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma<CG, KIND>(d, AMN ? mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
-                            BMN ? mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32), ID, (k | kk) ? 1u : 0u);
-            mma_commit<CG>(&bars->empty[st]);
+          for (int k = 0; k < len; ++k) {
+            if (!F32) {
+              if (!wait_full(it)) break;
+              block(d, it % STAGES, it % STAGES, k > 0);
+              mma_commit<CG>(&bars->empty[it % STAGES]);
+              ++it;
+            } else {
+              const uint32_t s0 = it % STAGES, s1 = (it + 1) % STAGES, s2 = (it + 2) % STAGES;
+              if (!wait_full(it)) break;
+              block(d, s0, s0, k > 0);
+              if (!wait_full(it + 1)) break;
+              block(d + BN, s0, s1, k > 0);
+              block(d + BN, s1, s0, true);
+              block(d + BN, s1, s1, true);
+              if (!wait_full(it + 2)) break;
+              block(d + BN, s0, s2, true);
+              block(d + BN, s2, s0, true);
+              mma_commit<CG>(&bars->empty[s0]);
+              mma_commit<CG>(&bars->empty[s1]);
+              mma_commit<CG>(&bars->empty[s2]);
+              it += 3;
+            }
           }
           if (ok) mma_commit<CG>(&bars->tfull[acc]);
           left -= len;
-          len = min(left, kRun);
         }
       }
       if (!ok) atomicExch(&bars->abort_, 1);
+    }
+    __syncwarp();
+  } else if (warp == S::kBias) {
+    // ------------------------------------------------ bias of the tiles' columns
+    if (S::BIAS && a.bias) {
+      pdl_wait();
+      uint32_t tile = 0;
+      for (int u = unit0; u < units; u += units_step, ++tile) {
+        const Unit t = unit_of(u);
+        const uint32_t p = tile & 1u;
+        bool ok = !*aborted;
+        if (ok && lane == 0 && tile >= 2) ok = mbar_wait(&bars->bempty[p], ((tile >> 1) - 1) & 1u);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) atomicExch(&bars->abort_, 1);
+          break;
+        }
+#pragma unroll
+        for (int i = lane; i < BN; i += 32) {  // (gated: the gate's columns, then the up half's)
+          const int n = t.n0 + i % ON;
+          sBias[p * BN + i] = n < a.N ? __ldg(a.bias + (i / ON) * a.N + n) : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->bfull[p]);
+      }
     }
     __syncwarp();
   } else {
@@ -409,26 +487,23 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
     uint8_t* buf = sE + warp * S::ITEM;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
     constexpr bool IN = (EPI == kEpiFwd && !GATED) || EPI == kEpiDz;
-    constexpr int GR = S::kGroups;
-    // byte `at` of an item's row r; 16-byte slots XOR-swizzled by the row, so that neither a
-    // slot of 8 rows nor whole rows meet in a bank
-    auto slot = [](int r, int at) {
-      return r * ROWB + (((at >> 4) ^ (ROWB == 64 ? (r >> 1) & 3 : r & 7)) << 4) + (at & 15);
-    };
-    const bool has_in = IN && (EPI == kEpiDz || a.in);
-    const TO* in = static_cast<const TO*>(a.in);
-    TO* out = static_cast<TO*>(a.out);
+    constexpr bool SCALED = KIND == kE4m3 && EPI == kEpiFwd;
+    constexpr bool TERMS_OUT = F32 && EPI == kEpiDz;  // dz leaves as three bf16 terms
+    constexpr bool PAIR = GATED && EPI != kEpiPart;   // an item takes gate and up accumulators
+    constexpr int GR = S::kGroups, ROWB = CW * int(sizeof(TO));
     constexpr int halves = GATED ? 2 : 1;
-    // columns this item kind walks: accumulator columns for partial sums of a gated layer
-    constexpr int WALK = GATED && EPI == kEpiPart ? BN : ON;
-    constexpr int NCH = WALK / CW;
+    // items of a tile side by side: over its accumulators for a gated layer's partial sums, else over its outputs
+    constexpr int NCH = (GATED && EPI == kEpiPart ? BN : ON) / CW;
+    constexpr int NI = (NCH + GR - 1) / GR;  // items per warp and tile
+    const bool has_in = IN && (EPI == kEpiDz || a.in), has_bias = S::BIAS && a.bias;
+    const TO* in = static_cast<const TO*>(a.in);
     const uint32_t tempty0 = CG == 2 ? mapa(smem_u32(&bars->tempty[0]), 0) : smem_u32(&bars->tempty[0]);
-    constexpr bool COLS = EPI == kEpiFwd || EPI == kEpiDz, SCALED = KIND == kE4m3 && EPI == kEpiFwd;
-    // columns j .. j + 7 of this lane's row, from and to an item's buffer
-    auto get8 = [&](const uint8_t* b, int j, float* v) {
+
+    // columns j .. j + 7 of this lane's row, from and to the buffer
+    auto get8 = [&](int j, float* v) {
 #pragma unroll
       for (int k = 0; k < int(sizeof(TO)) / 2; ++k) {
-        const uint4 u = *reinterpret_cast<const uint4*>(b + slot(lane, j * int(sizeof(TO)) + 16 * k));
+        const uint4 u = *reinterpret_cast<const uint4*>(buf + slot<ROWB>(lane, j * int(sizeof(TO)) + 16 * k));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -441,7 +516,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
         }
       }
     };
-    auto put8 = [&](uint8_t* b, int j, const float* v) {
+    auto put8 = [&](int j, const float* v) {
 #pragma unroll
       for (int k = 0; k < int(sizeof(TO)) / 2; ++k) {
         uint4 w;
@@ -451,10 +526,9 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
         else
           w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                          pack_bf16x2(v[6], v[7]));
-        *reinterpret_cast<uint4*>(b + slot(lane, j * int(sizeof(TO)) + 16 * k)) = w;
+        *reinterpret_cast<uint4*>(buf + slot<ROWB>(lane, j * int(sizeof(TO)) + 16 * k)) = w;
       }
     };
-
     // A 16-byte piece of an item for each lane: 4 (bf16) or 8 (fp32) lanes side
     // by side on a row. Pieces past the matrix's edge element by element.
     constexpr int EL = 16 / int(sizeof(TO)), LPR = CW / EL, RPI = 32 / LPR, NV = 32 / RPI;
@@ -481,28 +555,30 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
         }
       }
     };
-    auto store_item = [&](TO* base, int r0, int c0) {  // from the buffer
+    // the buffer's item (of element type T) to rows r0 .., columns c0 .. of base
+    auto store_item = [&](auto* base, int r0, int c0) {
+      using T = typename std::remove_pointer<decltype(base)>::type;
+      constexpr int ES = int(sizeof(T)), RB = CW * ES, E = 16 / ES, L = CW / E, RP = 32 / L;
       __syncwarp();
       if (a.out_vec) {
-        const int cc = c0 + piece_col;
+        const int pr = lane / L, pc = lane % L * E, cc = c0 + pc;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int rr = i * RPI + piece_row, r = r0 + rr;
-          const uint8_t* b = buf + slot(rr, piece_col * int(sizeof(TO)));
-          TO* p = base + (long long)r * a.ldo + cc;
+        for (int i = 0; i < 32 / RP; ++i) {
+          const int rr = i * RP + pr, r = r0 + rr;
+          const uint8_t* b = buf + slot<RB>(rr, pc * ES);
+          T* p = base + (long long)r * a.ldo + cc;
           if (r >= a.M || cc >= a.N) continue;
-          if (cc + EL <= a.N) {
+          if (cc + E <= a.N) {
             *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
           } else {
-            for (int e = 0; cc + e < a.N; ++e) p[e] = reinterpret_cast<const TO*>(b)[e];
+            for (int e = 0; cc + e < a.N; ++e) p[e] = reinterpret_cast<const T*>(b)[e];
           }
         }
       } else {
 #pragma unroll 8
         for (int r = 0; r < 32; ++r)
           if (r0 + r < a.M && c0 + lane < a.N)
-            base[(long long)(r0 + r) * a.ldo + c0 + lane] =
-                *reinterpret_cast<const TO*>(buf + slot(r, lane * int(sizeof(TO))));
+            base[(long long)(r0 + r) * a.ldo + c0 + lane] = *reinterpret_cast<const T*>(buf + slot<RB>(r, lane * ES));
       }
       __syncwarp();
     };
@@ -524,51 +600,33 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
       }
     };
     prefetch(unit0, grp);
-    // bias and scales of an item's columns, one column per lane: handed round by
-    // shuffles (the L1 that 220 KB of shared memory leave does not keep them)
-    struct Cols {
-      float b, bu, s, su;
-    };
-    auto load_cols = [&](int c0) {
-      Cols v = {0.f, 0.f, 1.f, 1.f};
-      if (COLS && c0 + lane < a.N) {
-        const int n = c0 + lane;
-        if (a.bias) {
-          v.b = __ldg(a.bias + n);
-          if (GATED) v.bu = __ldg(a.bias + a.N + n);
-        }
-        if (SCALED) {
-          v.s = __ldg(a.ws + n);
-          if (GATED) v.su = __ldg(a.ws + a.N + n);
-        }
-      }
-      return v;
-    };
 
-    uint32_t run = 0;
+    uint32_t run = 0, tile = 0;
     bool ok = true;
-    constexpr bool PAIR = GATED && EPI != kEpiPart;  // an item takes gate and up accumulators
-    constexpr int NI = (NCH + GR - 1) / GR;          // items per warp and tile
-    auto wait_run = [&]() {                          // the run's accumulator is complete
+    auto wait_for = [&](uint64_t* bar, uint32_t parity) {
       if (*aborted) ok = false;
-      if (ok && lane == 0) ok = mbar_wait(&bars->tfull[run & 1u], (run >> 1) & 1u);
+      if (ok && lane == 0) ok = mbar_wait(bar, parity);
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      return ok;
+    };
+    auto wait_run = [&]() {  // the run's accumulator is complete
+      wait_for(&bars->tfull[run & 1u], (run >> 1) & 1u);
       tc_fence_after();
       return ok;
     };
     auto done_run = [&]() {  // and may be overwritten
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0 + (run & 1u) * 8u);
+      if (lane == 0) mbar_arrive_relaxed(tempty0 + (run & 1u) * 8u);
       ++run;
     };
-    for (int u = unit0; u < units && ok; u += units_step) {
+    for (int u = unit0; u < units && ok; u += units_step, ++tile) {
       const Unit t = unit_of(u);
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
-      const bool live = row < a.M;
-      // one item: 32 rows by CW columns. PROMOTE: pg, pu_ hold its sums
-      auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu_) {
-        const int col0 = WALK == BN && GATED ? t.n0 + (c * CW) % ON : t.n0 + c * CW;
+      const float* bias_g = sBias + (tile & 1u) * BN;
+      // one item: 32 rows by CW columns. F32: pg, pu hold its sums
+      auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
+        const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
         if (row0 >= a.M || col0 >= a.N) {
           prefetch(u, c + GR);
           return;
@@ -580,11 +638,12 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
               load_item(v, row0, col0);
 #pragma unroll
               for (int i = 0; i < NV; ++i)
-                *reinterpret_cast<uint4*>(buf + slot(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = v[i];
+                *reinterpret_cast<uint4*>(buf + slot<ROWB>(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = v[i];
             } else {
 #pragma unroll
               for (int i = 0; i < NV; ++i)
-                *reinterpret_cast<uint4*>(buf + slot(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = pin[PRE ? i : 0];
+                *reinterpret_cast<uint4*>(buf + slot<ROWB>(i * RPI + piece_row, piece_col * int(sizeof(TO)))) =
+                    pin[PRE ? i : 0];
             }
           } else {  // one column per lane, 16 rows in flight
 #pragma unroll 1
@@ -597,46 +656,59 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
               }
 #pragma unroll
               for (int r = 0; r < 16; ++r)
-                *reinterpret_cast<TO*>(buf + slot(r0 + r, lane * int(sizeof(TO)))) = v[r];
+                *reinterpret_cast<TO*>(buf + slot<ROWB>(r0 + r, lane * int(sizeof(TO)))) = v[r];
             }
           }
           __syncwarp();
         }
-        const Cols cols = load_cols(col0);
-        const float xs = SCALED && live ? __ldg(a.xs + row) : 0.f;
+        // e4m3: the row's scale, and the columns' (one per lane, handed round by shuffles)
+        float xs = 0.f, ws = 0.f, wsu = 0.f;
+        if (SCALED) {
+          if (row < a.M) xs = __ldg(a.xs + row);
+          if (col0 + lane < a.N) {
+            ws = __ldg(a.ws + col0 + lane);
+            if (PAIR) wsu = __ldg(a.ws + a.N + col0 + lane);
+          }
+        }
         // g (and up): the accumulators of this lane's row, then the outputs
         float g_[32], up_[PAIR ? 32 : 1];
         float* g = g_;
         float* up = up_;
-        if (PROMOTE) {
+        if (F32) {
           g = pg;
-          up = pu_;
+          up = pu;
         } else {
           tmem_ld32(tacc + uint32_t(c * CW), g);
           if (PAIR) tmem_ld32(tacc + uint32_t(c * CW) + ON, up);
           tmem_ld_wait();
         }
-        // eight columns at a time, from the accumulators to the item's buffers
+        // eight columns at a time, from the accumulators to the buffer
         auto math = [&](auto act_tag) {
           constexpr int ACT = decltype(act_tag)::value;
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             float* v = g + j;
             float* w = up + (PAIR ? j : 0);
-            if (COLS) {
+            if (SCALED) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float b = __shfl_sync(0xffffffffu, cols.b, j + k);
-                v[k] = SCALED ? fmaf(v[k], xs * __shfl_sync(0xffffffffu, cols.s, j + k), b) : v[k] + b;
+                v[k] *= xs * __shfl_sync(0xffffffffu, ws, j + k);
+                if (PAIR) w[PAIR ? k : 0] *= xs * __shfl_sync(0xffffffffu, wsu, j + k);
+              }
+            }
+            if (has_bias) {
+#pragma unroll
+              for (int k = 0; k < 8; k += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(bias_g + cc + j + k);
+                v[k] += b.x, v[k + 1] += b.y, v[k + 2] += b.z, v[k + 3] += b.w;
                 if (PAIR) {
-                  const float bu = __shfl_sync(0xffffffffu, cols.bu, j + k);
-                  w[PAIR ? k : 0] = SCALED ? fmaf(w[PAIR ? k : 0], xs * __shfl_sync(0xffffffffu, cols.su, j + k), bu)
-                                           : w[PAIR ? k : 0] + bu;
+                  const float4 d = *reinterpret_cast<const float4*>(bias_g + ON + cc + j + k);
+                  w[PAIR ? k : 0] += d.x, w[PAIR ? k + 1 : 0] += d.y, w[PAIR ? k + 2 : 0] += d.z, w[PAIR ? k + 3 : 0] += d.w;
                 }
               }
             }
             float x[8];
-            if (has_in) get8(buf, j, x);
+            if (has_in) get8(j, x);
             if (EPI == kEpiFwd) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
@@ -653,7 +725,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
                 if (PAIR) w[PAIR ? k : 0] = x[k] * f.x;
               }
             }
-            put8(buf, j, v);
+            if (!TERMS_OUT) put8(j, v);
           }
         };
         if (EPI == kEpiFwd || EPI == kEpiDz) {
@@ -666,59 +738,94 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
         } else {
           math(std::integral_constant<int, DSF_ACT_NONE>{});
         }
-        // (a gated dz: du takes the buffer after dg has left it)
-        int plane = t.batch;
-        if (EPI == kEpiPart) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * a.nb + t.batch;
-        store_item(out + plane * a.out_plane, row0, col0);
-        if (EPI == kEpiDz && PAIR) {
+        auto sums = [&](float* v, int half) {  // (takes v apart)
+          const float s = column_sum(v, lane);
+          if (col0 + lane < a.N) a.part[((long long)(row0 >> 5) * halves + half) * a.N + col0 + lane] = s;
+        };
+        if (TERMS_OUT) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out);
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) put8(buf, j, up + (PAIR ? j : 0));
-          store_item(out + a.out_plane, row0, col0);
-        }
-        if (EPI == kEpiDz && a.part) {
-          float* p = a.part + (long long)(row0 >> 5) * (halves * a.N) + col0 + lane;
-          const float s = column_sum(g, lane);
-          if (col0 + lane < a.N) p[0] = s;
-          if (PAIR) {
-            const float s2 = column_sum(up, lane);
-            if (col0 + lane < a.N) p[a.N] = s2;
+          for (int h = 0; h < halves; ++h) {
+            float* v = h ? up : g;
+            if (a.part) {
+              float s[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] = v[k];
+              sums(s, h);
+            }
+            __syncwarp();  // (the input is read, or the last term gone, before the buffer is written)
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t lo = take_term(v[j + 2 * k]), hi = take_term(v[j + 2 * k + 1]);
+                  w[k] = __byte_perm(lo, hi, 0x7632);
+                }
+                *reinterpret_cast<uint4*>(buf + slot<64>(lane, 2 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              store_item(o + (term * halves + h) * a.out_plane, row0, col0);
+            }
+          }
+        } else {
+          int plane = t.batch;
+          if (EPI == kEpiPart) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * a.nb + t.batch;
+          TO* o = static_cast<TO*>(a.out) + plane * a.out_plane;
+          store_item(o, row0, col0);
+          if (EPI == kEpiDz && PAIR) {  // du takes the buffer after dg has left it
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) put8(j, up + (PAIR ? j : 0));
+            store_item(o + a.out_plane, row0, col0);
+          }
+          if (EPI == kEpiDz && a.part) {
+            sums(g, 0);
+            if (PAIR) sums(up, 1);
           }
         }
         prefetch(u, c + GR);
       };
-      if (PROMOTE) {
+      if (F32) {
         float sum[NI][PAIR ? 2 : 1][32];
-        const int runs = runs_of<PROMOTE>(a, t.kbn);
+        const int runs = (a.nseg * t.kbn + kRun - 1) / kRun;
         for (int r = 0; r < runs; ++r) {
           if (!wait_run()) break;
-          const uint32_t tacc = tbase + (run & 1u) * BN + lane_base;
+          const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
               if (grp + GR * i >= NCH) continue;
+              const uint32_t col = tacc + uint32_t((grp + GR * i) * CW + h * ON);
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {
-                float v[16];
-                tmem_ld16(tacc + uint32_t((grp + GR * i) * CW + h * ON + j), v);
+                float v[16], w[16];
+                tmem_ld16(col + j, v);
+                tmem_ld16(col + BN + j, w);  // the smaller products
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) sum[i][h][j + k] = r ? sum[i][h][j + k] + v[k] : v[k];
+                for (int k = 0; k < 16; ++k) sum[i][h][j + k] = (r ? sum[i][h][j + k] : 0.f) + (v[k] + w[k]);
               }
             }
           done_run();
         }
+        if (ok && has_bias) wait_for(&bars->bfull[tile & 1u], (tile >> 1) & 1u);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (ok && grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
+          if (grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
       } else {
         if (!wait_run()) break;
-        const uint32_t tacc = tbase + (run & 1u) * BN + lane_base;
+        if (has_bias && !wait_for(&bars->bfull[tile & 1u], (tile >> 1) & 1u)) break;
+        const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
 #pragma unroll 1
-        for (int c = grp; c < NCH && ok; c += GR) do_item(c, tacc, nullptr, nullptr);
-        if (!ok) break;
+        for (int c = grp; c < NCH; c += GR) do_item(c, tacc, nullptr, nullptr);
         done_run();
+      }
+      if (has_bias) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(smem_u32(&bars->bempty[tile & 1u]));
       }
     }
     if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
@@ -727,7 +834,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, TO>::kThreads, 1)
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
-  if (warp == S::kEpiWarps + 1) {
+  if (warp == S::kMma) {
     __syncwarp();
     tmem_dealloc_cg<CG>(tbase, S::TCOLS);
   }
@@ -741,26 +848,26 @@ struct Mat {
   long long rows, cols, ld, planes, plane;  // ld, plane: strides in elements
 };
 
-// One product; fills in tiles and splits' bookkeeping and launches. false:
-// a launch or a tensor map failed.
+// One product.
 struct Product {
   TcArgs a;
   Mat A, B;
   int major;
-  bool gated, f32;  // f32: fp32 operands (in terms) and outputs
-  int epi, cfg;  // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
+  bool gated, f32;  // f32: fp32 operands (in terms)
+  int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
 };
 
 bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows);
+// Launches; false: a launch or a tensor map failed.
 bool run_fwd_product(const Product& p, cudaStream_t s);   // K-major, bf16 operands
 bool run_e4m3_product(const Product& p, cudaStream_t s);  // K-major, e4m3 operands
 bool run_dz_product(const Product& p, cudaStream_t s);
 bool run_grad_product(const Product& p, cudaStream_t s);  // MN-major operands
 
-template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, class TO, bool PROMOTE>
+template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
 bool launch_tc(const Product& p, cudaStream_t s) {
-  using S = Shape<CG, BN, GATED, EPI, TO>;
-  auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, TO, PROMOTE>;
+  using S = Shape<CG, BN, GATED, EPI, F32>;
+  auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32>;
   static int grid_max[64] = {};  // (host threads may race on it: each computes the same value)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
@@ -809,15 +916,15 @@ bool launch_tc(const Product& p, cudaStream_t s) {
 }
 
 // Tile configurations: accumulator columns (an fp32 product's wide tiles are
-// half as wide) and rows.
-constexpr int cfg_bn(int cfg, bool promote) { return cfg == 0 ? (promote ? 128 : 256) : (cfg == 1 ? 128 : 64); }
+// half as wide: it holds two sets) and rows.
+constexpr int cfg_bn(int cfg, bool f32) { return cfg == 0 ? (f32 ? 128 : 256) : (cfg == 1 ? 128 : 64); }
 constexpr int cfg_rows(int cfg) { return cfg == 0 ? 256 : 128; }
 
-template <int MAJOR, int KIND, bool GATED, int EPI, class TO, bool PROMOTE>
+template <int MAJOR, int KIND, bool GATED, int EPI, bool F32>
 bool launch_cfg(const Product& p, cudaStream_t s) {
-  if (p.cfg == 0) return launch_tc<2, cfg_bn(0, PROMOTE), MAJOR, KIND, GATED, EPI, TO, PROMOTE>(p, s);
-  if (p.cfg == 1) return launch_tc<1, 128, MAJOR, KIND, GATED, EPI, TO, PROMOTE>(p, s);
-  if constexpr (!GATED) return launch_tc<1, 64, MAJOR, KIND, GATED, EPI, TO, PROMOTE>(p, s);
+  if (p.cfg == 0) return launch_tc<2, cfg_bn(0, F32), MAJOR, KIND, GATED, EPI, F32>(p, s);
+  if (p.cfg == 1) return launch_tc<1, 128, MAJOR, KIND, GATED, EPI, F32>(p, s);
+  if constexpr (!GATED) return launch_tc<1, 64, MAJOR, KIND, GATED, EPI, F32>(p, s);
   return false;
 }
 

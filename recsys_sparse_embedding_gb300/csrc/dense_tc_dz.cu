@@ -7,10 +7,10 @@ namespace dense {
 
 bool run_dz_product(const Product& p, cudaStream_t s) {
   if (p.f32)
-    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiDz, float, true>(p, s)
-                   : launch_cfg<kKK, kBf16, false, kEpiDz, float, true>(p, s);
-  return p.gated ? launch_cfg<kKK, kBf16, true, kEpiDz, __nv_bfloat16, false>(p, s)
-                 : launch_cfg<kKK, kBf16, false, kEpiDz, __nv_bfloat16, false>(p, s);
+    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiDz, true>(p, s)
+                   : launch_cfg<kKK, kBf16, false, kEpiDz, true>(p, s);
+  return p.gated ? launch_cfg<kKK, kBf16, true, kEpiDz, false>(p, s)
+                 : launch_cfg<kKK, kBf16, false, kEpiDz, false>(p, s);
 }
 
 }  // namespace dense

@@ -6,10 +6,10 @@ namespace dense {
 
 bool run_e4m3_product(const Product& p, cudaStream_t s) {
   if (p.epi == kEpiPart)
-    return p.gated ? launch_cfg<kKK, kE4m3, true, kEpiPart, float, false>(p, s)
-                   : launch_cfg<kKK, kE4m3, false, kEpiPart, float, false>(p, s);
-  return p.gated ? launch_cfg<kKK, kE4m3, true, kEpiFwd, __nv_bfloat16, false>(p, s)
-                 : launch_cfg<kKK, kE4m3, false, kEpiFwd, __nv_bfloat16, false>(p, s);
+    return p.gated ? launch_cfg<kKK, kE4m3, true, kEpiPart, false>(p, s)
+                   : launch_cfg<kKK, kE4m3, false, kEpiPart, false>(p, s);
+  return p.gated ? launch_cfg<kKK, kE4m3, true, kEpiFwd, false>(p, s)
+                 : launch_cfg<kKK, kE4m3, false, kEpiFwd, false>(p, s);
 }
 
 }  // namespace dense

@@ -41,19 +41,18 @@ bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int bo
 }
 
 bool run_fwd_product(const Product& p, cudaStream_t s) {
-  using T = __nv_bfloat16;
   if (p.epi == kEpiPart) {
     if (p.f32)
-      return p.gated ? launch_cfg<kKK, kBf16, true, kEpiPart, float, true>(p, s)
-                     : launch_cfg<kKK, kBf16, false, kEpiPart, float, true>(p, s);
-    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiPart, float, false>(p, s)
-                   : launch_cfg<kKK, kBf16, false, kEpiPart, float, false>(p, s);
+      return p.gated ? launch_cfg<kKK, kBf16, true, kEpiPart, true>(p, s)
+                     : launch_cfg<kKK, kBf16, false, kEpiPart, true>(p, s);
+    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiPart, false>(p, s)
+                   : launch_cfg<kKK, kBf16, false, kEpiPart, false>(p, s);
   }
   if (p.f32)
-    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiFwd, float, true>(p, s)
-                   : launch_cfg<kKK, kBf16, false, kEpiFwd, float, true>(p, s);
-  return p.gated ? launch_cfg<kKK, kBf16, true, kEpiFwd, T, false>(p, s)
-                 : launch_cfg<kKK, kBf16, false, kEpiFwd, T, false>(p, s);
+    return p.gated ? launch_cfg<kKK, kBf16, true, kEpiFwd, true>(p, s)
+                   : launch_cfg<kKK, kBf16, false, kEpiFwd, true>(p, s);
+  return p.gated ? launch_cfg<kKK, kBf16, true, kEpiFwd, false>(p, s)
+                 : launch_cfg<kKK, kBf16, false, kEpiFwd, false>(p, s);
 }
 
 }  // namespace dense

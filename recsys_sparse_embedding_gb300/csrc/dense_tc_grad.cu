@@ -7,12 +7,11 @@ namespace dense {
 
 template <int MAJOR>
 bool run(const Product& p, cudaStream_t s) {
-  using T = __nv_bfloat16;
   if (p.epi == kEpiPart)
-    return p.f32 ? launch_cfg<MAJOR, kBf16, false, kEpiPart, float, true>(p, s)
-                 : launch_cfg<MAJOR, kBf16, false, kEpiPart, float, false>(p, s);
-  return p.f32 ? launch_cfg<MAJOR, kBf16, false, kEpiOut, float, true>(p, s)
-               : launch_cfg<MAJOR, kBf16, false, kEpiOut, T, false>(p, s);
+    return p.f32 ? launch_cfg<MAJOR, kBf16, false, kEpiPart, true>(p, s)
+                 : launch_cfg<MAJOR, kBf16, false, kEpiPart, false>(p, s);
+  return p.f32 ? launch_cfg<MAJOR, kBf16, false, kEpiOut, true>(p, s)
+               : launch_cfg<MAJOR, kBf16, false, kEpiOut, false>(p, s);
 }
 
 bool run_grad_product(const Product& p, cudaStream_t s) { return p.major == kKN ? run<kKN>(p, s) : run<kNN>(p, s); }
