@@ -8,8 +8,6 @@
 //            128-byte swizzle, through a ring of stages;
 //   the MMA warp  issues the MMAs (tcgen05.mma, in the cluster's first CTA)
 //            into one of two accumulators in tensor memory;
-//   the bias warp  keeps the bias of this tile's and the next one's columns
-//            in shared memory;
 //   16 (or 8) epilogue warps  turn the other accumulator into outputs, in
 //            items of 32 rows (a warp's lane quarter, one row per lane) by 32
 //            columns. Inputs (the residual, or the upstream gradient; loaded
@@ -197,14 +195,18 @@ struct Shape {
   // have work for.
   static constexpr int kEpiWarps = GATED && ((F32 && EPI != kEpiPart) || EPI == kEpiDz) ? 8 : 16;
   static constexpr int kGroups = kEpiWarps / 4;
-  static constexpr int kLoad = kEpiWarps, kMma = kEpiWarps + 1, kBias = kEpiWarps + 2;
-  static constexpr int kThreads = 32 * (kEpiWarps + 3);
+  static constexpr int kLoad = kEpiWarps, kMma = kEpiWarps + 1;
+  static constexpr int kThreads = 32 * (kEpiWarps + 2);
   static constexpr int ITEM = 32 * 32 * int(sizeof(TO));
   static constexpr int BNC = BN / CG;  // B rows (or MN-major columns) in this CTA
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BNC * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int EBYTES = kEpiWarps * ITEM;
   static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiDz;
-  static constexpr int BIAS_BYTES = BIAS ? 2 * BN * 4 : 0, BAR_BYTES = 256;
+  // bias floats of an item that each epilogue warp keeps in shared memory (the
+  // gated forward's six stages leave room for the gate's alone; the up half's
+  // are handed round by shuffles)
+  static constexpr int BIAS_N = !BIAS ? 0 : (GATED && kEpiWarps == 8 ? 64 : 32);
+  static constexpr int BIAS_BYTES = kEpiWarps * BIAS_N * 4, BAR_BYTES = 256;
   static constexpr int kRoom = 227 * 1024 - EBYTES - BIAS_BYTES - BAR_BYTES;
   static constexpr int STAGES = kRoom / STAGE < 8 ? kRoom / STAGE : 8;
   static constexpr int SMEM = STAGES * STAGE + EBYTES + BIAS_BYTES + BAR_BYTES;
@@ -216,7 +218,7 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tfull[2], tempty[2], bfull[2], bempty[2];
+  uint64_t full[8], empty[8], tfull[2], tempty[2];
   uint32_t tmem;
   int abort_;
 };
@@ -304,8 +306,6 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
       mbar_init(&bars->tempty[i], S::kEpiWarps * CG);
-      mbar_init(&bars->bfull[i], 1);
-      mbar_init(&bars->bempty[i], S::kEpiWarps);
     }
     bars->abort_ = 0;
     fence_mbarrier_init();
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
     // ------------------------------------------------ loads (one thread)
     if (lane == 0) {
       pdl_wait();
-      uint32_t it = 0;  // stages filled so far
+      uint32_t it = 0, st = 0, lap = 0;  // stages filled so far; the next stage, and the ring's laps before it
       bool ok = true;
       const uint32_t full0 = CG == 2 ? mapa(smem_u32(&bars->full[0]), 0) : smem_u32(&bars->full[0]);
       for (int u = unit0; u < units && ok; u += units_step) {
@@ -361,9 +361,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
         for (int sg = 0; sg < a.nseg && ok; ++sg)
           for (int k = 0; k < t.kbn && ok; ++k)
 #pragma unroll 1
-            for (int term = 0; term < TERMS; ++term, ++it) {
-              const int st = int(it % STAGES);
-              if (it >= STAGES && !(ok = mbar_wait(&bars->empty[st], ((it / STAGES) - 1) & 1u))) break;
+            for (int term = 0; term < TERMS; ++term) {
+              if (lap && !(ok = mbar_wait(&bars->empty[st], (lap - 1) & 1u))) break;
               const int za = term * a.a_term + sg * a.a_seg + t.batch, zb = term * a.b_term + sg;
               const uint32_t bar = full0 + uint32_t(st) * 8u;
               if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], uint32_t(CG * S::STAGE));
@@ -389,6 +388,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
               } else {
                 tma_load_3d<CG>(sb, &mapB, kx, t.n0 + int(rank) * S::BNC, zb, bar);
               }
+              ++it;
+              if (++st == uint32_t(STAGES)) st = 0, ++lap;
             }
       }
       // the last loads have landed before the CTA may end (bounded)
@@ -402,19 +403,23 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
     if (lane == 0 && rank == 0) {
       constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (AMN ? 1u << 15 : 0u) |
                               (BMN ? 1u << 16 : 0u) | (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
-      uint32_t it = 0, run = 0;
+      uint32_t run = 0, st = 0, phase = 0;  // the next stage, and its barrier's phase
       bool ok = true;
-      // a K-block of A in stage sa times one of B in stage sb
-      auto block = [&](uint32_t d, uint32_t sta, uint32_t stb, bool accumulate) {
-        const uint32_t sa = smem_u32(sm + sta * S::STAGE), sb = smem_u32(sm + stb * S::STAGE) + S::A_BYTES;
+      const uint32_t s0 = smem_u32(sm);
+      const uint64_t da0 = AMN ? mn_desc(s0) : sw128_kmajor_desc(s0),
+                     db0 = BMN ? mn_desc(s0 + S::A_BYTES) : sw128_kmajor_desc(s0 + S::A_BYTES);
+      // a K-block of A in stage sa times one of B in stage sb (addresses in the
+      // descriptors count 16 bytes)
+      auto block = [&](uint32_t d, uint32_t sa, uint32_t sb, bool accumulate) {
+        const uint64_t da = da0 + sa * uint32_t(S::STAGE >> 4), db = db0 + sb * uint32_t(S::STAGE >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma<CG, KIND>(d, AMN ? mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
-                        BMN ? mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32), ID,
-                        (accumulate || kk > 0) ? 1u : 0u);
+          mma<CG, KIND>(d, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2), ID, (accumulate || kk > 0) ? 1u : 0u);
       };
-      auto wait_full = [&](uint32_t i) {
-        if (ok) ok = mbar_wait(&bars->full[i % STAGES], (i / STAGES) & 1u);
+      auto take = [&](uint32_t& stage) {  // the next stage, once it is filled
+        stage = st;
+        ok = mbar_wait(&bars->full[st], phase);
+        if (++st == uint32_t(STAGES)) st = 0, phase ^= 1u;
         tc_fence_after();
         return ok;
       };
@@ -426,26 +431,22 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
           if (run >= 2 && !(ok = mbar_wait(&bars->tempty[acc], ((run >> 1) - 1) & 1u))) break;
           tc_fence_after();
           for (int k = 0; k < len; ++k) {
-            if (!F32) {
-              if (!wait_full(it)) break;
-              block(d, it % STAGES, it % STAGES, k > 0);
-              mma_commit<CG>(&bars->empty[it % STAGES]);
-              ++it;
-            } else {
-              const uint32_t s0 = it % STAGES, s1 = (it + 1) % STAGES, s2 = (it + 2) % STAGES;
-              if (!wait_full(it)) break;
-              block(d, s0, s0, k > 0);
-              if (!wait_full(it + 1)) break;
-              block(d + BN, s0, s1, k > 0);
-              block(d + BN, s1, s0, true);
-              block(d + BN, s1, s1, true);
-              if (!wait_full(it + 2)) break;
-              block(d + BN, s0, s2, true);
-              block(d + BN, s2, s0, true);
-              mma_commit<CG>(&bars->empty[s0]);
-              mma_commit<CG>(&bars->empty[s1]);
-              mma_commit<CG>(&bars->empty[s2]);
-              it += 3;
+            uint32_t x, y, z;
+            if (!take(x)) break;
+            block(d, x, x, k > 0);
+            if (F32) {
+              if (!take(y)) break;
+              block(d + BN, x, y, k > 0);
+              block(d + BN, y, x, true);
+              block(d + BN, y, y, true);
+              if (!take(z)) break;
+              block(d + BN, x, z, true);
+              block(d + BN, z, x, true);
+            }
+            mma_commit<CG>(&bars->empty[x]);
+            if (F32) {
+              mma_commit<CG>(&bars->empty[y]);
+              mma_commit<CG>(&bars->empty[z]);
             }
           }
           if (ok) mma_commit<CG>(&bars->tfull[acc]);
@@ -455,36 +456,12 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       if (!ok) atomicExch(&bars->abort_, 1);
     }
     __syncwarp();
-  } else if (warp == S::kBias) {
-    // ------------------------------------------------ bias of the tiles' columns
-    if (S::BIAS && a.bias) {
-      pdl_wait();
-      uint32_t tile = 0;
-      for (int u = unit0; u < units; u += units_step, ++tile) {
-        const Unit t = unit_of(u);
-        const uint32_t p = tile & 1u;
-        bool ok = !*aborted;
-        if (ok && lane == 0 && tile >= 2) ok = mbar_wait(&bars->bempty[p], ((tile >> 1) - 1) & 1u);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) atomicExch(&bars->abort_, 1);
-          break;
-        }
-#pragma unroll
-        for (int i = lane; i < BN; i += 32) {  // (gated: the gate's columns, then the up half's)
-          const int n = t.n0 + i % ON;
-          sBias[p * BN + i] = n < a.N ? __ldg(a.bias + (i / ON) * a.N + n) : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->bfull[p]);
-      }
-    }
-    __syncwarp();
   } else {
     // ------------------------------------------------ epilogue
     pdl_wait();
     const int q = warp & 3, grp = warp >> 2;
     uint8_t* buf = sE + warp * S::ITEM;
+    float* wbias = sBias + warp * S::BIAS_N;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
     constexpr bool IN = (EPI == kEpiFwd && !GATED) || EPI == kEpiDz;
     constexpr bool SCALED = KIND == kE4m3 && EPI == kEpiFwd;
@@ -582,35 +559,38 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       }
       __syncwarp();
     };
-    // The input of the warp's next item ((unit, item) pairs in order), where it
-    // can be loaded in pieces: bf16 into registers; fp32, whose sums take the
-    // registers, as far as L2.
+    // What the warp's next item ((unit, item) pairs in order) takes from memory:
+    // its columns' bias, one column per lane; its input, where it can be loaded
+    // in pieces: bf16 into registers; fp32, whose sums take the registers, as
+    // far as L2.
     constexpr bool PRE = IN && sizeof(TO) == 2;
     uint4 pin[PRE ? NV : 1];
+    float bias_g = 0.f, bias_u = 0.f;
     auto prefetch = [&](int u, int c) {
-      if (!IN) return;
+      if (!IN && !S::BIAS) return;
       if (c >= NCH) c = grp, u += units_step;
-      const bool any = has_in && a.in_vec && u < units && c < NCH;
+      const bool any = u < units && c < NCH, load = any && has_in && a.in_vec;
       const Unit t = unit_of(any ? u : unit0);
+      const int r = any ? t.m0 + 32 * q : a.M, cc = t.n0 + c * CW;
       if (PRE) {
-        load_item(pin, any ? t.m0 + 32 * q : a.M, t.n0 + c * CW);
-      } else if (any) {
-        const int r = t.m0 + 32 * q + lane, cc = t.n0 + c * CW;
-        if (r < a.M && cc < a.N) prefetch_l2(in + (long long)r * a.ldi + cc);
+        load_item(pin, load ? r : a.M, cc);
+      } else if (IN && load) {
+        if (r + lane < a.M && cc < a.N) prefetch_l2(in + (long long)(r + lane) * a.ldi + cc);
+      }
+      if (S::BIAS) {
+        const bool there = any && has_bias && cc + lane < a.N;
+        bias_g = there ? __ldg(a.bias + cc + lane) : 0.f;
+        if (GATED) bias_u = there ? __ldg(a.bias + a.N + cc + lane) : 0.f;
       }
     };
     prefetch(unit0, grp);
 
-    uint32_t run = 0, tile = 0;
+    uint32_t run = 0;
     bool ok = true;
-    auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-      if (*aborted) ok = false;
-      if (ok && lane == 0) ok = mbar_wait(bar, parity);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      return ok;
-    };
     auto wait_run = [&]() {  // the run's accumulator is complete
-      wait_for(&bars->tfull[run & 1u], (run >> 1) & 1u);
+      if (*aborted) ok = false;
+      if (ok && lane == 0) ok = mbar_wait(&bars->tfull[run & 1u], (run >> 1) & 1u);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
       tc_fence_after();
       return ok;
     };
@@ -620,16 +600,20 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       if (lane == 0) mbar_arrive_relaxed(tempty0 + (run & 1u) * 8u);
       ++run;
     };
-    for (int u = unit0; u < units && ok; u += units_step, ++tile) {
+    for (int u = unit0; u < units && ok; u += units_step) {
       const Unit t = unit_of(u);
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
-      const float* bias_g = sBias + (tile & 1u) * BN;
       // one item: 32 rows by CW columns. F32: pg, pu hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
         if (row0 >= a.M || col0 >= a.N) {
           prefetch(u, c + GR);
           return;
+        }
+        if (S::BIAS) {
+          wbias[lane] = bias_g;
+          if (S::BIAS_N == 64) wbias[32 + lane] = bias_u;
+          if (!has_in) __syncwarp();
         }
         if (has_in) {
           if (a.in_vec) {
@@ -661,6 +645,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
           }
           __syncwarp();
         }
+        const float bu = bias_u;
+        prefetch(u, c + GR);  // (a whole item's time ahead)
         // e4m3: the row's scale, and the columns' (one per lane, handed round by shuffles)
         float xs = 0.f, ws = 0.f, wsu = 0.f;
         if (SCALED) {
@@ -696,15 +682,19 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
                 if (PAIR) w[PAIR ? k : 0] *= xs * __shfl_sync(0xffffffffu, wsu, j + k);
               }
             }
-            if (has_bias) {
+            if (S::BIAS) {
 #pragma unroll
               for (int k = 0; k < 8; k += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(bias_g + cc + j + k);
+                const float4 b = *reinterpret_cast<const float4*>(wbias + j + k);
                 v[k] += b.x, v[k + 1] += b.y, v[k + 2] += b.z, v[k + 3] += b.w;
-                if (PAIR) {
-                  const float4 d = *reinterpret_cast<const float4*>(bias_g + ON + cc + j + k);
+                if (PAIR && S::BIAS_N == 64) {
+                  const float4 d = *reinterpret_cast<const float4*>(wbias + 32 + j + k);
                   w[PAIR ? k : 0] += d.x, w[PAIR ? k + 1 : 0] += d.y, w[PAIR ? k + 2 : 0] += d.z, w[PAIR ? k + 3 : 0] += d.w;
                 }
+              }
+              if (PAIR && S::BIAS_N == 32) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[PAIR ? k : 0] += __shfl_sync(0xffffffffu, bu, j + k);
               }
             }
             float x[8];
@@ -784,7 +774,6 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
             if (PAIR) sums(up, 1);
           }
         }
-        prefetch(u, c + GR);
       };
       if (F32) {
         float sum[NI][PAIR ? 2 : 1][32];
@@ -810,22 +799,16 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
             }
           done_run();
         }
-        if (ok && has_bias) wait_for(&bars->bfull[tile & 1u], (tile >> 1) & 1u);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
           if (grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
       } else {
         if (!wait_run()) break;
-        if (has_bias && !wait_for(&bars->bfull[tile & 1u], (tile >> 1) & 1u)) break;
         const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
 #pragma unroll 1
         for (int c = grp; c < NCH; c += GR) do_item(c, tacc, nullptr, nullptr);
         done_run();
-      }
-      if (has_bias) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed(smem_u32(&bars->bempty[tile & 1u]));
       }
     }
     if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
