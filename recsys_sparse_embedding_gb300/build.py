@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdinsparse.so")
 
 UNITS = ["abi.cu", "bag.cu", "fwd_attn_tc.cu", "fwd_attn_f32.cu", "towers.cu", "hash.cu", "bwd.cu", "gemm.cu", "dense.cu", "dense_tc_fwd.cu",
-         "dense_tc_dz.cu", "dense_tc_grad.cu", "dense_tc_e4m3.cu", "norm.cu"]
+         "dense_tc_dz.cu", "dense_tc_grad.cu", "dense_tc_dual.cu", "dense_tc_e4m3.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

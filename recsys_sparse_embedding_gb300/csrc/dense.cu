@@ -48,38 +48,88 @@ constexpr int kMaxSplits = 32;
 // unit holds at most 256 x 256 fp32 per pair of SMs
 constexpr size_t kPartBytes = size_t(kSms / 2) * 256 * 256 * 4;
 
-struct Plan {
-  int cfg, mt, nt, kbps, splits;
+// Estimates in SM cycles, per tile configuration: a K-block of a 256 x 256
+// tile (on two SMs; fp32: 256 x 128, six products), 128 x 128 or 128 x 64
+// tile takes kStep cycles; a launch has its start and its last tile's
+// epilogue (kUnit); the chip takes its units in whole waves; a split product
+// pays for a second launch and its partial sums' way to L2 and back.
+struct Cost {
+  bool f32;
+  double step(int cfg) const {
+    constexpr double kStep[2][3] = {{560, 560, 400}, {1700, 1800, 1300}};
+    return kStep[f32][cfg];
+  }
+  static constexpr double kUnit = 1500, kTile = 300, kSecond = 5000, kBytesPerCycle = 2000;
+  static double parts(long long splits, double outputs) {
+    return splits > 1 ? kSecond + double(splits) * outputs * 8 / kBytesPerCycle : 0;
+  }
 };
 
-// Tile configuration and K-splits by an estimate in SM cycles: a K-block of
-// a 256 x 256 tile (on two SMs; fp32: 256 x 128, six products), 128 x 128 or 128 x 64 tile takes kStep
-// cycles, the chip takes its units in whole waves, and a split product pays
-// for a second launch and its partial sums' way to L2 and back.
-Plan plan(long long M, long long N, int nb, bool gated, bool f32, long long nkb, int nseg, bool may_split) {
-  const double kStep[3] = {f32 ? 1700. : 560., f32 ? 1800. : 560., f32 ? 1300. : 400.};
-  constexpr double kUnit = 1500, kSecond = 5000, kBytesPerCycle = 2000;
-  Plan best{};
-  double cost = 1e300;
+// The tiles of a product [nb][M][N] over segments of nkb K-blocks.
+void set_tiles(Job& o, int cfg, long long M, long long N, int nb, bool gated, bool f32, long long nkb, int nseg,
+               long long want) {
+  const long long on = cfg_bn(cfg, f32) / (gated ? 2 : 1), rows = cfg_rows(cfg);
+  o.M = int(M);
+  o.N = int(N);
+  o.mt = int((M + rows - 1) / rows);
+  o.nt = int((N + on - 1) / on);
+  o.nb = nb;
+  o.nkb = int(nkb);
+  o.kbps = int((nkb + want - 1) / want);
+  o.splits = int((nkb + o.kbps - 1) / o.kbps);
+  o.nseg = nseg;
+}
+long long tiles_of(const Job& o) { return (long long)o.mt * o.nt * o.nb; }
+long long slots_of(int cfg) { return cfg == 0 ? kSms / 2 : kSms; }
+
+// Picks the configuration and the K-splits of one product.
+void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg, bool may_split) {
+  const Cost cost{p.f32};
+  double best = 1e300;
+  Job o = p.a.job[0];
   for (int cfg = 0; cfg < 3; ++cfg) {
-    if (cfg == 2 && gated) continue;
-    const long long on = cfg_bn(cfg, f32) / (gated ? 2 : 1), mt = (M + cfg_rows(cfg) - 1) / cfg_rows(cfg),
-                    nt = (N + on - 1) / on, tiles = mt * nt * nb, slots = cfg == 0 ? kSms / 2 : kSms;
-    if (tiles > INT32_MAX / 64) continue;
+    if (cfg == 2 && p.gated) continue;
     for (int want = 1; want <= kMaxSplits && want <= nkb; ++want) {
-      if (want > 1 && (!may_split || tiles * want > slots)) break;
-      const long long kbps = (nkb + want - 1) / want, splits = (nkb + kbps - 1) / kbps;
-      if (splits != want) continue;
-      const long long waves = (tiles * splits + slots - 1) / slots;
-      double c = kUnit + double(waves) * (kStep[cfg] * double(kbps) * nseg + 300);
-      if (splits > 1) c += kSecond + double(splits) * double(M) * double(N) * nb * (gated ? 2 : 1) * 8 / kBytesPerCycle;
-      if (c < cost) {
-        cost = c;
-        best = Plan{cfg, int(mt), int(nt), int(kbps), int(splits)};
+      set_tiles(o, cfg, M, N, nb, p.gated, p.f32, nkb, nseg, want);
+      if (tiles_of(o) > INT32_MAX / 64) break;
+      if (want > 1 && (!may_split || tiles_of(o) * want > slots_of(cfg))) break;
+      if (o.splits != want) continue;
+      const long long waves = (tiles_of(o) * o.splits + slots_of(cfg) - 1) / slots_of(cfg);
+      const double c = Cost::kUnit + double(waves) * (cost.step(cfg) * double(o.kbps) * nseg + Cost::kTile) +
+                       Cost::parts(o.splits, double(M) * N * nb * (p.gated ? 2 : 1));
+      if (c < best) {
+        best = c;
+        p.cfg = cfg;
+        p.a.job[0] = o;
       }
     }
   }
-  return best;
+}
+
+// dW (job 0, which may be split) and dx (job 1) in one launch.
+void plan_dual(Product& p, long long M, long long N, long long K, int halves) {
+  const Cost cost{p.f32};
+  const long long kw = (M + 63) / 64, kx = (N + 63) / 64;
+  double best = 1e300;
+  TcArgs a = p.a;
+  for (int cfg = 0; cfg < 3; ++cfg)
+    for (int want = 1; want <= kMaxSplits && want <= kw; ++want) {
+      set_tiles(a.job[0], cfg, N, K, halves, false, p.f32, kw, 1, want);
+      set_tiles(a.job[1], cfg, M, K, 1, false, p.f32, kx, halves, 1);
+      const Job& w = a.job[0];
+      if (tiles_of(w) > INT32_MAX / 64 || tiles_of(a.job[1]) > INT32_MAX / 64) break;
+      if (want > 1 && tiles_of(w) * want > slots_of(cfg)) break;
+      if (w.splits != want) continue;
+      const Deal d = deal(a, slots_of(cfg));
+      const double c = Cost::kUnit + cost.step(cfg) * double(d.load) +
+                       Cost::parts(w.splits, double(N) * K * halves);
+      if (c < best) {
+        best = c;
+        p.cfg = cfg;
+        p.a.job[0] = a.job[0];
+        p.a.job[1] = a.job[1];
+      }
+    }
 }
 
 long long up(long long v, long long to) { return (v + to - 1) / to * to; }
@@ -339,34 +389,30 @@ bool lay_operands(const Ctx& c, const void* x, long long ldx, const void* dy, lo
   return lay(c.l->dtype, jobs, n, c.s);
 }
 
-void set_plan(Product& p, const Plan& q, long long M, long long N, int nb, long long nkb) {
-  p.cfg = q.cfg;
-  p.a.M = int(M);
-  p.a.N = int(N);
-  p.a.mt = q.mt;
-  p.a.nt = q.nt;
-  p.a.nb = nb;
-  p.a.nkb = int(nkb);
-  p.a.kbps = q.kbps;
-  p.a.splits = q.splits;
+// Job 0's partial sums.
+void set_part(Product& p, const Ctx& c) {
+  Job& o = p.a.job[0];
+  p.epi = kEpiPart;
+  o.out = c.ws + c.w.part;
+  o.ldo = up(o.N, 4);
+  o.out_plane = o.M * o.ldo;
+  o.out_vec = 1;
 }
 
-void set_part(Product& p, const Ctx& c) {
-  const long long ldp = up(p.a.N, 4);
-  p.epi = kEpiPart;
-  p.a.in = nullptr;
-  p.a.out = c.ws + c.w.part;
-  p.a.ldo = ldp;
-  p.a.out_plane = p.a.M * ldp;
-  p.a.out_vec = 1;
+void set_out(Job& o, void* out, long long ldo, int es) {
+  o.out = out;
+  o.ldo = ldo;
+  o.out_plane = o.M * ldo;
+  o.out_vec = vec_rows(out, ldo, es) && (o.nb == 1 || (o.out_plane * es) % 16 == 0);
 }
 
 bool finish(const Ctx& c, const Product& p, FinishArgs f, bool f32) {
   f.part = reinterpret_cast<const float*>(c.ws + c.w.part);
-  f.M = p.a.M;
-  f.N = p.a.N;
-  f.ldp = up(p.a.N, 4);
-  f.splits = p.a.splits;
+  const Job& o = p.a.job[0];
+  f.M = o.M;
+  f.N = o.N;
+  f.ldp = o.ldo;
+  f.splits = o.splits;
   const long long total = f.M * (f.ldp / 4) * (f.gated ? 1 : f.planes), blocks = (total + 255) / 256;
   const unsigned grid = unsigned(blocks < kSms * 16 ? blocks : kSms * 16);
   return pdl_launch(f32 ? finish_kernel<float> : finish_kernel<__nv_bfloat16>, dim3(grid), 256, c.s, f);
@@ -385,29 +431,26 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.f32 = f32;
   p.epi = dz ? kEpiDz : kEpiFwd;
   const long long nkb = (l->K + c.kbe - 1) / c.kbe;
-  p.a.nseg = 1;
-  p.a.a_term = 1;
-  p.a.b_term = 1;
-  set_plan(p, plan(c.M, c.N, 1, c.gated, f32, nkb, p.a.nseg, !dz), c.M, c.N, 1, nkb);
+  plan(p, c.M, c.N, 1, nkb, 1, !dz);
+  Job& o = p.a.job[0];
+  o.a_term = 1;
+  o.b_term = 1;
   p.a.act = l->act;
   p.a.bias = l->bias;
   p.a.xs = xs;
   p.a.ws = l->scale;
   p.a.status = c.status;
   p.a.part = sums;
-  if (p.a.splits > 1) {
+  if (o.splits > 1) {
     set_part(p, c);
   } else {
     p.a.in = in;
     p.a.ldi = ldi;
     p.a.in_vec = in && vec_rows(in, ldi, c.eo);
-    p.a.out = y;
-    p.a.ldo = ldy;
-    p.a.out_plane = c.M * ldy;
-    p.a.out_vec = vec_rows(y, ldy, dz ? 2 : c.eo);
+    set_out(o, y, ldy, dz ? 2 : c.eo);
   }
   const bool ok = dz ? run_dz_product(p, c.s) : (l->dtype == DSF_E4M3 ? run_e4m3_product(p, c.s) : run_fwd_product(p, c.s));
-  if (!ok || p.a.splits == 1) return ok;
+  if (!ok || o.splits == 1) return ok;
   FinishArgs f{};
   f.fwd = true;
   f.gated = c.gated;
@@ -423,40 +466,50 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   return finish(c, p, f, f32);
 }
 
-// A gradient product: dx (dz [.][M][N] times W) or dW
-// (dz^T times x, one batch per half).
-bool grad_product(const Ctx& c, const Mat& dz, bool dW, void* out, long long ldo) {
+// The gradient products: dx (dz [.][M][N] times W) and dW (dz^T times x, one
+// batch per half), each where asked for.
+bool grad_products(const Ctx& c, const Mat& dz, void* dx, long long lddx, void* dW) {
+  const int K = c.l->K;
   const bool f32 = c.l->dtype == DSF_F32;
+  if (!dx && !dW) return true;
   Product p{};
-  p.A = dz;
-  p.B = dW ? c.X : c.W;
-  p.major = dW ? kNN : kKN;
   p.gated = false;
   p.f32 = f32;
   p.epi = kEpiOut;
-  const int nb = dW ? c.halves : 1;
-  p.a.nseg = dW ? 1 : c.halves;
-  p.a.a_term = c.halves;
-  p.a.a_seg = dW ? 0 : 1;
-  p.a.b_term = dW ? 1 : c.halves;
-  const long long rows = dW ? c.N : c.M, depth = dW ? c.M : c.N, nkb = (depth + 63) / 64;
-  set_plan(p, plan(rows, c.l->K, nb, false, f32, nkb, p.a.nseg, true), rows, c.l->K, nb, nkb);
   p.a.status = c.status;
-  if (p.a.splits > 1) {
-    set_part(p, c);
+  if (dx && dW) {
+    p.major = kDual;
+    plan_dual(p, c.M, c.N, K, c.halves);
   } else {
-    p.a.out = out;
-    p.a.ldo = ldo;
-    p.a.out_plane = rows * ldo;
-    p.a.out_vec = vec_rows(out, ldo, c.es) && (nb == 1 || (rows * ldo * c.es) % 16 == 0);
+    p.major = dW ? kNN : kKN;
+    plan(p, dW ? c.N : c.M, K, dW ? c.halves : 1, ((dW ? c.M : c.N) + 63) / 64, dW ? 1 : c.halves, true);
   }
-  if (!run_grad_product(p, c.s)) return false;
-  if (p.a.splits == 1) return true;
+  Job &w = p.a.job[0], &x = p.a.job[dW ? 1 : 0];
+  if (dW) {
+    p.A = dz;
+    p.B = c.X;
+    w.a_term = c.halves;
+    w.a_seg = 0;
+    w.b_term = 1;
+    set_out(w, dW, K, c.es);
+  }
+  if (dx) {
+    (dW ? p.A1 : p.A) = dz;
+    (dW ? p.B1 : p.B) = c.W;
+    x.a_term = c.halves;
+    x.a_seg = 1;
+    x.b_term = c.halves;
+    set_out(x, dx, lddx, c.es);
+  }
+  const Job out = p.a.job[0];
+  if (out.splits > 1) set_part(p, c);
+  if (!(dx && dW ? run_dual_product(p, c.s) : run_grad_product(p, c.s))) return false;
+  if (out.splits == 1) return true;
   FinishArgs f{};
-  f.planes = nb;
-  f.out = out;
-  f.ldo = ldo;
-  f.out_plane = rows * ldo;
+  f.planes = out.nb;
+  f.out = out.out;
+  f.ldo = out.ldo;
+  f.out_plane = out.out_plane;
   return finish(c, p, f, f32);
 }
 
@@ -502,9 +555,7 @@ int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void
     }
     dz = laid_out(l->dtype, c.N) ? Mat{c.ws + c.w.gp, M, c.N, c.w.np, c.terms, M * c.w.np} : Mat{dy, M, c.N, lddy, 1, 0};
   }
-  if (dx && !grad_product(c, dz, false, dx, lddx)) return DSF_ECUDA;
-  if (dW && !grad_product(c, dz, true, dW, l->K)) return DSF_ECUDA;
-  return DSF_OK;
+  return grad_products(c, dz, dx, lddx, dW) ? DSF_OK : DSF_ECUDA;
 }
 
 int run_fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const float* xs, const void* res,

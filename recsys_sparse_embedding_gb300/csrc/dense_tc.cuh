@@ -55,10 +55,12 @@ enum Epi {
   kEpiDz = 1,    // out = dz (planes dg, du for a gated layer; fp32: its three
                  // terms) from in = dy; column sums
   kEpiOut = 2,   // out = the accumulator
-  kEpiPart = 3,  // fp32 partial sums of a K-split: plane split * planes + (half or batch)
+  kEpiPart = 3,  // fp32 partial sums of a K-split: plane split * planes + (half or batch); kDual: job 0 only
 };
 enum Kind { kBf16 = 0, kE4m3 = 1 };
-enum Major { kKK = 0, kKN = 1, kNN = 2 };  // A and B K-major; B MN-major; both
+// A and B K-major; B MN-major; both; two products in one launch, job 0 with
+// both MN-major (dW), job 1 with B (dx)
+enum Major { kKK = 0, kKN = 1, kNN = 2, kDual = 3 };
 
 // Division of unsigned 32-bit numbers by a fixed divisor: q = (mulhi(n, m) + n) >> l
 // with l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, exact for every n below 2^31.
@@ -72,7 +74,8 @@ inline Div make_div(uint32_t d) {
 }
 __device__ __forceinline__ uint32_t div_by(uint32_t n, const Div& v) { return (__umulhi(n, v.m) + n) >> v.l; }
 
-struct TcArgs {
+// One product: its tiles, its operands' planes, its output.
+struct Job {
   int M, N;          // rows; output columns (a gated layer's: F)
   int mt, nt, nb;    // tiles along M and N, batches (halves of dW)
   Div by_splits, by_batch, by_group, by_last;  // splits; mt nt; 8 nt; M tiles of the last group of 8
@@ -81,13 +84,22 @@ struct TcArgs {
   // planes: A: term * a_term + segment * a_seg + batch; B: term * b_term +
   // segment (a gated layer's: twice that, + half)
   int a_term, a_seg, b_term;
-  int act;
-  const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
-  const void* in;            // nullable unless kEpiDz
-  long long ldi;
   void* out;
   long long ldo, out_plane;  // strides in elements
-  int in_vec, out_vec;       // rows at 16-byte boundaries
+  int out_vec;               // rows at 16-byte boundaries
+};
+
+struct TcArgs {
+  Job job[2];
+  // kDual: the job with the longer units goes first, dealt round; `rest` of the
+  // clusters have one unit of it more than the others (h0 and h0 - 1), and the
+  // other job's units are dealt (l0 and l1 to each) so that the sums agree
+  int first, rest, h0, l0, l1;
+  int act;
+  const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
+  const void* in;               // nullable unless kEpiDz
+  long long ldi;
+  int in_vec;   // rows at 16-byte boundaries
   float* part;  // kEpiDz: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
   int* status;
 };
@@ -185,7 +197,7 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- shapes
-template <int CG, int BN, bool GATED, int EPI, bool F32>
+template <int CG, int BN, int MAJOR, bool GATED, int EPI, bool F32>
 struct Shape {
   using TO = typename std::conditional<F32 || EPI == kEpiPart, float, __nv_bfloat16>::type;  // input and output
   static constexpr int ON = GATED ? BN / 2 : BN;  // output columns per tile
@@ -272,12 +284,13 @@ constexpr int kRun = 4;  // F32: K-blocks per accumulator run
 
 // ---------------------------------------------------------------- the kernel
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
-__global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThreads, 1)
     tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mapA,
-              const __grid_constant__ CUtensorMap mapB) {
-  using S = Shape<CG, BN, GATED, EPI, F32>;
+              const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapA1,
+              const __grid_constant__ CUtensorMap mapB1) {
+  using S = Shape<CG, BN, MAJOR, GATED, EPI, F32>;
   using TO = typename S::TO;
-  constexpr bool AMN = MAJOR == kNN, BMN = MAJOR != kKK;
+  constexpr bool DUAL = MAJOR == kDual, BMN = MAJOR != kKK;
   constexpr int kBK = KIND == kBf16 ? 64 : 128;  // K elements per block (128 bytes)
   constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : 1;
   static_assert(!(GATED && BMN), "a gated layer's product is K-major");
@@ -292,11 +305,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int unit0 = blockIdx.x / CG, units_step = gridDim.x / CG;
-  const int tiles = a.mt * a.nt * a.nb, units = tiles * a.splits;
 
   if (warp == S::kLoad && lane == 0) {
     prefetch_map(&mapA);
     prefetch_map(&mapB);
+    if (DUAL) {
+      prefetch_map(&mapA1);
+      prefetch_map(&mapB1);
+    }
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -327,26 +343,44 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
   }
   volatile int* aborted = &bars->abort_;
 
-  // a unit: split-minor, then N tiles within groups of M tiles, so that the
-  // units in flight share rows of A and of B in L2
+  // The cluster's i-th unit; false after the last. In a product: split-minor,
+  // then N tiles within groups of M tiles, so that the units in flight share
+  // rows of A and of B in L2.
   struct Unit {
-    int m0, n0, batch, split, kb0, kbn;
+    int job, m0, n0, batch, split, kb0, kbn;
   };
-  auto unit_of = [&](int u) {
-    Unit t;
-    uint32_t r = div_by(u, a.by_splits);
-    t.split = u - int(r) * a.splits;
-    t.batch = int(div_by(r, a.by_batch));
-    r -= uint32_t(t.batch) * a.by_batch.d;
-    const uint32_t grp = div_by(r, a.by_group);
-    r -= grp * a.by_group.d;
-    const bool whole = int(grp * 8 + 8) <= a.mt;
-    const uint32_t n = whole ? r >> 3 : div_by(r, a.by_last), gm = whole ? 8 : a.by_last.d;
+  const auto& job0 = a.job[0];
+  const int units = job0.mt * job0.nt * job0.nb * job0.splits;
+  auto unit_at = [&](int i, Unit& t) {
+    int u = unit0 + i * units_step;
+    t.job = 0;
+    if (DUAL) {
+      const bool more = unit0 < a.rest;
+      const int h = a.h0 - (more ? 0 : 1), j = i - h;
+      t.job = j < 0 ? a.first : 1 - a.first;
+      if (j >= 0) {
+        if (j >= (more ? a.l0 : a.l1)) return false;
+        u = more ? j * a.rest + unit0 : a.rest * a.l0 + j * (units_step - a.rest) + unit0 - a.rest;
+        const Job& o = a.job[t.job];
+        if (u >= o.mt * o.nt * o.nb * o.splits) return false;
+      }
+    } else if (u >= units) {
+      return false;
+    }
+    const Job& o = a.job[DUAL ? t.job : 0];
+    uint32_t r = div_by(u, o.by_splits);
+    t.split = u - int(r) * o.splits;
+    t.batch = int(div_by(r, o.by_batch));
+    r -= uint32_t(t.batch) * o.by_batch.d;
+    const uint32_t grp = div_by(r, o.by_group);
+    r -= grp * o.by_group.d;
+    const bool whole = int(grp * 8 + 8) <= o.mt;
+    const uint32_t n = whole ? r >> 3 : div_by(r, o.by_last), gm = whole ? 8 : o.by_last.d;
     t.m0 = int(grp * 8 + r - n * gm) * 128 * CG + int(rank) * 128;
     t.n0 = int(n) * ON;
-    t.kb0 = t.split * a.kbps;
-    t.kbn = min(a.kbps, a.nkb - t.kb0);
-    return t;
+    t.kb0 = t.split * o.kbps;
+    t.kbn = min(o.kbps, o.nkb - t.kb0);
+    return true;
   };
 
   if (warp == S::kLoad) {
@@ -356,37 +390,41 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       uint32_t it = 0, st = 0, lap = 0;  // stages filled so far; the next stage, and the ring's laps before it
       bool ok = true;
       const uint32_t full0 = CG == 2 ? mapa(smem_u32(&bars->full[0]), 0) : smem_u32(&bars->full[0]);
-      for (int u = unit0; u < units && ok; u += units_step) {
-        const Unit t = unit_of(u);
-        for (int sg = 0; sg < a.nseg && ok; ++sg)
+      Unit t;
+      for (int i = 0; ok && unit_at(i, t); ++i) {
+        const Job& o = a.job[DUAL ? t.job : 0];
+        const bool amn = MAJOR == kNN || (DUAL && t.job == 0);
+        const void* ma = DUAL && t.job ? &mapA1 : &mapA;
+        const void* mb = DUAL && t.job ? &mapB1 : &mapB;
+        for (int sg = 0; sg < o.nseg && ok; ++sg)
           for (int k = 0; k < t.kbn && ok; ++k)
 #pragma unroll 1
             for (int term = 0; term < TERMS; ++term) {
               if (lap && !(ok = mbar_wait(&bars->empty[st], (lap - 1) & 1u))) break;
-              const int za = term * a.a_term + sg * a.a_seg + t.batch, zb = term * a.b_term + sg;
+              const int za = term * o.a_term + sg * o.a_seg + t.batch, zb = term * o.b_term + sg;
               const uint32_t bar = full0 + uint32_t(st) * 8u;
               if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], uint32_t(CG * S::STAGE));
               const uint32_t sa = smem_u32(sm + st * S::STAGE), sb = sa + S::A_BYTES;
               const int kx = (t.kb0 + k) * kBK;
-              if (AMN) {
-                tma_load_3d<CG>(sa, &mapA, t.m0, kx, za, bar);
-                tma_load_3d<CG>(sa + 8192, &mapA, t.m0 + 64, kx, za, bar);
+              if (amn) {
+                tma_load_3d<CG>(sa, ma, t.m0, kx, za, bar);
+                tma_load_3d<CG>(sa + 8192, ma, t.m0 + 64, kx, za, bar);
               } else {
-                tma_load_3d<CG>(sa, &mapA, kx, t.m0, za, bar);
+                tma_load_3d<CG>(sa, ma, kx, t.m0, za, bar);
               }
               if (GATED) {
                 if (CG == 2) {  // the gate half in one CTA, the up half in the other
-                  tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb + int(rank), bar);
+                  tma_load_3d<CG>(sb, mb, kx, t.n0, 2 * zb + int(rank), bar);
                 } else {
-                  tma_load_3d<CG>(sb, &mapB, kx, t.n0, 2 * zb, bar);
-                  tma_load_3d<CG>(sb + S::B_BYTES / 2, &mapB, kx, t.n0, 2 * zb + 1, bar);
+                  tma_load_3d<CG>(sb, mb, kx, t.n0, 2 * zb, bar);
+                  tma_load_3d<CG>(sb + S::B_BYTES / 2, mb, kx, t.n0, 2 * zb + 1, bar);
                 }
               } else if (BMN) {
 #pragma unroll
                 for (int j = 0; j < S::BNC / 64; ++j)
-                  tma_load_3d<CG>(sb + j * 8192, &mapB, t.n0 + int(rank) * S::BNC + 64 * j, kx, zb, bar);
+                  tma_load_3d<CG>(sb + j * 8192, mb, t.n0 + int(rank) * S::BNC + 64 * j, kx, zb, bar);
               } else {
-                tma_load_3d<CG>(sb, &mapB, kx, t.n0 + int(rank) * S::BNC, zb, bar);
+                tma_load_3d<CG>(sb, mb, kx, t.n0 + int(rank) * S::BNC, zb, bar);
               }
               ++it;
               if (++st == uint32_t(STAGES)) st = 0, ++lap;
@@ -401,20 +439,22 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
   } else if (warp == S::kMma) {
     // ------------------------------------------------ MMAs (one thread of the cluster)
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (AMN ? 1u << 15 : 0u) |
-                              (BMN ? 1u << 16 : 0u) | (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
+      constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (BMN ? 1u << 16 : 0u) |
+                              (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
       uint32_t run = 0, st = 0, phase = 0;  // the next stage, and its barrier's phase
       bool ok = true;
       const uint32_t s0 = smem_u32(sm);
-      const uint64_t da0 = AMN ? mn_desc(s0) : sw128_kmajor_desc(s0),
-                     db0 = BMN ? mn_desc(s0 + S::A_BYTES) : sw128_kmajor_desc(s0 + S::A_BYTES);
+      bool amn = MAJOR == kNN;
+      const uint64_t db0 = BMN ? mn_desc(s0 + S::A_BYTES) : sw128_kmajor_desc(s0 + S::A_BYTES);
       // a K-block of A in stage sa times one of B in stage sb (addresses in the
       // descriptors count 16 bytes)
       auto block = [&](uint32_t d, uint32_t sa, uint32_t sb, bool accumulate) {
-        const uint64_t da = da0 + sa * uint32_t(S::STAGE >> 4), db = db0 + sb * uint32_t(S::STAGE >> 4);
+        const uint64_t da = (amn ? mn_desc(s0) : sw128_kmajor_desc(s0)) + sa * uint32_t(S::STAGE >> 4),
+                       db = db0 + sb * uint32_t(S::STAGE >> 4);
+        const uint32_t id = ID | (amn ? 1u << 15 : 0u), step = amn ? 128 : 2;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma<CG, KIND>(d, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2), ID, (accumulate || kk > 0) ? 1u : 0u);
+        for (uint32_t kk = 0; kk < 4; ++kk)
+          mma<CG, KIND>(d, da + kk * step, db + kk * (BMN ? 128 : 2), id, (accumulate || kk > 0) ? 1u : 0u);
       };
       auto take = [&](uint32_t& stage) {  // the next stage, once it is filled
         stage = st;
@@ -423,9 +463,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
         tc_fence_after();
         return ok;
       };
-      for (int u = unit0; u < units && ok; u += units_step) {
-        const Unit t = unit_of(u);
-        for (int left = a.nseg * t.kbn; left > 0 && ok; ++run) {
+      Unit t;
+      for (int i = 0; ok && unit_at(i, t); ++i) {
+        if (DUAL) amn = t.job == 0;
+        for (int left = a.job[DUAL ? t.job : 0].nseg * t.kbn; left > 0 && ok; ++run) {
           const int len = F32 ? min(left, kRun) : left;
           const uint32_t acc = run & 1u, d = tbase + acc * S::ACC;
           if (run >= 2 && !(ok = mbar_wait(&bars->tempty[acc], ((run >> 1) - 1) & 1u))) break;
@@ -506,6 +547,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
         *reinterpret_cast<uint4*>(buf + slot<ROWB>(lane, j * int(sizeof(TO)) + 16 * k)) = w;
       }
     };
+    auto put8_bf16 = [&](int j, const float* v) {  // (where TO is float)
+      *reinterpret_cast<uint4*>(buf + slot<64>(lane, 2 * j)) =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    };
     // A 16-byte piece of an item for each lane: 4 (bf16) or 8 (fp32) lanes side
     // by side on a row. Pieces past the matrix's edge element by element.
     constexpr int EL = 16 / int(sizeof(TO)), LPR = CW / EL, RPI = 32 / LPR, NV = 32 / RPI;
@@ -517,14 +562,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
         const int r = r0 + i * RPI + piece_row;
         const TO* p = in + (long long)r * a.ldi + cc;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (r >= a.M || cc >= a.N) continue;
-        if (cc + EL <= a.N) {
+        if (r >= job0.M || cc >= job0.N) continue;
+        if (cc + EL <= job0.N) {
           v[i] = __ldg(reinterpret_cast<const uint4*>(p));
         } else {
           uint32_t w[4] = {};
 #pragma unroll
           for (int e = 0; e < EL - 1; ++e)
-            if (cc + e < a.N) {
+            if (cc + e < job0.N) {
               if (sizeof(TO) == 4) w[e] = __float_as_uint(to_float(p[e]));
               else w[e / 2] |= (__float_as_uint(to_float(p[e])) >> 16) << (16 * (e & 1));
             }
@@ -533,29 +578,29 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       }
     };
     // the buffer's item (of element type T) to rows r0 .., columns c0 .. of base
-    auto store_item = [&](auto* base, int r0, int c0) {
+    auto store_item = [&](const Job& o, auto* base, int r0, int c0) {
       using T = typename std::remove_pointer<decltype(base)>::type;
       constexpr int ES = int(sizeof(T)), RB = CW * ES, E = 16 / ES, L = CW / E, RP = 32 / L;
       __syncwarp();
-      if (a.out_vec) {
+      if (o.out_vec) {
         const int pr = lane / L, pc = lane % L * E, cc = c0 + pc;
 #pragma unroll
         for (int i = 0; i < 32 / RP; ++i) {
           const int rr = i * RP + pr, r = r0 + rr;
           const uint8_t* b = buf + slot<RB>(rr, pc * ES);
-          T* p = base + (long long)r * a.ldo + cc;
-          if (r >= a.M || cc >= a.N) continue;
-          if (cc + E <= a.N) {
+          T* p = base + (long long)r * o.ldo + cc;
+          if (r >= o.M || cc >= o.N) continue;
+          if (cc + E <= o.N) {
             *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
           } else {
-            for (int e = 0; cc + e < a.N; ++e) p[e] = reinterpret_cast<const T*>(b)[e];
+            for (int e = 0; cc + e < o.N; ++e) p[e] = reinterpret_cast<const T*>(b)[e];
           }
         }
       } else {
 #pragma unroll 8
         for (int r = 0; r < 32; ++r)
-          if (r0 + r < a.M && c0 + lane < a.N)
-            base[(long long)(r0 + r) * a.ldo + c0 + lane] = *reinterpret_cast<const T*>(buf + slot<RB>(r, lane * ES));
+          if (r0 + r < o.M && c0 + lane < o.N)
+            base[(long long)(r0 + r) * o.ldo + c0 + lane] = *reinterpret_cast<const T*>(buf + slot<RB>(r, lane * ES));
       }
       __syncwarp();
     };
@@ -566,24 +611,25 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
     constexpr bool PRE = IN && sizeof(TO) == 2;
     uint4 pin[PRE ? NV : 1];
     float bias_g = 0.f, bias_u = 0.f;
-    auto prefetch = [&](int u, int c) {
+    auto prefetch = [&](int i, int c) {
       if (!IN && !S::BIAS) return;
-      if (c >= NCH) c = grp, u += units_step;
-      const bool any = u < units && c < NCH, load = any && has_in && a.in_vec;
-      const Unit t = unit_of(any ? u : unit0);
-      const int r = any ? t.m0 + 32 * q : a.M, cc = t.n0 + c * CW;
+      if (c >= NCH) c = grp, ++i;
+      Unit t;
+      t.m0 = t.n0 = 0;
+      const bool any = unit_at(i, t) && c < NCH, load = any && has_in && a.in_vec;
+      const int r = any ? t.m0 + 32 * q : job0.M, cc = t.n0 + c * CW;
       if (PRE) {
-        load_item(pin, load ? r : a.M, cc);
+        load_item(pin, load ? r : job0.M, cc);
       } else if (IN && load) {
-        if (r + lane < a.M && cc < a.N) prefetch_l2(in + (long long)(r + lane) * a.ldi + cc);
+        if (r + lane < job0.M && cc < job0.N) prefetch_l2(in + (long long)(r + lane) * a.ldi + cc);
       }
       if (S::BIAS) {
-        const bool there = any && has_bias && cc + lane < a.N;
+        const bool there = any && has_bias && cc + lane < job0.N;
         bias_g = there ? __ldg(a.bias + cc + lane) : 0.f;
-        if (GATED) bias_u = there ? __ldg(a.bias + a.N + cc + lane) : 0.f;
+        if (GATED) bias_u = there ? __ldg(a.bias + job0.N + cc + lane) : 0.f;
       }
     };
-    prefetch(unit0, grp);
+    prefetch(0, grp);
 
     uint32_t run = 0;
     bool ok = true;
@@ -600,14 +646,15 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       if (lane == 0) mbar_arrive_relaxed(tempty0 + (run & 1u) * 8u);
       ++run;
     };
-    for (int u = unit0; u < units && ok; u += units_step) {
-      const Unit t = unit_of(u);
+    Unit t;
+    for (int i = 0; ok && unit_at(i, t); ++i) {
+      const Job& jb = a.job[DUAL ? t.job : 0];
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
       // one item: 32 rows by CW columns. F32: pg, pu hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
-        if (row0 >= a.M || col0 >= a.N) {
-          prefetch(u, c + GR);
+        if (row0 >= jb.M || col0 >= jb.N) {
+          prefetch(i, c + GR);
           return;
         }
         if (S::BIAS) {
@@ -636,7 +683,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
 #pragma unroll
               for (int r = 0; r < 16; ++r) {
                 v[r] = TO(0.f);
-                if (row0 + r0 + r < a.M && col0 + lane < a.N) v[r] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + lane];
+                if (row0 + r0 + r < jb.M && col0 + lane < jb.N) v[r] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + lane];
               }
 #pragma unroll
               for (int r = 0; r < 16; ++r)
@@ -646,14 +693,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
           __syncwarp();
         }
         const float bu = bias_u;
-        prefetch(u, c + GR);  // (a whole item's time ahead)
+        prefetch(i, c + GR);  // (a whole item's time ahead)
         // e4m3: the row's scale, and the columns' (one per lane, handed round by shuffles)
         float xs = 0.f, ws = 0.f, wsu = 0.f;
         if (SCALED) {
-          if (row < a.M) xs = __ldg(a.xs + row);
-          if (col0 + lane < a.N) {
+          if (row < jb.M) xs = __ldg(a.xs + row);
+          if (col0 + lane < jb.N) {
             ws = __ldg(a.ws + col0 + lane);
-            if (PAIR) wsu = __ldg(a.ws + a.N + col0 + lane);
+            if (PAIR) wsu = __ldg(a.ws + jb.N + col0 + lane);
           }
         }
         // g (and up): the accumulators of this lane's row, then the outputs
@@ -715,7 +762,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
                 if (PAIR) w[PAIR ? k : 0] = x[k] * f.x;
               }
             }
-            if (!TERMS_OUT) put8(j, v);
+            if (DUAL && EPI == kEpiPart && !F32 && t.job) put8_bf16(j, v);
+            else if (!TERMS_OUT) put8(j, v);
           }
         };
         if (EPI == kEpiFwd || EPI == kEpiDz) {
@@ -730,10 +778,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
         }
         auto sums = [&](float* v, int half) {  // (takes v apart)
           const float s = column_sum(v, lane);
-          if (col0 + lane < a.N) a.part[((long long)(row0 >> 5) * halves + half) * a.N + col0 + lane] = s;
+          if (col0 + lane < jb.N) a.part[((long long)(row0 >> 5) * halves + half) * jb.N + col0 + lane] = s;
         };
         if (TERMS_OUT) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(jb.out);
 #pragma unroll
           for (int h = 0; h < halves; ++h) {
             float* v = h ? up : g;
@@ -756,18 +804,23 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
                 }
                 *reinterpret_cast<uint4*>(buf + slot<64>(lane, 2 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              store_item(o + (term * halves + h) * a.out_plane, row0, col0);
+              store_item(jb, o + (term * halves + h) * jb.out_plane, row0, col0);
             }
           }
         } else {
+          // (two products: only job 0 has partial sums)
+          const bool part = EPI == kEpiPart && (!DUAL || t.job == 0);
           int plane = t.batch;
-          if (EPI == kEpiPart) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * a.nb + t.batch;
-          TO* o = static_cast<TO*>(a.out) + plane * a.out_plane;
-          store_item(o, row0, col0);
+          if (part) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * jb.nb + t.batch;
+          TO* o = static_cast<TO*>(jb.out) + plane * jb.out_plane;
+          if (DUAL && EPI == kEpiPart && !F32 && !part)
+            store_item(jb, static_cast<__nv_bfloat16*>(jb.out) + plane * jb.out_plane, row0, col0);
+          else
+            store_item(jb, o, row0, col0);
           if (EPI == kEpiDz && PAIR) {  // du takes the buffer after dg has left it
 #pragma unroll
             for (int j = 0; j < 32; j += 8) put8(j, up + (PAIR ? j : 0));
-            store_item(o + a.out_plane, row0, col0);
+            store_item(jb, o + jb.out_plane, row0, col0);
           }
           if (EPI == kEpiDz && a.part) {
             sums(g, 0);
@@ -777,7 +830,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, GATED, EPI, F32>::kThreads, 1)
       };
       if (F32) {
         float sum[NI][PAIR ? 2 : 1][32];
-        const int runs = (a.nseg * t.kbn + kRun - 1) / kRun;
+        const int runs = (jb.nseg * t.kbn + kRun - 1) / kRun;
         for (int r = 0; r < runs; ++r) {
           if (!wait_run()) break;
           const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
@@ -834,7 +887,7 @@ struct Mat {
 // One product.
 struct Product {
   TcArgs a;
-  Mat A, B;
+  Mat A, B, A1, B1;  // kDual: job 1's
   int major;
   bool gated, f32;  // f32: fp32 operands (in terms)
   int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
@@ -846,10 +899,44 @@ bool run_fwd_product(const Product& p, cudaStream_t s);   // K-major, bf16 opera
 bool run_e4m3_product(const Product& p, cudaStream_t s);  // K-major, e4m3 operands
 bool run_dz_product(const Product& p, cudaStream_t s);
 bool run_grad_product(const Product& p, cudaStream_t s);  // MN-major operands
+bool run_dual_product(const Product& p, cudaStream_t s);
+
+// How two products' units go to C clusters: the longer units dealt round (to
+// the first `rest` clusters h0, to the others h0 - 1), the others so that
+// every cluster's K-blocks come near the mean. load: the most of any.
+struct Deal {
+  int first, rest, h0, l0, l1;
+  long long load;
+};
+inline Deal deal(const TcArgs& a, long long C) {
+  long long n[2], w[2];
+  for (int j = 0; j < 2; ++j) {
+    const Job& o = a.job[j];
+    n[j] = (long long)o.mt * o.nt * o.nb * o.splits;
+    w[j] = (long long)o.kbps * o.nseg + 2;  // (+ 2: a unit's own cost)
+  }
+  const int f = w[0] >= w[1] ? 0 : 1;
+  const long long N = n[f], L = n[1 - f], W = w[f], V = w[1 - f];
+  const long long h0 = (N + C - 1) / C, rest = N - (h0 - 1) * C, others = C - rest;
+  const long long mean = (N * W + L * V + C - 1) / C, near = mean > h0 * W ? (mean - h0 * W) / V : 0;
+  Deal best{f, int(rest), int(h0), 0, 0, INT64_MAX};
+  for (long long t = near; t <= near + 1; ++t) {  // the mean from below, or from above
+    long long l0 = others > 0 ? t : (L + rest - 1) / rest;
+    if (l0 * rest > L) l0 = (L + rest - 1) / rest;
+    const long long left = L > rest * l0 ? L - rest * l0 : 0, l1 = others > 0 ? (left + others - 1) / others : 0;
+    const long long x = h0 * W + l0 * V, y = others > 0 ? (h0 - 1) * W + l1 * V : 0;
+    if ((x > y ? x : y) < best.load) {
+      best.l0 = int(l0);
+      best.l1 = int(l1);
+      best.load = x > y ? x : y;
+    }
+  }
+  return best;
+}
 
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
 bool launch_tc(const Product& p, cudaStream_t s) {
-  using S = Shape<CG, BN, GATED, EPI, F32>;
+  using S = Shape<CG, BN, MAJOR, GATED, EPI, F32>;
   auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32>;
   static int grid_max[64] = {};  // (host threads may race on it: each computes the same value)
   int dev = 0;
@@ -880,22 +967,38 @@ bool launch_tc(const Product& p, cudaStream_t s) {
       grid_max[dev] = sms;
     }
   }
-  const long long units = (long long)p.a.mt * p.a.nt * p.a.nb * p.a.splits;
-  if (units <= 0 || units * CG > INT32_MAX) return false;
   TcArgs a = p.a;
-  a.by_splits = make_div(uint32_t(a.splits));
-  a.by_batch = make_div(uint32_t(a.mt) * uint32_t(a.nt));
-  a.by_group = make_div(8u * uint32_t(a.nt));
-  a.by_last = make_div(a.mt % 8 ? uint32_t(a.mt % 8) : 8u);
-  const long long g = units * CG < grid_max[dev] ? units * CG : grid_max[dev];
+  long long n[2] = {0, 0};  // units
+  for (int j = 0; j < (MAJOR == kDual ? 2 : 1); ++j) {
+    Job& o = a.job[j];
+    n[j] = (long long)o.mt * o.nt * o.nb * o.splits;
+    if (n[j] <= 0 || n[j] * CG > INT32_MAX) return false;
+    o.by_splits = make_div(uint32_t(o.splits));
+    o.by_batch = make_div(uint32_t(o.mt) * uint32_t(o.nt));
+    o.by_group = make_div(8u * uint32_t(o.nt));
+    o.by_last = make_div(o.mt % 8 ? uint32_t(o.mt % 8) : 8u);
+  }
+  const long long want = (n[0] + n[1]) * CG, g = want < grid_max[dev] ? want : grid_max[dev];
+  if (MAJOR == kDual) {
+    const Deal d = deal(a, g / CG);
+    a.first = d.first;
+    a.rest = d.rest;
+    a.h0 = d.h0;
+    a.l0 = d.l0;
+    a.l1 = d.l1;
+  }
   cfg.gridDim = dim3(unsigned(g));
   constexpr int es = KIND == kBf16 ? 2 : 1;
-  CUtensorMap mA, mB;
-  if (!tensor_map_3d(&mA, p.A, es, MAJOR == kNN ? 64 : 128 / es, MAJOR == kNN ? 64 : 128)) return false;
+  constexpr bool amn = MAJOR == kNN || MAJOR == kDual;
+  CUtensorMap mA, mB, mA1, mB1;
+  if (!tensor_map_3d(&mA, p.A, es, amn ? 64 : 128 / es, amn ? 64 : 128)) return false;
   if (!tensor_map_3d(&mB, p.B, es, MAJOR != kKK ? 64 : 128 / es,
                      MAJOR != kKK ? 64 : (GATED && CG == 1 ? BN / 2 : BN / CG)))
     return false;
-  return cudaLaunchKernelEx(&cfg, kernel, a, mA, mB) == cudaSuccess;
+  mA1 = mA;
+  mB1 = mB;
+  if (MAJOR == kDual && (!tensor_map_3d(&mA1, p.A1, es, 64, 128) || !tensor_map_3d(&mB1, p.B1, es, 64, 64))) return false;
+  return cudaLaunchKernelEx(&cfg, kernel, a, mA, mB, mA1, mB1) == cudaSuccess;
 }
 
 // Tile configurations: accumulator columns (an fp32 product's wide tiles are
