@@ -504,33 +504,42 @@ def emb_adagrad_update(tables: EmbeddingTables, state: SparseState, lr: float = 
 _DTYPES = {torch.float32: DSF_F32, torch.bfloat16: DSF_BF16, torch.float8_e4m3fn: DSF_E4M3}
 
 
-def _mat(name: str, t: torch.Tensor, dtype, shape, device):
-    """Pointer and row stride of a [rows, cols] matrix whose columns are
-    contiguous; raises ValueError for anything else."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
-        raise ValueError("%s: %s %s on %s expected, got %s %s on %s" % (
-            name, dtype, list(shape), device, t.dtype, list(t.shape), t.device))
-    if shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
-        raise ValueError("%s: columns must be contiguous" % name)
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
-    if ld < shape[1]:
+def _mat(name: str, t: torch.Tensor, dtype, rows: int, cols: int, dev: int):
+    """Pointer and row stride of a [rows, cols] matrix on device dev whose
+    columns are contiguous; raises ValueError for anything else."""
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
+        raise ValueError("%s: %s [%d, %d] on cuda:%d expected, got %s %s on %s" % (
+            name, dtype, rows, cols, dev, t.dtype, list(t.shape), t.device))
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError("%s: rows overlap" % name)
+    if one != 1 and cols > 1 and rows > 0:
+        raise ValueError("%s: columns must be contiguous" % name)
     return t.data_ptr(), ld
 
 
-def _vec(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[int]:
+def _vec(name: str, t: Optional[torch.Tensor], n: int, dev: int) -> Optional[int]:
     """Pointer of a contiguous fp32 [n] vector (None for None)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
-        raise ValueError("%s: contiguous float32 [%d] on %s expected" % (name, n, device))
+    if t.dtype is not torch.float32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s: contiguous float32 [%d] on cuda:%d expected" % (name, n, dev))
     return t.data_ptr()
 
 
-def _on_current(device) -> None:
-    """The calls launch on the current device: its tensors have to be there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
+def _dev_of(t: torch.Tensor) -> int:
+    """The tensor's CUDA device index, which has to be the current device's:
+    the calls launch there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("a tensor on %s, but the current device is cuda:%d" % (t.device, torch.cuda.current_device()))
+    return dev
+
+
+def _on(dev: int, stream) -> Optional[int]:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
 class DenseLayer:
@@ -543,13 +552,16 @@ class DenseLayer:
         if W.dim() != 2 or W.dtype not in _DTYPES:
             raise ValueError("W: a float32, bfloat16 or float8_e4m3fn matrix expected")
         R, K = int(W.shape[0]), int(W.shape[1])
-        self.dtype = _DTYPES[W.dtype]
-        ptr, ldw = _mat("W", W, W.dtype, (R, K), W.device)
+        self.dtype, self.type = _DTYPES[W.dtype], W.dtype
+        self.dev = W.get_device()
+        if self.dev < 0:
+            raise ValueError("W: a CUDA tensor expected")
+        ptr, ldw = _mat("W", W, W.dtype, R, K, self.dev)
         if (scale is not None) != (self.dtype == DSF_E4M3):
             raise ValueError("scale: given for float8_e4m3fn weights, and only for them")
         self.W, self.bias, self.scale, self.R, self.K, self.act = W, bias, scale, R, K, int(act)
         self.out_dtype = torch.bfloat16 if self.dtype == DSF_E4M3 else W.dtype
-        self.c = CDense(ptr, _vec("bias", bias, R, W.device), _vec("scale", scale, R, W.device), ldw, R, K, self.dtype,
+        self.c = CDense(ptr, _vec("bias", bias, R, self.dev), _vec("scale", scale, R, self.dev), ldw, R, K, self.dtype,
                         self.act)
         self._ref = ctypes.byref(self.c)
 
@@ -567,39 +579,33 @@ class DenseWorkspace:
         if self.nbytes == 0:
             raise DsfError(DSF_EINVAL, "dsf_dense_workspace_bytes")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=layer.device)
-        self.ptr = self.buf.data_ptr()
+        self.ptr, self.dev = self.buf.data_ptr(), layer.dev
 
 
-def _x_of(layer: DenseLayer, x: torch.Tensor):
-    _on_current(layer.device)
-    if x.dim() != 2:
-        raise ValueError("x: a matrix expected")
-    M = int(x.shape[0])
-    return (M,) + _mat("x", x, layer.W.dtype, (M, layer.K), layer.device)
+def _x_of(layer: DenseLayer, x: torch.Tensor, workspace: DenseWorkspace):
+    dev = layer.dev
+    if dev != torch.cuda.current_device() or workspace.dev != dev:
+        raise ValueError("the layer is on cuda:%d, the workspace on cuda:%d, and the current device is cuda:%d" % (
+            dev, workspace.dev, torch.cuda.current_device()))
+    M = x.shape[0] if x.dim() == 2 else -1
+    return dev, M, _mat("x", x, layer.type, M, layer.K, dev)
 
 
 def _scale_of(layer: DenseLayer, x_scale, M: int):
     if (x_scale is not None) != (layer.dtype == DSF_E4M3):
         raise ValueError("x_scale: given for float8_e4m3fn layers, and only for them")
-    return _vec("x_scale", x_scale, M, layer.device)
-
-
-def _ws_of(layer: DenseLayer, workspace: DenseWorkspace):
-    if workspace.buf.device != layer.device:
-        raise ValueError("the workspace is on %s" % workspace.buf.device)
-    return workspace.ptr, workspace.nbytes
+    return _vec("x_scale", x_scale, M, layer.dev)
 
 
 def ctr_dense_fwd(layer: DenseLayer, x: torch.Tensor, y: torch.Tensor, workspace: DenseWorkspace,
                   residual: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y [M, N] = residual + act(x W^T + bias); y may be the residual."""
-    M, xp, ldx = _x_of(layer, x)
-    yp, ldy = _mat("y", y, layer.out_dtype, (M, layer.R), layer.device)
-    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, layer.out_dtype, (M, layer.R), layer.device)
-    wp, nb = _ws_of(layer, workspace)
-    _check(lib().ctr_dense_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), rp, ldr, M, yp, ldy, wp, nb,
-                               _dptr(status), _stream_ptr(stream)), "ctr_dense_fwd")
+    dev, M, (xp, ldx) = _x_of(layer, x, workspace)
+    yp, ldy = _mat("y", y, layer.out_dtype, M, layer.R, dev)
+    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, layer.out_dtype, M, layer.R, dev)
+    _check(lib().ctr_dense_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), rp, ldr, M, yp, ldy, workspace.ptr,
+                               workspace.nbytes, _dptr(status), _on(dev, stream)), "ctr_dense_fwd")
     return y
 
 
@@ -607,27 +613,25 @@ def ctr_glu_fwd(layer: DenseLayer, x: torch.Tensor, h: torch.Tensor, workspace: 
                 x_scale: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
     """h [M, F] = act(x Wg^T + bg) * (x Wu^T + bu), W = [Wg; Wu]."""
-    M, xp, ldx = _x_of(layer, x)
-    hp, ldh = _mat("h", h, layer.out_dtype, (M, layer.R // 2), layer.device)
-    wp, nb = _ws_of(layer, workspace)
-    _check(lib().ctr_glu_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), M, hp, ldh, wp, nb, _dptr(status),
-                             _stream_ptr(stream)), "ctr_glu_fwd")
+    dev, M, (xp, ldx) = _x_of(layer, x, workspace)
+    hp, ldh = _mat("h", h, layer.out_dtype, M, layer.R // 2, dev)
+    _check(lib().ctr_glu_fwd(layer._ref, xp, ldx, _scale_of(layer, x_scale, M), M, hp, ldh, workspace.ptr,
+                             workspace.nbytes, _dptr(status), _on(dev, stream)), "ctr_glu_fwd")
     return h
 
 
 def _layer_bwd(name, layer, x, dy, cols, workspace, dx, dW, db, status, stream):
-    M, xp, ldx = _x_of(layer, x)
-    T, dev = layer.W.dtype, layer.device
-    gp, ldg = _mat("the upstream gradient", dy, T, (M, cols), dev)
-    dxp, lddx = (None, 0) if dx is None else _mat("dx", dx, T, (M, layer.K), dev)
+    dev, M, (xp, ldx) = _x_of(layer, x, workspace)
+    T = layer.type
+    gp, ldg = _mat("the upstream gradient", dy, T, M, cols, dev)
+    dxp, lddx = (None, 0) if dx is None else _mat("dx", dx, T, M, layer.K, dev)
     dWp = None
     if dW is not None:
-        dWp, ld = _mat("dW", dW, T, (layer.R, layer.K), dev)
+        dWp, _ = _mat("dW", dW, T, layer.R, layer.K, dev)
         if not dW.is_contiguous():
             raise ValueError("dW: contiguous expected")
-    wp, nb = _ws_of(layer, workspace)
-    _check(getattr(lib(), name)(layer._ref, xp, ldx, gp, ldg, M, dxp, lddx, dWp, _vec("db", db, layer.R, dev), wp, nb,
-                                _dptr(status), _stream_ptr(stream)), name)
+    _check(getattr(lib(), name)(layer._ref, xp, ldx, gp, ldg, M, dxp, lddx, dWp, _vec("db", db, layer.R, dev),
+                                workspace.ptr, workspace.nbytes, _dptr(status), _on(dev, stream)), name)
 
 
 def ctr_dense_bwd(layer: DenseLayer, x: torch.Tensor, dy: torch.Tensor, workspace: DenseWorkspace,
@@ -653,6 +657,7 @@ class RmsNormWorkspace:
         if self.nbytes == 0:
             raise DsfError(DSF_EINVAL, "dsf_rms_norm_workspace_bytes")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr, self.dev = self.buf.data_ptr(), self.buf.get_device()
 
 
 def ctr_rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -660,18 +665,17 @@ def ctr_rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Te
                      eps: float = 1e-6, y_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """s = x + residual (into sum_out where given), y = s * weight /
     sqrt(mean(s^2) + eps); y float32, bfloat16, or float8_e4m3fn with y_scale."""
-    dev = x.device
-    _on_current(dev)
-    if x.dim() != 2 or x.dtype not in _DTYPES or y.dtype not in _DTYPES:
+    dev, xt, yt = _dev_of(x), x.dtype, y.dtype
+    if x.dim() != 2 or xt not in _DTYPES or yt not in _DTYPES:
         raise ValueError("x and y: matrices of a supported type expected")
-    M, N = int(x.shape[0]), int(x.shape[1])
-    xp, ldx = _mat("x", x, x.dtype, (M, N), dev)
-    yp, ldy = _mat("y", y, y.dtype, (M, N), dev)
-    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, x.dtype, (M, N), dev)
-    sp, lds = (None, 0) if sum_out is None else _mat("sum_out", sum_out, x.dtype, (M, N), dev)
-    _check(lib().ctr_rms_norm_fwd(xp, ldx, rp, ldr, _DTYPES[x.dtype], _vec("weight", weight, N, dev), M, N, float(eps),
-                                  sp, lds, yp, ldy, _DTYPES[y.dtype], _vec("y_scale", y_scale, M, dev),
-                                  _stream_ptr(stream)), "ctr_rms_norm_fwd")
+    M, N = x.shape
+    xp, ldx = _mat("x", x, xt, M, N, dev)
+    yp, ldy = _mat("y", y, yt, M, N, dev)
+    rp, ldr = (None, 0) if residual is None else _mat("residual", residual, xt, M, N, dev)
+    sp, lds = (None, 0) if sum_out is None else _mat("sum_out", sum_out, xt, M, N, dev)
+    _check(lib().ctr_rms_norm_fwd(xp, ldx, rp, ldr, _DTYPES[xt], _vec("weight", weight, N, dev), M, N, eps, sp, lds, yp,
+                                  ldy, _DTYPES[yt], _vec("y_scale", y_scale, M, dev), _on(dev, stream)),
+           "ctr_rms_norm_fwd")
     return y
 
 
@@ -680,18 +684,17 @@ def ctr_rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, dx: torch.Tensor, weight
                      workspace: Optional[RmsNormWorkspace] = None, stream=None) -> None:
     """dx = the norm's gradient at s for dy, plus dsum where given; dweight
     (which needs the workspace) overwritten."""
-    dev = s.device
-    _on_current(dev)
-    if s.dim() != 2 or s.dtype not in _DTYPES or dy.dtype not in _DTYPES:
+    dev, st, gt = _dev_of(s), s.dtype, dy.dtype
+    if s.dim() != 2 or st not in _DTYPES or gt not in _DTYPES:
         raise ValueError("s and dy: matrices of a supported type expected")
-    M, N = int(s.shape[0]), int(s.shape[1])
-    gp, ldg = _mat("dy", dy, dy.dtype, (M, N), dev)
-    sp, lds = _mat("s", s, s.dtype, (M, N), dev)
-    dp, ldd = (None, 0) if dsum is None else _mat("dsum", dsum, s.dtype, (M, N), dev)
-    xp, ldx = _mat("dx", dx, s.dtype, (M, N), dev)
-    if workspace is not None and workspace.buf.device != dev:
-        raise ValueError("the workspace is on %s" % workspace.buf.device)
-    _check(lib().ctr_rms_norm_bwd(gp, ldg, _DTYPES[dy.dtype], sp, lds, _DTYPES[s.dtype], _vec("weight", weight, N, dev),
-                                  M, N, float(eps), dp, ldd, xp, ldx, _vec("dweight", dweight, N, dev),
-                                  None if workspace is None else workspace.buf.data_ptr(),
-                                  0 if workspace is None else workspace.nbytes, _stream_ptr(stream)), "ctr_rms_norm_bwd")
+    M, N = s.shape
+    gp, ldg = _mat("dy", dy, gt, M, N, dev)
+    sp, lds = _mat("s", s, st, M, N, dev)
+    dp, ldd = (None, 0) if dsum is None else _mat("dsum", dsum, st, M, N, dev)
+    xp, ldx = _mat("dx", dx, st, M, N, dev)
+    wp, nb = (None, 0) if workspace is None else (workspace.ptr, workspace.nbytes)
+    if workspace is not None and workspace.dev != dev:
+        raise ValueError("the workspace is on cuda:%d" % workspace.dev)
+    _check(lib().ctr_rms_norm_bwd(gp, ldg, _DTYPES[gt], sp, lds, _DTYPES[st], _vec("weight", weight, N, dev), M, N, eps,
+                                  dp, ldd, xp, ldx, _vec("dweight", dweight, N, dev), wp, nb, _on(dev, stream)),
+           "ctr_rms_norm_bwd")
