@@ -516,7 +516,7 @@ bool grad_products(const Ctx& c, const Mat& dz, void* dx, long long lddx, void* 
 int fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const float* xs, const void* res, long long ldr,
         long long M, void* y, long long ldy, void* ws, int* status, cudaStream_t s) {
   bool ok;
-  if (M <= kSmallM) {
+  if (small_call(l->dtype, M, l->R, l->K)) {
     const int N = gated ? l->R / 2 : l->R;
     const SmallArgs a{x, l->W, ldx, l->ldw, l->bias, xs, l->scale, res, ldr, y, ldy, int(M), N, l->K, l->act};
     const bool vec = (l->K * esize(l->dtype)) % 16 == 0;
