@@ -48,20 +48,30 @@ constexpr int kMaxSplits = 32;
 // unit holds at most 256 x 256 fp32 per pair of SMs
 constexpr size_t kPartBytes = size_t(kSms / 2) * 256 * 256 * 4;
 
-// Estimates in SM cycles, per tile configuration: a K-block of a 256 x 256
-// tile (on two SMs; fp32: 256 x 128, six products), 128 x 128 or 128 x 64
-// tile takes kStep cycles; a launch has its start and its last tile's
-// epilogue (kUnit); the chip takes its units in whole waves; a split product
-// pays for a second launch and its partial sums' way to L2 and back.
+// Estimates in microseconds, per tile configuration (fitted to measured calls
+// of 200 to 8192 rows): a K-block of a 256 x 256 tile (on two SMs; fp32: 256 x
+// 128, six products), 128 x 128 or 128 x 64 tile takes `block`, its epilogue
+// `tail`, and the two overlap from tile to tile; a launch costs kLaunch; the
+// chip takes its units in whole waves; a split product pays for a second
+// launch and its partial sums' way to L2 and back.
 struct Cost {
   bool f32;
-  double step(int cfg) const {
-    constexpr double kStep[2][3] = {{560, 560, 400}, {1700, 1800, 1300}};
-    return kStep[f32][cfg];
+  double block(int cfg) const {
+    constexpr double kBlock[2][3] = {{0.31, 0.29, 0.275}, {0.9, 0.95, 0.75}};
+    return kBlock[f32][cfg];
   }
-  static constexpr double kUnit = 1500, kTile = 300, kSecond = 5000, kBytesPerCycle = 2000;
+  double tail(int cfg) const {
+    constexpr double kTail[2][3] = {{4.4, 2.2, 1.2}, {3.0, 3.0, 2.0}};
+    return kTail[f32][cfg];
+  }
+  // `units` in a row, of `blocks` K-blocks each
+  double run(int cfg, double units, double blocks) const {
+    const double m = blocks * block(cfg), e = tail(cfg);
+    return units * (m > e ? m : e) + (m > e ? e : m);
+  }
+  static constexpr double kLaunch = 2.4, kSecond = 2.2, kBytesPerUs = 4e6;
   static double parts(long long splits, double outputs) {
-    return splits > 1 ? kSecond + double(splits) * outputs * 8 / kBytesPerCycle : 0;
+    return splits > 1 ? kSecond + double(splits) * outputs * 8 / kBytesPerUs : 0;
   }
 };
 
@@ -95,7 +105,7 @@ void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg,
       if (want > 1 && (!may_split || tiles_of(o) * want > slots_of(cfg))) break;
       if (o.splits != want) continue;
       const long long waves = (tiles_of(o) * o.splits + slots_of(cfg) - 1) / slots_of(cfg);
-      const double c = Cost::kUnit + double(waves) * (cost.step(cfg) * double(o.kbps) * nseg + Cost::kTile) +
+      const double c = Cost::kLaunch + cost.run(cfg, double(waves), double(o.kbps) * nseg) +
                        Cost::parts(o.splits, double(M) * N * nb * (p.gated ? 2 : 1));
       if (c < best) {
         best = c;
@@ -120,14 +130,17 @@ void plan_dual(Product& p, long long M, long long N, long long K, int halves) {
       if (tiles_of(w) > INT32_MAX / 64 || tiles_of(a.job[1]) > INT32_MAX / 64) break;
       if (want > 1 && tiles_of(w) * want > slots_of(cfg)) break;
       if (w.splits != want) continue;
-      const Deal d = deal(a, slots_of(cfg));
-      const double c = Cost::kUnit + cost.step(cfg) * double(d.load) +
-                       Cost::parts(w.splits, double(N) * K * halves);
+            const double tail = cost.tail(cfg), tw = w.kbps * cost.block(cfg), tx = double(kx) * halves * cost.block(cfg);
+      const long long weight[2] = {(long long)(1e3 * (tw > tail ? tw : tail)), (long long)(1e3 * (tx > tail ? tx : tail))};
+      const Deal d = deal(a, weight, slots_of(cfg));
+      const double c = Cost::kLaunch + 1e-3 * double(d.load) + tail + Cost::parts(w.splits, double(N) * K * halves);
       if (c < best) {
         best = c;
         p.cfg = cfg;
         p.a.job[0] = a.job[0];
         p.a.job[1] = a.job[1];
+        p.weight[0] = weight[0];
+        p.weight[1] = weight[1];
       }
     }
 }

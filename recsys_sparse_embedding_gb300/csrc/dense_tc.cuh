@@ -611,17 +611,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     constexpr bool PRE = IN && sizeof(TO) == 2;
     uint4 pin[PRE ? NV : 1];
     float bias_g = 0.f, bias_u = 0.f;
-    auto prefetch = [&](int i, int c) {
+    auto prefetch = [&](bool any, const Unit& t, int c) {
       if (!IN && !S::BIAS) return;
-      if (c >= NCH) c = grp, ++i;
-      Unit t;
-      t.m0 = t.n0 = 0;
-      const bool any = unit_at(i, t) && c < NCH, load = any && has_in && a.in_vec;
       const int r = any ? t.m0 + 32 * q : job0.M, cc = t.n0 + c * CW;
-      if (PRE) {
-        load_item(pin, load ? r : job0.M, cc);
-      } else if (IN && load) {
-        if (r + lane < job0.M && cc < job0.N) prefetch_l2(in + (long long)(r + lane) * a.ldi + cc);
+      if (PRE) load_item(pin, has_in && a.in_vec ? r : job0.M, cc);
+      if (IN && has_in && !(PRE && a.in_vec) && r + lane < job0.M && cc < job0.N) {
+        const TO* p = in + (long long)(r + lane) * a.ldi + cc;
+        prefetch_l2(p);
+        prefetch_l2(p + min(CW, job0.N - cc) - 1);  // (unaligned rows: perhaps another line)
       }
       if (S::BIAS) {
         const bool there = any && has_bias && cc + lane < job0.N;
@@ -629,7 +626,19 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         if (GATED) bias_u = there ? __ldg(a.bias + job0.N + cc + lane) : 0.f;
       }
     };
-    prefetch(0, grp);
+    auto prefetch_after = [&](int i, const Unit& t, int c) {  // the item after item c of unit i
+      if (!IN && !S::BIAS) return;
+      if (c + GR < NCH) {
+        prefetch(true, t, c + GR);
+      } else {
+        Unit n;
+        n.m0 = n.n0 = 0;
+        prefetch(unit_at(i + 1, n) && grp < NCH, n, grp);
+      }
+    };
+    Unit t;
+    t.m0 = t.n0 = 0;
+    prefetch(unit_at(0, t) && grp < NCH, t, grp);
 
     uint32_t run = 0;
     bool ok = true;
@@ -646,7 +655,6 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       if (lane == 0) mbar_arrive_relaxed(tempty0 + (run & 1u) * 8u);
       ++run;
     };
-    Unit t;
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const Job& jb = a.job[DUAL ? t.job : 0];
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
@@ -654,8 +662,20 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
         if (row0 >= jb.M || col0 >= jb.N) {
-          prefetch(i, c + GR);
+          prefetch_after(i, t, c);
           return;
+        }
+        // g (and up): the accumulators of this lane's row, then the outputs. (Their
+        // loads run while the item's other inputs are laid out.)
+        float g_[32], up_[PAIR ? 32 : 1];
+        float* g = g_;
+        float* up = up_;
+        if (F32) {
+          g = pg;
+          up = pu;
+        } else {
+          tmem_ld32(tacc + uint32_t(c * CW), g);
+          if (PAIR) tmem_ld32(tacc + uint32_t(c * CW) + ON, up);
         }
         if (S::BIAS) {
           wbias[lane] = bias_g;
@@ -676,24 +696,25 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
                 *reinterpret_cast<uint4*>(buf + slot<ROWB>(i * RPI + piece_row, piece_col * int(sizeof(TO)))) =
                     pin[PRE ? i : 0];
             }
-          } else {  // one column per lane, 16 rows in flight
+          } else {  // one column per lane, RB rows in flight
+            constexpr int RB = S::kEpiWarps == 8 ? 32 : 16;
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 16) {
-              TO v[16];
+            for (int r0 = 0; r0 < 32; r0 += RB) {
+              TO v[RB];
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
+              for (int r = 0; r < RB; ++r) {
                 v[r] = TO(0.f);
                 if (row0 + r0 + r < jb.M && col0 + lane < jb.N) v[r] = in[(long long)(row0 + r0 + r) * a.ldi + col0 + lane];
               }
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
+              for (int r = 0; r < RB; ++r)
                 *reinterpret_cast<TO*>(buf + slot<ROWB>(r0 + r, lane * int(sizeof(TO)))) = v[r];
             }
           }
           __syncwarp();
         }
         const float bu = bias_u;
-        prefetch(i, c + GR);  // (a whole item's time ahead)
+        prefetch_after(i, t, c);  // (a whole item's time ahead)
         // e4m3: the row's scale, and the columns' (one per lane, handed round by shuffles)
         float xs = 0.f, ws = 0.f, wsu = 0.f;
         if (SCALED) {
@@ -703,18 +724,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             if (PAIR) wsu = __ldg(a.ws + jb.N + col0 + lane);
           }
         }
-        // g (and up): the accumulators of this lane's row, then the outputs
-        float g_[32], up_[PAIR ? 32 : 1];
-        float* g = g_;
-        float* up = up_;
-        if (F32) {
-          g = pg;
-          up = pu;
-        } else {
-          tmem_ld32(tacc + uint32_t(c * CW), g);
-          if (PAIR) tmem_ld32(tacc + uint32_t(c * CW) + ON, up);
-          tmem_ld_wait();
-        }
+        if (!F32) tmem_ld_wait();
         // eight columns at a time, from the accumulators to the buffer
         auto math = [&](auto act_tag) {
           constexpr int ACT = decltype(act_tag)::value;
@@ -891,6 +901,7 @@ struct Product {
   int major;
   bool gated, f32;  // f32: fp32 operands (in terms)
   int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
+  long long weight[2];  // kDual: a unit's time, by job
 };
 
 bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows);
@@ -903,18 +914,15 @@ bool run_dual_product(const Product& p, cudaStream_t s);
 
 // How two products' units go to C clusters: the longer units dealt round (to
 // the first `rest` clusters h0, to the others h0 - 1), the others so that
-// every cluster's K-blocks come near the mean. load: the most of any.
+// every cluster's time comes near the mean. w: a unit's time, by job; load:
+// the most of any.
 struct Deal {
   int first, rest, h0, l0, l1;
   long long load;
 };
-inline Deal deal(const TcArgs& a, long long C) {
-  long long n[2], w[2];
-  for (int j = 0; j < 2; ++j) {
-    const Job& o = a.job[j];
-    n[j] = (long long)o.mt * o.nt * o.nb * o.splits;
-    w[j] = (long long)o.kbps * o.nseg + 2;  // (+ 2: a unit's own cost)
-  }
+inline Deal deal(const TcArgs& a, const long long (&w)[2], long long C) {
+  long long n[2];
+  for (int j = 0; j < 2; ++j) n[j] = (long long)a.job[j].mt * a.job[j].nt * a.job[j].nb * a.job[j].splits;
   const int f = w[0] >= w[1] ? 0 : 1;
   const long long N = n[f], L = n[1 - f], W = w[f], V = w[1 - f];
   const long long h0 = (N + C - 1) / C, rest = N - (h0 - 1) * C, others = C - rest;
@@ -980,7 +988,7 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   }
   const long long want = (n[0] + n[1]) * CG, g = want < grid_max[dev] ? want : grid_max[dev];
   if (MAJOR == kDual) {
-    const Deal d = deal(a, g / CG);
+    const Deal d = deal(a, p.weight, g / CG);
     a.first = d.first;
     a.rest = d.rest;
     a.h0 = d.h0;
