@@ -442,7 +442,7 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.major = kKK;
   p.gated = c.gated;
   p.f32 = f32;
-  p.epi = dz ? kEpiDz : kEpiFwd;
+  p.epi = dz ? kEpiDz : (in ? kEpiRes : kEpiFwd);
   const long long nkb = (l->K + c.kbe - 1) / c.kbe;
   plan(p, c.M, c.N, 1, nkb, 1, !dz);
   Job& o = p.a.job[0];

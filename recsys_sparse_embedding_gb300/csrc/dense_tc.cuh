@@ -51,7 +51,8 @@ namespace dense {
 
 // What the epilogue does with an accumulator.
 enum Epi {
-  kEpiFwd = 0,   // out = residual + act(z), or act(z) * z' for a gated layer
+  kEpiFwd = 0,   // out = act(z), or act(z) * z' for a gated layer
+  kEpiRes = 4,   // out = in + act(z): the forward with a residual
   kEpiDz = 1,    // out = dz (planes dg, du for a gated layer; fp32: its three
                  // terms) from in = dy; column sums
   kEpiOut = 2,   // out = the accumulator
@@ -97,7 +98,7 @@ struct TcArgs {
   int first, rest, h0, l0, l1;
   int act;
   const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
-  const void* in;               // nullable unless kEpiDz
+  const void* in;               // kEpiRes, kEpiDz
   long long ldi;
   int in_vec;   // rows at 16-byte boundaries
   float* part;  // kEpiDz: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
@@ -213,7 +214,7 @@ struct Shape {
   static constexpr int BNC = BN / CG;  // B rows (or MN-major columns) in this CTA
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BNC * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int EBYTES = kEpiWarps * ITEM;
-  static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiDz;
+  static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiRes || EPI == kEpiDz;
   // bias floats of an item that each epilogue warp keeps in shared memory (the
   // gated forward's six stages leave room for the gate's alone; the up half's
   // are handed round by shuffles)
@@ -504,8 +505,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     uint8_t* buf = sE + warp * S::ITEM;
     float* wbias = sBias + warp * S::BIAS_N;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
-    constexpr bool IN = (EPI == kEpiFwd && !GATED) || EPI == kEpiDz;
-    constexpr bool SCALED = KIND == kE4m3 && EPI == kEpiFwd;
+    constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz;
+    constexpr bool SCALED = KIND == kE4m3 && FWD;
     constexpr bool TERMS_OUT = F32 && EPI == kEpiDz;  // dz leaves as three bf16 terms
     constexpr bool PAIR = GATED && EPI != kEpiPart;   // an item takes gate and up accumulators
     constexpr int GR = S::kGroups, ROWB = CW * int(sizeof(TO));
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     // items of a tile side by side: over its accumulators for a gated layer's partial sums, else over its outputs
     constexpr int NCH = (GATED && EPI == kEpiPart ? BN : ON) / CW;
     constexpr int NI = (NCH + GR - 1) / GR;  // items per warp and tile
-    const bool has_in = IN && (EPI == kEpiDz || a.in), has_bias = S::BIAS && a.bias;
+    const bool has_bias = S::BIAS && a.bias;
     const TO* in = static_cast<const TO*>(a.in);
     const uint32_t tempty0 = CG == 2 ? mapa(smem_u32(&bars->tempty[0]), 0) : smem_u32(&bars->tempty[0]);
 
@@ -557,10 +558,17 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     const int piece_row = lane / LPR, piece_col = lane % LPR * EL;
     auto load_item = [&](uint4* v, int r0, int c0) {
       const int cc = c0 + piece_col;
+      const TO* p0 = in + (long long)(r0 + piece_row) * a.ldi + cc;
+      const long long step = RPI * a.ldi;
+      if (r0 + 32 <= job0.M && c0 + CW <= job0.N) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p0 + i * step));
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int r = r0 + i * RPI + piece_row;
-        const TO* p = in + (long long)r * a.ldi + cc;
+        const TO* p = p0 + i * step;
         v[i] = make_uint4(0, 0, 0, 0);
         if (r >= job0.M || cc >= job0.N) continue;
         if (cc + EL <= job0.N) {
@@ -584,6 +592,15 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       __syncwarp();
       if (o.out_vec) {
         const int pr = lane / L, pc = lane % L * E, cc = c0 + pc;
+        if (r0 + 32 <= o.M && c0 + CW <= o.N) {
+          T* p = base + (long long)(r0 + pr) * o.ldo + cc;
+          const long long step = RP * o.ldo;
+#pragma unroll
+          for (int i = 0; i < 32 / RP; ++i)
+            *reinterpret_cast<uint4*>(p + i * step) = *reinterpret_cast<const uint4*>(buf + slot<RB>(i * RP + pr, pc * ES));
+          __syncwarp();
+          return;
+        }
 #pragma unroll
         for (int i = 0; i < 32 / RP; ++i) {
           const int rr = i * RP + pr, r = r0 + rr;
@@ -614,8 +631,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     auto prefetch = [&](bool any, const Unit& t, int c) {
       if (!IN && !S::BIAS) return;
       const int r = any ? t.m0 + 32 * q : job0.M, cc = t.n0 + c * CW;
-      if (PRE) load_item(pin, has_in && a.in_vec ? r : job0.M, cc);
-      if (IN && has_in && !(PRE && a.in_vec) && r + lane < job0.M && cc < job0.N) {
+      if (PRE) load_item(pin, a.in_vec ? r : job0.M, cc);
+      if (IN && !(PRE && a.in_vec) && r + lane < job0.M && cc < job0.N) {
         const TO* p = in + (long long)(r + lane) * a.ldi + cc;
         prefetch_l2(p);
         prefetch_l2(p + min(CW, job0.N - cc) - 1);  // (unaligned rows: perhaps another line)
@@ -680,9 +697,9 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         if (S::BIAS) {
           wbias[lane] = bias_g;
           if (S::BIAS_N == 64) wbias[32 + lane] = bias_u;
-          if (!has_in) __syncwarp();
+          if (!IN) __syncwarp();
         }
-        if (has_in) {
+        if (IN) {
           if (a.in_vec) {
             if (!PRE) {
               uint4 v[NV];
@@ -755,13 +772,13 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
               }
             }
             float x[8];
-            if (has_in) get8(j, x);
-            if (EPI == kEpiFwd) {
+            if (IN) get8(j, x);
+            if (FWD) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 v[k] = act_value<ACT>(v[k]);
                 if (PAIR) v[k] *= w[PAIR ? k : 0];
-                if (has_in) v[k] += x[k];
+                if (EPI == kEpiRes) v[k] += x[k];
               }
             }
             if (EPI == kEpiDz) {
@@ -776,7 +793,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             else if (!TERMS_OUT) put8(j, v);
           }
         };
-        if (EPI == kEpiFwd || EPI == kEpiDz) {
+        if (FWD || EPI == kEpiDz) {
           switch (a.act) {
             case DSF_ACT_RELU: math(std::integral_constant<int, DSF_ACT_RELU>{}); break;
             case DSF_ACT_SILU: math(std::integral_constant<int, DSF_ACT_SILU>{}); break;

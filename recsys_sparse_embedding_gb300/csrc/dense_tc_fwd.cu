@@ -48,6 +48,8 @@ bool run_fwd_product(const Product& p, cudaStream_t s) {
     return p.gated ? launch_cfg<kKK, kBf16, true, kEpiPart, false>(p, s)
                    : launch_cfg<kKK, kBf16, false, kEpiPart, false>(p, s);
   }
+  if (p.epi == kEpiRes)
+    return p.f32 ? launch_cfg<kKK, kBf16, false, kEpiRes, true>(p, s) : launch_cfg<kKK, kBf16, false, kEpiRes, false>(p, s);
   if (p.f32)
     return p.gated ? launch_cfg<kKK, kBf16, true, kEpiFwd, true>(p, s)
                    : launch_cfg<kKK, kBf16, false, kEpiFwd, true>(p, s);
