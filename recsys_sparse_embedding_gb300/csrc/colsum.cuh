@@ -7,42 +7,46 @@
 
 namespace dsf {
 
-// out[n] = sum over r of P[r][n]. A block of 32 warps takes 32 columns: warp g
-// adds rows g, g + 32, g + 64, ... in order (eight loads in flight), then warp
-// 0 adds the 32 sums in warp order, so the result does not depend on timing.
-// (Latency is what counts here: 608 x 256 took 19 us with 8 warps and four
-// loads in flight, the rows in sequence.)
+// out[n] = sum over r of P[r][n]. A block takes 8 columns (32-byte sectors):
+// lane l of warp g adds rows 4 g + l / 8, + 128, ... of column l % 8 in order
+// (four loads in flight), then the 128 sums are added in a fixed tree, so the
+// result does not depend on timing. (Latency is what counts here: 608 x 256 took
+// 19 us with 32 columns and 8 warps to a block, 7 with 32 columns and 32 warps.)
 template <int = 0>  // (a template so that several units may include it)
 __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ P, long long rows, int N,
                                                       float* __restrict__ out) {
-  constexpr int W = 32, U = 8;
-  __shared__ float part[W][33];
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int n = blockIdx.x * 32 + lane;
+  constexpr int W = 32, U = 4, R = 4 * W;
+  __shared__ float part[W][8];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, c = lane & 7;
+  const int n = blockIdx.x * 8 + c;
   pdl_go();
   pdl_wait();
   float s = 0.f;
   if (n < N) {
-    for (long long r0 = g; r0 < rows; r0 += W * U) {
+    for (long long r0 = 4 * g + (lane >> 3); r0 < rows; r0 += R * U) {
       float v[U];
 #pragma unroll
-      for (int t = 0; t < U; ++t) v[t] = r0 + W * t < rows ? P[(r0 + W * t) * N + n] : 0.f;
+      for (int t = 0; t < U; ++t) v[t] = r0 + R * t < rows ? P[(r0 + R * t) * N + n] : 0.f;
 #pragma unroll
       for (int t = 0; t < U; ++t) s += v[t];
     }
   }
-  part[g][lane] = s;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if (lane < 8) part[g][c] = s;
   __syncthreads();
-  if (g == 0 && n < N) {
-    float r = part[0][lane];
+  if (g == 0) {
+    s = 0.f;
 #pragma unroll
-    for (int k = 1; k < W; ++k) r += part[k][lane];
-    out[n] = r;
+    for (int k = 0; k < W / 4; ++k) s += part[(lane >> 3) * (W / 4) + k][c];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < 8 && n < N) out[n] = s;
   }
 }
 
 inline bool colsum(const float* P, long long rows, int N, float* out, cudaStream_t s) {
-  return pdl_launch(colsum_kernel<>, dim3(unsigned((N + 31) / 32)), 1024, s, P, rows, N, out);
+  return pdl_launch(colsum_kernel<>, dim3(unsigned((N + 7) / 8)), 1024, s, P, rows, N, out);
 }
 
 }  // namespace dsf

@@ -204,93 +204,168 @@ struct LayJob {
   void* dst;
   long long ld, rows, ldd, cols;
 };
+struct LayJobs {
+  LayJob j[3];
+  int b0, b1;  // blocks [0, b0) take job 0, [b0, b1) job 1, the others job 2
+};
+
+// The n (2 or 3) 16-byte vectors that hold the bytes from p on, shifted so that
+// w[0] starts with p's: bytes [p, p + 16 (n - 1)). p is a multiple of ES.
+template <int NV, int ES>
+__device__ __forceinline__ void load_shifted(const uint8_t* p, uint32_t* w) {
+  const uint32_t o = uint32_t(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* q = reinterpret_cast<const uint4*>(p - o);
+  uint32_t v[4 * NV + 4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint4 x = __ldg(q + i);
+    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[4 * NV + i] = 0;
+  if (o & 8u) {
+#pragma unroll
+    for (int i = 0; i < 4 * NV - 2; ++i) v[i] = v[i + 2];
+  }
+  if (o & 4u) {
+#pragma unroll
+    for (int i = 0; i < 4 * NV - 2; ++i) v[i] = v[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * (NV - 1); ++i) w[i] = ES == 4 ? v[i] : __funnelshift_r(v[i], v[i + 1], (o & 3u) * 8u);
+}
 
 template <int ES>  // source element: 4 (fp32 -> three bf16 terms), 2 or 1 (copied)
-__global__ void __launch_bounds__(256) lay_kernel(const LayJob j0, const LayJob j1, const LayJob j2, int b0, int b1) {
+__global__ void __launch_bounds__(256) lay_kernel(const __grid_constant__ LayJobs a) {
   pdl_go();
   pdl_wait();
-  const int blk = int(blockIdx.x), which = blk < b0 ? 0 : (blk < b1 ? 1 : 2);
-  const LayJob& j = which == 0 ? j0 : (which == 1 ? j1 : j2);
-  const int nblk = which == 0 ? b0 : (which == 1 ? b1 - b0 : int(gridDim.x) - b1);
-  const int local = blk - (which == 0 ? 0 : (which == 1 ? b0 : b1));
-  constexpr int V = ES == 1 ? 16 : 8;
-  const long long per_row = j.ldd / V, total = j.rows * per_row;
-  for (long long i = (long long)local * 256 + threadIdx.x; i < total; i += (long long)nblk * 256) {
-    const long long r = i / per_row;
-    const int c = int(i - r * per_row) * V;
-    if constexpr (ES == 4) {
-      const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
-      float x[8];
-      if (c + 8 <= j.cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
-        const float4 p = reinterpret_cast<const float4*>(s)[0], q = reinterpret_cast<const float4*>(s)[1];
-        x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-      } else {
+  const int blk = int(blockIdx.x), which = blk < a.b0 ? 0 : (blk < a.b1 ? 1 : 2);
+  const LayJob& j = a.j[which];  // (indexed in place: a choice among parameters would be copied to the stack)
+  const int first = which == 0 ? 0 : (which == 1 ? a.b0 : a.b1);
+  const int nblk = (which == 0 ? a.b0 : (which == 1 ? a.b1 : int(gridDim.x))) - first, local = blk - first;
+  constexpr int V = ES == 1 ? 16 : 8, NW = V * ES / 4, NV = NW / 4 + 1;  // elements, words, vectors of a piece
+  // a block takes whole rows side by side, or parts of one
+  const int per_row = int(j.ldd / V), tpr = min(per_row, 256), rpb = 256 / tpr;
+  const int rr = int(threadIdx.x) / tpr, c0 = int(threadIdx.x) - rr * tpr;
+  if (rr >= rpb) return;
+  const uint8_t* end = static_cast<const uint8_t*>(j.src) + ((j.rows - 1) * j.ld + j.cols) * ES;
+  for (long long r = (long long)local * rpb + rr; r < j.rows; r += (long long)nblk * rpb)
+   for (int c = c0 * V; c < j.ldd; c += tpr * V) {
+    const uint8_t* s = static_cast<const uint8_t*>(j.src) + (r * j.ld + c) * ES;
+    uint32_t w[NW];
+    // (whole vectors where all of them lie inside the matrix; what a row's last
+    // piece takes from behind the row is never read)
+    if (s - 15 >= static_cast<const uint8_t*>(j.src) && s + 16 * NV <= end) {
+      load_shifted<NV, ES>(s, w);
+    } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = c + k < j.cols ? s[k] : 0.f;
+      for (int k = 0; k < NW; ++k) w[k] = 0;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (c + k >= j.cols) continue;
+        if (ES == 4) w[k * ES / 4] = reinterpret_cast<const uint32_t*>(s)[k];
+        if (ES == 2) w[k * ES / 4] |= uint32_t(reinterpret_cast<const uint16_t*>(s)[k]) << (16 * (k % 2));
+        if (ES == 1) w[k * ES / 4] |= uint32_t(s[k]) << (8 * (k % 4));
       }
+    }
+    if constexpr (ES == 4) {
       uint16_t* d = static_cast<uint16_t*>(j.dst) + r * j.ldd + c;
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(w[k]);
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
-        uint32_t w[4];
+        uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t lo = take_term(x[2 * k]), hi = take_term(x[2 * k + 1]);
-          w[k] = __byte_perm(lo, hi, 0x7632);
+          h[k] = __byte_perm(lo, hi, 0x7632);
         }
-        *reinterpret_cast<uint4*>(d + t * j.rows * j.ldd) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(d + t * j.rows * j.ldd) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     } else {
-      using E = typename std::conditional<ES == 2, uint16_t, uint8_t>::type;
-      const E* s = static_cast<const E*>(j.src) + r * j.ld + c;
-      uint32_t w[4] = {};
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (c + k < j.cols) w[k * ES / 4] |= uint32_t(s[k]) << (8 * ES * (k % (4 / ES)));
-      *reinterpret_cast<uint4*>(static_cast<E*>(j.dst) + r * j.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(j.dst) + (r * j.ldd + c) * ES) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
 bool lay(int dtype, const LayJob* jobs, int n, cudaStream_t s) {
-  LayJob j[3] = {};
+  LayJobs a{};
   int b[3] = {}, tot = 0;
   const int V = dtype == DSF_E4M3 ? 16 : 8;
   for (int i = 0; i < n; ++i) {
-    j[i] = jobs[i];
-    const long long blocks = (jobs[i].rows * (jobs[i].ldd / V) + 255) / 256;
+    a.j[i] = jobs[i];
+    const long long per_row = jobs[i].ldd / V, rpb = per_row < 256 ? 256 / per_row : 1;
+    const long long blocks = (jobs[i].rows + rpb - 1) / rpb;
     b[i] = int(blocks < kSms * 16 ? blocks : kSms * 16);
     tot += b[i];
   }
   if (tot == 0) return true;
   auto* kernel = dtype == DSF_F32 ? lay_kernel<4> : (dtype == DSF_BF16 ? lay_kernel<2> : lay_kernel<1>);
-  return pdl_launch(kernel, dim3(unsigned(tot)), 256, s, j[0], j[1], j[2], b[0], b[0] + b[1]);
+  a.b0 = b[0];
+  a.b1 = b[0] + b[1];
+  return pdl_launch(kernel, dim3(unsigned(tot)), 256, s, a);
 }
 
-// Sums over blocks of 256 rows of a matrix (db where dz is dy): part[block][n].
-constexpr int kSumRows = 256;
-template <class T>
+// Sums over blocks of 128 rows of a matrix (db where dz is dy): part[block][n].
+// VEC: 16 bytes of a row per lane; else one element.
+constexpr int kSumRows = 128;
+template <class T, bool VEC>
 __global__ void __launch_bounds__(256) row_block_sums_kernel(const T* g, long long ld, long long M, int N, float* part) {
-  __shared__ float p[8][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.y * 32 + lane;
+  constexpr int E = VEC ? 16 / int(sizeof(T)) : 1;
+  __shared__ float p[8][32 * E];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n0 = blockIdx.y * 32 * E;
+  const int n = n0 + lane * E;  // (VEC: rows are whole vectors, what they hold past N is not stored)
   const long long r0 = (long long)blockIdx.x * kSumRows;
   pdl_go();
   pdl_wait();
-  float s = 0.f;
+  float s[E] = {};
   if (n < N) {
-#pragma unroll 8
-    for (int i = 0; i < kSumRows / 8; ++i) {
-      const long long r = r0 + w + 8 * i;
-      if (r < M) s += elem(g[r * ld + n]);
+    constexpr int U = 8;  // rows in flight
+#pragma unroll 1
+    for (int i0 = 0; i0 < kSumRows / 8; i0 += U) {
+      const T* q = g + (r0 + w + 8 * i0) * ld + n;
+      if constexpr (VEC) {
+        uint4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          u[i] = r0 + w + 8 * (i0 + i) < M ? __ldg(reinterpret_cast<const uint4*>(q + 8 * i * ld)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float v[E];
+          unpack(u[i], v, T());
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[e] += v[e];
+        }
+      } else {
+        float v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = r0 + w + 8 * (i0 + i) < M ? elem(q[8 * i * ld]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) s[0] += v[i];
+      }
     }
   }
-  p[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && n < N) {
-    float v = p[0][lane];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += p[k][lane];
-    part[(long long)blockIdx.x * N + n] = v;
+  for (int e = 0; e < E; ++e) p[w][lane * E + e] = s[e];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 32 * E; c += 256) {
+    if (n0 + c >= N) break;
+    float v = p[0][c];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += p[k][c];
+    part[(long long)blockIdx.x * N + n0 + c] = v;
   }
+}
+template <class T>
+bool row_block_sums(const void* g, long long ld, bool padded, long long M, int N, float* part, cudaStream_t s) {
+  constexpr int E = 16 / int(sizeof(T));
+  const T* q = static_cast<const T*>(g);
+  const unsigned blocks = unsigned((M + kSumRows - 1) / kSumRows);
+  if (at(g, 16) && (ld * int(sizeof(T))) % 16 == 0 && (N % E == 0 || padded))
+    return pdl_launch(row_block_sums_kernel<T, true>, dim3(blocks, unsigned((N + 32 * E - 1) / (32 * E))), 256, s, q, ld, M,
+                      N, part);
+  return pdl_launch(row_block_sums_kernel<T, false>, dim3(blocks, unsigned((N + 31) / 32)), 256, s, q, ld, M, N, part);
 }
 
 // The end of a split product: the splits' partial sums, added in order, then
@@ -559,11 +634,10 @@ int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void
   } else {
     if (db) {
       const long long blocks = (M + kSumRows - 1) / kSumRows;
-      const dim3 grid{unsigned(blocks), unsigned((c.N + 31) / 32)};
-      const bool ok = f32 ? pdl_launch(row_block_sums_kernel<float>, grid, 256, s, static_cast<const float*>(dy), lddy, M,
-                                       c.N, sums)
-                          : pdl_launch(row_block_sums_kernel<__nv_bfloat16>, grid, 256, s,
-                                       static_cast<const __nv_bfloat16*>(dy), lddy, M, c.N, sums);
+      const bool laid = !f32 && laid_out(l->dtype, c.N) && (dx || dW);  // (the aligned copy of dy)
+      const bool ok = f32    ? row_block_sums<float>(dy, lddy, false, M, c.N, sums, s)
+                      : laid ? row_block_sums<__nv_bfloat16>(c.ws + c.w.gp, c.w.np, true, M, c.N, sums, s)
+                             : row_block_sums<__nv_bfloat16>(dy, lddy, false, M, c.N, sums, s);
       if (!ok || !colsum(sums, blocks, c.N, db, s)) return DSF_ECUDA;
     }
     dz = laid_out(l->dtype, c.N) ? Mat{c.ws + c.w.gp, M, c.N, c.w.np, c.terms, M * c.w.np} : Mat{dy, M, c.N, lddy, 1, 0};
