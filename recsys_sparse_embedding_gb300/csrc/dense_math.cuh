@@ -28,47 +28,69 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
+// Two values at a time: the fp32 pipes take a pair per instruction.
+__device__ __forceinline__ float2 pair(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
 // 1 / (1 + exp(-z)); 0 for z far below zero, 1 far above
-__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.f + exp2_fast(-kLog2e * z)); }
+__device__ __forceinline__ float2 sigmoid(float2 z) {
+  const float2 t = z * pair(-kLog2e);
+  const float2 d = make_float2(exp2_fast(t.x), exp2_fast(t.y)) + pair(1.f);
+  return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+}
 
 // Phi(z), and exp(-z^2 / 2) in e. Below zero Phi is half of erfc itself.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  e = exp2_fast(-kLog2e * (x * x));
-  const float t = rcp_fast(fmaf(0.3275911f, x, 1.f));
-  float s = fmaf(1.061405429f, t, -1.453152027f);
-  s = fmaf(s, t, 1.421413741f);
-  s = fmaf(s, t, -0.284496736f);
-  s = fmaf(s, t, 0.254829592f);
-  const float half = 0.5f * s * t * e;
-  return z < 0.f ? half : 1.f - half;
+__device__ __forceinline__ float2 normal_cdf(float2 z, float2& e) {
+  const float2 x = make_float2(fabsf(z.x), fabsf(z.y)) * pair(0.70710678118654752f);
+  const float2 y = (x * x) * pair(-kLog2e);
+  e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+  const float2 d = __ffma2_rn(pair(0.3275911f), x, pair(1.f));
+  const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+  // (the coefficients halved)
+  float2 s = __ffma2_rn(pair(0.5f * 1.061405429f), t, pair(0.5f * -1.453152027f));
+  s = __ffma2_rn(s, t, pair(0.5f * 1.421413741f));
+  s = __ffma2_rn(s, t, pair(0.5f * -0.284496736f));
+  s = __ffma2_rn(s, t, pair(0.5f * 0.254829592f));
+  const float2 half = (s * t) * e, rest = __ffma2_rn(half, pair(-1.f), pair(1.f));
+  return make_float2(z.x < 0.f ? half.x : rest.x, z.y < 0.f ? half.y : rest.y);
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if (ACT == DSF_ACT_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays)
+__device__ __forceinline__ float2 act_value(float2 z) {
+  if (ACT == DSF_ACT_RELU) return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);  // (a NaN stays)
   if (ACT == DSF_ACT_SILU) return z * sigmoid(z);
   if (ACT == DSF_ACT_GELU) {
-    float e;
+    float2 e;
     return z * normal_cdf(z, e);
   }
   return z;
 }
-
-// act(z) and act'(z) together
 template <int ACT>
-__device__ __forceinline__ float2 act_both(float z) {
-  if (ACT == DSF_ACT_RELU) return z > 0.f ? make_float2(z, 1.f) : make_float2(z < 0.f ? 0.f : z, z != z ? z : 0.f);
+__device__ __forceinline__ float act_value(float z) {
+  return act_value<ACT>(pair(z)).x;
+}
+
+// act(z) in value, act'(z) in slope
+template <int ACT>
+__device__ __forceinline__ void act_both(float2 z, float2& value, float2& slope) {
+  value = z;
+  slope = pair(1.f);
+  if (ACT == DSF_ACT_RELU) {
+    value = act_value<ACT>(z);
+    slope = make_float2(z.x > 0.f ? 1.f : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? 1.f : (z.y != z.y ? z.y : 0.f));
+  }
   if (ACT == DSF_ACT_SILU) {
-    const float p = sigmoid(z);
-    return make_float2(z * p, p * fmaf(z, 1.f - p, 1.f));
+    const float2 p = sigmoid(z);
+    value = z * p;
+    slope = p * __ffma2_rn(z, __ffma2_rn(p, pair(-1.f), pair(1.f)), pair(1.f));
   }
   if (ACT == DSF_ACT_GELU) {
-    float e;
-    const float cdf = normal_cdf(z, e);
-    return make_float2(z * cdf, fmaf(z, 0.3989422804014327f * e, cdf));
+    float2 e;
+    const float2 cdf = normal_cdf(z, e);
+    value = z * cdf;
+    slope = __ffma2_rn(z * pair(0.3989422804014327f), e, cdf);
   }
-  return make_float2(z, 1.f);
 }
 
 }  // namespace dsf

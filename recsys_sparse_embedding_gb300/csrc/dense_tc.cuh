@@ -756,38 +756,33 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
                 if (PAIR) w[PAIR ? k : 0] *= xs * __shfl_sync(0xffffffffu, wsu, j + k);
               }
             }
-            if (S::BIAS) {
-#pragma unroll
-              for (int k = 0; k < 8; k += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(wbias + j + k);
-                v[k] += b.x, v[k + 1] += b.y, v[k + 2] += b.z, v[k + 3] += b.w;
-                if (PAIR && S::BIAS_N == 64) {
-                  const float4 d = *reinterpret_cast<const float4*>(wbias + 32 + j + k);
-                  w[PAIR ? k : 0] += d.x, w[PAIR ? k + 1 : 0] += d.y, w[PAIR ? k + 2 : 0] += d.z, w[PAIR ? k + 3 : 0] += d.w;
-                }
-              }
-              if (PAIR && S::BIAS_N == 32) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[PAIR ? k : 0] += __shfl_sync(0xffffffffu, bu, j + k);
-              }
-            }
             float x[8];
             if (IN) get8(j, x);
-            if (FWD) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                v[k] = act_value<ACT>(v[k]);
-                if (PAIR) v[k] *= w[PAIR ? k : 0];
-                if (EPI == kEpiRes) v[k] += x[k];
+            for (int k = 0; k < 8; k += 2) {
+              if (!S::BIAS) continue;
+              float2 z = make_float2(v[k], v[k + 1]) + *reinterpret_cast<const float2*>(wbias + j + k);
+              float2 y = pair(0.f);
+              if (PAIR) {
+                y = make_float2(w[PAIR ? k : 0], w[PAIR ? k + 1 : 0]);
+                if (S::BIAS_N == 64)
+                  y = y + *reinterpret_cast<const float2*>(wbias + 32 + j + k);
+                else
+                  y = y + make_float2(__shfl_sync(0xffffffffu, bu, j + k), __shfl_sync(0xffffffffu, bu, j + k + 1));
               }
-            }
-            if (EPI == kEpiDz) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 f = act_both<ACT>(v[k]);
-                v[k] = (PAIR ? x[k] * w[PAIR ? k : 0] : x[k]) * f.y;
-                if (PAIR) w[PAIR ? k : 0] = x[k] * f.x;
+              const float2 in2 = make_float2(x[k], x[k + 1]);
+              if (FWD) {
+                z = act_value<ACT>(z);
+                if (PAIR) z = z * y;
+                if (EPI == kEpiRes) z = z + in2;
+              } else {
+                float2 value, slope;
+                act_both<ACT>(z, value, slope);
+                z = (PAIR ? in2 * y : in2) * slope;
+                if (PAIR) y = in2 * value;
               }
+              v[k] = z.x, v[k + 1] = z.y;
+              if (PAIR) w[PAIR ? k : 0] = y.x, w[PAIR ? k + 1 : 0] = y.y;
             }
             if (DUAL && EPI == kEpiPart && !F32 && t.job) put8_bf16(j, v);
             else if (!TERMS_OUT) put8(j, v);
