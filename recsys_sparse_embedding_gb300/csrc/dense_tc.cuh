@@ -758,15 +758,22 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             }
             float x[8];
             if (IN) get8(j, x);
+            float b[8], d[8];  // (16 bytes a time: shared memory is what the MMAs run on)
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+              if (S::BIAS) *reinterpret_cast<float4*>(b + k) = *reinterpret_cast<const float4*>(wbias + j + k);
+              if (PAIR && S::BIAS_N == 64)
+                *reinterpret_cast<float4*>(d + k) = *reinterpret_cast<const float4*>(wbias + 32 + j + k);
+            }
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
               if (!S::BIAS) continue;
-              float2 z = make_float2(v[k], v[k + 1]) + *reinterpret_cast<const float2*>(wbias + j + k);
+              float2 z = make_float2(v[k], v[k + 1]) + make_float2(b[k], b[k + 1]);
               float2 y = pair(0.f);
               if (PAIR) {
                 y = make_float2(w[PAIR ? k : 0], w[PAIR ? k + 1 : 0]);
                 if (S::BIAS_N == 64)
-                  y = y + *reinterpret_cast<const float2*>(wbias + 32 + j + k);
+                  y = y + make_float2(d[k], d[k + 1]);
                 else
                   y = y + make_float2(__shfl_sync(0xffffffffu, bu, j + k), __shfl_sync(0xffffffffu, bu, j + k + 1));
               }
