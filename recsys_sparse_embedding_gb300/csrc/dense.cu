@@ -529,6 +529,7 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.a.ws = l->scale;
   p.a.status = c.status;
   p.a.part = sums;
+  p.a.grow = 1.f + 0.5f * float(4 * nkb) / float(1 << 25);  // (four additions per K-block)
   if (o.splits > 1) {
     set_part(p, c);
   } else {

@@ -129,3 +129,15 @@ def test_norm_refusals(L):
     assert bwd(dw=4096) == B.DSF_EWORKSPACE
     assert bwd(dw=4096, ws=4096 + 64, nb=need) == B.DSF_EWORKSPACE
     assert bwd(dw=4096, ws=4096, nb=need - 1) == B.DSF_EWORKSPACE
+
+
+@pytest.mark.parametrize("dtype", [B.DSF_F32, B.DSF_BF16, B.DSF_E4M3])
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("R,K", [(2, 1), (128, 256), (1366, 256), (300, 45), (8192, 4096)])
+def test_workspace_grows_with_the_rows(L, dtype, gated, R, K):
+    """A workspace for M rows serves every call of fewer."""
+    l = layer(dtype=dtype, R=R, K=K, ldw=K, scale=4096 if dtype == B.DSF_E4M3 else None)
+    for back in (0, 1) if dtype != B.DSF_E4M3 else (0,):
+        sizes = [L.dsf_dense_workspace_bytes(P(l), M, gated, back) for M in
+                 (0, 1, 8, 9, 31, 32, 33, 100, 127, 128, 129, 255, 257, 1000, 4096, 10001, 65536, 1 << 20)]
+        assert sizes == sorted(sizes) and sizes[0] > 0

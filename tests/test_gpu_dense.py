@@ -1,5 +1,7 @@
 """The dense layer, the gated layer and the RMS norm against 64-bit
 evaluations (tests/dense_ref.py has the bounds), through the C ABI."""
+import math
+
 import pytest
 import torch
 
@@ -59,7 +61,9 @@ def x_of(g, dtype, M, K):
 
 SIZES = [(1, 1, 1), (1, 256, 512), (2, 16, 8), (3, 37, 5), (8, 1024, 96), (9, 64, 300), (17, 176, 64), (64, 640, 33),
          (127, 64, 129), (128, 128, 128), (129, 200, 257), (256, 512, 256), (300, 1000, 96), (513, 48, 1040),
-         (1000, 513, 300), (2049, 256, 512), (385, 2100, 700)]
+         (1000, 513, 300), (2049, 256, 512), (385, 2100, 700),
+         # past the sizes that a few CUDA cores do: whole, ragged and odd tiles of each configuration
+         (129, 520, 600), (257, 1000, 333), (70, 2100, 1030), (2000, 96, 200), (4097, 160, 129), (640, 2048, 264)]
 ACT_OF = ["none", "relu", "silu", "gelu"]
 
 
@@ -322,6 +326,155 @@ def test_captured_and_replayed(dtype, M):
         torch.cuda.synchronize()
         for a, b in zip(eager[:4], graphed[:4]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_larger_workspace_serves_fewer_rows(gated):
+    """One workspace for up to 3000 rows, dirty, used for calls of fewer rows."""
+    g = gen(21)
+    K, N = 136, 120
+    layer = layer_of(g, BF16, 2 * N if gated else N, K, "silu")
+    ws = B.DenseWorkspace(layer, 3000, gated=gated, backward=True)
+    ws.buf.fill_(0xff)
+    for M in (3000, 1, 257, 2000, 9):
+        x, dy = rnd(g, M, K).to(BF16), rnd(g, M, N).to(BF16)
+        y = torch.empty(M, N, dtype=BF16, device="cuda")
+        out = dict(dx=torch.empty_like(x), dW=torch.empty_like(layer.W), db=torch.empty(layer.R, device="cuda"))
+        if gated:
+            B.ctr_glu_fwd(layer, x, y, ws)
+            B.ctr_glu_bwd(layer, x, dy, ws, **out)
+            ref, tol = R.glu(x, layer.W, layer.bias, "silu", BF16)
+        else:
+            B.ctr_dense_fwd(layer, x, y, ws)
+            B.ctr_dense_bwd(layer, x, dy, ws, **out)
+            ref, tol = R.dense(x, layer.W, layer.bias, "silu", None, BF16)
+        R.assert_within(y, ref, tol, "y, M = %d" % M)
+        check_bwd(layer, x, dy, "silu", gated, out)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_gradients_against_differences(gated, act):
+    """The change of a weighted sum of the outputs along a random direction of
+    (x, W, b), by central differences of the forward call in fp32. The
+    difference's own error: h^2 / 6 times a third derivative, estimated as
+    four thirds of what halving h changes in 64 bits (twice that is allowed),
+    and the outputs' roundings over h. Those are sums of their own, each of
+    which stays within its bound and, rounded to nearest, falls to either side
+    alike: their weighted sum has a standard deviation of at most the root of
+    the squared bounds' sum, and six of it are allowed."""
+    g = gen(31)
+    M, K, N, h = 40, 48, 32, 2.0 ** -6
+    rows = 2 * N if gated else N
+    x, W, b = rnd(g, M, K), rnd(g, rows, K, std=0.2), rnd(g, rows, std=0.3)
+    vx, vW, vb, c = rnd(g, M, K), rnd(g, rows, K, std=0.2), rnd(g, rows), rnd(g, M, N)
+    layer = B.DenseLayer(W, b, act=R.ACTS[act])
+    out = run_bwd(layer, x, c, gated, dx=torch.empty_like(x), dW=torch.empty_like(W), db=torch.empty_like(b))
+    slope = sum(float((out[n].double() * v.double()).sum()) for n, v in (("dx", vx), ("dW", vW), ("db", vb)))
+    noise = 0.0
+
+    def at(t, exact):
+        nonlocal noise
+        xt, Wt, bt = x + t * vx, W + t * vW, b + t * vb
+        ref, tol = R.glu(xt, Wt, bt, act, F32) if gated else R.dense(xt, Wt, bt, act, None, F32)
+        if exact:
+            return float((ref * c.double()).sum())
+        noise = math.hypot(noise, 6 * float((tol * c.double()).norm()) / (2 * h))
+        y = torch.empty(M, N, device="cuda")
+        at_t = B.DenseLayer(Wt, bt, act=R.ACTS[act])
+        (B.ctr_glu_fwd if gated else B.ctr_dense_fwd)(at_t, xt, y, B.DenseWorkspace(at_t, M, gated=gated))
+        return float((y.double() * c.double()).sum())
+
+    def diff(h, exact):
+        return (at(h, exact) - at(-h, exact)) / (2 * h)
+
+    got, d1, d2 = diff(h, False), diff(h, True), diff(h / 2, True)
+    assert abs(got - slope) <= 2 * 4 / 3 * abs(d1 - d2) + noise, (got, slope, d1, d2, noise)
+    # (the comparison says something: a slope along a random direction is of this size)
+    size = math.sqrt(sum(float((out[n].double() * v.double()).square().sum())
+                         for n, v in (("dx", vx), ("dW", vW), ("db", vb))))
+    assert noise < 0.1 * size, (noise, size)
+
+
+@pytest.mark.parametrize("wl", ["taobao", "long_multihot"])
+def test_a_tower_block_trained_after_the_sparse_path(wl):
+    """The operators as they are used: din_sparse_fwd's pooled rows normed,
+    through a gated layer and a dense layer back with the residual, normed to 8
+    bits into an e4m3 layer for serving; and for training a dense layer to the
+    logit, with every gradient back to the pooled rows, which din_sparse_bwd
+    takes. Each call against 64 bits on its own inputs; dpooled against 64-bit
+    autograd of the whole tower. There about ten values on the way are rounded
+    to bf16, each within 2^-8 / sqrt 3 in the mean: sqrt(10) of that is 7e-3,
+    and 2e-2 is allowed."""
+    from helpers import DeviceRun
+    from recsys_sparse_embedding_gb300 import synth
+    batch = synth.generate(wl, seed=4, B=600, nonzero_bias=True)
+    run = DeviceRun(batch)
+    db = run.db
+    mlp = db.mlp(B.DSF_MODE_BF16_TC)
+    run.ws.prepare(mlp)
+    M, D, F = batch.B, 256, 688
+    pooled, din = torch.empty(M, D, device="cuda"), torch.empty(M, 48, device="cuda")
+    B.din_sparse_fwd(db.tables, db.values, db.lengths, db.seq_values, db.seq_lengths, db.max_len, db.q_feat,
+                     db.seq_table, M, mlp, pooled, din, run.ws, status=run.status)
+    g = gen(77)
+    w = 1 + 0.2 * rnd(g, D)
+    up, down = layer_of(g, BF16, 2 * F, D, "silu"), layer_of(g, BF16, D, F, "none")
+    head = layer_of(g, BF16, 1, D, "none")
+    new = lambda *s, dt=BF16: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    res = pooled.to(BF16)
+    n, hid, y, logit = new(M, D), new(M, F), new(M, D), new(M, 1)
+    ws = [B.DenseWorkspace(up, M, gated=True, backward=True), B.DenseWorkspace(down, M, backward=True),
+          B.DenseWorkspace(head, M, backward=True)]
+    B.ctr_rms_norm_fwd(pooled, n, weight=w)
+    B.ctr_glu_fwd(up, n, hid, ws[0], status=run.status)
+    B.ctr_dense_fwd(down, hid, y, ws[1], residual=res, status=run.status)
+    B.ctr_dense_fwd(head, y, logit, ws[2], status=run.status)
+    ref, _ = R.norm(pooled, w, 1e-6)
+    R.assert_within(n, ref, (D + 8) * R.U * ref.abs() + 2.0 ** -8 * ref.abs() * 1.001 + 1e-38, "norm")
+    for got, (want, tol) in ((hid, R.glu(n, up.W, up.bias, "silu", BF16)),
+                             (y, R.dense(hid, down.W, down.bias, "none", res, BF16)),
+                             (logit, R.dense(y, head.W, head.bias, "none", None, BF16))):
+        R.assert_within(got, want, tol, "layer")
+    # serving: the sum of two blocks normed into 8 bits, and an e4m3 layer
+    q, qs, s = torch.empty(M, D, device="cuda").to(E4M3), new(M, dt=F32), new(M, D)
+    B.ctr_rms_norm_fwd(y, q, weight=w, residual=res, sum_out=s, y_scale=qs)
+    e8 = layer_of(g, E4M3, 520, D, "gelu")
+    z = new(M, 520)
+    B.ctr_dense_fwd(e8, q, z, B.DenseWorkspace(e8, M), x_scale=qs, status=run.status)
+    want, tol = R.dense(q, e8.W, e8.bias, "gelu", None, BF16, qs, e8.scale)
+    R.assert_within(z, want, tol, "e4m3 layer")
+    # training: back to the pooled rows
+    dlogit = rnd(g, M, 1, std=0.1).to(BF16)
+    dy, dhid, dn, dpooled = new(M, D), new(M, F), new(M, D), new(M, D, dt=F32)
+    grads = [dict(dW=torch.empty_like(l.W), db=torch.empty_like(l.bias)) for l in (up, down, head)]
+    dw = torch.empty_like(w)
+    B.ctr_dense_bwd(head, y, dlogit, ws[2], dx=dy, status=run.status, **grads[2])
+    B.ctr_dense_bwd(down, hid, dy, ws[1], dx=dhid, status=run.status, **grads[1])
+    B.ctr_glu_bwd(up, n, dhid, ws[0], dx=dn, status=run.status, **grads[0])
+    B.ctr_rms_norm_bwd(dn, pooled, dpooled, weight=w, dsum=dy.float(), dweight=dw, workspace=B.RmsNormWorkspace(M, D))
+    for layer, x, d, gated, got, dx in ((up, n, dhid, True, grads[0], dn), (down, hid, dy, False, grads[1], dhid),
+                                        (head, y, dlogit, False, grads[2], dy)):
+        check_bwd(layer, x, d, "silu" if gated else "none", gated, dict(got, dx=dx))
+    leaf = pooled.double().requires_grad_()
+    t = leaf * w.double() / torch.sqrt(leaf.square().mean(1, keepdim=True) + 1e-6)
+    zz = t @ up.W.double().t() + up.bias.double()
+    t = torch.nn.functional.silu(zz[:, :F]) * zz[:, F:] @ down.W.double().t() + down.bias.double() + leaf
+    t = t @ head.W.double().t() + head.bias.double()
+    want, = torch.autograd.grad(t, leaf, dlogit.double())
+    R.assert_norm(dpooled, want, 2e-2, "dpooled", M)
+    state = B.SparseState(db.tables, batch.values.size + 3 * batch.seq_values.shape[1])
+    bws = B.BwdWorkspace(M, batch.values.size, batch.seq_values.shape[1], batch.D)
+    B.din_sparse_bwd(db.tables, db.values, db.lengths, db.seq_values, db.seq_lengths, db.max_len, db.q_feat,
+                     db.seq_table, M, mlp, pooled, dpooled, torch.zeros(M, 48, device="cuda"), B.MlpGrads(batch.D),
+                     state, bws, status=run.status)
+    torch.cuda.synchronize()
+    assert int(run.status.item()) == 0
+    # feature 0's rows take their samples' slice of dpooled, summed
+    f0 = state.grad[0].double().sum(0)
+    lengths = torch.from_numpy(batch.lengths.reshape(batch.F, M)[0].astype("int64")).cuda()
+    want = (dpooled[:, :16].double() * lengths[:, None]).sum(0)
+    assert ((f0 - want).abs() <= 1e-5 * dpooled[:, :16].double().abs().mul(lengths[:, None]).sum(0) + 1e-6).all()
 
 
 # ------------------------------------------------------------------ RMS norm
