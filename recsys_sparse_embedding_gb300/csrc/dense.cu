@@ -607,7 +607,7 @@ int fwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const floa
   bool ok;
   if (small_call(l->dtype, M, l->R, l->K)) {
     const int N = gated ? l->R / 2 : l->R;
-    const SmallArgs a{x, l->W, ldx, l->ldw, l->bias, xs, l->scale, res, ldr, y, ldy, int(M), N, l->K, l->act};
+    const SmallArgs a{x, l->W, ldx, l->ldw, l->bias, xs, l->scale, res, ldr, y, ldy, int(M), N, l->K, l->act, 0};
     const bool vec = (l->K * esize(l->dtype)) % 16 == 0;
     ok = l->dtype == DSF_F32    ? launch_small<float, float>(a, gated, vec, s)
          : l->dtype == DSF_BF16 ? launch_small<__nv_bfloat16, __nv_bfloat16>(a, gated, vec, s)

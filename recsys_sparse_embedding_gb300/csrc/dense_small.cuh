@@ -6,7 +6,7 @@
 // tile would use 8 of its 128 rows. A warp takes one output column (a gated
 // layer: its gate and up rows), its lanes side by side along K in 16-byte
 // vectors, several in flight; x (a few KB) stays in L1. More than 8 rows go by
-// eights in blockIdx.y. fp32 sums, then
+// eights. fp32 sums, then
 // the operator's epilogue in the lane of each row.
 #pragma once
 #include <cuda_bf16.h>
@@ -30,6 +30,7 @@ struct SmallArgs {
   void* y;
   long long ldy;
   int M, N, K, act;
+  int col_blocks;  // blocks per 8 rows (set by the launch)
 };
 
 __device__ __forceinline__ float act_any(int act, float z) {
@@ -80,14 +81,15 @@ __global__ void __launch_bounds__(256) small_kernel(const SmallArgs a) {
   constexpr int E = VEC ? 16 / int(sizeof(T)) : 1;
   // vectors (or elements) of each row per lane and step (ONE: a row is one step of 32 lanes)
   constexpr int U = VEC ? (ONE ? 1 : (R >= 4 ? 2 : 4)) : 4;
-  const int lane = threadIdx.x & 31, n0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * NC;
+  const int chunk = int(blockIdx.x) / a.col_blocks, n_blk = int(blockIdx.x) - chunk * a.col_blocks;
+  const int lane = threadIdx.x & 31, n0 = (n_blk * 8 + int(threadIdx.x >> 5)) * NC;
   pdl_go();
   pdl_wait();
   if (n0 >= a.N) return;
-  const int m0 = int(blockIdx.y) * MT, rows = min(MT, a.M - m0);
+  const int m0 = chunk * MT, rows = min(MT, a.M - m0);
   const T* x[MT];  // (rows past the last read the last one)
 #pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = static_cast<const T*>(a.x) + (m0 + min(m, rows - 1)) * a.ldx;
+  for (int m = 0; m < MT; ++m) x[m] = static_cast<const T*>(a.x) + (long long)(m0 + min(m, rows - 1)) * a.ldx;
   const T* w[R];
 #pragma unroll
   for (int c = 0; c < R; ++c)  // (columns past the last read the last one's weights)
@@ -170,8 +172,9 @@ __global__ void __launch_bounds__(256) small_kernel(const SmallArgs a) {
 }
 
 template <class T, class TO, int MT, int NC, bool GATED>
-bool launch_small_v(const SmallArgs& a, bool vec, cudaStream_t s) {
-  const dim3 grid(unsigned((a.N + 8 * NC - 1) / (8 * NC)), unsigned((a.M + MT - 1) / MT));
+bool launch_small_v(SmallArgs a, bool vec, cudaStream_t s) {
+  a.col_blocks = (a.N + 8 * NC - 1) / (8 * NC);
+  const dim3 grid(unsigned(a.col_blocks) * unsigned((a.M + MT - 1) / MT));
   if (!vec) return pdl_launch(small_kernel<T, TO, MT, NC, GATED, false, false>, grid, 256, s, a);
   return a.K * int(sizeof(T)) <= 512 ? pdl_launch(small_kernel<T, TO, MT, NC, GATED, true, true>, grid, 256, s, a)
                                      : pdl_launch(small_kernel<T, TO, MT, NC, GATED, true, false>, grid, 256, s, a);
@@ -192,8 +195,8 @@ inline int small_columns(const SmallArgs& a) {
 // and 4.7; fp32 33.6 M 9.7 and 9.8, 67 M 11.5 to 16.9 and 10.2 to 13.1; e4m3
 // 8.4 M 3.1 and 4.1, 16.8 M 5.5 and 4.3.
 inline bool small_call(int dtype, long long M, int R, int K) {
-  const long long most = dtype == DSF_F32 ? 1 << 25 : (dtype == DSF_BF16 ? 1 << 24 : 1 << 23);
-  return M <= kSmallM || M * R * K <= most;
+  const double most = dtype == DSF_F32 ? 1 << 25 : (dtype == DSF_BF16 ? 1 << 24 : 1 << 23);
+  return M <= kSmallM || double(M) * R * K <= most;
 }
 template <class T, class TO, bool GATED>
 bool launch_small_g(const SmallArgs& a, bool vec, cudaStream_t s) {

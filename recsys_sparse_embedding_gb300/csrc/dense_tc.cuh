@@ -42,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   } else if (warp == S::kMma) {
     // ------------------------------------------------ MMAs (one thread of the cluster)
     if (lane == 0 && rank == 0) {
+      pdl_wait();  // (its waits are bounded, what the stream does before is not)
       constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (BMN ? 1u << 16 : 0u) |
                               (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
       uint32_t run = 0, st = 0, phase = 0;  // the next stage, and its barrier's phase
@@ -973,7 +975,7 @@ template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
 bool launch_tc(const Product& p, cudaStream_t s) {
   using S = Shape<CG, BN, MAJOR, GATED, EPI, F32>;
   auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32>;
-  static int grid_max[64] = {};  // (host threads may race on it: each computes the same value)
+  static std::atomic<int> grid_max[64];  // (host threads may race on it: each computes the same value)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   cudaLaunchConfig_t cfg = {};
@@ -989,7 +991,8 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  if (grid_max[dev] == 0) {
+  int most = grid_max[dev].load(std::memory_order_acquire);
+  if (most == 0) {
     int sms = 0, n = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -997,10 +1000,11 @@ bool launch_tc(const Product& p, cudaStream_t s) {
     if (CG == 2) {
       cfg.gridDim = dim3(unsigned(sms / 2 * 2));
       if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return false;
-      grid_max[dev] = 2 * n;
+      most = 2 * n;
     } else {
-      grid_max[dev] = sms;
+      most = sms;
     }
+    grid_max[dev].store(most, std::memory_order_release);
   }
   TcArgs a = p.a;
   long long n[2] = {0, 0};  // units
@@ -1013,7 +1017,7 @@ bool launch_tc(const Product& p, cudaStream_t s) {
     o.by_group = make_div(8u * uint32_t(o.nt));
     o.by_last = make_div(o.mt % 8 ? uint32_t(o.mt % 8) : 8u);
   }
-  const long long want = (n[0] + n[1]) * CG, g = want < grid_max[dev] ? want : grid_max[dev];
+  const long long want = (n[0] + n[1]) * CG, g = want < most ? want : most;
   if (MAJOR == kDual) {
     const Deal d = deal(a, p.weight, g / CG);
     a.first = d.first;

@@ -259,6 +259,34 @@ def test_extreme_fp32_values():
     assert not y[4:].any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_rows_of_a_tiny_layer(dtype):
+    """More rows than a grid's second dimension counts, one weight."""
+    M, g = 600001, gen(6)
+    layer = layer_of(g, dtype, 1, 1, "gelu")
+    x = rnd(g, M, 1).to(dtype)
+    y = torch.empty(M, 1, dtype=dtype, device="cuda")
+    B.ctr_dense_fwd(layer, x, y, B.DenseWorkspace(layer, M))
+    ref, tol = R.dense(x, layer.W, layer.bias, "gelu", None, dtype)
+    R.assert_within(y, ref, tol, "y")
+    out = run_bwd(layer, x, y, False, dx=torch.empty_like(x), dW=torch.empty_like(layer.W),
+                  db=torch.empty(1, device="cuda"))
+    check_bwd(layer, x, y, "gelu", False, out)
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_widest_layers(M):
+    """A layer of 2^20 outputs and one of 2^20 inputs (the largest there are)."""
+    g = gen(8)
+    for N, K in ((1 << 20, 8), (24, 1 << 20)):
+        layer = layer_of(g, BF16, N, K, "relu")
+        x = rnd(g, M, K).to(BF16)
+        y = torch.empty(M, N, dtype=BF16, device="cuda")
+        B.ctr_dense_fwd(layer, x, y, B.DenseWorkspace(layer, M))
+        ref, tol = R.dense(x, layer.W, layer.bias, "relu", None, BF16)
+        R.assert_within(y, ref, tol, "y")
+
+
 def test_offsets_past_32_bits():
     """An output of more than 2^31 elements; the rows around that offset and
     the last ones are checked."""
