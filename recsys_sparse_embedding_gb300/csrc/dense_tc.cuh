@@ -247,31 +247,27 @@ __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // The leading 8 significant bits of x, as bf16 bits in the upper half of the
-// word; x becomes what is left. A non-finite x leaves 0 (a NaN stays one).
+// word; x becomes what is left (of a non-finite x, a NaN).
 __device__ __forceinline__ uint32_t take_term(float& x) {
-  const uint32_t u = __float_as_uint(x);
-  if ((u & 0x7f800000u) == 0x7f800000u) {
-    x = 0.f;
-    return u & 0x007fffffu ? 0x7fc00000u : u;
-  }
-  const uint32_t h = u & 0xffff0000u;
+  const uint32_t h = __float_as_uint(x) & 0xffff0000u;
   x -= __uint_as_float(h);
   return h;
 }
 
 // sums of 32 columns over a warp's 32 rows (one row per lane): lane l returns
 // column l's. Each step halves the columns a lane holds.
-__device__ __forceinline__ float column_sum(float* v, int lane) {
+__device__ __forceinline__ float column_sum(const float* v, int lane) {
+  float t[16];
 #pragma unroll
   for (int w = 16; w; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
-      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+      const float lo = w == 16 ? v[i] : t[i], hi = w == 16 ? v[i + 16] : t[(i + w) & 15];
+      t[i] = (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, w);
     }
   }
-  return v[0];
+  return t[0];
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
@@ -815,7 +811,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         } else {
           math(std::integral_constant<int, DSF_ACT_NONE>{});
         }
-        auto sums = [&](float* v, int half) {  // (takes v apart)
+        auto sums = [&](const float* v, int half) {
           const float s = column_sum(v, lane);
           if (col0 + lane < jb.N) a.part[((long long)(row0 >> 5) * halves + half) * jb.N + col0 + lane] = s;
         };
@@ -824,12 +820,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
 #pragma unroll
           for (int h = 0; h < halves; ++h) {
             float* v = h ? up : g;
-            if (a.part) {
-              float s[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] = v[k];
-              sums(s, h);
-            }
+            if (a.part) sums(v, h);
             __syncwarp();  // (the input is read, or the last term gone, before the buffer is written)
 #pragma unroll
             for (int term = 0; term < 3; ++term) {
