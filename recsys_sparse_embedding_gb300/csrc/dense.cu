@@ -307,9 +307,10 @@ bool lay(int dtype, const LayJob* jobs, int n, cudaStream_t s) {
   return pdl_launch(kernel, dim3(unsigned(tot)), 256, s, a);
 }
 
-// Sums over blocks of 128 rows of a matrix (db where dz is dy): part[block][n].
-// VEC: 16 bytes of a row per lane; else one element.
-constexpr int kSumRows = 128;
+// Sums over blocks of 32 rows of a matrix (db where dz is dy): part[block][n].
+// VEC: 16 bytes of a row per lane; else one element. (8192 x 1024 in bf16 with
+// the sum over blocks: 5.1 us; 6.5 with 64 rows, 7.7 with 128.)
+constexpr int kSumRows = 32;
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) row_block_sums_kernel(const T* g, long long ld, long long M, int N, float* part) {
   constexpr int E = VEC ? 16 / int(sizeof(T)) : 1;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(256) row_block_sums_kernel(const T* g, long lo
   pdl_wait();
   float s[E] = {};
   if (n < N) {
-    constexpr int U = 8;  // rows in flight
+    constexpr int U = 4;  // rows in flight
 #pragma unroll 1
     for (int i0 = 0; i0 < kSumRows / 8; i0 += U) {
       const T* q = g + (r0 + w + 8 * i0) * ld + n;
@@ -625,7 +626,7 @@ int bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const void
   const bool f32 = l->dtype == DSF_F32, own_dz = gated || l->act != DSF_ACT_NONE;
   float* sums = reinterpret_cast<float*>(c.ws + c.w.sums);
   if (!dx && !dW && !db) return DSF_OK;
-  if (!lay_operands(c, x, ldx, own_dz || (!dx && !dW) ? nullptr : dy, lddy)) return DSF_ECUDA;
+  if ((own_dz || dx || dW) && !lay_operands(c, x, ldx, own_dz ? nullptr : dy, lddy)) return DSF_ECUDA;
   Mat dz;
   if (own_dz) {
     void* d = c.ws + c.w.dz;

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kMaxN = 32768;
 constexpr int kBlock = 256;          // threads per block (a wider group is its own block)
-constexpr int kMaxPartials = 152 * 4;  // blocks of the backward, each with one row of weight-gradient sums
+constexpr int kSms = 152;
 constexpr float kE4m3Max = 448.f;
 
 struct FwdArgs {
@@ -158,6 +158,29 @@ __device__ __forceinline__ float group_reduce(float v, float* buf) {
   return v;
 }
 
+// Two sums at once.
+template <int G>
+__device__ __forceinline__ void group_reduce2(float& a, float& b, float* buf_a, float* buf_b) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (G == 32) return;
+  if ((threadIdx.x & 31) == 0) {
+    buf_a[threadIdx.x >> 5] = a;
+    buf_b[threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  a = buf_a[0];
+  b = buf_b[0];
+#pragma unroll
+  for (int k = 1; k < G / 32; ++k) {
+    a += buf_a[k];
+    b += buf_b[k];
+  }
+}
+
 template <class TX, class TY, int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdArgs a) {
   constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
@@ -224,12 +247,78 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdA
   for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(y, i, t, a.N, s[i]);
 }
 
+// A set of 8 elements as it is stored: two per register in bf16.
+template <class T>
+struct Pack {
+  uint32_t w[2 * sizeof(T)];
+};
+__device__ __forceinline__ void open(const Pack<float>& p, float* v) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(p.w[k]);
+}
+__device__ __forceinline__ void open(const Pack<__nv_bfloat16>& p, float* v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(p.w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(p.w[k] & 0xffff0000u);
+  }
+}
+template <bool ALIGNED, int G, class T>
+__device__ __forceinline__ void load_pack(const T* row, int i, int t, int N, Pack<T>& p) {
+  constexpr int W = 2 * int(sizeof(T));
+#pragma unroll
+  for (int k = 0; k < W; ++k) p.w[k] = 0;
+  if (ALIGNED) {
+    const int e = 8 * (t + i * G);
+    if (e < N) {
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k) {
+        const uint4 u = reinterpret_cast<const uint4*>(row + e)[k];
+        p.w[4 * k] = u.x, p.w[4 * k + 1] = u.y, p.w[4 * k + 2] = u.z, p.w[4 * k + 3] = u.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = (8 * i + j) * G + t;
+      const uint32_t u = e < N ? __float_as_uint(to_f(row[e])) : 0u;
+      if (sizeof(T) == 4) p.w[j % W] = u;
+      else p.w[j / 2] |= j & 1 ? u : u >> 16;
+    }
+  }
+}
+template <bool ALIGNED, int G>
+__device__ __forceinline__ void load_weight(const float* w, int i, int t, int N, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = w ? 0.f : 1.f;
+  if (!w) return;
+  if (ALIGNED) {
+    const int e = 8 * (t + i * G);
+    if (e >= N) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + e) + k);
+      v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = x.z, v[4 * k + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = (8 * i + j) * G + t;
+      if (e < N) v[j] = __ldg(w + e);
+    }
+  }
+}
+
 // dx = r (g - s r^2 mean(g s)) + dsum with g = dy w and r = 1 / sqrt(mean(s^2)
-// + eps): both row sums come from one reading of s and dy. Blocks walk the
-// rows, so that a thread's weight-gradient sums (dy s r of its columns) stay
-// in registers over all of them; a block then writes one row of partial sums.
+// + eps): both row sums come from one reading of s and dy, which wait in
+// registers as they are stored (the weight is read twice, from L1). Blocks
+// walk the rows, so that a thread's weight-gradient sums (dy s r of its
+// columns) stay in registers over all of them; a block then writes one row of
+// partial sums. Two blocks of 256 threads per SM, 128 registers each: with the
+// operands held as fp32 it was one, and 65536 x 1024 in bf16 took 99 us where
+// HBM needs 59.
 template <class TY, class TX, int G, int V, bool ALIGNED>
-__global__ void __launch_bounds__(G > kBlock ? G : kBlock) bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(G > kBlock ? G : kBlock, G > kBlock ? 1 : 2) bwd_kernel(const BwdArgs a) {
   constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
   __shared__ float buf[2][2][32];
   __shared__ float wsum[G == 32 ? RPB : 1][G == 32 ? 8 * V * 32 : 1];
@@ -243,51 +332,49 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) bwd_kernel(const BwdA
   pdl_wait();
   int par = 0;  // two sets of reduction buffers: a row's writes never meet the last row's reads
   for (long long row = (long long)blockIdx.x * RPB + grp; row < a.M; row += (long long)gridDim.x * RPB, par ^= 1) {
-    float s[V][8], d[V][8];
+    Pack<TX> sp[V];
+    Pack<TY> dp[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(static_cast<const TX*>(a.s) + row * a.lds, i, t, a.N, s[i]);
+    for (int i = 0; i < V; ++i) load_pack<ALIGNED, G>(static_cast<const TX*>(a.s) + row * a.lds, i, t, a.N, sp[i]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) load_set<ALIGNED, G>(static_cast<const TY*>(a.dy) + row * a.lddy, i, t, a.N, d[i]);
+    for (int i = 0; i < V; ++i) load_pack<ALIGNED, G>(static_cast<const TY*>(a.dy) + row * a.lddy, i, t, a.N, dp[i]);
     float ss = 0.f, gs = 0.f;
-    float w[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (a.w) {
-        load_set<ALIGNED, G>(a.w, i, t, a.N, w[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
-      }
+      float s[8], d[8], w[8];
+      open(sp[i], s);
+      open(dp[i], d);
+      load_weight<ALIGNED, G>(a.w, i, t, a.N, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss = fmaf(s[i][j], s[i][j], ss);
-        gs = fmaf(d[i][j] * w[i][j], s[i][j], gs);
+        ss = fmaf(s[j], s[j], ss);
+        gs = fmaf(d[j] * w[j], s[j], gs);
       }
     }
-    ss = group_reduce<G, false>(ss, buf[par][0]);
-    gs = group_reduce<G, false>(gs, buf[par][1]);
+    group_reduce2<G>(ss, gs, buf[par][0], buf[par][1]);
     const float r = 1.f / sqrtf(ss / float(a.N) + a.eps);
     const float c = r * r * (gs / float(a.N));
+    TX* o = static_cast<TX*>(a.dx) + row * a.lddx;
+    const TX* u = static_cast<const TX*>(a.dsum) + row * a.ldds;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      float s[8], d[8], w[8];
+      open(sp[i], s);
+      open(dp[i], d);
+      load_weight<ALIGNED, G>(a.w, i, t, a.N, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[i][j] = fmaf(d[i][j] * r, s[i][j], dw[i][j]);
-        d[i][j] = r * (d[i][j] * w[i][j] - s[i][j] * c);
+        dw[i][j] = fmaf(d[j] * r, s[j], dw[i][j]);
+        d[j] = r * (d[j] * w[j] - s[j] * c);
       }
-    if (a.dsum) {
-      const TX* u = static_cast<const TX*>(a.dsum) + row * a.ldds;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
+      if (a.dsum) {
         float v[8];
         load_set<ALIGNED, G>(u, i, t, a.N, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] += v[j];
+        for (int j = 0; j < 8; ++j) d[j] += v[j];
       }
+      store_set<ALIGNED, G>(o, i, t, a.N, d);
     }
-    TX* o = static_cast<TX*>(a.dx) + row * a.lddx;
-#pragma unroll
-    for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(o, i, t, a.N, d[i]);
   }
   if (!a.part) return;
   float* out = a.part + (long long)blockIdx.x * a.N;
@@ -305,12 +392,7 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) bwd_kernel(const BwdA
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = ALIGNED ? 8 * (t + i * G) + j : (8 * i + j) * G + t;
-        if (e < a.N) out[e] = dw[i][j];
-      }
+    for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(out, i, t, a.N, dw[i]);
   }
 }
 
@@ -328,16 +410,32 @@ bool by_length(int N, F&& f) {
   return f.template operator()<1024, 4>();
 }
 
+// The backward with an fp32 operand holds twice the registers per element: two
+// sets per thread at most, as far as 1024 threads go.
+template <class F>
+bool by_length_wide(int N, F&& f) {
+  if (N <= 256) return f.template operator()<32, 1>();
+  if (N <= 512) return f.template operator()<32, 2>();
+  if (N <= 1024) return f.template operator()<64, 2>();
+  if (N <= 2048) return f.template operator()<128, 2>();
+  if (N <= 4096) return f.template operator()<256, 2>();
+  if (N <= 8192) return f.template operator()<512, 2>();
+  if (N <= 16384) return f.template operator()<1024, 2>();
+  return f.template operator()<1024, 4>();
+}
+
 bool aligned_rows(const void* p, long long ld, int es) {
   return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * es) % 16 == 0);
 }
 
 int esize(int dtype) { return dtype == DSF_F32 ? 4 : (dtype == DSF_BF16 ? 2 : 1); }
 
-long long bwd_blocks(long long M, int N) {
-  const long long rpb = N <= 1024 ? kBlock / 32 : 1;
-  const long long b = (M + rpb - 1) / rpb;
-  return b < kMaxPartials ? b : kMaxPartials;
+// Blocks of the backward, each with one row of weight-gradient sums: rpb rows
+// at a time each (8 where a row is a warp's), as many as are resident (512
+// threads per SM; blocks of 128 threads: four).
+long long bwd_blocks(long long M, int rpb, int threads) {
+  const long long b = (M + rpb - 1) / rpb, most = kSms * (threads < 512 ? 512 / threads : 1);
+  return b < most ? b : most;
 }
 
 template <class TX, class TY>
@@ -357,11 +455,13 @@ struct Bwd {
   const BwdArgs& a;
   bool al;
   cudaStream_t st;
+  long long* blocks;  // out: the rows of partial sums
   template <int G, int V>
   bool operator()() const {
     constexpr int T = G == 32 ? kBlock : G;
-    const unsigned grid = unsigned(bwd_blocks(a.M, a.N));
-    return pdl_launch(al ? bwd_kernel<TY, TX, G, V, true> : bwd_kernel<TY, TX, G, V, false>, dim3(grid), T, st, a);
+    *blocks = bwd_blocks(a.M, T / G, T);
+    return pdl_launch(al ? bwd_kernel<TY, TX, G, V, true> : bwd_kernel<TY, TX, G, V, false>, dim3(unsigned(*blocks)), T,
+                      st, a);
   }
 };
 
@@ -411,7 +511,7 @@ int ctr_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldr, i
 
 size_t dsf_rms_norm_workspace_bytes(int64_t M, int32_t N) {
   if (M < 0 || M > INT32_MAX || N < 1 || N > kMaxN) return 0;
-  const long long b = bwd_blocks(M, N);
+  const long long b = bwd_blocks(M, 1, 128);  // (the most of any variant)
   return (size_t(b > 0 ? b : 1) * N * 4 + 255) / 256 * 256;
 }
 
@@ -439,13 +539,15 @@ int ctr_rms_norm_bwd(const void* dy, int64_t lddy, int32_t dy_dtype, const void*
   const bool al = N % 8 == 0 && aligned_rows(dy, lddy, ey) && aligned_rows(s, lds, ex) &&
                   aligned_rows(dsum, ldds, ex) && aligned_rows(dx, lddx, ex) && aligned_rows(w, 0, 4);
   bool ok;
+  long long blocks = 0;
   if (dy_dtype == DSF_F32)
-    ok = x_dtype == DSF_F32 ? by_length(N, Bwd<float, float>{a, al, st}) : by_length(N, Bwd<float, __nv_bfloat16>{a, al, st});
+    ok = x_dtype == DSF_F32 ? by_length_wide(N, Bwd<float, float>{a, al, st, &blocks})
+                            : by_length_wide(N, Bwd<float, __nv_bfloat16>{a, al, st, &blocks});
   else
-    ok = x_dtype == DSF_F32 ? by_length(N, Bwd<__nv_bfloat16, float>{a, al, st})
-                            : by_length(N, Bwd<__nv_bfloat16, __nv_bfloat16>{a, al, st});
+    ok = x_dtype == DSF_F32 ? by_length_wide(N, Bwd<__nv_bfloat16, float>{a, al, st, &blocks})
+                            : by_length(N, Bwd<__nv_bfloat16, __nv_bfloat16>{a, al, st, &blocks});
   if (!ok) return DSF_ECUDA;
-  if (dw && !colsum(a.part, bwd_blocks(M, N), N, dw, st)) return DSF_ECUDA;
+  if (dw && !colsum(a.part, blocks, N, dw, st)) return DSF_ECUDA;
   return DSF_OK;
 }
 
