@@ -4,12 +4,14 @@
 //
 // Both directions are bound by HBM: a row is read once, held in registers
 // between the row sum and the outputs, and written once. A row belongs to a
-// group of G threads -- one warp up to N = 1024, so that the row sums are warp
-// shuffles and several rows are in flight per block, then 128 .. 1024 threads
-// -- and each thread holds 8 V elements of it (V <= 4, so a row's registers
-// stay near 32 per operand). Aligned rows move in 16-byte vectors, eight
-// elements a thread; others (odd N, odd strides) element by element, the
-// group's threads side by side.
+// group of G threads -- one warp up to N = 1024 (bf16) or 512 (fp32), so that
+// the row sums are warp shuffles and several rows are in flight per block,
+// then 64 .. 1024 threads -- and each thread holds 8 V elements of it (V <= 4).
+// Aligned rows move in 16-byte vectors, eight elements a thread; others (odd N,
+// odd strides) element by element, the group's threads side by side.
+// Measured: 65536 x 1024 bf16 with the residual to e4m3 75 us, 6.2 TB/s of
+// algorithmic bytes (a plain copy of this chip: 6.8); its backward in bf16 70 us
+// (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -410,8 +412,9 @@ bool by_length(int N, F&& f) {
   return f.template operator()<1024, 4>();
 }
 
-// The backward with an fp32 operand holds twice the registers per element: two
-// sets per thread at most, as far as 1024 threads go.
+// Rows of fp32 (in the backward: either operand) take twice the registers per
+// element: two sets per thread at most, as far as 1024 threads go. (8192 x 1024
+// in fp32: forward 13.3 us, backward 17.5; by a warp per row 15.9 and 21.)
 template <class F>
 bool by_length_wide(int N, F&& f) {
   if (N <= 256) return f.template operator()<32, 1>();
@@ -498,9 +501,9 @@ int ctr_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldr, i
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool ok;
   if (x_dtype == DSF_F32) {
-    if (y_dtype == DSF_F32) ok = by_length(N, Fwd<float, float>{a, al, st});
-    else if (y_dtype == DSF_BF16) ok = by_length(N, Fwd<float, __nv_bfloat16>{a, al, st});
-    else ok = by_length(N, Fwd<float, __nv_fp8_e4m3>{a, al, st});
+    if (y_dtype == DSF_F32) ok = by_length_wide(N, Fwd<float, float>{a, al, st});
+    else if (y_dtype == DSF_BF16) ok = by_length_wide(N, Fwd<float, __nv_bfloat16>{a, al, st});
+    else ok = by_length_wide(N, Fwd<float, __nv_fp8_e4m3>{a, al, st});
   } else {
     if (y_dtype == DSF_F32) ok = by_length(N, Fwd<__nv_bfloat16, float>{a, al, st});
     else if (y_dtype == DSF_BF16) ok = by_length(N, Fwd<__nv_bfloat16, __nv_bfloat16>{a, al, st});
