@@ -433,12 +433,34 @@ bool aligned_rows(const void* p, long long ld, int es) {
 
 int esize(int dtype) { return dtype == DSF_F32 ? 4 : (dtype == DSF_BF16 ? 2 : 1); }
 
-// Blocks of the backward, each with one row of weight-gradient sums: rpb rows
-// at a time each (8 where a row is a warp's), as many as are resident (512
-// threads per SM; blocks of 128 threads: four).
-long long bwd_blocks(long long M, int rpb, int threads) {
-  const long long b = (M + rpb - 1) / rpb, most = kSms * (threads < 512 ? 512 / threads : 1);
+// Blocks of the backward for rows in groups of G, each with one row of
+// weight-gradient sums: 8 rows at a time each where a row is a warp's, else one,
+// as many as are resident at 512 threads per SM (two blocks of 256, four of
+// 128, eight of 64).
+template <int G>
+long long bwd_blocks(long long M) {
+  constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
+  const long long b = (M + RPB - 1) / RPB, most = kSms * (T < 512 ? 512 / T : 1);
   return b < most ? b : most;
+}
+
+// What by_length and by_length_wide are given to learn a variant's blocks.
+struct BwdBlocks {
+  long long M;
+  long long* blocks;
+  template <int G, int V>
+  bool operator()() const {
+    *blocks = bwd_blocks<G>(M);
+    return true;
+  }
+};
+
+// Rows of partial sums of a backward call, whatever its operands' types are.
+long long part_rows(long long M, int N) {
+  long long a = 0, b = 0;
+  by_length(N, BwdBlocks{M, &a});
+  by_length_wide(N, BwdBlocks{M, &b});
+  return a > b ? a : b;
 }
 
 template <class TX, class TY>
@@ -462,7 +484,7 @@ struct Bwd {
   template <int G, int V>
   bool operator()() const {
     constexpr int T = G == 32 ? kBlock : G;
-    *blocks = bwd_blocks(a.M, T / G, T);
+    *blocks = bwd_blocks<G>(a.M);
     return pdl_launch(al ? bwd_kernel<TY, TX, G, V, true> : bwd_kernel<TY, TX, G, V, false>, dim3(unsigned(*blocks)), T,
                       st, a);
   }
@@ -514,7 +536,7 @@ int ctr_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldr, i
 
 size_t dsf_rms_norm_workspace_bytes(int64_t M, int32_t N) {
   if (M < 0 || M > INT32_MAX || N < 1 || N > kMaxN) return 0;
-  const long long b = bwd_blocks(M, 1, 128);  // (the most of any variant)
+  const long long b = part_rows(M, N);
   return (size_t(b > 0 ? b : 1) * N * 4 + 255) / 256 * 256;
 }
 
