@@ -9,9 +9,9 @@
 // then 64 .. 1024 threads -- and each thread holds 8 V elements of it (V <= 4).
 // Aligned rows move in 16-byte vectors, eight elements a thread; others (odd N,
 // odd strides) element by element, the group's threads side by side.
-// Measured: 65536 x 1024 bf16 with the residual to e4m3 75 us, 6.2 TB/s of
-// algorithmic bytes (a plain copy of this chip: 6.8); its backward in bf16 70 us
-// (5.7 TB/s).
+// Measured: 65536 x 1024 bf16 with the residual to e4m3 71 us, 6.6 TB/s of
+// algorithmic bytes (a plain copy of this chip: 6.8); its backward in bf16 72 us
+// with the weight's gradient, 68 without.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -65,8 +65,6 @@ template <>
 __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __nv_fp8_e4m3 from_f<__nv_fp8_e4m3>(float v) { return __nv_fp8_e4m3(v); }
 
 // eight consecutive elements, 16-byte aligned (e4m3: 8 bytes)
 __device__ __forceinline__ void load8(const float* p, float* v) {
@@ -95,7 +93,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float* v) {
+__device__ __forceinline__ uint2 pack8_e4m3(const float* v) {
   uint32_t u[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -103,7 +101,7 @@ __device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float* v) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2], v[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
     u[k] = lo | hi << 16;
   }
-  *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+  return make_uint2(u[0], u[1]);
 }
 
 // A group's share of a row: V sets of 8 elements per thread. ALIGNED: set i of
@@ -183,6 +181,43 @@ __device__ __forceinline__ void group_reduce2(float& a, float& b, float* buf_a, 
   }
 }
 
+// v / scale in e4m3, eight values. lo and hi are the rounded 1 / scale times 1 -
+// 2^-22 and 1 + 2^-22, so that a product with one of them is below the quotient
+// and one with the other above (four roundings of 2^-24 lie between). Where
+// both round to the same e4m3 value, so does the quotient; else, next to a
+// border, all eight are divided. That is rare with a weight; without one, bf16
+// rows often hold values in a ratio to their largest that is a border exactly.
+// (65536 x 1024 bf16 with the residual: 71 us with a weight, 78 without; 75 by
+// the product with the rounded 1 / scale alone, which is wrong once in 4 million
+// values with a weight and 2600 times without; 80 by divisions.)
+__device__ __forceinline__ uint2 quotients8(const float* v, float scale, float lo, float hi) {
+  float a[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a[j] = v[j] * lo;
+    b[j] = v[j] * hi;
+  }
+  const uint2 q = pack8_e4m3(a), u = pack8_e4m3(b);
+  if (q.x == u.x && q.y == u.y) return q;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] = v[j] / scale;
+  return pack8_e4m3(a);
+}
+// The set of eight e4m3 values, as store_set.
+template <bool ALIGNED, int G>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int N, uint2 q) {
+  if (ALIGNED) {
+    const int e = 8 * (t + i * G);
+    if (e < N) *reinterpret_cast<uint2*>(row + e) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = (8 * i + j) * G + t;
+      if (e < N) row[e] = uint8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+  }
+}
+
 template <class TX, class TY, int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdArgs a) {
   constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
@@ -230,7 +265,8 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdA
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * w[j];
   }
-  if (sizeof(TY) == 1) {
+  TY* y = static_cast<TY*>(a.y) + row * a.ldy;
+  if constexpr (sizeof(TY) == 1) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -239,14 +275,14 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock) fwd_kernel(const FwdA
     m = group_reduce<G, true>(m, buf[1]);
     const float scale = fmaxf(m / kE4m3Max, 1.17549435e-38f), inv = 1.f / scale;
     if (t == 0) a.scale[row] = scale;
+    const float lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
+      store_e4m3<ALIGNED, G>(reinterpret_cast<uint8_t*>(y), i, t, a.N, quotients8(s[i], scale, lo, hi));
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] *= inv;
+    for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(y, i, t, a.N, s[i]);
   }
-  TY* y = static_cast<TY*>(a.y) + row * a.ldy;
-#pragma unroll
-  for (int i = 0; i < V; ++i) store_set<ALIGNED, G>(y, i, t, a.N, s[i]);
 }
 
 // A set of 8 elements as it is stored: two per register in bf16.
