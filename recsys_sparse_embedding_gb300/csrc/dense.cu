@@ -50,18 +50,18 @@ constexpr size_t kPartBytes = size_t(kSms / 2) * 256 * 256 * 4;
 
 // Estimates in microseconds, per tile configuration (fitted to measured calls
 // of 200 to 8192 rows): a K-block of a 256 x 256 tile (on two SMs; fp32: 256 x
-// 128, six products), 128 x 128 or 128 x 64 tile takes `block`, its epilogue
+// 128, six products), 128 x 128, 128 x 64 or (in runs) 256 x 128 tile takes `block`, its epilogue
 // `tail`, and the two overlap from tile to tile; a launch costs kLaunch; the
 // chip takes its units in whole waves; a split product pays for a second
 // launch and its partial sums' way to L2 and back.
 struct Cost {
   bool f32;
   double block(int cfg) const {
-    constexpr double kBlock[2][3] = {{0.31, 0.29, 0.275}, {0.9, 0.95, 0.75}};
+    constexpr double kBlock[2][4] = {{0.31, 0.29, 0.275, 0.23}, {0.9, 0.95, 0.75, 0}};
     return kBlock[f32][cfg];
   }
   double tail(int cfg) const {
-    constexpr double kTail[2][3] = {{4.4, 2.2, 1.2}, {3.0, 3.0, 2.0}};
+    constexpr double kTail[2][4] = {{4.4, 2.2, 1.2, 2.6}, {3.0, 3.0, 2.0, 0}};
     return kTail[f32][cfg];
   }
   // `units` in a row, of `blocks` K-blocks each
@@ -90,15 +90,23 @@ void set_tiles(Job& o, int cfg, long long M, long long N, int nb, bool gated, bo
   o.nseg = nseg;
 }
 long long tiles_of(const Job& o) { return (long long)o.mt * o.nt * o.nb; }
-long long slots_of(int cfg) { return cfg == 0 ? kSms / 2 : kSms; }
+long long slots_of(int cfg) { return kSms * 128 / cfg_rows(cfg); }
+
+// K-blocks in one accumulator run of a bf16 dz product that db is summed from.
+// With more, its wide tiles are half as wide (configuration 3), so that the
+// epilogue's registers hold a tile's sums. (Without db, dz is rounded to bf16,
+// and the runs would not be seen.)
+constexpr long long kDzBlocks = 8;
 
 // Picks the configuration and the K-splits of one product.
 void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg, bool may_split) {
   const Cost cost{p.f32};
   double best = 1e300;
   Job o = p.a.job[0];
-  for (int cfg = 0; cfg < 3; ++cfg) {
+  const bool runs = p.epi == kEpiDz && !p.f32 && p.a.part && nkb > kDzBlocks;
+  for (int cfg = 0; cfg < 4; ++cfg) {
     if (cfg == 2 && p.gated) continue;
+    if (cfg % 3 == 0 && (cfg == 3) != runs) continue;
     for (int want = 1; want <= kMaxSplits && want <= nkb; ++want) {
       set_tiles(o, cfg, M, N, nb, p.gated, p.f32, nkb, nseg, want);
       if (tiles_of(o) > INT32_MAX / 64) break;
@@ -520,6 +528,7 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.f32 = f32;
   p.epi = dz ? kEpiDz : (in ? kEpiRes : kEpiFwd);
   const long long nkb = (l->K + c.kbe - 1) / c.kbe;
+  p.a.part = sums;
   plan(p, c.M, c.N, 1, nkb, 1, !dz);
   Job& o = p.a.job[0];
   o.a_term = 1;
@@ -529,8 +538,6 @@ bool layer_product(const Ctx& c, const float* xs, const void* in, long long ldi,
   p.a.xs = xs;
   p.a.ws = l->scale;
   p.a.status = c.status;
-  p.a.part = sums;
-  p.a.grow = 1.f + 0.5f * float(4 * nkb) / float(1 << 25);  // (four additions per K-block)
   if (o.splits > 1) {
     set_part(p, c);
   } else {

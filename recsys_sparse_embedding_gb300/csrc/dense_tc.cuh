@@ -27,19 +27,24 @@
 // significant bits of what is left. x y is the sum of the terms' products;
 // those below 2^-21 of it (x2 y3, x3 y2, x3 y3) are dropped. A K-block's three
 // terms of A and of B are loaded once and multiplied six ways: x1 y1 into one
-// accumulator, the five smaller products into another. The tensor cores
-// truncate each addition to an accumulator (measured: a run of n additions is
-// low by about n 2^-25 of the sum), so a run is 4 K-blocks, and the epilogue
-// warps add the runs up in registers, rounding to nearest. (bf16 operands take
-// all of K in one run. What that costs z is seen in one place, db, which is
-// fp32: there the mean loss, half of n 2^-25 for sums of random sign, is
-// multiplied back with the bias, which halves db's error: 5.6e-7 of its 2-norm
-// instead of 1.1e-6 in a gated layer of 16384 x 1024 -> 4096.)
+// accumulator, the five smaller products into another.
+//
+// Runs. The tensor cores truncate each addition to an accumulator towards zero.
+// Measured, a sum of n additions (K / 16) is low by 0.5 n 2^-25 of itself where
+// the terms' signs are random, by 0.9 (n = 64) to 3 n 2^-25 (n = 2^14 and more)
+// where they are alike, and by less where terms are zero, so no factor gives it
+// back. Where fp32 results depend on it, the accumulator takes a run of K-blocks
+// at a time, and the epilogue warps add the runs up in registers, rounding to
+// nearest: runs of 4 K-blocks in fp32, and of 8 in the z from which a bf16
+// backward sums db (gated, 16384 x 1024 -> 4096: db is off by 5.2e-7 of its
+// 2-norm, 1.1e-6 with all of K in one run, and no more at longer K: 2.4e-6 at
+// 2048 in one run). Its tiles are then 256 x 128, so that a tile's sums fit the
+// registers: the product and db's column sums take 244 us instead of 199.
+// (256 x 256 with sums in registers spills: 310 us.) Other products take all of
+// a unit's K in one run: their outputs are rounded to bf16.
 //
 // Measured, bf16: gated forward of 16384 x 1024 -> 4096 145 to 148 us (1.86
-// to 1.89 PFLOP/s; the tensor pipe is busy 84% of the launch); its dz product
-// 192 to 194 us with db (66%: held by the epilogue, which writes two outputs
-// and sums columns). 8192 x 4096 -> 1024 42 us (1.63 PFLOP/s: 128 tiles on 76
+// to 1.89 PFLOP/s; the tensor pipe is busy 84% of the launch). 8192 x 4096 -> 1024 42 us (1.63 PFLOP/s: 128 tiles on 76
 // CTA pairs are two waves, 84% filled), in e4m3 25 us. fp32 8192 x 256 -> 512
 // 20 us with its operands' laying out. 8192 x 512 -> 256 6.5 us: latency, one
 // tile per CTA.
@@ -114,7 +119,6 @@ struct TcArgs {
   const void* in;               // kEpiRes, kEpiDz
   long long ldi;
   int in_vec;   // rows at 16-byte boundaries
-  float grow;   // kEpiDz, bf16: 1 + the accumulator's mean loss
   float* part;  // kEpiDz: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
   int* status;
 };
@@ -147,6 +151,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -238,14 +247,17 @@ struct Shape {
   static constexpr int STAGES = kRoom / STAGE < 8 ? kRoom / STAGE : 8;
   static constexpr int SMEM = STAGES * STAGE + EBYTES + BIAS_BYTES + BAR_BYTES;
   static constexpr int ACC = F32 ? 2 * BN : BN;  // tensor-memory columns of an accumulator
-  static constexpr uint32_t TCOLS = 2 * ACC;
+  // K-blocks per accumulator run (0: all of a unit's), and accumulators
+  static constexpr int RUN = F32 ? 4 : (EPI == kEpiDz && BN < 256 ? 8 : 0);
+  static constexpr uint32_t NACC = !F32 && RUN ? 4 : 2;
+  static constexpr uint32_t TCOLS = NACC * ACC;
   static_assert(TCOLS <= 512 && (TCOLS & (TCOLS - 1)) == 0, "tensor memory columns");
   static_assert(STAGES >= 4, "ring");
   static_assert(B_BYTES % (GATED && CG == 1 ? 2048 : 1024) == 0, "swizzle atoms");
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tfull[2], tempty[2];
+  uint64_t full[8], empty[8], tfull[4], tempty[4];
   uint32_t tmem;
   int abort_;
 };
@@ -291,7 +303,6 @@ __device__ __forceinline__ int slot(int r, int at) {
   return r * ROWB + (((at >> 4) ^ (ROWB == 64 ? (r >> 1) & 3 : r & 7)) << 4) + (at & 15);
 }
 
-constexpr int kRun = 4;  // F32: K-blocks per accumulator run
 
 // ---------------------------------------------------------------- the kernel
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   using TO = typename S::TO;
   constexpr bool DUAL = MAJOR == kDual, BMN = MAJOR != kKK;
   constexpr int kBK = KIND == kBf16 ? 64 : 128;  // K elements per block (128 bytes)
-  constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : 1;
+  constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : 1, RUN = S::RUN;
   static_assert(!(GATED && BMN), "a gated layer's product is K-major");
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sE = sm + STAGES * S::STAGE;
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < int(S::NACC); ++i) {
       mbar_init(&bars->tfull[i], 1);
       mbar_init(&bars->tempty[i], S::kEpiWarps * CG);
     }
@@ -449,8 +460,11 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     __syncwarp();
   } else if (warp == S::kMma) {
     // ------------------------------------------------ MMAs (one thread of the cluster)
-    if (lane == 0 && rank == 0) {
+    // (The warp runs the loop together and one elected lane issues: descriptors
+    // then stay in uniform registers.)
+    if (rank == 0) {
       pdl_wait();  // (its waits are bounded, what the stream does before is not)
+      const bool lead = elect_one();
       constexpr uint32_t ID = (1u << 4) | (KIND == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (BMN ? 1u << 16 : 0u) |
                               (uint32_t(BN >> 3) << 17) | (uint32_t((128 * CG) >> 4) << 24);
       uint32_t run = 0, st = 0, phase = 0;  // the next stage, and its barrier's phase
@@ -464,13 +478,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         const uint64_t da = (amn ? mn_desc(s0) : sw128_kmajor_desc(s0)) + sa * uint32_t(S::STAGE >> 4),
                        db = db0 + sb * uint32_t(S::STAGE >> 4);
         const uint32_t id = ID | (amn ? 1u << 15 : 0u), step = amn ? 128 : 2;
+        if (!lead) return;
 #pragma unroll
         for (uint32_t kk = 0; kk < 4; ++kk)
           mma<CG, KIND>(d, da + kk * step, db + kk * (BMN ? 128 : 2), id, (accumulate || kk > 0) ? 1u : 0u);
       };
       auto take = [&](uint32_t& stage) {  // the next stage, once it is filled
         stage = st;
-        ok = mbar_wait(&bars->full[st], phase);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[st], phase));
         if (++st == uint32_t(STAGES)) st = 0, phase ^= 1u;
         tc_fence_after();
         return ok;
@@ -479,9 +494,11 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       for (int i = 0; ok && unit_at(i, t); ++i) {
         if (DUAL) amn = t.job == 0;
         for (int left = a.job[DUAL ? t.job : 0].nseg * t.kbn; left > 0 && ok; ++run) {
-          const int len = F32 ? min(left, kRun) : left;
-          const uint32_t acc = run & 1u, d = tbase + acc * S::ACC;
-          if (run >= 2 && !(ok = mbar_wait(&bars->tempty[acc], ((run >> 1) - 1) & 1u))) break;
+          const int len = RUN ? min(left, RUN) : left;
+          const uint32_t acc = run % S::NACC, d = tbase + acc * S::ACC;
+          if (run >= S::NACC &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->tempty[acc], (run / S::NACC - 1) & 1u))))
+            break;
           tc_fence_after();
           for (int k = 0; k < len; ++k) {
             uint32_t x, y, z;
@@ -496,17 +513,18 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
               block(d + BN, x, z, true);
               block(d + BN, z, x, true);
             }
+            if (!lead) continue;
             mma_commit<CG>(&bars->empty[x]);
             if (F32) {
               mma_commit<CG>(&bars->empty[y]);
               mma_commit<CG>(&bars->empty[z]);
             }
           }
-          if (ok) mma_commit<CG>(&bars->tfull[acc]);
+          if (ok && lead) mma_commit<CG>(&bars->tfull[acc]);
           left -= len;
         }
       }
-      if (!ok) atomicExch(&bars->abort_, 1);
+      if (!ok && lead) atomicExch(&bars->abort_, 1);
     }
     __syncwarp();
   } else {
@@ -519,7 +537,6 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz;
     constexpr bool SCALED = KIND == kE4m3 && FWD;
     constexpr bool TERMS_OUT = F32 && EPI == kEpiDz;  // dz leaves as three bf16 terms
-    constexpr bool GROWN = !F32 && EPI == kEpiDz;     // z = acc * grow + bias
     constexpr bool PAIR = GATED && EPI != kEpiPart;   // an item takes gate and up accumulators
     constexpr int GR = S::kGroups, ROWB = CW * int(sizeof(TO));
     constexpr int halves = GATED ? 2 : 1;
@@ -673,7 +690,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     bool ok = true;
     auto wait_run = [&]() {  // the run's accumulator is complete
       if (*aborted) ok = false;
-      if (ok && lane == 0) ok = mbar_wait(&bars->tfull[run & 1u], (run >> 1) & 1u);
+      if (ok && lane == 0) ok = mbar_wait(&bars->tfull[run % S::NACC], (run / S::NACC) & 1u);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       tc_fence_after();
       return ok;
@@ -681,13 +698,13 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     auto done_run = [&]() {  // and may be overwritten
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(tempty0 + (run & 1u) * 8u);
+      if (lane == 0) mbar_arrive_relaxed(tempty0 + (run % S::NACC) * 8u);
       ++run;
     };
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const Job& jb = a.job[DUAL ? t.job : 0];
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
-      // one item: 32 rows by CW columns. F32: pg, pu hold its sums
+      // one item: 32 rows by CW columns. In runs: pg, pu hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
         if (row0 >= jb.M || col0 >= jb.N) {
@@ -699,7 +716,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         float g_[32], up_[PAIR ? 32 : 1];
         float* g = g_;
         float* up = up_;
-        if (F32) {
+        if (RUN) {
           g = pg;
           up = pu;
         } else {
@@ -753,7 +770,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             if (PAIR) wsu = __ldg(a.ws + jb.N + col0 + lane);
           }
         }
-        if (!F32) tmem_ld_wait();
+        if (!RUN) tmem_ld_wait();
         // eight columns at a time, from the accumulators to the buffer
         auto math = [&](auto act_tag) {
           constexpr int ACT = decltype(act_tag)::value;
@@ -782,12 +799,12 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
               if (!S::BIAS) continue;
               const float2 b2 = make_float2(b[k], b[k + 1]);
               float2 z = make_float2(v[k], v[k + 1]);
-              z = GROWN ? __ffma2_rn(z, pair(a.grow), b2) : z + b2;
+              z = z + b2;
               float2 y = pair(0.f);
               if (PAIR) {
                 y = make_float2(w[PAIR ? k : 0], w[PAIR ? k + 1 : 0]);
                 if (S::BIAS_N == 64)
-                  y = GROWN ? __ffma2_rn(y, pair(a.grow), make_float2(d[k], d[k + 1])) : y + make_float2(d[k], d[k + 1]);
+                  y = y + make_float2(d[k], d[k + 1]);
                 else
                   y = y + make_float2(__shfl_sync(0xffffffffu, bu, j + k), __shfl_sync(0xffffffffu, bu, j + k + 1));
               }
@@ -866,12 +883,12 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
           }
         }
       };
-      if (F32) {
+      if constexpr (RUN > 0) {
         float sum[NI][PAIR ? 2 : 1][32];
-        const int runs = (jb.nseg * t.kbn + kRun - 1) / kRun;
+        const int runs = (jb.nseg * t.kbn + RUN - 1) / RUN;
         for (int r = 0; r < runs; ++r) {
           if (!wait_run()) break;
-          const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
+          const uint32_t tacc = tbase + (run % S::NACC) * S::ACC + lane_base;
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -882,10 +899,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
               for (int j = 0; j < 32; j += 16) {
                 float v[16], w[16];
                 tmem_ld16(col + j, v);
-                tmem_ld16(col + BN + j, w);  // the smaller products
+                if (F32) tmem_ld16(col + BN + j, w);  // the smaller products
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) sum[i][h][j + k] = (r ? sum[i][h][j + k] : 0.f) + (v[k] + w[k]);
+                for (int k = 0; k < 16; ++k) sum[i][h][j + k] = (r ? sum[i][h][j + k] : 0.f) + (F32 ? v[k] + w[k] : v[k]);
               }
             }
           done_run();
@@ -896,7 +913,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
           if (grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
       } else {
         if (!wait_run()) break;
-        const uint32_t tacc = tbase + (run & 1u) * S::ACC + lane_base;
+        const uint32_t tacc = tbase + (run % S::NACC) * S::ACC + lane_base;
 #pragma unroll 1
         for (int c = grp; c < NCH; c += GR) do_item(c, tacc, nullptr, nullptr);
         done_run();
@@ -928,7 +945,7 @@ struct Product {
   Mat A, B, A1, B1;  // kDual: job 1's
   int major;
   bool gated, f32;  // f32: fp32 operands (in terms)
-  int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64
+  int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64, 3 (bf16 dz in runs): CG 2 x BN 128
   long long weight[2];  // kDual: a unit's time, by job
 };
 
@@ -1041,13 +1058,15 @@ bool launch_tc(const Product& p, cudaStream_t s) {
 
 // Tile configurations: accumulator columns (an fp32 product's wide tiles are
 // half as wide: it holds two sets) and rows.
-constexpr int cfg_bn(int cfg, bool f32) { return cfg == 0 ? (f32 ? 128 : 256) : (cfg == 1 ? 128 : 64); }
-constexpr int cfg_rows(int cfg) { return cfg == 0 ? 256 : 128; }
+constexpr int cfg_bn(int cfg, bool f32) { return cfg == 0 ? (f32 ? 128 : 256) : (cfg == 2 ? 64 : 128); }
+constexpr int cfg_rows(int cfg) { return cfg % 3 == 0 ? 256 : 128; }
 
 template <int MAJOR, int KIND, bool GATED, int EPI, bool F32>
 bool launch_cfg(const Product& p, cudaStream_t s) {
   if (p.cfg == 0) return launch_tc<2, cfg_bn(0, F32), MAJOR, KIND, GATED, EPI, F32>(p, s);
   if (p.cfg == 1) return launch_tc<1, 128, MAJOR, KIND, GATED, EPI, F32>(p, s);
+  if constexpr (EPI == kEpiDz && !F32)
+    if (p.cfg == 3) return launch_tc<2, 128, MAJOR, KIND, GATED, EPI, F32>(p, s);
   if constexpr (!GATED) return launch_tc<1, 64, MAJOR, KIND, GATED, EPI, F32>(p, s);
   return false;
 }
