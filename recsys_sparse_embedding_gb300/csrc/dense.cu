@@ -680,8 +680,8 @@ int run_bwd(const dsf_dense* l, bool gated, const void* x, long long ldx, const 
   if (!ws || !at(ws, 256) || ws_bytes < ws_bytes_of(l, M, gated, true)) return DSF_EWORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) {
-    if (dW && cudaMemsetAsync(dW, 0, size_t(l->R) * l->K * es, s) != cudaSuccess) return DSF_ECUDA;
-    if (db && cudaMemsetAsync(db, 0, size_t(l->R) * 4, s) != cudaSuccess) return DSF_ECUDA;
+    if (dW && !succeeded(cudaMemsetAsync(dW, 0, size_t(l->R) * l->K * es, s))) return DSF_ECUDA;
+    if (db && !succeeded(cudaMemsetAsync(db, 0, size_t(l->R) * 4, s))) return DSF_ECUDA;
     return DSF_OK;
   }
   return bwd(l, gated, x, ldx, dy, lddy, M, dx, lddx, dW, db, ws, status, s);

@@ -993,7 +993,7 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32>;
   static std::atomic<int> grid_max[64];  // (host threads may race on it: each computes the same value)
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::SMEM;
@@ -1010,12 +1010,12 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   int most = grid_max[dev].load(std::memory_order_acquire);
   if (most == 0) {
     int sms = 0, n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    if (!succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM)) ||
+        !succeeded(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
       return false;
     if (CG == 2) {
       cfg.gridDim = dim3(unsigned(sms / 2 * 2));
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return false;
+      if (!succeeded(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) || n < 1) return false;
       most = 2 * n;
     } else {
       most = sms;
@@ -1053,7 +1053,7 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   mA1 = mA;
   mB1 = mB;
   if (MAJOR == kDual && (!tensor_map_3d(&mA1, p.A1, es, 64, 128) || !tensor_map_3d(&mB1, p.B1, es, 64, 64))) return false;
-  return cudaLaunchKernelEx(&cfg, kernel, a, mA, mB, mA1, mB1) == cudaSuccess;
+  return succeeded(cudaLaunchKernelEx(&cfg, kernel, a, mA, mB, mA1, mB1));
 }
 
 // Tile configurations: accumulator columns (an fp32 product's wide tiles are

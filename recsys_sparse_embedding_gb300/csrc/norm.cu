@@ -589,7 +589,7 @@ int ctr_rms_norm_bwd(const void* dy, int64_t lddy, int32_t dy_dtype, const void*
     return DSF_EWORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M == 0) {
-    if (dw && cudaMemsetAsync(dw, 0, size_t(N) * 4, st) != cudaSuccess) return DSF_ECUDA;
+    if (dw && !succeeded(cudaMemsetAsync(dw, 0, size_t(N) * 4, st))) return DSF_ECUDA;
     return DSF_OK;
   }
   if (!dy || !s || !dx || lddy < N || lds < N || lddx < N || (dsum && ldds < N)) return DSF_EINVAL;

@@ -15,6 +15,14 @@ namespace dsf {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Whether a runtime call succeeded. The error of one that did not is taken out
+// of the runtime's own record: an entry point that reads the record after its
+// launches would answer for it.
+inline bool succeeded(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaSuccess;
+}
+
 template <class... P, class... A>
 bool pdl_launch(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -26,7 +34,7 @@ bool pdl_launch(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t s,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) == cudaSuccess;
+  return succeeded(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...));
 }
 
 }  // namespace dsf
