@@ -3,11 +3,15 @@
 //   GELU  z Phi(z);                            derivative Phi(z) + z phi(z)
 // exp and the reciprocal are the hardware's approximations (a few 2^-23
 // relative, results below 2^-126 as zero): below the rounding of a bf16 result
-// and within a few units of an fp32 one. Phi is taken from the rational form
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions,
-//   erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0,
-// within 1.5e-7, with x = |z| / sqrt 2: its exp(-z^2 / 2) is also phi's, so
-// value and derivative take two special functions together.
+// and within a few units of an fp32 one. Phi is taken as
+//   Phi(-|z|) = exp(-z^2 / 2) t P(t), t = 1 / (1 + x / 2), x = |z| / sqrt 2,
+// with a polynomial P of degree 8 that was fitted to erfc(x) exp(x^2) / 2 by
+// Remez's exchange for the least relative error (0 <= x <= 9.4, where exp ends:
+// 1.0 2^-24 with the rounded coefficients). So small values keep their digits:
+// Phi is off by at most (1.25 z^2 + 32) 2^-24 of itself, the first part from the
+// exponent's roundings, which one rounding of z would cost as well. Its exp(-z^2
+// / 2) is also phi's, so value and derivative take two special functions
+// together.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -40,18 +44,20 @@ __device__ __forceinline__ float2 sigmoid(float2 z) {
   return make_float2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Phi(z), and exp(-z^2 / 2) in e. Below zero Phi is half of erfc itself.
+// Phi(z), and exp(-z^2 / 2) in e.
 __device__ __forceinline__ float2 normal_cdf(float2 z, float2& e) {
-  const float2 x = make_float2(fabsf(z.x), fabsf(z.y)) * pair(0.70710678118654752f);
-  const float2 y = (x * x) * pair(-kLog2e);
+  const float2 x = make_float2(fabsf(z.x), fabsf(z.y)), y = (z * z) * pair(-0.5f * kLog2e);
   e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-  const float2 d = __ffma2_rn(pair(0.3275911f), x, pair(1.f));
+  const float2 d = __ffma2_rn(pair(0.35355339059327376f), x, pair(1.f));
   const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
-  // (the coefficients halved)
-  float2 s = __ffma2_rn(pair(0.5f * 1.061405429f), t, pair(0.5f * -1.453152027f));
-  s = __ffma2_rn(s, t, pair(0.5f * 1.421413741f));
-  s = __ffma2_rn(s, t, pair(0.5f * -0.284496736f));
-  s = __ffma2_rn(s, t, pair(0.5f * 0.254829592f));
+  float2 s = __ffma2_rn(pair(-0.029465685f), t, pair(0.14195053f));
+  s = __ffma2_rn(s, t, pair(-0.2428992f));
+  s = __ffma2_rn(s, t, pair(0.13822791f));
+  s = __ffma2_rn(s, t, pair(-0.0127546815f));
+  s = __ffma2_rn(s, t, pair(0.10110574f));
+  s = __ffma2_rn(s, t, pair(0.12161241f));
+  s = __ffma2_rn(s, t, pair(0.14117926f));
+  s = __ffma2_rn(s, t, pair(0.1410437f));
   const float2 half = (s * t) * e, rest = __ffma2_rn(half, pair(-1.f), pair(1.f));
   return make_float2(z.x < 0.f ? half.x : rest.x, z.y < 0.f ? half.y : rest.y);
 }
