@@ -92,6 +92,18 @@ void set_tiles(Job& o, int cfg, long long M, long long N, int nb, bool gated, bo
 long long tiles_of(const Job& o) { return (long long)o.mt * o.nt * o.nb; }
 long long slots_of(int cfg) { return kSms * 128 / cfg_rows(cfg); }
 
+// K-blocks that a bf16 or e4m3 product takes in one accumulator run at most (as
+// far as kMaxSplits go): longer sums are split, and their parts added in fp32. A
+// sum of n = 4 kLongRun additions that truncate is low by up to 3 n 2^-25 =
+// 3.7e-4 of itself, a tenth of a bf16 rounding; over 2^20 inputs it would be 6e-3.
+constexpr long long kLongRun = 1024;
+
+// Splits that a product of `blocks` K-blocks has at least.
+long long least_splits(bool f32, long long blocks) {
+  const long long n = (blocks + kLongRun - 1) / kLongRun;
+  return f32 || n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits);
+}
+
 // K-blocks in one accumulator run of a bf16 dz product that db is summed from.
 // With more, its wide tiles are half as wide (configuration 3), so that the
 // epilogue's registers hold a tile's sums. (Without db, dz is rounded to bf16,
@@ -103,15 +115,16 @@ void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg,
   const Cost cost{p.f32};
   double best = 1e300;
   Job o = p.a.job[0];
-  const bool runs = p.epi == kEpiDz && !p.f32 && p.a.part && nkb > kDzBlocks;
+  const bool runs = p.epi == kEpiDz && !p.f32 && nkb > (p.a.part ? kDzBlocks : kLongRun);
+  const long long least = may_split ? least_splits(p.f32, nkb * nseg) : 1;
   for (int cfg = 0; cfg < 4; ++cfg) {
     if (cfg == 2 && p.gated) continue;
     if (cfg % 3 == 0 && (cfg == 3) != runs) continue;
-    for (int want = 1; want <= kMaxSplits && want <= nkb; ++want) {
+    for (long long want = least; want <= kMaxSplits && want <= nkb; ++want) {
       set_tiles(o, cfg, M, N, nb, p.gated, p.f32, nkb, nseg, want);
       if (tiles_of(o) > INT32_MAX / 64) break;
-      if (want > 1 && (!may_split || tiles_of(o) * want > slots_of(cfg))) break;
-      if (o.splits != want) continue;
+      if (want > least && (!may_split || tiles_of(o) * want > slots_of(cfg))) break;
+      if (want > least && o.splits != want) continue;
       const long long waves = (tiles_of(o) * o.splits + slots_of(cfg) - 1) / slots_of(cfg);
       const double c = Cost::kLaunch + cost.run(cfg, double(waves), double(o.kbps) * nseg) +
                        Cost::parts(o.splits, double(M) * N * nb * (p.gated ? 2 : 1));
@@ -127,18 +140,18 @@ void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg,
 // dW (job 0, which may be split) and dx (job 1) in one launch.
 void plan_dual(Product& p, long long M, long long N, long long K, int halves) {
   const Cost cost{p.f32};
-  const long long kw = (M + 63) / 64, kx = (N + 63) / 64;
+  const long long kw = (M + 63) / 64, kx = (N + 63) / 64, least = least_splits(p.f32, kw);
   double best = 1e300;
   TcArgs a = p.a;
   for (int cfg = 0; cfg < 3; ++cfg)
-    for (int want = 1; want <= kMaxSplits && want <= kw; ++want) {
+    for (long long want = least; want <= kMaxSplits && want <= kw; ++want) {
       set_tiles(a.job[0], cfg, N, K, halves, false, p.f32, kw, 1, want);
       set_tiles(a.job[1], cfg, M, K, 1, false, p.f32, kx, halves, 1);
       const Job& w = a.job[0];
       if (tiles_of(w) > INT32_MAX / 64 || tiles_of(a.job[1]) > INT32_MAX / 64) break;
-      if (want > 1 && tiles_of(w) * want > slots_of(cfg)) break;
-      if (w.splits != want) continue;
-            const double tail = cost.tail(cfg), tw = w.kbps * cost.block(cfg), tx = double(kx) * halves * cost.block(cfg);
+      if (want > least && tiles_of(w) * want > slots_of(cfg)) break;
+      if (want > least && w.splits != want) continue;
+      const double tail = cost.tail(cfg), tw = w.kbps * cost.block(cfg), tx = double(kx) * halves * cost.block(cfg);
       const long long weight[2] = {(long long)(1e3 * (tw > tail ? tw : tail)), (long long)(1e3 * (tx > tail ? tx : tail))};
       const Deal d = deal(a, weight, slots_of(cfg));
       const double c = Cost::kLaunch + 1e-3 * double(d.load) + tail + Cost::parts(w.splits, double(N) * K * halves);
@@ -176,20 +189,25 @@ Layout layout(const dsf_dense* l, long long M, bool gated, bool backward) {
     o += align256(bytes);
     return at;
   };
-  auto part_of = [](size_t outputs) {
-    const size_t b = outputs * 4 * kMaxSplits;
-    return b < kPartBytes ? b : kPartBytes;
+  // partial sums of a product of `blocks` K-blocks: those of the splits that it
+  // may have, or of those that it has at least
+  auto part_of = [l](size_t outputs, long long blocks) {
+    const size_t b = outputs * 4 * kMaxSplits, may = b < kPartBytes ? b : kPartBytes;
+    const size_t least = size_t(least_splits(l->dtype == DSF_F32, blocks));
+    return least > 1 && outputs * 4 * least > may ? outputs * 4 * least : may;
   };
+  auto blocks_of = [](long long k, int per) { return (k + per - 1) / per; };
   const bool lo = laid_out(l->dtype, l->K);
   w.xp = take(lo ? size_t(terms) * M * w.kp * pes : 0);
   w.wp = take(lo ? size_t(terms) * l->R * w.kp * pes : 0);
-  size_t part = part_of(size_t(M) * up(N, 4) * halves);
+  size_t part = part_of(size_t(M) * up(N, 4) * halves, blocks_of(l->K, l->dtype == DSF_E4M3 ? 128 : 64));
   if (backward) {
     const bool own_dz = gated || l->act != DSF_ACT_NONE;  // else dz is dy
     w.gp = take(!own_dz && laid_out(l->dtype, N) ? size_t(terms) * M * w.np * pes : 0);
     w.dz = take(own_dz ? size_t(terms) * halves * M * w.np * 2 : 0);
     w.sums = take(size_t((M + 31) / 32) * l->R * 4);
-    const size_t px = part_of(size_t(M) * up(l->K, 4)), pw = part_of(size_t(l->R) * up(l->K, 4));
+    const size_t px = part_of(size_t(M) * up(l->K, 4), blocks_of(N, 64) * halves);
+    const size_t pw = part_of(size_t(l->R) * up(l->K, 4), blocks_of(M, 64));
     part = part > px ? part : px;
     part = part > pw ? part : pw;
   }
@@ -569,6 +587,9 @@ bool grad_products(const Ctx& c, const Mat& dz, void* dx, long long lddx, void* 
   const int K = c.l->K;
   const bool f32 = c.l->dtype == DSF_F32;
   if (!dx && !dW) return true;
+  // (in the launch for both, dx's sums are not split)
+  if (dx && dW && least_splits(f32, (c.N + 63) / 64 * c.halves) > 1)
+    return grad_products(c, dz, nullptr, 0, dW) && grad_products(c, dz, dx, lddx, nullptr);
   Product p{};
   p.gated = false;
   p.f32 = f32;

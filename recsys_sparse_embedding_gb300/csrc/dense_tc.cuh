@@ -41,7 +41,8 @@
 // 2048 in one run). Its tiles are then 256 x 128, so that a tile's sums fit the
 // registers: the product and db's column sums take 244 us instead of 199.
 // (256 x 256 with sums in registers spills: 310 us.) Other products take all of
-// a unit's K in one run: their outputs are rounded to bf16.
+// a unit's K in one run: their outputs are rounded to bf16, and K is split before
+// its runs grow long enough to be seen there.
 //
 // Measured, bf16: gated forward of 16384 x 1024 -> 4096 145 to 148 us (1.86
 // to 1.89 PFLOP/s; the tensor pipe is busy 84% of the launch). 8192 x 4096 -> 1024 42 us (1.63 PFLOP/s: 128 tiles on 76
