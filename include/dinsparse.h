@@ -417,14 +417,21 @@ int emb_adagrad_update(const dsf_tables* tables, float* const* accum, const dsf_
  *   DSF_BF16  x, W, residual, y, dy, dx, dW are bf16; fp32 accumulation on
  *             the tensor cores, one rounding at the output. The backward
  *             rounds dz to bf16 where it enters the products for dx and dW.
- *   DSF_F32   all fp32, to fp32's accuracy: every operand is taken as the
- *             exact sum of three bf16 terms, and the six products of terms
- *             that reach fp32's last bits are accumulated in fp32 (an
- *             infinite operand gives infinities or NaN in what it enters).
+ *             The tensor cores truncate each addition, so sums of one sign
+ *             come out low, by up to 4e-4 of themselves (a tenth of a bf16
+ *             rounding; sums of more than 65536 terms are added in up to 32
+ *             parts). db is fp32, and z is taken for it in runs of 512 terms.
+ *   DSF_F32   all fp32: every operand is taken as the sum of three bf16 terms
+ *             (exact from 2^-110 up), and the six products of terms that reach
+ *             fp32's last bits are accumulated in fp32. An infinite operand
+ *             gives infinities or NaN in what it enters (a call of few rows
+ *             or of a small layer the former, others mostly the latter).
  *   DSF_E4M3  x [M, K] e4m3 with x_scale_dev fp32 [M], W e4m3 with
  *             layer->scale fp32 [R]: x and W stand for value * scale.
  *             residual and y are bf16. Forward only.
- * Biases and their gradients are fp32.
+ * Biases and their gradients are fp32. Activations are evaluated in fp32: SiLU
+ * to (1.5 |z| + 16) 2^-24 of its value (0 below z = -87), GELU to (1.25 z^2 +
+ * 32) 2^-24 (0 below z = -13.2).
  *
  * Alignment: every pointer is aligned to its element. When a row of x, W
  * (K elements) or, in a backward call, dy (R, or F elements) is a multiple of
@@ -463,7 +470,9 @@ int ctr_dense_fwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const 
  * [R, K] (contiguous), both of the layer's type, and db_dev fp32 [R]; each
  * nullable, and overwritten. The residual's gradient is dy itself. z = x W^T
  * + bias is computed again (the forward keeps nothing); ReLU's gradient at 0
- * is 0. Sums run in a fixed order: equal inputs give equal bits. */
+ * is 0. Sums run in a fixed order: equal calls give equal bits. That order may
+ * differ from the forward's, and between calls with and without db: where |z|
+ * is within its rounding of 0, ReLU's gradient may go either way. */
 int ctr_dense_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const void* dy_dev, int64_t lddy, int64_t M,
                   void* dx_dev, int64_t lddx, void* dW_dev, float* db_dev, void* workspace_dev, size_t ws_bytes,
                   int32_t* status_dev, void* stream);
@@ -484,7 +493,9 @@ int ctr_glu_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const vo
  * residual) are of x_dtype (DSF_F32 or DSF_BF16). weight_dev fp32 [N],
  * nullable (ones). y_dev is of y_dtype: DSF_F32, DSF_BF16, or DSF_E4M3 with
  * y_scale_dev fp32 [M] written: scale = max(max|y| of the row / 448, 2^-126),
- * values y / scale rounded to nearest even. eps > 0. */
+ * values y / scale rounded to nearest even. eps > 0. The sum of a row's s^2 is
+ * fp32 and has to be finite there (|s| below 1.8e19 / sqrt(N) is enough): a row
+ * past it is normed to 0. */
 int ctr_rms_norm_fwd(const void* x_dev, int64_t ldx, const void* residual_dev, int64_t ldr, int32_t x_dtype,
                      const float* weight_dev, int64_t M, int32_t N, float eps, void* sum_dev, int64_t lds,
                      void* y_dev, int64_t ldy, int32_t y_dtype, float* y_scale_dev, void* stream);

@@ -82,3 +82,32 @@ def test_long_gradients(gated, both, M, K, N):
     rows_m = slice(0, min(M, 2000))
     check(out["dx"][rows_m], d[rows_m] @ (W[N:] if gated else W).double())
     check(out["dW"][N:][some] if gated else out["dW"][some], d[:, some].t() @ x.double())
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N", [(40, 72), (600, 512)])
+def test_long_inputs_of_the_gradients(gated, M, N, monkeypatch):
+    """dz's sums over more than 65536 inputs, with db and without: z near 2 from
+    terms of one sign, each gradient within the bound of sums in runs of at most
+    32 additions."""
+    K = 70000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    rows = 2 * N if gated else N
+    W, x = (positive(g, rows, K) * (8.0 / K)).to(BF16), positive(g, M, K).to(BF16)
+    layer = B.DenseLayer(W, torch.zeros(rows, device="cuda"), act=B.DSF_ACT_SILU)
+    dy = positive(g, M, N).to(BF16)
+
+    def pre(x, W, b):
+        z = x.double() @ W.double().t() + b.double()  # (its terms have one sign)
+        return z, (32 + K / 1024 + 8) * R.U * z + 1e-38
+    monkeypatch.setattr(R, "pre", pre)
+    ref = R.grads(x, W, layer.bias, "silu", dy, gated)
+    ws = B.DenseWorkspace(layer, M, gated=gated, backward=True)
+    for names in (("dx", "dW"), ("dx", "dW", "db")):
+        out = {"dx": torch.empty_like(x), "dW": torch.empty_like(W), "db": torch.empty(rows, device="cuda")}
+        intact = guard(ws)
+        (B.ctr_glu_bwd if gated else B.ctr_dense_bwd)(layer, x, dy, ws, **{n: out[n] for n in names})
+        assert intact()
+        for n in names:
+            R.assert_within(out[n], *ref[n], "%s of %s" % (n, names))

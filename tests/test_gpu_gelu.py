@@ -1,4 +1,5 @@
-"""GELU where its values are small, in the dense layer and its gradient."""
+"""GELU and SiLU where their values are small, in the dense layer and its
+gradient."""
 import math
 
 import pytest
@@ -42,4 +43,34 @@ def test_gelus_negative_tail(M, dtype):
     cdf, zphi = 0.5 * torch.erfc(-d / math.sqrt(2)), d * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi)
     ref = cdf + zphi
     tol = (cdf + zphi.abs()) * (phi_bound(d) + 2.0 ** -22)
+    R.assert_within(dx, ref, tol + (2.02 if dtype == BF16 else 1) * R.HALF[dtype] * (ref.abs() + tol) + 1e-37, "slope")
+
+
+def sigmoid_bound(z):
+    """Relative bound of 1 / (1 + exp(-z)), z < 0, in units of 2^-24: the exponent
+    carries a rounding and its constant's, 1.5 units of z; exp2 4, the sum and
+    the quotient 4, two products 2; 16 covers them."""
+    return (1.5 * z.abs() + 16) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("M,dtype", [(7, F32), (7, BF16), (8192, F32), (8192, BF16)])
+def test_silus_negative_tail(M, dtype):
+    K, N = 64, 136
+    z = -torch.linspace(0.01, 70.0, M * K, device="cuda").view(M, K).to(dtype)
+    W = torch.zeros(N, K, dtype=dtype, device="cuda")
+    W[torch.arange(K), torch.arange(K)] = 1
+    layer = B.DenseLayer(W, None, act=B.DSF_ACT_SILU)
+    ws = B.DenseWorkspace(layer, M, backward=True)
+    y = torch.empty(M, N, dtype=dtype, device="cuda")
+    B.ctr_dense_fwd(layer, z, y, ws)
+    d = z.double()
+    ref = R.act(d, "silu")
+    R.assert_within(y[:, :K], ref, ref.abs() * (sigmoid_bound(d) + R.HALF[dtype]) + 1e-37, "value")
+    dx = torch.empty_like(z)
+    dy = torch.ones(M, N, dtype=dtype, device="cuda")
+    B.ctr_dense_bwd(layer, z, dy, ws, dx=dx)
+    # p + z p (1 - p): two terms of either sign, each with p's bound and three roundings more
+    p = torch.sigmoid(d)
+    ref = p * (1 + d * (1 - p))
+    tol = (p + (d * p).abs()) * (sigmoid_bound(d) + 2.0 ** -22)
     R.assert_within(dx, ref, tol + (2.02 if dtype == BF16 else 1) * R.HALF[dtype] * (ref.abs() + tol) + 1e-37, "slope")
