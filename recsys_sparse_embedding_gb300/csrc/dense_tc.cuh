@@ -39,16 +39,18 @@
 // backward sums db (gated, 16384 x 1024 -> 4096: db is off by 5.2e-7 of its
 // 2-norm, 1.1e-6 with all of K in one run, and no more at longer K: 2.4e-6 at
 // 2048 in one run). Its tiles are then 256 x 128, so that a tile's sums fit the
-// registers: the product and db's column sums take 244 us instead of 199.
-// (256 x 256 with sums in registers spills: 310 us.) Other products take all of
+// registers: the product and db's column sums take 229 us instead of 196.
+// (256 x 256 with sums in registers spills: 310 us against 290 in a version
+// whose MMA loop was slower.) Other products take all of
 // a unit's K in one run: their outputs are rounded to bf16, and K is split before
 // its runs grow long enough to be seen there.
 //
-// Measured, bf16: gated forward of 16384 x 1024 -> 4096 145 to 148 us (1.86
-// to 1.89 PFLOP/s; the tensor pipe is busy 84% of the launch). 8192 x 4096 -> 1024 42 us (1.63 PFLOP/s: 128 tiles on 76
-// CTA pairs are two waves, 84% filled), in e4m3 25 us. fp32 8192 x 256 -> 512
-// 20 us with its operands' laying out. 8192 x 512 -> 256 6.5 us: latency, one
-// tile per CTA.
+// Measured in a graph over changing operands, bf16: gated forward of 16384 x
+// 1024 -> 4096 142 us (1.93 PFLOP/s; the tensor pipe is busy 91% of the launch).
+// 8192 x 4096 -> 1024 42.5 us, 45.5 with the residual (1.62 and 1.51 PFLOP/s:
+// 128 tiles on 76 CTA pairs are two waves, 84% filled), in e4m3 25.3 and 27.9.
+// fp32 8192 x 256 -> 512 18.3 us with its operands' laying out. 8192 x 512 ->
+// 256 6.1 us: latency, one tile per CTA.
 //
 // Every wait is bounded; one that runs out sets DSF_FLAG_TIMEOUT.
 #pragma once
@@ -82,7 +84,8 @@ enum Kind { kBf16 = 0, kE4m3 = 1 };
 // both MN-major (dW), job 1 with B (dx)
 enum Major { kKK = 0, kKN = 1, kNN = 2, kDual = 3 };
 
-// Division of unsigned 32-bit numbers by a fixed divisor: q = (mulhi(n, m) + n) >> l
+// Division of unsigned 32-bit numbers by a fixed divisor (Granlund and
+// Montgomery, Division by invariant integers using multiplication): q = (mulhi(n, m) + n) >> l
 // with l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, exact for every n below 2^31.
 struct Div {
   uint32_t d, m, l;
@@ -254,6 +257,9 @@ struct Shape {
   static constexpr uint32_t TCOLS = NACC * ACC;
   static_assert(TCOLS <= 512 && (TCOLS & (TCOLS - 1)) == 0, "tensor memory columns");
   static_assert(STAGES >= 4, "ring");
+  // A successor that is started early, and waits for this kernel, must not hold
+  // tensor memory that a block here has yet to allocate.
+  static_assert(SMEM > 114 * 1024, "one block per SM");
   static_assert(B_BYTES % (GATED && CG == 1 ? 2048 : 1024) == 0, "swizzle atoms");
 };
 
@@ -462,7 +468,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   } else if (warp == S::kMma) {
     // ------------------------------------------------ MMAs (one thread of the cluster)
     // (The warp runs the loop together and one elected lane issues: descriptors
-    // then stay in uniform registers.)
+    // then stay in uniform registers. A K-block of 256 x 128 takes 0.22 us, by a
+    // loop of one lane 0.29.)
     if (rank == 0) {
       pdl_wait();  // (its waits are bounded, what the stream does before is not)
       const bool lead = elect_one();

@@ -352,9 +352,11 @@ __device__ __forceinline__ void load_weight(const float* w, int i, int t, int N,
 // registers as they are stored (the weight is read twice, from L1). Blocks
 // walk the rows, so that a thread's weight-gradient sums (dy s r of its
 // columns) stay in registers over all of them; a block then writes one row of
-// partial sums. Two blocks of 256 threads per SM, 128 registers each: with the
-// operands held as fp32 it was one, and 65536 x 1024 in bf16 took 99 us where
-// HBM needs 59.
+// partial sums. Blocks of up to 256 threads have 128 registers a thread, so that
+// 512 threads fit an SM: with the operands held as fp32 256 did, and 65536 x
+// 1024 in bf16 took 99 us where HBM needs 59. (Wider groups, one row per block,
+// have what 512 or 1024 threads leave, and spill: fp32 rows of 16384 take 57 us
+// per 1000 where HBM needs 29, of 32768 82 us per 500.)
 template <class TY, class TX, int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(G > kBlock ? G : kBlock, G > kBlock ? 1 : 2) bwd_kernel(const BwdArgs a) {
   constexpr int T = G == 32 ? kBlock : G, RPB = T / G;
@@ -450,7 +452,7 @@ bool by_length(int N, F&& f) {
 
 // Rows of fp32 (in the backward: either operand) take twice the registers per
 // element: two sets per thread at most, as far as 1024 threads go. (8192 x 1024
-// in fp32: forward 13.3 us, backward 17.5; by a warp per row 15.9 and 21.)
+// in fp32: forward 12.1 us; backward 18.0, 21.3 with the weight's gradient.)
 template <class F>
 bool by_length_wide(int N, F&& f) {
   if (N <= 256) return f.template operator()<32, 1>();
