@@ -514,6 +514,52 @@ int ctr_rms_norm_bwd(const void* dy_dev, int64_t lddy, int32_t dy_dtype, const v
                      int64_t ldds, void* dx_dev, int64_t lddx, float* dweight_dev, void* workspace_dev,
                      size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Sequence towers and their training: a gated linear recurrence over the click
+ * sequences. din_jagged_attn weighs a sequence's
+ * positions without regard to their order; the recurrence carries a state from
+ * click to click, and its gradients go back through the dense operators above.
+ * The pages have no counterpart.
+ *
+ * Rows are positions, sequence after sequence; lengths_dev int32 [B] as in
+ * dsf_seq, or NULL: B sequences of T / B rows each (T a multiple of B; one row
+ * each is a step of serving). Along each sequence and in each of D channels
+ *   z = sigmoid(gate_t),  h_t = (1 - z) h_{t-1} + z x_t,
+ * from h0 (nullable: zeros). x, gate, h, dh, dx and dgate are matrices [T, D]
+ * of dtype (DSF_F32 or DSF_BF16) with row strides in elements, any of them
+ * perhaps the columns of a wider matrix: x and gate the halves of one dense
+ * layer's output. h0, h_last, dh_last and dh0 are fp32 [B, D], contiguous: an
+ * empty sequence passes its state (or the state's gradient) on. The state is
+ * fp32 throughout; h is rounded where it is written.
+ *
+ * Lengths: a negative one counts as zero (DSF_FLAG_NEG_LENGTH). Where they add
+ * up to more than T, the sequences are cut at T (DSF_FLAG_COUNT); rows behind
+ * the last sequence are neither read nor written. T <= 2^30, D <= 2^20.
+ * Every pointer is aligned to its element; rows of a multiple of four elements
+ * whose vectors of four are aligned are faster. Outputs overlap no input and
+ * no other output. The workspace (256-byte aligned,
+ * dsf_gated_scan_workspace_bytes, which grows with T and B) needs no
+ * initialisation and holds nothing from one call to the next. Equal calls give
+ * equal bits; the order of sums depends on the rows' place in the call. A
+ * non-finite value stays in its sequence. DSF_FLAG_TIMEOUT in *status_dev
+ * (nullable) if a device wait ran out. */
+size_t dsf_gated_scan_workspace_bytes(int64_t T, int32_t B, int32_t D);
+
+int ctr_gated_scan_fwd(const void* x_dev, int64_t ldx, const void* gate_dev, int64_t ldg, int32_t dtype,
+                       const int32_t* lengths_dev, int64_t T, int32_t B, int32_t D, const float* h0_dev, void* h_dev,
+                       int64_t ldh, float* h_last_dev, void* workspace_dev, size_t ws_bytes, int32_t* status_dev,
+                       void* stream);
+
+/* The gradients for dh_dev [T, D] and dh_last_dev (nullable: zeros): dx_dev,
+ * dgate_dev and dh0_dev (nullable), overwritten. x, gate, lengths and h0 are
+ * the forward's, h_dev its output (in bf16 dgate therefore takes h_{t-1} as it
+ * was rounded, 2^-9 of it). */
+int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int64_t ldx, const void* gate_dev,
+                       int64_t ldg, const void* h_dev, int64_t ldh, int32_t dtype, const int32_t* lengths_dev,
+                       int64_t T, int32_t B, int32_t D, const float* h0_dev, const float* dh_last_dev, void* dx_dev,
+                       int64_t lddx, void* dgate_dev, int64_t lddg, float* dh0_dev, void* workspace_dev,
+                       size_t ws_bytes, int32_t* status_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,7 +36,8 @@ EXPORTS = ["dsf_workspace_bytes", "dsf_workspace_init", "dsf_prepare_mlp", "emb_
            "dsf_bwd_workspace_bytes", "din_sparse_bwd", "emb_adagrad_update", "dsf_read_status",
            "dsf_bwd_workspace_offsets",
            "dsf_dense_workspace_bytes", "ctr_dense_fwd", "ctr_dense_bwd", "ctr_glu_fwd", "ctr_glu_bwd",
-           "dsf_rms_norm_workspace_bytes", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd"]
+           "dsf_rms_norm_workspace_bytes", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd",
+           "dsf_gated_scan_workspace_bytes", "ctr_gated_scan_fwd", "ctr_gated_scan_bwd"]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -154,6 +155,14 @@ def lib() -> ctypes.CDLL:
                                        _i64, _vp, _vp, _sz, _vp]
         for f in (L.ctr_dense_fwd, L.ctr_glu_fwd, L.ctr_dense_bwd, L.ctr_glu_bwd, L.ctr_rms_norm_fwd,
                   L.ctr_rms_norm_bwd):
+            f.restype = ctypes.c_int
+        L.dsf_gated_scan_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.dsf_gated_scan_workspace_bytes.restype = _sz
+        L.ctr_gated_scan_fwd.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _sz,
+                                         _vp, _vp]
+        L.ctr_gated_scan_bwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _vp,
+                                         _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp, _vp]
+        for f in (L.ctr_gated_scan_fwd, L.ctr_gated_scan_bwd):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -698,3 +707,72 @@ def ctr_rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, dx: torch.Tensor, weight
     _check(lib().ctr_rms_norm_bwd(gp, ldg, _DTYPES[gt], sp, lds, _DTYPES[st], _vec("weight", weight, N, dev), M, N, eps,
                                   dp, ldd, xp, ldx, _vec("dweight", dweight, N, dev), wp, nb, _on(dev, stream)),
            "ctr_rms_norm_bwd")
+
+
+# ------------------------------------------------------------- sequence towers and their training
+class GatedScanWorkspace:
+    """Scratch of the gated scan's calls for up to T rows of D channels in up
+    to B sequences."""
+
+    def __init__(self, T: int, B: int, D: int, device="cuda"):
+        self.nbytes = int(lib().dsf_gated_scan_workspace_bytes(int(T), int(B), int(D)))
+        if self.nbytes == 0:
+            raise DsfError(DSF_EINVAL, "dsf_gated_scan_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr, self.dev = self.buf.data_ptr(), self.buf.get_device()
+
+
+def _scan_of(x: torch.Tensor, B: int, workspace: GatedScanWorkspace, lengths):
+    dev = _dev_of(x)
+    if workspace.dev != dev:
+        raise ValueError("the workspace is on cuda:%d" % workspace.dev)
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x: a float32 or bfloat16 matrix expected")
+    T, D = x.shape
+    if lengths is not None and (lengths.dtype is not torch.int32 or lengths.shape != (B,) or lengths.get_device() != dev
+                                or not lengths.is_contiguous()):
+        raise ValueError("lengths: contiguous int32 [%d] on cuda:%d expected" % (B, dev))
+    if lengths is None and (T % B if B > 0 else T):
+        raise ValueError("%d rows are not %d sequences of one length" % (T, B))
+    return dev, T, D, _dptr(lengths)
+
+
+def _state(name: str, t: Optional[torch.Tensor], B: int, D: int, dev: int) -> Optional[int]:
+    """Pointer of a contiguous fp32 [B, D] matrix (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != (B, D) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s: contiguous float32 [%d, %d] on cuda:%d expected" % (name, B, D, dev))
+    return t.data_ptr()
+
+
+def ctr_gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, h: torch.Tensor, B: int, workspace: GatedScanWorkspace,
+                       lengths: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                       h_last: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """h_t = (1 - z_t) h_{t-1} + z_t x_t with z = sigmoid(gate) along each of B
+    sequences of rows (lengths int32 [B]; None: of equal length), from h0
+    [B, D] (None: zeros); the last states into h_last where given."""
+    dev, T, D, lp = _scan_of(x, B, workspace, lengths)
+    xp, ldx = _mat("x", x, x.dtype, T, D, dev)
+    gp, ldg = _mat("gate", gate, x.dtype, T, D, dev)
+    hp, ldh = _mat("h", h, x.dtype, T, D, dev)
+    _check(lib().ctr_gated_scan_fwd(xp, ldx, gp, ldg, _DTYPES[x.dtype], lp, T, B, D, _state("h0", h0, B, D, dev), hp, ldh,
+                                    _state("h_last", h_last, B, D, dev), workspace.ptr, workspace.nbytes, _dptr(status),
+                                    _on(dev, stream)), "ctr_gated_scan_fwd")
+    return h
+
+
+def ctr_gated_scan_bwd(dh: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, h: torch.Tensor, dx: torch.Tensor,
+                       dgate: torch.Tensor, B: int, workspace: GatedScanWorkspace,
+                       lengths: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                       dh_last: Optional[torch.Tensor] = None, dh0: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of ctr_gated_scan_fwd (h: its output) for dh and dh_last
+    (None: zeros): dx, dgate, and dh0 where given, each overwritten."""
+    dev, T, D, lp = _scan_of(x, B, workspace, lengths)
+    m = [_mat(n, t, x.dtype, T, D, dev) for n, t in (("dh", dh), ("x", x), ("gate", gate), ("h", h), ("dx", dx),
+                                                     ("dgate", dgate))]
+    _check(lib().ctr_gated_scan_bwd(*m[0], *m[1], *m[2], *m[3], _DTYPES[x.dtype], lp, T, B, D, _state("h0", h0, B, D, dev),
+                                    _state("dh_last", dh_last, B, D, dev), *m[4], *m[5], _state("dh0", dh0, B, D, dev),
+                                    workspace.ptr, workspace.nbytes, _dptr(status), _on(dev, stream)), "ctr_gated_scan_bwd")

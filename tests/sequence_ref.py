@@ -1,0 +1,99 @@
+"""The sequence-tower operators in 64 bits, and how far a correct fp32
+evaluation may be from them, element by element.
+
+Scan. exp is off by at most (2 + 1.5 |g|) 2^-23 of itself (its argument is
+rounded), a quotient by 2 2^-23, so z and a by e = (8 + 2 |g|) 2^-23 of
+themselves. A state is a sum of products a_t .. a_s z_s x_s; each step adds at
+most 3 e of the sum of the terms' absolute values (z, a, the product and the
+sum), and composing pairs in blocks and groups adds at most 48 roundings of it.
+h is then rounded to its type, half a step: 2^-8 (bf16) or 2^-24 (fp32). The
+backward's g is such a sum as well; dgate takes h_{t-1} as it was written.
+"""
+import torch
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+U = 2.0 ** -23
+
+
+def recurrence(a, b):
+    """y_t = a_t y_{t-1} + b_t down the rows, y_{-1} = 0, by doubling."""
+    n = 1
+    while n < a.shape[0]:
+        b = torch.cat([b[:n], b[n:] + a[n:] * b[:-n]])
+        a = torch.cat([torch.zeros_like(a[:n]), a[n:] * a[:-n]])
+        n *= 2
+    return b
+
+
+def scan(x, gate, lengths, h0, dh=None, dh_last=None):
+    """{name: (value, bound)} of h, h_last and, for dh, dx, dgate, dh0: over
+    the rows of the sequences (lengths: a list)."""
+    out, dev = x.dtype, x.device
+    B, D, T = len(lengths), x.shape[1], sum(lengths)
+    n = torch.tensor(lengths, device=dev, dtype=torch.long)
+    begin, some = n.cumsum(0) - n, n > 0
+    first, last = begin[some], (begin + n - 1)[some]
+    X, Gt = x[:T].double(), gate[:T].double()
+    Z, Aa = torch.sigmoid(Gt), torch.sigmoid(-Gt)
+    e = (8 + 2 * Gt.abs()) * U
+    state = torch.zeros(B, D, dtype=torch.float64, device=dev) if h0 is None else h0.double()
+    inner = Aa.clone()  # 0 where a sequence begins
+    inner[first] = 0
+
+    def add(v, rows, extra):
+        v = v.clone()
+        v[rows] += extra
+        return v
+
+    def before(v, at_first):  # the row above; at a sequence's first row what is given
+        v = torch.cat([torch.zeros_like(v[:1]), v[:-1]])[:T]
+        v[first] = at_first
+        return v
+
+    h = recurrence(inner, add(Z * X, first, Aa[first] * state[some]))
+    H = recurrence(inner, add(Z * X.abs(), first, Aa[first] * state[some].abs()))  # of absolute values
+    prev, Hprev = before(h, state[some]), before(H, state[some].abs())
+    E = recurrence(inner, 3 * e * (Aa * Hprev + Z * X.abs()))
+    eh, eprev = E + 48 * U * H, before(E + 48 * U * H, 0)
+    tiny = 1e-38
+
+    def states(rows, v, empty):
+        r = empty.clone()
+        r[some] = v[rows]
+        return r
+
+    zero = torch.zeros_like(state)
+    ret = {"h": (h, eh + HALF[out] * (h.abs() + eh) + tiny),
+           "h_last": (states(last, h, state), states(last, eh, zero) + tiny)}
+    if dh is None:
+        return ret
+    end = zero if dh_last is None else dh_last.double()
+    outer = torch.cat([inner[1:], torch.zeros_like(inner[:1])])[:T]  # a_{t+1}; 0 where a sequence ends
+
+    def backwards(b):
+        return recurrence(outer.flip(0), b.flip(0)).flip(0)
+
+    d = dh[:T].double()
+    g, G = backwards(add(d, last, end[some])), backwards(add(d.abs(), last, end[some].abs()))
+    e_next = torch.cat([e[1:], e[:1]])[:T]
+    Eg = backwards(U * G + 3 * e_next * (G - add(d.abs(), last, end[some].abs()))) + 48 * U * G
+    w = (X - prev) * Z * Aa
+    ew = (eprev + HALF[out] * prev.abs()) * Z * Aa + w.abs() * 3 * e + 2 * U * (X.abs() + prev.abs()) * Z * Aa
+    if h0 is not None:  # (a sequence's first row takes h0 itself)
+        ew[first] -= (HALF[out] * prev.abs() * Z * Aa)[first]
+
+    def rounded(v, t):
+        return v, t + HALF[out] * (v.abs() + t) + tiny
+
+    ret["dx"] = rounded(g * Z, Eg * Z + G * Z * 2 * e)
+    ret["dgate"] = rounded(g * w, Eg * (w.abs() + ew) + G * ew + 2 * U * G * w.abs())
+    ret["dh0"] = (states(first, Aa * g, end), states(first, Aa * (Eg + 3 * e * G), zero) + tiny)
+    return ret
+
+
+def assert_within(got, ref, what):
+    v, tol = ref
+    err = (got.double() - v).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), "%s: %d of %d beyond the bound, worst error/bound %.3g" % (
+        what, int(bad.sum()), bad.numel(), float((err / tol).nan_to_num(float("inf")).max()))
