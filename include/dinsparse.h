@@ -560,6 +560,38 @@ int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int6
                        int64_t lddx, void* dgate_dev, int64_t lddg, float* dh0_dev, void* workspace_dev,
                        size_t ws_bytes, int32_t* status_dev, void* stream);
 
+/* Softmax cross entropy of M rows against a catalogue: the next item's loss of
+ * a sequence or user tower over all rows of an item table. layer: W [V, K] the
+ * catalogue (V = layer->R), bias nullable (a popularity correction; -inf takes
+ * an item out), act DSF_ACT_NONE, dtype DSF_BF16 or DSF_F32, K <= 8192.
+ *   z = x W^T + bias,  lse = log sum_v exp z_v,  loss = lse - z_target
+ * with target_dev int64 [M]. A target of -1 leaves its row out: loss 0, no
+ * gradient (whatever x holds there, NaN included); one outside [0, V) the same
+ * and DSF_FLAG_ID_RANGE. loss and lse are fp32 [M]. A row none of whose items
+ * is possible has lse -inf, loss NaN (0 where it is left out) and no gradient;
+ * a target that is not possible has loss +inf. Types, sums and alignment (rows
+ * of x and W) are the dense layer's above; the logits and their softmax are
+ * fp32 (the backward's exp(z - lse) carries lse's rounding, 2^-24 |lse|: logits
+ * near 0 are the most exact). The logits are never kept: the forward's workspace holds 8 bytes for
+ * each 128 of them (in blocks of 32768 rows), the backward's a piece of their
+ * gradients (256 MB, or M x 256 of them), beside operands that are laid out.
+ * Equal calls give equal bits. */
+size_t dsf_softmax_xent_workspace_bytes(const dsf_dense* layer, int64_t M, int32_t backward);
+
+int ctr_softmax_xent_fwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const int64_t* target_dev, int64_t M,
+                         float* loss_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes, int32_t* status_dev,
+                         void* stream);
+
+/* The gradients for dloss_dev fp32 [M] (nullable: ones): with dz = dloss
+ * (exp(z - lse) - [v = target]), dx_dev [M, K] = dz W, dW_dev [V, K]
+ * (contiguous) = dz^T x, both of the layer's type, and db_dev fp32 [V], each
+ * nullable and overwritten. lse_dev is the forward's. As in ctr_dense_bwd, a
+ * bf16 dz is rounded to bf16 where it enters the products. */
+int ctr_softmax_xent_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const int64_t* target_dev,
+                         const float* lse_dev, const float* dloss_dev, int64_t M, void* dx_dev, int64_t lddx,
+                         void* dW_dev, float* db_dev, void* workspace_dev, size_t ws_bytes, int32_t* status_dev,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,7 +37,8 @@ EXPORTS = ["dsf_workspace_bytes", "dsf_workspace_init", "dsf_prepare_mlp", "emb_
            "dsf_bwd_workspace_offsets",
            "dsf_dense_workspace_bytes", "ctr_dense_fwd", "ctr_dense_bwd", "ctr_glu_fwd", "ctr_glu_bwd",
            "dsf_rms_norm_workspace_bytes", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd",
-           "dsf_gated_scan_workspace_bytes", "ctr_gated_scan_fwd", "ctr_gated_scan_bwd"]
+           "dsf_gated_scan_workspace_bytes", "ctr_gated_scan_fwd", "ctr_gated_scan_bwd",
+           "dsf_softmax_xent_workspace_bytes", "ctr_softmax_xent_fwd", "ctr_softmax_xent_bwd"]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -163,6 +164,13 @@ def lib() -> ctypes.CDLL:
         L.ctr_gated_scan_bwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _vp,
                                          _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp, _vp]
         for f in (L.ctr_gated_scan_fwd, L.ctr_gated_scan_bwd):
+            f.restype = ctypes.c_int
+        L.dsf_softmax_xent_workspace_bytes.argtypes = [P(CDense), _i64, _i32]
+        L.dsf_softmax_xent_workspace_bytes.restype = _sz
+        L.ctr_softmax_xent_fwd.argtypes = [P(CDense), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
+        L.ctr_softmax_xent_bwd.argtypes = [P(CDense), _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp,
+                                           _vp]
+        for f in (L.ctr_softmax_xent_fwd, L.ctr_softmax_xent_bwd):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -776,3 +784,53 @@ def ctr_gated_scan_bwd(dh: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, h:
     _check(lib().ctr_gated_scan_bwd(*m[0], *m[1], *m[2], *m[3], _DTYPES[x.dtype], lp, T, B, D, _state("h0", h0, B, D, dev),
                                     _state("dh_last", dh_last, B, D, dev), *m[4], *m[5], _state("dh0", dh0, B, D, dev),
                                     workspace.ptr, workspace.nbytes, _dptr(status), _on(dev, stream)), "ctr_gated_scan_bwd")
+
+
+class SoftmaxXentWorkspace:
+    """Scratch of the cross entropy of up to M rows against a catalogue layer;
+    backward: for the gradients too."""
+
+    def __init__(self, layer: DenseLayer, M: int, backward: bool = False):
+        self.nbytes = int(lib().dsf_softmax_xent_workspace_bytes(layer._ref, int(M), int(bool(backward))))
+        if self.nbytes == 0:
+            raise DsfError(DSF_EINVAL, "dsf_softmax_xent_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=layer.device)
+        self.ptr, self.dev = self.buf.data_ptr(), layer.dev
+
+
+def _target_of(target: torch.Tensor, M: int, dev: int) -> int:
+    if target.dtype is not torch.int64 or target.shape != (M,) or target.get_device() != dev or not target.is_contiguous():
+        raise ValueError("target: contiguous int64 [%d] on cuda:%d expected" % (M, dev))
+    return target.data_ptr()
+
+
+def ctr_softmax_xent_fwd(layer: DenseLayer, x: torch.Tensor, target: torch.Tensor, loss: torch.Tensor, lse: torch.Tensor,
+                         workspace: SoftmaxXentWorkspace, status: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """loss [M] = lse - z_target, lse [M] = log sum exp of z = x W^T + bias over
+    the catalogue's V rows W (layer, without an activation); target int64 [M],
+    -1: the row is left out (loss 0). The logits are not kept."""
+    dev, M, (xp, ldx) = _x_of(layer, x, workspace)
+    _check(lib().ctr_softmax_xent_fwd(layer._ref, xp, ldx, _target_of(target, M, dev), M, _vec("loss", loss, M, dev),
+                                      _vec("lse", lse, M, dev), workspace.ptr, workspace.nbytes, _dptr(status),
+                                      _on(dev, stream)), "ctr_softmax_xent_fwd")
+    return loss
+
+
+def ctr_softmax_xent_bwd(layer: DenseLayer, x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                         workspace: SoftmaxXentWorkspace, dloss: Optional[torch.Tensor] = None,
+                         dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                         db: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of ctr_softmax_xent_fwd (lse: its output) for dloss [M] (None:
+    ones), each overwritten where given."""
+    dev, M, (xp, ldx) = _x_of(layer, x, workspace)
+    dxp, lddx = (None, 0) if dx is None else _mat("dx", dx, layer.type, M, layer.K, dev)
+    dWp = None
+    if dW is not None:
+        dWp, _ = _mat("dW", dW, layer.type, layer.R, layer.K, dev)
+        if not dW.is_contiguous():
+            raise ValueError("dW: contiguous expected")
+    _check(lib().ctr_softmax_xent_bwd(layer._ref, xp, ldx, _target_of(target, M, dev), _vec("lse", lse, M, dev),
+                                      _vec("dloss", dloss, M, dev), M, dxp, lddx, dWp, _vec("db", db, layer.R, dev),
+                                      workspace.ptr, workspace.nbytes, _dptr(status), _on(dev, stream)),
+           "ctr_softmax_xent_bwd")

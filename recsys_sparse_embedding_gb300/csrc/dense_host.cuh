@@ -233,6 +233,8 @@ struct LayJob {
   const void* src;
   void* dst;
   long long ld, rows, ldd, cols;
+  const long long* target;  // nullable: rows whose target lies outside [0, ids) become zero
+  long long ids;
 };
 struct LayJobs {
   LayJob j[3];
@@ -283,9 +285,14 @@ __global__ void __launch_bounds__(256) lay_kernel(const __grid_constant__ LayJob
    for (int c = c0 * V; c < j.ldd; c += tpr * V) {
     const uint8_t* s = static_cast<const uint8_t*>(j.src) + (r * j.ld + c) * ES;
     uint32_t w[NW];
+    const long long id = j.target ? __ldg(j.target + r) : 0;
+    const bool zero = j.target && (id < 0 || id >= j.ids);
     // (whole vectors where all of them lie inside the matrix; what a row's last
     // piece takes from behind the row is never read)
-    if (s - 15 >= static_cast<const uint8_t*>(j.src) && s + 16 * NV <= end) {
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < NW; ++k) w[k] = 0;
+    } else if (s - 15 >= static_cast<const uint8_t*>(j.src) && s + 16 * NV <= end) {
       load_shifted<NV, ES>(s, w);
     } else {
 #pragma unroll
@@ -501,10 +508,10 @@ bool lay_operands(const Ctx& c, const void* x, long long ldx, const void* dy, lo
   LayJob jobs[3];
   int n = 0;
   if (laid_out(c.l->dtype, c.l->K)) {
-    jobs[n++] = LayJob{x, c.ws + c.w.xp, ldx, c.M, c.w.kp, c.l->K};
-    jobs[n++] = LayJob{c.l->W, c.ws + c.w.wp, c.l->ldw, c.l->R, c.w.kp, c.l->K};
+    jobs[n++] = LayJob{x, c.ws + c.w.xp, ldx, c.M, c.w.kp, c.l->K, nullptr, 0};
+    jobs[n++] = LayJob{c.l->W, c.ws + c.w.wp, c.l->ldw, c.l->R, c.w.kp, c.l->K, nullptr, 0};
   }
-  if (dy && laid_out(c.l->dtype, c.N)) jobs[n++] = LayJob{dy, c.ws + c.w.gp, lddy, c.M, c.w.np, c.N};
+  if (dy && laid_out(c.l->dtype, c.N)) jobs[n++] = LayJob{dy, c.ws + c.w.gp, lddy, c.M, c.w.np, c.N, nullptr, 0};
   return lay(c.l->dtype, jobs, n, c.s);
 }
 

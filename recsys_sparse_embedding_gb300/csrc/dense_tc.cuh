@@ -78,6 +78,11 @@ enum Epi {
                  // terms) from in = dy; column sums
   kEpiOut = 2,   // out = the accumulator
   kEpiPart = 3,  // fp32 partial sums of a K-split: plane split * planes + (half or batch); kDual: job 0 only
+  kEpiAcc = 5,   // the same, added to what the planes hold
+  // softmax cross entropy over the columns (z in units of log 2 where it is an
+  // exponent; the target's column per row):
+  kEpiLse = 6,   // per row and tile the maximum and the sum of exp(z - it); z of the target
+  kEpiXent = 7,  // out = g (exp(z - lse) - [column = target]) (fp32: its three terms); column sums
 };
 enum Kind { kBf16 = 0, kE4m3 = 1 };
 // A and B K-major; B MN-major; both; two products in one launch, job 0 with
@@ -123,7 +128,12 @@ struct TcArgs {
   const void* in;               // kEpiRes, kEpiDz
   long long ldi;
   int in_vec;   // rows at 16-byte boundaries
-  float* part;  // kEpiDz: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
+  float* part;  // kEpiDz, kEpiXent: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
+  const long long* target;  // kEpiLse, kEpiXent: per row the target's column in all of W (outside: none)
+  int v0;                   // the first column here, of them
+  float2* stat;             // kEpiLse: [N tile][M] (maximum, sum)
+  float* zt;                // kEpiLse: [M]
+  const float2* rows;       // kEpiXent: [M] (lse, g)
   int* status;
 };
 
@@ -227,7 +237,7 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 // ---------------------------------------------------------------- shapes
 template <int CG, int BN, int MAJOR, bool GATED, int EPI, bool F32>
 struct Shape {
-  using TO = typename std::conditional<F32 || EPI == kEpiPart, float, __nv_bfloat16>::type;  // input and output
+  using TO = typename std::conditional<F32 || EPI == kEpiPart || EPI == kEpiAcc, float, __nv_bfloat16>::type;  // input and output
   static constexpr int ON = GATED ? BN / 2 : BN;  // output columns per tile
   // Epilogue warps: four per lane quarter (scheduler). Two where the kernel
   // needs the registers (168 instead of 96 a thread: a gated dz, whose items
@@ -241,7 +251,7 @@ struct Shape {
   static constexpr int BNC = BN / CG;  // B rows (or MN-major columns) in this CTA
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BNC * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int EBYTES = kEpiWarps * ITEM;
-  static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiRes || EPI == kEpiDz;
+  static constexpr bool BIAS = EPI == kEpiFwd || EPI == kEpiRes || EPI == kEpiDz || EPI == kEpiLse || EPI == kEpiXent;
   // bias floats of an item that each epilogue warp keeps in shared memory (the
   // gated forward's six stages leave room for the gate's alone; the up half's
   // are handed round by shuffles)
@@ -269,6 +279,8 @@ struct Bars {
   int abort_;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
+
+constexpr float kFar = 3e38f;  // (stands for an infinite maximum, so that differences of maxima stay defined)
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -542,9 +554,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     uint8_t* buf = sE + warp * S::ITEM;
     float* wbias = sBias + warp * S::BIAS_N;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
-    constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz;
+    constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz || EPI == kEpiAcc;
+    constexpr bool XENT = EPI == kEpiLse || EPI == kEpiXent;
     constexpr bool SCALED = KIND == kE4m3 && FWD;
-    constexpr bool TERMS_OUT = F32 && EPI == kEpiDz;  // dz leaves as three bf16 terms
+    constexpr bool TERMS_OUT = F32 && (EPI == kEpiDz || EPI == kEpiXent);  // dz leaves as three bf16 terms
     constexpr bool PAIR = GATED && EPI != kEpiPart;   // an item takes gate and up accumulators
     constexpr int GR = S::kGroups, ROWB = CW * int(sizeof(TO));
     constexpr int halves = GATED ? 2 : 1;
@@ -552,7 +565,10 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     constexpr int NCH = (GATED && EPI == kEpiPart ? BN : ON) / CW;
     constexpr int NI = (NCH + GR - 1) / GR;  // items per warp and tile
     const bool has_bias = S::BIAS && a.bias;
-    const TO* in = static_cast<const TO*>(a.in);
+    const TO* in0 = static_cast<const TO*>(a.in);
+    auto in_of = [&](const Unit& t) {  // (kEpiAcc: the unit's plane)
+      return EPI == kEpiAcc ? in0 + (t.split * job0.nb + t.batch) * job0.out_plane : in0;
+    };
     const uint32_t tempty0 = CG == 2 ? mapa(smem_u32(&bars->tempty[0]), 0) : smem_u32(&bars->tempty[0]);
 
     // columns j .. j + 7 of this lane's row, from and to the buffer
@@ -593,7 +609,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     // by side on a row. Pieces past the matrix's edge element by element.
     constexpr int EL = 16 / int(sizeof(TO)), LPR = CW / EL, RPI = 32 / LPR, NV = 32 / RPI;
     const int piece_row = lane / LPR, piece_col = lane % LPR * EL;
-    auto load_item = [&](uint4* v, int r0, int c0) {
+    auto load_item = [&](const TO* in, uint4* v, int r0, int c0) {
       const int cc = c0 + piece_col;
       const TO* p0 = in + (long long)(r0 + piece_row) * a.ldi + cc;
       const long long step = RPI * a.ldi;
@@ -668,7 +684,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     auto prefetch = [&](bool any, const Unit& t, int c) {
       if (!IN && !S::BIAS) return;
       const int r = any ? t.m0 + 32 * q : job0.M, cc = t.n0 + c * CW;
-      if (PRE) load_item(pin, a.in_vec ? r : job0.M, cc);
+      const TO* in = in_of(t);
+      if (PRE) load_item(in, pin, a.in_vec ? r : job0.M, cc);
       if (IN && !(PRE && a.in_vec) && r + lane < job0.M && cc < job0.N) {
         const TO* p = in + (long long)(r + lane) * a.ldi + cc;
         prefetch_l2(p);
@@ -686,13 +703,25 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         prefetch(true, t, c + GR);
       } else {
         Unit n;
-        n.m0 = n.n0 = 0;
+        n.m0 = n.n0 = n.split = n.batch = 0;
         prefetch(unit_at(i + 1, n) && grp < NCH, n, grp);
       }
     };
     Unit t;
-    t.m0 = t.n0 = 0;
+    t.m0 = t.n0 = t.split = t.batch = 0;
     prefetch(unit_at(0, t) && grp < NCH, t, grp);
+    // what a cross entropy's next unit takes per row: the target, lse and g
+    long long next_target = -1;
+    float2 next_row = make_float2(0.f, 0.f);
+    auto prefetch_row = [&](int i) {
+      if (!XENT) return;
+      Unit n;
+      if (!unit_at(i, n)) return;
+      const int r = n.m0 + 32 * q + lane;
+      next_target = r < job0.M ? __ldg(a.target + r) : -1;
+      if (EPI == kEpiXent) next_row = r < job0.M ? __ldg(a.rows + r) : make_float2(0.f, 0.f);
+    };
+    prefetch_row(0);
 
     uint32_t run = 0;
     bool ok = true;
@@ -709,9 +738,39 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       if (lane == 0) mbar_arrive_relaxed(tempty0 + (run % S::NACC) * 8u);
       ++run;
     };
+    // kEpiLse: the tile's maximum and sum of each row, of the warps that share its
+    // rows (by way of their buffers, two in turn: a warp is at most one unit ahead)
+    int units_met = 0;
+    auto unit_stat = [&](int i, const Unit& t, int row, float top, float total) {
+      const int at = (i & 1) * 32 + lane;
+      reinterpret_cast<float2*>(buf)[at] = make_float2(top, total);
+      ++units_met;
+      asm volatile("bar.sync %0, %1;" ::"r"(2 + q), "n"(32 * GR) : "memory");
+      if (grp != 0) return;
+      float2 p[GR];
+      float m = -kFar, s = 0.f;
+#pragma unroll
+      for (int k = 0; k < GR; ++k) {
+        p[k] = reinterpret_cast<const float2*>(sE + (q + 4 * k) * S::ITEM)[at];
+        m = fmaxf(m, p[k].x);
+      }
+#pragma unroll
+      for (int k = 0; k < GR; ++k) s += p[k].y * exp2_fast(p[k].x - m);
+      if (row < job0.M) a.stat[(long long)(t.n0 / ON) * job0.M + row] = make_float2(m, s);
+    };
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const Job& jb = a.job[DUAL ? t.job : 0];
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
+      const TO* in = in_of(t);
+      // the target's column here (or one that no item has)
+      int tgt = -1;
+      float2 of_row = next_row;
+      if (XENT) {
+        const long long d = next_target - a.v0;
+        tgt = next_target >= 0 && d >= 0 && d < jb.N ? int(d) : -1;
+        prefetch_row(i + 1);
+      }
+      float top = -kFar, total = 0.f;  // kEpiLse: over the warp's items
       // one item: 32 rows by CW columns. In runs: pg, pu hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
@@ -740,7 +799,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
           if (a.in_vec) {
             if (!PRE) {
               uint4 v[NV];
-              load_item(v, row0, col0);
+              load_item(in, v, row0, col0);
 #pragma unroll
               for (int i = 0; i < NV; ++i)
                 *reinterpret_cast<uint4*>(buf + slot<ROWB>(i * RPI + piece_row, piece_col * int(sizeof(TO)))) = v[i];
@@ -779,6 +838,74 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
           }
         }
         if (!RUN) tmem_ld_wait();
+        if (XENT) {
+          const float* b = wbias;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(b + j);
+            float2 lo = make_float2(g[j], g[j + 1]), hi = make_float2(g[j + 2], g[j + 3]);
+            lo = lo + make_float2(f.x, f.y);
+            hi = hi + make_float2(f.z, f.w);
+            g[j] = lo.x, g[j + 1] = lo.y, g[j + 2] = hi.x, g[j + 3] = hi.y;
+          }
+          const bool target_here = __any_sync(0xffffffffu, unsigned(tgt - col0) < 32u);
+          if constexpr (EPI == kEpiLse) {
+            if (col0 + CW > jb.N) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (col0 + k >= jb.N) g[k] = -INFINITY;
+            }
+            if (target_here) {
+              float z = 0.f;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (tgt - col0 == k) z = g[k];
+              if (unsigned(tgt - col0) < 32u && row < jb.M) a.zt[row] = z;
+            }
+            float m[4];  // (fmaxf leaves a NaN to the sum)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(g[k], g[k + 4]), g[k + 8]);
+#pragma unroll
+            for (int k = 12; k < 32; k += 4)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], g[k + e]);
+            const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            const float now = fmaxf(top, fminf(most * kLog2e, kFar));
+            float2 s[2] = {make_float2(total * exp2_fast(top - now), 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 e = __ffma2_rn(make_float2(g[k + 2 * h], g[k + 2 * h + 1]), pair(kLog2e), pair(-now));
+                s[h] = s[h] + make_float2(exp2_fast(e.x), exp2_fast(e.y));
+              }
+            top = now;
+            total = (s[0].x + s[0].y) + (s[1].x + s[1].y);
+            __syncwarp();  // (the bias is read)
+            return;
+          } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 e = __ffma2_rn(make_float2(g[k], g[k + 1]), pair(kLog2e), pair(-of_row.x));
+            g[k] = of_row.y * exp2_fast(e.x);
+            g[k + 1] = of_row.y * exp2_fast(e.y);
+          }
+          if (of_row.y == 0.f) {  // (a row left out, whatever it holds)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) g[k] = 0.f;
+          }
+          if (target_here) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (tgt - col0 == k) g[k] -= of_row.y;
+          }
+          if (col0 + CW > jb.N) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (col0 + k >= jb.N) g[k] = 0.f;
+          }
+          }
+        }
         // eight columns at a time, from the accumulators to the buffer
         auto math = [&](auto act_tag) {
           constexpr int ACT = decltype(act_tag)::value;
@@ -798,13 +925,14 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             float b[8], d[8];  // (16 bytes a time: shared memory is what the MMAs run on)
 #pragma unroll
             for (int k = 0; k < 8; k += 4) {
-              if (S::BIAS) *reinterpret_cast<float4*>(b + k) = *reinterpret_cast<const float4*>(wbias + j + k);
+              if (S::BIAS && !XENT) *reinterpret_cast<float4*>(b + k) = *reinterpret_cast<const float4*>(wbias + j + k);
               if (PAIR && S::BIAS_N == 64)
                 *reinterpret_cast<float4*>(d + k) = *reinterpret_cast<const float4*>(wbias + 32 + j + k);
             }
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-              if (!S::BIAS) continue;
+              if (EPI == kEpiAcc) v[k] += x[k], v[k + 1] += x[k + 1];
+              if (!S::BIAS || XENT) continue;
               const float2 b2 = make_float2(b[k], b[k + 1]);
               float2 z = make_float2(v[k], v[k + 1]);
               z = z + b2;
@@ -872,7 +1000,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
           }
         } else {
           // (two products: only job 0 has partial sums)
-          const bool part = EPI == kEpiPart && (!DUAL || t.job == 0);
+          const bool part = EPI == kEpiAcc || (EPI == kEpiPart && (!DUAL || t.job == 0));
           int plane = t.batch;
           if (part) plane = GATED ? t.split * 2 + (c * CW) / ON : t.split * jb.nb + t.batch;
           TO* o = static_cast<TO*>(jb.out) + plane * jb.out_plane;
@@ -885,7 +1013,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             for (int j = 0; j < 32; j += 8) put8(j, up + (PAIR ? j : 0));
             store_item(jb, o + jb.out_plane, row0, col0);
           }
-          if (EPI == kEpiDz && a.part) {
+          if ((EPI == kEpiDz || EPI == kEpiXent) && a.part) {
             sums(g, 0);
             if (PAIR) sums(up, 1);
           }
@@ -917,15 +1045,21 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         }
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (grp + GR * i < NCH) do_item(grp + GR * i, 0, sum[i][0], sum[i][PAIR ? 1 : 0]);
+        for (int k = 0; k < NI; ++k)
+          if (grp + GR * k < NCH) do_item(grp + GR * k, 0, sum[k][0], sum[k][PAIR ? 1 : 0]);
+        if constexpr (EPI == kEpiLse) unit_stat(i, t, row, top, total);
       } else {
         if (!wait_run()) break;
         const uint32_t tacc = tbase + (run % S::NACC) * S::ACC + lane_base;
 #pragma unroll 1
         for (int c = grp; c < NCH; c += GR) do_item(c, tacc, nullptr, nullptr);
         done_run();
+        if constexpr (EPI == kEpiLse) unit_stat(i, t, row, top, total);
       }
+    }
+    if constexpr (EPI == kEpiLse) {  // (the other warps wait for one that gave up)
+      if (!ok)
+        for (; unit_at(units_met, t); ++units_met) asm volatile("bar.sync %0, %1;" ::"r"(2 + q), "n"(32 * GR) : "memory");
     }
     if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
   }
@@ -964,6 +1098,8 @@ bool run_e4m3_product(const Product& p, cudaStream_t s);  // K-major, e4m3 opera
 bool run_dz_product(const Product& p, cudaStream_t s);
 bool run_grad_product(const Product& p, cudaStream_t s);  // MN-major operands
 bool run_dual_product(const Product& p, cudaStream_t s);
+bool run_xent_product(const Product& p, cudaStream_t s);  // kEpiLse, kEpiXent: configurations 0 and 1
+bool run_acc_product(const Product& p, cudaStream_t s);   // kEpiAcc, B MN-major
 
 // How two products' units go to C clusters: the longer units dealt round (to
 // the first `rest` clusters h0, to the others h0 - 1), the others so that

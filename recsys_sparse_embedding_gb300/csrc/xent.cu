@@ -1,0 +1,360 @@
+// The softmax cross entropy of rows against a catalogue (ctr_softmax_xent_* in
+// dinsparse.h): z = x W^T + bias over V columns, lse = log sum exp z, loss =
+// lse - z_target, dz = g (exp(z - lse) - [v = target]), dx = dz W, dW = dz^T x,
+// db = sum of dz.
+//
+// The logits are never kept. The forward is one pass of the product x W^T whose
+// epilogue reduces a tile's columns to a (maximum, sum of exponentials) pair per
+// row (8 bytes for 256 or 128 logits); a second kernel merges a row's pairs.
+// Exponents are in units of log 2: exp(z - m) = 2^(z log2 e - m'), and m' is
+// kept as it was subtracted, so its rounding cancels. The backward takes the
+// catalogue in pieces: the product again, its epilogue writing the piece's dz
+// (one rounding to bf16, or an fp32 operand's three terms), then dW's rows of
+// the piece, complete, and dx added up over the pieces in fp32 planes. So
+// memory holds M x (a piece), whatever V is, and sums run in a fixed order.
+#include "dense_host.cuh"
+
+namespace dsf {
+namespace dense {
+namespace {
+
+constexpr int kMaxK = 8192;
+constexpr long long kFwdRows = 32768;       // rows per forward product (its pairs take V / 16 bytes a row)
+constexpr size_t kPieceBytes = 256u << 20;  // dz of a piece
+
+// ---------------------------------------------------------------- small kernels
+// A row's pairs [nt][M] to lse and loss. `rows` (a power of two up to 32)
+// neighbouring rows per block; the other threads share out the tiles.
+struct MergeArgs {
+  const float2* stat;
+  const float* zt;
+  const long long* target;
+  float *loss, *lse;
+  long long M;
+  int nt, rows;
+  long long V;
+  int* status;
+};
+constexpr int kMerge = 512;
+__global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ MergeArgs a) {
+  __shared__ float2 part[kMerge];
+  pdl_go();
+  pdl_wait();
+  const int r = threadIdx.x & (a.rows - 1), slice = threadIdx.x / a.rows, slices = kMerge / a.rows;
+  const long long row = (long long)blockIdx.x * a.rows + r;
+  float m = -kFar, s = 0.f;
+  if (row < a.M) {
+    constexpr int U = 8;
+    for (int t0 = slice; t0 < a.nt; t0 += slices * U) {
+      float2 p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        p[u] = t0 + u * slices < a.nt ? __ldg(a.stat + (long long)(t0 + u * slices) * a.M + row) : make_float2(-kFar, 0.f);
+      float now = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) now = fmaxf(now, p[u].x);
+      s *= exp2_fast(m - now);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += p[u].y * exp2_fast(p[u].x - now);
+      m = now;
+    }
+  }
+  part[threadIdx.x] = make_float2(m, s);
+  for (int n = slices / 2; n; n >>= 1) {
+    __syncthreads();
+    if (slice < n) {
+      const float2 p = part[threadIdx.x], q = part[threadIdx.x + n * a.rows];
+      const float now = fmaxf(p.x, q.x);
+      part[threadIdx.x] = make_float2(now, p.y * exp2_fast(p.x - now) + q.y * exp2_fast(q.x - now));
+    }
+  }
+  if (slice != 0 || row >= a.M) return;
+  const float2 p = part[threadIdx.x];
+  const float lse = (p.x + log2f(p.y)) * 0.69314718055994530942f;
+  const long long t = a.target[row];
+  const bool there = t >= 0 && t < a.V;
+  a.lse[row] = lse;
+  a.loss[row] = there ? lse - a.zt[row] : 0.f;
+  if (!there && t != -1 && a.status) atomicOr(a.status, DSF_FLAG_ID_RANGE);
+}
+
+// What the backward's product takes per row: lse in units of log 2, and dloss
+// (0: the row is left out; also where no column is possible).
+__global__ void __launch_bounds__(256) rows_kernel(const long long* target, const float* lse, const float* dloss, long long M,
+                                                   long long V, float2* rows, int* status) {
+  pdl_go();
+  pdl_wait();
+  const long long r = blockIdx.x * 256LL + threadIdx.x;
+  if (r >= M) return;
+  const long long t = target[r];
+  const float l = lse[r];
+  bool there = t >= 0 && t < V;
+  if (!there && t != -1 && status) atomicOr(status, DSF_FLAG_ID_RANGE);
+  if (l == -INFINITY) there = false;
+  rows[r] = make_float2(there ? l * kLog2e : 0.f, there ? (dloss ? dloss[r] : 1.f) : 0.f);
+}
+
+// ---------------------------------------------------------------- layout
+// Columns of a piece for M rows.
+long long piece_of(const dsf_dense* l, long long M) {
+  const long long terms = l->dtype == DSF_F32 ? 3 : 1, all = up(l->R, 256);
+  const long long p = (long long)(kPieceBytes / (2 * size_t(terms) * size_t(M))) / 256 * 256;
+  return p < 256 ? 256 : (p < all ? p : all);
+}
+
+struct XLayout {
+  size_t xp, wp, stat, zt, rows, dz, sums, part, planes, total;
+  long long kp;
+};
+XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
+  XLayout w{};
+  const bool f32 = l->dtype == DSF_F32;
+  const size_t terms = f32 ? 3 : 1, m = size_t(M);
+  w.kp = up(l->K, 8);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = o;
+    o += align256(bytes);
+    return here;
+  };
+  const bool lo = laid_out(l->dtype, l->K);
+  w.xp = take(lo || backward ? terms * m * w.kp * 2 : 0);
+  w.wp = take(lo ? terms * size_t(l->R) * w.kp * 2 : 0);
+  const size_t block = m < size_t(kFwdRows) ? m : size_t(kFwdRows);
+  const size_t stat = block * size_t((l->R + 127) / 128) * 8;
+  // the forward's and the backward's scratch share their room
+  size_t o0 = o;
+  w.stat = take(stat);
+  w.zt = take(m * 4);
+  size_t most = o;
+  if (backward) {
+    o = o0;
+    const size_t all = size_t(up(l->R, 256)), K4 = size_t(up(l->K, 4)) * 4;
+    auto least = [](size_t a, size_t b) { return a < b ? a : b; };
+    auto greatest = [](size_t a, size_t b) { return a > b ? a : b; };
+    // (each is at least what any smaller M takes: a piece is at most kPieceBytes of dz, or 256 columns)
+    w.rows = take(m * 8);
+    w.dz = take(least(2 * terms * m * all, greatest(kPieceBytes, 2 * terms * m * 256)));
+    w.sums = take(least((m + 31) / 32 * all * 4, kPieceBytes / 16 / terms + (m + 31) / 32 * 256 * 4 + all * 4));
+    // planes of dx: the splits of a product, or those of sums of more than 65536 terms
+    const size_t outputs = m * K4;
+    const size_t planes = greatest(least(outputs * kMaxSplits, kPartBytes), outputs + K4 * (kPieceBytes / 131072 + 1));
+    w.planes = take(planes);
+    // partial sums of dW's rows of a piece, or, where one piece is all, of dx
+    const size_t wide = all * K4;
+    w.part = take(greatest(greatest(least(wide * kMaxSplits, kPartBytes), planes),
+                           M > 65536 ? least(wide, K4 * (256 + kPieceBytes / 2 / 65536)) * kMaxSplits : 0));
+    most = most > o ? most : o;
+  }
+  w.total = most + 256;
+  return w;
+}
+
+// ---------------------------------------------------------------- products
+// The logits' tiles: 256 or 128 rows. (The narrow one where few rows leave
+// half of the wide one empty.)
+void plan_xent(Product& p, long long M, long long N, long long nkb) {
+  const Cost cost{p.f32};
+  double best = 1e300;
+  Job o = p.a.job[0];
+  for (int cfg = 0; cfg < 2; ++cfg) {
+    set_tiles(o, cfg, M, N, 1, false, p.f32, nkb, 1, 1);
+    const long long waves = (tiles_of(o) + slots_of(cfg) - 1) / slots_of(cfg);
+    const double c = cost.run(cfg, double(waves), double(o.kbps));
+    if (c < best) {
+      best = c;
+      p.cfg = cfg;
+      p.a.job[0] = o;
+    }
+  }
+}
+
+bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, long long M, float* loss,
+              float* lse, uint8_t* ws, int* status, cudaStream_t s) {
+  const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
+  const XLayout w = xent_layout(l, M, false);
+  const int terms = f32 ? 3 : 1, es = esize(l->dtype);
+  if (lo) {
+    const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, l->K, nullptr, 0},
+                            {l->W, ws + w.wp, l->ldw, l->R, w.kp, l->K, nullptr, 0}};
+    if (!lay(l->dtype, jobs, 2, s)) return false;
+  }
+  float2* stat = reinterpret_cast<float2*>(ws + w.stat);
+  float* zt = reinterpret_cast<float*>(ws + w.zt);
+  for (long long r = 0; r < M; r += kFwdRows) {
+    const long long m = M - r < kFwdRows ? M - r : kFwdRows;
+    Product p{};
+    p.A = lo ? Mat{ws + w.xp + r * w.kp * 2, m, l->K, w.kp, terms, M * w.kp}
+             : Mat{static_cast<const uint8_t*>(x) + r * ldx * es, m, l->K, ldx, 1, 0};
+    p.B = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, terms, l->R * w.kp} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
+    p.major = kKK;
+    p.f32 = f32;
+    p.epi = kEpiLse;
+    p.a.job[0].a_term = p.a.job[0].b_term = 1;
+    plan_xent(p, m, l->R, (l->K + 63) / 64);
+    p.a.bias = l->bias;
+    p.a.target = target + r;
+    p.a.stat = stat;
+    p.a.zt = zt + r;
+    p.a.status = status;
+    if (!run_xent_product(p, s)) return false;
+    MergeArgs g{stat, zt + r, target + r, loss + r, lse + r, m, p.a.job[0].nt, 32, l->R, status};
+    while (g.rows > 1 && g.rows / 2 >= m) g.rows /= 2;
+    while (g.rows > 8 && (m + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
+    if (!pdl_launch(merge_kernel, dim3(unsigned((m + g.rows - 1) / g.rows)), kMerge, s, g)) return false;
+  }
+  return true;
+}
+
+bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, const float* lse,
+              const float* dloss, long long M, void* dx, long long lddx, void* dW, float* db, uint8_t* ws, int* status,
+              cudaStream_t s) {
+  const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
+  const XLayout w = xent_layout(l, M, true);
+  const int terms = f32 ? 3 : 1, es = esize(l->dtype), K = l->K;
+  // x with the rows that are left out as zeros: their dz is zero, and dW adds
+  // dz x, whatever x holds there
+  const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, K, target, l->R},
+                          {l->W, ws + w.wp, l->ldw, l->R, w.kp, K, nullptr, 0}};
+  if (!lay(l->dtype, jobs, lo ? 2 : 1, s)) return false;
+  float2* rows = reinterpret_cast<float2*>(ws + w.rows);
+  if (!pdl_launch(rows_kernel, dim3(unsigned((M + 255) / 256)), 256, s, target, lse, dloss, M, (long long)l->R, rows, status))
+    return false;
+  float* sums = reinterpret_cast<float*>(ws + w.sums);
+  Ctx c{};
+  c.l = l;
+  c.M = M;
+  c.halves = 1;
+  c.es = c.eo = es;
+  c.terms = terms;
+  c.kbe = 64;
+  c.ws = ws;
+  c.w.part = w.part;
+  c.status = status;
+  c.s = s;
+  c.X = Mat{ws + w.xp, M, K, w.kp, terms, M * w.kp};
+  const long long P = piece_of(l, M);
+  const bool one = P >= l->R;
+  Product acc{};  // dx over the pieces: the first piece's plan for all of them
+  int planes = 0;
+  for (long long v = 0; v < l->R; v += P) {
+    const long long n = l->R - v < P ? l->R - v : P, np = up(n, 8);
+    c.N = int(n);
+    c.W = lo ? Mat{ws + w.wp + v * w.kp * 2, n, K, w.kp, terms, l->R * w.kp}
+             : Mat{static_cast<const uint8_t*>(l->W) + v * l->ldw * es, n, K, l->ldw, 1, 0};
+    const Mat dz{ws + w.dz, M, n, np, terms, M * np};
+    Product p{};
+    p.A = c.X;
+    p.B = c.W;
+    p.major = kKK;
+    p.f32 = f32;
+    p.epi = kEpiXent;
+    p.a.job[0].a_term = p.a.job[0].b_term = 1;
+    plan_xent(p, M, n, (K + 63) / 64);
+    p.a.bias = l->bias ? l->bias + v : nullptr;
+    p.a.part = db ? sums : nullptr;
+    p.a.target = target;
+    p.a.v0 = int(v);
+    p.a.rows = rows;
+    p.a.status = status;
+    set_out(p.a.job[0], ws + w.dz, np, 2);
+    if (!run_xent_product(p, s)) return false;
+    if (db && !colsum(sums, (M + 31) / 32, int(n), db + v, s)) return false;
+    void* dWv = dW ? static_cast<uint8_t*>(dW) + v * K * es : nullptr;
+    if (one) return grad_products(c, dz, dx, lddx, dWv);
+    if (dWv && !grad_products(c, dz, nullptr, 0, dWv)) return false;
+    if (!dx) continue;
+    const long long nkb = (n + 63) / 64;
+    Job& o = acc.a.job[0];
+    if (v == 0) {
+      acc.major = kKN;
+      acc.f32 = f32;
+      acc.a.status = status;
+      plan(acc, M, K, 1, nkb, 1, true);
+      planes = o.splits;
+      acc.epi = kEpiPart;
+    } else {
+      acc.epi = kEpiAcc;
+      set_tiles(o, acc.cfg, M, K, 1, false, f32, nkb, 1, planes);
+    }
+    o.a_term = o.b_term = o.a_seg = 1;
+    o.out = ws + w.planes;
+    o.ldo = up(K, 4);
+    o.out_plane = M * o.ldo;
+    o.out_vec = 1;
+    acc.A = dz;
+    acc.B = c.W;
+    acc.a.in = o.out;
+    acc.a.ldi = o.ldo;
+    acc.a.in_vec = 1;
+    if (!(v == 0 ? run_grad_product(acc, s) : run_acc_product(acc, s))) return false;
+  }
+  if (!dx) return true;
+  c.w.part = w.planes;
+  acc.a.job[0].splits = planes;
+  FinishArgs f{};
+  f.planes = 1;
+  f.out = dx;
+  f.ldo = lddx;
+  return finish(c, acc, f, f32);
+}
+
+// ---------------------------------------------------------------- checks
+int check_xent(const dsf_dense* l) {
+  if (int rc = check_layer(l, false)) return rc;
+  if (l->dtype == DSF_E4M3 || l->K > kMaxK) return DSF_EUNSUPPORTED;
+  return l->act == DSF_ACT_NONE ? DSF_OK : DSF_EINVAL;
+}
+
+}  // namespace
+}  // namespace dense
+}  // namespace dsf
+
+using namespace dsf::dense;
+
+extern "C" {
+
+size_t dsf_softmax_xent_workspace_bytes(const dsf_dense* l, int64_t M, int32_t backward) {
+  if (check_xent(l) != DSF_OK || M < 0 || M > kMaxM || backward < 0 || backward > 1) return 0;
+  return xent_layout(l, M, backward != 0).total;
+}
+
+int ctr_softmax_xent_fwd(const dsf_dense* l, const void* x, int64_t ldx, const int64_t* target, int64_t M, float* loss,
+                         float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  if (int rc = check_xent(l)) return rc;
+  if (M < 0 || M > kMaxM) return DSF_EINVAL;
+  if (M == 0) return DSF_OK;
+  if (!rows_ok(x, ldx, l->K, esize(l->dtype)) || !target || !at(target, 8) || !loss || !at(loss, 4) || !lse || !at(lse, 4))
+    return DSF_EINVAL;
+  if (!ws || !at(ws, 256) || ws_bytes < xent_layout(l, M, false).total) return DSF_EWORKSPACE;
+  return xent_fwd(l, x, ldx, reinterpret_cast<const long long*>(target), M, loss, lse, static_cast<uint8_t*>(ws), status,
+                  static_cast<cudaStream_t>(stream))
+             ? DSF_OK
+             : DSF_ECUDA;
+}
+
+int ctr_softmax_xent_bwd(const dsf_dense* l, const void* x, int64_t ldx, const int64_t* target, const float* lse,
+                         const float* dloss, int64_t M, void* dx, int64_t lddx, void* dW, float* db, void* ws,
+                         size_t ws_bytes, int32_t* status, void* stream) {
+  if (int rc = check_xent(l)) return rc;
+  if (M < 0 || M > kMaxM) return DSF_EINVAL;
+  const int es = esize(l->dtype);
+  if (!at(dW, es) || !at(db, 4)) return DSF_EINVAL;
+  if (M > 0 && (!rows_ok(x, ldx, l->K, es) || !target || !at(target, 8) || !lse || !at(lse, 4) || !at(dloss, 4) ||
+                (dx && (lddx < l->K || !at(dx, es)))))
+    return DSF_EINVAL;
+  if (!ws || !at(ws, 256) || ws_bytes < xent_layout(l, M, true).total) return DSF_EWORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (dW && !dsf::succeeded(cudaMemsetAsync(dW, 0, size_t(l->R) * l->K * es, s))) return DSF_ECUDA;
+    if (db && !dsf::succeeded(cudaMemsetAsync(db, 0, size_t(l->R) * 4, s))) return DSF_ECUDA;
+    return DSF_OK;
+  }
+  if (!dx && !dW && !db) return DSF_OK;
+  return xent_bwd(l, x, ldx, reinterpret_cast<const long long*>(target), lse, dloss, M, dx, lddx, dW, db,
+                  static_cast<uint8_t*>(ws), status, s)
+             ? DSF_OK
+             : DSF_ECUDA;
+}
+
+}  // extern "C"

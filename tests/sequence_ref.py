@@ -97,3 +97,50 @@ def assert_within(got, ref, what):
     bad = ~(err <= tol)
     assert not bad.any(), "%s: %d of %d beyond the bound, worst error/bound %.3g" % (
         what, int(bad.sum()), bad.numel(), float((err / tol).nan_to_num(float("inf")).max()))
+
+
+def xent(x, W, b, target, dloss=None):
+    """{name: (value, bound)} of loss, lse and, with dloss, dx, dW, db, in 64
+    bits. A logit is off by at most ez = (K + 8) 2^-23 of the sum of its terms'
+    absolute values (as in dense_ref). exp(z - lse) is off by at most ez, what
+    lse is off by, 2 2^-23 of |z| + |lse| (the exponent's roundings) and 4 2^-23
+    of itself; a sum of V of them by (300 + V / 1024) 2^-23 (256 in a row's lane
+    and merge at most, and a 1024th of the columns in a thread's tiles); log by
+    2^-22. A bf16 dz is rounded, half a step."""
+    out = x.dtype
+    there = (target >= 0) & (target < W.shape[0])
+    xd, Wd = x.double(), W.double()
+    xd = torch.where(there[:, None], xd, torch.zeros_like(xd))
+    V, K = W.shape
+    z, a = xd @ Wd.t(), xd.abs() @ Wd.abs().t()
+    if b is not None:
+        z, a = z + b.double(), a + torch.nan_to_num(b.double().abs(), posinf=0.0)
+    ez = (K + 8) * U * a
+    lse = torch.logsumexp(z, 1)
+    p = torch.nan_to_num(torch.exp(z - lse[:, None]))  # (nothing possible: no gradient)
+    fin = torch.nan_to_num(z, neginf=0.0).abs()
+    ep = ez + 2 * U * (fin + torch.nan_to_num(lse, neginf=0.0).abs()[:, None]) + 4 * U
+    elsum = (p * ep).sum(1) + (300 + V / 1024) * U
+    el = elsum + 2 * U * torch.nan_to_num(lse, neginf=0.0).abs() + 2 * U
+    at = target.clamp(0, V - 1)[:, None]
+    zt, et = z.gather(1, at)[:, 0], ez.gather(1, at)[:, 0]
+    zero = torch.zeros_like(lse)
+    loss = torch.where(there, lse - zt, zero)
+    ret = {"lse": (lse, el), "loss": (loss, torch.where(there, el + et + U * loss.abs(), zero) + 1e-38)}
+    if dloss is None:
+        return ret
+    g = torch.where(there & torch.isfinite(lse), dloss.double(), zero)[:, None]
+    dz = g * p
+    dz.scatter_add_(1, at, -g)
+    e = g.abs() * p * (ep + el[:, None]) + 4 * U * dz.abs()
+    er = e + (HALF[out] * (dz.abs() + e) if out == torch.bfloat16 else 0)
+
+    def product(q, eq, r, n):
+        v = q @ r
+        t = eq @ r.abs() + (n + 8) * U * ((q.abs() + eq) @ r.abs())
+        return v, t + HALF[out] * (v.abs() + t) + 1e-38
+
+    M = x.shape[0]
+    ret["dx"], ret["dW"] = product(dz, er, Wd, V), product(dz.t(), er.t(), xd, M)
+    ret["db"] = dz.sum(0), e.sum(0) + (M + 8) * U * (dz.abs() + e).sum(0) + 1e-38
+    return ret
