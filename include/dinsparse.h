@@ -592,6 +592,31 @@ int ctr_softmax_xent_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx,
                          void* dW_dev, float* db_dev, void* workspace_dev, size_t ws_bytes, int32_t* status_dev,
                          void* stream);
 
+/* One optimiser step on a dense matrix W [R, C] (a layer's weights; the tables
+ * have emb_adagrad_update), with an orthogonalised update:
+ *   m = mu m + g,  u = g + mu m (nesterov = 1) or m (0),  X = u / (|u| + 1e-7),
+ *   steps times  A = X X^T,  X = (a I + b A + c A^2) X,
+ *   W = (1 - lr weight_decay) W - lr sqrt(max(1, R / C)) X
+ * with |u| the 2-norm of all of u and (a, b, c) = (3.4445, -4.7750, 2.0315):
+ * Newton-Schulz steps, after five of which X's singular values are near 1. W_dev
+ * and grad_dev have row strides and types of their own (DSF_F32 or DSF_BF16;
+ * a bf16 W is rounded to nearest even); momentum_dev is fp32 [R, C], contiguous.
+ * W and momentum are updated in place; they overlap neither each other nor
+ * grad. X and the products are fp32 (as the dense layer's DSF_F32). R, C <=
+ * 2^20, the smaller one <= 2^15; 0 <= mu < 1, weight_decay >= 0, 1 <= steps <=
+ * 16. The sum of u^2 is fp32 and has to be finite there; a gradient of zeros
+ * with no momentum leaves X zero, a non-finite one reaches all of W. Every
+ * pointer is aligned to its element. The workspace (256-byte aligned) needs no
+ * initialisation and holds nothing from one call to the next; it serves any
+ * matrix of its shape. Equal calls give equal bits. DSF_FLAG_TIMEOUT in
+ * *status_dev (nullable) if a device wait ran out. */
+size_t dsf_muon_workspace_bytes(int32_t R, int32_t C);
+
+int ctr_muon_update(void* W_dev, int64_t ldw, int32_t w_dtype, const void* grad_dev, int64_t ldg, int32_t g_dtype,
+                    float* momentum_dev, int32_t R, int32_t C, float lr, float mu, float weight_decay,
+                    int32_t nesterov, int32_t steps, void* workspace_dev, size_t ws_bytes, int32_t* status_dev,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

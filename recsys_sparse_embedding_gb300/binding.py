@@ -38,7 +38,8 @@ EXPORTS = ["dsf_workspace_bytes", "dsf_workspace_init", "dsf_prepare_mlp", "emb_
            "dsf_dense_workspace_bytes", "ctr_dense_fwd", "ctr_dense_bwd", "ctr_glu_fwd", "ctr_glu_bwd",
            "dsf_rms_norm_workspace_bytes", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd",
            "dsf_gated_scan_workspace_bytes", "ctr_gated_scan_fwd", "ctr_gated_scan_bwd",
-           "dsf_softmax_xent_workspace_bytes", "ctr_softmax_xent_fwd", "ctr_softmax_xent_bwd"]
+           "dsf_softmax_xent_workspace_bytes", "ctr_softmax_xent_fwd", "ctr_softmax_xent_bwd",
+           "dsf_muon_workspace_bytes", "ctr_muon_update"]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -172,6 +173,11 @@ def lib() -> ctypes.CDLL:
                                            _vp]
         for f in (L.ctr_softmax_xent_fwd, L.ctr_softmax_xent_bwd):
             f.restype = ctypes.c_int
+        L.dsf_muon_workspace_bytes.argtypes = [_i32, _i32]
+        L.dsf_muon_workspace_bytes.restype = _sz
+        L.ctr_muon_update.argtypes = [_vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32, _i32, ctypes.c_float, ctypes.c_float,
+                                      ctypes.c_float, _i32, _i32, _vp, _sz, _vp, _vp]
+        L.ctr_muon_update.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -834,3 +840,40 @@ def ctr_softmax_xent_bwd(layer: DenseLayer, x: torch.Tensor, target: torch.Tenso
                                       _vec("dloss", dloss, M, dev), M, dxp, lddx, dWp, _vec("db", db, layer.R, dev),
                                       workspace.ptr, workspace.nbytes, _dptr(status), _on(dev, stream)),
            "ctr_softmax_xent_bwd")
+
+
+class MuonWorkspace:
+    """Scratch of ctr_muon_update for matrices of W's shape."""
+
+    def __init__(self, W: torch.Tensor):
+        if W.dim() != 2:
+            raise ValueError("W: a matrix expected")
+        self.R, self.C = (int(n) for n in W.shape)
+        self.nbytes = int(lib().dsf_muon_workspace_bytes(self.R, self.C))
+        if self.nbytes == 0:
+            raise DsfError(DSF_EINVAL, "dsf_muon_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=W.device)
+        self.ptr, self.dev = self.buf.data_ptr(), self.buf.get_device()
+
+
+def ctr_muon_update(W: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, workspace: MuonWorkspace,
+                    lr: float = 0.02, mu: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True, steps: int = 5,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One optimiser step on a dense matrix: momentum = mu momentum + grad, the
+    update grad + mu momentum (nesterov) or momentum orthogonalised by `steps`
+    Newton-Schulz steps, W = W - lr (weight_decay W + sqrt(max(1, rows /
+    columns)) update). W and grad float32 or bfloat16, momentum float32."""
+    dev = _dev_of(W)
+    if workspace.dev != dev:
+        raise ValueError("the workspace is on cuda:%d" % workspace.dev)
+    if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16) or grad.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("W and grad: float32 or bfloat16 matrices expected")
+    R, C = W.shape
+    wp, ldw = _mat("W", W, W.dtype, R, C, dev)
+    gp, ldg = _mat("grad", grad, grad.dtype, R, C, dev)
+    if momentum.dtype is not torch.float32 or momentum.shape != (R, C) or momentum.get_device() != dev \
+            or not momentum.is_contiguous():
+        raise ValueError("momentum: contiguous float32 [%d, %d] on cuda:%d expected" % (R, C, dev))
+    _check(lib().ctr_muon_update(wp, ldw, _DTYPES[W.dtype], gp, ldg, _DTYPES[grad.dtype], momentum.data_ptr(), R, C, lr, mu,
+                                 weight_decay, int(bool(nesterov)), int(steps), workspace.ptr, workspace.nbytes,
+                                 _dptr(status), _on(dev, stream)), "ctr_muon_update")

@@ -144,3 +144,22 @@ def xent(x, W, b, target, dloss=None):
     ret["dx"], ret["dW"] = product(dz, er, Wd, V), product(dz.t(), er.t(), xd, M)
     ret["db"] = dz.sum(0), e.sum(0) + (M + 8) * U * (dz.abs() + e).sum(0) + 1e-38
     return ret
+
+
+NS = (3.4445, -4.7750, 2.0315)
+
+
+def muon(W, grad, momentum, lr, mu, decay, nesterov, steps):
+    """(W, momentum) after a step, in 64 bits."""
+    g, m = grad.double(), mu * momentum.double() + grad.double()
+    u = g + mu * m if nesterov else m
+    X = u / (u.norm() + 1e-7)
+    for _ in range(steps):
+        if X.shape[0] <= X.shape[1]:
+            A = X @ X.t()
+            X = NS[0] * X + (NS[1] * A + NS[2] * A @ A) @ X
+        else:
+            A = X.t() @ X
+            X = NS[0] * X + X @ (NS[1] * A + NS[2] * A @ A)
+    s = max(1.0, W.shape[0] / W.shape[1]) ** 0.5
+    return (1 - lr * decay) * W.double() - lr * s * X, m, lr * s * X
