@@ -10,18 +10,24 @@
 // compose. Rows are taken as one stream in which a sequence's first row is a
 // reset (its state comes from h0), so jagged lengths cost nothing.
 //
-// One pass over memory: a block holds a chunk of rows by up to 64 channels in
-// registers (256 threads: V channels by NT rows each; the threads' row ranges
-// are composed by shuffles and shared memory), publishes the chunk's pair,
-// takes the pairs of the chunks before it as far as its first sequence
-// reaches, and then writes its rows. Without the chain (a pass for the pairs,
-// a second over x and gate) a long sequence would move 5/3 of the bytes.
-// Fixed order: chunks are in groups of 32; a chunk starts from the state at
-// the end of the group before its own and composes the pairs of its group in
-// a fixed tree, so equal calls give equal bits, however blocks are scheduled,
-// and the chain through memory has one step per group. Blocks take their
-// chunks by a ticket, so a block only waits for blocks that have started;
-// every wait is bounded and sets DSF_FLAG_TIMEOUT when it runs out.
+// One pass over memory. An item is a chunk of rows by up to 64 channels (a
+// thread: 4 channels by NT rows). Its pair is published as soon as its rows have
+// arrived; a chunk's state is then put together from the pairs of the chunks
+// before it. (Without that, a pass for the pairs and a second over x and gate
+// would move 5/3 of the bytes.) Blocks are persistent and keep three items in
+// shared memory: one being loaded (cp.async, each thread what it will use
+// itself), one whose pair is taken, and one whose rows are written, its gates
+// computed again from the raw rows; so the wait for the chunks before is spent on
+// the next item. Blocks take items by a ticket, so they only wait for blocks that
+// have started, whatever else runs; every wait is bounded and sets
+// DSF_FLAG_TIMEOUT when it runs out.
+//
+// Fixed order: chunks are in groups of 32; a chunk starts from the state at the
+// end of the group before its own and composes the pairs of its group in a
+// fixed tree, so equal calls give equal bits, however blocks are scheduled, and
+// the chain through memory has one step per group. A pair and a state are 8
+// bytes, stored and polled whole; all bits set means "not there yet" (no
+// arithmetic gives that NaN), so no flag and no fence is needed.
 //
 // A reset is carried as A = -1 (A is never negative otherwise): nothing is
 // multiplied across a sequence's border, so a non-finite state stays in its
@@ -30,8 +36,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
+#include "dense_math.cuh"
 #include "dinsparse.h"
 #include "pdl.cuh"
 #include "ptx.cuh"
@@ -41,10 +49,16 @@ namespace scan {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kGroup = 32;          // chunks per group
-constexpr int kFwdRows = 8, kBwdRows = 4;  // rows per thread
+constexpr int kGroup = 32;  // chunks per group
+constexpr int kStages = 3;
 constexpr int kMaxDim = 1 << 20;
 constexpr long long kMaxRows = 1 << 30;
+
+// rows per thread: 32 (fp32: 64) KB an item
+template <class T, bool REV>
+constexpr int rows_of() {
+  return REV || sizeof(T) == 4 ? 4 : 8;
+}
 
 struct Args {
   const void *x, *gate, *h, *dh;  // h, dh: backward
@@ -53,55 +67,86 @@ struct Args {
   const float* in;  // [B, D]: h0; dh_last (nullable)
   const float* h0;  // backward: [B, D] (nullable)
   float* out;       // [B, D]: h_last; dh0 (nullable)
-  const int* off;   // [B + 1] first rows of the sequences; null: equal lengths L
-  const int* first; // [chunks + 1]: the sequence of a chunk's first row
-  int T, B, D, L;
-  int chunks, tiles, log_ct;
+  const int* total;           // rows of all sequences; null: T, equal lengths L
+  const uint8_t* mark;        // per row: 1 a sequence's first, 2 its last
+  const int *first, *last;    // the sequence of such a row (other entries hold nothing)
+  int T, D, L;
+  int tiles, log_ct;
   int chain;  // whether a sequence may go on from chunk to chunk
-  uint32_t *ticket, *flags, *group_flags;  // flags: [chunks][tiles]; group_flags: [groups][tiles]
-  float2* pairs;                           // [chunks][tiles][CT V]
-  float* states;                           // [groups][tiles][CT V]
+  uint32_t* ticket;           // one less than the next item
+  unsigned long long* pairs;  // [chunks][tiles][4 CT]
+  unsigned long long* states; // [groups][tiles][4 CT]: a state, and 0
   int* status;
 };
 
-// V neighbouring elements of a row
-template <class T, int V>
+// four neighbouring elements of a row
+template <class T>
 struct Raw;
 template <>
-struct Raw<float, 4> {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ void get(float* f) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
-  static __device__ void put(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+struct Raw<float> {
+  uint4 v;
+  __device__ void get(float2* f) const {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ void set(const float2* f) {
+    v = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
   }
 };
 template <>
-struct Raw<__nv_bfloat16, 4> {
-  uint2 v = make_uint2(0, 0);
-  __device__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
-  __device__ void get(float* f) const {
-    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+struct Raw<__nv_bfloat16> {
+  uint2 v;
+  __device__ void get(float2* f) const {
+    f[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
   }
-  static __device__ void put(__nv_bfloat16* p, const float* f) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-  }
+  __device__ void set(const float2* f) { v = make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y)); }
 };
+// n (0 .. 4) elements from p, the others zero; any alignment
 template <class T>
-struct Raw<T, 1> {
-  T v = T(0.f);
-  __device__ void load(const T* p) { v = *p; }
-  __device__ void get(float* f) const { f[0] = float(v); }
-  static __device__ void put(T* p, const float* f) { *p = T(f[0]); }
-};
+__device__ __forceinline__ void load_few(Raw<T>& r, const T* p, int n) {
+  float2 f[2] = {};
+  if (n > 0) f[0].x = float(p[0]);
+  if (n > 1) f[0].y = float(p[1]);
+  if (n > 2) f[1].x = float(p[2]);
+  if (n > 3) f[1].y = float(p[3]);
+  r.set(f);
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void store4(T* p, const float2* f, int n) {
+  if (VEC) {
+    Raw<T> r;
+    r.set(f);
+    *reinterpret_cast<decltype(r.v)*>(p) = r.v;
+    return;
+  }
+  if (n > 0) p[0] = T(f[0].x);
+  if (n > 1) p[1] = T(f[0].y);
+  if (n > 2) p[2] = T(f[1].x);
+  if (n > 3) p[3] = T(f[1].y);
+}
+template <bool VEC>
+__device__ __forceinline__ void load_state(const float* p, float2* f, int n) {
+  Raw<float> r;
+  if (VEC) r.v = __ldg(reinterpret_cast<const uint4*>(p));
+  else load_few(r, p, n);
+  r.get(f);
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, bool any) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+               "r"(any ? BYTES : 0)
+               : "memory");
+}
 
-// z = sigmoid(g) and a = 1 - z, both to a few last bits of their own size
-__device__ __forceinline__ void gate_of(float g, float& z, float& a) {
-  const float t = __expf(-fabsf(g)), r = __fdividef(1.f, 1.f + t), s = t * r;
-  z = g >= 0.f ? r : s;
-  a = g >= 0.f ? s : r;
-  if (g != g) z = a = g;
+// z = sigmoid(g) and a = 1 - z = t z, t = exp(-g), each to a few last bits of its
+// own size (below 2^-126: 0)
+__device__ __forceinline__ void gate_of(float2 g, float2& z, float2& a) {
+  const float2 e = g * pair(-kLog2e), t = make_float2(exp2_fast(e.x), exp2_fast(e.y)), d = t + pair(1.f);
+  z = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+  a = t * z;
+  if (t.x > 0x1p126f) a.x = 1.f;
+  if (t.y > 0x1p126f) a.y = 1.f;
 }
 
 // (A, B) := (A, B) after (Ap, Bp)
@@ -112,293 +157,384 @@ __device__ __forceinline__ void compose(float Ap, float Bp, float& A, float& B) 
 }
 __device__ __forceinline__ float apply(float A, float B, float y) { return A < 0.f ? B : fmaf(A, y, B); }
 
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+constexpr unsigned long long kNone = ~0ull;
+// A pair or a state, once it is there; false after about a second.
+__device__ __forceinline__ bool take(const unsigned long long* p, unsigned long long v, float2& f) {
+  bool ok = true;
+  if (v == kNone) {
+    const uint64_t t0 = globaltimer_ns();
+    while ((v = ld_relaxed_u64(p)) == kNone)
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        ok = false;
+        break;
+      }
+  }
+  f = make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+  return ok;
 }
-__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-// Waits until *p is set; false after about a second.
-__device__ bool wait_set(const uint32_t* p) {
-  if (ld_acquire(p)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!ld_acquire(p))
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  return true;
+__device__ __forceinline__ void give(unsigned long long* p, float2 f) {
+  st_relaxed_u64(p, uint64_t(__float_as_uint(f.y)) << 32 | __float_as_uint(f.x));
 }
 
-template <class T, int V, int NT, bool REV>
-__global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant__ Args a) {
-  constexpr int kMaxC = kThreads / 4 * NT;
-  __shared__ int s_start[kMaxC], s_end[kMaxC];  // the sequence that a row is the first (last) of, or -1
-  __shared__ float2 s_pair[kWarps][64], s_look[kWarps][64];
+template <class T, bool REV>
+struct Shared {
+  static constexpr int NT = rows_of<T, REV>(), NA = REV ? 4 : 2;
+  static constexpr int kData = NA * NT * kThreads * int(sizeof(Raw<T>));
+  static constexpr int kMark = 8 * kThreads;
+  static constexpr int kStage = kData + kMark;
+  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kBlocks = kBytes > 102 * 1024 ? 1 : 2;  // per SM
+};
+
+template <class T, bool REV, bool VEC>
+__global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel(const __grid_constant__ Args a) {
+  using S = Shared<T, REV>;
+  constexpr int NT = S::NT, NA = S::NA;
+  extern __shared__ __align__(16) uint8_t sm[];
+  // the warps' pairs of an item, then those of the warps before; two in turn
+  __shared__ float2 s_pair[2][kWarps][64];
+  __shared__ float2 s_look[kThreads];
   __shared__ float s_carry[64];
-  __shared__ int s_idx;
+  __shared__ int s_comes[2], s_ticket;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int CT = 1 << a.log_ct, ct = tid & (CT - 1), slice = tid >> a.log_ct, TS = kThreads >> a.log_ct, C = TS * NT;
+  const int CT = 1 << a.log_ct, ct = tid & (CT - 1), slice = tid >> a.log_ct, C = (kThreads >> a.log_ct) * NT, W = 4 * CT;
   pdl_go();
   pdl_wait();
-  int idx = blockIdx.x;
-  if (a.chain) {
-    if (tid == 0) s_idx = int(atomicAdd(a.ticket, 1u));
-    __syncthreads();
-    idx = s_idx;
-  }
-  const int rank = idx / a.tiles, tile = idx - rank * a.tiles, chunk = REV ? a.chunks - 1 - rank : rank;
-  const int total = a.off ? a.off[a.B] : a.T, t0 = chunk * C;
-  if (t0 >= total) return;
-  const int n = min(C, total - t0), c0 = (tile * CT + ct) * V;
-  const bool live = c0 < a.D;
-  // the thread's rows, in scan order: row u0 + i of the chunk, or from its end
+  const int total = a.total ? *a.total : a.T, chunks = (total + C - 1) / C;
+  const long long items = (long long)chunks * a.tiles;
+
+  struct Item {
+    int rank, tile, t0, n;  // n = 0: none
+  };
+  auto item_at = [&](long long idx) {
+    Item it{0, 0, 0, 0};
+    if (idx >= items) return it;
+    it.rank = int(idx / a.tiles);
+    it.tile = int(idx - (long long)it.rank * a.tiles);
+    it.t0 = (REV ? chunks - 1 - it.rank : it.rank) * C;
+    it.n = min(C, total - it.t0);
+    return it;
+  };
+  // the thread's rows, in scan order: upwards, or from the chunk's end
   auto row_of = [&](int i) { return REV ? C - 1 - (slice * NT + i) : slice * NT + i; };
+  const int low = REV ? C - NT - slice * NT : slice * NT;  // the lowest of them
+  auto slot = [&](int st, int arr, int i) {
+    return reinterpret_cast<Raw<T>*>(sm + st * S::kStage) + (arr * NT + i) * kThreads + tid;
+  };
+  auto marks = [&](int st) { return reinterpret_cast<uint8_t*>(sm + st * S::kStage + S::kData) + 8 * tid; };
+  auto width = [&](const Item& it) { return a.D - (it.tile * CT + ct) * 4; };  // channels from the thread's first on
 
-  Raw<T, V> rx[NT], rg[NT], rh[REV ? NT : 1], rd[REV ? NT : 1];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int k = row_of(i);
-    if (!live || k >= n) continue;
-    const long long t = t0 + k;
-    rx[i].load(static_cast<const T*>(a.x) + t * a.ldx + c0);
-    rg[i].load(static_cast<const T*>(a.gate) + t * a.ldg + c0);
-    if (REV) {
-      rd[REV ? i : 0].load(static_cast<const T*>(a.dh) + t * a.lddh + c0);
-      if (t > 0) rh[REV ? i : 0].load(static_cast<const T*>(a.h) + (t - 1) * a.ldh + c0);
-    }
-  }
-  // where sequences start and end
-  int from = 0;  // ragged: the sequence of the chunk's first row
-  if (a.off) {
-    from = a.first[chunk];
-    for (int k = tid; k < C; k += kThreads) s_start[k] = s_end[k] = -1;
-    __syncthreads();
-    for (int s = from + tid; s < a.B; s += kThreads) {
-      const int b = a.off[s], e = a.off[s + 1];
-      if (b >= t0 + n) break;
-      if (e == b) continue;
-      if (b >= t0) s_start[b - t0] = s;
-      if (e <= t0 + n) s_end[e - 1 - t0] = s;
-    }
-  } else {
-    for (int k = tid; k < C; k += kThreads) {
-      const int t = t0 + k, s = t / a.L, r = t - s * a.L;
-      s_start[k] = r == 0 ? s : -1;
-      s_end[k] = r == a.L - 1 ? s : -1;
-    }
-  }
-  __syncthreads();
+  // a chunk's rows that are all there (most are): the loops over them unrolled
+  auto whole = [&](const Item& it) { return VEC && it.n == C && (!REV || it.t0 > 0); };
 
-  // the rows' pairs, and what the outputs take besides
-  float A[NT][V], Bv[NT][V], w[REV ? NT : 1][V], z[REV ? NT : 1][V];  // REV: Bv is dh
-  uint32_t reset = 0;
+  auto load = [&](const Item& it, int st) {
+    const int c0 = (it.tile * CT + ct) * 4, w = min(4, width(it));
+    const bool live = it.n > 0 && w > 0;
+    if (live) {
+      const T* src[4] = {static_cast<const T*>(a.x), static_cast<const T*>(a.gate), static_cast<const T*>(a.dh),
+                         static_cast<const T*>(a.h)};
+      const long long ld[4] = {a.ldx, a.ldg, a.lddh, a.ldh};
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int k = row_of(i);
-    const bool in = live && k < n;
-    float x[V], g[V];
-    rx[i].get(x);
-    rg[i].get(g);
-    const int seq = in ? (REV ? s_end[k] : s_start[k]) : -1;
-    if (seq >= 0) reset |= 1u << i;
-    float s[V], hp[V], d[V];
-    Raw<float, V> state;
-    if (seq >= 0 && a.in) state.load(a.in + (long long)seq * a.D + c0);
-    state.get(s);
-    if (REV) {
-      rh[REV ? i : 0].get(hp);
-      rd[REV ? i : 0].get(d);
-      const int b = in ? s_start[k] : -1;
-      if (b >= 0) {
-        Raw<float, V> r;
-        if (a.h0) r.load(a.h0 + (long long)b * a.D + c0);
-        r.get(hp);
+      for (int arr = 0; arr < NA; ++arr) {
+        const long long t = it.t0 + low - (arr == 3 ? 1 : 0);  // h: the row before
+        const T* p = src[arr] + t * ld[arr] + c0;
+        Raw<T>* d = slot(st, arr, REV ? NT - 1 : 0);
+        constexpr int kNext = REV ? -kThreads : kThreads;
+        if (whole(it)) {
+#pragma unroll
+          for (int k = 0; k < NT; ++k, p += ld[arr]) cp_async<int(sizeof(Raw<T>))>(d + k * kNext, p, true);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < NT; ++k, p += ld[arr], d += kNext) {
+            const bool any = low + k < it.n && t + k >= 0;
+            if (VEC) {
+              cp_async<int(sizeof(Raw<T>))>(d, any ? p : src[arr], any);
+            } else {
+              Raw<T> r;
+              load_few(r, p, any ? w : 0);
+              *d = r;
+            }
+          }
+        }
+      }
+      if (a.total) cp_async<NT>(marks(st), a.mark + it.t0 + low, true);
+    }
+    cp_async_commit();
+    if (live && !a.total) {
+      int r = (it.t0 + low) % a.L;
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        marks(st)[k] = uint8_t((r == 0 ? 1 : 0) | (r == a.L - 1 ? 2 : 0));
+        r = r + 1 == a.L ? 0 : r + 1;
       }
     }
+  };
+  // the marks of the thread's rows as two sets of bits (bit i: row i in scan
+  // order): where the recurrence starts anew, and where its state leaves
+  auto sets = [&](const Item& it, int st, uint32_t& reset, uint32_t& leave) {
+    reset = leave = 0;
+    uint32_t m[2] = {0, 0};
+    m[0] = *reinterpret_cast<const uint32_t*>(marks(st));
+    if (NT == 8) m[1] = *reinterpret_cast<const uint32_t*>(marks(st) + 4);
+    if (!(m[0] | m[1])) return;
+#pragma unroll 1
+    for (int k = 0; k < NT; ++k) {
+      const uint32_t b = (k < 4 ? m[0] : m[1]) >> (8 * (k & 3)) & 3u;
+      if (low + k >= it.n) continue;
+      const int i = REV ? NT - 1 - k : k;
+      reset |= ((REV ? b >> 1 : b) & 1u) << i;
+      leave |= ((REV ? b : b >> 1) & 1u) << i;
+    }
+  };
+  auto seq_first = [&](long long t) { return a.total ? a.first[t] : int(t / a.L); };
+  auto seq_last = [&](long long t) { return a.total ? a.last[t] : int(t / a.L); };
+
+  // what a row brings: a and B (backward: dh in its place)
+  auto row_pair = [&](int st, int i, float2* A, float2* Bv, float2* z) {
+    float2 v[2], g[2];
+    slot(st, REV ? 2 : 0, i)->get(v);
+    slot(st, 1, i)->get(g);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float zz, aa;
-      gate_of(g[v], zz, aa);
-      if (REV) {
-        A[i][v] = in ? aa : 1.f;
-        Bv[i][v] = in ? d[v] + s[v] : 0.f;
-        w[REV ? i : 0][v] = (x[v] - hp[v]) * (zz * aa);
-        z[REV ? i : 0][v] = zz;
+    for (int h = 0; h < 2; ++h) {
+      gate_of(g[h], z[h], A[h]);
+      Bv[h] = REV ? v[h] : z[h] * v[h];
+    }
+  };
+  // at a reset, the state's part of B
+  auto add_state = [&](const Item& it, int i, const float2* A, float2* Bv) {
+    if (!a.in) return;
+    const long long t = it.t0 + row_of(i);
+    float2 s[2];
+    load_state<VEC>(a.in + (long long)(REV ? seq_last(t) : seq_first(t)) * a.D + (it.tile * CT + ct) * 4, s, width(it));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) Bv[h] = REV ? Bv[h] + s[h] : __ffma2_rn(A[h], s[h], Bv[h]);
+  };
+
+  float PA[2][4], PB[2][4];  // the pairs of the warp's threads before this one: of the item, of the next
+  float2 tot = make_float2(1.f, 0.f);  // (tid < W) the item's pair in channel tid
+  bool ok = true;
+
+  auto phase1 = [&](const Item& it, int st, int par, float* QA, float* QB) {
+    const bool live = it.n > 0 && width(it) > 0;
+    float2 A[2] = {pair(1.f), pair(1.f)}, Bv[2] = {};
+    bool any = false;
+    if (live) {
+      uint32_t reset, leave;
+      sets(it, st, reset, leave);
+      any = reset != 0;
+      auto row = [&](int i, bool r) {
+        float2 ra[2], rb[2], z[2];
+        row_pair(st, i, ra, rb, z);
+        if (r) {
+          add_state(it, i, ra, rb);
+          Bv[0] = Bv[1] = pair(0.f);
+          if (!REV) ra[0] = ra[1] = pair(0.f);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Bv[h] = REV ? ra[h] * (Bv[h] + rb[h]) : __ffma2_rn(ra[h], Bv[h], rb[h]);
+          A[h] = A[h] * ra[h];
+        }
+      };
+      if (whole(it) && !any) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) row(i, false);
       } else {
-        A[i][v] = in ? aa : 1.f;
-        Bv[i][v] = in ? (seq >= 0 ? fmaf(aa, s[v], zz * x[v]) : zz * x[v]) : 0.f;
+#pragma unroll 1
+        for (int i = 0; i < NT; ++i)
+          if (row_of(i) < it.n) row(i, reset >> i & 1u);
       }
+      if (tid == 0) s_comes[par] = a.chain && !(reset & 1u) && !(REV && it.n < C);
     }
-  }
-  // the thread's pair, then the pairs of the threads before it
-  float PA[V], PB[V];
+    float qa[4] = {A[0].x, A[0].y, A[1].x, A[1].y}, qb[4] = {Bv[0].x, Bv[0].y, Bv[1].x, Bv[1].y};
 #pragma unroll
-  for (int v = 0; v < V; ++v) PA[v] = 1.f, PB[v] = 0.f;
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool r = reset >> i & 1;
-      if (REV) PB[v] = A[i][v] * (r ? Bv[i][v] : PB[v] + Bv[i][v]);
-      else PB[v] = r ? Bv[i][v] : fmaf(A[i][v], PB[v], Bv[i][v]);
-      PA[v] = r || PA[v] < 0.f ? -1.f : PA[v] * A[i][v];
-    }
-  auto warp_scan = [&](float* qa, float* qb) {  // inclusive, over the warp's slices
+    for (int v = 0; v < 4; ++v)
+      if (any) qa[v] = -1.f;
     for (int d = CT; d < 32; d <<= 1)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int v = 0; v < 4; ++v) {
         const float ap = __shfl_up_sync(0xffffffffu, qa[v], d), bp = __shfl_up_sync(0xffffffffu, qb[v], d);
         if (lane >= d) compose(ap, bp, qa[v], qb[v]);
       }
-  };
-  warp_scan(PA, PB);
-  if (lane >= 32 - CT)
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_pair[warp][ct * V + v] = make_float2(PA[v], PB[v]);
-  // exclusive within the warp
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float ap = __shfl_up_sync(0xffffffffu, PA[v], CT & 31), bp = __shfl_up_sync(0xffffffffu, PB[v], CT & 31);
-    PA[v] = lane >= CT ? ap : 1.f;
-    PB[v] = lane >= CT ? bp : 0.f;
-  }
-  __syncthreads();
-  float WA[V], WB[V], SA[V], SB[V];  // the pairs of the warps before this one; of the block
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    SA[v] = 1.f, SB[v] = 0.f, WA[v] = 1.f, WB[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k == warp) WA[v] = SA[v], WB[v] = SB[v];
-      float2 p = s_pair[k][ct * V + v];
-      compose(SA[v], SB[v], p.x, p.y);
-      SA[v] = p.x, SB[v] = p.y;
-    }
-    compose(WA[v], WB[v], PA[v], PB[v]);
-  }
-
-  // the chain: what goes on to the next chunk, and what comes from the last
-  const bool goes_on = a.chain && (REV ? t0 > 0 && s_start[0] < 0 : t0 + n < total && s_end[n - 1] < 0);
-  const bool comes_in = a.chain && (REV ? s_end[n - 1] < 0 : s_start[0] < 0);
-  const int W = CT * V, group = rank / kGroup;
-  bool ok = true;
-  if (goes_on && warp == 0) {
-    if (lane < CT && live)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        __stcg(&a.pairs[((long long)rank * a.tiles + tile) * W + ct * V + v], make_float2(SA[v], SB[v]));
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) st_release(a.flags + (long long)rank * a.tiles + tile, 1u);
-  }
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
-  if (comes_in) {
-    // the chunk where the chunk's first sequence (in scan order) begins
-    int begin;
-    if (a.off) {
-      const int s = REV ? a.first[chunk + 1] : from;
-      begin = REV ? a.chunks - 1 - (a.off[s + 1] - 1) / C : a.off[s] / C;
-    } else {
-      const int s = (REV ? t0 + n - 1 : t0) / a.L;
-      begin = REV ? a.chunks - 1 - (s * a.L + a.L - 1) / C : s * a.L / C;
-    }
-    const int lo = max(begin, group * kGroup), count = rank - lo;
-    const int each = (kGroup + TS - 1) / TS;
-    float QA[V], QB[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) QA[v] = 1.f, QB[v] = 0.f;
-    for (int j = slice * each; j < min(count, (slice + 1) * each); ++j) {
-      const long long at = (long long)(lo + j) * a.tiles + tile;
-      ok = wait_set(a.flags + at) && ok;
-      if (live)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float2 p = __ldcg(&a.pairs[at * W + ct * V + v]);
-          compose(QA[v], QB[v], p.x, p.y);
-          QA[v] = p.x, QB[v] = p.y;
-        }
-    }
-    __syncwarp();
-    warp_scan(QA, QB);
     if (lane >= 32 - CT)
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_look[warp][ct * V + v] = make_float2(QA[v], QB[v]);
-    __syncthreads();
-    if (tid < CT) {
-      const long long at = (long long)(group - 1) * a.tiles + tile;
-      const bool before = begin < group * kGroup;
-      if (before) ok = wait_set(a.group_flags + at) && ok;
+      for (int v = 0; v < 4; ++v) s_pair[par][warp][ct * 4 + v] = make_float2(qa[v], qb[v]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float y = before && live ? __ldcg(&a.states[at * W + ct * V + v]) : 0.f;
+    for (int v = 0; v < 4; ++v) {
+      const float ap = __shfl_up_sync(0xffffffffu, qa[v], CT), bp = __shfl_up_sync(0xffffffffu, qb[v], CT);
+      QA[v] = lane >= CT ? ap : 1.f;
+      QB[v] = lane >= CT ? bp : 0.f;
+    }
+  };
+
+  // Items in flight: cur (rows to be written), nxt (pair to be taken) and aft
+  // (being loaded), in three stages; the ticket of the one after it is fetched.
+  long long idx = blockIdx.x;
+  auto request = [&](bool more) {
+    if (!a.chain) idx += gridDim.x;
+    else if (tid == 0) s_ticket = int(more ? min((long long)(atomicAdd(a.ticket, 1u) + 1u), items) : items);
+  };
+  if (a.chain) {
+    request(true);
+    __syncthreads();
+    idx = s_ticket;
+    __syncthreads();
+  }
+  Item cur{0, 0, 0, 0}, nxt = item_at(idx);
+  load(nxt, 0);
+  request(nxt.n > 0);
+  __syncthreads();
+  if (a.chain) idx = s_ticket;
+  __syncthreads();
+  int st = 0, par = 0;  // the stage of nxt; parity of its buffers
+  for (;;) {
+    const Item aft = item_at(idx);
+    const int st_aft = st + 1 == kStages ? 0 : st + 1;
+    load(aft, st_aft);
+    request(aft.n > 0);
+    cp_async_wait_one_pending();
+    if (nxt.n > 0) phase1(nxt, st, par, PA[1], PB[1]);
+    // the pairs of cur's group before it
+    const bool comes = cur.n > 0 && s_comes[par ^ 1];
+    const int group = cur.rank / kGroup;
+    if (comes) {
+      const int per = kGroup * W / kThreads, ch = tid & (W - 1), j0 = group * kGroup + tid / W * per;
+      const unsigned long long* p = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + ch;
+      const long long step = (long long)a.tiles * W;
+      unsigned long long raw[8];  // (per is 2, 4 or 8)
+      float QA = 1.f, QB = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) raw[j] = j < per && j0 + j < cur.rank ? ld_relaxed_u64(p + j * step) : 0ull;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= per || j0 + j >= cur.rank) continue;
+        float2 f;
+        ok = take(p + j * step, raw[j], f) && ok;
+        compose(QA, QB, f.x, f.y);
+        QA = f.x, QB = f.y;
+      }
+      s_look[tid] = make_float2(QA, QB);
+    }
+    __syncthreads();
+    if (a.chain) idx = s_ticket;
+    if (tid < W) {
+      float y = 0.f;
+      const long long at = (long long)cur.tile * W + tid;
+      if (comes) {
+        float QA = 1.f, QB = 0.f;
+        for (int k = tid; k < kThreads; k += W) {
+          float2 f = s_look[k];
+          compose(QA, QB, f.x, f.y);
+          QA = f.x, QB = f.y;
+        }
+        if (QA >= 0.f && group > 0) {
+          const unsigned long long* p = a.states + (long long)(group - 1) * a.tiles * W + at;
+          float2 f;
+          ok = take(p, ld_relaxed_u64(p), f) && ok;
+          y = f.x;
+        }
+        y = apply(QA, QB, y);
+        s_carry[tid] = y;
+      }
+      if (a.chain && cur.n > 0 && cur.rank % kGroup == kGroup - 1)
+        give(a.states + (long long)group * a.tiles * W + at, make_float2(apply(tot.x, tot.y, y), 0.f));
+      if (nxt.n > 0) {
+        float2 s = make_float2(1.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-          const float2 p = s_look[k][ct * V + v];
-          y = apply(p.x, p.y, y);
+          float2 f = s_pair[par][k][tid];
+          s_pair[par][k][tid] = s;
+          compose(s.x, s.y, f.x, f.y);
+          s = f;
         }
-        s_carry[ct * V + v] = y;
+        tot = s;
+        if (a.chain) give(a.pairs + ((long long)nxt.rank * a.tiles + nxt.tile) * W + tid, s);
       }
     }
     __syncthreads();
+    if (cur.n > 0 && width(cur) > 0) {
+      const int sc = st == 0 ? kStages - 1 : st - 1, w = width(cur), c0 = (cur.tile * CT + ct) * 4;
+      uint32_t reset, leave;
+      sets(cur, sc, reset, leave);
+      float2 y[2];
+      float* yf = reinterpret_cast<float*>(y);
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = s_carry[ct * V + v];
-  }
-  if (goes_on && rank % kGroup == kGroup - 1 && warp == 0) {
-    if (lane < CT && live)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        __stcg(&a.states[((long long)group * a.tiles + tile) * W + ct * V + v], apply(SA[v], SB[v], carry[v]));
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) st_release(a.group_flags + (long long)group * a.tiles + tile, 1u);
-  }
-  if (!ok && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
-  if (!live) return;
-
-  float y[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) y[v] = apply(PA[v], PB[v], carry[v]);
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int k = row_of(i);
-    if (k >= n) continue;
-    const long long t = t0 + k;
-    const bool r = reset >> i & 1;
-    if (REV) {
-      float dx[V], dg[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = r ? Bv[i][v] : Bv[i][v] + y[v];
-        dx[v] = g * z[REV ? i : 0][v];
-        dg[v] = g * w[REV ? i : 0][v];
-        y[v] = A[i][v] * g;
+      for (int v = 0; v < 4; ++v) {
+        const float2 e = s_pair[par ^ 1][warp][ct * 4 + v];
+        float A = PA[0][v], B = PB[0][v];
+        compose(e.x, e.y, A, B);
+        yf[v] = apply(A, B, comes ? s_carry[ct * 4 + v] : 0.f);
       }
-      Raw<T, V>::put(static_cast<T*>(a.o0) + t * a.ldo0 + c0, dx);
-      Raw<T, V>::put(static_cast<T*>(a.o1) + t * a.ldo1 + c0, dg);
-    } else {
+      // a row: its state, its outputs; r: a reset, l: the state leaves
+      auto row = [&](int i, bool r, bool l, T* o0, T* o1) {
+        const long long t = cur.t0 + row_of(i);
+        float2 A[2], Bv[2], z[2];
+        row_pair(sc, i, A, Bv, z);
+        if (r) {
+          add_state(cur, i, A, Bv);
+          y[0] = y[1] = pair(0.f);
+        }
+        if (REV) {
+          float2 x[2], hp[2], dx[2], dg[2];
+          slot(sc, 0, i)->get(x);
+          slot(sc, 3, i)->get(hp);
+          if (l) {
+            hp[0] = hp[1] = pair(0.f);
+            if (a.h0) load_state<VEC>(a.h0 + (long long)seq_first(t) * a.D + c0, hp, w);
+          }
 #pragma unroll
-      for (int v = 0; v < V; ++v) y[v] = r ? Bv[i][v] : fmaf(A[i][v], y[v], Bv[i][v]);
-      Raw<T, V>::put(static_cast<T*>(a.o0) + t * a.ldo0 + c0, y);
+          for (int h = 0; h < 2; ++h) {
+            const float2 g = Bv[h] + y[h];
+            dx[h] = g * z[h];
+            dg[h] = g * (__ffma2_rn(hp[h], pair(-1.f), x[h]) * (z[h] * A[h]));
+            y[h] = A[h] * g;
+          }
+          store4<VEC>(o0, dx, w);
+          store4<VEC>(o1, dg, w);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) y[h] = __ffma2_rn(r ? pair(0.f) : A[h], y[h], Bv[h]);
+          store4<VEC>(o0, y, w);
+        }
+        if (l && a.out) store4<VEC>(a.out + (long long)(REV ? seq_first(t) : seq_last(t)) * a.D + c0, y, w);
+      };
+      const long long t1 = cur.t0 + row_of(0), d0 = REV ? -a.ldo0 : a.ldo0, d1 = -a.ldo1;
+      T* o0 = static_cast<T*>(a.o0) + t1 * a.ldo0 + c0;
+      T* o1 = REV ? static_cast<T*>(a.o1) + t1 * a.ldo1 + c0 : nullptr;
+      if (whole(cur) && !(reset | leave)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0) row(i, false, false, o0, o1);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0)
+          if (row_of(i) < cur.n) row(i, reset >> i & 1u, leave >> i & 1u, o0, o1);
+      }
     }
-    const int s = REV ? s_start[k] : s_end[k];
-    if (s >= 0 && a.out) Raw<float, V>::put(a.out + (long long)s * a.D + c0, y);
+    if (nxt.n == 0) break;
+    cur = nxt;
+    nxt = aft;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) PA[0][v] = PA[1][v], PB[0][v] = PB[1][v];
+    st = st_aft;
+    par ^= 1;
   }
+  cp_async_wait_all();
+  if (!ok && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
 }
 
-// Before the scan: the sequences' first rows (lengths added up, each block all
-// of those before its own: at most B / 1024 blocks read them from L2), the
-// sequence of each chunk's first row, empty sequences' states (passed on), and
-// the chain's flags zeroed.
+// Before the scan: the sequences' borders (lengths added up, each block all of
+// those before its own, from L2) as marks on their rows, empty sequences' states
+// (passed on), and the chain's pairs and ticket set to "not there".
 struct PrepArgs {
-  const int* lengths;  // null: only the flags, or every sequence is empty
-  int *off, *first;
-  int T, B, D, C, chunks;
-  uint32_t* zero;
-  long long zeros;
+  const int* lengths;  // null: no marks
+  uint8_t* mark;
+  int *first, *last, *total;
+  int T, B, D;
+  uint4* fill;
+  long long fills;
   const float* in;
   float* out;
+  uint32_t* ticket;
   int* status;
 };
 constexpr int kPrep = 1024;
@@ -408,7 +544,9 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_go();
   pdl_wait();
-  for (long long i = (long long)blockIdx.x * kPrep + tid; i < a.zeros; i += (long long)gridDim.x * kPrep) a.zero[i] = 0u;
+  for (long long i = (long long)blockIdx.x * kPrep + tid; i < a.fills; i += (long long)gridDim.x * kPrep)
+    a.fill[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = ~0u;
   const long long s0 = (long long)blockIdx.x * kPrep;
   if (s0 >= a.B) return;
   const long long s = s0 + tid;
@@ -416,47 +554,54 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
   if (a.lengths) {
     if (tid == 0) bad = 0;
     long long sum = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (long long i = tid; i < s0; i += kPrep) sum += max(__ldg(a.lengths + i), 0);
     const int raw = s < a.B ? __ldg(a.lengths + s) : 0, len = max(raw, 0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) part[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      before = 0;
-      for (int w = 0; w < kPrep / 32; ++w) before += part[w];
+    if (warp == 0) {
+      sum = part[lane];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) before = sum;
     }
     if (raw < 0) bad = 1;
-    __syncthreads();
-    long long end = len;  // inclusive, in the block
+    long long end = len;  // inclusive, in the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long p = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += p;
     }
+    __syncthreads();
     if (lane == 31) part[warp] = end;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) end += part[w];
-    end += before;
+    long long ahead = lane < warp ? part[lane] : 0;  // of the warps before
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    end += ahead + before;
     const long long T = a.T;
     if (s == a.B - 1 && a.status && end > T) atomicOr(a.status, DSF_FLAG_COUNT);
     if (tid == 0 && bad && a.status) atomicOr(a.status, DSF_FLAG_NEG_LENGTH);
     b = int(min(end - len, T));
     e = int(min(end, T));
-    if (s < a.B) {
-      a.off[s] = b;
-      if (s == a.B - 1) a.off[a.B] = e;
+    if (s == a.B - 1) *a.total = e;
+    const bool some = s < a.B && e > b, many = some && e - b > 32;
+    if (some) {
+      a.first[b] = int(s);
+      a.last[e - 1] = int(s);
+      if (!many)
+        for (int t = b; t < e; ++t) a.mark[t] = uint8_t((t == b ? 1 : 0) | (t == e - 1 ? 2 : 0));
     }
-    // chunks that begin in this sequence (many of a long one: by the warp)
-    const int k0 = (b + a.C - 1) / a.C, k1 = e > b ? (e - 1) / a.C + 1 : k0;
-    const bool many = s < a.B && k1 - k0 > 4;
-    if (s < a.B && !many)
-      for (int k = k0; k < k1; ++k) a.first[k] = int(s);
+    // a long sequence's marks by the warp: 16 rows per lane, its ends row by row
     for (uint32_t m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
-      const int l = __ffs(m) - 1;
-      const int j0 = __shfl_sync(0xffffffffu, k0, l), j1 = __shfl_sync(0xffffffffu, k1, l);
-      for (int k = j0 + lane; k < j1; k += 32) a.first[k] = int(s0) + warp * 32 + l;
+      const int l = __ffs(m) - 1, tb = __shfl_sync(0xffffffffu, b, l), te = __shfl_sync(0xffffffffu, e, l);
+      const int v0 = (tb + 16) / 16, v1 = (te - 1) / 16;  // whole vectors behind the first row and before the last
+      for (long long v = v0 + lane; v < v1; v += 32) reinterpret_cast<uint4*>(a.mark)[v] = make_uint4(0, 0, 0, 0);
+      const int head = min(te, v0 * 16), rear = max(head, v1 * 16);
+      for (int t = tb + lane; t < head; t += 32) a.mark[t] = uint8_t((t == tb ? 1 : 0) | (t == te - 1 ? 2 : 0));
+      for (int t = rear + lane; t < te; t += 32) a.mark[t] = uint8_t(t == te - 1 ? 2 : 0);
     }
   }
   if (!a.out) return;
@@ -471,20 +616,23 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool at(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr int rows_per_thread(int es, bool rev) {
+  return es == 4 ? (rev ? rows_of<float, true>() : rows_of<float, false>())
+                 : (rev ? rows_of<__nv_bfloat16, true>() : rows_of<__nv_bfloat16, false>());
+}
+
 struct Plan {
-  int V, NT, log_ct, C, tiles;
+  int log_ct, C, tiles;
   long long chunks, groups;
-  size_t off, first, flags, pairs, states, total;  // flags: the ticket, the chunks', the groups'
+  size_t mark, first, last, sync, sync_bytes, total;  // sync: the ticket and total, pairs, states
+  size_t pairs, states;
 };
-Plan plan(long long T, long long B, int D, bool vec, bool rev) {
+Plan plan(long long T, int D, int nt) {
   Plan p{};
-  p.V = vec ? 4 : 1;
-  p.NT = rev ? kBwdRows : kFwdRows;
-  const int most = vec ? 4 : 5, lanes = (D + p.V - 1) / p.V;  // threads along the channels: 4 .. 16 (32)
-  p.log_ct = 2;
-  while (p.log_ct < most && (1 << p.log_ct) < lanes) ++p.log_ct;
-  p.C = (kThreads >> p.log_ct) * p.NT;
-  const int width = (1 << p.log_ct) * p.V;
+  p.log_ct = 2;  // 4, 8 or 16 threads of 4 channels
+  while (p.log_ct < 4 && (4 << p.log_ct) < D) ++p.log_ct;
+  p.C = (kThreads >> p.log_ct) * nt;
+  const int width = 4 << p.log_ct;
   p.tiles = (D + width - 1) / width;
   p.chunks = (T + p.C - 1) / p.C;
   p.groups = (p.chunks + kGroup - 1) / kGroup;
@@ -494,11 +642,13 @@ Plan plan(long long T, long long B, int D, bool vec, bool rev) {
     o += align256(bytes);
     return here;
   };
-  p.off = take(size_t(B + 1) * 4);
-  p.first = take(size_t(p.chunks + 1) * 4);
-  p.flags = take(size_t(1 + (p.chunks + p.groups) * p.tiles) * 4);
+  p.mark = take(size_t(p.chunks) * p.C);
+  p.first = take(size_t(T) * 4);
+  p.last = take(size_t(T) * 4);
+  p.sync = take(256);
   p.pairs = take(size_t(p.chunks) * p.tiles * width * 8);
-  p.states = take(size_t(p.groups) * p.tiles * width * 4);
+  p.states = take(size_t(p.groups) * p.tiles * width * 8);
+  p.sync_bytes = o - p.sync;
   p.total = o;
   return p;
 }
@@ -506,58 +656,67 @@ Plan plan(long long T, long long B, int D, bool vec, bool rev) {
 bool sizes_ok(int64_t T, int64_t B, int32_t D) {
   return T >= 0 && T <= kMaxRows && B >= 0 && B <= kMaxRows && D >= 1 && D <= kMaxDim;
 }
-size_t ws_bytes_of(int64_t T, int64_t B, int32_t D) {
-  size_t most = 0;
-  for (int i = 0; i < 4; ++i) {
-    if ((i & 1) && D % 4) continue;
-    const Plan p = plan(T, B, D, i & 1, i & 2);
-    most = p.total > most ? p.total : most;
-  }
-  return most + 256;
+size_t ws_bytes_of(int64_t T, int32_t D) {
+  const size_t a = plan(T, D, 4).total, b = plan(T, D, 8).total;
+  return (a > b ? a : b) + 256;
 }
 
-template <class T, int V, int NT, bool REV>
-bool launch(const Args& a, long long blocks, cudaStream_t s) {
-  return pdl_launch(scan_kernel<T, V, NT, REV>, dim3(unsigned(blocks)), kThreads, s, a);
+template <class T, bool REV, bool VEC>
+bool launch(const Args& a, long long items, cudaStream_t s) {
+  using S = Shared<T, REV>;
+  auto* kernel = scan_kernel<T, REV, VEC>;
+  static std::atomic<int> most[64];  // (host threads may race on it: each computes the same value)
+  int dev = 0;
+  if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return false;
+  int blocks = most[dev].load(std::memory_order_acquire);
+  if (blocks == 0) {
+    int sms = 0, per = 0;
+    if (!succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes)) ||
+        !succeeded(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) ||
+        !succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, S::kBytes)) || per < 1)
+      return false;
+    blocks = sms * per;
+    most[dev].store(blocks, std::memory_order_release);
+  }
+  return pdl_launch_smem(kernel, dim3(unsigned(items < blocks ? items : blocks)), kThreads, S::kBytes, s, a);
 }
 
 // rows of `es`-byte elements that vectors of four may be taken from
 bool vec_rows(const void* p, long long ld, int es) { return !p || (at(p, 4 * es) && ld % 4 == 0); }
 
 template <bool REV>
-int run(Args a, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaStream_t s) {
+int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaStream_t s) {
   const int es = dtype == DSF_F32 ? 4 : 2;
   const bool vec = a.D % 4 == 0 && vec_rows(a.x, a.ldx, es) && vec_rows(a.gate, a.ldg, es) && vec_rows(a.h, a.ldh, es) &&
                    vec_rows(a.dh, a.lddh, es) && vec_rows(a.o0, a.ldo0, es) && vec_rows(a.o1, a.ldo1, es) && at(a.in, 16) &&
                    at(a.h0, 16) && at(a.out, 16);
-  const Plan p = plan(a.T, a.B, a.D, vec, REV);
-  if (p.chunks * p.tiles > INT32_MAX) return DSF_EUNSUPPORTED;
-  a.chunks = int(p.chunks);
+  const Plan p = plan(a.T, a.D, rows_per_thread(es, REV));
   a.tiles = p.tiles;
   a.log_ct = p.log_ct;
-  a.L = a.B > 0 ? a.T / a.B : 0;
-  a.off = lengths ? reinterpret_cast<int*>(ws + p.off) : nullptr;
+  a.L = a.T / B;
+  a.ticket = reinterpret_cast<uint32_t*>(ws + p.sync);
+  int* total = reinterpret_cast<int*>(ws + p.sync) + 32;
+  a.total = lengths ? total : nullptr;
+  a.mark = ws + p.mark;
   a.first = reinterpret_cast<int*>(ws + p.first);
-  a.ticket = reinterpret_cast<uint32_t*>(ws + p.flags);
-  a.flags = a.ticket + 1;
-  a.group_flags = a.flags + p.chunks * p.tiles;
-  a.pairs = reinterpret_cast<float2*>(ws + p.pairs);
-  a.states = reinterpret_cast<float*>(ws + p.states);
+  a.last = reinterpret_cast<int*>(ws + p.last);
+  a.pairs = reinterpret_cast<unsigned long long*>(ws + p.pairs);
+  a.states = reinterpret_cast<unsigned long long*>(ws + p.states);
   a.chain = p.chunks > 1 && (lengths || p.C % a.L != 0);
+  if (p.chunks * p.tiles > INT32_MAX / 2) return DSF_EUNSUPPORTED;
   if (lengths || a.chain || (a.T == 0 && a.out)) {
-    PrepArgs q{lengths, reinterpret_cast<int*>(ws + p.off), reinterpret_cast<int*>(ws + p.first), a.T, a.B, a.D, p.C,
-               int(p.chunks), a.ticket, a.chain ? 1 + (p.chunks + p.groups) * p.tiles : 0, a.in, a.out, a.status};
-    long long blocks = (lengths || a.T == 0) ? ((long long)a.B + kPrep - 1) / kPrep : 1;
-    const long long zeroing = (q.zeros + 8 * kPrep - 1) / (8 * kPrep), most = 152;
-    if (blocks < zeroing) blocks = zeroing < most ? zeroing : (blocks < most ? most : blocks);
+    PrepArgs q{lengths, ws + p.mark, const_cast<int*>(a.first), const_cast<int*>(a.last), total, a.T, B, a.D,
+               reinterpret_cast<uint4*>(ws + p.pairs), a.chain ? (long long)((p.sync_bytes - 256) / 16) : 0, a.in, a.out, a.ticket, a.status};
+    long long blocks = (lengths || a.T == 0) ? ((long long)B + kPrep - 1) / kPrep : 1;
+    const long long filling = (q.fills + 4 * kPrep - 1) / (4 * kPrep), most = 152;
+    if (blocks < filling) blocks = filling < most ? filling : (blocks < most ? most : blocks);
     if (!pdl_launch(prep_kernel, dim3(unsigned(blocks)), kPrep, s, q)) return DSF_ECUDA;
   }
   if (a.T == 0) return DSF_OK;
-  constexpr int NT = REV ? kBwdRows : kFwdRows;
-  const long long blocks = p.chunks * p.tiles;
-  const bool ok = dtype == DSF_F32
-                      ? (vec ? launch<float, 4, NT, REV>(a, blocks, s) : launch<float, 1, NT, REV>(a, blocks, s))
-                      : (vec ? launch<__nv_bfloat16, 4, NT, REV>(a, blocks, s) : launch<__nv_bfloat16, 1, NT, REV>(a, blocks, s));
+  const long long items = p.chunks * p.tiles;
+  const bool ok = dtype == DSF_F32 ? (vec ? launch<float, REV, true>(a, items, s) : launch<float, REV, false>(a, items, s))
+                                   : (vec ? launch<__nv_bfloat16, REV, true>(a, items, s)
+                                          : launch<__nv_bfloat16, REV, false>(a, items, s));
   return ok ? DSF_OK : DSF_ECUDA;
 }
 
@@ -571,8 +730,8 @@ int check(int32_t dtype, const int32_t* lengths, int64_t T, int32_t B, int32_t D
   if (!lengths && B > 0 && T % B != 0) return DSF_EINVAL;
   return DSF_OK;
 }
-int check_ws(int64_t T, int32_t B, int32_t D, const void* ws, size_t ws_bytes) {
-  return ws && at(ws, 256) && ws_bytes >= ws_bytes_of(T, B, D) ? DSF_OK : DSF_EWORKSPACE;
+int check_ws(int64_t T, int32_t D, const void* ws, size_t ws_bytes) {
+  return ws && at(ws, 256) && ws_bytes >= ws_bytes_of(T, D) ? DSF_OK : DSF_EWORKSPACE;
 }
 
 }  // namespace
@@ -584,7 +743,7 @@ using namespace dsf::scan;
 extern "C" {
 
 size_t dsf_gated_scan_workspace_bytes(int64_t T, int32_t B, int32_t D) {
-  return sizes_ok(T, B, D) ? ws_bytes_of(T, B, D) : 0;
+  return sizes_ok(T, B, D) ? ws_bytes_of(T, D) : 0;
 }
 
 int ctr_gated_scan_fwd(const void* x, int64_t ldx, const void* gate, int64_t ldg, int32_t dtype, const int32_t* lengths,
@@ -593,13 +752,13 @@ int ctr_gated_scan_fwd(const void* x, int64_t ldx, const void* gate, int64_t ldg
   if (int rc = check(dtype, lengths, T, B, D, h0, h_last, nullptr)) return rc;
   const int es = dtype == DSF_F32 ? 4 : 2;
   if (T > 0 && (!rows_ok(x, ldx, D, es) || !rows_ok(gate, ldg, D, es) || !rows_ok(h, ldh, D, es))) return DSF_EINVAL;
-  if (int rc = check_ws(T, B, D, ws, ws_bytes)) return rc;
+  if (int rc = check_ws(T, D, ws, ws_bytes)) return rc;
   if (B == 0) return DSF_OK;
   Args a{};
   a.x = x, a.ldx = ldx, a.gate = gate, a.ldg = ldg, a.o0 = h, a.ldo0 = ldh;
   a.in = h0, a.out = h_last;
-  a.T = int(T), a.B = B, a.D = D, a.status = status;
-  return run<false>(a, dtype, lengths, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+  a.T = int(T), a.D = D, a.status = status;
+  return run<false>(a, B, dtype, lengths, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
 }
 
 int ctr_gated_scan_bwd(const void* dh, int64_t lddh, const void* x, int64_t ldx, const void* gate, int64_t ldg,
@@ -611,14 +770,14 @@ int ctr_gated_scan_bwd(const void* dh, int64_t lddh, const void* x, int64_t ldx,
   if (T > 0 && (!rows_ok(dh, lddh, D, es) || !rows_ok(x, ldx, D, es) || !rows_ok(gate, ldg, D, es) ||
                 !rows_ok(h, ldh, D, es) || !rows_ok(dx, lddx, D, es) || !rows_ok(dgate, lddg, D, es)))
     return DSF_EINVAL;
-  if (int rc = check_ws(T, B, D, ws, ws_bytes)) return rc;
+  if (int rc = check_ws(T, D, ws, ws_bytes)) return rc;
   if (B == 0) return DSF_OK;
   Args a{};
   a.x = x, a.ldx = ldx, a.gate = gate, a.ldg = ldg, a.h = h, a.ldh = ldh, a.dh = dh, a.lddh = lddh;
   a.o0 = dx, a.ldo0 = lddx, a.o1 = dgate, a.ldo1 = lddg;
   a.in = dh_last, a.h0 = h0, a.out = dh0;
-  a.T = int(T), a.B = B, a.D = D, a.status = status;
-  return run<true>(a, dtype, lengths, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+  a.T = int(T), a.D = D, a.status = status;
+  return run<true>(a, B, dtype, lengths, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -24,10 +24,11 @@ inline bool succeeded(cudaError_t e) {
 }
 
 template <class... P, class... A>
-bool pdl_launch(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t s, A&&... args) {
+bool pdl_launch_smem(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -35,6 +36,11 @@ bool pdl_launch(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t s,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return succeeded(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...));
+}
+
+template <class... P, class... A>
+bool pdl_launch(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t s, A&&... args) {
+  return pdl_launch_smem(kernel, grid, block, 0, s, std::forward<A>(args)...);
 }
 
 }  // namespace dsf
