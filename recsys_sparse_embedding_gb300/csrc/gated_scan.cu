@@ -140,7 +140,9 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src, bool any) {
 }
 
 // z = sigmoid(g) and a = 1 - z = t z, t = exp(-g), each to a few last bits of its
-// own size (below 2^-126: 0)
+// own size (below 2^-126: 0). (One reciprocal of a product for four channels, with
+// a branch for far gates, was slower: the special functions do not bind, and the
+// branch keeps the rows apart.)
 __device__ __forceinline__ void gate_of(float2 g, float2& z, float2& a) {
   const float2 e = g * pair(-kLog2e), t = make_float2(exp2_fast(e.x), exp2_fast(e.y)), d = t + pair(1.f);
   z = make_float2(rcp_fast(d.x), rcp_fast(d.y));
@@ -201,16 +203,16 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
   pdl_go();
   pdl_wait();
   const int total = a.total ? *a.total : a.T, chunks = (total + C - 1) / C;
-  const long long items = (long long)chunks * a.tiles;
+  const int items = chunks * a.tiles;  // (below 2^30: checked by the host)
 
   struct Item {
     int rank, tile, t0, n;  // n = 0: none
   };
-  auto item_at = [&](long long idx) {
+  auto item_at = [&](int idx) {
     Item it{0, 0, 0, 0};
     if (idx >= items) return it;
-    it.rank = int(idx / a.tiles);
-    it.tile = int(idx - (long long)it.rank * a.tiles);
+    it.rank = int(uint32_t(idx) / uint32_t(a.tiles));
+    it.tile = idx - it.rank * a.tiles;
     it.t0 = (REV ? chunks - 1 - it.rank : it.rank) * C;
     it.n = min(C, total - it.t0);
     return it;
@@ -369,54 +371,60 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
 
   // Items in flight: cur (rows to be written), nxt (pair to be taken) and aft
   // (being loaded), in three stages; the ticket of the one after it is fetched.
-  long long idx = blockIdx.x;
+  int idx = blockIdx.x;
+  uint32_t drawn = 0;  // (thread 0)
   auto request = [&](bool more) {
     if (!a.chain) idx += gridDim.x;
-    else if (tid == 0) s_ticket = int(more ? min((long long)(atomicAdd(a.ticket, 1u) + 1u), items) : items);
+    else if (tid == 0) drawn = more ? atomicAdd(a.ticket, 1u) + 1u : uint32_t(items);
+  };
+  auto announce = [&]() {
+    if (a.chain && tid == 0) s_ticket = int(min(drawn, uint32_t(items)));
+    __syncthreads();
+    if (a.chain) idx = s_ticket;
   };
   if (a.chain) {
     request(true);
-    __syncthreads();
-    idx = s_ticket;
+    announce();
     __syncthreads();
   }
   Item cur{0, 0, 0, 0}, nxt = item_at(idx);
   load(nxt, 0);
   request(nxt.n > 0);
-  __syncthreads();
-  if (a.chain) idx = s_ticket;
+  announce();
   __syncthreads();
   int st = 0, par = 0;  // the stage of nxt; parity of its buffers
   for (;;) {
     const Item aft = item_at(idx);
     const int st_aft = st + 1 == kStages ? 0 : st + 1;
-    load(aft, st_aft);
     request(aft.n > 0);
+    load(aft, st_aft);
+    // the pairs of cur's group before it and the state before the group (looked at
+    // now, awaited after the next item's rows)
+    const bool comes = cur.n > 0 && s_comes[par ^ 1];
+    const int group = cur.rank / kGroup, per = kGroup * W / kThreads, j0 = group * kGroup + tid / W * per;
+    const long long step = (long long)a.tiles * W;
+    const unsigned long long* pp = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + (tid & (W - 1));
+    const unsigned long long* ps = a.states + ((long long)(group - 1) * a.tiles + cur.tile) * W + tid;
+    unsigned long long raw[8], raw_state = 0;  // (per is 2, 4 or 8)
+    const int mine = comes ? min(per, cur.rank - j0) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw[j] = j < mine ? ld_relaxed_u64(pp + j * step) : 0ull;
+    if (comes && group > 0 && tid < W) raw_state = ld_relaxed_u64(ps);
     cp_async_wait_one_pending();
     if (nxt.n > 0) phase1(nxt, st, par, PA[1], PB[1]);
-    // the pairs of cur's group before it
-    const bool comes = cur.n > 0 && s_comes[par ^ 1];
-    const int group = cur.rank / kGroup;
     if (comes) {
-      const int per = kGroup * W / kThreads, ch = tid & (W - 1), j0 = group * kGroup + tid / W * per;
-      const unsigned long long* p = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + ch;
-      const long long step = (long long)a.tiles * W;
-      unsigned long long raw[8];  // (per is 2, 4 or 8)
       float QA = 1.f, QB = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) raw[j] = j < per && j0 + j < cur.rank ? ld_relaxed_u64(p + j * step) : 0ull;
-#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j >= per || j0 + j >= cur.rank) continue;
+        if (j >= mine) continue;
         float2 f;
-        ok = take(p + j * step, raw[j], f) && ok;
+        ok = take(pp + j * step, raw[j], f) && ok;
         compose(QA, QB, f.x, f.y);
         QA = f.x, QB = f.y;
       }
       s_look[tid] = make_float2(QA, QB);
     }
-    __syncthreads();
-    if (a.chain) idx = s_ticket;
+    announce();
     if (tid < W) {
       float y = 0.f;
       const long long at = (long long)cur.tile * W + tid;
@@ -428,9 +436,8 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
           QA = f.x, QB = f.y;
         }
         if (QA >= 0.f && group > 0) {
-          const unsigned long long* p = a.states + (long long)(group - 1) * a.tiles * W + at;
           float2 f;
-          ok = take(p, ld_relaxed_u64(p), f) && ok;
+          ok = take(ps, raw_state, f) && ok;
           y = f.x;
         }
         y = apply(QA, QB, y);
