@@ -10,19 +10,19 @@
 // compose. Rows are taken as one stream in which a sequence's first row is a
 // reset (its state comes from h0), so jagged lengths cost nothing.
 //
-// One pass over memory. An item is a chunk of rows by up to 64 channels (a
-// thread: 4 channels by NT rows). Its pair is published as soon as its rows have
-// arrived; a chunk's state is then put together from the pairs of the chunks
-// before it. (Without that, a pass for the pairs and a second over x and gate
-// would move 5/3 of the bytes.) Blocks are persistent and keep three items in
-// shared memory: one being loaded (cp.async, each thread what it will use
-// itself), one whose pair is taken, and one whose rows are written, its gates
-// computed again from the raw rows; so the wait for the chunks before is spent on
-// the next item. Blocks take items by a ticket, so they only wait for blocks that
-// have started, whatever else runs; every wait is bounded and sets
-// DSF_FLAG_TIMEOUT when it runs out.
+// One pass over memory. An item is a chunk of rows by up to 32 channels (a
+// thread: 4 channels by NT rows, in registers as what each row is without the
+// state before the thread's rows and what that state is multiplied with). The
+// item's pair is published at once; its state is then put together from the
+// pairs of the chunks before it, and its rows are written. (Without that, a pass
+// for the pairs and a second over x and gate would move 5/3 of the bytes.) Blocks
+// are persistent: as soon as an item's rows are in registers, the next item's are
+// on their way to shared memory (cp.async, each thread what it will use itself).
+// Blocks take items by a ticket, so they only wait for blocks that have started,
+// whatever else runs; every wait is bounded and sets DSF_FLAG_TIMEOUT when it
+// runs out.
 //
-// Fixed order: chunks are in groups of 32; a chunk starts from the state at the
+// Fixed order: chunks are in groups of 8; a chunk starts from the state at the
 // end of the group before its own and composes the pairs of its group in a
 // fixed tree, so equal calls give equal bits, however blocks are scheduled, and
 // the chain through memory has one step per group. A pair and a state are 8
@@ -38,6 +38,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "dense_math.cuh"
 #include "dinsparse.h"
@@ -49,15 +50,16 @@ namespace scan {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kGroup = 32;  // chunks per group
-constexpr int kStages = 3;
+constexpr int kMostWidth = 32;  // channels of an item
+constexpr int kGroup = 8;       // chunks per group: a thread takes one pair at most
+static_assert(kGroup * kMostWidth <= kThreads, "a pair per thread");
 constexpr int kMaxDim = 1 << 20;
 constexpr long long kMaxRows = 1 << 30;
 
-// rows per thread: 32 (fp32: 64) KB an item
+// rows per thread (the backward keeps four values of each element, the forward two)
 template <class T, bool REV>
 constexpr int rows_of() {
-  return REV || sizeof(T) == 4 ? 4 : 8;
+  return REV ? 4 : 8;
 }
 
 struct Args {
@@ -182,22 +184,18 @@ template <class T, bool REV>
 struct Shared {
   static constexpr int NT = rows_of<T, REV>(), NA = REV ? 4 : 2;
   static constexpr int kData = NA * NT * kThreads * int(sizeof(Raw<T>));
-  static constexpr int kMark = 8 * kThreads;
-  static constexpr int kStage = kData + kMark;
-  static constexpr int kBytes = kStages * kStage;
-  static constexpr int kBlocks = kBytes > 102 * 1024 ? 1 : 2;  // per SM
+  static constexpr int kBytes = kData + 8 * kThreads;
 };
 
 template <class T, bool REV, bool VEC>
-__global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __grid_constant__ Args a) {
   using S = Shared<T, REV>;
   constexpr int NT = S::NT, NA = S::NA;
   extern __shared__ __align__(16) uint8_t sm[];
-  // the warps' pairs of an item, then those of the warps before; two in turn
-  __shared__ float2 s_pair[2][kWarps][64];
+  __shared__ float2 s_pair[kWarps][kMostWidth];  // the warps' pairs, then those of the warps before
   __shared__ float2 s_look[kThreads];
-  __shared__ float s_carry[64];
-  __shared__ int s_comes[2], s_ticket;
+  __shared__ float s_carry[kMostWidth];
+  __shared__ int s_comes, s_ticket;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CT = 1 << a.log_ct, ct = tid & (CT - 1), slice = tid >> a.log_ct, C = (kThreads >> a.log_ct) * NT, W = 4 * CT;
   pdl_go();
@@ -220,16 +218,14 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
   // the thread's rows, in scan order: upwards, or from the chunk's end
   auto row_of = [&](int i) { return REV ? C - 1 - (slice * NT + i) : slice * NT + i; };
   const int low = REV ? C - NT - slice * NT : slice * NT;  // the lowest of them
-  auto slot = [&](int st, int arr, int i) {
-    return reinterpret_cast<Raw<T>*>(sm + st * S::kStage) + (arr * NT + i) * kThreads + tid;
-  };
-  auto marks = [&](int st) { return reinterpret_cast<uint8_t*>(sm + st * S::kStage + S::kData) + 8 * tid; };
+  auto slot = [&](int arr, int i) { return reinterpret_cast<Raw<T>*>(sm) + (arr * NT + i) * kThreads + tid; };
+  uint8_t* marks = sm + S::kData + 8 * tid;
   auto width = [&](const Item& it) { return a.D - (it.tile * CT + ct) * 4; };  // channels from the thread's first on
 
   // a chunk's rows that are all there (most are): the loops over them unrolled
   auto whole = [&](const Item& it) { return VEC && it.n == C && (!REV || it.t0 > 0); };
 
-  auto load = [&](const Item& it, int st) {
+  auto load = [&](const Item& it) {
     const int c0 = (it.tile * CT + ct) * 4, w = min(4, width(it));
     const bool live = it.n > 0 && w > 0;
     if (live) {
@@ -240,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
       for (int arr = 0; arr < NA; ++arr) {
         const long long t = it.t0 + low - (arr == 3 ? 1 : 0);  // h: the row before
         const T* p = src[arr] + t * ld[arr] + c0;
-        Raw<T>* d = slot(st, arr, REV ? NT - 1 : 0);
+        Raw<T>* d = slot(arr, REV ? NT - 1 : 0);
         constexpr int kNext = REV ? -kThreads : kThreads;
         if (whole(it)) {
 #pragma unroll
@@ -259,30 +255,28 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
           }
         }
       }
-      if (a.total) cp_async<NT>(marks(st), a.mark + it.t0 + low, true);
+      if (a.total) cp_async<NT>(marks, a.mark + it.t0 + low, true);
     }
     cp_async_commit();
     if (live && !a.total) {
       int r = (it.t0 + low) % a.L;
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        marks(st)[k] = uint8_t((r == 0 ? 1 : 0) | (r == a.L - 1 ? 2 : 0));
+        marks[k] = uint8_t((r == 0 ? 1 : 0) | (r == a.L - 1 ? 2 : 0));
         r = r + 1 == a.L ? 0 : r + 1;
       }
     }
   };
   // the marks of the thread's rows as two sets of bits (bit i: row i in scan
   // order): where the recurrence starts anew, and where its state leaves
-  auto sets = [&](const Item& it, int st, uint32_t& reset, uint32_t& leave) {
+  auto sets = [&](const Item& it, uint32_t& reset, uint32_t& leave) {
     reset = leave = 0;
-    uint32_t m[2] = {0, 0};
-    m[0] = *reinterpret_cast<const uint32_t*>(marks(st));
-    if (NT == 8) m[1] = *reinterpret_cast<const uint32_t*>(marks(st) + 4);
-    if (!(m[0] | m[1])) return;
-#pragma unroll 1
+    const uint32_t m0 = *reinterpret_cast<const uint32_t*>(marks),
+                   m1 = NT == 8 ? *reinterpret_cast<const uint32_t*>(marks + 4) : 0;
+    if (!(m0 | m1)) return;
+#pragma unroll
     for (int k = 0; k < NT; ++k) {
-      const uint32_t b = (k < 4 ? m[0] : m[1]) >> (8 * (k & 3)) & 3u;
-      if (low + k >= it.n) continue;
+      const uint32_t b = low + k < it.n ? (k < 4 ? m0 : m1) >> (8 * (k & 3)) & 3u : 0u;
       const int i = REV ? NT - 1 - k : k;
       reset |= ((REV ? b >> 1 : b) & 1u) << i;
       leave |= ((REV ? b : b >> 1) & 1u) << i;
@@ -291,67 +285,149 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
   auto seq_first = [&](long long t) { return a.total ? a.first[t] : int(t / a.L); };
   auto seq_last = [&](long long t) { return a.total ? a.last[t] : int(t / a.L); };
 
-  // what a row brings: a and B (backward: dh in its place)
-  auto row_pair = [&](int st, int i, float2* A, float2* Bv, float2* z) {
-    float2 v[2], g[2];
-    slot(st, REV ? 2 : 0, i)->get(v);
-    slot(st, 1, i)->get(g);
+  // The thread's rows in scan order. Forward: h = u[0] + u[1] y with y the state
+  // before them; backward: dx = u[0] + u[1] y, dgate = u[2] + u[3] y.
+  constexpr int NU = REV ? 4 : 2;
+  float2 u[NT][NU][2];
+  float2 A[2], Bv[2];  // the thread's pair
+  float2 leaveA[2], leaveB[2];  // backward: that of the rows up to the first that leaves, if no reset is among them
+  uint32_t reset, leave;
+  auto rows = [&](const Item& it, auto plain) {
+    constexpr bool PLAIN = decltype(plain)::value;
+    const int c0 = (it.tile * CT + ct) * 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      gate_of(g[h], z[h], A[h]);
-      Bv[h] = REV ? v[h] : z[h] * v[h];
+    for (int i = 0; i < NT; ++i) {
+      const bool in = PLAIN || row_of(i) < it.n;
+      if (!in) continue;
+      float2 g[2], v[2], z[2], a1[2], x[2], hp[2];
+      slot(1, i)->get(g);
+      slot(REV ? 2 : 0, i)->get(v);
+      if (REV) {
+        slot(0, i)->get(x);
+        slot(3, i)->get(hp);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) gate_of(g[h], z[h], a1[h]);
+      if (!PLAIN) {
+        const long long t = it.t0 + row_of(i);
+        if (reset >> i & 1u) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) A[h] = Bv[h] = pair(0.f);
+          if (a.in) {
+            load_state<VEC>(a.in + (long long)(REV ? seq_last(t) : seq_first(t)) * a.D + c0, Bv, width(it));
+          }
+        }
+        if (REV && (leave >> i & 1u)) {
+          hp[0] = hp[1] = pair(0.f);
+          if (a.h0) load_state<VEC>(a.h0 + (long long)seq_first(t) * a.D + c0, hp, width(it));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (REV) {
+          const float2 w = __ffma2_rn(hp[h], pair(-1.f), x[h]) * (z[h] * a1[h]), s = v[h] + Bv[h];
+          u[i][0][h] = z[h] * s;
+          u[i][1][h] = z[h] * A[h];
+          u[i][NU - 2][h] = w * s;
+          u[i][NU - 1][h] = w * A[h];
+          Bv[h] = a1[h] * s;
+          A[h] = a1[h] * A[h];
+          if (!PLAIN && (leave >> i & 1u) && !(reset & ((2u << i) - 1))) leaveA[h] = A[h], leaveB[h] = Bv[h];
+        } else {
+          Bv[h] = __ffma2_rn(a1[h], Bv[h], z[h] * v[h]);
+          A[h] = A[h] * a1[h];
+          u[i][0][h] = Bv[h];
+          u[i][1][h] = A[h];
+        }
+      }
+      if (!PLAIN && REV && (leave >> i & 1u) && (reset & ((2u << i) - 1)) && a.out)
+        store4<VEC>(a.out + (long long)seq_first(it.t0 + row_of(i)) * a.D + c0, Bv, width(it));
     }
   };
-  // at a reset, the state's part of B
-  auto add_state = [&](const Item& it, int i, const float2* A, float2* Bv) {
-    if (!a.in) return;
-    const long long t = it.t0 + row_of(i);
-    float2 s[2];
-    load_state<VEC>(a.in + (long long)(REV ? seq_last(t) : seq_first(t)) * a.D + (it.tile * CT + ct) * 4, s, width(it));
+  // the rows' outputs, and the states that leave: those of the pair's last row y
+  // steps on by
+  auto write = [&](const Item& it, const float2* y, auto plain) {
+    constexpr bool PLAIN = decltype(plain)::value;
+    const int c0 = (it.tile * CT + ct) * 4, w = width(it);
+    const long long t1 = it.t0 + row_of(0), d0 = REV ? -a.ldo0 : a.ldo0, d1 = -a.ldo1;
+    T* o0 = static_cast<T*>(a.o0) + t1 * a.ldo0 + c0;
+    T* o1 = REV ? static_cast<T*>(a.o1) + t1 * a.ldo1 + c0 : nullptr;
+    const int first = PLAIN || !reset ? NT : __ffs(reset) - 1;  // (from there on y has no part)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) Bv[h] = REV ? Bv[h] + s[h] : __ffma2_rn(A[h], s[h], Bv[h]);
-  };
-
-  float PA[2][4], PB[2][4];  // the pairs of the warp's threads before this one: of the item, of the next
-  float2 tot = make_float2(1.f, 0.f);  // (tid < W) the item's pair in channel tid
-  bool ok = true;
-
-  auto phase1 = [&](const Item& it, int st, int par, float* QA, float* QB) {
-    const bool live = it.n > 0 && width(it) > 0;
-    float2 A[2] = {pair(1.f), pair(1.f)}, Bv[2] = {};
-    bool any = false;
-    if (live) {
-      uint32_t reset, leave;
-      sets(it, st, reset, leave);
-      any = reset != 0;
-      auto row = [&](int i, bool r) {
-        float2 ra[2], rb[2], z[2];
-        row_pair(st, i, ra, rb, z);
-        if (r) {
-          add_state(it, i, ra, rb);
-          Bv[0] = Bv[1] = pair(0.f);
-          if (!REV) ra[0] = ra[1] = pair(0.f);
-        }
+    for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0) {
+      if (!PLAIN && row_of(i) >= it.n) continue;
+      float2 p[2], q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        p[h] = __ffma2_rn(u[i][1][h], y[h], u[i][0][h]);
+        if (REV) q[h] = __ffma2_rn(u[i][NU - 1][h], y[h], u[i][NU - 2][h]);
+      }
+      if (!PLAIN && i >= first) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          Bv[h] = REV ? ra[h] * (Bv[h] + rb[h]) : __ffma2_rn(ra[h], Bv[h], rb[h]);
-          A[h] = A[h] * ra[h];
+          p[h] = u[i][0][h];
+          if (REV) q[h] = u[i][NU - 2][h];
         }
-      };
-      if (whole(it) && !any) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) row(i, false);
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < NT; ++i)
-          if (row_of(i) < it.n) row(i, reset >> i & 1u);
       }
-      if (tid == 0) s_comes[par] = a.chain && !(reset & 1u) && !(REV && it.n < C);
+      store4<VEC>(o0, p, w);
+      if (REV) store4<VEC>(o1, q, w);
+      if (!PLAIN && !REV && (leave >> i & 1u) && a.out)
+        store4<VEC>(a.out + (long long)seq_last(it.t0 + row_of(i)) * a.D + c0, p, w);
     }
-    float qa[4] = {A[0].x, A[0].y, A[1].x, A[1].y}, qb[4] = {Bv[0].x, Bv[0].y, Bv[1].x, Bv[1].y};
+    if (!PLAIN && REV && leave && !(reset & ((leave & -leave) * 2 - 1)) && a.out) {
+      float2 p[2];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (any) qa[v] = -1.f;
+      for (int h = 0; h < 2; ++h) p[h] = __ffma2_rn(leaveA[h], y[h], leaveB[h]);
+      store4<VEC>(a.out + (long long)seq_first(it.t0 + row_of(__ffs(leave) - 1)) * a.D + c0, p, w);
+    }
+  };
+
+  int idx = blockIdx.x;
+  uint32_t drawn = 0;  // (thread 0)
+  auto request = [&]() {
+    if (!a.chain) idx += gridDim.x;
+    else if (tid == 0) drawn = atomicAdd(a.ticket, 1u) + 1u;
+  };
+  auto announce = [&]() {
+    if (a.chain && tid == 0) s_ticket = int(min(drawn, uint32_t(items)));
+    __syncthreads();
+    if (a.chain) idx = s_ticket;
+  };
+  if (a.chain) {
+    request();
+    announce();
+    __syncthreads();
+  }
+  bool ok = true;
+  Item cur = item_at(idx);
+  load(cur);
+  while (cur.n > 0) {
+    request();
+    // the pairs of the item's group before it and the state before the group (looked
+    // at now, awaited when the item's own pair is out)
+    const int group = cur.rank / kGroup, j0 = group * kGroup + tid / W;
+    const long long step = (long long)a.tiles * W;
+    const unsigned long long* pp = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + (tid & (W - 1));
+    const unsigned long long* ps = a.states + ((long long)(group - 1) * a.tiles + cur.tile) * W + tid;
+    unsigned long long raw = kNone, raw_state = kNone;
+    const bool mine = a.chain && j0 < cur.rank;
+    if (mine) raw = ld_relaxed_u64(pp);
+    if (a.chain && group > 0 && tid < W) raw_state = ld_relaxed_u64(ps);
+
+    cp_async_wait_all();
+    const bool live = width(cur) > 0;
+    A[0] = A[1] = pair(1.f);
+    Bv[0] = Bv[1] = pair(0.f);
+    reset = leave = 0;
+    if (live) sets(cur, reset, leave);
+    const bool plain = whole(cur) && !(reset | leave);
+    if (live) {
+      if (plain) rows(cur, std::true_type{});
+      else rows(cur, std::false_type{});
+    }
+    if (tid == 0) s_comes = a.chain && !(reset & 1u) && !(REV && cur.n < C);
+    float qa[4] = {A[0].x, A[0].y, A[1].x, A[1].y}, qb[4] = {Bv[0].x, Bv[0].y, Bv[1].x, Bv[1].y};
+    if (reset) qa[0] = qa[1] = qa[2] = qa[3] = -1.f;
     for (int d = CT; d < 32; d <<= 1)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -360,78 +436,37 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
       }
     if (lane >= 32 - CT)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s_pair[par][warp][ct * 4 + v] = make_float2(qa[v], qb[v]);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float ap = __shfl_up_sync(0xffffffffu, qa[v], CT), bp = __shfl_up_sync(0xffffffffu, qb[v], CT);
-      QA[v] = lane >= CT ? ap : 1.f;
-      QB[v] = lane >= CT ? bp : 0.f;
-    }
-  };
-
-  // Items in flight: cur (rows to be written), nxt (pair to be taken) and aft
-  // (being loaded), in three stages; the ticket of the one after it is fetched.
-  int idx = blockIdx.x;
-  uint32_t drawn = 0;  // (thread 0)
-  auto request = [&](bool more) {
-    if (!a.chain) idx += gridDim.x;
-    else if (tid == 0) drawn = more ? atomicAdd(a.ticket, 1u) + 1u : uint32_t(items);
-  };
-  auto announce = [&]() {
-    if (a.chain && tid == 0) s_ticket = int(min(drawn, uint32_t(items)));
-    __syncthreads();
-    if (a.chain) idx = s_ticket;
-  };
-  if (a.chain) {
-    request(true);
+      for (int v = 0; v < 4; ++v) s_pair[warp][ct * 4 + v] = make_float2(qa[v], qb[v]);
     announce();
-    __syncthreads();
-  }
-  Item cur{0, 0, 0, 0}, nxt = item_at(idx);
-  load(nxt, 0);
-  request(nxt.n > 0);
-  announce();
-  __syncthreads();
-  int st = 0, par = 0;  // the stage of nxt; parity of its buffers
-  for (;;) {
-    const Item aft = item_at(idx);
-    const int st_aft = st + 1 == kStages ? 0 : st + 1;
-    request(aft.n > 0);
-    load(aft, st_aft);
-    // the pairs of cur's group before it and the state before the group (looked at
-    // now, awaited after the next item's rows)
-    const bool comes = cur.n > 0 && s_comes[par ^ 1];
-    const int group = cur.rank / kGroup, per = kGroup * W / kThreads, j0 = group * kGroup + tid / W * per;
-    const long long step = (long long)a.tiles * W;
-    const unsigned long long* pp = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + (tid & (W - 1));
-    const unsigned long long* ps = a.states + ((long long)(group - 1) * a.tiles + cur.tile) * W + tid;
-    unsigned long long raw[8], raw_state = 0;  // (per is 2, 4 or 8)
-    const int mine = comes ? min(per, cur.rank - j0) : 0;
+    const bool comes = s_comes;
+    const Item nxt = item_at(idx);
+    load(nxt);  // (in the place that the thread has just read)
+    float2 tot = make_float2(1.f, 0.f);  // (tid < W) the item's pair in channel tid
+    if (tid < W) {
+      float2 p[kWarps];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) raw[j] = j < mine ? ld_relaxed_u64(pp + j * step) : 0ull;
-    if (comes && group > 0 && tid < W) raw_state = ld_relaxed_u64(ps);
-    cp_async_wait_one_pending();
-    if (nxt.n > 0) phase1(nxt, st, par, PA[1], PB[1]);
-    if (comes) {
-      float QA = 1.f, QB = 0.f;
+      for (int k = 0; k < kWarps; ++k) p[k] = s_pair[k][tid];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= mine) continue;
-        float2 f;
-        ok = take(pp + j * step, raw[j], f) && ok;
-        compose(QA, QB, f.x, f.y);
-        QA = f.x, QB = f.y;
+      for (int k = 0; k < kWarps; ++k) {
+        s_pair[k][tid] = tot;
+        compose(tot.x, tot.y, p[k].x, p[k].y);
+        tot = p[k];
       }
-      s_look[tid] = make_float2(QA, QB);
+      if (a.chain) give(a.pairs + ((long long)cur.rank * a.tiles + cur.tile) * W + tid, tot);
     }
-    announce();
+    if (comes) {
+      float2 f = make_float2(1.f, 0.f);
+      if (mine) ok = take(pp, raw, f) && ok;
+      if (tid < kGroup * W) s_look[tid] = f;
+      __syncthreads();
+    }
     if (tid < W) {
       float y = 0.f;
-      const long long at = (long long)cur.tile * W + tid;
       if (comes) {
         float QA = 1.f, QB = 0.f;
-        for (int k = tid; k < kThreads; k += W) {
-          float2 f = s_look[k];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+          float2 f = s_look[k * W + tid];
           compose(QA, QB, f.x, f.y);
           QA = f.x, QB = f.y;
         }
@@ -441,91 +476,32 @@ __global__ void __launch_bounds__(kThreads, Shared<T, REV>::kBlocks) scan_kernel
           y = f.x;
         }
         y = apply(QA, QB, y);
-        s_carry[tid] = y;
       }
-      if (a.chain && cur.n > 0 && cur.rank % kGroup == kGroup - 1)
-        give(a.states + (long long)group * a.tiles * W + at, make_float2(apply(tot.x, tot.y, y), 0.f));
-      if (nxt.n > 0) {
-        float2 s = make_float2(1.f, 0.f);
+      s_carry[tid] = y;
+      if (a.chain && cur.rank % kGroup == kGroup - 1) give(const_cast<unsigned long long*>(ps) + step, make_float2(apply(tot.x, tot.y, y), 0.f));
+    }
+    // the state before the thread's rows: of the warp's threads before it, of the warps
+    // before, of the chunks before
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          float2 f = s_pair[par][k][tid];
-          s_pair[par][k][tid] = s;
-          compose(s.x, s.y, f.x, f.y);
-          s = f;
-        }
-        tot = s;
-        if (a.chain) give(a.pairs + ((long long)nxt.rank * a.tiles + nxt.tile) * W + tid, s);
-      }
+    for (int v = 0; v < 4; ++v) {
+      const float ap = __shfl_up_sync(0xffffffffu, qa[v], CT), bp = __shfl_up_sync(0xffffffffu, qb[v], CT);
+      qa[v] = lane >= CT ? ap : 1.f;
+      qb[v] = lane >= CT ? bp : 0.f;
     }
     __syncthreads();
-    if (cur.n > 0 && width(cur) > 0) {
-      const int sc = st == 0 ? kStages - 1 : st - 1, w = width(cur), c0 = (cur.tile * CT + ct) * 4;
-      uint32_t reset, leave;
-      sets(cur, sc, reset, leave);
+    if (live) {
       float2 y[2];
       float* yf = reinterpret_cast<float*>(y);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float2 e = s_pair[par ^ 1][warp][ct * 4 + v];
-        float A = PA[0][v], B = PB[0][v];
-        compose(e.x, e.y, A, B);
-        yf[v] = apply(A, B, comes ? s_carry[ct * 4 + v] : 0.f);
+        const float2 e = s_pair[warp][ct * 4 + v];
+        yf[v] = apply(qa[v], qb[v], apply(e.x, e.y, s_carry[ct * 4 + v]));
       }
-      // a row: its state, its outputs; r: a reset, l: the state leaves
-      auto row = [&](int i, bool r, bool l, T* o0, T* o1) {
-        const long long t = cur.t0 + row_of(i);
-        float2 A[2], Bv[2], z[2];
-        row_pair(sc, i, A, Bv, z);
-        if (r) {
-          add_state(cur, i, A, Bv);
-          y[0] = y[1] = pair(0.f);
-        }
-        if (REV) {
-          float2 x[2], hp[2], dx[2], dg[2];
-          slot(sc, 0, i)->get(x);
-          slot(sc, 3, i)->get(hp);
-          if (l) {
-            hp[0] = hp[1] = pair(0.f);
-            if (a.h0) load_state<VEC>(a.h0 + (long long)seq_first(t) * a.D + c0, hp, w);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 g = Bv[h] + y[h];
-            dx[h] = g * z[h];
-            dg[h] = g * (__ffma2_rn(hp[h], pair(-1.f), x[h]) * (z[h] * A[h]));
-            y[h] = A[h] * g;
-          }
-          store4<VEC>(o0, dx, w);
-          store4<VEC>(o1, dg, w);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) y[h] = __ffma2_rn(r ? pair(0.f) : A[h], y[h], Bv[h]);
-          store4<VEC>(o0, y, w);
-        }
-        if (l && a.out) store4<VEC>(a.out + (long long)(REV ? seq_first(t) : seq_last(t)) * a.D + c0, y, w);
-      };
-      const long long t1 = cur.t0 + row_of(0), d0 = REV ? -a.ldo0 : a.ldo0, d1 = -a.ldo1;
-      T* o0 = static_cast<T*>(a.o0) + t1 * a.ldo0 + c0;
-      T* o1 = REV ? static_cast<T*>(a.o1) + t1 * a.ldo1 + c0 : nullptr;
-      if (whole(cur) && !(reset | leave)) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0) row(i, false, false, o0, o1);
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0)
-          if (row_of(i) < cur.n) row(i, reset >> i & 1u, leave >> i & 1u, o0, o1);
-      }
+      if (plain) write(cur, y, std::true_type{});
+      else write(cur, y, std::false_type{});
     }
-    if (nxt.n == 0) break;
     cur = nxt;
-    nxt = aft;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) PA[0][v] = PA[1][v], PB[0][v] = PB[1][v];
-    st = st_aft;
-    par ^= 1;
   }
-  cp_async_wait_all();
   if (!ok && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
 }
 
@@ -594,21 +570,11 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
     b = int(min(end - len, T));
     e = int(min(end, T));
     if (s == a.B - 1) *a.total = e;
-    const bool some = s < a.B && e > b, many = some && e - b > 32;
-    if (some) {
+    if (s < a.B && e > b) {  // (the marks are zero beforehand)
       a.first[b] = int(s);
       a.last[e - 1] = int(s);
-      if (!many)
-        for (int t = b; t < e; ++t) a.mark[t] = uint8_t((t == b ? 1 : 0) | (t == e - 1 ? 2 : 0));
-    }
-    // a long sequence's marks by the warp: 16 rows per lane, its ends row by row
-    for (uint32_t m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
-      const int l = __ffs(m) - 1, tb = __shfl_sync(0xffffffffu, b, l), te = __shfl_sync(0xffffffffu, e, l);
-      const int v0 = (tb + 16) / 16, v1 = (te - 1) / 16;  // whole vectors behind the first row and before the last
-      for (long long v = v0 + lane; v < v1; v += 32) reinterpret_cast<uint4*>(a.mark)[v] = make_uint4(0, 0, 0, 0);
-      const int head = min(te, v0 * 16), rear = max(head, v1 * 16);
-      for (int t = tb + lane; t < head; t += 32) a.mark[t] = uint8_t((t == tb ? 1 : 0) | (t == te - 1 ? 2 : 0));
-      for (int t = rear + lane; t < te; t += 32) a.mark[t] = uint8_t(t == te - 1 ? 2 : 0);
+      a.mark[b] = e - b == 1 ? 3 : 1;
+      if (e - b > 1) a.mark[e - 1] = 2;
     }
   }
   if (!a.out) return;
@@ -636,8 +602,10 @@ struct Plan {
 };
 Plan plan(long long T, int D, int nt) {
   Plan p{};
-  p.log_ct = 2;  // 4, 8 or 16 threads of 4 channels
-  while (p.log_ct < 4 && (4 << p.log_ct) < D) ++p.log_ct;
+  // 8 threads of 4 channels, or 4 where that leaves fewer without one. (Of 8192 x 1024
+  // rows' passes, 4, 8 and 16: 804, 715 and 882 us; wide chunks are short in rows, and
+  // wait for more of them that are under way.)
+  p.log_ct = (D + 31) / 32 * 2 == (D + 15) / 16 ? 3 : 2;
   p.C = (kThreads >> p.log_ct) * nt;
   const int width = 4 << p.log_ct;
   p.tiles = (D + width - 1) / width;
@@ -717,6 +685,7 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
     long long blocks = (lengths || a.T == 0) ? ((long long)B + kPrep - 1) / kPrep : 1;
     const long long filling = (q.fills + 4 * kPrep - 1) / (4 * kPrep), most = 152;
     if (blocks < filling) blocks = filling < most ? filling : (blocks < most ? most : blocks);
+    if (lengths && a.T > 0 && !succeeded(cudaMemsetAsync(ws + p.mark, 0, size_t(a.T), s))) return DSF_ECUDA;
     if (!pdl_launch(prep_kernel, dim3(unsigned(blocks)), kPrep, s, q)) return DSF_ECUDA;
   }
   if (a.T == 0) return DSF_OK;
