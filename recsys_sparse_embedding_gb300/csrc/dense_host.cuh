@@ -114,8 +114,8 @@ long long least_splits(bool f32, long long blocks) {
 // and the runs would not be seen.)
 constexpr long long kDzBlocks = 8;
 
-// Picks the configuration and the K-splits of one product.
-void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg, bool may_split) {
+// Picks the configuration and the K-splits of one product; its time by the model.
+double plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg, bool may_split) {
   const Cost cost{p.f32};
   double best = 1e300;
   Job o = p.a.job[0];
@@ -139,10 +139,11 @@ void plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg,
       }
     }
   }
+  return best;
 }
 
 // dW (job 0, which may be split) and dx (job 1) in one launch.
-void plan_dual(Product& p, long long M, long long N, long long K, int halves) {
+double plan_dual(Product& p, long long M, long long N, long long K, int halves) {
   const Cost cost{p.f32};
   const long long kw = (M + 63) / 64, kx = (N + 63) / 64, least = least_splits(p.f32, kw);
   double best = 1e300;
@@ -168,6 +169,7 @@ void plan_dual(Product& p, long long M, long long N, long long K, int halves) {
         p.weight[1] = weight[1];
       }
     }
+  return best;
 }
 
 long long up(long long v, long long to) { return (v + to - 1) / to * to; }

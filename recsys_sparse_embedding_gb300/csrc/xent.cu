@@ -169,6 +169,17 @@ void plan_xent(Product& p, long long M, long long N, long long nkb) {
   }
 }
 
+// Whether dx and dW are best made in one launch, where dx's sums (over the
+// columns) are not split: with few rows and many columns each of its few tiles
+// would take all of them in turn (500 x 176 fp32 over 12,961 columns: 200 us in
+// one launch).
+bool together(long long M, long long N, long long K, bool f32) {
+  Product p{}, q{}, r{};
+  p.f32 = q.f32 = r.f32 = f32;
+  p.epi = q.epi = r.epi = kEpiOut;
+  return plan_dual(p, M, N, K, 1) <= plan(q, N, K, 1, (M + 63) / 64, 1, true) + plan(r, M, K, 1, (N + 63) / 64, 1, true);
+}
+
 bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, long long M, float* loss,
               float* lse, uint8_t* ws, int* status, cudaStream_t s) {
   const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
@@ -261,6 +272,10 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
     if (!run_xent_product(p, s)) return false;
     if (db && !colsum(sums, (M + 31) / 32, int(n), db + v, s)) return false;
     void* dWv = dW ? static_cast<uint8_t*>(dW) + v * K * es : nullptr;
+    if (one && dx && dWv && !together(M, n, K, f32)) {
+      if (!grad_products(c, dz, nullptr, 0, dWv)) return false;
+      return grad_products(c, dz, dx, lddx, nullptr);
+    }
     if (one) return grad_products(c, dz, dx, lddx, dWv);
     if (dWv && !grad_products(c, dz, nullptr, 0, dWv)) return false;
     if (!dx) continue;
