@@ -81,7 +81,7 @@ enum Epi {
   kEpiAcc = 5,   // the same, added to what the planes hold
   // softmax cross entropy over the columns (z in units of log 2 where it is an
   // exponent; the target's column per row):
-  kEpiLse = 6,   // per row and tile the maximum and the sum of exp(z - it); z of the target
+  kEpiLse = 6,   // per row a reference and the sum of exp(z - it), over the tiles that a warp has of the row; z of the target
   kEpiXent = 7,  // out = g (exp(z - lse) - [column = target]) (fp32: its three terms); column sums
 };
 enum Kind { kBf16 = 0, kE4m3 = 1 };
@@ -131,7 +131,12 @@ struct TcArgs {
   float* part;  // kEpiDz, kEpiXent: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
   const long long* target;  // kEpiLse, kEpiXent: per row the target's column in all of W (outside: none)
   int v0;                   // the first column here, of them
-  float2* stat;             // kEpiLse: [N tile][M] (maximum, sum)
+  float2* stat;             // kEpiLse: [lane * warps per row + warp][M] (reference, sum)
+  // kEpiLse, kEpiXent: gm neighbouring M tiles are worked on together, each by
+  // `lanes` clusters that share out its N tiles; so a cluster stays with its rows,
+  // and a tile of B serves gm tiles of A from L2
+  int gm, lanes, positions;  // positions: N tiles times groups of gm
+  Div by_nt;
   float* zt;                // kEpiLse: [M]
   const float2* rows;       // kEpiXent: [M] (lse, g)
   int* status;
@@ -390,6 +395,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   struct Unit {
     int job, m0, n0, batch, split, kb0, kbn;
   };
+  const int lane_of = EPI == kEpiLse || EPI == kEpiXent ? unit0 / a.gm : 0, mg = unit0 - lane_of * a.gm;
   const auto& job0 = a.job[0];
   const int units = job0.mt * job0.nt * job0.nb * job0.splits;
   auto unit_at = [&](int i, Unit& t) {
@@ -405,6 +411,17 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         const Job& o = a.job[t.job];
         if (u >= o.mt * o.nt * o.nb * o.splits) return false;
       }
+    } else if (EPI == kEpiLse || EPI == kEpiXent) {
+      const int at = lane_of + i * a.lanes;
+      if (lane_of >= a.lanes || at >= a.positions) return false;
+      const int group = int(div_by(at, a.by_nt)), m = group * a.gm + mg;
+      if (m >= job0.mt) return false;
+      t.split = t.batch = 0;
+      t.m0 = m * 128 * CG + int(rank) * 128;
+      t.n0 = (at - group * job0.nt) * ON;
+      t.kb0 = 0;
+      t.kbn = job0.nkb;
+      return true;
     } else if (u >= units) {
       return false;
     }
@@ -681,8 +698,9 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     constexpr bool PRE = IN && sizeof(TO) == 2;
     uint4 pin[PRE ? NV : 1];
     float bias_g = 0.f, bias_u = 0.f;
+    const bool ahead = IN || (XENT ? has_bias : S::BIAS);  // whether items take anything from memory
     auto prefetch = [&](bool any, const Unit& t, int c) {
-      if (!IN && !S::BIAS) return;
+      if (!ahead) return;
       const int r = any ? t.m0 + 32 * q : job0.M, cc = t.n0 + c * CW;
       const TO* in = in_of(t);
       if (PRE) load_item(in, pin, a.in_vec ? r : job0.M, cc);
@@ -698,7 +716,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       }
     };
     auto prefetch_after = [&](int i, const Unit& t, int c) {  // the item after item c of unit i
-      if (!IN && !S::BIAS) return;
+      if (!ahead) return;
       if (c + GR < NCH) {
         prefetch(true, t, c + GR);
       } else {
@@ -710,19 +728,6 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     Unit t;
     t.m0 = t.n0 = t.split = t.batch = 0;
     prefetch(unit_at(0, t) && grp < NCH, t, grp);
-    // what a cross entropy's next unit takes per row: the target, lse and g
-    long long next_target = -1;
-    float2 next_row = make_float2(0.f, 0.f);
-    auto prefetch_row = [&](int i) {
-      if (!XENT) return;
-      Unit n;
-      if (!unit_at(i, n)) return;
-      const int r = n.m0 + 32 * q + lane;
-      next_target = r < job0.M ? __ldg(a.target + r) : -1;
-      if (EPI == kEpiXent) next_row = r < job0.M ? __ldg(a.rows + r) : make_float2(0.f, 0.f);
-    };
-    prefetch_row(0);
-
     uint32_t run = 0;
     bool ok = true;
     auto wait_run = [&]() {  // the run's accumulator is complete
@@ -738,39 +743,30 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       if (lane == 0) mbar_arrive_relaxed(tempty0 + (run % S::NACC) * 8u);
       ++run;
     };
-    // kEpiLse: the tile's maximum and sum of each row, of the warps that share its
-    // rows (by way of their buffers, two in turn: a warp is at most one unit ahead)
-    int units_met = 0;
-    auto unit_stat = [&](int i, const Unit& t, int row, float top, float total) {
-      const int at = (i & 1) * 32 + lane;
-      reinterpret_cast<float2*>(buf)[at] = make_float2(top, total);
-      ++units_met;
-      asm volatile("bar.sync %0, %1;" ::"r"(2 + q), "n"(32 * GR) : "memory");
-      if (grp != 0) return;
-      float2 p[GR];
-      float m = -kFar, s = 0.f;
-#pragma unroll
-      for (int k = 0; k < GR; ++k) {
-        p[k] = reinterpret_cast<const float2*>(sE + (q + 4 * k) * S::ITEM)[at];
-        m = fmaxf(m, p[k].x);
-      }
-#pragma unroll
-      for (int k = 0; k < GR; ++k) s += p[k].y * exp2_fast(p[k].x - m);
-      if (row < job0.M) a.stat[(long long)(t.n0 / ON) * job0.M + row] = make_float2(m, s);
+    // a cross entropy's rows: the target's column (or one that no item has), lse and
+    // g; kEpiLse: the reference (in units of log 2) and sum over the warp's items so
+    // far, written when the warp goes on to other rows
+    int stat_m0 = -1, tgt = -1;
+    float2 of_row = make_float2(0.f, 0.f);
+    bool fresh = true;
+    float top = -kFar, total = 0.f;
+    auto put_stat = [&]() {
+      const int r = stat_m0 + 32 * q + lane;
+      if (stat_m0 >= 0 && r < job0.M) a.stat[((long long)lane_of * GR + grp) * job0.M + r] = make_float2(top, total);
     };
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const Job& jb = a.job[DUAL ? t.job : 0];
       const int row0 = t.m0 + 32 * q, row = row0 + lane;
       const TO* in = in_of(t);
-      // the target's column here (or one that no item has)
-      int tgt = -1;
-      float2 of_row = next_row;
-      if (XENT) {
-        const long long d = next_target - a.v0;
-        tgt = next_target >= 0 && d >= 0 && d < jb.N ? int(d) : -1;
-        prefetch_row(i + 1);
+      if (XENT && t.m0 != stat_m0) {  // other rows: their targets, lse and g
+        if (EPI == kEpiLse) put_stat();
+        stat_m0 = t.m0;
+        fresh = true;
+        top = -kFar, total = 0.f;
+        const long long id = row < jb.M ? __ldg(a.target + row) : -1, d = id - a.v0;
+        tgt = id >= 0 && d >= 0 && d < jb.N ? int(d) : -1;
+        if (EPI == kEpiXent) of_row = row < jb.M ? __ldg(a.rows + row) : make_float2(0.f, 0.f);
       }
-      float top = -kFar, total = 0.f;  // kEpiLse: over the warp's items
       // one item: 32 rows by CW columns. In runs: pg, pu hold its sums
       auto do_item = [&](int c, uint32_t tacc, float* pg, float* pu) {
         const int cc = GATED && EPI == kEpiPart ? (c * CW) % ON : c * CW, col0 = t.n0 + cc;
@@ -840,6 +836,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         if (!RUN) tmem_ld_wait();
         if (XENT) {
           const float* b = wbias;
+          if (has_bias)
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(b + j);
@@ -862,33 +859,44 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
                 if (tgt - col0 == k) z = g[k];
               if (unsigned(tgt - col0) < 32u && row < jb.M) a.zt[row] = z;
             }
-            float m[4];  // (fmaxf leaves a NaN to the sum)
+            // Any reference serves that keeps the sum in range: the first item's
+            // maximum, until a sum grows past 2^80 (or is none)
+            auto add = [&](float ref) {
+              float2 s[2] = {pair(0.f), pair(0.f)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(g[k], g[k + 4]), g[k + 8]);
+              for (int k = 0; k < 32; k += 4)
 #pragma unroll
-            for (int k = 12; k < 32; k += 4)
+                for (int h = 0; h < 2; ++h) {
+                  const float2 e = __ffma2_rn(make_float2(g[k + 2 * h], g[k + 2 * h + 1]), pair(kLog2e), pair(-ref));
+                  s[h] = s[h] + make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                }
+              return (s[0].x + s[0].y) + (s[1].x + s[1].y);
+            };
+            float more = 0.f;
+            if (!fresh) more = total + add(top);
+            if (fresh || __any_sync(0xffffffffu, !(more < 0x1p80f))) {
+              float m[4];  // (fmaxf leaves a NaN to the sum)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], g[k + e]);
-            const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-            const float now = fmaxf(top, fminf(most * kLog2e, kFar));
-            float2 s[2] = {make_float2(total * exp2_fast(top - now), 0.f), make_float2(0.f, 0.f)};
+              for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(g[k], g[k + 4]), g[k + 8]);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
+              for (int k = 12; k < 32; k += 4)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float2 e = __ffma2_rn(make_float2(g[k + 2 * h], g[k + 2 * h + 1]), pair(kLog2e), pair(-now));
-                s[h] = s[h] + make_float2(exp2_fast(e.x), exp2_fast(e.y));
-              }
-            top = now;
-            total = (s[0].x + s[0].y) + (s[1].x + s[1].y);
+                for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], g[k + e]);
+              const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+              const float now = fmaxf(top, fminf(most * kLog2e, kFar));
+              more = total * exp2_fast(top - now) + add(now);
+              top = now;
+              fresh = false;
+            }
+            total = more;
             __syncwarp();  // (the bias is read)
             return;
           } else {
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             const float2 e = __ffma2_rn(make_float2(g[k], g[k + 1]), pair(kLog2e), pair(-of_row.x));
-            g[k] = of_row.y * exp2_fast(e.x);
-            g[k + 1] = of_row.y * exp2_fast(e.y);
+            const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y)) * pair(of_row.y);
+            g[k] = p.x, g[k + 1] = p.y;
           }
           if (of_row.y == 0.f) {  // (a row left out, whatever it holds)
 #pragma unroll
@@ -1047,20 +1055,15 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
 #pragma unroll
         for (int k = 0; k < NI; ++k)
           if (grp + GR * k < NCH) do_item(grp + GR * k, 0, sum[k][0], sum[k][PAIR ? 1 : 0]);
-        if constexpr (EPI == kEpiLse) unit_stat(i, t, row, top, total);
       } else {
         if (!wait_run()) break;
         const uint32_t tacc = tbase + (run % S::NACC) * S::ACC + lane_base;
 #pragma unroll 1
         for (int c = grp; c < NCH; c += GR) do_item(c, tacc, nullptr, nullptr);
         done_run();
-        if constexpr (EPI == kEpiLse) unit_stat(i, t, row, top, total);
       }
     }
-    if constexpr (EPI == kEpiLse) {  // (the other warps wait for one that gave up)
-      if (!ok)
-        for (; unit_at(units_met, t); ++units_met) asm volatile("bar.sync %0, %1;" ::"r"(2 + q), "n"(32 * GR) : "memory");
-    }
+    if constexpr (EPI == kEpiLse) put_stat();
     if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
   }
   tc_fence_before();
@@ -1089,6 +1092,7 @@ struct Product {
   bool gated, f32;  // f32: fp32 operands (in terms)
   int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64, 3 (bf16 dz in runs): CG 2 x BN 128
   long long weight[2];  // kDual: a unit's time, by job
+  int* lse_grid;        // kEpiLse: where the launch writes the lanes and the M tiles of a group
 };
 
 bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows);
@@ -1127,6 +1131,19 @@ inline Deal deal(const TcArgs& a, const long long (&w)[2], long long C) {
       best.l1 = int(l1);
       best.load = x > y ? x : y;
     }
+  }
+  return best;
+}
+
+// A cross entropy's groups: of 4 M tiles, or fewer where those would leave clusters without
+// work (a tile of B is read from memory once per group: more than 2 are enough).
+inline int lse_group(long long mt, long long clusters) {
+  int best = 1;
+  double most = 0;
+  for (int gm = 4; gm >= 1; gm /= 2) {
+    if (gm > clusters) continue;
+    const double e = double(mt) / double((mt + gm - 1) / gm * gm) * double(clusters / gm * gm) / double(clusters);
+    if (e > most + 0.03) best = gm, most = e;
   }
   return best;
 }
@@ -1185,6 +1202,16 @@ bool launch_tc(const Product& p, cudaStream_t s) {
     a.h0 = d.h0;
     a.l0 = d.l0;
     a.l1 = d.l1;
+  }
+  if (EPI == kEpiLse || EPI == kEpiXent) {
+    const Job& o = a.job[0];
+    a.gm = lse_group(o.mt, g / CG);
+    a.lanes = int(g / CG / a.gm);
+    a.by_nt = make_div(uint32_t(o.nt));
+    const long long positions = (long long)((o.mt + a.gm - 1) / a.gm) * o.nt;
+    if (positions + a.lanes > INT32_MAX) return false;
+    a.positions = int(positions);
+    if (EPI == kEpiLse) p.lse_grid[0] = a.lanes, p.lse_grid[1] = a.gm;
   }
   cfg.gridDim = dim3(unsigned(g));
   constexpr int es = KIND == kBf16 ? 2 : 1;

@@ -4,8 +4,8 @@
 // db = sum of dz.
 //
 // The logits are never kept. The forward is one pass of the product x W^T whose
-// epilogue reduces a tile's columns to a (maximum, sum of exponentials) pair per
-// row (8 bytes for 256 or 128 logits); a second kernel merges a row's pairs.
+// epilogue keeps a (reference, sum of exponentials) pair per row in registers over
+// all of the tiles that a warp has of the row; a second kernel merges a row's pairs.
 // Exponents are in units of log 2: exp(z - m) = 2^(z log2 e - m'), and m' is
 // kept as it was subtracted, so its rounding cancels. The backward takes the
 // catalogue in pieces: the product again, its epilogue writing the piece's dz
@@ -19,23 +19,24 @@ namespace dense {
 namespace {
 
 constexpr int kMaxK = 8192;
-constexpr long long kFwdRows = 32768;       // rows per forward product (its pairs take V / 16 bytes a row)
 constexpr size_t kPieceBytes = 256u << 20;  // dz of a piece
 
 // ---------------------------------------------------------------- small kernels
-// A row's pairs [nt][M] to lse and loss. `rows` (a power of two up to 32)
-// neighbouring rows per block; the other threads share out the tiles.
+// A row's pairs [lanes * kWarpsPerRow][M] to lse and loss: of the lanes that had one
+// of its tiles (dense_tc.cuh). `rows` (a power of two up to 32) neighbouring rows
+// per block; the other threads share out the pairs.
+constexpr int kWarpsPerRow = 4;
 struct MergeArgs {
   const float2* stat;
   const float* zt;
   const long long* target;
   float *loss, *lse;
   long long M;
-  int nt, rows;
+  int lanes, nt, tile_rows, rows;  // tile_rows: of a group of M tiles
   long long V;
   int* status;
 };
-constexpr int kMerge = 512;
+constexpr int kMerge = 256;
 __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ MergeArgs a) {
   __shared__ float2 part[kMerge];
   pdl_go();
@@ -44,18 +45,15 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   const long long row = (long long)blockIdx.x * a.rows + r;
   float m = -kFar, s = 0.f;
   if (row < a.M) {
-    constexpr int U = 8;
-    for (int t0 = slice; t0 < a.nt; t0 += slices * U) {
-      float2 p[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        p[u] = t0 + u * slices < a.nt ? __ldg(a.stat + (long long)(t0 + u * slices) * a.M + row) : make_float2(-kFar, 0.f);
-      float now = m;
-#pragma unroll
-      for (int u = 0; u < U; ++u) now = fmaxf(now, p[u].x);
-      s *= exp2_fast(m - now);
-#pragma unroll
-      for (int u = 0; u < U; ++u) s += p[u].y * exp2_fast(p[u].x - now);
+    const long long group = row / a.tile_rows;
+    const int first = int(group * a.nt % a.lanes);  // the lane of the group's first N tile
+    for (int k = slice; k < a.lanes * kWarpsPerRow; k += slices) {
+      int lane = k / kWarpsPerRow - first;
+      if (lane < 0) lane += a.lanes;
+      if (lane >= a.nt) continue;
+      const float2 p = __ldg(a.stat + (long long)k * a.M + row);
+      const float now = fmaxf(m, p.x);
+      s = s * exp2_fast(m - now) + p.y * exp2_fast(p.x - now);
       m = now;
     }
   }
@@ -120,8 +118,9 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
   const bool lo = laid_out(l->dtype, l->K);
   w.xp = take(lo || backward ? terms * m * w.kp * 2 : 0);
   w.wp = take(lo ? terms * size_t(l->R) * w.kp * 2 : 0);
-  const size_t block = m < size_t(kFwdRows) ? m : size_t(kFwdRows);
-  const size_t stat = block * size_t((l->R + 127) / 128) * 8;
+  // (lanes: as many as clusters; a quarter of those from 32 M tiles on, in any of
+  // lse_group's choices)
+  const size_t stat = (m * (kSms / 4) + (m < 8192 ? m : 8192) * kSms) * kWarpsPerRow * 8;
   // the forward's and the backward's scratch share their room
   size_t o0 = o;
   w.stat = take(stat);
@@ -184,7 +183,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
               float* lse, uint8_t* ws, int* status, cudaStream_t s) {
   const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
   const XLayout w = xent_layout(l, M, false);
-  const int terms = f32 ? 3 : 1, es = esize(l->dtype);
+  const int terms = f32 ? 3 : 1;
   if (lo) {
     const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, l->K, nullptr, 0},
                             {l->W, ws + w.wp, l->ldw, l->R, w.kp, l->K, nullptr, 0}};
@@ -192,29 +191,26 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   }
   float2* stat = reinterpret_cast<float2*>(ws + w.stat);
   float* zt = reinterpret_cast<float*>(ws + w.zt);
-  for (long long r = 0; r < M; r += kFwdRows) {
-    const long long m = M - r < kFwdRows ? M - r : kFwdRows;
-    Product p{};
-    p.A = lo ? Mat{ws + w.xp + r * w.kp * 2, m, l->K, w.kp, terms, M * w.kp}
-             : Mat{static_cast<const uint8_t*>(x) + r * ldx * es, m, l->K, ldx, 1, 0};
-    p.B = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, terms, l->R * w.kp} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
-    p.major = kKK;
-    p.f32 = f32;
-    p.epi = kEpiLse;
-    p.a.job[0].a_term = p.a.job[0].b_term = 1;
-    plan_xent(p, m, l->R, (l->K + 63) / 64);
-    p.a.bias = l->bias;
-    p.a.target = target + r;
-    p.a.stat = stat;
-    p.a.zt = zt + r;
-    p.a.status = status;
-    if (!run_xent_product(p, s)) return false;
-    MergeArgs g{stat, zt + r, target + r, loss + r, lse + r, m, p.a.job[0].nt, 32, l->R, status};
-    while (g.rows > 1 && g.rows / 2 >= m) g.rows /= 2;
-    while (g.rows > 8 && (m + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
-    if (!pdl_launch(merge_kernel, dim3(unsigned((m + g.rows - 1) / g.rows)), kMerge, s, g)) return false;
-  }
-  return true;
+  Product p{};
+  p.A = lo ? Mat{ws + w.xp, M, l->K, w.kp, terms, M * w.kp} : Mat{x, M, l->K, ldx, 1, 0};
+  p.B = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, terms, l->R * w.kp} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
+  p.major = kKK;
+  p.f32 = f32;
+  p.epi = kEpiLse;
+  p.a.job[0].a_term = p.a.job[0].b_term = 1;
+  plan_xent(p, M, l->R, (l->K + 63) / 64);
+  p.a.bias = l->bias;
+  p.a.target = target;
+  p.a.stat = stat;
+  p.a.zt = zt;
+  p.a.status = status;
+  int grid[2] = {};
+  p.lse_grid = grid;
+  if (!run_xent_product(p, s)) return false;
+  MergeArgs g{stat, zt, target, loss, lse, M, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status};
+  while (g.rows > 1 && g.rows / 2 >= M) g.rows /= 2;
+  while (g.rows > 8 && (M + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
+  return pdl_launch(merge_kernel, dim3(unsigned((M + g.rows - 1) / g.rows)), kMerge, s, g);
 }
 
 bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, const float* lse,
