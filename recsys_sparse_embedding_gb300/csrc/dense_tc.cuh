@@ -874,7 +874,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             };
             float more = 0.f;
             if (!fresh) more = total + add(top);
-            if (fresh || __any_sync(0xffffffffu, !(more < 0x1p80f))) {
+            const bool anew = fresh || !(more < 0x1p80f);  // (row by row: a row's bits depend on no other's)
+            if (__any_sync(0xffffffffu, anew)) {
               float m[4];  // (fmaxf leaves a NaN to the sum)
 #pragma unroll
               for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(g[k], g[k + 4]), g[k + 8]);
@@ -884,8 +885,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
                 for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], g[k + e]);
               const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
               const float now = fmaxf(top, fminf(most * kLog2e, kFar));
-              more = total * exp2_fast(top - now) + add(now);
-              top = now;
+              const float again = total * exp2_fast(top - now) + add(now);
+              if (anew) more = again, top = now;
               fresh = false;
             }
             total = more;

@@ -13,6 +13,7 @@
 // the piece, complete, and dx added up over the pieces in fp32 planes. So
 // memory holds M x (a piece), whatever V is, and sums run in a fixed order.
 #include "dense_host.cuh"
+#include "xent_grad.cuh"
 
 namespace dsf {
 namespace dense {
@@ -89,10 +90,30 @@ __global__ void __launch_bounds__(256) rows_kernel(const long long* target, cons
   bool there = t >= 0 && t < V;
   if (!there && t != -1 && status) atomicOr(status, DSF_FLAG_ID_RANGE);
   if (l == -INFINITY) there = false;
-  rows[r] = make_float2(there ? l * kLog2e : 0.f, there ? (dloss ? dloss[r] : 1.f) : 0.f);
+  rows[r] = make_float2(there ? l * kLog2e : kFar, there ? (dloss ? dloss[r] : 1.f) : 0.f);
+}
+
+// db from its four parts
+__global__ void __launch_bounds__(256) db_kernel(const float* part, int V, float* db) {
+  pdl_go();
+  pdl_wait();
+  const int v = blockIdx.x * 256 + threadIdx.x;
+  if (v < V) db[v] = (part[v] + part[V + v]) + (part[2LL * V + v] + part[3LL * V + v]);
 }
 
 // ---------------------------------------------------------------- layout
+// Whether the gradients are taken in one pass each (xent_grad.cuh).
+bool one_pass(const dsf_dense* l, long long M) {
+  return l->dtype == DSF_BF16 && l->K <= 256 && M >= 512 && M <= 65536 && l->R >= 8192;
+}
+// Chunks of the columns in which dx is summed: a few units for each SM, and at
+// most 512 tiles in one.
+constexpr long long kDxUnits = 4 * kSms;
+int dx_chunks(long long M, long long V) {
+  const long long mt = (M + 127) / 128, ct = (V + 127) / 128, least = (ct + 511) / 512, want = (kDxUnits + mt - 1) / mt;
+  return int(want > least ? (want < ct ? want : ct) : least);
+}
+
 // Columns of a piece for M rows.
 long long piece_of(const dsf_dense* l, long long M) {
   const long long terms = l->dtype == DSF_F32 ? 3 : 1, all = up(l->R, 256);
@@ -134,11 +155,13 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
     // (each is at least what any smaller M takes: a piece is at most kPieceBytes of dz, or 256 columns)
     w.rows = take(m * 8);
     w.dz = take(least(2 * terms * m * all, greatest(kPieceBytes, 2 * terms * m * 256)));
-    w.sums = take(least((m + 31) / 32 * all * 4, kPieceBytes / 16 / terms + (m + 31) / 32 * 256 * 4 + all * 4));
+    w.sums = take(greatest(all * 16, least((m + 31) / 32 * all * 4, kPieceBytes / 16 / terms + (m + 31) / 32 * 256 * 4 + all * 4)));
     // planes of dx: the splits of a product, or those of sums of more than 65536 terms
     const size_t outputs = m * K4;
     const size_t planes = greatest(least(outputs * kMaxSplits, kPartBytes), outputs + K4 * (kPieceBytes / 131072 + 1));
-    w.planes = take(planes);
+    // (one_pass: dx_chunks of them, at most kDxUnits / mt + 1 or 16)
+    const size_t mt = (m + 127) / 128, chunks = greatest(128 * K4 * (size_t(kDxUnits) + mt), outputs * 16);
+    w.planes = take(l->dtype == DSF_BF16 && l->K <= 256 ? greatest(planes, chunks) : planes);
     // partial sums of dW's rows of a piece, or, where one piece is all, of dx
     const size_t wide = all * K4;
     w.part = take(greatest(greatest(least(wide * kMaxSplits, kPartBytes), planes),
@@ -240,6 +263,42 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   c.status = status;
   c.s = s;
   c.X = Mat{ws + w.xp, M, K, w.kp, terms, M * w.kp};
+  if (one_pass(l, M)) {
+    c.W = lo ? Mat{ws + w.wp, l->R, K, w.kp, 1, 0} : Mat{l->W, l->R, K, l->ldw, 1, 0};
+    GradArgs g{};
+    g.K = K;
+    g.rows = rows;
+    g.target = target;
+    g.bias = l->bias;
+    g.status = status;
+    const int mt = int((M + 127) / 128), vt = int((l->R + 127) / 128);
+    if (dW || db) {
+      g.R = l->R, g.C = int(M), g.rt = vt, g.ct = mt;
+      g.chunks = 1, g.per = mt;
+      g.out = dW, g.ldo = K;
+      g.db = db ? sums : nullptr;
+      if (!run_xent_grad(true, g, c.W, c.X, s)) return false;
+      if (db && !pdl_launch(db_kernel, dim3(unsigned((l->R + 255) / 256)), 256, s, (const float*)sums, l->R, db)) return false;
+    }
+    if (!dx) return true;
+    const int chunks = dx_chunks(M, l->R);
+    g.R = int(M), g.C = l->R, g.rt = mt, g.ct = vt;
+    g.per = (vt + chunks - 1) / chunks;
+    g.chunks = (vt + g.per - 1) / g.per;
+    g.out = ws + w.planes;
+    g.ldo = up(K, 4);
+    g.plane = M * g.ldo;
+    if (!run_xent_grad(false, g, c.X, c.W, s)) return false;
+    Product sum{};
+    Job& o = sum.a.job[0];
+    o.M = int(M), o.N = K, o.splits = g.chunks, o.ldo = g.ldo;
+    c.w.part = w.planes;
+    FinishArgs f{};
+    f.planes = 1;
+    f.out = dx;
+    f.ldo = lddx;
+    return finish(c, sum, f, false);
+  }
   const long long P = piece_of(l, M);
   const bool one = P >= l->R;
   Product acc{};  // dx over the pieces: the first piece's plan for all of them

@@ -1,0 +1,398 @@
+// The cross entropy's gradients where x and W are narrow (bf16, K <= 256): dx and
+// dW each in one pass that computes the logits again and keeps nothing of them.
+//
+// A block has 128 rows of one matrix (x for dx, W for dW) in shared memory and
+// streams the other's by 128: S = rows times streamed rows on the tensor cores,
+// 16 warps turn S into dz = g (exp(z - lse) - [target]), rounded to bf16, in tensor
+// memory in S's own place, and dz times the streamed rows (the same shared memory,
+// now MN-major) is added to the block's output in tensor memory. dz in memory
+// instead costs 6 bytes a logit (written, read twice): at K = 64 that took 7.9 of a
+// training step's 10.1 ms (8192 rows, 846,812 columns).
+//
+//   load warp   TMA: the block's rows once per unit, then the streamed tiles
+//   MMA warp    S of tile j, then dz of tile j - 1 times its rows
+//   16 epilogue warps in two sets: even tiles and odd ones. A warp has 32 rows (a
+//               tensor-memory quarter) by 64 columns of its tiles.
+//
+// Tensor memory: two S buffers of 128 columns, the output's K columns at 256.
+// Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
+// columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
+#pragma once
+#include "dense_tc.cuh"
+
+namespace dsf {
+namespace dense {
+
+struct GradArgs {
+  int R, C;             // the blocks' rows, the streamed rows
+  int rt, ct;           // tiles of 128 of them
+  int chunks, per;      // chunks of the streamed tiles, tiles in one
+  int K;
+  const float2* rows;        // [M] lse in units of log 2, g
+  const long long* target;   // [M]
+  const float* bias;         // [V], nullable
+  void* out;                 // dW bf16 [R][K]; dx fp32 [chunks][R][ldo]
+  long long ldo, plane;
+  float* db;                 // dW: [4][R] sums of dz (nullable)
+  int* status;
+};
+
+template <int NK>
+struct GradShape {
+  static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kThreads = 32 * 18;
+  static constexpr int TILE = NK * 16384;
+  static constexpr int CONST_BYTES = kWarps * 512;  // per warp: 64 columns' lse and g, or bias
+  static constexpr int kRoom = 227 * 1024 - TILE - CONST_BYTES - 512;
+  static constexpr int STAGES = kRoom / TILE < 8 ? kRoom / TILE : 8;
+  static constexpr int SMEM = (STAGES + 1) * TILE + CONST_BYTES + 512;
+  static_assert(STAGES >= 2 && SMEM > 114 * 1024, "ring; one block per SM");
+};
+
+struct GradBars {
+  uint64_t full[8], empty[8], rows_full, rows_empty, s_full[2], p_full[2], acc_full, acc_empty;
+  uint32_t tmem;
+  int abort_;
+};
+static_assert(sizeof(GradBars) <= 512, "barrier block");
+
+// MN-major operand of 128 K indices per 64 columns (mn_desc's has 64)
+__device__ __forceinline__ uint64_t mn_desc_128(uint32_t addr) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | uint64_t(16384u >> 4) << 16 | uint64_t(1024u >> 4) << 32 |
+         uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+template <bool DW, int NK>
+__global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
+    xent_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap map_rows,
+                     const __grid_constant__ CUtensorMap map_stream) {
+  using S = GradShape<NK>;
+  constexpr int STAGES = S::STAGES;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t* s_rows = sm + STAGES * S::TILE;
+  float* s_const = reinterpret_cast<float*>(s_rows + S::TILE);
+  GradBars* bars = reinterpret_cast<GradBars*>(s_rows + S::TILE + S::CONST_BYTES);
+  if (smem_u32(sm) & 1023u) {  // (the swizzle atoms' alignment; every thread of the grid takes the same way)
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == S::kLoad && lane == 0) {
+    prefetch_map(&map_rows);
+    prefetch_map(&map_stream);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->rows_full, 1);
+    mbar_init(&bars->rows_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 8);
+    }
+    mbar_init(&bars->acc_full, 1);
+    mbar_init(&bars->acc_empty, S::kWarps);
+    bars->abort_ = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  pdl_go();
+  uint32_t tbase = 0;
+  if (warp == S::kMma) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  tbase = bars->tmem;
+  volatile int* aborted = &bars->abort_;
+  pdl_wait();
+
+  // the block's i-th unit: rows [128 r, ...) over the chunk's tiles. Neighbouring
+  // blocks have neighbouring rows of one chunk, so that its tiles come from L2.
+  const int units = a.rt * a.chunks;
+  struct Unit {
+    int r0, c0, n, chunk;  // first row, first streamed tile, tiles
+  };
+  auto unit_at = [&](int i, Unit& t) {
+    const int u = int(blockIdx.x) + i * int(gridDim.x);
+    if (u >= units) return false;
+    t.chunk = u / a.rt;
+    t.r0 = (u - t.chunk * a.rt) * 128;
+    t.c0 = t.chunk * a.per;
+    t.n = min(a.per, a.ct - t.c0);
+    return true;
+  };
+
+  if (warp == S::kLoad) {
+    // ------------------------------------------------ loads (one thread)
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t it = 0;
+      int i = 0;
+      Unit t;
+      for (; ok && unit_at(i, t); ++i) {
+        if (i > 0 && !(ok = mbar_wait(&bars->rows_empty, (i - 1) & 1))) break;
+        mbar_arrive_expect_tx(&bars->rows_full, S::TILE);
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          tma_load_3d<1>(smem_u32(s_rows + k * 16384), &map_rows, k * 64, t.r0, 0, smem_u32(&bars->rows_full));
+        for (int j = 0; j < t.n; ++j, ++it) {
+          const uint32_t st = it % STAGES, lap = it / STAGES;
+          if (lap && !(ok = mbar_wait(&bars->empty[st], (lap - 1) & 1u))) break;
+          mbar_arrive_expect_tx(&bars->full[st], S::TILE);
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+            tma_load_3d<1>(smem_u32(sm + st * S::TILE + k * 16384), &map_stream, k * 64, (t.c0 + j) * 128, 0,
+                           smem_u32(&bars->full[st]));
+        }
+      }
+      if (!ok) atomicExch(&bars->abort_, 1);
+      // the last loads have landed before the block may end (bounded; a unit that
+      // gave up while it waited for the rows' place has counted one too many)
+      if (i > 0 && ok && !mbar_wait(&bars->rows_full, (i - 1) & 1)) atomicExch(&bars->abort_, 1);
+      for (uint32_t j = it > uint32_t(STAGES) ? it - STAGES : 0; j < it; ++j)
+        if (!mbar_wait(&bars->full[j % STAGES], (j / STAGES) & 1u)) atomicExch(&bars->abort_, 1);
+    }
+    __syncwarp();
+  } else if (warp == S::kMma) {
+    // ------------------------------------------------ MMAs (the warp together, one lane issues)
+    const bool lead = elect_one();
+    constexpr uint32_t ID1 = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+    constexpr uint32_t ID2 = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(NK * 64 >> 3) << 17) |
+                             (uint32_t(128 >> 4) << 24);
+    const uint32_t s0 = smem_u32(sm), acc = tbase + 256;
+    const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows));
+    bool ok = true;
+    uint32_t it = 0;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u));
+      tc_fence_after();
+      return ok;
+    };
+    // dz of tile t times its rows; first: of unit i
+    auto second = [&](uint32_t t, bool first, int i) {
+      if (!wait(&bars->p_full[t & 1], t >> 1)) return;
+      if (first && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) return;
+      const uint32_t st = t % STAGES;
+      if (!lead) return;
+      const uint64_t db = mn_desc_128(s0 + st * S::TILE);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k)
+        tc_mma_f16_ts(acc, tbase + (t & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, !first || k > 0);
+      tc_commit(&bars->empty[st]);
+    };
+    Unit t;
+    for (int i = 0; ok && unit_at(i, t); ++i) {
+      if (!wait(&bars->rows_full, uint32_t(i))) break;
+      for (int j = 0; j < t.n && ok; ++j, ++it) {
+        const uint32_t st = it % STAGES;
+        if (!wait(&bars->full[st], it / STAGES)) break;
+        // (S's buffer holds dz of tile it - 2 until that has been multiplied)
+        if (it >= 2 && !wait(&bars->empty[(it - 2) % STAGES], (it - 2) / STAGES)) break;
+        if (lead) {
+          const uint64_t db = sw128_kmajor_desc(s0 + st * S::TILE);
+#pragma unroll
+          for (uint32_t k = 0; k < 4 * NK; ++k)
+            mma<1, kBf16>(tbase + (it & 1) * 128, da + (k >> 2) * 1024 + (k & 3) * 2, db + (k >> 2) * 1024 + (k & 3) * 2, ID1,
+                          k > 0);
+          tc_commit(&bars->s_full[it & 1]);
+        }
+        if (j > 0) second(it - 1, j == 1, i);
+      }
+      if (!ok) break;
+      second(it - 1, t.n == 1, i);
+      if (ok && lead) {
+        tc_commit(&bars->rows_empty);
+        tc_commit(&bars->acc_full);
+      }
+    }
+    if (!ok && lead) atomicExch(&bars->abort_, 1);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
+    const uint32_t lane_base = uint32_t(q * 32) << 16, s_at = tbase + set * 128 + half * 64 + lane_base;
+    float* con = s_const + warp * 128;  // the warp's 64 columns: lse, g; or bias
+    bool ok = true;
+    uint32_t it = 0;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (*aborted) ok = false;
+      if (ok && lane == 0) ok = mbar_wait(bar, phase & 1u);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      tc_fence_after();
+      return ok;
+    };
+    const bool consts = DW || a.bias;
+    // what the warp's next tile takes per column (lane: columns lane and lane + 32)
+    float2 c_row[2] = {};
+    int c_id[2] = {-1, -1};
+    auto prefetch = [&](const Unit& t, int j) {
+      if (!consts || j >= t.n) return;
+      const int col = (t.c0 + j) * 128 + half * 64 + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = col + 32 * h;
+        if (DW) {
+          c_row[h] = c < a.C ? __ldg(a.rows + c) : make_float2(kFar, 0.f);
+          const long long id = c < a.C ? __ldg(a.target + c) : -1;
+          c_id[h] = id >= 0 && id < a.R ? int(id) : -1;
+        } else {
+          c_row[h].x = c < a.C ? __ldg(a.bias + c) : 0.f;
+        }
+      }
+    };
+    Unit t;
+    for (int i = 0; ok && unit_at(i, t); ++i) {
+      const int row = t.r0 + 32 * q + lane;
+      float bias = 0.f, sum = 0.f;
+      float2 mine = make_float2(0.f, 0.f);
+      int tgt = -1;
+      if (row < a.R) {
+        if (DW) {
+          if (a.bias) bias = __ldg(a.bias + row);
+        } else {
+          mine = __ldg(a.rows + row);
+          const long long id = __ldg(a.target + row);
+          tgt = id >= 0 && id < a.C ? int(id) : -1;
+        }
+      }
+      const int j0 = (int(it & 1) ^ set);  // the set's first tile of the unit
+      prefetch(t, j0);
+      for (int j = 0; j < t.n; ++j, ++it) {
+        if (int(it & 1) != set) continue;
+        int id[2] = {c_id[0], c_id[1]};
+        float g_of[2] = {c_row[0].y, c_row[1].y};
+        if (consts) {
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            con[32 * h + lane] = c_row[h].x;
+            if (DW) con[64 + 32 * h + lane] = c_row[h].y;
+          }
+          __syncwarp();
+          prefetch(t, j + 2);
+        }
+        if (!wait(&bars->s_full[set], it >> 1)) break;
+        const int col = (t.c0 + j) * 128 + half * 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float z[32];
+          tmem_ld32(s_at + 32 * h, z);
+          tmem_ld_wait();
+          const float* cl = con + 32 * h;
+          if (DW) {
+            const float2 b2 = pair(bias);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(cl + k), g = *reinterpret_cast<const float4*>(cl + 64 + k);
+              const float2 e0 = __ffma2_rn(make_float2(z[k], z[k + 1]) + b2, pair(kLog2e), make_float2(-l.x, -l.y));
+              const float2 e1 = __ffma2_rn(make_float2(z[k + 2], z[k + 3]) + b2, pair(kLog2e), make_float2(-l.z, -l.w));
+              const float2 p0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y)) * make_float2(g.x, g.y);
+              const float2 p1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y)) * make_float2(g.z, g.w);
+              z[k] = p0.x, z[k + 1] = p0.y, z[k + 2] = p1.x, z[k + 3] = p1.y;
+            }
+            // the columns whose target is one of the warp's rows
+            for (uint32_t hit = __ballot_sync(0xffffffffu, unsigned(id[h] - (row - lane)) < 32u); hit; hit &= hit - 1) {
+              const int l = __ffs(hit) - 1, v = __shfl_sync(0xffffffffu, id[h], l);
+              const float g = __shfl_sync(0xffffffffu, g_of[h], l);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k == l && v == row) z[k] -= g;
+            }
+            if (a.db) {
+              float2 s = pair(0.f);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) s = s + make_float2(z[k], z[k + 1]);
+              sum += s.x + s.y;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float2 z0 = make_float2(z[k], z[k + 1]), z1 = make_float2(z[k + 2], z[k + 3]);
+              if (a.bias) {
+                const float4 b = *reinterpret_cast<const float4*>(cl + k);
+                z0 = z0 + make_float2(b.x, b.y);
+                z1 = z1 + make_float2(b.z, b.w);
+              }
+              const float2 e0 = __ffma2_rn(z0, pair(kLog2e), pair(-mine.x)), e1 = __ffma2_rn(z1, pair(kLog2e), pair(-mine.x));
+              const float2 p0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y)) * pair(mine.y);
+              const float2 p1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y)) * pair(mine.y);
+              z[k] = p0.x, z[k + 1] = p0.y, z[k + 2] = p1.x, z[k + 3] = p1.y;
+            }
+            const int c = col + 32 * h;
+            if (__any_sync(0xffffffffu, unsigned(tgt - c) < 32u)) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (tgt - c == k) z[k] -= mine.y;
+            }
+            if (mine.y == 0.f || c + 32 > a.C) {  // a row left out, whatever it holds; the end of the columns
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (mine.y == 0.f || c + k >= a.C) z[k] = 0.f;
+            }
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
+          tmem_st16(s_at + 16 * h, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[set]);
+      }
+      if (!ok || !wait(&bars->acc_full, uint32_t(i))) break;
+      if (DW && a.db && row < a.R) a.db[(long long)(set * 2 + half) * a.R + row] = sum;
+      // the output's columns, a quarter of them per warp of the rows
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const int c = ((set * 2 + half) * NK + k) * 16;
+        float v[16];
+        tmem_ld16(tbase + 256 + c + lane_base, v);
+        tmem_ld_wait();
+        if (row >= a.R || c >= a.K || !a.out) continue;
+        if (DW) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + c;
+          if (c + 16 <= a.K && a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(o + e) =
+                  make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
+                             pack_bf16x2(v[e + 6], v[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < a.K) o[e] = __float2bfloat16(v[e]);
+          }
+        } else {  // (rows of whole vectors)
+          float* o = static_cast<float*>(a.out) + t.chunk * a.plane + (long long)row * a.ldo + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            if (c + e < a.K) *reinterpret_cast<float4*>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->acc_empty);
+    }
+    if (!ok && lane == 0) atomicExch(&bars->abort_, 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == S::kMma) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+  if (threadIdx.x == 0 && bars->abort_ && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
+}
+
+// dx (DW = false) or dW over `chunks` chunks of the streamed tiles; rows, stream:
+// the matrices, 128-row boxes.
+bool run_xent_grad(bool dw, GradArgs a, const Mat& rows, const Mat& stream, cudaStream_t s);
+
+}  // namespace dense
+}  // namespace dsf

@@ -94,6 +94,47 @@ def test_a_catalogue_in_pieces(dtype, M, K, V):
     check(c, o)
 
 
+@pytest.mark.parametrize("M,K,V", [(512, 64, 8192), (513, 16, 8193), (600, 192, 9000), (1000, 256, 10001), (777, 130, 8500),
+                                   (4097, 100, 20011), (512, 8, 140001), (2000, 33, 30000), (65536, 24, 8200)])
+def test_narrow_rows_in_one_pass(M, K, V):
+    """bf16 of at most 256 columns: dx and dW without dz in memory."""
+    for bias in (True, False):
+        c = case(M + K, BF16, M, K, V, bias)
+        o, status = run(c)
+        assert status == 0
+        check(c, o)
+    c["target"].random_(0, 3)  # every target in three columns, and every row's
+    o, status = run(c)
+    assert status == 0
+    check(c, o)
+    for want in (("dx",), ("dW",), ("db",)):
+        p, _ = run(c, want=want)
+        assert torch.equal(p[want[0]], o[want[0]]), want
+
+
+@pytest.mark.parametrize("K", [48, 256])
+def test_rows_left_out_and_items_taken_out_in_one_pass(K):
+    c = case(15, BF16, 900, K, 9000, out=0.5)
+    gone = torch.rand(9000, generator=gen(16), device="cuda") < 0.3
+    gone[:600] = True
+    c["b"] = torch.where(gone, torch.full_like(c["b"], -INF), c["b"])
+    c["target"] = torch.where(c["target"] < 0, c["target"], torch.nonzero(~gone)[:, 0][c["target"] % int((~gone).sum())])
+    o, status = run(c)
+    assert status == 0
+    check(c, o)
+    bad = dict(c, x=c["x"].clone())
+    bad["x"][c["target"] < 0] = NAN
+    p, _ = run(bad)
+    for k in ("loss", "dx", "dW", "db"):
+        assert torch.equal(o[k], p[k]), k
+    assert (p["dx"][c["target"] < 0] == 0).all() and (p["dW"][gone] == 0).all() and (p["db"][gone] == 0).all()
+    bad["x"][5] = NAN
+    bad["target"][5] = 8000
+    p, _ = run(bad)
+    keep = torch.arange(900, device="cuda") != 5
+    assert torch.equal(o["dx"][keep], p["dx"][keep]) and torch.isnan(p["dx"][5].float()).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_more_rows_than_a_block_of_them(dtype):
     c = case(2, dtype, 70001, 16, 300)
