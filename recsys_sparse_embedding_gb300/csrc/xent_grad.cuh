@@ -10,11 +10,12 @@
 // training step's 10.1 ms (8192 rows, 846,812 columns).
 //
 //   load warp   TMA: the block's rows once per unit, then the streamed tiles
-//   MMA warp    S of tile j, then dz of tile j - 1 times its rows
+//   MMA warp    S of tile j, then dz of tile j - 2 (K above 128: j - 1) times its rows
 //   16 epilogue warps in two sets: even tiles and odd ones. A warp has 32 rows (a
 //               tensor-memory quarter) by 64 columns of its tiles.
 //
-// Tensor memory: two S buffers of 128 columns, the output's K columns at 256.
+// Tensor memory: three S buffers of 128 columns (two where K is above 128), so that a
+// set finds its next tile's S there when it has done one; then the output's columns.
 // Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
 // columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
 #pragma once
@@ -45,11 +46,13 @@ struct GradShape {
   static constexpr int kRoom = 227 * 1024 - TILE - CONST_BYTES - 512;
   static constexpr int STAGES = kRoom / TILE < 8 ? kRoom / TILE : 8;
   static constexpr int SMEM = (STAGES + 1) * TILE + CONST_BYTES + 512;
+  static constexpr int NB = NK <= 2 ? 3 : 2;  // S buffers
+  static_assert(STAGES >= NB && NB * 128 + NK * 64 <= 512, "tiles under way; tensor memory");
   static_assert(STAGES >= 2 && SMEM > 114 * 1024, "ring; one block per SM");
 };
 
 struct GradBars {
-  uint64_t full[8], empty[8], rows_full, rows_empty, s_full[2], p_full[2], acc_full, acc_empty;
+  uint64_t full[8], empty[8], rows_full, rows_empty, s_full[3], p_full[3], acc_full, acc_empty;
   uint32_t tmem;
   int abort_;
 };
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     xent_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap map_rows,
                      const __grid_constant__ CUtensorMap map_stream) {
   using S = GradShape<NK>;
-  constexpr int STAGES = S::STAGES;
+  constexpr int STAGES = S::STAGES, NB = S::NB;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* s_rows = sm + STAGES * S::TILE;
   float* s_const = reinterpret_cast<float*>(s_rows + S::TILE);
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     }
     mbar_init(&bars->rows_full, 1);
     mbar_init(&bars->rows_empty, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 8);
     }
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     constexpr uint32_t ID1 = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     constexpr uint32_t ID2 = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(NK * 64 >> 3) << 17) |
                              (uint32_t(128 >> 4) << 24);
-    const uint32_t s0 = smem_u32(sm), acc = tbase + 256;
+    const uint32_t s0 = smem_u32(sm), acc = tbase + NB * 128;
     const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows));
     bool ok = true;
     uint32_t it = 0;
@@ -174,14 +177,14 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     };
     // dz of tile t times its rows; first: of unit i
     auto second = [&](uint32_t t, bool first, int i) {
-      if (!wait(&bars->p_full[t & 1], t >> 1)) return;
+      if (!wait(&bars->p_full[t % NB], t / NB)) return;
       if (first && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) return;
       const uint32_t st = t % STAGES;
       if (!lead) return;
       const uint64_t db = mn_desc_128(s0 + st * S::TILE);
 #pragma unroll
       for (uint32_t k = 0; k < 8; ++k)
-        tc_mma_f16_ts(acc, tbase + (t & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, !first || k > 0);
+        tc_mma_f16_ts(acc, tbase + (t % NB) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, !first || k > 0);
       tc_commit(&bars->empty[st]);
     };
     Unit t;
@@ -190,20 +193,20 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
       for (int j = 0; j < t.n && ok; ++j, ++it) {
         const uint32_t st = it % STAGES;
         if (!wait(&bars->full[st], it / STAGES)) break;
-        // (S's buffer holds dz of tile it - 2 until that has been multiplied)
-        if (it >= 2 && !wait(&bars->empty[(it - 2) % STAGES], (it - 2) / STAGES)) break;
+        // (S's buffer holds dz of tile it - NB until that has been multiplied)
+        if (it >= NB && !wait(&bars->empty[(it - NB) % STAGES], (it - NB) / STAGES)) break;
         if (lead) {
           const uint64_t db = sw128_kmajor_desc(s0 + st * S::TILE);
 #pragma unroll
           for (uint32_t k = 0; k < 4 * NK; ++k)
-            mma<1, kBf16>(tbase + (it & 1) * 128, da + (k >> 2) * 1024 + (k & 3) * 2, db + (k >> 2) * 1024 + (k & 3) * 2, ID1,
+            mma<1, kBf16>(tbase + (it % NB) * 128, da + (k >> 2) * 1024 + (k & 3) * 2, db + (k >> 2) * 1024 + (k & 3) * 2, ID1,
                           k > 0);
-          tc_commit(&bars->s_full[it & 1]);
+          tc_commit(&bars->s_full[it % NB]);
         }
-        if (j > 0) second(it - 1, j == 1, i);
+        if (j >= NB - 1) second(it - (NB - 1), j == NB - 1, i);
       }
+      for (int j = max(t.n - (NB - 1), 0); ok && j < t.n; ++j) second(it - (t.n - j), j == 0, i);
       if (!ok) break;
-      second(it - 1, t.n == 1, i);
       if (ok && lead) {
         tc_commit(&bars->rows_empty);
         tc_commit(&bars->acc_full);
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
   } else {
     // ------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
-    const uint32_t lane_base = uint32_t(q * 32) << 16, s_at = tbase + set * 128 + half * 64 + lane_base;
+    const uint32_t lane_base = uint32_t(q * 32) << 16, s_col = tbase + half * 64 + lane_base;
     float* con = s_const + warp * 128;  // the warp's 64 columns: lse, g; or bias
     bool ok = true;
     uint32_t it = 0;
@@ -275,13 +278,17 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
           __syncwarp();
           prefetch(t, j + 2);
         }
-        if (!wait(&bars->s_full[set], it >> 1)) break;
+        if (!wait(&bars->s_full[it % NB], it / NB)) break;
+        const uint32_t s_at = s_col + (it % NB) * 128;
         const int col = (t.c0 + j) * 128 + half * 64;
+        float zz[2][32];
+        tmem_ld32(s_at, zz[0]);
+        tmem_ld_wait();
+        tmem_ld32(s_at + 32, zz[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float z[32];
-          tmem_ld32(s_at + 32 * h, z);
-          tmem_ld_wait();
+          float* z = zz[h];
+          if (h) tmem_ld_wait();
           const float* cl = con + 32 * h;
           if (DW) {
             const float2 b2 = pair(bias);
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[set]);
+        if (lane == 0) mbar_arrive(&bars->p_full[it % NB]);
       }
       if (!ok || !wait(&bars->acc_full, uint32_t(i))) break;
       if (DW && a.db && row < a.R) a.db[(long long)(set * 2 + half) * a.R + row] = sum;
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
       for (int k = 0; k < NK; ++k) {
         const int c = ((set * 2 + half) * NK + k) * 16;
         float v[16];
-        tmem_ld16(tbase + 256 + c + lane_base, v);
+        tmem_ld16(tbase + NB * 128 + c + lane_base, v);
         tmem_ld_wait();
         if (row >= a.R || c >= a.K || !a.out) continue;
         if (DW) {
