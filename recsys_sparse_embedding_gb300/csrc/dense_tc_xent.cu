@@ -1,7 +1,7 @@
 // The softmax cross entropy's products: the logits twice (kEpiLse, kEpiXent),
 // and dx added up over the pieces of the catalogue (kEpiAcc).
 #include "dense_tc.cuh"
-#include "xent_grad.cuh"
+#include "xent_pass.cuh"
 
 namespace dsf {
 namespace dense {
@@ -21,15 +21,15 @@ bool run_acc_product(const Product& p, cudaStream_t s) {
   return p.f32 ? launch_cfg<kKN, kBf16, false, kEpiAcc, true>(p, s) : launch_cfg<kKN, kBf16, false, kEpiAcc, false>(p, s);
 }
 
-template <bool DW, int NK>
-bool launch_grad(const GradArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {
-  auto* kernel = xent_grad_kernel<DW, NK>;
+template <int MODE, int NK>
+bool launch_pass(const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {
+  auto* kernel = xent_pass_kernel<MODE, NK>;
   static std::atomic<int> grid_max[64];  // (host threads may race on it: each computes the same value)
   int dev = 0;
   if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return false;
   int most = grid_max[dev].load(std::memory_order_acquire);
   if (most == 0) {
-    if (!succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GradShape<NK>::SMEM)) ||
+    if (!succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PassShape<NK>::SMEM)) ||
         !succeeded(cudaDeviceGetAttribute(&most, cudaDevAttrMultiProcessorCount, dev)) || most < 1)
       return false;
     grid_max[dev].store(most, std::memory_order_release);
@@ -38,18 +38,24 @@ bool launch_grad(const GradArgs& a, const Mat& rows, const Mat& stream, cudaStre
   if (!tensor_map_3d(&mr, rows, 2, 64, 128) || !tensor_map_3d(&ms, stream, 2, 64, 128)) return false;
   const long long units = (long long)a.rt * a.chunks;
   if (units > INT32_MAX / 2) return false;
-  return pdl_launch_smem(kernel, dim3(unsigned(units < most ? units : most)), GradShape<NK>::kThreads, GradShape<NK>::SMEM, s,
+  return pdl_launch_smem(kernel, dim3(unsigned(units < most ? units : most)), PassShape<NK>::kThreads, PassShape<NK>::SMEM, s,
                          a, mr, ms);
 }
 
-bool run_xent_grad(bool dw, GradArgs a, const Mat& rows, const Mat& stream, cudaStream_t s) {
+template <int MODE>
+bool run_pass(const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {
   switch ((a.K + 63) / 64) {
-    case 1: return dw ? launch_grad<true, 1>(a, rows, stream, s) : launch_grad<false, 1>(a, rows, stream, s);
-    case 2: return dw ? launch_grad<true, 2>(a, rows, stream, s) : launch_grad<false, 2>(a, rows, stream, s);
-    case 3: return dw ? launch_grad<true, 3>(a, rows, stream, s) : launch_grad<false, 3>(a, rows, stream, s);
-    case 4: return dw ? launch_grad<true, 4>(a, rows, stream, s) : launch_grad<false, 4>(a, rows, stream, s);
+    case 1: return launch_pass<MODE, 1>(a, rows, stream, s);
+    case 2: return launch_pass<MODE, 2>(a, rows, stream, s);
+    case 3: return launch_pass<MODE, 3>(a, rows, stream, s);
+    case 4: return launch_pass<MODE, 4>(a, rows, stream, s);
   }
   return false;
+}
+
+bool run_xent_pass(int mode, const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {
+  return mode == kSums ? run_pass<kSums>(a, rows, stream, s)
+                       : (mode == kDx ? run_pass<kDx>(a, rows, stream, s) : run_pass<kDw>(a, rows, stream, s));
 }
 
 }  // namespace dense

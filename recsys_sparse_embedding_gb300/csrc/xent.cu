@@ -13,7 +13,7 @@
 // the piece, complete, and dx added up over the pieces in fp32 planes. So
 // memory holds M x (a piece), whatever V is, and sums run in a fixed order.
 #include "dense_host.cuh"
-#include "xent_grad.cuh"
+#include "xent_pass.cuh"
 
 namespace dsf {
 namespace dense {
@@ -77,20 +77,47 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   if (!there && t != -1 && a.status) atomicOr(a.status, DSF_FLAG_ID_RANGE);
 }
 
-// What the backward's product takes per row: lse in units of log 2, and dloss
-// (0: the row is left out; also where no column is possible).
-__global__ void __launch_bounds__(256) rows_kernel(const long long* target, const float* lse, const float* dloss, long long M,
-                                                   long long V, float2* rows, int* status) {
+// What the backward's products take per row: lse in units of log 2 (kFar: the row is
+// left out; also where no column is possible) and dloss; as pairs, or in one array
+// each, with the target, up to a whole tile of 128 rows.
+struct RowsArgs {
+  const long long* target;
+  const float *lse, *dloss;
+  long long M, V;
+  float2* rows;
+  float *l, *g;
+  int *id, *status;
+};
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowsArgs a) {
   pdl_go();
   pdl_wait();
   const long long r = blockIdx.x * 256LL + threadIdx.x;
-  if (r >= M) return;
-  const long long t = target[r];
-  const float l = lse[r];
-  bool there = t >= 0 && t < V;
-  if (!there && t != -1 && status) atomicOr(status, DSF_FLAG_ID_RANGE);
-  if (l == -INFINITY) there = false;
-  rows[r] = make_float2(there ? l * kLog2e : kFar, there ? (dloss ? dloss[r] : 1.f) : 0.f);
+  bool there = false;
+  float l = kFar, g = 0.f;
+  long long t = -1;
+  if (r < a.M) {
+    t = a.target[r];
+    l = a.lse[r];
+    there = t >= 0 && t < a.V;
+    if (!there && t != -1 && a.status) atomicOr(a.status, DSF_FLAG_ID_RANGE);
+    if (l == -INFINITY) there = false;
+    l = there ? l * kLog2e : kFar;
+    g = there ? (a.dloss ? a.dloss[r] : 1.f) : 0.f;
+    if (a.rows) a.rows[r] = make_float2(l, g);
+  }
+  if (a.l && r < (a.M + 127) / 128 * 128) {
+    a.l[r] = l;
+    a.g[r] = g;
+    a.id[r] = there ? int(t) : -1;
+  }
+}
+
+// A bias in whole tiles of 128
+__global__ void __launch_bounds__(256) bias_kernel(const float* bias, int V, float* out) {
+  pdl_go();
+  pdl_wait();
+  const int v = blockIdx.x * 256 + threadIdx.x;
+  if (v < (V + 127) / 128 * 128) out[v] = v < V ? bias[v] : 0.f;
 }
 
 // db from its four parts
@@ -102,12 +129,11 @@ __global__ void __launch_bounds__(256) db_kernel(const float* part, int V, float
 }
 
 // ---------------------------------------------------------------- layout
-// Whether the gradients are taken in one pass each (xent_grad.cuh).
-bool one_pass(const dsf_dense* l, long long M) {
-  return l->dtype == DSF_BF16 && l->K <= 256 && M >= 512 && M <= 65536 && l->R >= 8192;
-}
-// Chunks of the columns in which dx is summed: a few units for each SM, and at
-// most 512 tiles in one.
+// Whether the rows' sums, or the gradients, are taken in one pass each (xent_pass.cuh).
+bool narrow(const dsf_dense* l) { return l->dtype == DSF_BF16 && l->K <= 256 && l->R >= 8192; }
+bool one_pass(const dsf_dense* l, long long M) { return narrow(l) && M >= 512 && M <= 65536; }
+// Chunks of the columns in which the sums and dx are taken: a few units for each SM,
+// and at most 512 tiles in one.
 constexpr long long kDxUnits = 4 * kSms;
 int dx_chunks(long long M, long long V) {
   const long long mt = (M + 127) / 128, ct = (V + 127) / 128, least = (ct + 511) / 512, want = (kDxUnits + mt - 1) / mt;
@@ -122,7 +148,7 @@ long long piece_of(const dsf_dense* l, long long M) {
 }
 
 struct XLayout {
-  size_t xp, wp, stat, zt, rows, dz, sums, part, planes, total;
+  size_t xp, wp, bias, stat, zt, rows, dz, sums, part, planes, total;
   long long kp;
 };
 XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
@@ -141,7 +167,12 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
   w.wp = take(lo ? terms * size_t(l->R) * w.kp * 2 : 0);
   // (lanes: as many as clusters; a quarter of those from 32 M tiles on, in any of
   // lse_group's choices)
-  const size_t stat = (m * (kSms / 4) + (m < 8192 ? m : 8192) * kSms) * kWarpsPerRow * 8;
+  size_t stat = (m * (kSms / 4) + (m < 8192 ? m : 8192) * kSms) * kWarpsPerRow * 8;
+  const bool by_pass = narrow(l);
+  const size_t mt = (m + 127) / 128, pieces = 128 * (size_t(kDxUnits) + mt);  // rows times chunks, at most these or 16 times the rows
+  if (by_pass && stat < (pieces > m * 16 ? pieces : m * 16) * kWarpsPerRow * 8)
+    stat = (pieces > m * 16 ? pieces : m * 16) * kWarpsPerRow * 8;
+  w.bias = take(by_pass && l->bias ? size_t(up(l->R, 128)) * 4 : 0);
   // the forward's and the backward's scratch share their room
   size_t o0 = o;
   w.stat = take(stat);
@@ -153,15 +184,13 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
     auto least = [](size_t a, size_t b) { return a < b ? a : b; };
     auto greatest = [](size_t a, size_t b) { return a > b ? a : b; };
     // (each is at least what any smaller M takes: a piece is at most kPieceBytes of dz, or 256 columns)
-    w.rows = take(m * 8);
+    w.rows = take((m + 128) * 12);
     w.dz = take(least(2 * terms * m * all, greatest(kPieceBytes, 2 * terms * m * 256)));
     w.sums = take(greatest(all * 16, least((m + 31) / 32 * all * 4, kPieceBytes / 16 / terms + (m + 31) / 32 * 256 * 4 + all * 4)));
     // planes of dx: the splits of a product, or those of sums of more than 65536 terms
     const size_t outputs = m * K4;
     const size_t planes = greatest(least(outputs * kMaxSplits, kPartBytes), outputs + K4 * (kPieceBytes / 131072 + 1));
-    // (one_pass: dx_chunks of them, at most kDxUnits / mt + 1 or 16)
-    const size_t mt = (m + 127) / 128, chunks = greatest(128 * K4 * (size_t(kDxUnits) + mt), outputs * 16);
-    w.planes = take(l->dtype == DSF_BF16 && l->K <= 256 ? greatest(planes, chunks) : planes);
+    w.planes = take(by_pass ? greatest(planes, greatest(pieces * K4, outputs * 16)) : planes);  // (dx_chunks of them)
     // partial sums of dW's rows of a piece, or, where one piece is all, of dx
     const size_t wide = all * K4;
     w.part = take(greatest(greatest(least(wide * kMaxSplits, kPartBytes), planes),
@@ -202,6 +231,18 @@ bool together(long long M, long long N, long long K, bool f32) {
   return plan_dual(p, M, N, K, 1) <= plan(q, N, K, 1, (M + 63) / 64, 1, true) + plan(r, M, K, 1, (N + 63) / 64, 1, true);
 }
 
+bool merge(MergeArgs g, cudaStream_t s) {
+  while (g.rows > 1 && g.rows / 2 >= g.M) g.rows /= 2;
+  while (g.rows > 8 && (g.M + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
+  return pdl_launch(merge_kernel, dim3(unsigned((g.M + g.rows - 1) / g.rows)), kMerge, s, g);
+}
+
+// The bias as the passes take it, where there is one
+bool lay_bias(const dsf_dense* l, void* ws, const float** bias, cudaStream_t s) {
+  *bias = l->bias ? static_cast<const float*>(ws) : nullptr;
+  return !l->bias || pdl_launch(bias_kernel, dim3(unsigned((l->R + 127 + 255) / 256)), 256, s, l->bias, l->R, static_cast<float*>(ws));
+}
+
 bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, long long M, float* loss,
               float* lse, uint8_t* ws, int* status, cudaStream_t s) {
   const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
@@ -214,6 +255,25 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   }
   float2* stat = reinterpret_cast<float2*>(ws + w.stat);
   float* zt = reinterpret_cast<float*>(ws + w.zt);
+  if (narrow(l)) {
+    PassArgs a{};
+    const float* bias = nullptr;
+    if (!lay_bias(l, ws + w.bias, &bias, s)) return false;
+    a.R = int(M), a.C = l->R, a.K = l->K;
+    a.rt = int((M + 127) / 128), a.ct = int((l->R + 127) / 128);
+    const int chunks = dx_chunks(M, l->R);
+    a.per = (a.ct + chunks - 1) / chunks;
+    a.chunks = (a.ct + a.per - 1) / a.per;
+    a.col0 = bias;
+    a.target = target;
+    a.stat = stat;
+    a.zt = zt;
+    a.status = status;
+    const Mat X = lo ? Mat{ws + w.xp, M, l->K, w.kp, 1, 0} : Mat{x, M, l->K, ldx, 1, 0},
+              W = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, 1, 0} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
+    return run_xent_pass(kSums, a, X, W, s) &&
+           merge(MergeArgs{stat, zt, target, loss, lse, M, a.chunks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
+  }
   Product p{};
   p.A = lo ? Mat{ws + w.xp, M, l->K, w.kp, terms, M * w.kp} : Mat{x, M, l->K, ldx, 1, 0};
   p.B = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, terms, l->R * w.kp} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
@@ -230,10 +290,8 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   int grid[2] = {};
   p.lse_grid = grid;
   if (!run_xent_product(p, s)) return false;
-  MergeArgs g{stat, zt, target, loss, lse, M, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status};
-  while (g.rows > 1 && g.rows / 2 >= M) g.rows /= 2;
-  while (g.rows > 8 && (M + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
-  return pdl_launch(merge_kernel, dim3(unsigned((M + g.rows - 1) / g.rows)), kMerge, s, g);
+  return merge(MergeArgs{stat, zt, target, loss, lse, M, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status},
+               s);
 }
 
 bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, const float* lse,
@@ -247,9 +305,12 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, K, target, l->R},
                           {l->W, ws + w.wp, l->ldw, l->R, w.kp, K, nullptr, 0}};
   if (!lay(l->dtype, jobs, lo ? 2 : 1, s)) return false;
-  float2* rows = reinterpret_cast<float2*>(ws + w.rows);
-  if (!pdl_launch(rows_kernel, dim3(unsigned((M + 255) / 256)), 256, s, target, lse, dloss, M, (long long)l->R, rows, status))
-    return false;
+  const bool pass = one_pass(l, M);
+  const long long Mp = up(M, 128);
+  float* l_of = reinterpret_cast<float*>(ws + w.rows);
+  float2* rows = pass ? nullptr : reinterpret_cast<float2*>(l_of);
+  RowsArgs ra{target, lse, dloss, M, l->R, rows, pass ? l_of : nullptr, l_of + Mp, reinterpret_cast<int*>(l_of + 2 * Mp), status};
+  if (!pdl_launch(rows_kernel, dim3(unsigned((Mp + 255) / 256)), 256, s, ra)) return false;
   float* sums = reinterpret_cast<float*>(ws + w.sums);
   Ctx c{};
   c.l = l;
@@ -263,32 +324,36 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   c.status = status;
   c.s = s;
   c.X = Mat{ws + w.xp, M, K, w.kp, terms, M * w.kp};
-  if (one_pass(l, M)) {
+  if (pass) {
     c.W = lo ? Mat{ws + w.wp, l->R, K, w.kp, 1, 0} : Mat{l->W, l->R, K, l->ldw, 1, 0};
-    GradArgs g{};
-    g.K = K;
-    g.rows = rows;
-    g.target = target;
-    g.bias = l->bias;
-    g.status = status;
-    const int mt = int((M + 127) / 128), vt = int((l->R + 127) / 128);
+    const int mt = int(Mp / 128), vt = int((l->R + 127) / 128);
     if (dW || db) {
+      PassArgs g{};
+      g.K = K, g.status = status;
       g.R = l->R, g.C = int(M), g.rt = vt, g.ct = mt;
       g.chunks = 1, g.per = mt;
+      g.col0 = ra.l, g.col1 = ra.g, g.col_id = ra.id;
+      g.row0 = l->bias;
       g.out = dW, g.ldo = K;
       g.db = db ? sums : nullptr;
-      if (!run_xent_grad(true, g, c.W, c.X, s)) return false;
+      if (!run_xent_pass(kDw, g, c.W, c.X, s)) return false;
       if (db && !pdl_launch(db_kernel, dim3(unsigned((l->R + 255) / 256)), 256, s, (const float*)sums, l->R, db)) return false;
     }
     if (!dx) return true;
+    PassArgs g{};
+    const float* bias = nullptr;
+    if (!lay_bias(l, ws + w.bias, &bias, s)) return false;
     const int chunks = dx_chunks(M, l->R);
+    g.K = K, g.status = status;
     g.R = int(M), g.C = l->R, g.rt = mt, g.ct = vt;
     g.per = (vt + chunks - 1) / chunks;
     g.chunks = (vt + g.per - 1) / g.per;
+    g.col0 = bias;
+    g.row0 = ra.l, g.row1 = ra.g, g.target = target;
     g.out = ws + w.planes;
     g.ldo = up(K, 4);
     g.plane = M * g.ldo;
-    if (!run_xent_grad(false, g, c.X, c.W, s)) return false;
+    if (!run_xent_pass(kDx, g, c.X, c.W, s)) return false;
     Product sum{};
     Job& o = sum.a.job[0];
     o.M = int(M), o.N = K, o.splits = g.chunks, o.ldo = g.ldo;

@@ -1,15 +1,17 @@
-// The cross entropy's gradients where x and W are narrow (bf16, K <= 256): dx and
-// dW each in one pass that computes the logits again and keeps nothing of them.
+// The cross entropy where x and W are narrow (bf16, K <= 256): the rows' sums, dx and
+// dW in one pass each that computes the logits and keeps nothing of them.
 //
-// A block has 128 rows of one matrix (x for dx, W for dW) in shared memory and
-// streams the other's by 128: S = rows times streamed rows on the tensor cores,
-// 16 warps turn S into dz = g (exp(z - lse) - [target]), rounded to bf16, in tensor
-// memory in S's own place, and dz times the streamed rows (the same shared memory,
-// now MN-major) is added to the block's output in tensor memory. dz in memory
-// instead costs 6 bytes a logit (written, read twice): at K = 64 that took 7.9 of a
-// training step's 10.1 ms (8192 rows, 846,812 columns).
+// A block has 128 rows of one matrix (x for the sums and dx, W for dW) in shared
+// memory and streams the other's by 128: S = rows times streamed rows on the tensor
+// cores. 16 warps add up exp(S - reference) per row (the sums); or they turn S into
+// dz = g (exp(z - lse) - [target]), rounded to bf16, in tensor memory in S's own
+// place, and dz times the streamed rows (the same shared memory, now MN-major) is
+// added to the block's output in tensor memory. dz in memory instead costs 6 bytes
+// a logit (written, read twice): at K = 64 that took 7.9 of a training step's 10.1
+// ms (8192 rows, 846,812 columns).
 //
-//   load warp   TMA: the block's rows once per unit, then the streamed tiles
+//   load warp   TMA: the block's rows once per unit, then the streamed tiles, with
+//               what the epilogue takes per column (bias, or lse, g and target)
 //   MMA warp    S of tile j, then dz of tile j - 2 (K above 128: j - 1) times its rows
 //   16 epilogue warps in two sets: even tiles and odd ones. A warp has 32 rows (a
 //               tensor-memory quarter) by 64 columns of its tiles.
@@ -24,39 +26,47 @@
 namespace dsf {
 namespace dense {
 
-struct GradArgs {
+enum XentMode { kSums = 0, kDx = 1, kDw = 2 };
+
+struct PassArgs {
   int R, C;             // the blocks' rows, the streamed rows
   int rt, ct;           // tiles of 128 of them
   int chunks, per;      // chunks of the streamed tiles, tiles in one
   int K;
-  const float2* rows;        // [M] lse in units of log 2, g
-  const long long* target;   // [M]
-  const float* bias;         // [V], nullable
-  void* out;                 // dW bf16 [R][K]; dx fp32 [chunks][R][ldo]
+  // per streamed row, in whole tiles of 128: kSums, kDx: bias (nullable); kDw: lse in
+  // units of log 2 (kFar where a row is left out or past the end), g, target
+  const float *col0, *col1;
+  const int* col_id;
+  // per row of the block: kDx: lse, g; kDw: bias (nullable)
+  const float *row0, *row1;
+  const long long* target;  // kSums, kDx
+  void* out;            // dW bf16 [R][K] (nullable); dx fp32 [chunks][R][ldo]
   long long ldo, plane;
-  float* db;                 // dW: [4][R] sums of dz (nullable)
+  float* db;            // kDw: [4][R] sums of dz (nullable)
+  float2* stat;         // kSums: [4 chunks][R] (reference, sum)
+  float* zt;            // kSums: [R] the target's logit
   int* status;
 };
 
 template <int NK>
-struct GradShape {
+struct PassShape {
   static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kThreads = 32 * 18;
   static constexpr int TILE = NK * 16384;
-  static constexpr int CONST_BYTES = kWarps * 512;  // per warp: 64 columns' lse and g, or bias
-  static constexpr int kRoom = 227 * 1024 - TILE - CONST_BYTES - 512;
-  static constexpr int STAGES = kRoom / TILE < 8 ? kRoom / TILE : 8;
-  static constexpr int SMEM = (STAGES + 1) * TILE + CONST_BYTES + 512;
+  static constexpr int COLS = 3 * 512;  // a stage's values per column
+  static constexpr int kRoom = 227 * 1024 - TILE - 512;
+  static constexpr int STAGES = kRoom / (TILE + COLS) < 8 ? kRoom / (TILE + COLS) : 8;
+  static constexpr int SMEM = (STAGES + 1) * TILE + STAGES * COLS + 512;
   static constexpr int NB = NK <= 2 ? 3 : 2;  // S buffers
   static_assert(STAGES >= NB && NB * 128 + NK * 64 <= 512, "tiles under way; tensor memory");
   static_assert(STAGES >= 2 && SMEM > 114 * 1024, "ring; one block per SM");
 };
 
-struct GradBars {
+struct PassBars {
   uint64_t full[8], empty[8], rows_full, rows_empty, s_full[3], p_full[3], acc_full, acc_empty;
   uint32_t tmem;
   int abort_;
 };
-static_assert(sizeof(GradBars) <= 512, "barrier block");
+static_assert(sizeof(PassBars) <= 512, "barrier block");
 
 // MN-major operand of 128 K indices per 64 columns (mn_desc's has 64)
 __device__ __forceinline__ uint64_t mn_desc_128(uint32_t addr) {
@@ -64,16 +74,17 @@ __device__ __forceinline__ uint64_t mn_desc_128(uint32_t addr) {
          uint64_t(1) << 46 | uint64_t(2) << 61;
 }
 
-template <bool DW, int NK>
-__global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
-    xent_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap map_rows,
+template <int MODE, int NK>
+__global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
+    xent_pass_kernel(const __grid_constant__ PassArgs a, const __grid_constant__ CUtensorMap map_rows,
                      const __grid_constant__ CUtensorMap map_stream) {
-  using S = GradShape<NK>;
-  constexpr int STAGES = S::STAGES, NB = S::NB;
+  using S = PassShape<NK>;
+  constexpr int STAGES = S::STAGES, NB = S::NB, COLS = S::COLS;
+  constexpr bool DW = MODE == kDw;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* s_rows = sm + STAGES * S::TILE;
-  float* s_const = reinterpret_cast<float*>(s_rows + S::TILE);
-  GradBars* bars = reinterpret_cast<GradBars*>(s_rows + S::TILE + S::CONST_BYTES);
+  uint8_t* s_cols = s_rows + S::TILE;
+  PassBars* bars = reinterpret_cast<PassBars*>(s_cols + STAGES * COLS);
   if (smem_u32(sm) & 1023u) {  // (the swizzle atoms' alignment; every thread of the grid takes the same way)
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
     return;
@@ -145,7 +156,13 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
         for (int j = 0; j < t.n; ++j, ++it) {
           const uint32_t st = it % STAGES, lap = it / STAGES;
           if (lap && !(ok = mbar_wait(&bars->empty[st], (lap - 1) & 1u))) break;
-          mbar_arrive_expect_tx(&bars->full[st], S::TILE);
+          mbar_arrive_expect_tx(&bars->full[st], S::TILE + (DW ? 3 * 512 : (a.col0 ? 512 : 0)));
+          const long long at = (long long)(t.c0 + j) * 128;
+          if (DW || a.col0) bulk_g2s(s_cols + st * COLS, a.col0 + at, 512, &bars->full[st]);
+          if (DW) {
+            bulk_g2s(s_cols + st * COLS + 512, a.col1 + at, 512, &bars->full[st]);
+            bulk_g2s(s_cols + st * COLS + 1024, a.col_id + at, 512, &bars->full[st]);
+          }
 #pragma unroll
           for (int k = 0; k < NK; ++k)
             tma_load_3d<1>(smem_u32(sm + st * S::TILE + k * 16384), &map_stream, k * 64, (t.c0 + j) * 128, 0,
@@ -178,12 +195,12 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     // dz of tile t times its rows; first: of unit i
     auto second = [&](uint32_t t, bool first, int i) {
       if (!wait(&bars->p_full[t % NB], t / NB)) return;
-      if (first && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) return;
+      if (MODE != kSums && first && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) return;
       const uint32_t st = t % STAGES;
       if (!lead) return;
       const uint64_t db = mn_desc_128(s0 + st * S::TILE);
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k)
+      for (uint32_t k = 0; MODE != kSums && k < 8; ++k)
         tc_mma_f16_ts(acc, tbase + (t % NB) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, !first || k > 0);
       tc_commit(&bars->empty[st]);
     };
@@ -218,138 +235,151 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
     // ------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
     const uint32_t lane_base = uint32_t(q * 32) << 16, s_col = tbase + half * 64 + lane_base;
-    float* con = s_const + warp * 128;  // the warp's 64 columns: lse, g; or bias
     bool ok = true;
     uint32_t it = 0;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-      if (*aborted) ok = false;
-      if (ok && lane == 0) ok = mbar_wait(bar, phase & 1u);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1u)))
+        ok = __all_sync(0xffffffffu, !*aborted && mbar_wait(bar, phase & 1u));
       tc_fence_after();
       return ok;
     };
-    const bool consts = DW || a.bias;
-    // what the warp's next tile takes per column (lane: columns lane and lane + 32)
-    float2 c_row[2] = {};
-    int c_id[2] = {-1, -1};
-    auto prefetch = [&](const Unit& t, int j) {
-      if (!consts || j >= t.n) return;
-      const int col = (t.c0 + j) * 128 + half * 64 + lane;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = col + 32 * h;
-        if (DW) {
-          c_row[h] = c < a.C ? __ldg(a.rows + c) : make_float2(kFar, 0.f);
-          const long long id = c < a.C ? __ldg(a.target + c) : -1;
-          c_id[h] = id >= 0 && id < a.R ? int(id) : -1;
-        } else {
-          c_row[h].x = c < a.C ? __ldg(a.bias + c) : 0.f;
-        }
-      }
-    };
     Unit t;
     for (int i = 0; ok && unit_at(i, t); ++i) {
-      const int row = t.r0 + 32 * q + lane;
-      float bias = 0.f, sum = 0.f;
-      float2 mine = make_float2(0.f, 0.f);
+      const int row0 = t.r0 + 32 * q, row = row0 + lane;
+      const bool some = row0 < a.R;  // whether the warp's rows are there
+      float bias = 0.f, sum = 0.f, lse = 0.f, g = 0.f, top = -kFar;
+      bool fresh = true;
       int tgt = -1;
       if (row < a.R) {
         if (DW) {
-          if (a.bias) bias = __ldg(a.bias + row);
+          if (a.row0) bias = __ldg(a.row0 + row);
         } else {
-          mine = __ldg(a.rows + row);
           const long long id = __ldg(a.target + row);
           tgt = id >= 0 && id < a.C ? int(id) : -1;
+          if (MODE == kDx) lse = __ldg(a.row0 + row), g = __ldg(a.row1 + row);
         }
       }
-      const int j0 = (int(it & 1) ^ set);  // the set's first tile of the unit
-      prefetch(t, j0);
       for (int j = 0; j < t.n; ++j, ++it) {
         if (int(it & 1) != set) continue;
-        int id[2] = {c_id[0], c_id[1]};
-        float g_of[2] = {c_row[0].y, c_row[1].y};
-        if (consts) {
-          __syncwarp();
+        const uint32_t st = it % STAGES, b = it % NB;
+        if (!wait(&bars->full[st], it / STAGES) || !wait(&bars->s_full[b], it / NB)) break;
+        const uint32_t s_at = s_col + b * 128;
+        const int c0 = (t.c0 + j) * 128 + half * 64;
+        if (some) {
+          float zz[2][32];
+          tmem_ld32(s_at, zz[0]);
+          tmem_ld_wait();
+          tmem_ld32(s_at + 32, zz[1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            con[32 * h + lane] = c_row[h].x;
-            if (DW) con[64 + 32 * h + lane] = c_row[h].y;
-          }
-          __syncwarp();
-          prefetch(t, j + 2);
-        }
-        if (!wait(&bars->s_full[it % NB], it / NB)) break;
-        const uint32_t s_at = s_col + (it % NB) * 128;
-        const int col = (t.c0 + j) * 128 + half * 64;
-        float zz[2][32];
-        tmem_ld32(s_at, zz[0]);
-        tmem_ld_wait();
-        tmem_ld32(s_at + 32, zz[1]);
+            float* z = zz[h];
+            if (h) tmem_ld_wait();
+            const float* cl = reinterpret_cast<const float*>(s_cols + st * COLS) + half * 64 + 32 * h;
+            const int c = c0 + 32 * h;
+            if (DW) {
+              const float2 b2 = pair(bias);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float* z = zz[h];
-          if (h) tmem_ld_wait();
-          const float* cl = con + 32 * h;
-          if (DW) {
-            const float2 b2 = pair(bias);
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(cl + k), g = *reinterpret_cast<const float4*>(cl + 64 + k);
-              const float2 e0 = __ffma2_rn(make_float2(z[k], z[k + 1]) + b2, pair(kLog2e), make_float2(-l.x, -l.y));
-              const float2 e1 = __ffma2_rn(make_float2(z[k + 2], z[k + 3]) + b2, pair(kLog2e), make_float2(-l.z, -l.w));
-              const float2 p0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y)) * make_float2(g.x, g.y);
-              const float2 p1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y)) * make_float2(g.z, g.w);
-              z[k] = p0.x, z[k + 1] = p0.y, z[k + 2] = p1.x, z[k + 3] = p1.y;
-            }
-            // the columns whose target is one of the warp's rows
-            for (uint32_t hit = __ballot_sync(0xffffffffu, unsigned(id[h] - (row - lane)) < 32u); hit; hit &= hit - 1) {
-              const int l = __ffs(hit) - 1, v = __shfl_sync(0xffffffffu, id[h], l);
-              const float g = __shfl_sync(0xffffffffu, g_of[h], l);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k == l && v == row) z[k] -= g;
-            }
-            if (a.db) {
-              float2 s = pair(0.f);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) s = s + make_float2(z[k], z[k + 1]);
-              sum += s.x + s.y;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              float2 z0 = make_float2(z[k], z[k + 1]), z1 = make_float2(z[k + 2], z[k + 3]);
-              if (a.bias) {
-                const float4 b = *reinterpret_cast<const float4*>(cl + k);
-                z0 = z0 + make_float2(b.x, b.y);
-                z1 = z1 + make_float2(b.z, b.w);
+              for (int k = 0; k < 32; k += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(cl + k), gg = *reinterpret_cast<const float4*>(cl + 128 + k);
+                const float2 e0 = __ffma2_rn(make_float2(z[k], z[k + 1]) + b2, pair(kLog2e), make_float2(-l.x, -l.y));
+                const float2 e1 = __ffma2_rn(make_float2(z[k + 2], z[k + 3]) + b2, pair(kLog2e), make_float2(-l.z, -l.w));
+                const float2 p0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y)) * make_float2(gg.x, gg.y);
+                const float2 p1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y)) * make_float2(gg.z, gg.w);
+                z[k] = p0.x, z[k + 1] = p0.y, z[k + 2] = p1.x, z[k + 3] = p1.y;
               }
-              const float2 e0 = __ffma2_rn(z0, pair(kLog2e), pair(-mine.x)), e1 = __ffma2_rn(z1, pair(kLog2e), pair(-mine.x));
-              const float2 p0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y)) * pair(mine.y);
-              const float2 p1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y)) * pair(mine.y);
-              z[k] = p0.x, z[k + 1] = p0.y, z[k + 2] = p1.x, z[k + 3] = p1.y;
-            }
-            const int c = col + 32 * h;
-            if (__any_sync(0xffffffffu, unsigned(tgt - c) < 32u)) {
+              // the columns whose target is one of the warp's rows
+              const int id = reinterpret_cast<const int*>(cl)[256 + lane];
+              for (uint32_t hit = __ballot_sync(0xffffffffu, unsigned(id - row0) < 32u); hit; hit &= hit - 1) {
+                const int l = __ffs(hit) - 1, v = __shfl_sync(0xffffffffu, id, l);
+                const float gl = cl[128 + l];
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (tgt - c == k) z[k] -= mine.y;
-            }
-            if (mine.y == 0.f || c + 32 > a.C) {  // a row left out, whatever it holds; the end of the columns
+                for (int k = 0; k < 32; ++k)
+                  if (k == l && v == row) z[k] -= gl;
+              }
+              if (a.db) {
+                float2 s2 = pair(0.f);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (mine.y == 0.f || c + k >= a.C) z[k] = 0.f;
+                for (int k = 0; k < 32; k += 2) s2 = s2 + make_float2(z[k], z[k + 1]);
+                sum += s2.x + s2.y;
+              }
+            } else {
+              if (a.col0)
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(cl + k);
+                const float2 z0 = make_float2(z[k], z[k + 1]) + make_float2(f.x, f.y),
+                             z1 = make_float2(z[k + 2], z[k + 3]) + make_float2(f.z, f.w);
+                z[k] = z0.x, z[k + 1] = z0.y, z[k + 2] = z1.x, z[k + 3] = z1.y;
+              }
+              if (c + 32 > a.C) {  // the end of the columns
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (c + k >= a.C) z[k] = -INFINITY;
+              }
+              const bool target_here = __any_sync(0xffffffffu, unsigned(tgt - c) < 32u);
+              if (MODE == kSums) {
+                if (target_here) {
+                  float zt = 0.f;
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (tgt - c == k) zt = z[k];
+                  if (unsigned(tgt - c) < 32u) a.zt[row] = zt;
+                }
+                // (as in dense_tc.cuh: any reference that keeps the sum in range)
+                auto add = [&](float ref) {
+                  float2 s2[2] = {pair(0.f), pair(0.f)};
+#pragma unroll
+                  for (int k = 0; k < 32; k += 4)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      const float2 x =
+                          __ffma2_rn(make_float2(z[k + 2 * e], z[k + 2 * e + 1]), pair(kLog2e), pair(-ref));
+                      s2[e] = s2[e] + make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                    }
+                  return (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                };
+                float more = 0.f;
+                if (!fresh) more = sum + add(top);
+                const bool anew = fresh || !(more < 0x1p80f);
+                if (__any_sync(0xffffffffu, anew)) {
+                  float most = z[0];  // (fmaxf leaves a NaN to the sum)
+#pragma unroll
+                  for (int k = 1; k < 32; ++k) most = fmaxf(most, z[k]);
+                  const float now = fmaxf(top, fminf(most * kLog2e, kFar)), again = sum * exp2_fast(top - now) + add(now);
+                  if (anew) more = again, top = now;
+                  fresh = false;
+                }
+                sum = more;
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  const float2 e = __ffma2_rn(make_float2(z[k], z[k + 1]), pair(kLog2e), pair(-lse));
+                  const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y)) * pair(g);
+                  z[k] = p.x, z[k + 1] = p.y;
+                }
+                if (target_here) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (tgt - c == k) z[k] -= g;
+                }
+              }
+            }
+            if (MODE != kSums) {
+              uint32_t p[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) p[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
+              tmem_st16(s_at + 16 * h, p);
             }
           }
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) p[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
-          tmem_st16(s_at + 16 * h, p);
+          if (MODE != kSums) tmem_st_wait();
         }
-        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[it % NB]);
+        if (lane == 0) mbar_arrive(&bars->p_full[b]);
+      }
+      if (MODE == kSums) {
+        if (ok && row < a.R) a.stat[((long long)t.chunk * 4 + set * 2 + half) * a.R + row] = make_float2(top, sum);
+        continue;
       }
       if (!ok || !wait(&bars->acc_full, uint32_t(i))) break;
       if (DW && a.db && row < a.R) a.db[(long long)(set * 2 + half) * a.R + row] = sum;
@@ -376,6 +406,10 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
           }
         } else {  // (rows of whole vectors)
           float* o = static_cast<float*>(a.out) + t.chunk * a.plane + (long long)row * a.ldo + c;
+          if (g == 0.f) {  // (a row left out, whatever W holds)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          }
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
             if (c + e < a.K) *reinterpret_cast<float4*>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -397,9 +431,8 @@ __global__ void __launch_bounds__(GradShape<NK>::kThreads, 1)
   if (threadIdx.x == 0 && bars->abort_ && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
 }
 
-// dx (DW = false) or dW over `chunks` chunks of the streamed tiles; rows, stream:
-// the matrices, 128-row boxes.
-bool run_xent_grad(bool dw, GradArgs a, const Mat& rows, const Mat& stream, cudaStream_t s);
+// One of XentMode's passes over `chunks` chunks of the streamed tiles.
+bool run_xent_pass(int mode, const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace dsf
