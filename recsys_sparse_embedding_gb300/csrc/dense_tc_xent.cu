@@ -44,13 +44,7 @@ bool launch_pass(const PassArgs& a, const Mat& rows, const Mat& stream, cudaStre
 
 template <int MODE>
 bool run_pass(const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {
-  switch ((a.K + 63) / 64) {
-    case 1: return launch_pass<MODE, 1>(a, rows, stream, s);
-    case 2: return launch_pass<MODE, 2>(a, rows, stream, s);
-    case 3: return launch_pass<MODE, 3>(a, rows, stream, s);
-    case 4: return launch_pass<MODE, 4>(a, rows, stream, s);
-  }
-  return false;
+  return a.K <= 64 ? launch_pass<MODE, 1>(a, rows, stream, s) : launch_pass<MODE, 2>(a, rows, stream, s);
 }
 
 bool run_xent_pass(int mode, const PassArgs& a, const Mat& rows, const Mat& stream, cudaStream_t s) {

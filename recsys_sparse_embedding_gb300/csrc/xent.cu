@@ -23,7 +23,7 @@ constexpr int kMaxK = 8192;
 constexpr size_t kPieceBytes = 256u << 20;  // dz of a piece
 
 // ---------------------------------------------------------------- small kernels
-// A row's pairs [lanes * kWarpsPerRow][M] to lse and loss: of the lanes that had one
+// A row's pairs [lanes * parts][M] to lse and loss: of the lanes that had one
 // of its tiles (dense_tc.cuh). `rows` (a power of two up to 32) neighbouring rows
 // per block; the other threads share out the pairs.
 constexpr int kWarpsPerRow = 4;
@@ -33,7 +33,7 @@ struct MergeArgs {
   const long long* target;
   float *loss, *lse;
   long long M;
-  int lanes, nt, tile_rows, rows;  // tile_rows: of a group of M tiles
+  int parts, lanes, nt, tile_rows, rows;  // tile_rows: of a group of M tiles
   long long V;
   int* status;
 };
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   if (row < a.M) {
     const long long group = row / a.tile_rows;
     const int first = int(group * a.nt % a.lanes);  // the lane of the group's first N tile
-    for (int k = slice; k < a.lanes * kWarpsPerRow; k += slices) {
-      int lane = k / kWarpsPerRow - first;
+    for (int k = slice; k < a.lanes * a.parts; k += slices) {
+      int lane = k / a.parts - first;
       if (lane < 0) lane += a.lanes;
       if (lane >= a.nt) continue;
       const float2 p = __ldg(a.stat + (long long)k * a.M + row);
@@ -75,6 +75,94 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   a.lse[row] = lse;
   a.loss[row] = there ? lse - a.zt[row] : 0.f;
   if (!there && t != -1 && a.status) atomicOr(a.status, DSF_FLAG_ID_RANGE);
+}
+
+// The sums of up to MT rows from W's rows as they lie in memory, on the CUDA cores: a
+// tensor-core tile would use MT of its 128 rows. The catalogue's bytes are what counts
+// (one row, 846,812 x 64 bf16: 26 us with the merge; by tiles 44). 2^log_g lanes side by side have one row of
+// W (a 16-byte vector each), a warp 32 / 2^log_g rows, and U of those in flight; each
+// lane keeps the reference and sum of its rows (alike in the lanes of a row).
+struct FewArgs {
+  const void *x, *W;
+  long long ldx, ldw;
+  const float* bias;
+  const long long* target;
+  float2* stat;  // [blocks][M]
+  float* zt;
+  int M, V, nv, log_g;  // nv: vectors of a row
+};
+constexpr int kFewBlocks = 4 * kSms;
+template <class T, int MT>
+__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int E = 16 / int(sizeof(T)), U = 4;
+  __shared__ float2 part[8][MT];
+  pdl_go();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = 1 << a.log_g, at = lane & (g - 1);
+  const bool live = at < a.nv;
+  float x[MT][E];
+  int tgt[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int r = min(m, a.M - 1);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (live) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + r * a.ldx) + at);
+    unpack(v, x[m], T());
+    const long long id = __ldg(a.target + r);
+    tgt[m] = m < a.M && id >= 0 && id < a.V ? int(id) : -1;
+  }
+  float top[MT], sum[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) top[m] = -kFar, sum[m] = 0.f;
+  const int per = 32 >> a.log_g;  // W's rows of a warp and step
+  const long long step = (long long)gridDim.x * 8 * per;
+  for (long long v0 = ((long long)blockIdx.x * 8 + warp) * per + (lane >> a.log_g); v0 - (lane >> a.log_g) < a.V; v0 += U * step) {
+    uint4 w[U];
+    float b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long v = v0 + u * step;
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (live && v < a.V) w[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.W) + v * a.ldw) + at);
+      b[u] = v < a.V ? (a.bias ? __ldg(a.bias + v) : 0.f) : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long v = v0 + u * step;
+      float wf[E];
+      unpack(w[u], wf, T());
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float z = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) z = fmaf(x[m][e], wf[e], z);
+        for (int o = g / 2; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        z += b[u];
+        if (v == tgt[m] && at == 0) a.zt[m] = z;
+        const float zl = z * kLog2e, now = fmaxf(top[m], fminf(zl, kFar));
+        sum[m] = sum[m] * exp2_fast(top[m] - now) + exp2_fast(zl - now);
+        top[m] = now;
+      }
+    }
+  }
+  // over the warp's rows of W, the block's warps
+  auto both = [](float2 p, float2 q) {
+    const float now = fmaxf(p.x, q.x);
+    return make_float2(now, p.y * exp2_fast(p.x - now) + q.y * exp2_fast(q.x - now));
+  };
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float2 p = make_float2(top[m], sum[m]);
+    for (int o = g; o < 32; o <<= 1)
+      p = both(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o), __shfl_xor_sync(0xffffffffu, p.y, o)));
+    if (lane == 0) part[warp][m] = p;
+  }
+  __syncthreads();
+  if (threadIdx.x < unsigned(a.M)) {
+    float2 p = part[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) p = both(p, part[k][threadIdx.x]);
+    a.stat[(long long)blockIdx.x * a.M + threadIdx.x] = p;
+  }
 }
 
 // What the backward's products take per row: lse in units of log 2 (kFar: the row is
@@ -130,8 +218,16 @@ __global__ void __launch_bounds__(256) db_kernel(const float* part, int V, float
 
 // ---------------------------------------------------------------- layout
 // Whether the rows' sums, or the gradients, are taken in one pass each (xent_pass.cuh).
-bool narrow(const dsf_dense* l) { return l->dtype == DSF_BF16 && l->K <= 256 && l->R >= 8192; }
-bool one_pass(const dsf_dense* l, long long M) { return narrow(l) && M >= 512 && M <= 65536; }
+// (Both ways, us: the sums of 1024 rows over 100,000 columns of 64 42 and 45, of 512 33
+// and 29, of 8192 over 8192 34 and 39; the gradients 116 and 138, 85 and 80, 110 and 85.)
+bool narrow(const dsf_dense* l, long long M) {
+  return l->dtype == DSF_BF16 && l->K <= 128 && M <= 65536 && double(M) * l->R >= 1e8;
+}
+// Whether the sums are few_kernel's: of up to 4 rows, whole vectors, at most 32 of them.
+bool few(const dsf_dense* l, long long M) {
+  const int bytes = l->K * esize(l->dtype);
+  return M <= 4 && bytes % 16 == 0 && bytes <= 512;
+}
 // Chunks of the columns in which the sums and dx are taken: a few units for each SM,
 // and at most 512 tiles in one.
 constexpr long long kDxUnits = 4 * kSms;
@@ -168,7 +264,7 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
   // (lanes: as many as clusters; a quarter of those from 32 M tiles on, in any of
   // lse_group's choices)
   size_t stat = (m * (kSms / 4) + (m < 8192 ? m : 8192) * kSms) * kWarpsPerRow * 8;
-  const bool by_pass = narrow(l);
+  const bool by_pass = l->dtype == DSF_BF16 && l->K <= 128;  // (for some number of rows)
   const size_t mt = (m + 127) / 128, pieces = 128 * (size_t(kDxUnits) + mt);  // rows times chunks, at most these or 16 times the rows
   if (by_pass && stat < (pieces > m * 16 ? pieces : m * 16) * kWarpsPerRow * 8)
     stat = (pieces > m * 16 ? pieces : m * 16) * kWarpsPerRow * 8;
@@ -248,14 +344,25 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   const bool f32 = l->dtype == DSF_F32, lo = laid_out(l->dtype, l->K);
   const XLayout w = xent_layout(l, M, false);
   const int terms = f32 ? 3 : 1;
-  if (lo) {
+  if (lo && !few(l, M)) {
     const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, l->K, nullptr, 0},
                             {l->W, ws + w.wp, l->ldw, l->R, w.kp, l->K, nullptr, 0}};
     if (!lay(l->dtype, jobs, 2, s)) return false;
   }
   float2* stat = reinterpret_cast<float2*>(ws + w.stat);
   float* zt = reinterpret_cast<float*>(ws + w.zt);
-  if (narrow(l)) {
+  if (few(l, M)) {
+    FewArgs a{x, l->W, ldx, l->ldw, l->bias, target, stat, zt, int(M), l->R, l->K * esize(l->dtype) / 16, 0};
+    while ((1 << a.log_g) < a.nv) ++a.log_g;
+    const long long steps = ((long long)l->R * (1 << a.log_g) + 255) / 256;  // (a block's rows of W in a step)
+    const int blocks = int(steps < kFewBlocks ? steps : kFewBlocks);
+    const bool ok = f32 ? (M == 1 ? pdl_launch(few_kernel<float, 1>, dim3(unsigned(blocks)), 256, s, a)
+                                  : pdl_launch(few_kernel<float, 4>, dim3(unsigned(blocks)), 256, s, a))
+                        : (M == 1 ? pdl_launch(few_kernel<__nv_bfloat16, 1>, dim3(unsigned(blocks)), 256, s, a)
+                                  : pdl_launch(few_kernel<__nv_bfloat16, 4>, dim3(unsigned(blocks)), 256, s, a));
+    return ok && merge(MergeArgs{stat, zt, target, loss, lse, M, 1, blocks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
+  }
+  if (narrow(l, M)) {
     PassArgs a{};
     const float* bias = nullptr;
     if (!lay_bias(l, ws + w.bias, &bias, s)) return false;
@@ -272,7 +379,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
     const Mat X = lo ? Mat{ws + w.xp, M, l->K, w.kp, 1, 0} : Mat{x, M, l->K, ldx, 1, 0},
               W = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, 1, 0} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
     return run_xent_pass(kSums, a, X, W, s) &&
-           merge(MergeArgs{stat, zt, target, loss, lse, M, a.chunks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
+           merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow, a.chunks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
   }
   Product p{};
   p.A = lo ? Mat{ws + w.xp, M, l->K, w.kp, terms, M * w.kp} : Mat{x, M, l->K, ldx, 1, 0};
@@ -290,7 +397,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   int grid[2] = {};
   p.lse_grid = grid;
   if (!run_xent_product(p, s)) return false;
-  return merge(MergeArgs{stat, zt, target, loss, lse, M, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status},
+  return merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status},
                s);
 }
 
@@ -305,7 +412,7 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, K, target, l->R},
                           {l->W, ws + w.wp, l->ldw, l->R, w.kp, K, nullptr, 0}};
   if (!lay(l->dtype, jobs, lo ? 2 : 1, s)) return false;
-  const bool pass = one_pass(l, M);
+  const bool pass = narrow(l, M);
   const long long Mp = up(M, 128);
   float* l_of = reinterpret_cast<float*>(ws + w.rows);
   float2* rows = pass ? nullptr : reinterpret_cast<float2*>(l_of);

@@ -1,4 +1,4 @@
-// The cross entropy where x and W are narrow (bf16, K <= 256): the rows' sums, dx and
+// The cross entropy where x and W are narrow (bf16, K <= 128): the rows' sums, dx and
 // dW in one pass each that computes the logits and keeps nothing of them.
 //
 // A block has 128 rows of one matrix (x for the sums and dx, W for dW) in shared
@@ -12,12 +12,18 @@
 //
 //   load warp   TMA: the block's rows once per unit, then the streamed tiles, with
 //               what the epilogue takes per column (bias, or lse, g and target)
-//   MMA warp    S of tile j, then dz of tile j - 2 (K above 128: j - 1) times its rows
+//   MMA warp    S of tile j, then dz of tile j - 2 times its rows
 //   16 epilogue warps in two sets: even tiles and odd ones. A warp has 32 rows (a
 //               tensor-memory quarter) by 64 columns of its tiles.
 //
-// Tensor memory: three S buffers of 128 columns (two where K is above 128), so that a
-// set finds its next tile's S there when it has done one; then the output's columns.
+// Tensor memory: three S buffers of 128 columns, so that a set finds its next tile's
+// S there when it has done one; then the output's columns. What binds (8192 rows and
+// 131,072 columns of 64; the backward's passes 415 us each, the sums' 320): the
+// epilogue and the second product, whose operand comes from tensor memory, take turns
+// there. Without the second product a tile takes 0.67 us, with it 0.96; dz in buffers
+// of its own (0.98), 24 epilogue warps (0.95), and the exponentials (none: 0.94)
+// change little. From K = 192 on dz in memory is as fast (1.5 ms against 1.6 for both
+// gradients at 192, 1.6 against 1.9 at 256).
 // Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
 // columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
 #pragma once
@@ -56,7 +62,7 @@ struct PassShape {
   static constexpr int kRoom = 227 * 1024 - TILE - 512;
   static constexpr int STAGES = kRoom / (TILE + COLS) < 8 ? kRoom / (TILE + COLS) : 8;
   static constexpr int SMEM = (STAGES + 1) * TILE + STAGES * COLS + 512;
-  static constexpr int NB = NK <= 2 ? 3 : 2;  // S buffers
+  static constexpr int NB = 3;  // S buffers
   static_assert(STAGES >= NB && NB * 128 + NK * 64 <= 512, "tiles under way; tensor memory");
   static_assert(STAGES >= 2 && SMEM > 114 * 1024, "ring; one block per SM");
 };

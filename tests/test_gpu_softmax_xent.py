@@ -68,7 +68,7 @@ def check(c, o, ones=False, norm=True):
             assert e <= NORM[F32 if k == "db" else c["x"].dtype] * n, k
 
 
-SIZES = [(1, 1, 1), (1, 64, 1000), (2, 16, 2), (3, 48, 5), (8, 176, 300), (9, 64, 129), (40, 16, 257), (64, 1024, 3001),
+SIZES = [(1, 1, 1), (1, 8, 5), (3, 256, 70000), (4, 16, 9001), (2, 128, 1), (4, 72, 130), (5, 64, 9001), (1, 64, 1000), (2, 16, 2), (3, 48, 5), (8, 176, 300), (9, 64, 129), (40, 16, 257), (64, 1024, 3001),
          (127, 8, 33), (128, 64, 128), (129, 100, 1031), (257, 37, 4099), (300, 256, 2000), (513, 520, 777),
          (1000, 64, 12961), (2049, 48, 513), (100, 2050, 300), (31, 200, 40001)]
 
@@ -94,10 +94,10 @@ def test_a_catalogue_in_pieces(dtype, M, K, V):
     check(c, o)
 
 
-@pytest.mark.parametrize("M,K,V", [(512, 64, 8192), (513, 16, 8193), (600, 192, 9000), (1000, 256, 10001), (777, 130, 8500),
-                                   (4097, 100, 20011), (512, 8, 140001), (2000, 33, 30000), (65536, 24, 8200)])
+@pytest.mark.parametrize("M,K,V", [(1024, 64, 98304), (513, 16, 200001), (4097, 100, 25011), (120, 8, 840001),
+                                   (2000, 33, 60000), (65536, 24, 1600), (9000, 128, 12007)])
 def test_narrow_rows_in_one_pass(M, K, V):
-    """bf16 of at most 256 columns: dx and dW without dz in memory."""
+    """bf16 of at most 128 columns, 10^8 logits: dx and dW without dz in memory."""
     for bias in (True, False):
         c = case(M + K, BF16, M, K, V, bias)
         o, status = run(c)
@@ -112,10 +112,10 @@ def test_narrow_rows_in_one_pass(M, K, V):
         assert torch.equal(p[want[0]], o[want[0]]), want
 
 
-@pytest.mark.parametrize("K", [48, 256])
+@pytest.mark.parametrize("K", [48, 128])
 def test_rows_left_out_and_items_taken_out_in_one_pass(K):
-    c = case(15, BF16, 900, K, 9000, out=0.5)
-    gone = torch.rand(9000, generator=gen(16), device="cuda") < 0.3
+    c = case(15, BF16, 900, K, 120000, out=0.5)
+    gone = torch.rand(120000, generator=gen(16), device="cuda") < 0.3
     gone[:600] = True
     c["b"] = torch.where(gone, torch.full_like(c["b"], -INF), c["b"])
     c["target"] = torch.where(c["target"] < 0, c["target"], torch.nonzero(~gone)[:, 0][c["target"] % int((~gone).sum())])
