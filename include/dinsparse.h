@@ -538,7 +538,7 @@ int ctr_rms_norm_bwd(const void* dy_dev, int64_t lddy, int32_t dy_dtype, const v
  * Every pointer is aligned to its element; rows of a multiple of four elements
  * whose vectors of four are aligned are faster. Outputs overlap no input and
  * no other output. The workspace (256-byte aligned,
- * dsf_gated_scan_workspace_bytes, which grows with T and B) needs no
+ * dsf_gated_scan_workspace_bytes, which grows with T) needs no
  * initialisation and holds nothing from one call to the next. Equal calls give
  * equal bits; the order of sums depends on the rows' place in the call. A
  * non-finite value stays in its sequence. DSF_FLAG_TIMEOUT in *status_dev
@@ -602,7 +602,8 @@ int ctr_softmax_xent_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx,
  * and grad_dev have row strides and types of their own (DSF_F32 or DSF_BF16;
  * a bf16 W is rounded to nearest even); momentum_dev is fp32 [R, C], contiguous.
  * W and momentum are updated in place; they overlap neither each other nor
- * grad. X and the products are fp32 (as the dense layer's DSF_F32). R, C <=
+ * grad. X and the products are fp32 (as the dense layer's DSF_F32), for a bf16 W
+ * to 17 bits (X is then 5e-5 off). R, C <=
  * 2^20, the smaller one <= 2^15; 0 <= mu < 1, weight_decay >= 0, 1 <= steps <=
  * 16. The sum of u^2 is fp32 and has to be finite there; a gradient of zeros
  * with no momentum leaves X zero, a non-finite one reaches all of W. Every

@@ -60,9 +60,10 @@ constexpr size_t kPartBytes = size_t(kSms / 2) * 256 * 256 * 4;
 // launch and its partial sums' way to L2 and back.
 struct Cost {
   bool f32;
+  double products = 1;  // of a K-block (operands in two terms: three)
   double block(int cfg) const {
     constexpr double kBlock[2][4] = {{0.31, 0.29, 0.275, 0.23}, {0.9, 0.95, 0.75, 0}};
-    return kBlock[f32][cfg];
+    return products * kBlock[f32][cfg];
   }
   double tail(int cfg) const {
     constexpr double kTail[2][4] = {{4.4, 2.2, 1.2, 2.6}, {3.0, 3.0, 2.0, 0}};
@@ -116,7 +117,7 @@ constexpr long long kDzBlocks = 8;
 
 // Picks the configuration and the K-splits of one product; its time by the model.
 double plan(Product& p, long long M, long long N, int nb, long long nkb, int nseg, bool may_split) {
-  const Cost cost{p.f32};
+  const Cost cost{p.f32, p.two ? 3.0 : 1.0};
   double best = 1e300;
   Job o = p.a.job[0];
   const bool runs = p.epi == kEpiDz && !p.f32 && nkb > (p.a.part ? kDzBlocks : kLongRun);

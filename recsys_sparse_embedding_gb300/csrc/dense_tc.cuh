@@ -27,7 +27,9 @@
 // significant bits of what is left. x y is the sum of the terms' products;
 // those below 2^-21 of it (x2 y3, x3 y2, x3 y3) are dropped. A K-block's three
 // terms of A and of B are loaded once and multiplied six ways: x1 y1 into one
-// accumulator, the five smaller products into another.
+// accumulator, the five smaller products into another. TWO: the same with two terms,
+// each rounded to nearest (x to 2^-17), and the three products x1 y1, x1 y2, x2 y1 in
+// one accumulator: half the work, for results that are not kept in fp32.
 //
 // Runs. The tensor cores truncate each addition to an accumulator towards zero.
 // Measured, a sum of n additions (K / 16) is low by 0.5 n 2^-25 of itself where
@@ -329,7 +331,7 @@ __device__ __forceinline__ int slot(int r, int at) {
 
 
 // ---------------------------------------------------------------- the kernel
-template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
+template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32, bool TWO>
 __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThreads, 1)
     tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mapA,
               const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapA1,
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   using TO = typename S::TO;
   constexpr bool DUAL = MAJOR == kDual, BMN = MAJOR != kKK;
   constexpr int kBK = KIND == kBf16 ? 64 : 128;  // K elements per block (128 bytes)
-  constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : 1, RUN = S::RUN;
+  constexpr int ON = S::ON, CW = 32, STAGES = S::STAGES, TERMS = F32 ? 3 : (TWO ? 2 : 1), RUN = S::RUN;
   static_assert(!(GATED && BMN), "a gated layer's product is K-major");
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sE = sm + STAGES * S::STAGE;
@@ -541,6 +543,11 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             uint32_t x, y, z;
             if (!take(x)) break;
             block(d, x, x, k > 0);
+            if (TWO) {
+              if (!take(y)) break;
+              block(d, x, y, true);
+              block(d, y, x, true);
+            }
             if (F32) {
               if (!take(y)) break;
               block(d + BN, x, y, k > 0);
@@ -552,10 +559,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             }
             if (!lead) continue;
             mma_commit<CG>(&bars->empty[x]);
-            if (F32) {
-              mma_commit<CG>(&bars->empty[y]);
-              mma_commit<CG>(&bars->empty[z]);
-            }
+            if (F32 || TWO) mma_commit<CG>(&bars->empty[y]);
+            if (F32) mma_commit<CG>(&bars->empty[z]);
           }
           if (ok && lead) mma_commit<CG>(&bars->tfull[acc]);
           left -= len;
@@ -1090,7 +1095,7 @@ struct Product {
   TcArgs a;
   Mat A, B, A1, B1;  // kDual: job 1's
   int major;
-  bool gated, f32;  // f32: fp32 operands (in terms)
+  bool gated, f32, two;  // f32: fp32 operands (in three terms); two: in two terms
   int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64, 3 (bf16 dz in runs): CG 2 x BN 128
   long long weight[2];  // kDual: a unit's time, by job
   int* lse_grid;        // kEpiLse: where the launch writes the lanes and the M tiles of a group
@@ -1105,6 +1110,7 @@ bool run_grad_product(const Product& p, cudaStream_t s);  // MN-major operands
 bool run_dual_product(const Product& p, cudaStream_t s);
 bool run_xent_product(const Product& p, cudaStream_t s);  // kEpiLse, kEpiXent: configurations 0 and 1
 bool run_acc_product(const Product& p, cudaStream_t s);   // kEpiAcc, B MN-major
+bool run_two_product(const Product& p, cudaStream_t s);   // operands in two terms: kEpiPart, any one Major
 
 // How two products' units go to C clusters: the longer units dealt round (to
 // the first `rest` clusters h0, to the others h0 - 1), the others so that
@@ -1149,10 +1155,10 @@ inline int lse_group(long long mt, long long clusters) {
   return best;
 }
 
-template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32>
+template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32, bool TWO = false>
 bool launch_tc(const Product& p, cudaStream_t s) {
   using S = Shape<CG, BN, MAJOR, GATED, EPI, F32>;
-  auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32>;
+  auto* kernel = tc_kernel<CG, BN, MAJOR, KIND, GATED, EPI, F32, TWO>;
   static std::atomic<int> grid_max[64];  // (host threads may race on it: each computes the same value)
   int dev = 0;
   if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return false;

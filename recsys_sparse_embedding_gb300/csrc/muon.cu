@@ -6,11 +6,15 @@
 // all of (0, 1] near 1, so X ends near the closest orthogonal matrix. (A = X^T X
 // on the right where C < R: the products are on the shorter side, n.)
 //
-// A small singular value grows by a = 3.44 a step, 485 times in five, and what
-// the products round with it. So X, A and the polynomial are fp32, taken as
-// three bf16 terms each, and the products (2 n^2 m, 2 n^3 and 2 n^2 m operations)
-// are the six-term products of dense_tc.cuh: 15 of them, each with fp32 partial
-// sums that a second kernel adds up and lays out as the next operand's terms.
+// A small singular value grows by a = 3.44 a step, 485 times in five, and with it
+// what the products round. Where W is fp32, X, A and the polynomial are fp32 taken as
+// three bf16 terms each (six products of terms; X ends 1e-6 to 1e-5 off, as in fp32
+// throughout). A bf16 W is rounded to 2^-9 in the end: two terms (2^-17, three
+// products) leave X 2.5e-5 to 5e-5 off, which W's rounding hides at half the work.
+// (One bf16 product would leave 1 to 3% of X, one fp16 0.2 to 0.3%.)
+//
+// A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations) each leave fp32
+// partial sums that a second kernel adds up and lays out as the next operand's terms.
 #include "dense_host.cuh"
 
 namespace dsf {
@@ -53,9 +57,17 @@ __device__ __forceinline__ void put4(T* p, int n, bool vec, const float* v) {
   for (int k = 0; k < 4; ++k)
     if (k < n) put(p + k, v[k]);
 }
-// the three bf16 terms of four values (columns past the matrix: zeros)
-__device__ __forceinline__ void put_terms(__nv_bfloat16* p, long long plane, const float* v) {
+// the three bf16 terms of four values, or the two nearest
+__device__ __forceinline__ void put_terms(__nv_bfloat16* p, long long plane, const float* v, bool two) {
   float x[4] = {v[0], v[1], v[2], v[3]};
+  if (two) {
+    uint2 h = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p) = h;
+    const float l[4] = {x[0] - __uint_as_float(h.x << 16), x[1] - __uint_as_float(h.x & 0xffff0000u),
+                        x[2] - __uint_as_float(h.y << 16), x[3] - __uint_as_float(h.y & 0xffff0000u)};
+    *reinterpret_cast<uint2*>(p + plane) = make_uint2(pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3]));
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
     uint32_t h[2];
@@ -121,6 +133,7 @@ struct ScaleArgs {
   __nv_bfloat16* x;
   long long ldu, ldx, plane;
   int R, n4, blocks;
+  bool two;
 };
 __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ ScaleArgs a) {
   __shared__ float part[8];
@@ -135,7 +148,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Scal
     const int c = int(i - r * a.n4) * 4;
     const float4 u = *reinterpret_cast<const float4*>(a.u + r * a.ldu + c);
     const float v[4] = {u.x / d, u.y / d, u.z / d, u.w / d};
-    put_terms(a.x + r * a.ldx + c, a.plane, v);
+    put_terms(a.x + r * a.ldx + c, a.plane, v, a.two);
   }
 }
 
@@ -153,7 +166,7 @@ struct JoinArgs {
   long long ldt, tplane;
   void* W;
   long long ldw;
-  bool w_vec;
+  bool w_vec, two;
   float decay, rate;
 };
 template <int MODE, class TW>
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k >= n) v[k] = 0.f;
-    put_terms(a.terms + r * a.ldt + c, a.tplane, v);
+    put_terms(a.terms + r * a.ldt + c, a.tplane, v, a.two);
   }
 }
 
@@ -231,11 +244,12 @@ unsigned blocks_for(long long items) {
 }
 
 // The product's partial sums to w.part.
-bool part_product(Product& p, int major, const Mat& A, const Mat& B, long long M, long long N, long long K, uint8_t* ws,
-                  const MuonLayout& w, int* status, cudaStream_t s) {
+bool part_product(Product& p, bool two, int major, const Mat& A, const Mat& B, long long M, long long N, long long K,
+                  uint8_t* ws, const MuonLayout& w, int* status, cudaStream_t s) {
   p = Product{};
   p.major = major;
-  p.f32 = true;
+  p.f32 = !two;
+  p.two = two;
   p.epi = kEpiOut;
   plan(p, M, N, 1, (K + 63) / 64, 1, true);
   p.epi = kEpiPart;
@@ -248,7 +262,7 @@ bool part_product(Product& p, int major, const Mat& A, const Mat& B, long long M
   o.ldo = up(N, 4);
   o.out_plane = M * o.ldo;
   o.out_vec = 1;
-  return major == kKK ? run_fwd_product(p, s) : run_grad_product(p, s);
+  return two ? run_two_product(p, s) : (major == kKK ? run_fwd_product(p, s) : run_grad_product(p, s));
 }
 
 template <int MODE, class TW>
@@ -261,6 +275,7 @@ bool join(const Product& p, JoinArgs j, uint8_t* ws, const MuonLayout& w, cudaSt
   j.M = o.M;
   j.N = o.N;
   j.n4 = int(o.ldo / 4);
+  j.two = p.two;
   return pdl_launch(join_kernel<MODE, TW>, dim3(blocks_for((long long)j.M * j.n4)), 256, s, j);
 }
 
@@ -280,6 +295,7 @@ struct Step {
 bool muon(const Step& q, long long R, long long C, uint8_t* ws, int* status, cudaStream_t s) {
   const MuonLayout w = muon_layout(R, C);
   const int n4 = int(up(C, 4) / 4);
+  const bool two = q.w_dtype == DSF_BF16;
   const long long items = R * n4;
   float* u = reinterpret_cast<float*>(ws + w.u);
   float* squares = reinterpret_cast<float*>(ws + w.squares);
@@ -291,12 +307,13 @@ bool muon(const Step& q, long long R, long long C, uint8_t* ws, int* status, cud
     return false;
   __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(ws + w.x);
   if (!pdl_launch(scale_kernel, dim3(blocks_for(items)), 256, s,
-                  ScaleArgs{u, squares, x, w.ldx, w.ldx, R * w.ldx, int(R), n4, int(norm_blocks)}))
+                  ScaleArgs{u, squares, x, w.ldx, w.ldx, R * w.ldx, int(R), n4, int(norm_blocks), two}))
     return false;
   const long long n = w.n;
   const bool wide = R <= C;
-  const Mat X{x, R, C, w.ldx, 3, R * w.ldx}, A{ws + w.a_terms, n, n, w.lda, 3, n * w.lda},
-      B{ws + w.b_terms, n, n, w.lda, 3, n * w.lda};
+  const long long terms = two ? 2 : 3;
+  const Mat X{x, R, C, w.ldx, terms, R * w.ldx}, A{ws + w.a_terms, n, n, w.lda, terms, n * w.lda},
+      B{ws + w.b_terms, n, n, w.lda, terms, n * w.lda};
   float* a32 = reinterpret_cast<float*>(ws + w.a);
   Product p;
   for (int i = 0; i < q.steps; ++i) {
@@ -305,12 +322,12 @@ bool muon(const Step& q, long long R, long long C, uint8_t* ws, int* status, cud
     j.ldt = w.lda;
     j.tplane = n * w.lda;
     j.terms = reinterpret_cast<__nv_bfloat16*>(ws + w.a_terms);
-    if (!part_product(p, wide ? kKK : kNN, X, X, n, n, wide ? C : R, ws, w, status, s) || !join<kSum, float>(p, j, ws, w, s))
+    if (!part_product(p, two, wide ? kKK : kNN, X, X, n, n, wide ? C : R, ws, w, status, s) || !join<kSum, float>(p, j, ws, w, s))
       return false;
     j.terms = reinterpret_cast<__nv_bfloat16*>(ws + w.b_terms);
-    if (!part_product(p, kKK, A, A, n, n, n, ws, w, status, s) || !join<kPoly, float>(p, j, ws, w, s)) return false;
-    const bool ok = wide ? part_product(p, kKN, B, X, R, C, n, ws, w, status, s)
-                         : part_product(p, kKK, X, B, R, C, n, ws, w, status, s);
+    if (!part_product(p, two, kKK, A, A, n, n, n, ws, w, status, s) || !join<kPoly, float>(p, j, ws, w, s)) return false;
+    const bool ok = wide ? part_product(p, two, kKN, B, X, R, C, n, ws, w, status, s)
+                         : part_product(p, two, kKK, X, B, R, C, n, ws, w, status, s);
     if (!ok) return false;
     JoinArgs f{};
     if (i + 1 < q.steps) {

@@ -100,7 +100,7 @@ def test_long_sequences_over_many_groups_of_chunks(dtype, D, lengths):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("nb,L,D", [(1, 1, 64), (512, 1, 256), (7, 1, 33), (3, 64, 64), (5, 100, 48), (2, 5000, 64), (300, 8, 20)])
+@pytest.mark.parametrize("nb,L,D", [(1, 1, 64), (512, 1, 256), (7, 1, 33), (1000, 1, 2), (3, 1, 1001), (3, 64, 64), (5, 100, 48), (2, 5000, 64), (300, 8, 20)])
 def test_equal_lengths(dtype, nb, L, D):
     v = inputs(nb + L, dtype, nb * L, D, nb)
     o, status = run(v, None, nb, equal=True)
