@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libdinsparse.so")
 
 UNITS = ["abi.cu", "bag.cu", "fwd_attn_tc.cu", "fwd_attn_f32.cu", "towers.cu", "hash.cu", "bwd.cu", "gemm.cu", "dense.cu", "dense_tc_fwd.cu",
          "dense_tc_dz.cu", "dense_tc_grad.cu", "dense_tc_dual.cu", "dense_tc_e4m3.cu", "norm.cu",
-         "gated_scan.cu", "dense_tc_xent.cu", "dense_tc_two.cu", "xent.cu",
+         "gated_scan.cu", "dense_tc_xent.cu", "dense_tc_two.cu", "dense_tc_terms.cu", "xent.cu",
          "muon.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

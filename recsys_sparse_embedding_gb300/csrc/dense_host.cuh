@@ -109,6 +109,14 @@ long long least_splits(bool f32, long long blocks) {
   return f32 || n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits);
 }
 
+// The same of a product of operands in two terms, which is to be exact to 2^-15 or so:
+// at most 128 K-blocks (three additions each) in one run.
+constexpr long long kTwoRun = 128;
+long long least_splits_two(long long blocks) {
+  const long long n = (blocks + kTwoRun - 1) / kTwoRun;
+  return n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits);
+}
+
 // K-blocks in one accumulator run of a bf16 dz product that db is summed from.
 // With more, its wide tiles are half as wide (configuration 3), so that the
 // epilogue's registers hold a tile's sums. (Without db, dz is rounded to bf16,
@@ -121,7 +129,8 @@ double plan(Product& p, long long M, long long N, int nb, long long nkb, int nse
   double best = 1e300;
   Job o = p.a.job[0];
   const bool runs = p.epi == kEpiDz && !p.f32 && nkb > (p.a.part ? kDzBlocks : kLongRun);
-  const long long least = may_split ? least_splits(p.f32, nkb * nseg) : 1;
+  const long long least =
+      !may_split ? 1 : (p.two ? least_splits_two(nkb * nseg) : least_splits(p.f32, nkb * nseg));
   for (int cfg = 0; cfg < 4; ++cfg) {
     if (cfg == 2 && p.gated) continue;
     if (cfg % 3 == 0 && (cfg == 3) != runs) continue;

@@ -81,6 +81,9 @@ enum Epi {
   kEpiOut = 2,   // out = the accumulator
   kEpiPart = 3,  // fp32 partial sums of a K-split: plane split * planes + (half or batch); kDual: job 0 only
   kEpiAcc = 5,   // the same, added to what the planes hold
+  // operands of the next product (TWO: in two terms, else in three):
+  kEpiTerms = 8,  // out = the accumulator's terms; in fp32 too where f32 is given
+  kEpiPoly = 9,   // out = the terms of c0 [row = column] + c1 in + c2 times the accumulator
   // softmax cross entropy over the columns (z in units of log 2 where it is an
   // exponent; the target's column per row):
   kEpiLse = 6,   // per row a reference and the sum of exp(z - it), over the tiles that a warp has of the row; z of the target
@@ -127,7 +130,7 @@ struct TcArgs {
   int first, rest, h0, l0, l1;
   int act;
   const float *bias, *xs, *ws;  // z = acc * xs[m] * ws[n] + bias[n] (each nullable; the up half at n + N)
-  const void* in;               // kEpiRes, kEpiDz
+  const void* in;               // kEpiRes, kEpiDz, kEpiAcc, kEpiPoly
   long long ldi;
   int in_vec;   // rows at 16-byte boundaries
   float* part;  // kEpiDz, kEpiXent: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
@@ -141,6 +144,8 @@ struct TcArgs {
   Div by_nt;
   float* zt;                // kEpiLse: [M]
   const float2* rows;       // kEpiXent: [M] (lse, g)
+  float* f32;               // kEpiTerms: rows of ldo elements (nullable)
+  float c0, c1, c2;         // kEpiPoly
   int* status;
 };
 
@@ -244,7 +249,8 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 // ---------------------------------------------------------------- shapes
 template <int CG, int BN, int MAJOR, bool GATED, int EPI, bool F32>
 struct Shape {
-  using TO = typename std::conditional<F32 || EPI == kEpiPart || EPI == kEpiAcc, float, __nv_bfloat16>::type;  // input and output
+  using TO = typename std::conditional<F32 || EPI == kEpiPart || EPI == kEpiAcc || EPI == kEpiTerms || EPI == kEpiPoly, float,
+                                       __nv_bfloat16>::type;  // input and output
   static constexpr int ON = GATED ? BN / 2 : BN;  // output columns per tile
   // Epilogue warps: four per lane quarter (scheduler). Two where the kernel
   // needs the registers (168 instead of 96 a thread: a gated dz, whose items
@@ -576,10 +582,11 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     uint8_t* buf = sE + warp * S::ITEM;
     float* wbias = sBias + warp * S::BIAS_N;
     const uint32_t lane_base = uint32_t(q * 32) << 16;
-    constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz || EPI == kEpiAcc;
+    constexpr bool FWD = EPI == kEpiFwd || EPI == kEpiRes, IN = EPI == kEpiRes || EPI == kEpiDz || EPI == kEpiAcc || EPI == kEpiPoly;
     constexpr bool XENT = EPI == kEpiLse || EPI == kEpiXent;
     constexpr bool SCALED = KIND == kE4m3 && FWD;
-    constexpr bool TERMS_OUT = F32 && (EPI == kEpiDz || EPI == kEpiXent);  // dz leaves as three bf16 terms
+    // the item leaves as three (TWO: two) bf16 terms
+    constexpr bool TERMS_OUT = (F32 && (EPI == kEpiDz || EPI == kEpiXent)) || EPI == kEpiTerms || EPI == kEpiPoly;
     constexpr bool PAIR = GATED && EPI != kEpiPart;   // an item takes gate and up accumulators
     constexpr int GR = S::kGroups, ROWB = CW * int(sizeof(TO));
     constexpr int halves = GATED ? 2 : 1;
@@ -946,6 +953,9 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
               if (EPI == kEpiAcc) v[k] += x[k], v[k + 1] += x[k + 1];
+              if (EPI == kEpiPoly)
+#pragma unroll
+                for (int e = k; e < k + 2; ++e) v[e] = fmaf(a.c2, v[e], a.c1 * x[e]) + (row == col0 + j + e ? a.c0 : 0.f);
               if (!S::BIAS || XENT) continue;
               const float2 b2 = make_float2(b[k], b[k + 1]);
               float2 z = make_float2(v[k], v[k + 1]);
@@ -997,13 +1007,24 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
             float* v = h ? up : g;
             if (a.part) sums(v, h);
             __syncwarp();  // (the input is read, or the last term gone, before the buffer is written)
+            if (EPI == kEpiTerms && a.f32) {
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
+              for (int j = 0; j < 32; j += 8) put8(j, v + j);
+              store_item(jb, a.f32, row0, col0);
+            }
+#pragma unroll
+            for (int term = 0; term < (TWO ? 2 : 3); ++term) {
 #pragma unroll
               for (int j = 0; j < 32; j += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                  if (TWO) {
+                    float* e = v + j + 2 * k;
+                    w[k] = pack_bf16x2(e[0], e[1]);
+                    e[0] -= __uint_as_float(w[k] << 16), e[1] -= __uint_as_float(w[k] & 0xffff0000u);
+                    continue;
+                  }
                   const uint32_t lo = take_term(v[j + 2 * k]), hi = take_term(v[j + 2 * k + 1]);
                   w[k] = __byte_perm(lo, hi, 0x7632);
                 }
@@ -1111,6 +1132,7 @@ bool run_dual_product(const Product& p, cudaStream_t s);
 bool run_xent_product(const Product& p, cudaStream_t s);  // kEpiLse, kEpiXent: configurations 0 and 1
 bool run_acc_product(const Product& p, cudaStream_t s);   // kEpiAcc, B MN-major
 bool run_two_product(const Product& p, cudaStream_t s);   // operands in two terms: kEpiPart, any one Major
+bool run_terms_product(const Product& p, cudaStream_t s);  // kEpiTerms, kEpiPoly (K-major): operands in two or three terms
 
 // How two products' units go to C clusters: the longer units dealt round (to
 // the first `rest` clusters h0, to the others h0 - 1), the others so that

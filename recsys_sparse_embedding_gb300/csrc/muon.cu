@@ -13,8 +13,9 @@
 // products) leave X 2.5e-5 to 5e-5 off, which W's rounding hides at half the work.
 // (One bf16 product would leave 1 to 3% of X, one fp16 0.2 to 0.3%.)
 //
-// A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations) each leave fp32
-// partial sums that a second kernel adds up and lays out as the next operand's terms.
+// A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations) leave the next
+// operand's terms in their epilogues; where a product is better split over K, it
+// leaves fp32 partial sums that a second kernel adds up and lays out.
 #include "dense_host.cuh"
 
 namespace dsf {
@@ -161,7 +162,8 @@ struct JoinArgs {
   const float* part;
   long long ldp, plane;
   int splits, M, N, n4;
-  float* f32;  // [M][ldp]
+  float* f32;  // [M][ld32]
+  long long ld32;
   __nv_bfloat16* terms;
   long long ldt, tplane;
   void* W;
@@ -194,12 +196,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
       continue;
     }
     if (MODE == kPoly) {
-      const float4 f = *reinterpret_cast<const float4*>(a.f32 + r * a.ldp + c);
+      const float4 f = *reinterpret_cast<const float4*>(a.f32 + r * a.ld32 + c);
       const float A[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = fmaf(kC, v[k], kB * A[k]) + (r == c + k ? kA : 0.f);
     } else if (a.f32) {
-      *reinterpret_cast<float4*>(a.f32 + r * a.ldp + c) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(a.f32 + r * a.ld32 + c) = make_float4(v[0], v[1], v[2], v[3]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
 }
 
 struct MuonLayout {
-  size_t x, a_terms, b_terms, a, u, squares, part, total;
+  size_t x, x1, a_terms, b_terms, a, u, squares, part, total;
   long long ldx, lda, R, C, n;
 };
 MuonLayout muon_layout(long long R, long long C) {
@@ -222,12 +224,14 @@ MuonLayout muon_layout(long long R, long long C) {
     o += align256(bytes);
     return here;
   };
-  auto part_of = [](size_t outputs) {
+  auto part_of = [](size_t outputs, long long K) {
     const size_t all = outputs * 4 * kMaxSplits, may = all < kPartBytes ? all : kPartBytes;
-    return may > outputs * 4 ? may : outputs * 4;
+    const size_t least = outputs * 4 * size_t(least_splits_two((K + 63) / 64));
+    return may > least ? may : least;
   };
-  const size_t px = part_of(size_t(R) * w.ldx), pa = part_of(size_t(w.n) * w.lda);
+  const size_t px = part_of(size_t(R) * w.ldx, w.n), pa = part_of(size_t(w.n) * w.lda, R > C ? R : C);
   w.x = take(size_t(R) * w.ldx * 6);
+  w.x1 = take(size_t(R) * w.ldx * 6);
   w.a_terms = take(size_t(w.n) * w.lda * 6);
   w.b_terms = take(size_t(w.n) * w.lda * 6);
   w.a = take(size_t(w.n) * w.lda * 4);
@@ -243,40 +247,89 @@ unsigned blocks_for(long long items) {
   return unsigned(b < 1 ? 1 : (b < kSms * 8 ? b : kSms * 8));
 }
 
-// The product's partial sums to w.part.
-bool part_product(Product& p, bool two, int major, const Mat& A, const Mat& B, long long M, long long N, long long K,
-                  uint8_t* ws, const MuonLayout& w, int* status, cudaStream_t s) {
-  p = Product{};
+struct Operand {  // terms [.][rows][ld]
+  __nv_bfloat16* p;
+  long long rows, cols, ld;
+  Mat mat(long long terms) const { return Mat{p, rows, cols, ld, terms, rows * ld}; }
+};
+
+struct Call {
+  bool two;
+  uint8_t* ws;
+  MuonLayout w;
+  int* status;
+  cudaStream_t s;
+};
+
+// A B (or A B^T, A^T B by `major`) over K terms of the sum, planned.
+Product planned(const Call& c, int major, const Operand& A, const Operand& B, long long M, long long N, long long K, bool split,
+                double* time) {
+  Product p{};
   p.major = major;
-  p.f32 = !two;
-  p.two = two;
+  p.f32 = !c.two;
+  p.two = c.two;
   p.epi = kEpiOut;
-  plan(p, M, N, 1, (K + 63) / 64, 1, true);
-  p.epi = kEpiPart;
-  p.A = A;
-  p.B = B;
-  p.a.status = status;
-  Job& o = p.a.job[0];
-  o.a_term = o.b_term = 1;
-  o.out = ws + w.part;
-  o.ldo = up(N, 4);
-  o.out_plane = M * o.ldo;
-  o.out_vec = 1;
-  return two ? run_two_product(p, s) : (major == kKK ? run_fwd_product(p, s) : run_grad_product(p, s));
+  *time = plan(p, M, N, 1, (K + 63) / 64, 1, split);
+  if (p.a.job[0].splits == 1) *time += split ? Cost::kSecond : 0;  // (its second launch, if it leaves sums)
+  p.A = A.mat(c.two ? 2 : 3);
+  p.B = B.mat(c.two ? 2 : 3);
+  p.a.status = c.status;
+  p.a.job[0].a_term = p.a.job[0].b_term = 1;
+  return p;
 }
 
+// The product's partial sums to w.part, then the join.
 template <int MODE, class TW>
-bool join(const Product& p, JoinArgs j, uint8_t* ws, const MuonLayout& w, cudaStream_t s) {
-  const Job& o = p.a.job[0];
-  j.part = reinterpret_cast<const float*>(ws + w.part);
+bool split_product(const Call& c, Product p, JoinArgs j) {
+  Job& o = p.a.job[0];
+  p.epi = kEpiPart;
+  o.out = c.ws + c.w.part;
+  o.ldo = up(o.N, 4);
+  o.out_plane = o.M * o.ldo;
+  o.out_vec = 1;
+  if (!(c.two ? run_two_product(p, c.s) : (p.major == kKK ? run_fwd_product(p, c.s) : run_grad_product(p, c.s)))) return false;
+  j.part = reinterpret_cast<const float*>(c.ws + c.w.part);
   j.ldp = o.ldo;
   j.plane = o.out_plane;
   j.splits = o.splits;
   j.M = o.M;
   j.N = o.N;
   j.n4 = int(o.ldo / 4);
-  j.two = p.two;
-  return pdl_launch(join_kernel<MODE, TW>, dim3(blocks_for((long long)j.M * j.n4)), 256, s, j);
+  j.two = c.two;
+  return pdl_launch(join_kernel<MODE, TW>, dim3(blocks_for((long long)j.M * j.n4)), 256, c.s, j);
+}
+
+// The product to out's terms (and fp32 f32 [M][out.ld], nullable), or, with poly, those
+// of the polynomial with A = f32.
+bool terms_product(const Call& c, int major, const Operand& A, const Operand& B, long long K, const Operand& out, float* f32,
+                   bool poly) {
+  double whole, parts;
+  Product p = planned(c, major, A, B, out.rows, out.cols, K, false, &whole);
+  const Product q = planned(c, major, A, B, out.rows, out.cols, K, true, &parts);
+  if (whole <= parts && (!c.two || least_splits_two((K + 63) / 64) == 1)) {
+    Job& o = p.a.job[0];
+    p.epi = poly ? kEpiPoly : kEpiTerms;
+    o.out = out.p;
+    o.ldo = out.ld;
+    o.out_plane = out.rows * out.ld;
+    o.out_vec = 1;
+    if (poly) {
+      p.a.in = f32;
+      p.a.ldi = out.ld;
+      p.a.in_vec = 1;
+      p.a.c0 = kA, p.a.c1 = kB, p.a.c2 = kC;
+    } else {
+      p.a.f32 = f32;
+    }
+    return run_terms_product(p, c.s);
+  }
+  JoinArgs j{};
+  j.f32 = f32;
+  j.ld32 = out.ld;
+  j.terms = out.p;
+  j.ldt = out.ld;
+  j.tplane = out.rows * out.ld;
+  return poly ? split_product<kPoly, float>(c, q, j) : split_product<kSum, float>(c, q, j);
 }
 
 struct Step {
@@ -311,39 +364,34 @@ bool muon(const Step& q, long long R, long long C, uint8_t* ws, int* status, cud
     return false;
   const long long n = w.n;
   const bool wide = R <= C;
-  const long long terms = two ? 2 : 3;
-  const Mat X{x, R, C, w.ldx, terms, R * w.ldx}, A{ws + w.a_terms, n, n, w.lda, terms, n * w.lda},
-      B{ws + w.b_terms, n, n, w.lda, terms, n * w.lda};
+  auto at_ws = [&](size_t o) { return reinterpret_cast<__nv_bfloat16*>(ws + o); };
+  const Call c{two, ws, w, status, s};
+  const Operand A{at_ws(w.a_terms), n, n, w.lda}, B{at_ws(w.b_terms), n, n, w.lda};
+  Operand X{x, R, C, w.ldx}, Y{at_ws(w.x1), R, C, w.ldx};
   float* a32 = reinterpret_cast<float*>(ws + w.a);
-  Product p;
   for (int i = 0; i < q.steps; ++i) {
-    JoinArgs j{};
-    j.f32 = a32;
-    j.ldt = w.lda;
-    j.tplane = n * w.lda;
-    j.terms = reinterpret_cast<__nv_bfloat16*>(ws + w.a_terms);
-    if (!part_product(p, two, wide ? kKK : kNN, X, X, n, n, wide ? C : R, ws, w, status, s) || !join<kSum, float>(p, j, ws, w, s))
+    if (!terms_product(c, wide ? kKK : kNN, X, X, wide ? C : R, A, a32, false) ||
+        !terms_product(c, kKK, A, A, n, B, a32, true))
       return false;
-    j.terms = reinterpret_cast<__nv_bfloat16*>(ws + w.b_terms);
-    if (!part_product(p, two, kKK, A, A, n, n, n, ws, w, status, s) || !join<kPoly, float>(p, j, ws, w, s)) return false;
-    const bool ok = wide ? part_product(p, two, kKN, B, X, R, C, n, ws, w, status, s)
-                         : part_product(p, two, kKK, X, B, R, C, n, ws, w, status, s);
-    if (!ok) return false;
-    JoinArgs f{};
+    const int major = wide ? kKN : kKK;
+    const Operand &left = wide ? B : X, &right = wide ? X : B;
     if (i + 1 < q.steps) {
-      f.terms = x;
-      f.ldt = w.ldx;
-      f.tplane = R * w.ldx;
-      if (!join<kSum, float>(p, f, ws, w, s)) return false;
+      if (!terms_product(c, major, left, right, n, Y, nullptr, false)) return false;
+      const Operand t = X;
+      X = Y;
+      Y = t;
       continue;
     }
+    double time;
+    const Product p = planned(c, major, left, right, R, C, n, true, &time);
+    JoinArgs f{};
     const int wes = q.w_dtype == DSF_F32 ? 4 : 2;
     f.W = q.W;
     f.ldw = q.ldw;
     f.w_vec = at(q.W, 4 * wes) && q.ldw % 4 == 0;
     f.decay = 1.f - q.lr * q.decay;
     f.rate = q.lr * (R > C ? sqrtf(float(R) / float(C)) : 1.f);
-    return q.w_dtype == DSF_F32 ? join<kStep, float>(p, f, ws, w, s) : join<kStep, __nv_bfloat16>(p, f, ws, w, s);
+    return q.w_dtype == DSF_F32 ? split_product<kStep, float>(c, p, f) : split_product<kStep, __nv_bfloat16>(c, p, f);
   }
   return true;
 }

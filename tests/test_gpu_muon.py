@@ -52,7 +52,7 @@ def check(c, W, m, rank=None, lr=0.02, mu=0.95, weight_decay=0.0, nesterov=True,
 
 
 SHAPES = [(1, 1), (1, 40), (40, 1), (3, 5), (16, 16), (64, 176), (176, 64), (33, 257), (300, 100), (256, 512), (512, 256),
-          (1366, 256), (129, 1000), (640, 640), (1024, 2048), (4096, 72)]
+          (1366, 256), (129, 1000), (640, 640), (1024, 2048), (4096, 72), (40, 30000), (70001, 24)]
 
 
 @pytest.mark.parametrize("r,c", SHAPES)
