@@ -295,12 +295,13 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
               }
               // the columns whose target is one of the warp's rows
               const int id = reinterpret_cast<const int*>(cl)[256 + lane];
-              for (uint32_t hit = __ballot_sync(0xffffffffu, unsigned(id - row0) < 32u); hit; hit &= hit - 1) {
-                const int l = __ffs(hit) - 1, v = __shfl_sync(0xffffffffu, id, l);
-                const float gl = cl[128 + l];
+              // (few but in the tiles of popular rows of W)
+              if (__any_sync(0xffffffffu, unsigned(id - row0) < 32u)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (k == l && v == row) z[k] -= gl;
+                for (int k = 0; k < 32; ++k) {
+                  const volatile int* d = reinterpret_cast<const int*>(cl) + 256 + k;  // (one at a time: registers)
+                  if (*d == row) z[k] -= cl[128 + k];
+                }
               }
               if (a.db) {
                 float2 s2 = pair(0.f);
