@@ -534,11 +534,12 @@ int ctr_rms_norm_bwd(const void* dy_dev, int64_t lddy, int32_t dy_dtype, const v
  *
  * Lengths: a negative one counts as zero (DSF_FLAG_NEG_LENGTH). Where they add
  * up to more than T, the sequences are cut at T (DSF_FLAG_COUNT); rows behind
- * the last sequence are neither read nor written. T <= 2^30, D <= 2^20.
+ * the last sequence are neither read nor written. T <= 2^30, D <= 2^20, B with
+ * lengths <= 2^26.
  * Every pointer is aligned to its element; rows of a multiple of four elements
  * whose vectors of four are aligned are faster. Outputs overlap no input and
  * no other output. The workspace (256-byte aligned,
- * dsf_gated_scan_workspace_bytes, which grows with T) needs no
+ * dsf_gated_scan_workspace_bytes, which grows with T and B) needs no
  * initialisation and holds nothing from one call to the next. Equal calls give
  * equal bits; the order of sums depends on the rows' place in the call. A
  * non-finite value stays in its sequence. DSF_FLAG_TIMEOUT in *status_dev
@@ -563,7 +564,8 @@ int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int6
 /* Softmax cross entropy of M rows against a catalogue: the next item's loss of
  * a sequence or user tower over all rows of an item table. layer: W [V, K] the
  * catalogue (V = layer->R), bias nullable (a popularity correction; -inf takes
- * an item out), act DSF_ACT_NONE, dtype DSF_BF16 or DSF_F32, K <= 8192.
+ * an item out), act DSF_ACT_NONE, dtype DSF_BF16 or DSF_F32, K <= 8192,
+ * M x V <= 2^44.
  *   z = x W^T + bias,  lse = log sum_v exp z_v,  loss = lse - z_target
  * with target_dev int64 [M]. A target of -1 leaves its row out: loss 0, no
  * gradient (whatever x holds there, NaN included); one outside [0, V) the same

@@ -54,7 +54,7 @@ constexpr int kMostWidth = 32;  // channels of an item
 constexpr int kGroup = 8;       // chunks per group: a thread takes one pair at most
 static_assert(kGroup * kMostWidth <= kThreads, "a pair per thread");
 constexpr int kMaxDim = 1 << 20;
-constexpr long long kMaxRows = 1 << 30;
+constexpr long long kMaxRows = 1 << 30, kMaxSequences = 1 << 26;  // (sequences that have lengths)
 
 // rows per thread (the backward keeps four values of each element, the forward two)
 template <class T, bool REV>
@@ -539,10 +539,12 @@ __global__ void __launch_bounds__(256) step_kernel(const __grid_constant__ Args 
 }
 
 // Before the scan: the sequences' borders (lengths added up, each block all of
-// those before its own, from L2) as marks on their rows, empty sequences' states
+// those before its own, from L2; of very many sequences the sums of a block's
+// lengths, which sums_kernel leaves) as marks on their rows, empty sequences' states
 // (passed on), and the chain's pairs and ticket set to "not there".
 struct PrepArgs {
   const int* lengths;  // null: no marks
+  long long* sums;     // of 1024 lengths each (nullable)
   uint8_t* mark;
   int *first, *last, *total;
   int T, B, D;
@@ -554,6 +556,23 @@ struct PrepArgs {
   int* status;
 };
 constexpr int kPrep = 1024;
+constexpr int kManySequences = 1 << 16;  // (the 8 MB that 64 blocks then read in all take less than a launch)
+__global__ void __launch_bounds__(kPrep) sums_kernel(const int* lengths, int B, long long* sums) {
+  __shared__ long long part[kPrep / 32];
+  pdl_go();
+  pdl_wait();
+  const long long s = (long long)blockIdx.x * kPrep + threadIdx.x;
+  long long n = s < B ? max(__ldg(lengths + s), 0) : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  n = part[threadIdx.x];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if (threadIdx.x == 0) sums[blockIdx.x] = n;
+}
 __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ PrepArgs a) {
   __shared__ long long part[kPrep / 32], before;
   __shared__ int bad;
@@ -570,8 +589,12 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
   if (a.lengths) {
     if (tid == 0) bad = 0;
     long long sum = 0;
+    if (a.sums) {
+      for (int i = tid; i < int(blockIdx.x); i += kPrep) sum += a.sums[i];
+    } else {
 #pragma unroll 8
-    for (long long i = tid; i < s0; i += kPrep) sum += max(__ldg(a.lengths + i), 0);
+      for (long long i = tid; i < s0; i += kPrep) sum += max(__ldg(a.lengths + i), 0);
+    }
     const int raw = s < a.B ? __ldg(a.lengths + s) : 0, len = max(raw, 0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -631,9 +654,9 @@ struct Plan {
   int log_ct, C, tiles;
   long long chunks, groups;
   size_t mark, first, last, sync, sync_bytes, total;  // sync: the ticket and total, pairs, states
-  size_t pairs, states;
+  size_t pairs, states, sums;
 };
-Plan plan(long long T, int D, int nt) {
+Plan plan(long long T, long long B, int D, int nt) {
   Plan p{};
   // 8 threads of 4 channels, or 4 where that leaves fewer without one. (Of 8192 x 1024
   // rows' passes, 4, 8 and 16: 804, 715 and 882 us; wide chunks are short in rows, and
@@ -657,6 +680,7 @@ Plan plan(long long T, int D, int nt) {
   p.pairs = take(size_t(p.chunks) * p.tiles * width * 8);
   p.states = take(size_t(p.groups) * p.tiles * width * 8);
   p.sync_bytes = o - p.sync;
+  p.sums = take(B > kManySequences ? size_t((B + kPrep - 1) / kPrep) * 8 : 0);
   p.total = o;
   return p;
 }
@@ -664,8 +688,8 @@ Plan plan(long long T, int D, int nt) {
 bool sizes_ok(int64_t T, int64_t B, int32_t D) {
   return T >= 0 && T <= kMaxRows && B >= 0 && B <= kMaxRows && D >= 1 && D <= kMaxDim;
 }
-size_t ws_bytes_of(int64_t T, int32_t D) {
-  const size_t a = plan(T, D, 4).total, b = plan(T, D, 8).total;
+size_t ws_bytes_of(int64_t T, int32_t B, int32_t D) {
+  const size_t a = plan(T, B, D, 4).total, b = plan(T, B, D, 8).total;
   return (a > b ? a : b) + 256;
 }
 
@@ -708,7 +732,7 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
                                             : pdl_launch(step_kernel<__nv_bfloat16, false>, grid, 256, s, a));
     return ok ? DSF_OK : DSF_ECUDA;
   }
-  const Plan p = plan(a.T, a.D, rows_per_thread(es, REV));
+  const Plan p = plan(a.T, B, a.D, rows_per_thread(es, REV));
   a.tiles = p.tiles;
   a.log_ct = p.log_ct;
   a.L = a.T / B;
@@ -723,12 +747,15 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
   a.chain = p.chunks > 1 && (lengths || p.C % a.L != 0);
   if (p.chunks * p.tiles > INT32_MAX / 2) return DSF_EUNSUPPORTED;
   if (lengths || a.chain || (a.T == 0 && a.out)) {
-    PrepArgs q{lengths, ws + p.mark, const_cast<int*>(a.first), const_cast<int*>(a.last), total, a.T, B, a.D,
+    long long* sums = lengths && B > kManySequences ? reinterpret_cast<long long*>(ws + p.sums) : nullptr;
+    PrepArgs q{lengths, sums, ws + p.mark, const_cast<int*>(a.first), const_cast<int*>(a.last), total, a.T, B, a.D,
                reinterpret_cast<uint4*>(ws + p.pairs), a.chain ? (long long)((p.sync_bytes - 256) / 16) : 0, a.in, a.out, a.ticket, a.status};
     long long blocks = (lengths || a.T == 0) ? ((long long)B + kPrep - 1) / kPrep : 1;
     const long long filling = (q.fills + 4 * kPrep - 1) / (4 * kPrep), most = 152;
     if (blocks < filling) blocks = filling < most ? filling : (blocks < most ? most : blocks);
     if (lengths && a.T > 0 && !succeeded(cudaMemsetAsync(ws + p.mark, 0, size_t(a.T), s))) return DSF_ECUDA;
+    if (sums && !pdl_launch(sums_kernel, dim3(unsigned(((long long)B + kPrep - 1) / kPrep)), kPrep, s, lengths, B, sums))
+      return DSF_ECUDA;
     if (!pdl_launch(prep_kernel, dim3(unsigned(blocks)), kPrep, s, q)) return DSF_ECUDA;
   }
   if (a.T == 0) return DSF_OK;
@@ -747,10 +774,11 @@ int check(int32_t dtype, const int32_t* lengths, int64_t T, int32_t B, int32_t D
   if (dtype != DSF_F32 && dtype != DSF_BF16) return DSF_EUNSUPPORTED;
   if (!sizes_ok(T, B, D) || !at(lengths, 4) || !at(s0, 4) || !at(s1, 4) || !at(s2, 4)) return DSF_EINVAL;
   if (!lengths && B > 0 && T % B != 0) return DSF_EINVAL;
+  if (lengths && B > kMaxSequences) return DSF_EUNSUPPORTED;
   return DSF_OK;
 }
-int check_ws(int64_t T, int32_t D, const void* ws, size_t ws_bytes) {
-  return ws && at(ws, 256) && ws_bytes >= ws_bytes_of(T, D) ? DSF_OK : DSF_EWORKSPACE;
+int check_ws(int64_t T, int32_t B, int32_t D, const void* ws, size_t ws_bytes) {
+  return ws && at(ws, 256) && ws_bytes >= ws_bytes_of(T, B, D) ? DSF_OK : DSF_EWORKSPACE;
 }
 
 }  // namespace
@@ -762,7 +790,7 @@ using namespace dsf::scan;
 extern "C" {
 
 size_t dsf_gated_scan_workspace_bytes(int64_t T, int32_t B, int32_t D) {
-  return sizes_ok(T, B, D) ? ws_bytes_of(T, D) : 0;
+  return sizes_ok(T, B, D) ? ws_bytes_of(T, B, D) : 0;
 }
 
 int ctr_gated_scan_fwd(const void* x, int64_t ldx, const void* gate, int64_t ldg, int32_t dtype, const int32_t* lengths,
@@ -771,7 +799,7 @@ int ctr_gated_scan_fwd(const void* x, int64_t ldx, const void* gate, int64_t ldg
   if (int rc = check(dtype, lengths, T, B, D, h0, h_last, nullptr)) return rc;
   const int es = dtype == DSF_F32 ? 4 : 2;
   if (T > 0 && (!rows_ok(x, ldx, D, es) || !rows_ok(gate, ldg, D, es) || !rows_ok(h, ldh, D, es))) return DSF_EINVAL;
-  if (int rc = check_ws(T, D, ws, ws_bytes)) return rc;
+  if (int rc = check_ws(T, B, D, ws, ws_bytes)) return rc;
   if (B == 0) return DSF_OK;
   Args a{};
   a.x = x, a.ldx = ldx, a.gate = gate, a.ldg = ldg, a.o0 = h, a.ldo0 = ldh;
@@ -789,7 +817,7 @@ int ctr_gated_scan_bwd(const void* dh, int64_t lddh, const void* x, int64_t ldx,
   if (T > 0 && (!rows_ok(dh, lddh, D, es) || !rows_ok(x, ldx, D, es) || !rows_ok(gate, ldg, D, es) ||
                 !rows_ok(h, ldh, D, es) || !rows_ok(dx, lddx, D, es) || !rows_ok(dgate, lddg, D, es)))
     return DSF_EINVAL;
-  if (int rc = check_ws(T, D, ws, ws_bytes)) return rc;
+  if (int rc = check_ws(T, B, D, ws, ws_bytes)) return rc;
   if (B == 0) return DSF_OK;
   Args a{};
   a.x = x, a.ldx = ldx, a.gate = gate, a.ldg = ldg, a.h = h, a.ldh = ldh, a.dh = dh, a.lddh = lddh;
