@@ -12,6 +12,10 @@
 // (one rounding to bf16, or an fp32 operand's three terms), then dW's rows of
 // the piece, complete, and dx added up over the pieces in fp32 planes. So
 // memory holds M x (a piece), whatever V is, and sums run in a fixed order.
+// (Pieces of 256 MB: 16384 rows, 65,536 columns of 1024 bf16, the sums and all
+// gradients, 5.9 ms; of 64 MB 6.7, of 96 MB 6.5, of 1 GB 5.7.)
+// Where x and W are narrow, passes that keep no dz at all take over (xent_pass.cuh),
+// and few_kernel has the sums of a step of serving, 4 rows at most.
 #include "dense_host.cuh"
 #include "xent_pass.cuh"
 
@@ -20,6 +24,7 @@ namespace dense {
 namespace {
 
 constexpr int kMaxK = 8192;
+constexpr long long kMaxLogits = 1LL << 44;  // (2^30 tiles)
 constexpr size_t kPieceBytes = 256u << 20;  // dz of a piece
 
 // ---------------------------------------------------------------- small kernels
@@ -79,9 +84,10 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
 
 // The sums of up to MT rows from W's rows as they lie in memory, on the CUDA cores: a
 // tensor-core tile would use MT of its 128 rows. The catalogue's bytes are what counts
-// (one row, 846,812 x 64 bf16: 26 us with the merge; by tiles 44). 2^log_g lanes side by side have one row of
-// W (a 16-byte vector each), a warp 32 / 2^log_g rows, and U of those in flight; each
-// lane keeps the reference and sum of its rows (alike in the lanes of a row).
+// (one row, 846,812 x 64 bf16: 26 us with the merge; by tiles 44). 2^log_g lanes side
+// by side have one row of W (a 16-byte vector each), a warp 32 / 2^log_g rows, and U
+// of those in flight; each lane keeps the reference and sum of its rows (alike in the
+// lanes of a row).
 struct FewArgs {
   const void *x, *W;
   long long ldx, ldw;
@@ -217,11 +223,14 @@ __global__ void __launch_bounds__(256) db_kernel(const float* part, int V, float
 }
 
 // ---------------------------------------------------------------- layout
-// Whether the rows' sums, or the gradients, are taken in one pass each (xent_pass.cuh).
-// (Both ways, us: the sums of 1024 rows over 100,000 columns of 64 42 and 45, of 512 33
-// and 29, of 8192 over 8192 34 and 39; the gradients 116 and 138, 85 and 80, 110 and 85.)
+// Whether the rows' sums, or the gradients, are taken in one pass each (xent_pass.cuh):
+// where there are 1e8 logits and, for each 64 of K, two tiles of rows. (The gradients
+// both ways, us, at K = 64: 512 rows over 100,000 columns 85 and 80, 1024 120 and 142,
+// 128 over 846,812 248 and 220, 256 286 and 320; at K = 128: 256 rows over 846,812 420
+// and 364, 2048 over 131,072 278 and 353. The sums alike: 1024 rows over 100,000 of 64 42
+// and 45, of 512 33 and 29, 128 over 846,812 103 and 80, 256 106 and 109.)
 bool narrow(const dsf_dense* l, long long M) {
-  return l->dtype == DSF_BF16 && l->K <= 128 && M <= 65536 && double(M) * l->R >= 1e8;
+  return l->dtype == DSF_BF16 && l->K <= 128 && M <= 65536 && M > (l->K <= 64 ? 128 : 384) && double(M) * l->R >= 1e8;
 }
 // Whether the sums are few_kernel's: of up to 4 rows, whole vectors, at most 32 of them.
 bool few(const dsf_dense* l, long long M) {
@@ -547,6 +556,10 @@ int check_xent(const dsf_dense* l) {
   if (l->dtype == DSF_E4M3 || l->K > kMaxK) return DSF_EUNSUPPORTED;
   return l->act == DSF_ACT_NONE ? DSF_OK : DSF_EINVAL;
 }
+int check_rows(const dsf_dense* l, int64_t M) {
+  if (M < 0 || M > kMaxM) return DSF_EINVAL;
+  return M > kMaxLogits / l->R ? DSF_EUNSUPPORTED : DSF_OK;
+}
 
 }  // namespace
 }  // namespace dense
@@ -557,14 +570,14 @@ using namespace dsf::dense;
 extern "C" {
 
 size_t dsf_softmax_xent_workspace_bytes(const dsf_dense* l, int64_t M, int32_t backward) {
-  if (check_xent(l) != DSF_OK || M < 0 || M > kMaxM || backward < 0 || backward > 1) return 0;
+  if (check_xent(l) != DSF_OK || check_rows(l, M) != DSF_OK || backward < 0 || backward > 1) return 0;
   return xent_layout(l, M, backward != 0).total;
 }
 
 int ctr_softmax_xent_fwd(const dsf_dense* l, const void* x, int64_t ldx, const int64_t* target, int64_t M, float* loss,
                          float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
   if (int rc = check_xent(l)) return rc;
-  if (M < 0 || M > kMaxM) return DSF_EINVAL;
+  if (int rc = check_rows(l, M)) return rc;
   if (M == 0) return DSF_OK;
   if (!rows_ok(x, ldx, l->K, esize(l->dtype)) || !target || !at(target, 8) || !loss || !at(loss, 4) || !lse || !at(lse, 4))
     return DSF_EINVAL;
@@ -579,7 +592,7 @@ int ctr_softmax_xent_bwd(const dsf_dense* l, const void* x, int64_t ldx, const i
                          const float* dloss, int64_t M, void* dx, int64_t lddx, void* dW, float* db, void* ws,
                          size_t ws_bytes, int32_t* status, void* stream) {
   if (int rc = check_xent(l)) return rc;
-  if (M < 0 || M > kMaxM) return DSF_EINVAL;
+  if (int rc = check_rows(l, M)) return rc;
   const int es = esize(l->dtype);
   if (!at(dW, es) || !at(db, 4)) return DSF_EINVAL;
   if (M > 0 && (!rows_ok(x, ldx, l->K, es) || !target || !at(target, 8) || !lse || !at(lse, 4) || !at(dloss, 4) ||

@@ -21,9 +21,9 @@
 // 131,072 columns of 64; the backward's passes 415 us each, the sums' 320): the
 // epilogue and the second product, whose operand comes from tensor memory, take turns
 // there. Without the second product a tile takes 0.67 us, with it 0.96; dz in buffers
-// of its own (0.98), 24 epilogue warps (0.95), and the exponentials (none: 0.94)
-// change little. From K = 192 on dz in memory is as fast (1.5 ms against 1.6 for both
-// gradients at 192, 1.6 against 1.9 at 256).
+// of its own (1.00), in shared memory (1.03), 24 epilogue warps (0.96), and the
+// exponentials (none: 0.95) change little. At K = 256 dz in memory is faster (both
+// gradients 1.6 ms against 1.9), at 128 slower (1.42 against 0.98).
 // Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
 // columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
 #pragma once

@@ -145,6 +145,17 @@ def test_bad_lengths(lengths, T, cut, flag):
     check(v, cut, o)
 
 
+@pytest.mark.parametrize("nb,mean", [(65536, 0.8), (65537, 0.8), (200003, 0.6)])
+def test_very_many_sequences(nb, mean):
+    """Most of them empty; one of a negative length among the last."""
+    lengths = jagged(7, nb, mean)
+    v = inputs(8, F32, sum(lengths) + 2, 8, nb)
+    o, status = run(v, lengths[:-3] + [-4] + lengths[-2:], nb)
+    cut = lengths[:-3] + [0] + lengths[-2:]
+    assert status == B.FLAG_NEG_LENGTH
+    check(v, cut, o)
+
+
 @pytest.mark.parametrize("D", [48, 33])
 def test_non_finite_values_stay_in_their_sequence(D):
     lengths = [5, 300, 1, 700, 40, 1300]

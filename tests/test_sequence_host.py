@@ -121,3 +121,23 @@ def test_muon_refusals(L):
     for kw in (dict(ws=None), dict(ws=4096 + 128), dict(nb=need - 1)):
         assert call(**kw) == B.DSF_EWORKSPACE, kw
     assert L.dsf_muon_workspace_bytes(0, 4) == 0 and L.dsf_muon_workspace_bytes(1 << 16, 1 << 16) == 0
+
+
+def test_sizes_beyond_the_limits_are_refused(L):
+    """More logits than 2^44, more sequences with lengths than 2^26."""
+    l = layer(R=1 << 20, K=8, ldw=8)
+    for M, code in ((1 << 24, B.DSF_EWORKSPACE), ((1 << 24) + 1, B.DSF_EUNSUPPORTED)):
+        assert L.ctr_softmax_xent_fwd(P(l), 4096, 8, 4096, M, 4096, 4096, 4096, 16, None, None) == code
+        assert L.ctr_softmax_xent_bwd(P(l), 4096, 8, 4096, 4096, None, M, 4096, 8, 4096, 4096, 4096, 16, None, None) == code
+        for back in (0, 1):
+            assert (L.dsf_softmax_xent_workspace_bytes(P(l), M, back) == 0) == (code == B.DSF_EUNSUPPORTED)
+    for nb, code in ((1 << 26, B.DSF_EWORKSPACE), ((1 << 26) + 1, B.DSF_EUNSUPPORTED)):
+        assert L.ctr_gated_scan_fwd(4096, 16, 4096, 16, B.DSF_F32, 4096, 12, nb, 16, None, 4096, 16, None, 4096, 16, None,
+                                    None) == code
+        assert L.ctr_gated_scan_bwd(4096, 16, 4096, 16, 4096, 16, 4096, 16, B.DSF_F32, 4096, 12, nb, 16, None, None, 4096, 16,
+                                    4096, 16, None, 4096, 16, None, None) == code
+
+
+def test_scan_workspace_grows_with_the_sequences(L):
+    sizes = [L.dsf_gated_scan_workspace_bytes(5000, nb, 33) for nb in (0, 1, 1024, 65536, 65537, 70000, 1 << 20, 1 << 26)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
