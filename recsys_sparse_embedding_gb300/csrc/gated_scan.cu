@@ -22,9 +22,9 @@
 // whatever else runs; every wait is bounded and sets DSF_FLAG_TIMEOUT when it
 // runs out.
 //
-// Fixed order: chunks are in groups of 8; a chunk starts from the state at the
-// end of the group before its own and composes the pairs of its group in a
-// fixed tree, so equal calls give equal bits, however blocks are scheduled, and
+// Fixed order: chunks are in groups (8 of 32 channels, 16 of 16: a pair per thread); a
+// chunk starts from the state at the end of the group before its own and composes the
+// pairs of its group in a fixed tree, so equal calls give equal bits, however blocks are scheduled, and
 // the chain through memory has one step per group. A pair and a state are 8
 // bytes, stored and polled whole; all bits set means "not there yet" (no
 // arithmetic gives that NaN), so no flag and no fence is needed.
@@ -49,10 +49,9 @@ namespace dsf {
 namespace scan {
 namespace {
 
+constexpr int kSms = 152;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostWidth = 32;  // channels of an item
-constexpr int kGroup = 8;       // chunks per group: a thread takes one pair at most
-static_assert(kGroup * kMostWidth <= kThreads, "a pair per thread");
 constexpr int kMaxDim = 1 << 20;
 constexpr long long kMaxRows = 1 << 30, kMaxSequences = 1 << 26;  // (sequences that have lengths)
 
@@ -180,6 +179,12 @@ __device__ __forceinline__ void give(unsigned long long* p, float2 f) {
   st_relaxed_u64(p, uint64_t(__float_as_uint(f.y)) << 32 | __float_as_uint(f.x));
 }
 
+// What a warp's rows are: none a sequence's border; some; or not all of the chunk's
+// rows are there.
+enum { kPlain = 0, kMarked = 1, kPartial = 2 };
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
 template <class T, bool REV>
 struct Shared {
   static constexpr int NT = rows_of<T, REV>(), NA = REV ? 4 : 2;
@@ -193,11 +198,12 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
   constexpr int NT = S::NT, NA = S::NA;
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ float2 s_pair[kWarps][kMostWidth];  // the warps' pairs, then those of the warps before
-  __shared__ float2 s_look[kThreads];
+  __shared__ float2 s_look[kWarps * kMostWidth];
   __shared__ float s_carry[kMostWidth];
   __shared__ int s_comes, s_ticket;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CT = 1 << a.log_ct, ct = tid & (CT - 1), slice = tid >> a.log_ct, C = (kThreads >> a.log_ct) * NT, W = 4 * CT;
+  const int log_group = 6 - a.log_ct;  // chunks of a group: a pair per thread
   pdl_go();
   pdl_wait();
   const int total = a.total ? *a.total : a.T, chunks = (total + C - 1) / C;
@@ -292,13 +298,12 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
   float2 A[2], Bv[2];  // the thread's pair
   float2 leaveA[2], leaveB[2];  // backward: that of the rows up to the first that leaves, if no reset is among them
   uint32_t reset, leave;
-  auto rows = [&](const Item& it, auto plain) {
-    constexpr bool PLAIN = decltype(plain)::value;
+  auto rows = [&](const Item& it, auto kind) {
+    constexpr bool PLAIN = kind == kPlain, WHOLE = kind != kPartial;
     const int c0 = (it.tile * CT + ct) * 4;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const bool in = PLAIN || row_of(i) < it.n;
-      if (!in) continue;
+      if (!WHOLE && row_of(i) >= it.n) continue;
       float2 g[2], v[2], z[2], a1[2], x[2], hp[2];
       slot(1, i)->get(g);
       slot(REV ? 2 : 0, i)->get(v);
@@ -346,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
   };
   // the rows' outputs, and the states that leave: those of the pair's last row y
   // steps on by
-  auto write = [&](const Item& it, const float2* y, auto plain) {
-    constexpr bool PLAIN = decltype(plain)::value;
+  auto write = [&](const Item& it, const float2* y, auto kind) {
+    constexpr bool PLAIN = kind == kPlain, WHOLE = kind != kPartial;
     const int c0 = (it.tile * CT + ct) * 4, w = width(it);
     const long long t1 = it.t0 + row_of(0), d0 = REV ? -a.ldo0 : a.ldo0, d1 = -a.ldo1;
     T* o0 = static_cast<T*>(a.o0) + t1 * a.ldo0 + c0;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
     const int first = PLAIN || !reset ? NT : __ffs(reset) - 1;  // (from there on y has no part)
 #pragma unroll
     for (int i = 0; i < NT; ++i, o0 += d0, o1 += REV ? d1 : 0) {
-      if (!PLAIN && row_of(i) >= it.n) continue;
+      if (!WHOLE && row_of(i) >= it.n) continue;
       float2 p[2], q[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
     request();
     // the pairs of the item's group before it and the state before the group (looked
     // at now, awaited when the item's own pair is out)
-    const int group = cur.rank / kGroup, j0 = group * kGroup + tid / W;
+    const int group = cur.rank >> log_group, j0 = (group << log_group) + tid / W;
     const long long step = (long long)a.tiles * W;
     const unsigned long long* pp = a.pairs + ((long long)j0 * a.tiles + cur.tile) * W + (tid & (W - 1));
     const unsigned long long* ps = a.states + ((long long)(group - 1) * a.tiles + cur.tile) * W + tid;
@@ -420,10 +425,11 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
     Bv[0] = Bv[1] = pair(0.f);
     reset = leave = 0;
     if (live) sets(cur, reset, leave);
-    const bool plain = whole(cur) && !(reset | leave);
+    const int kind = whole(cur) ? (__any_sync(0xffffffffu, reset | leave) ? kMarked : kPlain) : kPartial;  // (the warp's: one way for all)
     if (live) {
-      if (plain) rows(cur, std::true_type{});
-      else rows(cur, std::false_type{});
+      if (kind == kPlain) rows(cur, Kind<kPlain>{});
+      else if (kind == kMarked) rows(cur, Kind<kMarked>{});
+      else rows(cur, Kind<kPartial>{});
     }
     if (tid == 0) s_comes = a.chain && !(reset & 1u) && !(REV && cur.n < C);
     float qa[4] = {A[0].x, A[0].y, A[1].x, A[1].y}, qb[4] = {Bv[0].x, Bv[0].y, Bv[1].x, Bv[1].y};
@@ -457,7 +463,11 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
     if (comes) {
       float2 f = make_float2(1.f, 0.f);
       if (mine) ok = take(pp, raw, f) && ok;
-      if (tid < kGroup * W) s_look[tid] = f;
+      for (int d = W; d < 32; d <<= 1) {  // (the warp's pairs)
+        const float ap = __shfl_up_sync(0xffffffffu, f.x, d), bp = __shfl_up_sync(0xffffffffu, f.y, d);
+        if (lane >= d) compose(ap, bp, f.x, f.y);
+      }
+      if (lane >= 32 - W) s_look[warp * W + (lane & (W - 1))] = f;
       __syncthreads();
     }
     if (tid < W) {
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
       if (comes) {
         float QA = 1.f, QB = 0.f;
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) {
+        for (int k = 0; k < kWarps; ++k) {
           float2 f = s_look[k * W + tid];
           compose(QA, QB, f.x, f.y);
           QA = f.x, QB = f.y;
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
         y = apply(QA, QB, y);
       }
       s_carry[tid] = y;
-      if (a.chain && cur.rank % kGroup == kGroup - 1) give(const_cast<unsigned long long*>(ps) + step, make_float2(apply(tot.x, tot.y, y), 0.f));
+      if (a.chain && ((cur.rank + 1) & ((1 << log_group) - 1)) == 0) give(const_cast<unsigned long long*>(ps) + step, make_float2(apply(tot.x, tot.y, y), 0.f));
     }
     // the state before the thread's rows: of the warp's threads before it, of the warps
     // before, of the chunks before
@@ -497,8 +507,9 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
         const float2 e = s_pair[warp][ct * 4 + v];
         yf[v] = apply(qa[v], qb[v], apply(e.x, e.y, s_carry[ct * 4 + v]));
       }
-      if (plain) write(cur, y, std::true_type{});
-      else write(cur, y, std::false_type{});
+      if (kind == kPlain) write(cur, y, Kind<kPlain>{});
+      else if (kind == kMarked) write(cur, y, Kind<kMarked>{});
+      else write(cur, y, Kind<kPartial>{});
     }
     cur = nxt;
   }
@@ -548,6 +559,7 @@ struct PrepArgs {
   uint8_t* mark;
   int *first, *last, *total;
   int T, B, D;
+  bool clear;  // whether the marks have to be set to 0 first
   uint4* fill;
   long long fills;
   const float* in;
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(kPrep) sums_kernel(const int* lengths, int B, 
   if (threadIdx.x == 0) sums[blockIdx.x] = n;
 }
 __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ PrepArgs a) {
-  __shared__ long long part[kPrep / 32], before;
+  __shared__ long long part[kPrep / 32], before, after;
   __shared__ int bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_go();
@@ -621,12 +633,21 @@ __global__ void __launch_bounds__(kPrep) prep_kernel(const __grid_constant__ Pre
     for (int o = 16; o; o >>= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
     end += ahead + before;
     const long long T = a.T;
+    if (a.clear) {  // the rows of the block's sequences
+      if (tid == kPrep - 1) after = end;
+      __syncthreads();
+      const long long lo = min(before, T), hi = min(after, T), lo16 = min((lo + 15) & ~15LL, hi), hi16 = max(hi & ~15LL, lo16);
+      if (tid < lo16 - lo) a.mark[lo + tid] = 0;
+      for (long long i = lo16 + 16 * tid; i < hi16; i += 16 * kPrep) *reinterpret_cast<uint4*>(a.mark + i) = make_uint4(0, 0, 0, 0);
+      if (tid < hi - hi16) a.mark[hi16 + tid] = 0;
+      __syncthreads();
+    }
     if (s == a.B - 1 && a.status && end > T) atomicOr(a.status, DSF_FLAG_COUNT);
     if (tid == 0 && bad && a.status) atomicOr(a.status, DSF_FLAG_NEG_LENGTH);
     b = int(min(end - len, T));
     e = int(min(end, T));
     if (s == a.B - 1) *a.total = e;
-    if (s < a.B && e > b) {  // (the marks are zero beforehand)
+    if (s < a.B && e > b) {  // (the others are zero)
       a.first[b] = int(s);
       a.last[e - 1] = int(s);
       a.mark[b] = e - b == 1 ? 3 : 1;
@@ -651,22 +672,20 @@ constexpr int rows_per_thread(int es, bool rev) {
 }
 
 struct Plan {
-  int log_ct, C, tiles;
+  int D, log_ct, C, tiles;
   long long chunks, groups;
   size_t mark, first, last, sync, sync_bytes, total;  // sync: the ticket and total, pairs, states
   size_t pairs, states, sums;
 };
-Plan plan(long long T, long long B, int D, int nt) {
+Plan plan(long long T, long long B, int D, int nt, int log_ct) {
   Plan p{};
-  // 8 threads of 4 channels, or 4 where that leaves fewer without one. (Of 8192 x 1024
-  // rows' passes, 4, 8 and 16: 804, 715 and 882 us; wide chunks are short in rows, and
-  // wait for more of them that are under way.)
-  p.log_ct = (D + 31) / 32 * 2 == (D + 15) / 16 ? 3 : 2;
+  p.D = D;
+  p.log_ct = log_ct;
   p.C = (kThreads >> p.log_ct) * nt;
   const int width = 4 << p.log_ct;
   p.tiles = (D + width - 1) / width;
   p.chunks = (T + p.C - 1) / p.C;
-  p.groups = (p.chunks + kGroup - 1) / kGroup;
+  p.groups = ((p.chunks - 1) >> (6 - p.log_ct)) + 1;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t here = o;
@@ -688,9 +707,25 @@ Plan plan(long long T, long long B, int D, int nt) {
 bool sizes_ok(int64_t T, int64_t B, int32_t D) {
   return T >= 0 && T <= kMaxRows && B >= 0 && B <= kMaxRows && D >= 1 && D <= kMaxDim;
 }
+// Threads of 4 channels side by side, as a power of two: 8; 4 where that leaves fewer
+// without a channel, or where the chain binds: a group of 8 x 8 chunks' rows takes 0.55
+// us, unless other sequences' are under way beside it, and the bytes move at 3.2 TB/s.
+// (Chunks of 16 channels are longer in rows, and 16 of them are a group. Forward and
+// backward with 8 | 4 | 2 threads, bf16, us: one sequence of 262,144 x 64 207 | 188 | 205,
+// 64 of them 166 | 171 | 195; 131,071 x 1024 652 | 766 | 1084.)
+int pick_ct(const Plan& p, long long B, size_t bytes) {
+  if (p.tiles * 2 != (p.D + 15) / 16) return 2;
+  const double window = 2.0 * kSms / p.tiles, chunks = double(p.chunks) / double(B), beside = chunks < window ? window / chunks : 1;
+  return double(p.groups) * 0.55 / beside > double(bytes) / 3.2e6 ? 2 : 3;
+}
 size_t ws_bytes_of(int64_t T, int32_t B, int32_t D) {
-  const size_t a = plan(T, B, D, 4).total, b = plan(T, B, D, 8).total;
-  return (a > b ? a : b) + 256;
+  size_t most = 0;
+  for (int log_ct = 2; log_ct < 4; ++log_ct)
+    for (int nt = 4; nt <= 8; nt += 4) {
+      const size_t n = plan(T, B, D, nt, log_ct).total;
+      most = most > n ? most : n;
+    }
+  return most + 256;
 }
 
 template <class T, bool REV, bool VEC>
@@ -732,7 +767,9 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
                                             : pdl_launch(step_kernel<__nv_bfloat16, false>, grid, 256, s, a));
     return ok ? DSF_OK : DSF_ECUDA;
   }
-  const Plan p = plan(a.T, B, a.D, rows_per_thread(es, REV));
+  const int nt = rows_per_thread(es, REV);
+  Plan p = plan(a.T, B, a.D, nt, 3);
+  if (pick_ct(p, B, size_t(a.T) * a.D * es * (REV ? 6 : 3)) == 2) p = plan(a.T, B, a.D, nt, 2);
   a.tiles = p.tiles;
   a.log_ct = p.log_ct;
   a.L = a.T / B;
@@ -748,12 +785,15 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
   if (p.chunks * p.tiles > INT32_MAX / 2) return DSF_EUNSUPPORTED;
   if (lengths || a.chain || (a.T == 0 && a.out)) {
     long long* sums = lengths && B > kManySequences ? reinterpret_cast<long long*>(ws + p.sums) : nullptr;
-    PrepArgs q{lengths, sums, ws + p.mark, const_cast<int*>(a.first), const_cast<int*>(a.last), total, a.T, B, a.D,
+    // the marks: each block its sequences' rows (one may have all of them), or a launch of its own
+    const long long parts = ((long long)B + kPrep - 1) / kPrep;
+    const bool clear = a.T <= (1 << 17) * (parts < 4 ? parts : 4);
+    PrepArgs q{lengths, sums, ws + p.mark, const_cast<int*>(a.first), const_cast<int*>(a.last), total, a.T, B, a.D, clear,
                reinterpret_cast<uint4*>(ws + p.pairs), a.chain ? (long long)((p.sync_bytes - 256) / 16) : 0, a.in, a.out, a.ticket, a.status};
     long long blocks = (lengths || a.T == 0) ? ((long long)B + kPrep - 1) / kPrep : 1;
-    const long long filling = (q.fills + 4 * kPrep - 1) / (4 * kPrep), most = 152;
+    const long long filling = (q.fills + 4 * kPrep - 1) / (4 * kPrep), most = kSms;
     if (blocks < filling) blocks = filling < most ? filling : (blocks < most ? most : blocks);
-    if (lengths && a.T > 0 && !succeeded(cudaMemsetAsync(ws + p.mark, 0, size_t(a.T), s))) return DSF_ECUDA;
+    if (lengths && !clear && !succeeded(cudaMemsetAsync(ws + p.mark, 0, size_t(a.T), s))) return DSF_ECUDA;
     if (sums && !pdl_launch(sums_kernel, dim3(unsigned(((long long)B + kPrep - 1) / kPrep)), kPrep, s, lengths, B, sums))
       return DSF_ECUDA;
     if (!pdl_launch(prep_kernel, dim3(unsigned(blocks)), kPrep, s, q)) return DSF_ECUDA;
