@@ -152,6 +152,39 @@ double plan(Product& p, long long M, long long N, int nb, long long nkb, int nse
   return best;
 }
 
+// The tiles of a square product that touch its lower triangle: tile row m covers the
+// columns up to its own last row's.
+long long tri_tiles(const Job& o, int cfg, bool f32) {
+  const long long q = cfg_rows(cfg) / cfg_bn(cfg, f32);
+  return q * o.mt * (o.mt - 1) / 2 + o.nt;
+}
+
+// plan() for a symmetric product [n][n] of which those tiles are made, its partial sums
+// of at most `room` bytes (or of as many as it has to have); its time with the second launch.
+double plan_tri(Product& p, long long n, long long nkb, size_t room) {
+  const Cost cost{p.f32, p.two ? 3.0 : 1.0};
+  double best = 1e300;
+  Job o = p.a.job[0];
+  const long long least = p.two ? least_splits_two(nkb) : 1;
+  for (int cfg = 0; cfg < 3; ++cfg)
+    for (long long want = least; want <= kMaxSplits && want <= nkb; ++want) {
+      set_tiles(o, cfg, n, n, 1, false, p.f32, nkb, 1, want);
+      const long long tiles = tri_tiles(o, cfg, p.f32);
+      if (want > least && (tiles * want > slots_of(cfg) || size_t(want) * n * ((n + 3) / 4 * 4) * 4 > room)) break;
+      if (want > least && o.splits != want) continue;
+      const long long waves = (tiles * o.splits + slots_of(cfg) - 1) / slots_of(cfg);
+      const double c = Cost::kLaunch + cost.run(cfg, double(waves), double(o.kbps)) + Cost::kSecond +
+                       double(o.splits) * double(n) * double(n) * 4 / Cost::kBytesPerUs;
+      if (c < best) {
+        best = c;
+        p.cfg = cfg;
+        p.a.job[0] = o;
+        p.a.tri = int(tiles);
+      }
+    }
+  return best;
+}
+
 // dW (job 0, which may be split) and dx (job 1) in one launch.
 double plan_dual(Product& p, long long M, long long N, long long K, int halves) {
   const Cost cost{p.f32};

@@ -146,6 +146,7 @@ struct TcArgs {
   const float2* rows;       // kEpiXent: [M] (lse, g)
   float* f32;               // kEpiTerms: rows of ldo elements (nullable)
   float c0, c1, c2;         // kEpiPoly
+  int tri;                  // kEpiPart: 0, or the tiles of a symmetric product that touch its lower triangle (tri_tiles)
   int* status;
 };
 
@@ -405,7 +406,8 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
   };
   const int lane_of = EPI == kEpiLse || EPI == kEpiXent ? unit0 / a.gm : 0, mg = unit0 - lane_of * a.gm;
   const auto& job0 = a.job[0];
-  const int units = job0.mt * job0.nt * job0.nb * job0.splits;
+  const bool tri = EPI == kEpiPart && !DUAL && a.tri != 0;
+  const int units = (tri ? a.tri : job0.mt * job0.nt * job0.nb) * job0.splits;
   auto unit_at = [&](int i, Unit& t) {
     int u = unit0 + i * units_step;
     t.job = 0;
@@ -436,6 +438,18 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     const Job& o = a.job[DUAL ? t.job : 0];
     uint32_t r = div_by(u, o.by_splits);
     t.split = u - int(r) * o.splits;
+    if (tri) {  // M tile m has its first Q (m + 1) N tiles
+      constexpr int Q = 128 * CG / ON;
+      int m = int((sqrtf(8.f / Q * float(r) + 1.f) - 1.f) * 0.5f);
+      if (Q * m * (m + 1) / 2 > int(r)) --m;
+      if (Q * (m + 1) * (m + 2) / 2 <= int(r)) ++m;
+      t.batch = 0;
+      t.m0 = m * 128 * CG + int(rank) * 128;
+      t.n0 = (int(r) - Q * m * (m + 1) / 2) * ON;
+      t.kb0 = t.split * o.kbps;
+      t.kbn = min(o.kbps, o.nkb - t.kb0);
+      return true;
+    }
     t.batch = int(div_by(r, o.by_batch));
     r -= uint32_t(t.batch) * o.by_batch.d;
     const uint32_t grp = div_by(r, o.by_group);
@@ -1216,7 +1230,7 @@ bool launch_tc(const Product& p, cudaStream_t s) {
   long long n[2] = {0, 0};  // units
   for (int j = 0; j < (MAJOR == kDual ? 2 : 1); ++j) {
     Job& o = a.job[j];
-    n[j] = (long long)o.mt * o.nt * o.nb * o.splits;
+    n[j] = (long long)(EPI == kEpiPart && MAJOR != kDual && a.tri ? a.tri : (long long)o.mt * o.nt * o.nb) * o.splits;
     if (n[j] <= 0 || n[j] * CG > INT32_MAX) return false;
     o.by_splits = make_div(uint32_t(o.splits));
     o.by_batch = make_div(uint32_t(o.mt) * uint32_t(o.nt));

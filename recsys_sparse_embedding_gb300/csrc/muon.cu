@@ -13,9 +13,10 @@
 // products) leave X 2.5e-5 to 5e-5 off, which W's rounding hides at half the work.
 // (One bf16 product would leave 1 to 3% of X, one fp16 0.2 to 0.3%.)
 //
-// A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations) leave the next
-// operand's terms in their epilogues; where a product is better split over K, it
-// leaves fp32 partial sums that a second kernel adds up and lays out.
+// A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations; the first two are
+// symmetric, and large ones are made by half) leave the next operand's terms in their
+// epilogues; where a product is better split over K, it leaves fp32 partial sums that
+// a second kernel adds up and lays out.
 #include "dense_host.cuh"
 
 namespace dsf {
@@ -25,6 +26,7 @@ namespace {
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f, kEps = 1e-7f;
 constexpr int kMaxShort = 1 << 15, kMaxSteps = 16;
 constexpr int kNormBlocks = 512;
+constexpr size_t kTriBytes = 2 * kPartBytes;  // of A's partial sums (whole squares, though half of the tiles are made)
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16(v); }
@@ -157,7 +159,8 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Scal
 //   kSum   as terms, and in fp32 where f32 is given;
 //   kPoly  a I + b A + c (the sum), A = f32, as terms;
 //   kStep  W = decay W - rate (the sum).
-enum { kSum = 0, kPoly = 1, kStep = 2 };
+// (kMirror, kMirrorPoly: kSum and kPoly by mirror_kernel)
+enum { kSum = 0, kPoly = 1, kStep = 2, kMirror = 3, kMirrorPoly = 4 };
 struct JoinArgs {
   const float* part;
   long long ldp, plane;
@@ -210,6 +213,53 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   }
 }
 
+// A symmetric product's partial sums, of which the lower triangle is there, as
+// join_kernel's kSum or kPoly. A block has 32 x 32 elements of the triangle and writes them,
+// turned over in shared memory, above the diagonal too.
+template <bool POLY>
+__global__ void __launch_bounds__(256) mirror_kernel(const __grid_constant__ JoinArgs a) {
+  __shared__ float tile[32][33];
+  pdl_go();
+  pdl_wait();
+  const int b = blockIdx.x, r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+  int i = int((sqrtf(8.f * float(b) + 1.f) - 1.f) * 0.5f);
+  if (i * (i + 1) / 2 > b) --i;
+  if ((i + 1) * (i + 2) / 2 <= b) ++i;
+  const int r0 = i * 32, c0 = (b - i * (i + 1) / 2) * 32;
+  auto out = [&](long long row, int col, float* v) {
+    if (row >= a.N || col >= a.N) return;
+    float4* q = reinterpret_cast<float4*>(a.f32 + row * a.ld32 + col);
+    if (POLY) {
+      const float4 f = *q;
+      const float A[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = fmaf(kC, v[k], kB * A[k]) + (row == col + k ? kA : 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k >= a.N) v[k] = 0.f;
+    if (!POLY) *q = make_float4(v[0], v[1], v[2], v[3]);
+    put_terms(a.terms + row * a.ldt + col, a.tplane, v, a.two);
+  };
+  float v[4] = {};
+  if (r0 + r < a.N && c0 + c < a.N) {
+    const float* p = a.part + (long long)(r0 + r) * a.ldp + c0 + c;
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) {
+      const float4 f = *reinterpret_cast<const float4*>(p + z * a.plane);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k];
+  out(r0 + r, c0 + c, v);
+  __syncthreads();
+  if (r0 == c0) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = tile[c + k][r];
+  out(c0 + r, r0 + c, v);
+}
+
 struct MuonLayout {
   size_t x, x1, a_terms, b_terms, a, u, squares, part, total;
   long long ldx, lda, R, C, n;
@@ -224,12 +274,12 @@ MuonLayout muon_layout(long long R, long long C) {
     o += align256(bytes);
     return here;
   };
-  auto part_of = [](size_t outputs, long long K) {
-    const size_t all = outputs * 4 * kMaxSplits, may = all < kPartBytes ? all : kPartBytes;
+  auto part_of = [](size_t outputs, long long K, size_t room) {
+    const size_t all = outputs * 4 * kMaxSplits, may = all < room ? all : room;
     const size_t least = outputs * 4 * size_t(least_splits_two((K + 63) / 64));
     return may > least ? may : least;
   };
-  const size_t px = part_of(size_t(R) * w.ldx, w.n), pa = part_of(size_t(w.n) * w.lda, R > C ? R : C);
+  const size_t px = part_of(size_t(R) * w.ldx, w.n, kPartBytes), pa = part_of(size_t(w.n) * w.lda, R > C ? R : C, kTriBytes);
   w.x = take(size_t(R) * w.ldx * 6);
   w.x1 = take(size_t(R) * w.ldx * 6);
   w.a_terms = take(size_t(w.n) * w.lda * 6);
@@ -296,7 +346,12 @@ bool split_product(const Call& c, Product p, JoinArgs j) {
   j.N = o.N;
   j.n4 = int(o.ldo / 4);
   j.two = c.two;
-  return pdl_launch(join_kernel<MODE, TW>, dim3(blocks_for((long long)j.M * j.n4)), 256, c.s, j);
+  if constexpr (MODE >= kMirror) {
+    const long long b = (j.N + 31) / 32;
+    return pdl_launch(mirror_kernel<MODE == kMirrorPoly>, dim3(unsigned(b * (b + 1) / 2)), 256, c.s, j);
+  } else {
+    return pdl_launch(join_kernel<MODE, TW>, dim3(blocks_for((long long)j.M * j.n4)), 256, c.s, j);
+  }
 }
 
 // The product to out's terms (and fp32 f32 [M][out.ld], nullable), or, with poly, those
@@ -330,6 +385,31 @@ bool terms_product(const Call& c, int major, const Operand& A, const Operand& B,
   j.ldt = out.ld;
   j.tplane = out.rows * out.ld;
   return poly ? split_product<kPoly, float>(c, q, j) : split_product<kSum, float>(c, q, j);
+}
+
+// The symmetric products: A = X X^T (or X^T X) over K terms of the sum, or the polynomial
+// in A from A A. From n = 1024 on only the tiles of the lower triangle are made, added up
+// and mirrored, the polynomial's where that is faster than its own epilogue. (A with all of
+// its tiles and with these, the call's us: fp32 1024 x 4096 460 and 421, 4096 x 4096 7337
+// and 6371; bf16 8192 x 1024 454 and 411; but fp32 512 x 256 121 and 130, bf16 20,000 x
+// 300 320 and 367, 700 x 900 172 and 175: few blocks then add up many splits.
+// The polynomial: fp32 1024 x 4096 421 and 402, 4096 x 4096 6371 and 5513.)
+constexpr long long kMirrorFrom = 1024;
+bool symmetric_product(const Call& c, int major, const Operand& X, long long K, const Operand& out, float* a32, bool poly) {
+  const long long n = out.rows;
+  if (n < kMirrorFrom) return terms_product(c, major, X, X, K, out, a32, poly);
+  double whole, parts;
+  planned(c, major, X, X, n, n, K, false, &whole);
+  Product p = planned(c, major, X, X, n, n, K, true, &parts);
+  const double time = plan_tri(p, n, (K + 63) / 64, kTriBytes);
+  if (poly && whole <= time) return terms_product(c, major, X, X, K, out, a32, poly);
+  JoinArgs j{};
+  j.f32 = a32;
+  j.ld32 = out.ld;
+  j.terms = out.p;
+  j.ldt = out.ld;
+  j.tplane = n * out.ld;
+  return poly ? split_product<kMirrorPoly, float>(c, p, j) : split_product<kMirror, float>(c, p, j);
 }
 
 struct Step {
@@ -370,8 +450,7 @@ bool muon(const Step& q, long long R, long long C, uint8_t* ws, int* status, cud
   Operand X{x, R, C, w.ldx}, Y{at_ws(w.x1), R, C, w.ldx};
   float* a32 = reinterpret_cast<float*>(ws + w.a);
   for (int i = 0; i < q.steps; ++i) {
-    if (!terms_product(c, wide ? kKK : kNN, X, X, wide ? C : R, A, a32, false) ||
-        !terms_product(c, kKK, A, A, n, B, a32, true))
+    if (!symmetric_product(c, wide ? kKK : kNN, X, wide ? C : R, A, a32, false) || !symmetric_product(c, kKK, A, n, B, a32, true))
       return false;
     const int major = wide ? kKN : kKK;
     const Operand &left = wide ? B : X, &right = wide ? X : B;

@@ -5,8 +5,9 @@ Bounds. The update's 2-norm error: each product of fp32 operands is off by a few
 singular values and on errors, so the errors of five steps add up to at most
 3.44 + ... + 3.44^5 < 700 times 8 2^-24 (its three products and roundings) of the
 starting norm 1, against an update of norm near sqrt(n) (rank n), or near sqrt(r)
-for a gradient of rank r: 700 * 8 * 2^-24 = 3.4e-4 of sqrt(n or r). W is then
-rounded: half a step of its value. Momentum: two roundings."""
+for a gradient of rank r: 700 * 8 * 2^-24 = 3.4e-4 of sqrt(n or r). (For a bf16 W,
+X has 17 bits: at most 5e-5 of its norm off where it was measured, so the bound is
+kept.) W is then rounded: half a step of its value. Momentum: two roundings."""
 import pytest
 import torch
 
@@ -61,6 +62,16 @@ def test_muon(r, c, wt, gt):
     d = case(r + c, wt, gt, r, c)
     W, m = step(d)
     check(d, W, m)
+
+
+@pytest.mark.parametrize("r,c", [(1024, 1024), (1025, 1101), (1030, 4098), (5000, 1027), (1153, 1409), (2300, 2310)])
+@pytest.mark.parametrize("wt", [F32, BF16])
+def test_symmetric_products_by_half_of_their_tiles(r, c, wt):
+    d = case(r * 3 + c, wt, F32, r, c)
+    W, m = step(d)
+    check(d, W, m)
+    V, n = step(d)
+    assert torch.equal(W, V) and torch.equal(m, n)
 
 
 @pytest.mark.parametrize("kw", [dict(nesterov=False), dict(steps=1), dict(steps=9), dict(mu=0.0), dict(lr=0.5, weight_decay=0.1),
