@@ -354,6 +354,13 @@ bool split_product(const Call& c, Product p, JoinArgs j) {
   }
 }
 
+// Up to this size of the output three terms are written faster by the second kernel than
+// by a product's epilogue, one item of a warp after the other, by 3 us or so. (Calls of
+// 64 x 64 88 and 73 us, 256 x 256 139 and 117, 300 x 900 153 and 136; but if larger outputs
+// are split too, 8192 x 512 285 and 308, 20,000 x 300 411 and 431; in two terms 64 x 64 62
+// and 66.)
+constexpr long long kSmallOutput = 300000;
+
 // The product to out's terms (and fp32 f32 [M][out.ld], nullable), or, with poly, those
 // of the polynomial with A = f32.
 bool terms_product(const Call& c, int major, const Operand& A, const Operand& B, long long K, const Operand& out, float* f32,
@@ -361,7 +368,8 @@ bool terms_product(const Call& c, int major, const Operand& A, const Operand& B,
   double whole, parts;
   Product p = planned(c, major, A, B, out.rows, out.cols, K, false, &whole);
   const Product q = planned(c, major, A, B, out.rows, out.cols, K, true, &parts);
-  if (whole <= parts && (!c.two || least_splits_two((K + 63) / 64) == 1)) {
+  const double ahead = !c.two && out.rows * out.cols <= kSmallOutput ? 3 : 0;
+  if (whole <= parts - ahead && (!c.two || least_splits_two((K + 63) / 64) == 1)) {
     Job& o = p.a.job[0];
     p.epi = poly ? kEpiPoly : kEpiTerms;
     o.out = out.p;
