@@ -53,14 +53,22 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   if (row < a.M) {
     const long long group = row / a.tile_rows;
     const int first = int(group * a.nt % a.lanes);  // the lane of the group's first N tile
-    for (int k = slice; k < a.lanes * a.parts; k += slices) {
-      int lane = k / a.parts - first;
-      if (lane < 0) lane += a.lanes;
-      if (lane >= a.nt) continue;
-      const float2 p = __ldg(a.stat + (long long)k * a.M + row);
-      const float now = fmaxf(m, p.x);
-      s = s * exp2_fast(m - now) + p.y * exp2_fast(p.x - now);
-      m = now;
+    for (int k0 = slice; k0 < a.lanes * a.parts; k0 += 4 * slices) {
+      float2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u * slices;
+        int lane = k / a.parts - first;
+        if (lane < 0) lane += a.lanes;
+        p[u] = make_float2(-kFar, 0.f);
+        if (k < a.lanes * a.parts && lane < a.nt) p[u] = __ldg(a.stat + (long long)k * a.M + row);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float now = fmaxf(m, p[u].x);
+        s = s * exp2_fast(m - now) + p[u].y * exp2_fast(p[u].x - now);
+        m = now;
+      }
     }
   }
   part[threadIdx.x] = make_float2(m, s);
@@ -338,7 +346,7 @@ bool together(long long M, long long N, long long K, bool f32) {
 
 bool merge(MergeArgs g, cudaStream_t s) {
   while (g.rows > 1 && g.rows / 2 >= g.M) g.rows /= 2;
-  while (g.rows > 8 && (g.M + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
+  while (g.rows > 4 && (g.M + g.rows - 1) / g.rows < 2 * kSms) g.rows /= 2;
   return pdl_launch(merge_kernel, dim3(unsigned((g.M + g.rows - 1) / g.rows)), kMerge, s, g);
 }
 
