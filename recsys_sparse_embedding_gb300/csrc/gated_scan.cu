@@ -72,7 +72,7 @@ struct Args {
   const uint8_t* mark;        // per row: 1 a sequence's first, 2 its last
   const int *first, *last;    // the sequence of such a row (other entries hold nothing)
   int T, D, L;
-  int tiles, log_ct;
+  int tiles;
   int chain;  // whether a sequence may go on from chunk to chunk
   uint32_t* ticket;           // one less than the next item
   unsigned long long* pairs;  // [chunks][tiles][4 CT]
@@ -192,7 +192,7 @@ struct Shared {
   static constexpr int kBytes = kData + 8 * kThreads;
 };
 
-template <class T, bool REV, bool VEC>
+template <class T, bool REV, bool VEC, int LOG_CT>
 __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __grid_constant__ Args a) {
   using S = Shared<T, REV>;
   constexpr int NT = S::NT, NA = S::NA;
@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) scan_kernel(const __
   __shared__ float s_carry[kMostWidth];
   __shared__ int s_comes, s_ticket;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int CT = 1 << a.log_ct, ct = tid & (CT - 1), slice = tid >> a.log_ct, C = (kThreads >> a.log_ct) * NT, W = 4 * CT;
-  const int log_group = 6 - a.log_ct;  // chunks of a group: a pair per thread
+  constexpr int CT = 1 << LOG_CT, C = (kThreads >> LOG_CT) * NT, W = 4 * CT;
+  constexpr int log_group = 6 - LOG_CT;  // chunks of a group: a pair per thread
+  const int ct = tid & (CT - 1), slice = tid >> LOG_CT;
   pdl_go();
   pdl_wait();
   const int total = a.total ? *a.total : a.T, chunks = (total + C - 1) / C;
@@ -728,10 +729,10 @@ size_t ws_bytes_of(int64_t T, int32_t B, int32_t D) {
   return most + 256;
 }
 
-template <class T, bool REV, bool VEC>
+template <class T, bool REV, bool VEC, int LOG_CT>
 bool launch(const Args& a, long long items, cudaStream_t s) {
   using S = Shared<T, REV>;
-  auto* kernel = scan_kernel<T, REV, VEC>;
+  auto* kernel = scan_kernel<T, REV, VEC, LOG_CT>;
   static std::atomic<int> most[64];  // (host threads may race on it: each computes the same value)
   int dev = 0;
   if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return false;
@@ -771,7 +772,6 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
   Plan p = plan(a.T, B, a.D, nt, 3);
   if (pick_ct(p, B, size_t(a.T) * a.D * es * (REV ? 6 : 3)) == 2) p = plan(a.T, B, a.D, nt, 2);
   a.tiles = p.tiles;
-  a.log_ct = p.log_ct;
   a.L = a.T / B;
   a.ticket = reinterpret_cast<uint32_t*>(ws + p.sync);
   int* total = reinterpret_cast<int*>(ws + p.sync) + 32;
@@ -800,9 +800,13 @@ int run(Args a, int B, int32_t dtype, const int32_t* lengths, uint8_t* ws, cudaS
   }
   if (a.T == 0) return DSF_OK;
   const long long items = p.chunks * p.tiles;
-  const bool ok = dtype == DSF_F32 ? (vec ? launch<float, REV, true>(a, items, s) : launch<float, REV, false>(a, items, s))
-                                   : (vec ? launch<__nv_bfloat16, REV, true>(a, items, s)
-                                          : launch<__nv_bfloat16, REV, false>(a, items, s));
+  auto any = [&](auto type, auto vectors) {
+    using T = decltype(type);
+    constexpr bool VEC = decltype(vectors)::value;
+    return p.log_ct == 3 ? launch<T, REV, VEC, 3>(a, items, s) : launch<T, REV, VEC, 2>(a, items, s);
+  };
+  const bool ok = dtype == DSF_F32 ? (vec ? any(float(), std::true_type{}) : any(float(), std::false_type{}))
+                                   : (vec ? any(__nv_bfloat16(), std::true_type{}) : any(__nv_bfloat16(), std::false_type{}));
   return ok ? DSF_OK : DSF_ECUDA;
 }
 
