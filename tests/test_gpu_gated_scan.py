@@ -145,6 +145,14 @@ def test_bad_lengths(lengths, T, cut, flag):
     check(v, cut, o)
 
 
+@pytest.mark.parametrize("D,lengths", [(4, [140000, 3]), (64, [0, 131073]), (36, [1] * 1500 + [270000])], ids=["4", "64", "36"])
+def test_more_rows_than_one_block_marks(D, lengths):
+    v = inputs(9, F32, sum(lengths), D, len(lengths))
+    o, status = run(v, lengths, len(lengths))
+    assert status == 0
+    check(v, lengths, o)
+
+
 @pytest.mark.parametrize("nb,mean", [(65536, 0.8), (65537, 0.8), (200003, 0.6)])
 def test_very_many_sequences(nb, mean):
     """Most of them empty; one of a negative length among the last."""

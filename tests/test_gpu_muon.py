@@ -64,7 +64,7 @@ def test_muon(r, c, wt, gt):
     check(d, W, m)
 
 
-@pytest.mark.parametrize("r,c", [(1024, 1024), (1025, 1101), (1030, 4098), (5000, 1027), (1153, 1409), (2300, 2310)])
+@pytest.mark.parametrize("r,c", [(1024, 1024), (1025, 1101), (1030, 4098), (5000, 1027), (1153, 1409), (2300, 2310), (40001, 1030)])
 @pytest.mark.parametrize("wt", [F32, BF16])
 def test_symmetric_products_by_half_of_their_tiles(r, c, wt):
     d = case(r * 3 + c, wt, F32, r, c)
