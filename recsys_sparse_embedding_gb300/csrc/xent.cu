@@ -16,6 +16,8 @@
 // gradients, 5.9 ms; of 64 MB 6.7, of 96 MB 6.5, of 1 GB 5.7.)
 // Where x and W are narrow, passes that keep no dz at all take over (xent_pass.cuh),
 // and few_kernel has the sums of a step of serving, 4 rows at most.
+#include <climits>
+
 #include "dense_host.cuh"
 #include "xent_pass.cuh"
 
@@ -245,12 +247,17 @@ bool few(const dsf_dense* l, long long M) {
   const int bytes = l->K * esize(l->dtype);
   return M <= 4 && bytes % 16 == 0 && bytes <= 512;
 }
-// Chunks of the columns in which the sums and dx are taken: a few units for each SM,
-// and at most 512 tiles in one.
-constexpr long long kDxUnits = 4 * kSms;
+// Chunks of the columns in which the sums and dx are taken: at most 512 tiles in one, and
+// units whose whole rounds over the SMs take the least time (a unit costs 6 tiles more).
+constexpr long long kDxUnits = 8 * kSms;
 int dx_chunks(long long M, long long V) {
   const long long mt = (M + 127) / 128, ct = (V + 127) / 128, least = (ct + 511) / 512, want = (kDxUnits + mt - 1) / mt;
-  return int(want > least ? (want < ct ? want : ct) : least);
+  long long best = least, time = LLONG_MAX;
+  for (long long c = least; c <= (want < ct ? want : ct) || c == least; ++c) {
+    const long long per = (ct + c - 1) / c, units = mt * ((ct + per - 1) / per), t = (units + kSms - 1) / kSms * (per + 6);
+    if (t < time) best = c, time = t;
+  }
+  return int(best);
 }
 
 // Columns of a piece for M rows.

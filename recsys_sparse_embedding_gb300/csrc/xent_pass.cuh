@@ -59,16 +59,20 @@ struct PassShape {
   static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kThreads = 32 * 18;
   static constexpr int TILE = NK * 16384;
   static constexpr int COLS = 3 * 512;  // a stage's values per column
-  static constexpr int kRoom = 227 * 1024 - TILE - 512;
+  // Buffers of the block's rows: with two, a unit's are there before the one before it
+  // ends, and its streamed tiles are not held up (K > 64: the room is better spent on
+  // those).
+  static constexpr int RB = NK == 1 ? 2 : 1;
+  static constexpr int kRoom = 227 * 1024 - RB * TILE - 512;
   static constexpr int STAGES = kRoom / (TILE + COLS) < 8 ? kRoom / (TILE + COLS) : 8;
-  static constexpr int SMEM = (STAGES + 1) * TILE + STAGES * COLS + 512;
+  static constexpr int SMEM = (STAGES + RB) * TILE + STAGES * COLS + 512;
   static constexpr int NB = 3;  // S buffers
   static_assert(STAGES >= NB && NB * 128 + NK * 64 <= 512, "tiles under way; tensor memory");
   static_assert(STAGES >= 2 && SMEM > 114 * 1024, "ring; one block per SM");
 };
 
 struct PassBars {
-  uint64_t full[8], empty[8], rows_full, rows_empty, s_full[3], p_full[3], acc_full, acc_empty;
+  uint64_t full[8], empty[8], rows_full[2], rows_empty[2], s_full[3], p_full[3], acc_full, acc_empty;
   uint32_t tmem;
   int abort_;
 };
@@ -85,11 +89,11 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
     xent_pass_kernel(const __grid_constant__ PassArgs a, const __grid_constant__ CUtensorMap map_rows,
                      const __grid_constant__ CUtensorMap map_stream) {
   using S = PassShape<NK>;
-  constexpr int STAGES = S::STAGES, NB = S::NB, COLS = S::COLS;
+  constexpr int STAGES = S::STAGES, NB = S::NB, COLS = S::COLS, RB = S::RB;
   constexpr bool DW = MODE == kDw;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* s_rows = sm + STAGES * S::TILE;
-  uint8_t* s_cols = s_rows + S::TILE;
+  uint8_t* s_cols = s_rows + RB * S::TILE;
   PassBars* bars = reinterpret_cast<PassBars*>(s_cols + STAGES * COLS);
   if (smem_u32(sm) & 1023u) {  // (the swizzle atoms' alignment; every thread of the grid takes the same way)
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, DSF_FLAG_TIMEOUT);
@@ -105,8 +109,10 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->empty[i], 1);
     }
-    mbar_init(&bars->rows_full, 1);
-    mbar_init(&bars->rows_empty, 1);
+    for (int i = 0; i < RB; ++i) {
+      mbar_init(&bars->rows_full[i], 1);
+      mbar_init(&bars->rows_empty[i], 1);
+    }
     for (int i = 0; i < NB; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 8);
@@ -151,14 +157,17 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       uint32_t it = 0;
-      int i = 0;
+      int i = 0;  // (units whose rows are asked for)
       Unit t;
-      for (; ok && unit_at(i, t); ++i) {
-        if (i > 0 && !(ok = mbar_wait(&bars->rows_empty, (i - 1) & 1))) break;
-        mbar_arrive_expect_tx(&bars->rows_full, S::TILE);
+      while (ok && unit_at(i, t)) {
+        uint64_t* rows_full = &bars->rows_full[i % RB];
+        uint8_t* rows = s_rows + i % RB * S::TILE;
+        if (i >= RB && !(ok = mbar_wait(&bars->rows_empty[i % RB], (i / RB - 1) & 1))) break;
+        ++i;
+        mbar_arrive_expect_tx(rows_full, S::TILE);
 #pragma unroll
         for (int k = 0; k < NK; ++k)
-          tma_load_3d<1>(smem_u32(s_rows + k * 16384), &map_rows, k * 64, t.r0, 0, smem_u32(&bars->rows_full));
+          tma_load_3d<1>(smem_u32(rows + k * 16384), &map_rows, k * 64, t.r0, 0, smem_u32(rows_full));
         for (int j = 0; j < t.n; ++j, ++it) {
           const uint32_t st = it % STAGES, lap = it / STAGES;
           if (lap && !(ok = mbar_wait(&bars->empty[st], (lap - 1) & 1u))) break;
@@ -176,9 +185,9 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
         }
       }
       if (!ok) atomicExch(&bars->abort_, 1);
-      // the last loads have landed before the block may end (bounded; a unit that
-      // gave up while it waited for the rows' place has counted one too many)
-      if (i > 0 && ok && !mbar_wait(&bars->rows_full, (i - 1) & 1)) atomicExch(&bars->abort_, 1);
+      // the last loads have landed before the block may end (bounded)
+      for (int k = max(i - RB, 0); k < i; ++k)
+        if (!mbar_wait(&bars->rows_full[k % RB], (k / RB) & 1)) atomicExch(&bars->abort_, 1);
       for (uint32_t j = it > uint32_t(STAGES) ? it - STAGES : 0; j < it; ++j)
         if (!mbar_wait(&bars->full[j % STAGES], (j / STAGES) & 1u)) atomicExch(&bars->abort_, 1);
     }
@@ -190,7 +199,6 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
     constexpr uint32_t ID2 = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(NK * 64 >> 3) << 17) |
                              (uint32_t(128 >> 4) << 24);
     const uint32_t s0 = smem_u32(sm), acc = tbase + NB * 128;
-    const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows));
     bool ok = true;
     uint32_t it = 0;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -212,7 +220,8 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
     };
     Unit t;
     for (int i = 0; ok && unit_at(i, t); ++i) {
-      if (!wait(&bars->rows_full, uint32_t(i))) break;
+      if (!wait(&bars->rows_full[i % RB], uint32_t(i / RB))) break;
+      const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows) + i % RB * S::TILE);
       for (int j = 0; j < t.n && ok; ++j, ++it) {
         const uint32_t st = it % STAGES;
         if (!wait(&bars->full[st], it / STAGES)) break;
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
       for (int j = max(t.n - (NB - 1), 0); ok && j < t.n; ++j) second(it - (t.n - j), j == 0, i);
       if (!ok) break;
       if (ok && lead) {
-        tc_commit(&bars->rows_empty);
+        tc_commit(&bars->rows_empty[i % RB]);
         tc_commit(&bars->acc_full);
       }
     }
