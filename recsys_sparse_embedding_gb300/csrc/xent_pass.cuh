@@ -12,7 +12,8 @@
 //
 //   load warp   TMA: the block's rows once per unit, then the streamed tiles, with
 //               what the epilogue takes per column (bias, or lse, g and target)
-//   MMA warp    S of tile j, then dz of tile j - 2 times its rows
+//   MMA warps   one for S, one for dz times its rows: each waits for its own operands
+//               only (one warp for both, in turn, took 1290 cycles a tile of waiting)
 //   16 epilogue warps in two sets: even tiles and odd ones. A warp has 32 rows (a
 //               tensor-memory quarter) by 64 columns of its tiles.
 //
@@ -56,7 +57,7 @@ struct PassArgs {
 
 template <int NK>
 struct PassShape {
-  static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kThreads = 32 * 18;
+  static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kMma2 = 18, kThreads = 32 * 19;
   static constexpr int TILE = NK * 16384;
   static constexpr int COLS = 3 * 512;  // a stage's values per column
   // Buffers of the block's rows: with two, a unit's are there before the one before it
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
         if (!mbar_wait(&bars->full[j % STAGES], (j / STAGES) & 1u)) atomicExch(&bars->abort_, 1);
     }
     __syncwarp();
-  } else if (warp == S::kMma) {
-    // ------------------------------------------------ MMAs (the warp together, one lane issues)
+  } else if (warp == S::kMma || warp == S::kMma2) {
+    // ------------------------------------------------ MMAs (a warp together, one lane issues)
     const bool lead = elect_one();
     constexpr uint32_t ID1 = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     constexpr uint32_t ID2 = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(NK * 64 >> 3) << 17) |
@@ -206,28 +207,17 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
       tc_fence_after();
       return ok;
     };
-    // dz of tile t times its rows; first: of unit i
-    auto second = [&](uint32_t t, bool first, int i) {
-      if (!wait(&bars->p_full[t % NB], t / NB)) return;
-      if (MODE != kSums && first && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) return;
-      const uint32_t st = t % STAGES;
-      if (!lead) return;
-      const uint64_t db = mn_desc_128(s0 + st * S::TILE);
-#pragma unroll
-      for (uint32_t k = 0; MODE != kSums && k < 8; ++k)
-        tc_mma_f16_ts(acc, tbase + (t % NB) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, !first || k > 0);
-      tc_commit(&bars->empty[st]);
-    };
     Unit t;
     for (int i = 0; ok && unit_at(i, t); ++i) {
-      if (!wait(&bars->rows_full[i % RB], uint32_t(i / RB))) break;
-      const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows) + i % RB * S::TILE);
-      for (int j = 0; j < t.n && ok; ++j, ++it) {
-        const uint32_t st = it % STAGES;
-        if (!wait(&bars->full[st], it / STAGES)) break;
-        // (S's buffer holds dz of tile it - NB until that has been multiplied)
-        if (it >= NB && !wait(&bars->empty[(it - NB) % STAGES], (it - NB) / STAGES)) break;
-        if (lead) {
+      if (warp == S::kMma) {
+        if (!wait(&bars->rows_full[i % RB], uint32_t(i / RB))) break;
+        const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows) + i % RB * S::TILE);
+        for (int j = 0; j < t.n; ++j, ++it) {
+          const uint32_t st = it % STAGES;
+          if (!wait(&bars->full[st], it / STAGES)) break;
+          // (S's buffer holds dz of tile it - NB until that has been multiplied)
+          if (it >= NB && !wait(&bars->empty[(it - NB) % STAGES], (it - NB) / STAGES)) break;
+          if (!lead) continue;
           const uint64_t db = sw128_kmajor_desc(s0 + st * S::TILE);
 #pragma unroll
           for (uint32_t k = 0; k < 4 * NK; ++k)
@@ -235,13 +225,21 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
                           k > 0);
           tc_commit(&bars->s_full[it % NB]);
         }
-        if (j >= NB - 1) second(it - (NB - 1), j == NB - 1, i);
-      }
-      for (int j = max(t.n - (NB - 1), 0); ok && j < t.n; ++j) second(it - (t.n - j), j == 0, i);
-      if (!ok) break;
-      if (ok && lead) {
-        tc_commit(&bars->rows_empty[i % RB]);
-        tc_commit(&bars->acc_full);
+        if (ok && lead) tc_commit(&bars->rows_empty[i % RB]);
+      } else {
+        // dz of the tile times its rows
+        for (int j = 0; j < t.n; ++j, ++it) {
+          const uint32_t st = it % STAGES;
+          if (!wait(&bars->full[st], it / STAGES) || !wait(&bars->p_full[it % NB], it / NB)) break;
+          if (MODE != kSums && j == 0 && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) break;
+          if (!lead) continue;
+          const uint64_t db = mn_desc_128(s0 + st * S::TILE);
+#pragma unroll
+          for (uint32_t k = 0; MODE != kSums && k < 8; ++k)
+            tc_mma_f16_ts(acc, tbase + (it % NB) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, j > 0 || k > 0);
+          tc_commit(&bars->empty[st]);
+        }
+        if (ok && lead) tc_commit(&bars->acc_full);
       }
     }
     if (!ok && lead) atomicExch(&bars->abort_, 1);
