@@ -38,8 +38,8 @@ bool launch_pass(const PassArgs& a, const Mat& rows, const Mat& stream, cudaStre
   if (!tensor_map_3d(&mr, rows, 2, 64, 128) || !tensor_map_3d(&ms, stream, 2, 64, 128)) return false;
   const long long units = (long long)a.rt * a.chunks;
   if (units > INT32_MAX / 2) return false;
-  return pdl_launch_smem(kernel, dim3(unsigned(units < most ? units : most)), PassShape<NK>::kThreads, PassShape<NK>::SMEM, s,
-                         a, mr, ms);
+  return pdl_launch_smem(kernel, dim3(unsigned(units < most ? units : most)), PassShape<NK>::threads(MODE),
+                         PassShape<NK>::SMEM, s, a, mr, ms);
 }
 
 template <int MODE>

@@ -57,7 +57,8 @@ struct PassArgs {
 
 template <int NK>
 struct PassShape {
-  static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kMma2 = 18, kThreads = 32 * 19;
+  static constexpr int kWarps = 16, kLoad = 16, kMma = 17, kMma2 = 18;
+  static constexpr int threads(int mode) { return mode == kSums ? 32 * 18 : 32 * 19; }  // (the sums have one product)
   static constexpr int TILE = NK * 16384;
   static constexpr int COLS = 3 * 512;  // a stage's values per column
   // Buffers of the block's rows: with two, a unit's are there before the one before it
@@ -86,7 +87,7 @@ __device__ __forceinline__ uint64_t mn_desc_128(uint32_t addr) {
 }
 
 template <int MODE, int NK>
-__global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
+__global__ void __launch_bounds__(PassShape<NK>::threads(MODE), 1)
     xent_pass_kernel(const __grid_constant__ PassArgs a, const __grid_constant__ CUtensorMap map_rows,
                      const __grid_constant__ CUtensorMap map_stream) {
   using S = PassShape<NK>;
@@ -207,9 +208,12 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
       tc_fence_after();
       return ok;
     };
+    auto done = [&](uint32_t t) {  // (the sums) tile t has been read
+      if (wait(&bars->p_full[t % NB], t / NB) && lead) tc_commit(&bars->empty[t % STAGES]);
+    };
     Unit t;
     for (int i = 0; ok && unit_at(i, t); ++i) {
-      if (warp == S::kMma) {
+      if (MODE == kSums || warp == S::kMma) {
         if (!wait(&bars->rows_full[i % RB], uint32_t(i / RB))) break;
         const uint64_t da = sw128_kmajor_desc(smem_u32(s_rows) + i % RB * S::TILE);
         for (int j = 0; j < t.n; ++j, ++it) {
@@ -217,25 +221,29 @@ __global__ void __launch_bounds__(PassShape<NK>::kThreads, 1)
           if (!wait(&bars->full[st], it / STAGES)) break;
           // (S's buffer holds dz of tile it - NB until that has been multiplied)
           if (it >= NB && !wait(&bars->empty[(it - NB) % STAGES], (it - NB) / STAGES)) break;
-          if (!lead) continue;
-          const uint64_t db = sw128_kmajor_desc(s0 + st * S::TILE);
+          if (lead) {
+            const uint64_t db = sw128_kmajor_desc(s0 + st * S::TILE);
 #pragma unroll
-          for (uint32_t k = 0; k < 4 * NK; ++k)
-            mma<1, kBf16>(tbase + (it % NB) * 128, da + (k >> 2) * 1024 + (k & 3) * 2, db + (k >> 2) * 1024 + (k & 3) * 2, ID1,
-                          k > 0);
-          tc_commit(&bars->s_full[it % NB]);
+            for (uint32_t k = 0; k < 4 * NK; ++k)
+              mma<1, kBf16>(tbase + (it % NB) * 128, da + (k >> 2) * 1024 + (k & 3) * 2,
+                            db + (k >> 2) * 1024 + (k & 3) * 2, ID1, k > 0);
+            tc_commit(&bars->s_full[it % NB]);
+          }
+          if (MODE == kSums && j >= NB - 1) done(it - (NB - 1));
         }
+        if (MODE == kSums)
+          for (int j = max(t.n - (NB - 1), 0); ok && j < t.n; ++j) done(it - (t.n - j));
         if (ok && lead) tc_commit(&bars->rows_empty[i % RB]);
       } else {
         // dz of the tile times its rows
         for (int j = 0; j < t.n; ++j, ++it) {
           const uint32_t st = it % STAGES;
           if (!wait(&bars->full[st], it / STAGES) || !wait(&bars->p_full[it % NB], it / NB)) break;
-          if (MODE != kSums && j == 0 && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) break;
+          if (j == 0 && i > 0 && !wait(&bars->acc_empty, uint32_t(i - 1))) break;
           if (!lead) continue;
           const uint64_t db = mn_desc_128(s0 + st * S::TILE);
 #pragma unroll
-          for (uint32_t k = 0; MODE != kSums && k < 8; ++k)
+          for (uint32_t k = 0; k < 8; ++k)
             tc_mma_f16_ts(acc, tbase + (it % NB) * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * 128, ID2, j > 0 || k > 0);
           tc_commit(&bars->empty[st]);
         }
