@@ -234,13 +234,15 @@ __global__ void __launch_bounds__(256) db_kernel(const float* part, int V, float
 
 // ---------------------------------------------------------------- layout
 // Whether the rows' sums, or the gradients, are taken in one pass each (xent_pass.cuh):
-// where there are 1e8 logits and, for each 64 of K, two tiles of rows. (The gradients
-// both ways, us, at K = 64: 512 rows over 100,000 columns 85 and 80, 1024 120 and 142,
-// 128 over 846,812 248 and 220, 256 286 and 320; at K = 128: 256 rows over 846,812 420
-// and 364, 2048 over 131,072 278 and 353. The sums alike: 1024 rows over 100,000 of 64 42
-// and 45, of 512 33 and 29, 128 over 846,812 103 and 80, 256 106 and 109.)
-bool narrow(const dsf_dense* l, long long M) {
-  return l->dtype == DSF_BF16 && l->K <= 128 && M <= 65536 && M > (l->K <= 64 ? 128 : 384) && double(M) * l->R >= 1e8;
+// from 4e7 logits on, where the catalogue gives the SMs work (a unit of dW's pass is 128 of
+// its rows); the sums of 1e8 in any case. (The gradients both ways, us, at K = 64: 512 rows
+// over 100,000 columns 65 and 82, 2000 over 20,000 61 and 70, 64 over 846,812 172 and 199,
+// 8192 over 8192 85 and 85, 20,000 over 6000 182 and 155; at K = 128: 128 rows over
+// 1,000,000 295 and 320, 512 over 100,000 81 and 94. The sums of those: 44 and 49, 42 and
+// 46, 68 and 72, 53 and 61, 77 and 92; 81 and 82, 46 and 48.)
+bool narrow(const dsf_dense* l, long long M, bool backward) {
+  const double logits = double(M) * l->R;
+  return l->dtype == DSF_BF16 && l->K <= 128 && M <= 65536 && ((logits >= 1e8 && !backward) || (l->R >= 8192 && logits >= 4e7));
 }
 // Whether the sums are few_kernel's: of up to 4 rows, whole vectors, at most 32 of them.
 bool few(const dsf_dense* l, long long M) {
@@ -386,7 +388,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
                                   : pdl_launch(few_kernel<__nv_bfloat16, 4>, dim3(unsigned(blocks)), 256, s, a));
     return ok && merge(MergeArgs{stat, zt, target, loss, lse, M, 1, blocks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
   }
-  if (narrow(l, M)) {
+  if (narrow(l, M, false)) {
     PassArgs a{};
     const float* bias = nullptr;
     if (!lay_bias(l, ws + w.bias, &bias, s)) return false;
@@ -436,7 +438,7 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   const LayJob jobs[2] = {{x, ws + w.xp, ldx, M, w.kp, K, target, l->R},
                           {l->W, ws + w.wp, l->ldw, l->R, w.kp, K, nullptr, 0}};
   if (!lay(l->dtype, jobs, lo ? 2 : 1, s)) return false;
-  const bool pass = narrow(l, M);
+  const bool pass = narrow(l, M, true);
   const long long Mp = up(M, 128);
   float* l_of = reinterpret_cast<float*>(ws + w.rows);
   float2* rows = pass ? nullptr : reinterpret_cast<float2*>(l_of);
@@ -523,7 +525,8 @@ bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long*
     if (!run_xent_product(p, s)) return false;
     if (db && !colsum(sums, (M + 31) / 32, int(n), db + v, s)) return false;
     void* dWv = dW ? static_cast<uint8_t*>(dW) + v * K * es : nullptr;
-    if (one && dx && dWv && !together(M, n, K, f32)) {
+    // (apart, too, where larger calls take a pass each: no output then depends on which are asked for)
+    if (one && dx && dWv && (narrow(l, M, false) || !together(M, n, K, f32))) {
       if (!grad_products(c, dz, nullptr, 0, dWv)) return false;
       return grad_products(c, dz, dx, lddx, nullptr);
     }
