@@ -19,12 +19,11 @@
 //
 // Tensor memory: three S buffers of 128 columns, so that a set finds its next tile's
 // S there when it has done one; then the output's columns. What binds (8192 rows and
-// 131,072 columns of 64; the backward's passes 415 us each, the sums' 320): the
-// epilogue and the second product, whose operand comes from tensor memory, take turns
-// there. Without the second product a tile takes 0.67 us, with it 0.96; dz in buffers
-// of its own (1.00), in shared memory (1.03), 24 epilogue warps (0.96), and the
-// exponentials (none: 0.95) change little. At K = 256 dz in memory is faster (both
-// gradients 1.6 ms against 1.9), at 128 slower (1.42 against 0.98).
+// 131,072 columns of 64: 294 us for the sums, 575 for both gradients, 1290 cycles a
+// tile): the exponentials, 1024 cycles of the special functions. Slower or no faster:
+// dz in buffers of its own in tensor memory or in shared memory, S given back as soon
+// as it is in registers (they spill), 24 epilogue warps, four S buffers for the sums.
+// At K = 256 dz in memory was faster (both gradients 1.6 ms against 1.9).
 // Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
 // columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
 #pragma once
