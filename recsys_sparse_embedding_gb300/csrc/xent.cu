@@ -251,11 +251,13 @@ bool few(const dsf_dense* l, long long M) {
 }
 // Chunks of the columns in which the sums and dx are taken: at most 512 tiles in one, and
 // units whose whole rounds over the SMs take the least time (a unit costs 6 tiles more).
-constexpr long long kDxUnits = 8 * kSms;
+constexpr int kDxRounds = 8;
+constexpr long long kDxUnits = kDxRounds * kSms;
 int dx_chunks(long long M, long long V) {
-  const long long mt = (M + 127) / 128, ct = (V + 127) / 128, least = (ct + 511) / 512, want = (kDxUnits + mt - 1) / mt;
+  const long long mt = (M + 127) / 128, ct = (V + 127) / 128, least = (ct + 511) / 512;
   long long best = least, time = LLONG_MAX;
-  for (long long c = least; c <= (want < ct ? want : ct) || c == least; ++c) {
+  for (int r = 0; r <= kDxRounds; ++r) {  // (the most chunks in r rounds; the fewest there can be)
+    const long long most = r * kSms / mt, c = r == 0 || most < least ? least : (most < ct ? most : ct);
     const long long per = (ct + c - 1) / c, units = mt * ((ct + per - 1) / per), t = (units + kSms - 1) / kSms * (per + 6);
     if (t < time) best = c, time = t;
   }
