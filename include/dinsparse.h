@@ -575,7 +575,7 @@ int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int6
  * of x and W) are the dense layer's above; the logits and their softmax are
  * fp32 (the backward's exp(z - lse) carries lse's rounding, 2^-24 |lse|: logits
  * near 0 are the most exact). The logits are never kept: the forward's workspace
- * holds 1.2 KB a row (and 40 MB more at most), the backward's a piece of their
+ * holds 1.2 KB a row (and 44 MB more at most), the backward's a piece of their
  * gradients (256 MB, or M x 256 of them) and partial sums of dx in fp32 (at most
  * 32 of them, or 110 MB), beside operands that are laid out.
  * Equal calls give equal bits. */

@@ -136,7 +136,7 @@ struct TcArgs {
   float* part;  // kEpiDz, kEpiXent: column sums of 32 rows each, [ceil(M / 32)][halves * N] (nullable)
   const long long* target;  // kEpiLse, kEpiXent: per row the target's column in all of W (outside: none)
   int v0;                   // the first column here, of them
-  float2* stat;             // kEpiLse: [lane * warps per row + warp][M] (reference, sum)
+  float2* stat;             // kEpiLse: [slot * warps per row + warp][M] (reference, sum); a lane's slot: its first N tile of the row
   // kEpiLse, kEpiXent: gm neighbouring M tiles are worked on together, each by
   // `lanes` clusters that share out its N tiles; so a cluster stays with its rows,
   // and a tile of B serves gm tiles of A from L2
@@ -772,13 +772,13 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     // a cross entropy's rows: the target's column (or one that no item has), lse and
     // g; kEpiLse: the reference (in units of log 2) and sum over the warp's items so
     // far, written when the warp goes on to other rows
-    int stat_m0 = -1, tgt = -1;
+    int stat_m0 = -1, stat_slot = 0, tgt = -1;
     float2 of_row = make_float2(0.f, 0.f);
     bool fresh = true;
     float top = -kFar, total = 0.f;
     auto put_stat = [&]() {
       const int r = stat_m0 + 32 * q + lane;
-      if (stat_m0 >= 0 && r < job0.M) a.stat[((long long)lane_of * GR + grp) * job0.M + r] = make_float2(top, total);
+      if (stat_m0 >= 0 && r < job0.M) a.stat[((long long)stat_slot * GR + grp) * job0.M + r] = make_float2(top, total);
     };
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const Job& jb = a.job[DUAL ? t.job : 0];
@@ -787,6 +787,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
       if (XENT && t.m0 != stat_m0) {  // other rows: their targets, lse and g
         if (EPI == kEpiLse) put_stat();
         stat_m0 = t.m0;
+        stat_slot = t.n0 / ON;
         fresh = true;
         top = -kFar, total = 0.f;
         const long long id = row < jb.M ? __ldg(a.target + row) : -1, d = id - a.v0;
@@ -1133,7 +1134,7 @@ struct Product {
   bool gated, f32, two;  // f32: fp32 operands (in three terms); two: in two terms
   int epi, cfg;     // cfg: 0: CG 2, 1: CG 1 x BN 128, 2: CG 1 x BN 64, 3 (bf16 dz in runs): CG 2 x BN 128
   long long weight[2];  // kDual: a unit's time, by job
-  int* lse_grid;        // kEpiLse: where the launch writes the lanes and the M tiles of a group
+  int* lse_slots;       // kEpiLse: where the launch writes how many slots a row has
 };
 
 bool tensor_map_3d(CUtensorMap* m, const Mat& x, int esize, int box_cols, int box_rows);
@@ -1178,8 +1179,10 @@ inline Deal deal(const TcArgs& a, const long long (&w)[2], long long C) {
   return best;
 }
 
-// A cross entropy's groups: of 4 M tiles, or fewer where those would leave clusters without
-// work (a tile of B is read from memory once per group: more than 2 are enough).
+// A cross entropy's groups: of 4 M tiles, or fewer where those would leave more clusters
+// without work, by 3 of 100 at least per choice (a tile of B is read from memory once per
+// group: more than 2 are enough). So single tiles may be taken up to 93 (of 96 in groups of
+// 4, 3 of 100 are none), groups of 4 are from there on.
 inline int lse_group(long long mt, long long clusters) {
   int best = 1;
   double most = 0;
@@ -1189,6 +1192,15 @@ inline int lse_group(long long mt, long long clusters) {
     if (e > most + 0.03) best = gm, most = e;
   }
   return best;
+}
+
+// Slots times rows that M rows' pairs have room for (growing with M): a slot for every
+// cluster up to those 93 tiles, for a quarter of them beyond. A launch has no more lanes
+// than slots (or than N tiles: a lane without one has no pair).
+constexpr long long kLseClusters = 152, kLseSingle = 93 * 128;
+inline long long lse_room(long long M) {
+  const long long m = M < kLseSingle ? M : kLseSingle;
+  return m * kLseClusters + (M - m) * (kLseClusters / 4);
 }
 
 template <int CG, int BN, int MAJOR, int KIND, bool GATED, int EPI, bool F32, bool TWO = false>
@@ -1250,11 +1262,13 @@ bool launch_tc(const Product& p, cudaStream_t s) {
     const Job& o = a.job[0];
     a.gm = lse_group(o.mt, g / CG);
     a.lanes = int(g / CG / a.gm);
+    const long long room = lse_room(o.M) / o.M;  // (what binds only where the device has more clusters)
+    if (EPI == kEpiLse && o.nt > room && a.lanes > room) a.lanes = int(room);
     a.by_nt = make_div(uint32_t(o.nt));
     const long long positions = (long long)((o.mt + a.gm - 1) / a.gm) * o.nt;
     if (positions + a.lanes > INT32_MAX) return false;
     a.positions = int(positions);
-    if (EPI == kEpiLse) p.lse_grid[0] = a.lanes, p.lse_grid[1] = a.gm;
+    if (EPI == kEpiLse) *p.lse_slots = o.nt < a.lanes ? o.nt : a.lanes;
   }
   cfg.gridDim = dim3(unsigned(g));
   constexpr int es = KIND == kBf16 ? 2 : 1;

@@ -30,9 +30,8 @@ constexpr long long kMaxLogits = 1LL << 44;  // (2^30 tiles)
 constexpr size_t kPieceBytes = 256u << 20;  // dz of a piece
 
 // ---------------------------------------------------------------- small kernels
-// A row's pairs [lanes * parts][M] to lse and loss: of the lanes that had one
-// of its tiles (dense_tc.cuh). `rows` (a power of two up to 32) neighbouring rows
-// per block; the other threads share out the pairs.
+// A row's pairs [pairs][M] to lse and loss. `rows` (a power of two up to 32)
+// neighbouring rows per block; the other threads share out the pairs.
 constexpr int kWarpsPerRow = 4;
 struct MergeArgs {
   const float2* stat;
@@ -40,7 +39,7 @@ struct MergeArgs {
   const long long* target;
   float *loss, *lse;
   long long M;
-  int parts, lanes, nt, tile_rows, rows;  // tile_rows: of a group of M tiles
+  int pairs, rows;
   long long V;
   int* status;
 };
@@ -53,17 +52,13 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   const long long row = (long long)blockIdx.x * a.rows + r;
   float m = -kFar, s = 0.f;
   if (row < a.M) {
-    const long long group = row / a.tile_rows;
-    const int first = int(group * a.nt % a.lanes);  // the lane of the group's first N tile
-    for (int k0 = slice; k0 < a.lanes * a.parts; k0 += 4 * slices) {
+    for (int k0 = slice; k0 < a.pairs; k0 += 4 * slices) {
       float2 p[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int k = k0 + u * slices;
-        int lane = k / a.parts - first;
-        if (lane < 0) lane += a.lanes;
         p[u] = make_float2(-kFar, 0.f);
-        if (k < a.lanes * a.parts && lane < a.nt) p[u] = __ldg(a.stat + (long long)k * a.M + row);
+        if (k < a.pairs) p[u] = __ldg(a.stat + (long long)k * a.M + row);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -108,6 +103,7 @@ struct FewArgs {
   int M, V, nv, log_g;  // nv: vectors of a row
 };
 constexpr int kFewBlocks = 4 * kSms;
+static_assert(kFewBlocks <= kLseClusters * kWarpsPerRow, "lse_room");
 template <class T, int MT>
 __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int E = 16 / int(sizeof(T)), U = 4;
@@ -289,9 +285,7 @@ XLayout xent_layout(const dsf_dense* l, long long M, bool backward) {
   const bool lo = laid_out(l->dtype, l->K);
   w.xp = take(lo || backward ? terms * m * w.kp * 2 : 0);
   w.wp = take(lo ? terms * size_t(l->R) * w.kp * 2 : 0);
-  // (lanes: as many as clusters; a quarter of those from 32 M tiles on, in any of
-  // lse_group's choices)
-  size_t stat = (m * (kSms / 4) + (m < 8192 ? m : 8192) * kSms) * kWarpsPerRow * 8;
+  size_t stat = size_t(lse_room(M)) * kWarpsPerRow * 8;  // (few_kernel's blocks: as many pairs of up to 4 rows)
   const bool by_pass = l->dtype == DSF_BF16 && l->K <= 128;  // (for some number of rows)
   const size_t mt = (m + 127) / 128, pieces = 128 * (size_t(kDxUnits) + mt);  // rows times chunks, at most these or 16 times the rows
   if (by_pass && stat < (pieces > m * 16 ? pieces : m * 16) * kWarpsPerRow * 8)
@@ -388,7 +382,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
                                   : pdl_launch(few_kernel<float, 4>, dim3(unsigned(blocks)), 256, s, a))
                         : (M == 1 ? pdl_launch(few_kernel<__nv_bfloat16, 1>, dim3(unsigned(blocks)), 256, s, a)
                                   : pdl_launch(few_kernel<__nv_bfloat16, 4>, dim3(unsigned(blocks)), 256, s, a));
-    return ok && merge(MergeArgs{stat, zt, target, loss, lse, M, 1, blocks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
+    return ok && merge(MergeArgs{stat, zt, target, loss, lse, M, blocks, 32, l->R, status}, s);
   }
   if (narrow(l, M, false)) {
     PassArgs a{};
@@ -407,7 +401,7 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
     const Mat X = lo ? Mat{ws + w.xp, M, l->K, w.kp, 1, 0} : Mat{x, M, l->K, ldx, 1, 0},
               W = lo ? Mat{ws + w.wp, l->R, l->K, w.kp, 1, 0} : Mat{l->W, l->R, l->K, l->ldw, 1, 0};
     return run_xent_pass(kSums, a, X, W, s) &&
-           merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow, a.chunks, INT32_MAX, INT32_MAX, 32, l->R, status}, s);
+           merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow * a.chunks, 32, l->R, status}, s);
   }
   Product p{};
   p.A = lo ? Mat{ws + w.xp, M, l->K, w.kp, terms, M * w.kp} : Mat{x, M, l->K, ldx, 1, 0};
@@ -422,11 +416,10 @@ bool xent_fwd(const dsf_dense* l, const void* x, long long ldx, const long long*
   p.a.stat = stat;
   p.a.zt = zt;
   p.a.status = status;
-  int grid[2] = {};
-  p.lse_grid = grid;
+  int slots = 0;
+  p.lse_slots = &slots;
   if (!run_xent_product(p, s)) return false;
-  return merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow, grid[0], p.a.job[0].nt, grid[1] * cfg_rows(p.cfg), 32, l->R, status},
-               s);
+  return merge(MergeArgs{stat, zt, target, loss, lse, M, kWarpsPerRow * slots, 32, l->R, status}, s);
 }
 
 bool xent_bwd(const dsf_dense* l, const void* x, long long ldx, const long long* target, const float* lse,
