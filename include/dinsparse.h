@@ -606,9 +606,9 @@ int ctr_softmax_xent_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx,
  * a bf16 W is rounded to nearest even); momentum_dev is fp32 [R, C], contiguous.
  * W and momentum are updated in place; they overlap neither each other nor
  * grad. X and the products are fp32 (as the dense layer's DSF_F32), for a bf16 W
- * to 17 bits (X is then 5e-5 off). R, C <=
- * 2^20, the smaller one <= 2^15; 0 <= mu < 1, weight_decay >= 0, 1 <= steps <=
- * 16. The sum of u^2 is fp32 and has to be finite there; a gradient of zeros
+ * to 17 bits (after five steps X is then up to 7e-5 of its norm off, of R or C
+ * below 64 up to 4e-4). R, C <= 2^20, the smaller one <= 2^15; 0 <= mu < 1,
+ * weight_decay >= 0, 1 <= steps <= 16. The sum of u^2 is fp32 and has to be finite there; a gradient of zeros
  * with no momentum leaves X zero, a non-finite one reaches all of W. Every
  * pointer is aligned to its element. The workspace (256-byte aligned) needs no
  * initialisation and holds nothing from one call to the next; it serves any

@@ -110,12 +110,17 @@ long long least_splits(bool f32, long long blocks) {
 }
 
 // The same of a product of operands in two terms, which is to be exact to 2^-15 or so:
-// at most 128 K-blocks (three additions each) in one run.
-constexpr long long kTwoRun = 128;
+// at most 64 K-blocks (three times four additions each) in one run, whatever the splits
+// (256 of them for kMaxDim). What is cut off scales all of the orthogonalised update:
+// that of 262,145 x 64 by 6.5e-5 with runs of 128, of 2^20 x 16 by 2.5e-4 with 32
+// splits at most.
+constexpr long long kTwoRun = 64;
 long long least_splits_two(long long blocks) {
   const long long n = (blocks + kTwoRun - 1) / kTwoRun;
-  return n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits);
+  return n < 1 ? 1 : n;
 }
+// Splits that a product may have which has at least `least`.
+long long most_splits(long long least) { return least < kMaxSplits ? kMaxSplits : least; }
 
 // K-blocks in one accumulator run of a bf16 dz product that db is summed from.
 // With more, its wide tiles are half as wide (configuration 3), so that the
@@ -134,7 +139,7 @@ double plan(Product& p, long long M, long long N, int nb, long long nkb, int nse
   for (int cfg = 0; cfg < 4; ++cfg) {
     if (cfg == 2 && p.gated) continue;
     if (cfg % 3 == 0 && (cfg == 3) != runs) continue;
-    for (long long want = least; want <= kMaxSplits && want <= nkb; ++want) {
+    for (long long want = least; want <= most_splits(least) && want <= nkb; ++want) {
       set_tiles(o, cfg, M, N, nb, p.gated, p.f32, nkb, nseg, want);
       if (tiles_of(o) > INT32_MAX / 64) break;
       if (want > least && (!may_split || tiles_of(o) * want > slots_of(cfg))) break;
@@ -167,7 +172,7 @@ double plan_tri(Product& p, long long n, long long nkb, size_t room) {
   Job o = p.a.job[0];
   const long long least = p.two ? least_splits_two(nkb) : 1;
   for (int cfg = 0; cfg < 3; ++cfg)
-    for (long long want = least; want <= kMaxSplits && want <= nkb; ++want) {
+    for (long long want = least; want <= most_splits(least) && want <= nkb; ++want) {
       set_tiles(o, cfg, n, n, 1, false, p.f32, nkb, 1, want);
       const long long tiles = tri_tiles(o, cfg, p.f32);
       if (want > least && (tiles * want > slots_of(cfg) || size_t(want) * n * ((n + 3) / 4 * 4) * 4 > room)) break;

@@ -8,10 +8,12 @@
 //
 // A small singular value grows by a = 3.44 a step, 485 times in five, and with it
 // what the products round. Where W is fp32, X, A and the polynomial are fp32 taken as
-// three bf16 terms each (six products of terms; X ends 1e-6 to 1e-5 off, as in fp32
-// throughout). A bf16 W is rounded to 2^-9 in the end: two terms (2^-17, three
-// products) leave X 2.5e-5 to 5e-5 off, which W's rounding hides at half the work.
-// (One bf16 product would leave 1 to 3% of X, one fp16 0.2 to 0.3%.)
+// three bf16 terms each (six products of terms; X ends 5e-7 to 6e-6 off. The updated W
+// is 1.0e-7 off, twice what products in fp32 leave: 512 x 256). A bf16 W is rounded to
+// 2^-8 of an element at most in the end: two terms (2^-17, three products) leave X 2e-5
+// to 6e-5 off, which W's rounding hides at half the work. (Of fewer than 64 rows or
+// columns up to 4e-4: an error of a large singular value's direction grows with a small
+// one's. One bf16 product would leave 1 to 3% of X, one fp16 0.2 to 0.3%.)
 //
 // A step's three products (2 n^2 m, 2 n^3 and 2 n^2 m operations; the first two are
 // symmetric, and large ones are made by half) leave the next operand's terms in their

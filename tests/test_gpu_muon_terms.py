@@ -87,3 +87,16 @@ def test_other_numbers_of_steps(r, c, steps):
     bound = max(1.0, r / c) ** 0.5 * grows_to(torch.linalg.svdvals((grad / grad.norm()).double()), steps) + 2.0 ** -24 * float(ref.norm())
     assert bound <= 0.02 * float(ref.norm())  # (far below what a step more or less, or a lost term, does)
     assert float((W - ref).norm()) <= bound
+
+
+@pytest.mark.parametrize("kind", ["spread", "directions"])
+@pytest.mark.parametrize("r,c", [(262144, 32), (262145, 64), (1 << 20, 16), (16, 1 << 20), (1 << 20, 100)])
+def test_long_sums_in_two_terms(r, c, kind):
+    """A sum of one sign (A's diagonal) is low by what the tensor cores truncate
+    in one run, which scales X as a whole: its mean scale is to be 1 within the
+    5e-5 that X may be off (a half step of every element, of random sign, leaves
+    2^-8 / sqrt(elements) of it at most)."""
+    W, ref = update(gradient(r + c, r, c, kind), BF16)
+    check(W, ref, BF16)
+    scale = float((W * ref).sum() / ref.square().sum())
+    assert abs(scale - 1) <= STATED[BF16] + 2.0 ** -8 / ref.numel() ** 0.5, scale - 1
