@@ -574,7 +574,9 @@ int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int6
  * a target that is not possible has loss +inf. Types, sums and alignment (rows
  * of x and W) are the dense layer's above; the logits and their softmax are
  * fp32 (the backward's exp(z - lse) carries lse's rounding, 2^-24 |lse|: logits
- * near 0 are the most exact). The logits are never kept: the forward's workspace
+ * near 0 are the most exact). Logits are expected within 7e8 of zero: one below
+ * -7.5e8 counts as -inf (so a bias of -1e9 or of the type's lowest value masks an
+ * item), one above makes lse +inf. The logits are never kept: the forward's workspace
  * holds 1.2 KB a row (and 44 MB more at most), the backward's a piece of their
  * gradients (256 MB, or M x 256 of them) and partial sums of dx in fp32 (at most
  * 32 of them, or 110 MB), beside operands that are laid out.

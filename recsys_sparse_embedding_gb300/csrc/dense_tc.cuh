@@ -294,7 +294,12 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-constexpr float kFar = 3e38f;  // (stands for an infinite maximum, so that differences of maxima stay defined)
+constexpr float kFar = 3e38f;  // (for infinity where differences have to stay defined: no reference; the lse of a row left out)
+// References of sums of exponentials lie within this of zero, in units of log 2: z log2 e -
+// reference is then off by at most 64 where the reference was rounded, which the exponentials'
+// range bears and the reference takes back. A logit farther below adds nothing, as -inf
+// (masks of -1e9 or of the type's lowest value); one farther above makes the sum infinite.
+constexpr float kFarthest = 0x1p30f;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
     int stat_m0 = -1, stat_slot = 0, tgt = -1;
     float2 of_row = make_float2(0.f, 0.f);
     bool fresh = true;
-    float top = -kFar, total = 0.f;
+    float top = -kFarthest, total = 0.f;
     auto put_stat = [&]() {
       const int r = stat_m0 + 32 * q + lane;
       if (stat_m0 >= 0 && r < job0.M) a.stat[((long long)stat_slot * GR + grp) * job0.M + r] = make_float2(top, total);
@@ -789,7 +794,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
         stat_m0 = t.m0;
         stat_slot = t.n0 / ON;
         fresh = true;
-        top = -kFar, total = 0.f;
+        top = -kFarthest, total = 0.f;
         const long long id = row < jb.M ? __ldg(a.target + row) : -1, d = id - a.v0;
         tgt = id >= 0 && d >= 0 && d < jb.N ? int(d) : -1;
         if (EPI == kEpiXent) of_row = row < jb.M ? __ldg(a.rows + row) : make_float2(0.f, 0.f);
@@ -911,7 +916,7 @@ __global__ void __launch_bounds__(Shape<CG, BN, MAJOR, GATED, EPI, F32>::kThread
 #pragma unroll
                 for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], g[k + e]);
               const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-              const float now = fmaxf(top, fminf(most * kLog2e, kFar));
+              const float now = fmaxf(top, fminf(most * kLog2e, kFarthest));
               const float again = total * exp2_fast(top - now) + add(now);
               if (anew) more = again, top = now;
               fresh = false;

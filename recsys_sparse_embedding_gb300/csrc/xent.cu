@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kMerge) merge_kernel(const __grid_constant__ M
   const long long t = a.target[row];
   const bool there = t >= 0 && t < a.V;
   a.lse[row] = lse;
-  a.loss[row] = there ? lse - a.zt[row] : 0.f;
+  // (nothing possible: NaN, also where the target's logit is finite)
+  a.loss[row] = !there ? 0.f : (lse == -INFINITY ? NAN : lse - a.zt[row]);
   if (!there && t != -1 && a.status) atomicOr(a.status, DSF_FLAG_ID_RANGE);
 }
 
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewArg
   }
   float top[MT], sum[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) top[m] = -kFar, sum[m] = 0.f;
+  for (int m = 0; m < MT; ++m) top[m] = -kFarthest, sum[m] = 0.f;
   const int per = 32 >> a.log_g;  // W's rows of a warp and step
   const long long step = (long long)gridDim.x * 8 * per;
   for (long long v0 = ((long long)blockIdx.x * 8 + warp) * per + (lane >> a.log_g); v0 - (lane >> a.log_g) < a.V; v0 += U * step) {
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewArg
         for (int o = g / 2; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         z += b[u];
         if (v == tgt[m] && at == 0) a.zt[m] = z;
-        const float zl = z * kLog2e, now = fmaxf(top[m], fminf(zl, kFar));
+        const float zl = z * kLog2e, now = fmaxf(top[m], fminf(zl, kFarthest));
         sum[m] = sum[m] * exp2_fast(top[m] - now) + exp2_fast(zl - now);
         top[m] = now;
       }

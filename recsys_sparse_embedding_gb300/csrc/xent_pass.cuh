@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(PassShape<NK>::threads(MODE), 1)
     for (int i = 0; ok && unit_at(i, t); ++i) {
       const int row0 = t.r0 + 32 * q, row = row0 + lane;
       const bool some = row0 < a.R;  // whether the warp's rows are there
-      float bias = 0.f, sum = 0.f, lse = 0.f, g = 0.f, top = -kFar;
+      float bias = 0.f, sum = 0.f, lse = 0.f, g = 0.f, top = -kFarthest;
       bool fresh = true;
       int tgt = -1;
       if (row < a.R) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(PassShape<NK>::threads(MODE), 1)
                   float most = z[0];  // (fmaxf leaves a NaN to the sum)
 #pragma unroll
                   for (int k = 1; k < 32; ++k) most = fmaxf(most, z[k]);
-                  const float now = fmaxf(top, fminf(most * kLog2e, kFar)), again = sum * exp2_fast(top - now) + add(now);
+                  const float now = fmaxf(top, fminf(most * kLog2e, kFarthest)), again = sum * exp2_fast(top - now) + add(now);
                   if (anew) more = again, top = now;
                   fresh = false;
                 }
