@@ -78,6 +78,26 @@ def test_nothing_is_written_behind_the_forwards_workspace(dtype, K, M, V):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,K,V", [(1, 64, 100001), (4, 256, 3000), (120, 8, 840001), (513, 16, 200001), (1024, 64, 98304), (5000, 100, 20011),
+                                   (65536, 24, 1600), (20000, 128, 5003)])
+def test_nothing_is_written_behind_a_narrow_forwards_workspace(M, K, V):
+    """few rows, or the sums in one pass"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + K)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    W = (torch.randn(V, K, generator=g, device="cuda") * 1.5 * K ** -0.5).to(BF16)
+    target = torch.randint(-1, V, (M,), generator=g, device="cuda")
+    for bias in (None, torch.randn(V, generator=g, device="cuda")):
+        layer = B.DenseLayer(W, bias)
+        loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        ws = B.SoftmaxXentWorkspace(layer, M)
+        intact = guard(ws)
+        B.ctr_softmax_xent_fwd(layer, x, target, loss, lse, ws)
+        assert intact()
+        assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,M,K,V", [(BF16, 5, 64, 3000), (BF16, 700, 64, 70001), (BF16, 700, 72, 5), (F32, 333, 48, 2001),
                                          (BF16, 2000, 136, 12345), (F32, 3000, 20, 16001), (BF16, 70001, 64, 901)])
 def test_nothing_is_written_behind_the_backwards_workspace(dtype, M, K, V):
