@@ -516,10 +516,11 @@ int ctr_rms_norm_bwd(const void* dy_dev, int64_t lddy, int32_t dy_dtype, const v
 
 /* ------------------------------------------------------------------------
  * Sequence towers and their training: a gated linear recurrence over the click
- * sequences. din_jagged_attn weighs a sequence's
- * positions without regard to their order; the recurrence carries a state from
- * click to click, and its gradients go back through the dense operators above.
- * The pages have no counterpart.
+ * sequences, the softmax cross entropy against an item table, and an update of
+ * dense matrices. din_jagged_attn weighs a sequence's positions without regard
+ * to their order; the recurrence carries a state from click to click, and its
+ * gradients go back through the dense operators above. The pages have no
+ * counterpart.
  *
  * Rows are positions, sequence after sequence; lengths_dev int32 [B] as in
  * dsf_seq, or NULL: B sequences of T / B rows each (T a multiple of B; one row
@@ -554,7 +555,7 @@ int ctr_gated_scan_fwd(const void* x_dev, int64_t ldx, const void* gate_dev, int
 /* The gradients for dh_dev [T, D] and dh_last_dev (nullable: zeros): dx_dev,
  * dgate_dev and dh0_dev (nullable), overwritten. x, gate, lengths and h0 are
  * the forward's, h_dev its output (in bf16 dgate therefore takes h_{t-1} as it
- * was rounded, 2^-9 of it). */
+ * was rounded, off by up to 2^-8 of it). */
 int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int64_t ldx, const void* gate_dev,
                        int64_t ldg, const void* h_dev, int64_t ldh, int32_t dtype, const int32_t* lengths_dev,
                        int64_t T, int32_t B, int32_t D, const float* h0_dev, const float* dh_last_dev, void* dx_dev,
@@ -579,8 +580,8 @@ int ctr_gated_scan_bwd(const void* dh_dev, int64_t lddh, const void* x_dev, int6
  * item), one above makes lse +inf. The logits are never kept: the forward's workspace
  * holds 1.2 KB a row (and 44 MB more at most), the backward's a piece of their
  * gradients (256 MB, or M x 256 of them) and partial sums of dx in fp32 (at most
- * 32 of them, or 110 MB), beside operands that are laid out.
- * Equal calls give equal bits. */
+ * 32 of them, or 110 MB), beside operands that are laid out. Outputs overlap
+ * neither inputs nor each other. Equal calls give equal bits. */
 size_t dsf_softmax_xent_workspace_bytes(const dsf_dense* layer, int64_t M, int32_t backward);
 
 int ctr_softmax_xent_fwd(const dsf_dense* layer, const void* x_dev, int64_t ldx, const int64_t* target_dev, int64_t M,
@@ -610,9 +611,9 @@ int ctr_softmax_xent_bwd(const dsf_dense* layer, const void* x_dev, int64_t ldx,
  * grad. X and the products are fp32 (as the dense layer's DSF_F32), for a bf16 W
  * to 17 bits (after five steps X is then up to 7e-5 of its norm off, of R or C
  * below 64 up to 4e-4). R, C <= 2^20, the smaller one <= 2^15; 0 <= mu < 1,
- * weight_decay >= 0, 1 <= steps <= 16. The sum of u^2 is fp32 and has to be finite there; a gradient of zeros
- * with no momentum leaves X zero, a non-finite one reaches all of W. Every
- * pointer is aligned to its element. The workspace (256-byte aligned) needs no
+ * weight_decay >= 0, 1 <= steps <= 16. The sum of u^2 is fp32 and has to be
+ * finite there; a gradient of zeros with no momentum leaves X zero, a non-finite
+ * one reaches all of W. Every pointer is aligned to its element. The workspace (256-byte aligned) needs no
  * initialisation and holds nothing from one call to the next; it serves any
  * matrix of its shape. Equal calls give equal bits. DSF_FLAG_TIMEOUT in
  * *status_dev (nullable) if a device wait ran out. */

@@ -140,8 +140,9 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src, bool any) {
                : "memory");
 }
 
-// z = sigmoid(g) and a = 1 - z = t z, t = exp(-g), each to a few last bits of its
-// own size (below 2^-126: 0). (One reciprocal of a product for four channels, with
+// z = sigmoid(g) and a = 1 - z = t z, t = exp(-g), each to (8 + 2 |g|) 2^-23 of its own
+// size (below 2^-126: 0); what grows with |g| is the exponent's rounding, as much as one
+// of g itself. (One reciprocal of a product for four channels, with
 // a branch for far gates, was slower: the special functions do not bind, and the
 // branch keeps the rows apart.)
 __device__ __forceinline__ void gate_of(float2 g, float2& z, float2& a) {

@@ -18,11 +18,16 @@
 //               tensor-memory quarter) by 64 columns of its tiles.
 //
 // Tensor memory: three S buffers of 128 columns, so that a set finds its next tile's
-// S there when it has done one; then the output's columns. What binds (8192 rows and
-// 131,072 columns of 64: 294 us for the sums, 575 for both gradients, 1290 cycles a
-// tile): the exponentials, 1024 cycles of the special functions. Slower or no faster:
+// S there when it has done one; then the output's columns. No unit is full (8192 rows and
+// 131,072 columns of 64, under ncu 273 us for the sums, 263 for dx, 336 for dW): the
+// exponentials take 512 cycles a tile (32 ex2 a clock and SM, measured on their own), 44,
+// 47 and 39% of the time; the tensor pipe is busy 22, 47 and 38%, the issue slots 55 to
+// 61%, and in dW's pass shared memory's read path 70% (lse, g and target per column). An
+// SM's 19 warps wait on what they issued themselves: results, tensor memory, branches.
+// (Registers are all taken, 96 a thread; ptxas reports 116 to 120 bytes of spill stores for
+// dW's pass, 20 for dx's.) Slower or no faster:
 // dz in buffers of its own in tensor memory or in shared memory, S given back as soon
-// as it is in registers (they spill), 24 epilogue warps, four S buffers for the sums.
+// as it is in registers (they spill more), 24 epilogue warps, four S buffers for the sums.
 // At K = 256 dz in memory was faster (both gradients 1.6 ms against 1.9).
 // Sums of a unit are at most 512 tiles (65536 terms) long; dx is split over the
 // columns anyway (planes, added in order by finish_kernel). Every wait is bounded.
