@@ -140,17 +140,20 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src, bool any) {
                : "memory");
 }
 
-// z = sigmoid(g) and a = 1 - z = t z, t = exp(-g), each to (8 + 2 |g|) 2^-23 of its own
-// size (below 2^-126: 0); what grows with |g| is the exponent's rounding, as much as one
-// of g itself. (One reciprocal of a product for four channels, with
-// a branch for far gates, was slower: the special functions do not bind, and the
-// branch keeps the rows apart.)
+// z = sigmoid(g) and a = 1 - z, each to (8 + 2 |g|) 2^-23 of its own size (below 2^-126:
+// 0); what grows with |g| is the exponent's rounding, as much as one of g itself. Where a
+// is below a half it is t z, t = exp(-g). Above, that product would be up to 2^-23 off 1,
+// alike in every row of a constant gate: a closed one lost or gained 2% of its state in
+// 131,072 rows. 1 - z is rounded once, never passes 1, and is 1 where z is nothing beside
+// it. (One reciprocal of a product for four channels, with a branch for far gates, was
+// slower: the special functions do not bind, and the branch keeps the rows apart.)
 __device__ __forceinline__ void gate_of(float2 g, float2& z, float2& a) {
   const float2 e = g * pair(-kLog2e), t = make_float2(exp2_fast(e.x), exp2_fast(e.y)), d = t + pair(1.f);
   z = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+  const float2 rest = __ffma2_rn(z, pair(-1.f), pair(1.f));
   a = t * z;
-  if (t.x > 0x1p126f) a.x = 1.f;
-  if (t.y > 0x1p126f) a.y = 1.f;
+  if (t.x > 1.f) a.x = rest.x;
+  if (t.y > 1.f) a.y = rest.y;
 }
 
 // (A, B) := (A, B) after (Ap, Bp)
